@@ -1507,6 +1507,7 @@ tfm_status tfm_device_status(void* handle) {
     if (e != cudaSuccess) return tfm::cuda_fail(e, "read device error word");
     if (v == TFM_EBADTOKEN) return fail(TFM_EBADTOKEN, "a token id was outside [0, vocab)");
     if (v == TFM_ETIMEOUT) return fail(TFM_ETIMEOUT, "a pipeline wait timed out on the device");
+    if (v == TFM_EINVAL) return fail(TFM_EINVAL, "a sequence offset, length or count was out of range");
     if (v != 0) return fail((tfm_status)v, "device error %d", v);
     return TFM_OK;
 }

@@ -232,4 +232,59 @@ cudaError_t launch_attention_pp(const AttnPlan& p, cudaStream_t st);
 bool attention_short_supported(int dh, int S, int window);
 cudaError_t launch_attention_short(const AttnPlan& p, cudaStream_t st);
 
+// ---- batched serving (batch.cu has the entry points)
+// Causal attention over packed sequences (k_packed.cu): strides in elements,
+// {q token, q head, k token, k head, v token, v head, o token, o head}.
+struct PackedArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    void* o;
+    const int32_t* cu;
+    int n_seq, T, H, Hkv, dh;
+    int64_t strides[8];
+    float scale;
+    int window;
+    int bf16;
+    void* ws;
+};
+size_t packed_workspace_bytes(int T, int n_seq);
+tfm_status launch_packed_attention(const PackedArgs& a, cudaStream_t st, cudaError_t* e);
+
+// Attention over a shared prefix and each sequence's own cache (k_prefix.cu).
+struct PrefixArgs {
+    const void* q;
+    const void* kp;
+    const void* vp;
+    const void* kc;
+    const void* vc;
+    void* o;
+    const int32_t* lens;
+    int B, H, Hkv, T, P, max_prefix, max_seq, dh;
+    float scale;
+    void* ws;
+};
+size_t prefix_workspace_bytes(int B, int H, int Hkv, int T, int dh);
+tfm_status launch_prefix_attention(const PrefixArgs& a, cudaStream_t st, cudaError_t* e);
+
+// Verification of drafted tokens (k_verify.cu).
+struct VerifyArgs {
+    const float* target;
+    int64_t ld_target;
+    const float* dlogits;
+    int64_t ld_draft;
+    const int32_t* draft;
+    const int32_t* n_draft;
+    const float* u;
+    const float* noise;
+    int64_t ld_noise;
+    int B, K, V;
+    float temperature;
+    int32_t* tokens;
+    int32_t* n_accepted;
+    void* ws;
+};
+size_t verify_workspace_bytes(int B, int K, int V);
+cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t st);
+
 }  // namespace tfm

@@ -98,6 +98,15 @@ _SIGS = {
     "tfm_decode_attention_workspace_bytes": ([_I32, _I32, _I32, _I32], _SZ),
     "tfm_decode_attention": ([_V, _V, _V, _V, _I32, _I32, _I32, _I32, _I32, _I32, _F, _I32, _V,
                               _SZ, _V], _I32),
+    "tfm_packed_attention_workspace_bytes": ([_I32, _I32], _SZ),
+    "tfm_packed_attention": ([_V, _V, _V, _V, _V, _I32, _I32, _I32, _I32, _I32,
+                              ctypes.POINTER(ctypes.c_int64), _F, _I32, _I32, _V, _SZ, _V], _I32),
+    "tfm_prefix_attention_workspace_bytes": ([_I32, _I32, _I32, _I32, _I32], _SZ),
+    "tfm_prefix_attention": ([_V, _V, _V, _V, _V, _V, _V, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
+                              _I32, _F, _V, _SZ, _V], _I32),
+    "tfm_verify_draft_workspace_bytes": ([_I32, _I32, _I32], _SZ),
+    "tfm_verify_draft": ([_V, _I64, _V, _I64, _V, _V, _V, _V, _I64, _I32, _I32, _I32, _F, _V, _V,
+                          _V, _SZ, _V], _I32),
     "tfm_linear": ([_V, _V, _V, _I64, _I32, _I32, _I64, _I32, _I32, _I32, _V], _I32),
     "tfm_swiglu": ([_V, _V, _V, _V, _V, _I64, _I32, _I32, _I32, _V, _SZ, _I32, _V], _I32),
     "tfm_swiglu_workspace_bytes": ([_I64, _I32, _I32], _SZ),
@@ -504,6 +513,143 @@ def decode_attention(q, k_cache, v_cache, o, pos, workspace, window=0, scale=0.0
     nbytes = workspace.numel() * workspace.element_size()
     _check(load().tfm_decode_attention(qp, kp, vp, op, B, H, Hkv, max_seq, int(pos), dh, scale,
                                        int(window), wp, nbytes, _stream(stream)))
+
+
+# ---- batched serving: packed prompts, a shared prefix, drafted tokens
+_Strides = ctypes.c_int64 * 8
+
+
+def _one_device(*named):
+    """Every tensor is on the current CUDA device, where the library launches."""
+    here = _torch().cuda.current_device()
+    for t, name in named:
+        if t is not None and t.device.index != here:
+            raise ValueError(f"{name}: on {t.device}, the current device is cuda:{here}")
+
+
+def _space(workspace):
+    return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+
+
+def packed_attention_workspace_bytes(T, n_seq):
+    return load().tfm_packed_attention_workspace_bytes(T, n_seq)
+
+
+def packed_attention(q, k, v, o, cu_seqlens, workspace, window=0, scale=0.0, stream=None):
+    """Causal attention over packed sequences: q, o [T, H, dh] and k, v
+    [T, Hkv, dh] (bf16 or fp32) with dense rows of dh and any token and head
+    strides; sequence b is the rows [cu_seqlens[b], cu_seqlens[b + 1]) (int32,
+    device).  Query i sees keys i-window < j <= i of its sequence (0: all)."""
+    for t, name in ((q, "q"), (k, "k"), (v, "v"), (o, "o")):
+        if not t.is_cuda:
+            raise ValueError(f"{name}: a CUDA tensor is required, got one on {t.device}")
+        if t.dim() != 3 or (t.numel() and t.stride(2) != 1 and t.shape[2] != 1):
+            raise ValueError(f"{name}: [T, heads, dh] with dense rows of dh is required")
+        if t.dtype != q.dtype:
+            raise TypeError(f"{name}: dtype {t.dtype}, {q.dtype} is required")
+    T, H, dh = q.shape
+    Hkv = k.shape[1]
+    _shape(k, (T, Hkv, dh), "k")
+    _shape(v, (T, Hkv, dh), "v")
+    _shape(o, (T, H, dh), "o")
+    cp = _dev(cu_seqlens, "cu_seqlens", _t("int32"))
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens: one dimension of n_seq + 1 offsets is required")
+    wp, nbytes = _space(workspace)
+    _one_device((q, "q"), (k, "k"), (v, "v"), (o, "o"), (cu_seqlens, "cu_seqlens"), (workspace, "workspace"))
+    strides = _Strides(q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+                       o.stride(0), o.stride(1))
+    _check(load().tfm_packed_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), cp,
+                                       cu_seqlens.shape[0] - 1, T, H, Hkv, dh, strides, scale,
+                                       int(window), _mode_of(q), wp, nbytes, _stream(stream)))
+
+
+def prefix_attention_workspace_bytes(B, H, Hkv, T, dh):
+    return load().tfm_prefix_attention_workspace_bytes(B, H, Hkv, T, dh)
+
+
+def prefix_attention(q, k_prefix, v_prefix, k_cache, v_cache, o, lens, workspace, prefix_len=None,
+                     scale=0.0, stream=None):
+    """Attention of T new tokens per sequence, q [B, H, T, dh], over a shared
+    prefix [Hkv, max_prefix, dh] (its first prefix_len positions; default all)
+    and each sequence's own cache [B, Hkv, max_seq, dh] of lens[b] positions
+    (int32, device), the T new ones the last; o [B, T, H*dh]; all bf16."""
+    bf = _t("bfloat16")
+    qp = _dev(q, "q", bf)
+    if q.dim() != 4:
+        raise ValueError("q: [B, H, T, dh] is required")
+    B, H, T, dh = q.shape
+    ptrs = [_dev(t, name, bf) for t, name in ((k_prefix, "k_prefix"), (v_prefix, "v_prefix"),
+                                              (k_cache, "k_cache"), (v_cache, "v_cache"))]
+    if k_cache.dim() != 4 or k_cache.shape[0] < B or k_cache.shape[3] != dh:
+        raise ValueError(f"k_cache: shape {tuple(k_cache.shape)} does not hold {B} sequences of d_head {dh}")
+    Hkv, max_seq = k_cache.shape[1], k_cache.shape[2]
+    _shape(v_cache, k_cache.shape, "v_cache")
+    if k_prefix.dim() != 3 or k_prefix.shape[0] != Hkv or k_prefix.shape[2] != dh:
+        raise ValueError(f"k_prefix: shape {tuple(k_prefix.shape)}, ({Hkv}, max_prefix, {dh}) is required")
+    _shape(v_prefix, k_prefix.shape, "v_prefix")
+    _numel(lens, B, "lens")
+    lp = _dev(lens, "lens", _t("int32"))
+    _numel(o, B * T * H * dh, "o")
+    op = _dev(o, "o", bf)
+    wp, nbytes = _space(workspace)
+    _one_device((q, "q"), (k_prefix, "k_prefix"), (v_prefix, "v_prefix"), (k_cache, "k_cache"),
+                (v_cache, "v_cache"), (o, "o"), (lens, "lens"), (workspace, "workspace"))
+    max_prefix = k_prefix.shape[1]
+    _check(load().tfm_prefix_attention(qp, *ptrs, op, lp, B, H, Hkv, T,
+                                       max_prefix if prefix_len is None else int(prefix_len),
+                                       max_prefix, max_seq, dh, scale, wp, nbytes, _stream(stream)))
+
+
+def verify_draft_workspace_bytes(B, K, V):
+    return load().tfm_verify_draft_workspace_bytes(B, K, V)
+
+
+def verify_draft(target, draft_logits, draft, n_draft, u, noise, vocab, tokens, n_accepted,
+                 workspace, temperature=1.0, stream=None):
+    """Verifies drafted tokens draft [B, K] (int32; n_draft [B] of them, or None:
+    all) drawn from draft_logits [B*K, >= vocab] against the target's logits
+    target [B*(K+1), >= vocab] with the uniform numbers u [B, K] and the Exp(1)
+    numbers noise [B, >= vocab] (fp32); writes tokens [B, K+1] (the accepted
+    ones, the new one, -1) and n_accepted [B].  temperature 0 is greedy, and
+    draft_logits, u and noise may be None."""
+    f32, i32 = _t("float32"), _t("int32")
+    if draft.dim() != 2:
+        raise ValueError("draft: [B, K] is required")
+    B, K = draft.shape
+    dp = _dev(draft, "draft", i32)
+    greedy = temperature == 0
+    checked = []
+    for t, name, rows, must in ((target, "target", B * (K + 1), True),
+                                (draft_logits, "draft_logits", B * K, not greedy and K > 0),
+                                (noise, "noise", B, not greedy)):
+        if t is None:
+            if must:
+                raise ValueError(f"{name}: required unless temperature is 0")
+            checked.append((None, 0))
+            continue
+        ptr = _dev(t, name, f32, rows=True)
+        if t.shape[0] < rows or t.shape[1] < vocab:
+            raise ValueError(f"{name}: {rows} rows of at least {vocab} columns are required, got {tuple(t.shape)}")
+        checked.append((ptr, t.stride(0)))
+    (tp, ldt), (lp, ldd), (zp, ldn) = checked
+    if u is None:
+        if not greedy and K:
+            raise ValueError("u: required unless temperature is 0")
+    else:
+        _numel(u, B * K, "u")
+    if n_draft is not None:
+        _numel(n_draft, B, "n_draft")
+    _numel(tokens, B * (K + 1), "tokens")
+    _numel(n_accepted, B, "n_accepted")
+    up, np_ = _dev(u, "u", f32), _dev(n_draft, "n_draft", i32)
+    op, ap = _dev(tokens, "tokens", i32), _dev(n_accepted, "n_accepted", i32)
+    wp, nbytes = _space(workspace)
+    _one_device((target, "target"), (draft_logits, "draft_logits"), (draft, "draft"), (n_draft, "n_draft"),
+                (u, "u"), (noise, "noise"), (tokens, "tokens"), (n_accepted, "n_accepted"),
+                (workspace, "workspace"))
+    _check(load().tfm_verify_draft(tp, ldt, lp, ldd, dp, np_, up, zp, ldn, B, K, int(vocab),
+                                   float(temperature), op, ap, wp, nbytes, _stream(stream)))
 
 
 def linear(x, W, y, accumulate=False, stream=None):

@@ -33,7 +33,8 @@
  *  - Every function returns a tfm_status.  Argument errors are found on the
  *    host before anything is launched (TFM_EINVAL / TFM_EUNSUPPORTED) and
  *    leave outputs untouched.  Errors found on the device (a token id outside
- *    [0, vocab), a pipeline wait that gave up) set a sticky device error word
+ *    [0, vocab), a sequence length out of range, a pipeline wait that gave up)
+ *    set a sticky device error word
  *    that tfm_device_status() reads and clears.  tfm_last_error() gives a
  *    thread-local message for the last failing call.
  *  - "bf16 mode" stores weights and activations in bfloat16 and accumulates in
@@ -320,7 +321,8 @@ tfm_status tfm_decode_step(void* handle, const int32_t* tokens, int32_t B, int32
                            float* logits, int64_t ld_logits, void* stream);
 
 /* Synchronises the device, then returns and clears the sticky device error word
- * (TFM_OK, TFM_EBADTOKEN or TFM_ETIMEOUT), or TFM_ECUDA if the context faulted.
+ * (TFM_OK, TFM_EBADTOKEN, TFM_ETIMEOUT, or TFM_EINVAL for a sequence offset,
+ * length or count out of range), or TFM_ECUDA if the context faulted.
  * handle may be NULL (component calls share the same word). */
 tfm_status tfm_device_status(void* handle);
 
@@ -357,8 +359,9 @@ const char* tfm_profile_kind_name(int32_t kind);
 /* ---------------------------------------------------------------- components
  * Single operations on caller buffers (device pointers), for testing each step
  * against the oracle and for callers that assemble their own model.
- * Empty calls (M = 0; B, H or S = 0 for RoPE; B or S = 0 for attention; B = 0
- * for decode attention) check their other arguments, then return TFM_OK
+ * Empty calls (M = 0; B, H or S = 0 for RoPE; B or S = 0 for attention; T or
+ * n_seq = 0 for packed attention; B = 0 for decode and prefix attention and for
+ * verification) check their other arguments, then return TFM_OK
  * without launching anything or reading any pointer, which may then be NULL. */
 
 /* Embedding lookup (CS336 walkthrough, section 5.2): h[m, :] = E[tokens[m], :]
@@ -425,6 +428,105 @@ tfm_status tfm_decode_attention(const void* q, const void* k_cache, const void* 
                                 int32_t B, int32_t H, int32_t Hkv, int32_t max_seq, int32_t pos,
                                 int32_t dh, float scale, int32_t window, void* workspace,
                                 size_t workspace_bytes, void* stream);
+
+/* ---- Serving a batch whose sequences have different lengths: packed prompts,
+ * new tokens over a prefix all sequences share, and drafted tokens checked
+ * against the model's own distribution.  All three read their lengths from the
+ * device, so a recorded graph serves every later batch of the same bounds. */
+
+/* Causal attention over packed prompts: n_seq sequences one behind the other in
+ * T rows, sequence b the rows [cu_seqlens[b], cu_seqlens[b + 1]) (int32
+ * [n_seq + 1], device; a sequence may be empty).  Within each sequence it is
+ * tfm_causal_attention_window: query i sees the sequence's keys
+ * i - window < j <= i (window 0: all j <= i), query head h reads kv head
+ * h / (H / Hkv).  No row sees another sequence, whatever that one holds (NaN and
+ * infinities included), and no key behind a query changes its row.  Rows of o
+ * that belong to no sequence are not written.
+ * q, o [T, H, dh] and k, v [T, Hkv, dh] with any token and head strides:
+ * strides (host, may be NULL: all dense, token-major) holds, in elements,
+ * {q token, q head, k token, k head, v token, v head, o token, o head}, so that
+ * the head-major q, k, v of tfm_rope and tfm_causal_attention ([H, T, dh]) and
+ * the columns of one fused [T, (H + 2 Hkv) dh] projection are read in place.
+ * Strides are at least dh (a dimension of one row or head excepted), multiples
+ * of 16 bytes and below 2^39 bytes; o's rows must not overlap.  bf16 mode: dh in {32, 64, 128};
+ * fp32 mode: dh % 4 == 0, dh <= 128.  T <= 2^30, n_seq <= 2^20,
+ * (T / 128 + n_seq) * H < 2^31.  scale <= 0 means 1/sqrt(dh); it must be finite.
+ * Pointers 16-byte aligned, cu_seqlens 4-byte.  workspace: device, 16-byte
+ * aligned, tfm_packed_attention_workspace_bytes(T, n_seq) bytes (0 for bad
+ * sizes), not used by another call in flight; its contents need not survive.
+ * Offsets that decrease or leave [0, T] set TFM_EINVAL in the device error word
+ * (tfm_device_status); such a sequence is skipped and nothing outside the
+ * buffers is touched.  Capturable in a CUDA graph. */
+size_t tfm_packed_attention_workspace_bytes(int32_t T, int32_t n_seq);
+tfm_status tfm_packed_attention(const void* q, const void* k, const void* v, void* o,
+                                const int32_t* cu_seqlens, int32_t n_seq, int32_t T, int32_t H,
+                                int32_t Hkv, int32_t dh, const int64_t* strides, float scale,
+                                int32_t window, int32_t mode, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* Attention of T new tokens per sequence (T = 1: a decode step; T > 1: a step
+ * that scores drafted tokens) over a prefix that all B sequences share and each
+ * sequence's own cache.  The keys and values of the prefix are held once and
+ * read once for all sequences: k_prefix, v_prefix [Hkv, max_prefix, dh] hold
+ * positions [0, prefix_len); k_cache, v_cache [B, Hkv, max_seq, dh] hold the
+ * lens[b] positions after the prefix (lens int32 [B], device), the T new tokens
+ * the last of them.  New token t of sequence b sees the prefix and its own
+ * positions [0, lens[b] - (T - 1 - t)); a token that sees no key at all gets
+ * zeros.  q [B, H, T, dh] (for T = 1 the q of tfm_decode_attention), o
+ * [B, T, H*dh]; query head h reads kv head h / (H / Hkv).  What lies in the
+ * caches behind lens[b] and in the prefix behind prefix_len is not looked at.
+ * bf16 only, everything dense; dh in {32, 64, 128}, (H / Hkv) * T <= 128,
+ * B <= 4096, B * H * T <= 2^24, B * Hkv * max_seq <= 2^31 - 1.
+ * prefix_len may be 0 (its pointers may then be NULL), and lens[b] may be 0.
+ * scale <= 0 means 1/sqrt(dh); it must be finite.  Pointers 16-byte aligned,
+ * lens 4-byte.  workspace: device, 16-byte aligned,
+ * tfm_prefix_attention_workspace_bytes(B, H, Hkv, T, dh) bytes (0 for bad
+ * sizes), not used by another call in flight.  A length outside [0, max_seq]
+ * sets TFM_EINVAL in the device error word and counts as 0.  Capturable in a
+ * CUDA graph (the lengths are read when it runs). */
+size_t tfm_prefix_attention_workspace_bytes(int32_t B, int32_t H, int32_t Hkv, int32_t T, int32_t dh);
+tfm_status tfm_prefix_attention(const void* q, const void* k_prefix, const void* v_prefix,
+                                const void* k_cache, const void* v_cache, void* o,
+                                const int32_t* lens, int32_t B, int32_t H, int32_t Hkv, int32_t T,
+                                int32_t prefix_len, int32_t max_prefix, int32_t max_seq, int32_t dh,
+                                float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Verification of drafted tokens: per sequence b, n = n_draft[b] <= K tokens
+ * draft[b, 0..n) (int32 [B, K]) that a drafting model drew from its logits
+ * draft_logits [B*K, ld_draft] (row b*K + i), checked against the target model's
+ * logits target [B*(K+1), ld_target] (row b*(K+1) + i: its scores of the token
+ * at place i, after i drafted ones).  With p_i = softmax(target_i / temperature)
+ * and q_i = softmax(draft_i / temperature), token x = draft[b, i] is accepted iff
+ * every earlier one was and u[b, i] * q_i(x) < p_i(x) (u fp32 [B, K], uniform in
+ * [0, 1)).  One new token follows the accepted ones: at a refused place i it is
+ * drawn from max(p_i - q_i, 0) (from p_i, should that be zero everywhere),
+ * after n accepted tokens from p_n.  The draw is an exponential race: the token
+ * with the largest weight / noise[b, v] wins, noise [B, ld_noise] fp32
+ * independent Exp(1) values (normal, positive), so every token is distributed
+ * as if drawn from the target model alone.  temperature 0 is greedy: accepted
+ * iff x is target_i's largest logit, the new token the largest logit;
+ * draft_logits, u and noise are then not read and may be NULL.
+ * Ties go to the lowest token.  A logit of -infinity or NaN has no weight; +infinity takes
+ * all of it.  Outputs: n_accepted [B], tokens [B, K + 1] (int32): the accepted
+ * tokens, the new one, then -1; the new one is -1 as well if no token has any
+ * weight.  Statistics are kept in fp32, decisions that fp32 leaves open are made
+ * in fp64.
+ * n_draft (int32 [B], device) may be NULL: K everywhere.  A value outside [0, K]
+ * sets TFM_EINVAL in the device error word and is clamped; a drafted id outside
+ * [0, V) sets TFM_EBADTOKEN and is refused.  V >= 1, 0 <= K <= 64, leading
+ * dimensions >= V and multiples of 4, logits and noise 16-byte aligned, the rest
+ * 4-byte, V <= 2^30, B * (K + 1) <= 2^20, B * (2K + 1) * V / 4096 < 2^30,
+ * 0 <= temperature < infinity.
+ * workspace: device, 16-byte aligned, tfm_verify_draft_workspace_bytes(B, K, V)
+ * bytes (0 for bad sizes), not used by another call in flight.  Results do not
+ * depend on timing; capturable in a CUDA graph. */
+size_t tfm_verify_draft_workspace_bytes(int32_t B, int32_t K, int32_t V);
+tfm_status tfm_verify_draft(const float* target, int64_t ld_target, const float* draft_logits,
+                            int64_t ld_draft, const int32_t* draft, const int32_t* n_draft,
+                            const float* u, const float* noise, int64_t ld_noise, int32_t B,
+                            int32_t K, int32_t V, float temperature, int32_t* tokens,
+                            int32_t* n_accepted, void* workspace, size_t workspace_bytes,
+                            void* stream);
 
 /* Bias-free Linear (CS336 walkthrough, section 5.3): y = x W^T.
  * x [M, K], W [N, K] (bf16 or fp32 by mode); y [M, ldy] fp32 when
