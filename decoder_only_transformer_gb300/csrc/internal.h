@@ -222,6 +222,10 @@ struct AttnPlan {
     int window;                     // > 0: sliding window (query i sees keys i-window < j <= i)
 };
 bool attention_tc_supported(int dh);
+// Tensor map of [T, heads, dh] bf16 rows at any strides (elements), for TMA
+// tiles of box_rows rows of one head.
+bool rows_heads_map(CUtensorMap* map, const void* ptr, int64_t T, int64_t heads, int dh, int64_t token_stride,
+                    int64_t head_stride, int box_rows = 128);
 tfm_status plan_attention_tc(AttnPlan* p, const void* q, const void* k, const void* v, void* o,
                              int B, int H, int Hkv, int S, int dh, float scale);
 cudaError_t launch_attention_tc(const AttnPlan& p, cudaStream_t st);

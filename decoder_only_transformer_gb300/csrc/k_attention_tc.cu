@@ -581,6 +581,23 @@ cudaError_t launch_tc(const AttnPlan& p, cudaStream_t st) {
 
 }  // namespace
 
+// [T, heads, dh] bf16 at any token and head stride (elements), box min(dh, 64) x
+// 128 rows x 1 head, zero fill past T.
+bool rows_heads_map(CUtensorMap* map, const void* ptr, int64_t T, int64_t heads, int dh, int64_t token_stride,
+                    int64_t head_stride, int box_rows) {
+    EncodeTiledFn fn = att_encode_fn();
+    if (!fn) return false;
+    const cuuint32_t inner = dh >= 64 ? 64 : (cuuint32_t)dh;
+    cuuint64_t dims[3] = {(cuuint64_t)dh, (cuuint64_t)T, (cuuint64_t)heads};
+    cuuint64_t strides[2] = {(cuuint64_t)(token_stride * 2), (cuuint64_t)(head_stride * 2)};
+    cuuint32_t box[3] = {inner, (cuuint32_t)box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              inner * 2 == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool attention_tc_supported(int dh) { return dh == 32 || dh == 64 || dh == 128; }
 
 tfm_status plan_attention_tc(AttnPlan* p, const void* q, const void* k, const void* v, void* o,

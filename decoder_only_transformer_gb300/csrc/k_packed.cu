@@ -3,6 +3,8 @@
 // o_i = sum_j p_ij v_j with p_i = softmax_j(scale q_i . k_j) over the keys of
 // row i's own sequence, max(start, i - window + 1) <= j <= i (window 0: from the
 // sequence's start); query head h reads kv head h / (H / Hkv).
+#include <climits>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -21,24 +23,14 @@ __device__ __forceinline__ SeqRange seq_range(const int32_t* __restrict__ cu, in
     return SeqRange{ok ? s : 0, ok ? e - s : 0};
 }
 
-template <typename E>
-__device__ __forceinline__ float to_f32(E x);
-template <>
-__device__ __forceinline__ float to_f32<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void from_f32(float* d, float x) { *d = x; }
-__device__ __forceinline__ void from_f32(__nv_bfloat16* d, float x) { *d = __float2bfloat16_rn(x); }
-
 struct PackedStrides {
     int64_t qt, qh, kt, kh, vt, vh, ot, oh;
 };
 
 // One warp per (row, head): lane l holds coordinates l, l + 32, ...; the visible
 // keys in order with a running maximum and sum.
-template <typename E>
-__global__ void __launch_bounds__(256) k_packed_rows(const E* __restrict__ q, const E* __restrict__ k,
-                                                     const E* __restrict__ v, E* __restrict__ o,
+__global__ void __launch_bounds__(256) k_packed_rows(const float* __restrict__ q, const float* __restrict__ k,
+                                                     const float* __restrict__ v, float* __restrict__ o,
                                                      const int32_t* __restrict__ cu, int n_seq, int T,
                                                      int H, int Hkv, int dh, PackedStrides sd,
                                                      float scale, int window, int* err) {
@@ -62,23 +54,23 @@ __global__ void __launch_bounds__(256) k_packed_rows(const E* __restrict__ q, co
     if (lo == 0) return;
     const SeqRange r = seq_range(cu, lo - 1, T);
     if (i < r.start || i >= r.start + r.len) return;
-    const E* qr = q + i * sd.qt + h * sd.qh;
+    const float* qr = q + i * sd.qt + h * sd.qh;
     float qv[4], acc[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
         const int d = lane + 32 * t;
-        qv[t] = d < dh ? to_f32(qr[d]) : 0.f;
+        qv[t] = d < dh ? (qr[d]) : 0.f;
         acc[t] = 0.f;
     }
     float mx = -INFINITY, sum = 0.f;
     const int j0 = (window > 0 && i - window + 1 > r.start) ? i - window + 1 : r.start;
     for (int j = j0; j <= i; ++j) {
-        const E* kr = k + j * sd.kt + g * sd.kh;
-        const E* vr = v + j * sd.vt + g * sd.vh;
+        const float* kr = k + j * sd.kt + g * sd.kh;
+        const float* vr = v + j * sd.vt + g * sd.vh;
         float part = 0.f;
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-            if (lane + 32 * t < dh) part = fmaf(qv[t], to_f32(kr[lane + 32 * t]), part);
+            if (lane + 32 * t < dh) part = fmaf(qv[t], (kr[lane + 32 * t]), part);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
         const float s = part * scale;
@@ -87,33 +79,738 @@ __global__ void __launch_bounds__(256) k_packed_rows(const E* __restrict__ q, co
         sum = sum * corr + p;
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-            if (lane + 32 * t < dh) acc[t] = acc[t] * corr + p * to_f32(vr[lane + 32 * t]);
+            if (lane + 32 * t < dh) acc[t] = acc[t] * corr + p * (vr[lane + 32 * t]);
         mx = mnew;
     }
     const float inv = 1.0f / sum;
-    E* orow = o + i * sd.ot + h * sd.oh;
+    float* orow = o + i * sd.ot + h * sd.oh;
 #pragma unroll
     for (int t = 0; t < 4; ++t)
-        if (lane + 32 * t < dh) from_f32(orow + lane + 32 * t, acc[t] * inv);
+        if (lane + 32 * t < dh) orow[lane + 32 * t] = acc[t] * inv;
 }
 
-template <typename E>
 cudaError_t launch_rows(const PackedArgs& a, cudaStream_t st) {
     const int64_t blocks = ((int64_t)a.T * a.H + 7) / 8;
     const PackedStrides sd{a.strides[0], a.strides[1], a.strides[2], a.strides[3],
                            a.strides[4], a.strides[5], a.strides[6], a.strides[7]};
-    return launch_pdl(k_packed_rows<E>, dim3((unsigned)blocks), dim3(256), 0, st,
-                      static_cast<const E*>(a.q), static_cast<const E*>(a.k),
-                      static_cast<const E*>(a.v), static_cast<E*>(a.o), a.cu, a.n_seq, a.T, a.H,
+    return launch_pdl(k_packed_rows, dim3((unsigned)blocks), dim3(256), 0, st,
+                      static_cast<const float*>(a.q), static_cast<const float*>(a.k),
+                      static_cast<const float*>(a.v), static_cast<float*>(a.o), a.cu, a.n_seq, a.T, a.H,
                       a.Hkv, a.dh, sd, a.scale, a.window, device_error_word());
+}
+
+// ------------------------------------------------------------------ work list
+// A work item is two query tiles of 128 rows that read the same keys: with an
+// even group two neighbouring query heads on the same rows (equal lengths, no
+// half-empty pair in short sequences), otherwise two neighbouring tiles of one
+// head.  The list holds one entry per block of kRows rows (128 or 256) of a
+// sequence, the longest key ranges first, so that the persistent kernel's snake
+// order deals every CTA about the same number of key tiles whatever the lengths
+// are.
+//
+// Blocks are found without a scan: block t of sequence b has the slot
+// cu[b] / kRows + b + t, slots of different sequences never meet (a sequence of
+// L rows from row c on has at most (c + L) / kRows - c / kRows + 1 blocks), and
+// the sequence of a slot is found by a search over cu[b] / kRows + b, which
+// grows with b.  A counting sort over at most 1024 length classes then orders them.
+constexpr int kPlanThreads = 1024;
+constexpr int kBins = 1024;
+
+struct __align__(16) Block {
+    int start, len;    // rows of the sequence
+    int row;           // the block's first row in it
+    int pad;
+};
+
+template <int kRows>
+__global__ void __launch_bounds__(kPlanThreads) k_packed_plan(const int32_t* __restrict__ cu, int n_seq,
+                                                              int T, int slots, int shift, int window_blocks,
+                                                              int* __restrict__ count,
+                                                              Block* __restrict__ list, int* err) {
+    __shared__ int bins[kBins];
+    __shared__ int warp_sum[kPlanThreads / 32];
+    pdl_wait();
+    pdl_trigger();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    bins[tid] = 0;
+    for (int b = tid; b < n_seq; b += kPlanThreads) {
+        const int s = __ldg(cu + b), e = __ldg(cu + b + 1);
+        if (s < 0 || s > e || e > T) raise_error(err, TFM_EINVAL);
+    }
+    __syncthreads();
+    // block of slot s, and its length class; false: the slot is empty
+    auto find = [&](int s, Block& blk, int& bin) -> bool {
+        int lo = 0, hi = n_seq;                       // the last b with cu[b] / kRows + b <= s
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (__ldg(cu + mid) / kRows + mid <= s) lo = mid + 1; else hi = mid;
+        }
+        if (lo == 0) return false;
+        const int b = lo - 1;
+        const SeqRange r = seq_range(cu, b, T);
+        const int t = s - (r.start / kRows + b);
+        if (t < 0 || (int64_t)t * kRows >= r.len) return false;
+        blk = Block{r.start, r.len, t * kRows, 0};
+        bin = kBins - 1 - ((t < window_blocks ? t : window_blocks) >> shift);
+        return true;
+    };
+    Block blk;
+    int bin;
+    for (int s = tid; s < slots; s += kPlanThreads)
+        if (find(s, blk, bin)) atomicAdd(&bins[bin], 1);
+    __syncthreads();
+    // exclusive sums of the classes' counts
+    const int n = bins[tid];
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    bins[tid] = before + sum - n;
+    if (tid == kPlanThreads - 1) *count = before + sum;
+    __syncthreads();
+    for (int s = tid; s < slots; s += kPlanThreads)
+        if (find(s, blk, bin)) list[atomicAdd(&bins[bin], 1)] = blk;
+}
+
+// ------------------------------------------------------------------ tensor cores
+constexpr int kQ = 128;
+constexpr int kKV = 128;
+constexpr int kThreadsP = 384;          // control, softmax of tile A, softmax of tile B
+constexpr float kRescale = 8.0f;        // log2 units: P entries stay below 2^8
+constexpr int kPoison = 8;
+
+template <int DH>
+struct Pk {
+    // d_head 128: S and O of two tiles fill tensor memory, P takes the place of S
+    static constexpr bool kAlias = DH == 128;
+    static constexpr int kRowBytes = DH >= 64 ? 128 : 64;   // of a shared-memory tile
+    static constexpr int kSub = DH / 64 > 1 ? DH / 64 : 1;  // 64-column sub-tiles
+    static constexpr int kTile = kQ * DH * 2;               // bytes of a Q, K or V tile
+    static constexpr int kNQ = DH == 128 ? 3 : 4;
+    static constexpr int kSK = DH == 128 ? 2 : (DH == 64 ? 4 : 6);
+    static constexpr int kSV = kSK;
+    static constexpr int kKOff = kNQ * kTile;
+    static constexpr int kVOff = kKOff + kSK * kTile;
+    static constexpr int kBarOff = kVOff + kSV * kTile;
+    static constexpr int kNumBars = 2 * (kNQ + kSK + kSV) + kSV + 9;
+    static constexpr int kMiscOff = kBarOff + 8 * kNumBars;
+    static constexpr int kBytes = kMiscOff + 16 + 4 * kPoison + 1024;
+    // tensor-memory columns: S (2 x 128), O (2 x DH), P (2 x 64, or in S's place)
+    static constexpr int kOCol = 2 * kKV;
+    __host__ __device__ static constexpr int p_col(int x) { return kAlias ? x * kKV : kOCol + 2 * DH + x * (kKV / 2); }
+    static constexpr uint32_t kSwz = DH == 32 ? 4u : 2u;
+    static constexpr uint32_t kGroup = 8 * kRowBytes;
+    static_assert(kBytes <= 232448, "shared memory budget");
+    static_assert(kAlias ? kOCol + 2 * DH <= 512 : p_col(1) + kKV / 2 <= 512, "tensor memory budget");
+};
+
+// Both tiles of an item read key tiles j0 + j, j in [0, nmax); tile x those with
+// lo[x] <= j < n[x] (n[1] = 0: there is no tile B).
+struct Item {
+    int start, len, row[2], h[2], g, j0, lo[2], n[2], nmax;
+};
+
+struct PackedGeom {
+    int group, subs;       // subs: items per block (H / 2 pairs of heads, or H heads)
+    int by_heads;          // 1: two heads of one tile, 0: two tiles of one head
+    int window;
+};
+
+template <bool kWin>
+__device__ __forceinline__ void make_item(Item& it, const int4 blk, int sub, const PackedGeom& gm) {
+    it.start = blk.x;
+    it.len = blk.y;
+    it.row[0] = blk.z;
+    it.h[0] = gm.by_heads ? 2 * sub : sub;
+    it.h[1] = gm.by_heads ? it.h[0] + 1 : sub;
+    it.g = it.h[0] / gm.group;
+    it.row[1] = gm.by_heads ? blk.z : blk.z + kQ;
+    const bool two = it.row[1] < it.len;
+    const int wsA = it.row[0] - gm.window + 1, wsB = it.row[1] - gm.window + 1;
+    const int jA = (kWin && wsA > 0) ? wsA / kKV : 0, jB = (kWin && wsB > 0) ? wsB / kKV : 0;
+    it.j0 = jA;
+    it.lo[0] = 0;
+    it.n[0] = it.row[0] / kQ + 1 - jA;
+    it.lo[1] = two ? jB - jA : 0;
+    it.n[1] = two ? it.row[1] / kQ + 1 - jA : 0;
+    it.nmax = it.n[1] > it.n[0] ? it.n[1] : it.n[0];
+}
+
+// Whether key tile j of the item holds a key that some row of it does not see:
+// the diagonals, and with a window the tiles that start before some row's window.
+template <bool kWin>
+__device__ __forceinline__ bool masked_tile(const Item& it, int j, int window) {
+    const int k0 = (it.j0 + j) * kKV;
+    return k0 == it.row[0] || (it.n[1] && k0 == it.row[1]) ||
+           (kWin && k0 < it.row[it.n[1] ? 1 : 0] + kQ - window);
+}
+
+template <int DH, bool kWin>
+__global__ void __launch_bounds__(kThreadsP, 1)
+    k_packed_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap vmap, const __nv_bfloat16* __restrict__ v,
+                __nv_bfloat16* __restrict__ o, const int* __restrict__ count,
+                const Block* __restrict__ list, PackedGeom gm, int64_t vt, int64_t vh, int64_t ot,
+                int64_t oh, float scale_log2, int* err) {
+    using L = Pk<DH>;
+    constexpr int NQ = L::kNQ, SK = L::kSK, SV = L::kSV;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - raw);
+    const uint32_t sQ = base, sK = base + L::kKOff, sV = base + L::kVOff, bars = base + L::kBarOff;
+    auto q_full = [&](int s) { return bars + 8u * s; };
+    auto q_empty = [&](int s) { return bars + 8u * (NQ + s); };
+    auto k_full = [&](int s) { return bars + 8u * (2 * NQ + s); };
+    auto k_empty = [&](int s) { return bars + 8u * (2 * NQ + SK + s); };
+    auto v_full = [&](int s) { return bars + 8u * (2 * NQ + 2 * SK + s); };
+    auto v_empty = [&](int s) { return bars + 8u * (2 * NQ + 2 * SK + SV + s); };
+    constexpr int B0 = 2 * (NQ + SK + SV);
+    auto s_full = [&](int x) { return bars + 8u * (B0 + x); };
+    auto s_free = [&](int x) { return bars + 8u * (B0 + 2 + x); };
+    auto p_full = [&](int x) { return bars + 8u * (B0 + 4 + x); };
+    auto o_done = [&](int x) { return bars + 8u * (B0 + 6 + x); };
+    const uint32_t done_bar = bars + 8u * (B0 + 8);
+    auto v_clean = [&](int s) { return bars + 8u * (B0 + 9 + s); };
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(gbase + L::kMiscOff);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMiscOff + 4);
+    volatile int* poison = reinterpret_cast<volatile int*>(gbase + L::kMiscOff + 16);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < NQ; ++s) {
+            mbar_init(q_full(s), 1);
+            mbar_init(q_empty(s), 1);
+        }
+        for (int s = 0; s < SK; ++s) {
+            mbar_init(k_full(s), 1);
+            mbar_init(k_empty(s), 1);
+        }
+        for (int s = 0; s < SV; ++s) {
+            mbar_init(v_full(s), 1);
+            mbar_init(v_empty(s), 1);
+            mbar_init(v_clean(s), 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(s_full(x), 1);
+            mbar_init(s_free(x), 4);
+            mbar_init(p_full(x), 4);
+            mbar_init(o_done(x), 1);
+        }
+        mbar_init(done_bar, L::kAlias ? 1 : 2);
+        *abort_flag = 0;
+        for (int i = 0; i < kPoison; ++i) poison[i] = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&qmap);
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+    }
+    if (warp == 1) tmem_alloc(smem_u32(tmem_holder), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    pdl_wait();
+    pdl_trigger();
+
+    // Items are dealt round by round in snake order (even rounds c, odd rounds
+    // G-1-c); every role walks the same sequence, loading the entry of its next
+    // item while it works on the current one.
+    const int total = __ldg(count) * gm.subs;
+    const int G = (int)gridDim.x, c = (int)blockIdx.x;
+    const int rounds = (total + G - 1) / G;
+    auto index_of = [&](int rnd) { return rnd * G + ((rnd & 1) ? G - 1 - c : c); };
+    auto entry = [&](int rnd) -> int4 {
+        const int idx = index_of(rnd);
+        if (rnd >= rounds || idx >= total) return make_int4(0, 0, 0, -1);
+        return __ldg(reinterpret_cast<const int4*>(list) + idx / gm.subs);
+    };
+    int4 ahead = entry(0);
+    int at_round = 0;
+    // The next item; false when there is none.
+    auto next_item = [&](Item& it) -> bool {
+        const int4 e = ahead;
+        if (e.w < 0) return false;                    // only the last round can be short
+        make_item<kWin>(it, e, index_of(at_round) % gm.subs, gm);
+        ahead = entry(++at_round);
+        return true;
+    };
+
+    constexpr uint32_t idesc_s = umma_idesc_bf16(kQ, kKV);
+    constexpr uint32_t idesc_o = umma_idesc_bf16(kQ, DH, true);
+    // Q, K: K-major tiles in 64-column sub-tiles of 16 KB; V: MN-major
+    const uint64_t dq = sdesc(sQ, L::kSwz, 16, L::kGroup), dk = sdesc(sK, L::kSwz, 16, L::kGroup);
+    const uint64_t dv = sdesc(sV, L::kSwz, DH > 64 ? 16384 : 0, L::kGroup);
+    auto issue_s = [&](int x, int qs, int ks) {
+        const uint64_t a0 = dq + (uint64_t)(qs * (L::kTile >> 4)), b0 = dk + (uint64_t)(ks * (L::kTile >> 4));
+#pragma unroll
+        for (int kk = 0; kk < DH / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+            umma_bf16(tmem_base + x * kKV, a0 + off, b0 + off, idesc_s, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(s_full(x));
+    };
+    auto issue_pv = [&](int x, int vs, bool first) {
+        const uint64_t b0 = dv + (uint64_t)(vs * (L::kTile >> 4));
+#pragma unroll
+        for (int kk = 0; kk < kKV / 16; ++kk)
+            umma_bf16_ts(tmem_base + L::kOCol + x * DH, tmem_base + L::p_col(x) + kk * 8,
+                         b0 + kk * ((16 * L::kRowBytes) >> 4), idesc_o, (!first || kk > 0) ? 1u : 0u);
+    };
+
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 0) {
+        // ---------------------------------------------------------- TMA producer
+        // Per item Q_A, Q_B and K_0, then V_j, K_{j+1}, the order in which the
+        // MMA threads take them.  It leaves once its last copies have landed.
+        if (lane == 0) {
+            int qn = 0, kn = 0, vn = 0;
+            bool ok = true;
+            Item it;
+            auto load = [&](uint32_t dst, const CUtensorMap* map, int row, int head, uint32_t bar) {
+#pragma unroll
+                for (int s = 0; s < L::kSub; ++s)
+                    tma_load_3d(dst + s * 16384, map, 64 * s, row, head, bar);
+            };
+            while (ok && next_item(it)) {
+                for (int x = 0; x < 2 && ok; ++x) {
+                    if (it.n[x] == 0) continue;
+                    const int s = qn % NQ;
+                    ok = mbar_wait(q_empty(s), ((uint32_t)(qn / NQ) & 1u) ^ 1u, err, abort_flag);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(q_full(s), L::kTile);
+                    load(sQ + s * L::kTile, &qmap, it.start + it.row[x], it.h[x], q_full(s));
+                    ++qn;
+                }
+                for (int j = 0; j <= it.nmax && ok; ++j) {
+                    if (j > 0) {
+                        const int s = vn % SV;
+                        ok = mbar_wait(v_empty(s), ((uint32_t)(vn / SV) & 1u) ^ 1u, err, abort_flag);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(v_full(s), L::kTile);
+                        load(sV + s * L::kTile, &vmap, it.start + (it.j0 + j - 1) * kKV, it.g, v_full(s));
+                        ++vn;
+                    }
+                    if (j < it.nmax) {
+                        const int s = kn % SK;
+                        ok = mbar_wait(k_empty(s), ((uint32_t)(kn / SK) & 1u) ^ 1u, err, abort_flag);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(k_full(s), L::kTile);
+                        load(sK + s * L::kTile, &kmap, it.start + (it.j0 + j) * kKV, it.g, k_full(s));
+                        ++kn;
+                    }
+                }
+            }
+            for (int k = qn < NQ ? 0 : qn - NQ; k < qn; ++k)
+                mbar_wait(q_full(k % NQ), (uint32_t)(k / NQ) & 1u, err, abort_flag);
+            for (int k = kn < SK ? 0 : kn - SK; k < kn; ++k)
+                mbar_wait(k_full(k % SK), (uint32_t)(k / SK) & 1u, err, abort_flag);
+            for (int k = vn < SV ? 0 : vn - SV; k < vn; ++k)
+                mbar_wait(v_full(k % SV), (uint32_t)(k / SV) & 1u, err, abort_flag);
+        }
+    } else if (warp == 3) {
+        // ---------------------------------------------------------- V check
+        // In a tile that some row does not see whole, P is zero where the row
+        // does not look, but zero times infinity is not: such values are taken
+        // out here (and added back for the rows that see them, in the epilogue).
+        int vn = 0, items = 0;
+        bool ok = true;
+        Item it;
+        for (; ok && next_item(it); ++items)
+            for (int j = 0; j < it.nmax; ++j, ++vn) {
+                // every tile is waited for: a barrier's parity tells only its last phase
+                const int s = vn % SV;
+                if (!(ok = warp_wait(v_full(s), (uint32_t)(vn / SV) & 1u, err, abort_flag))) break;
+                if (!masked_tile<kWin>(it, j, gm.window)) continue;
+                const uint32_t at = sV + s * L::kTile + lane * 16;
+                bool found = false;
+#pragma unroll 1
+                for (int i = 0; i < L::kTile; i += 4 * 512) {
+                    uint4 w[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) w[u] = ld_shared_v4(at + i + u * 512);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const uint32_t bx = __vcmpeq2(w[u].x & 0x7F807F80u, 0x7F807F80u);
+                        const uint32_t by = __vcmpeq2(w[u].y & 0x7F807F80u, 0x7F807F80u);
+                        const uint32_t bz = __vcmpeq2(w[u].z & 0x7F807F80u, 0x7F807F80u);
+                        const uint32_t bw = __vcmpeq2(w[u].w & 0x7F807F80u, 0x7F807F80u);
+                        if (bx | by | bz | bw) {
+                            found = true;
+                            st_shared_v4(at + i + u * 512, w[u].x & ~bx, w[u].y & ~by, w[u].z & ~bz,
+                                         w[u].w & ~bw);
+                        }
+                    }
+                }
+                if (__any_sync(0xffffffffu, found)) {
+                    if (lane == 0) poison[items % kPoison] = items + 1;
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(v_clean(s));
+            }
+    } else if (L::kAlias && warp == 1) {
+        // ---------------------------------------------------------- MMAs, one thread
+        // A round is one key tile.  Behind P_x.V of a round comes S_x of the next
+        // (of the same or the next item), which overwrites P_x: MMAs of one
+        // thread complete in the order they are issued.  While the softmax works
+        // on one tile, the other one's P.V and S run.
+        if (lane == 0) {
+            bool ok = true;
+            int kn = 0, vn = 0, qn = 0, pc[2] = {0, 0};
+            uint32_t clean = 0;                        // a V slot's checks so far, modulo 2
+            Item cur, nxt;
+            bool has = next_item(cur);
+            int qs[2] = {0, 0};
+            auto open_item = [&](const Item& it) {     // Q slots of an item
+                for (int x = 0; x < 2; ++x)
+                    if (it.n[x]) qs[x] = qn++;
+            };
+            auto do_s = [&](const Item& it, int j, int x) {
+                if (j < it.lo[x] || j >= it.n[x]) return;
+                const int s = qs[x] % NQ;
+                if (j == it.lo[x]) ok = ok && mbar_wait(q_full(s), (uint32_t)(qs[x] / NQ) & 1u, err, abort_flag);
+                ok = ok && mbar_wait(k_full(kn % SK), (uint32_t)(kn / SK) & 1u, err, abort_flag);
+                if (!ok) return;
+                tc_fence_after();
+                issue_s(x, s, kn % SK);
+                if (j == it.n[x] - 1) umma_commit(q_empty(s));
+            };
+            if (has) {
+                open_item(cur);
+                do_s(cur, 0, 0);
+                do_s(cur, 0, 1);
+                if (ok) umma_commit(k_empty(kn % SK));
+                ++kn;
+            }
+            while (has && ok) {
+                bool has_next = false;
+                for (int j = 0; j < cur.nmax && ok; ++j, ++vn) {
+                    const bool last = j == cur.nmax - 1;
+                    if (last) {
+                        has_next = next_item(nxt);
+                        if (has_next) open_item(nxt);
+                    }
+                    const bool ahead_s = !last || has_next;
+                    const Item& si = last ? nxt : cur;
+                    const int sj = last ? 0 : j + 1;
+                    ok = mbar_wait(v_full(vn % SV), (uint32_t)(vn / SV) & 1u, err, abort_flag);
+                    if (ok && masked_tile<kWin>(cur, j, gm.window)) {
+                        ok = mbar_wait(v_clean(vn % SV), (clean >> (vn % SV)) & 1u, err, abort_flag);
+                        clean ^= 1u << (vn % SV);
+                    }
+                    for (int x = 0; x < 2 && ok; ++x) {
+                        if (j >= cur.lo[x] && j < cur.n[x]) {
+                            ok = mbar_wait(p_full(x), (uint32_t)pc[x] & 1u, err, abort_flag);
+                            if (!ok) break;
+                            ++pc[x];
+                            tc_fence_after();
+                            issue_pv(x, vn % SV, j == cur.lo[x]);
+                            if (j == cur.n[x] - 1) umma_commit(o_done(x));
+                        }
+                        if (x == 1) umma_commit(v_empty(vn % SV));
+                        if (ahead_s) do_s(si, sj, x);
+                    }
+                    if (ok && ahead_s) {
+                        umma_commit(k_empty(kn % SK));
+                        ++kn;
+                    }
+                }
+                has = has_next;
+                cur = nxt;
+            }
+            umma_commit(done_bar);
+            mbar_wait(done_bar, 0, err, abort_flag);
+        }
+    } else if (!L::kAlias && warp == 1) {
+        // ---------------------------------------------------------- S MMAs
+        // S_x of the next tile as soon as the softmax has read the last one into
+        // registers (P has columns of its own).
+        if (lane == 0) {
+            bool ok = true;
+            int kn = 0, qn = 0, cnt[2] = {0, 0};
+            Item it;
+            while (ok && next_item(it)) {
+                int qs[2] = {0, 0};
+                for (int x = 0; x < 2; ++x)
+                    if (it.n[x]) qs[x] = qn++;
+                for (int j = 0; j < it.nmax && ok; ++j, ++kn) {
+                    ok = mbar_wait(k_full(kn % SK), (uint32_t)(kn / SK) & 1u, err, abort_flag);
+                    for (int x = 0; x < 2 && ok; ++x) {
+                        if (j < it.lo[x] || j >= it.n[x]) continue;
+                        const int s = qs[x] % NQ;
+                        if (j == it.lo[x]) ok = mbar_wait(q_full(s), (uint32_t)(qs[x] / NQ) & 1u, err, abort_flag);
+                        if (ok && cnt[x] > 0) ok = mbar_wait(s_free(x), (uint32_t)(cnt[x] - 1) & 1u, err, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_s(x, s, kn % SK);
+                        if (j == it.n[x] - 1) umma_commit(q_empty(s));
+                        ++cnt[x];
+                    }
+                    if (ok) umma_commit(k_empty(kn % SK));
+                }
+            }
+            umma_commit(done_bar);
+            mbar_wait(done_bar, 0, err, abort_flag);
+        }
+    } else if (!L::kAlias && warp == 2) {
+        // ---------------------------------------------------------- P.V MMAs
+        if (lane == 0) {
+            bool ok = true;
+            int vn = 0, cnt[2] = {0, 0};
+            uint32_t clean = 0;                        // a V slot's checks so far, modulo 2
+            Item it;
+            while (ok && next_item(it))
+                for (int j = 0; j < it.nmax && ok; ++j, ++vn) {
+                    ok = mbar_wait(v_full(vn % SV), (uint32_t)(vn / SV) & 1u, err, abort_flag);
+                    if (ok && masked_tile<kWin>(it, j, gm.window)) {
+                        ok = mbar_wait(v_clean(vn % SV), (clean >> (vn % SV)) & 1u, err, abort_flag);
+                        clean ^= 1u << (vn % SV);
+                    }
+                    for (int x = 0; x < 2 && ok; ++x) {
+                        if (j < it.lo[x] || j >= it.n[x]) continue;
+                        ok = mbar_wait(p_full(x), (uint32_t)cnt[x] & 1u, err, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_pv(x, vn % SV, j == it.lo[x]);
+                        umma_commit(o_done(x));
+                        ++cnt[x];
+                    }
+                    if (ok) umma_commit(v_empty(vn % SV));
+                }
+            umma_commit(done_bar);
+            mbar_wait(done_bar, 0, err, abort_flag);
+        }
+    }
+    } else {
+        // ---------------------------------------------------------- softmax (warps 4..11)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int x = (warp >> 2) - 1;                 // 0: tile A, 1: tile B
+        const int q4 = warp & 3;
+        const int r = q4 * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+        const uint32_t t_s = tmem_base + x * kKV + lane_off;
+        const uint32_t t_o = tmem_base + L::kOCol + x * DH + lane_off;
+        const uint32_t t_p = tmem_base + L::p_col(x) + lane_off;
+        int cnt = 0, items = 0, outs = 0;              // tiles of this x, items, items with this x
+        bool ok = true;
+        Item it;
+        for (; ok && next_item(it); ++items) {
+            const int n = it.n[x];
+            if (n == 0) continue;
+            const int row0 = it.row[x], qi = row0 + r;
+            const int kmin = kWin ? qi - gm.window + 1 : 0;
+            const int win_lo = kWin ? row0 + kQ - gm.window : INT_MIN;
+            float m = -INFINITY, l = 0.f;
+            for (int j = it.lo[x]; j < n && ok; ++j, ++cnt) {
+                if (!warp_wait(s_full(x), (uint32_t)cnt & 1u, err, abort_flag)) { ok = false; break; }
+                tc_fence_after();
+                uint32_t sr[kKV / 32][32];
+#pragma unroll
+                for (int cc = 0; cc < kKV / 32; ++cc) tmem_ld32_issue(t_s + cc * 32, sr[cc]);
+                tmem_ld_wait();
+                if (!L::kAlias) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_free(x));
+                }
+                float s[kKV];
+#pragma unroll
+                for (int cc = 0; cc < kKV / 32; ++cc) {
+                    reg_fence32(sr[cc]);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) s[cc * 32 + e] = __uint_as_float(sr[cc][e]);
+                }
+                const int k0 = (it.j0 + j) * kKV;
+                // A row of the sequence sees keys up to itself, which lie in the
+                // sequence: the diagonal masks the next sequence's keys too.
+                if (k0 == row0) {
+#pragma unroll
+                    for (int cc = 0; cc < kKV; ++cc) s[cc] = cc > r ? -INFINITY : s[cc];
+                }
+                if (kWin && k0 < win_lo) {
+                    const int lo = kmin - k0;
+#pragma unroll
+                    for (int cc = 0; cc < kKV; ++cc) s[cc] = cc < lo ? -INFINITY : s[cc];
+                }
+                float mx4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int cc = 4; cc < kKV; cc += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx4[e] = fmax3(mx4[e], s[cc + 2 * e], s[cc + 2 * e + 1]);
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * scale_log2;
+                float corr = 1.f;
+                if (mx > m + kRescale) {
+                    corr = fast_exp2(m - mx);
+                    m = mx;
+                }
+                const bool need_rescale = __any_sync(0xffffffffu, corr != 1.f && j > it.lo[x]);
+                const uint64_t scale2 = f2_pack(scale_log2, scale_log2);
+                const float negm = (kWin && m == -INFINITY) ? 0.f : -m;
+                const uint64_t negm2 = f2_pack(negm, negm);
+                uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
+                uint32_t pw[kKV / 64][32];
+#pragma unroll
+                for (int h64 = 0; h64 < kKV / 64; ++h64) {
+#pragma unroll
+                    for (int e = 0; e < 64; e += 2) {
+                        float t0, t1;
+                        const int cc = h64 * 64 + e;
+                        f2_unpack(f2_fma(f2_pack(s[cc], s[cc + 1]), scale2, negm2), t0, t1);
+                        const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
+                        sum2[(e >> 1) & 3] = f2_add(sum2[(e >> 1) & 3], f2_pack(p0, p1));
+                        pw[h64][e >> 1] = pack_bf16x2(p0, p1);
+                    }
+                }
+                // P.V of the previous tile must be complete before P and O are
+                // written; in S's place it is, as S comes behind it.
+                if (!L::kAlias) {
+                    if (cnt > 0 && !warp_wait(o_done(x), (uint32_t)(cnt - 1) & 1u, err, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                }
+#pragma unroll
+                for (int h64 = 0; h64 < kKV / 64; ++h64) tmem_st32_async(t_p + h64 * 32, pw[h64]);
+                tmem_st_wait();
+                float sa[4], sb[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f2_unpack(sum2[e], sa[e], sb[e]);
+                const float sum = ((sa[0] + sb[0]) + (sa[1] + sb[1])) + ((sa[2] + sb[2]) + (sa[3] + sb[3]));
+                l = l * corr + sum;
+                if (need_rescale) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int cc = 0; cc < DH / 32; ++cc) {
+                        float ov[32];
+                        tmem_ld32(t_o + cc * 32, ov);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) ov[e] *= corr;
+                        tmem_st32(t_o + cc * 32, ov);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(x));
+            }
+            if (!ok) break;
+            ok = warp_wait(o_done(x), (uint32_t)(L::kAlias ? outs : cnt - 1) & 1u, err, abort_flag);
+            ++outs;
+            if (!ok) break;
+            tc_fence_after();
+            const float inv = 1.0f / l;
+            const bool fix = poison[items % kPoison] == items + 1;
+            __nv_bfloat16* orow = o + (int64_t)(it.start + qi) * ot + (int64_t)it.h[x] * oh;
+#pragma unroll 1
+            for (int cc = 0; cc < DH / 32; ++cc) {
+                float ov[32];
+                tmem_ld32(t_o + cc * 32, ov);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) ov[e] *= inv;
+                if (fix && qi < it.len) {
+                    // what the V check took out, for the keys this row sees
+                    for (int j = it.lo[x]; j < n; ++j) {
+                        if (!masked_tile<kWin>(it, j, gm.window)) continue;
+                        const int k0 = (it.j0 + j) * kKV;
+                        for (int key = max(k0, kWin ? kmin : 0); key <= min(k0 + kKV - 1, qi); ++key) {
+                            const __nv_bfloat16* vr = v + (int64_t)(it.start + key) * vt + (int64_t)it.g * vh + cc * 32;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const float w = __bfloat162float(vr[e]);
+                                if (!(fabsf(w) < INFINITY)) ov[e] += w;
+                            }
+                        }
+                    }
+                }
+                if (qi < it.len) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint4 w;
+                        w.x = pack_bf16x2(ov[e], ov[e + 1]);
+                        w.y = pack_bf16x2(ov[e + 2], ov[e + 3]);
+                        w.z = pack_bf16x2(ov[e + 4], ov[e + 5]);
+                        w.w = pack_bf16x2(ov[e + 6], ov[e + 7]);
+                        *reinterpret_cast<uint4*>(orow + cc * 32 + e) = w;
+                    }
+                }
+                __syncwarp();
+            }
+            // O is read out before this warp publishes the next item's first P
+            tc_fence_before();
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem_base, 512);
+}
+
+template <int DH, bool kWin>
+cudaError_t launch_tc(const PackedArgs& a, const CUtensorMap* maps, const PackedGeom& gm, int slots, cudaStream_t st) {
+    using L = Pk<DH>;
+    cudaError_t e = cudaFuncSetAttribute(k_packed_tc<DH, kWin>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+    if (e != cudaSuccess) return e;
+    const int64_t items = (int64_t)slots * gm.subs;
+    const int grid = items < sm_count() ? (int)items : sm_count();
+    return launch_pdl(k_packed_tc<DH, kWin>, dim3(grid), dim3(kThreadsP), L::kBytes, st, maps[0], maps[1], maps[2],
+                      static_cast<const __nv_bfloat16*>(a.v), static_cast<__nv_bfloat16*>(a.o),
+                      static_cast<const int*>(a.ws),
+                      reinterpret_cast<const Block*>(static_cast<const uint8_t*>(a.ws) + 256), gm,
+                      a.strides[4], a.strides[5], a.strides[6], a.strides[7],
+                      a.scale * 1.4426950408889634f, device_error_word());
+}
+
+template <int DH>
+cudaError_t launch_tc_w(const PackedArgs& a, const CUtensorMap* maps, const PackedGeom& gm, int slots, cudaStream_t st) {
+    return a.window > 0 ? launch_tc<DH, true>(a, maps, gm, slots, st) : launch_tc<DH, false>(a, maps, gm, slots, st);
+}
+
+template <int kRows>
+cudaError_t launch_plan(const PackedArgs& a, int slots, cudaStream_t st) {
+    int shift = 0;
+    while (((a.T / kRows + 1) >> shift) >= kBins) ++shift;
+    // behind a window's length all blocks read the same number of key tiles
+    const int wb = a.window > 0 ? (a.window + kRows - 1) / kRows : INT_MAX;
+    return launch_pdl(k_packed_plan<kRows>, dim3(1), dim3(kPlanThreads), 0, st, a.cu, a.n_seq, a.T, slots, shift, wb,
+                      static_cast<int*>(a.ws), reinterpret_cast<Block*>(static_cast<uint8_t*>(a.ws) + 256),
+                      device_error_word());
 }
 
 }  // namespace
 
-size_t packed_workspace_bytes(int T, int n_seq) { return 256 + 16 * ((size_t)T / 128 + n_seq); }
+// The number of blocks, then the blocks (of 128 rows, or fewer of 256).
+size_t packed_workspace_bytes(int T, int n_seq) { return 256 + sizeof(Block) * ((size_t)T / 128 + n_seq); }
 
 tfm_status launch_packed_attention(const PackedArgs& a, cudaStream_t st, cudaError_t* e) {
-    *e = a.bf16 ? launch_rows<__nv_bfloat16>(a, st) : launch_rows<float>(a, st);
+    if (!a.bf16) {
+        *e = launch_rows(a, st);
+        return TFM_OK;
+    }
+    CUtensorMap maps[3];
+    const void* ptr[3] = {a.q, a.k, a.v};
+    for (int i = 0; i < 3; ++i)
+        if (!rows_heads_map(&maps[i], ptr[i], a.T, i ? a.Hkv : a.H, a.dh, a.strides[2 * i], a.strides[2 * i + 1]))
+            return TFM_ECUDA;
+    PackedGeom gm;
+    gm.group = a.H / a.Hkv;
+    gm.by_heads = gm.group % 2 == 0;
+    gm.subs = gm.by_heads ? a.H / 2 : a.H;
+    gm.window = a.window;
+    const int slots = a.T / (gm.by_heads ? 128 : 256) + a.n_seq;
+    *e = gm.by_heads ? launch_plan<128>(a, slots, st) : launch_plan<256>(a, slots, st);
+    if (*e != cudaSuccess) return TFM_OK;
+    *e = a.dh == 32 ? launch_tc_w<32>(a, maps, gm, slots, st)
+         : a.dh == 64 ? launch_tc_w<64>(a, maps, gm, slots, st)
+                      : launch_tc_w<128>(a, maps, gm, slots, st);
     return TFM_OK;
 }
 
