@@ -155,6 +155,7 @@ tfm_status tfm_prefix_attention(const void* q, const void* k_prefix, const void*
     a.ws = workspace;
     cudaError_t e = cudaSuccess;
     const tfm_status st = tfm::launch_prefix_attention(a, static_cast<cudaStream_t>(stream), &e);
+    if (st == TFM_EINVAL) return fail(st, "B * H * T * prefix_len too large");
     if (st != TFM_OK) return fail(st, "could not encode prefix attention tensor maps");
     return e == cudaSuccess ? TFM_OK : cuda_fail(e, "prefix attention launch");
 }

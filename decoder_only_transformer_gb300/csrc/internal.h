@@ -226,6 +226,9 @@ bool attention_tc_supported(int dh);
 // tiles of box_rows rows of one head.
 bool rows_heads_map(CUtensorMap* map, const void* ptr, int64_t T, int64_t heads, int dh, int64_t token_stride,
                     int64_t head_stride, int box_rows = 128);
+// Tensor map of dense queries [B, Hkv, GT, dh]: boxes of nb sequences' GT rows of
+// one kv head.
+bool query_groups_map(CUtensorMap* map, const void* ptr, int B, int Hkv, int GT, int dh, int nb);
 tfm_status plan_attention_tc(AttnPlan* p, const void* q, const void* k, const void* v, void* o,
                              int B, int H, int Hkv, int S, int dh, float scale);
 cudaError_t launch_attention_tc(const AttnPlan& p, cudaStream_t st);

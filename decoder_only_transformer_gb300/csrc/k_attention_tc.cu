@@ -598,6 +598,22 @@ bool rows_heads_map(CUtensorMap* map, const void* ptr, int64_t T, int64_t heads,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [B, Hkv, GT, dh] bf16, dense, as boxes of nb sequences' GT rows of one kv head.
+bool query_groups_map(CUtensorMap* map, const void* ptr, int B, int Hkv, int GT, int dh, int nb) {
+    EncodeTiledFn fn = att_encode_fn();
+    if (!fn) return false;
+    const cuuint32_t inner = dh >= 64 ? 64 : (cuuint32_t)dh;
+    const cuuint64_t row = (cuuint64_t)dh * 2, group = row * GT;
+    cuuint64_t dims[4] = {(cuuint64_t)dh, (cuuint64_t)GT, (cuuint64_t)Hkv, (cuuint64_t)B};
+    cuuint64_t strides[3] = {row, group, group * Hkv};
+    cuuint32_t box[4] = {inner, (cuuint32_t)GT, 1, (cuuint32_t)nb};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              inner * 2 == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool attention_tc_supported(int dh) { return dh == 32 || dh == 64 || dh == 128; }
 
 tfm_status plan_attention_tc(AttnPlan* p, const void* q, const void* k, const void* v, void* o,

@@ -3,6 +3,23 @@
 //
 // Row (b, h, t): o = sum_j p_j v_j, p = softmax(scale q . k_j) over the keys
 // [0, P) of the prefix and the own keys [0, lens[b] - (T - 1 - t)).
+//
+// The query rows that read the same keys are stacked: for the prefix all
+// sequences' rows of a kv head, 128 at a time, so that its keys and values are
+// read once for the batch; for an own cache the G T rows (G = H / Hkv) of its
+// sequence.  Either way a job is "up to 128 rows against a range of keys", the
+// tile of the tensor cores, and one kernel runs both: S = Q K^T (tcgen05, keys
+// in tiles of 64), softmax with a running maximum, O += P V.  With few rows most
+// of a tile's rows are padding, which costs nothing that counts: a tile of 64
+// keys takes 32 KB of d_head 128 from memory, ~1500 cycles of an SM's share of
+// HBM bandwidth, and its two products ~500.  (On CUDA cores G T = 4 rows would
+// already need ~40 % of all FMAs to keep up with memory.)
+//
+// All tiles of all jobs are laid end to end and cut into equal runs, one per
+// CTA, whatever the lengths are (two CTAs per SM, so that one's loads run during
+// the other's softmax).  A run crosses jobs; each piece of a job leaves (max,
+// sum, unnormalised O) per row, and a second kernel joins a row's pieces of the
+// prefix and its own cache exactly: with M = max m, o = sum 2^(m - M) O / sum 2^(m - M) l.
 #include "common.cuh"
 #include "internal.h"
 
@@ -10,71 +27,724 @@ namespace tfm {
 
 namespace {
 
-// One warp per row.
-__global__ void __launch_bounds__(256) k_prefix_rows(
-    const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ kp,
-    const __nv_bfloat16* __restrict__ vp, const __nv_bfloat16* __restrict__ kc,
-    const __nv_bfloat16* __restrict__ vc, __nv_bfloat16* __restrict__ o,
-    const int32_t* __restrict__ lens, int B, int H, int Hkv, int T, int P, int max_prefix,
-    int max_seq, int dh, float scale, int* err) {
+constexpr int kRowsP = 128;
+constexpr int kKeys = 64;               // keys per tile
+constexpr int kThreadsX = 224;          // 4 softmax warps, TMA, MMA, V check
+constexpr int kMaxCtas = 304;
+constexpr float kRescaleX = 8.0f;       // log2 units: P entries stay below 2^8
+constexpr int kPoisonX = 8;
+
+template <int DH>
+struct Px {
+    static constexpr int kRowBytes = DH >= 64 ? 128 : 64;
+    static constexpr int kSub = DH / 64 > 1 ? DH / 64 : 1;
+    static constexpr int kQ = kRowsP * DH * 2;               // bytes of the Q region
+    static constexpr int kTile = kKeys * DH * 2;             // of a K or V tile
+    static constexpr int kSubTile = kKeys * kRowBytes;
+    static constexpr int kRing = DH == 128 ? 2 : DH == 64 ? 4 : 6;
+    static constexpr int kMaxQ = 8;                          // Q slots of own jobs
+    static constexpr int kKOff = kQ;
+    static constexpr int kVOff = kKOff + kRing * kTile;
+    static constexpr int kBarOff = kVOff + kRing * kTile;
+    static constexpr int kNumBars = 2 * kMaxQ + 5 * kRing + 7;
+    static constexpr int kMiscOff = kBarOff + 8 * kNumBars;
+    static constexpr int kCumOff = kMiscOff + 16 + 4 * kPoisonX;
+    static constexpr int kBase = kCumOff + 1024;             // + 4 (B + 1)
+    static constexpr int kOCol = 2 * kKeys;                  // S 2 x 64 (P in its place), O
+    static constexpr uint32_t kSwz = DH == 32 ? 4u : 2u;
+    static constexpr uint32_t kGroup = 8 * kRowBytes;
+    static_assert(kOCol + DH <= 256, "tensor memory: two CTAs per SM");
+};
+
+// How the work is laid out; the same on the host and in both kernels.
+struct PrefixGeom {
+    int B, Hkv, GT, T, P, max_seq;
+    int nb;            // sequences per row tile of the prefix: nb * GT <= 128
+    int nrt;           // row tiles
+    int np;            // key tiles of the prefix
+    int ctas;
+    int q_slots, q_pad;   // Q slots of own jobs, rows of each (GT padded)
+};
+
+// Run of CTA i of n over u units: [start, end).
+__device__ __forceinline__ int run_start(int i, int u, int n) {
+    const int q = u / n, r = u - q * n;
+    return i * q + min(i, r);
+}
+__device__ __forceinline__ int cta_of(int x, int u, int n) {
+    const int q = u / n, r = u - q * n, split = r * (q + 1);
+    return x < split ? x / (q + 1) : r + (x - split) / q;
+}
+
+__device__ __forceinline__ int own_len(const int32_t* __restrict__ lens, int b, int max_seq) {
+    const int n = __ldg(lens + b);
+    return n < 0 || n > max_seq ? 0 : n;
+}
+
+// A piece of a job: key tiles [t0, t1) of it.
+struct Seg {
+    int own;           // 0: prefix
+    int g, b;          // kv head; first sequence of the row tile, or the sequence
+    int t0, t1;
+    int keys;          // P, or the sequence's length
+    int rows;          // valid rows
+    int job;           // index among the jobs of its kind
+};
+
+struct Walk {
+    int u, end, up;    // next unit, end of the run, units of the prefix
+};
+
+__device__ __forceinline__ bool next_seg(Walk& w, Seg& s, const PrefixGeom& gm, const int* cum,
+                                         const int32_t* __restrict__ lens) {
+    if (w.u >= w.end) return false;
+    if (w.u < w.up) {
+        s.own = 0;
+        s.job = w.u / gm.np;
+        s.t0 = w.u - s.job * gm.np;
+        s.t1 = min(gm.np, s.t0 + w.end - w.u);
+        s.g = s.job / gm.nrt;
+        s.b = (s.job - s.g * gm.nrt) * gm.nb;
+        s.keys = gm.P;
+        s.rows = min(gm.nb, gm.B - s.b) * gm.GT;
+    } else {
+        const int v = w.u - w.up;
+        int lo = 0, hi = gm.B;                        // the last b with cum[b] Hkv <= v and keys
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (cum[mid] * gm.Hkv <= v) lo = mid + 1; else hi = mid;
+        }
+        s.own = 1;
+        s.b = lo - 1;
+        const int nt = cum[lo] - cum[lo - 1], x = v - cum[lo - 1] * gm.Hkv;
+        s.g = x / nt;
+        s.t0 = x - s.g * nt;
+        s.t1 = min(nt, s.t0 + w.end - w.u);
+        s.keys = own_len(lens, s.b, gm.max_seq);
+        s.rows = gm.GT;
+        s.job = s.b * gm.Hkv + s.g;
+    }
+    w.u += s.t1 - s.t0;
+    return true;
+}
+
+// An own tile that holds keys some row does not see: behind the length, or the
+// newest tokens' own.
+__device__ __forceinline__ bool check_tile(const Seg& s, int t, int T) {
+    return s.own && (t + 1) * kKeys > s.keys - (T - 1);
+}
+
+// cum[b]: key tiles of the own caches of sequences before b, by the whole block.
+__device__ __forceinline__ void scan_lengths(int* cum, int* warp_sum, const int32_t* __restrict__ lens,
+                                             const PrefixGeom& gm) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+    int base = 0;
+    for (int b0 = 0; b0 < gm.B; b0 += blockDim.x) {
+        const int b = b0 + tid;
+        int n = b < gm.B ? (own_len(lens, b, gm.max_seq) + kKeys - 1) / kKeys : 0;
+        int sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        if (lane == 31) warp_sum[warp] = sum;
+        __syncthreads();
+        int before = base, all = base;
+        for (int w = 0; w < nw; ++w) {
+            if (w < warp) before += warp_sum[w];
+            all += warp_sum[w];
+        }
+        if (b < gm.B) cum[b + 1] = before + sum;
+        base = all;
+        __syncthreads();
+    }
+    if (tid == 0) cum[0] = 0;
+    __syncthreads();
+}
+
+struct PrefixParts {
+    float* o_prefix;       // [jobs + ctas][128][dh]
+    float2* ml_prefix;     // [jobs + ctas][128]: max (log2), sum
+    float* o_own;          // [B Hkv + ctas][GT][dh]
+    float2* ml_own;        // [B Hkv + ctas][GT]
+    int* cum;              // [B + 1]
+};
+
+template <int DH>
+__global__ void __launch_bounds__(kThreadsX, 2)
+    k_prefix_part(const __grid_constant__ CUtensorMap qpmap, const __grid_constant__ CUtensorMap qomap,
+                  const __grid_constant__ CUtensorMap kpmap, const __grid_constant__ CUtensorMap vpmap,
+                  const __grid_constant__ CUtensorMap kcmap, const __grid_constant__ CUtensorMap vcmap,
+                  const __nv_bfloat16* __restrict__ vc, const int32_t* __restrict__ lens, PrefixGeom gm,
+                  PrefixParts out, float scale_log2, int* err) {
+    using L = Px<DH>;
+    constexpr int R = L::kRing;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - raw);
+    const uint32_t sQ = base, sK = base + L::kKOff, sV = base + L::kVOff, bars = base + L::kBarOff;
+    auto q_full = [&](int s) { return bars + 8u * s; };
+    auto q_empty = [&](int s) { return bars + 8u * (L::kMaxQ + s); };
+    constexpr int B0 = 2 * L::kMaxQ;
+    auto k_full = [&](int s) { return bars + 8u * (B0 + s); };
+    auto k_empty = [&](int s) { return bars + 8u * (B0 + R + s); };
+    auto v_full = [&](int s) { return bars + 8u * (B0 + 2 * R + s); };
+    auto v_empty = [&](int s) { return bars + 8u * (B0 + 3 * R + s); };
+    auto v_clean = [&](int s) { return bars + 8u * (B0 + 4 * R + s); };
+    constexpr int B1 = B0 + 5 * R;
+    auto s_full = [&](int i) { return bars + 8u * (B1 + i); };
+    auto p_full = [&](int i) { return bars + 8u * (B1 + 2 + i); };
+    auto pv_done = [&](int i) { return bars + 8u * (B1 + 4 + i); };
+    const uint32_t done_bar = bars + 8u * (B1 + 6);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(gbase + L::kMiscOff);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMiscOff + 4);
+    volatile int* poison = reinterpret_cast<volatile int*>(gbase + L::kMiscOff + 16);
+    int* cum = reinterpret_cast<int*>(gbase + L::kCumOff);
+    __shared__ int warp_sum[kThreadsX / 32];
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 4 && lane == 0) {
+        for (int s = 0; s < L::kMaxQ; ++s) {
+            mbar_init(q_full(s), 1);
+            mbar_init(q_empty(s), 1);
+        }
+        for (int s = 0; s < R; ++s) {
+            mbar_init(k_full(s), 1);
+            mbar_init(k_empty(s), 1);
+            mbar_init(v_full(s), 1);
+            mbar_init(v_empty(s), 1);
+            mbar_init(v_clean(s), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full(i), 1);
+            mbar_init(p_full(i), 4);
+            mbar_init(pv_done(i), 1);
+        }
+        mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        for (int i = 0; i < kPoisonX; ++i) poison[i] = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&qpmap);
+        tma_prefetch_desc(&qomap);
+        tma_prefetch_desc(&kpmap);
+        tma_prefetch_desc(&vpmap);
+        tma_prefetch_desc(&kcmap);
+        tma_prefetch_desc(&vcmap);
+    }
+    if (warp == 5) tmem_alloc(smem_u32(tmem_holder), 256);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    pdl_wait();
+    pdl_trigger();
+    scan_lengths(cum, warp_sum, lens, gm);
+    const int cta = (int)blockIdx.x;
+    if (cta == 0)
+        for (int b = threadIdx.x; b <= gm.B; b += kThreadsX) {
+            out.cum[b] = cum[b];
+            if (b < gm.B && (lens[b] < 0 || lens[b] > gm.max_seq)) raise_error(err, TFM_EINVAL);
+        }
+    const int up = gm.Hkv * gm.nrt * gm.np, units = up + gm.Hkv * cum[gm.B];
+    Walk walk{run_start(cta, units, gm.ctas), run_start(cta + 1, units, gm.ctas), up};
+    const int tiles = walk.end - walk.u;               // of this CTA, in all its pieces
+
+    // Q slots: a piece of the prefix takes the whole region (slot 0's barriers),
+    // own pieces take q_slots slots in turn, the first after a prefix piece slot 0
+    // (a run has its pieces of the prefix first).
+    if (warp == 4) {
+        // ---------------------------------------------------------- TMA producer
+        // Q of a piece before its first K; K_{n+1} before V_n, the order in which
+        // the MMA thread takes them.
+        if (lane == 0) {
+            bool ok = true;
+            int kn = 0, vn = 0, slot = 0;
+            uint32_t q_used = 0, q_par = 0;             // slots used before, their parity
+            Walk wk = walk, wv = walk;
+            Seg sk, sv;
+            int tk = 0, tv = 0;
+            bool hk = next_seg(wk, sk, gm, cum, lens), hv = next_seg(wv, sv, gm, cum, lens);
+            tk = hk ? sk.t0 : 0;
+            tv = hv ? sv.t0 : 0;
+            bool fresh = true;
+            auto load_q = [&]() {
+                const int s = sk.own ? slot : 0;
+                if (q_used >> s & 1u) {
+                    ok = mbar_wait(q_empty(s), (q_par >> s) & 1u, err, abort_flag);
+                    q_par ^= 1u << s;
+                    if (!ok) return;
+                }
+                q_used |= 1u << s;
+                const int rows = sk.own ? gm.GT : gm.nb * gm.GT;
+                mbar_arrive_expect_tx(q_full(s), (uint32_t)rows * DH * 2);
+                const uint32_t dst = sQ + (sk.own ? s * gm.q_pad * DH * 2 : 0);
+                const uint32_t sub = (sk.own ? gm.q_pad : kRowsP) * L::kRowBytes;
+#pragma unroll
+                for (int c = 0; c < L::kSub; ++c)
+                    asm volatile(
+                        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst + c * sub),
+                        "l"(reinterpret_cast<uint64_t>(sk.own ? &qomap : &qpmap)), "r"(64 * c), "r"(0),
+                        "r"(sk.g), "r"(sk.b), "r"(q_full(s))
+                        : "memory");
+                slot = sk.own ? (s + 1 == gm.q_slots ? 0 : s + 1) : 0;
+            };
+            auto load = [&](const Seg& s, int t, bool is_k, uint32_t dst, uint32_t bar) {
+                mbar_arrive_expect_tx(bar, L::kTile);
+                const CUtensorMap* map = s.own ? (is_k ? &kcmap : &vcmap) : (is_k ? &kpmap : &vpmap);
+                const int z = s.own ? s.b * gm.Hkv + s.g : s.g;
+#pragma unroll
+                for (int c = 0; c < L::kSub; ++c)
+                    tma_load_3d(dst + c * L::kSubTile, map, 64 * c, t * kKeys, z, bar);
+            };
+            for (int n = 0; n <= tiles && ok; ++n) {
+                if (n < tiles) {
+                    if (fresh) load_q();
+                    if (!ok) break;
+                    const int s = kn % R;
+                    if (!(ok = mbar_wait(k_empty(s), ((uint32_t)(kn / R) & 1u) ^ 1u, err, abort_flag))) break;
+                    load(sk, tk, true, sK + s * L::kTile, k_full(s));
+                    ++kn;
+                    fresh = ++tk == sk.t1;
+                    if (fresh) {
+                        hk = next_seg(wk, sk, gm, cum, lens);
+                        tk = hk ? sk.t0 : 0;
+                    }
+                }
+                if (n > 0) {
+                    const int s = vn % R;
+                    if (!(ok = mbar_wait(v_empty(s), ((uint32_t)(vn / R) & 1u) ^ 1u, err, abort_flag))) break;
+                    load(sv, tv, false, sV + s * L::kTile, v_full(s));
+                    ++vn;
+                    if (++tv == sv.t1) {
+                        hv = next_seg(wv, sv, gm, cum, lens);
+                        tv = hv ? sv.t0 : 0;
+                    }
+                }
+            }
+            // nothing may be in flight when the CTA ends
+            for (int k = kn < R ? 0 : kn - R; k < kn; ++k)
+                mbar_wait(k_full(k % R), (uint32_t)(k / R) & 1u, err, abort_flag);
+            for (int k = vn < R ? 0 : vn - R; k < vn; ++k)
+                mbar_wait(v_full(k % R), (uint32_t)(k / R) & 1u, err, abort_flag);
+        }
+    } else if (warp == 5) {
+        // ---------------------------------------------------------- MMAs
+        // S_0, S_1, then P_n.V_n and S_{n+2}, which takes the place of P_n: the
+        // MMAs of one thread complete in the order they are issued.
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = umma_idesc_bf16(kRowsP, kKeys);
+            constexpr uint32_t idesc_o = umma_idesc_bf16(kRowsP, DH, true);
+            const uint64_t dq = sdesc(sQ, L::kSwz, 16, L::kGroup), dk = sdesc(sK, L::kSwz, 16, L::kGroup);
+            const uint64_t dv = sdesc(sV, L::kSwz, DH > 64 ? L::kSubTile : 0, L::kGroup);
+            bool ok = true;
+            int kn = 0, slot = 0, cur_slot = 0;
+            uint32_t q_par = 0, clean = 0;
+            Walk ws = walk, wp = walk;
+            Seg ss, sp;
+            int ts = 0, tp = 0;
+            bool fresh = true;
+            auto do_s = [&]() {
+                if (fresh) {
+                    if (!next_seg(ws, ss, gm, cum, lens)) return;
+                    ts = ss.t0;
+                    cur_slot = ss.own ? slot : 0;
+                    slot = ss.own ? (cur_slot + 1 == gm.q_slots ? 0 : cur_slot + 1) : 0;
+                    if (!(ok = mbar_wait(q_full(cur_slot), (q_par >> cur_slot) & 1u, err, abort_flag))) return;
+                    q_par ^= 1u << cur_slot;
+                }
+                const int s = kn % R;
+                if (!(ok = mbar_wait(k_full(s), (uint32_t)(kn / R) & 1u, err, abort_flag))) return;
+                tc_fence_after();
+                const uint64_t a0 = dq + (uint64_t)((ss.own ? cur_slot * gm.q_pad * DH * 2 : 0) >> 4);
+                const uint32_t asub = ((ss.own ? gm.q_pad : kRowsP) * L::kRowBytes) >> 4;
+                const uint64_t b0 = dk + (uint64_t)((s * L::kTile) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < DH / 16; ++kk)
+                    umma_bf16(tmem_base + (kn & 1) * kKeys, a0 + (kk >> 2) * asub + (kk & 3) * 2,
+                              b0 + (kk >> 2) * (L::kSubTile >> 4) + (kk & 3) * 2, idesc_s, kk > 0 ? 1u : 0u);
+                umma_commit(k_empty(s));
+                umma_commit(s_full(kn & 1));
+                ++kn;
+                fresh = ++ts == ss.t1;
+                if (fresh) umma_commit(q_empty(cur_slot));
+            };
+            if (tiles > 0) do_s();
+            if (ok && tiles > 1) do_s();
+            bool hp = next_seg(wp, sp, gm, cum, lens);
+            tp = hp ? sp.t0 : 0;
+            for (int n = 0; n < tiles && ok; ++n) {
+                const int s = n % R;
+                if (!(ok = mbar_wait(v_full(s), (uint32_t)(n / R) & 1u, err, abort_flag))) break;
+                if (check_tile(sp, tp, gm.T)) {
+                    if (!(ok = mbar_wait(v_clean(s), (clean >> s) & 1u, err, abort_flag))) break;
+                    clean ^= 1u << s;
+                }
+                if (!(ok = mbar_wait(p_full(n & 1), (uint32_t)(n >> 1) & 1u, err, abort_flag))) break;
+                tc_fence_after();
+                const uint64_t b0 = dv + (uint64_t)((s * L::kTile) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 16; ++kk)
+                    umma_bf16_ts(tmem_base + L::kOCol, tmem_base + (n & 1) * kKeys + kk * 8,
+                                 b0 + kk * ((16 * L::kRowBytes) >> 4), idesc_o,
+                                 (tp > sp.t0 || kk > 0) ? 1u : 0u);
+                umma_commit(v_empty(s));
+                umma_commit(pv_done(n & 1));
+                if (++tp == sp.t1) {
+                    hp = next_seg(wp, sp, gm, cum, lens);
+                    tp = hp ? sp.t0 : 0;
+                }
+                if (n + 2 < tiles) do_s();
+            }
+            umma_commit(done_bar);
+            mbar_wait(done_bar, 0, err, abort_flag);
+        }
+    } else if (warp == 6) {
+        // ---------------------------------------------------------- V check
+        // Values that are not finite are taken out of the tiles whose keys some
+        // row does not see (zero times infinity is not zero) and added back in
+        // the epilogue for the rows that do.
+        Walk wv = walk;
+        Seg sv;
+        bool ok = true;
+        int n = 0;
+        for (int seg = 0; ok && next_seg(wv, sv, gm, cum, lens); ++seg)
+            for (int t = sv.t0; t < sv.t1; ++t, ++n) {
+                const int s = n % R;
+                if (!(ok = warp_wait(v_full(s), (uint32_t)(n / R) & 1u, err, abort_flag))) break;
+                if (!check_tile(sv, t, gm.T)) continue;
+                const uint32_t at = sV + s * L::kTile + lane * 16;
+                bool found = false;
+#pragma unroll 1
+                for (int i = 0; i < L::kTile; i += 4 * 512) {
+                    uint4 w[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) w[x] = ld_shared_v4(at + i + x * 512);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t bx = __vcmpeq2(w[x].x & 0x7F807F80u, 0x7F807F80u);
+                        const uint32_t by = __vcmpeq2(w[x].y & 0x7F807F80u, 0x7F807F80u);
+                        const uint32_t bz = __vcmpeq2(w[x].z & 0x7F807F80u, 0x7F807F80u);
+                        const uint32_t bw = __vcmpeq2(w[x].w & 0x7F807F80u, 0x7F807F80u);
+                        if (bx | by | bz | bw) {
+                            found = true;
+                            st_shared_v4(at + i + x * 512, w[x].x & ~bx, w[x].y & ~by, w[x].z & ~bz,
+                                         w[x].w & ~bw);
+                        }
+                    }
+                }
+                if (__any_sync(0xffffffffu, found)) {
+                    if (lane == 0) poison[seg % kPoisonX] = seg + 1;
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(v_clean(s));
+            }
+    } else {
+        // ---------------------------------------------------------- softmax (warps 0..3)
+        const int r = warp * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+        const uint32_t t_o = tmem_base + L::kOCol + lane_off;
+        Walk ww = walk;
+        Seg sg;
+        bool ok = true;
+        int n = 0;
+        for (int seg = 0; ok && next_seg(ww, sg, gm, cum, lens); ++seg) {
+            const bool busy = warp * 32 < sg.rows;     // warps without rows only keep step
+            // keys this row sees: all of the prefix, or the own ones up to its token
+            const int lim = sg.own ? sg.keys - (gm.T - 1 - r % gm.T) : sg.keys;
+            float m = -INFINITY, l = 0.f;
+            for (int t = sg.t0; t < sg.t1; ++t, ++n) {
+                const int sb = n & 1;
+                if (!warp_wait(s_full(sb), (uint32_t)(n >> 1) & 1u, err, abort_flag)) { ok = false; break; }
+                tc_fence_after();
+                if (busy) {
+                    const uint32_t t_s = tmem_base + sb * kKeys + lane_off;
+                    uint32_t sr[2][32];
+                    tmem_ld32_issue(t_s, sr[0]);
+                    tmem_ld32_issue(t_s + 32, sr[1]);
+                    tmem_ld_wait();
+                    reg_fence32(sr[0]);
+                    reg_fence32(sr[1]);
+                    float s[kKeys];
+#pragma unroll
+                    for (int e = 0; e < kKeys; ++e) s[e] = __uint_as_float(sr[e >> 5][e & 31]);
+                    const int k0 = t * kKeys;
+                    if (k0 + kKeys > sg.keys - (sg.own ? gm.T - 1 : 0)) {
+                        const int d = lim - k0;
+#pragma unroll
+                        for (int e = 0; e < kKeys; ++e) s[e] = e >= d ? -INFINITY : s[e];
+                    }
+                    float mx4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                    for (int e = 4; e + 8 <= kKeys; e += 8)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mx4[i] = fmax3(mx4[i], s[e + 2 * i], s[e + 2 * i + 1]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mx4[i] = fmaxf(mx4[i], s[kKeys - 4 + i]);
+                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * scale_log2;
+                    float corr = 1.f;
+                    if (mx > m + kRescaleX) {
+                        corr = fast_exp2(m - mx);
+                        m = mx;
+                    }
+                    const bool need_rescale = __any_sync(0xffffffffu, corr != 1.f && t > sg.t0);
+                    const uint64_t scale2 = f2_pack(scale_log2, scale_log2);
+                    const float negm = m == -INFINITY ? 0.f : -m;     // no visible key yet: every p is 0
+                    const uint64_t negm2 = f2_pack(negm, negm);
+                    uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
+                    uint32_t pw[32];
+#pragma unroll
+                    for (int e = 0; e < kKeys; e += 2) {
+                        float t0, t1;
+                        f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), scale2, negm2), t0, t1);
+                        const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
+                        sum2[(e >> 1) & 3] = f2_add(sum2[(e >> 1) & 3], f2_pack(p0, p1));
+                        pw[e >> 1] = pack_bf16x2(p0, p1);
+                    }
+                    tmem_st32_async(t_s, pw);
+                    tmem_st_wait();
+                    float sa[4], sb4[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f2_unpack(sum2[e], sa[e], sb4[e]);
+                    l = l * corr + (((sa[0] + sb4[0]) + (sa[1] + sb4[1])) + ((sa[2] + sb4[2]) + (sa[3] + sb4[3])));
+                    if (need_rescale) {
+                        // O must hold P_{n-1} V_{n-1}
+                        if (!warp_wait(pv_done((n - 1) & 1), (uint32_t)((n - 1) >> 1) & 1u, err, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < DH / 32; ++c) {
+                            float v[32];
+                            tmem_ld32(t_o + c * 32, v);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] *= corr;
+                            tmem_st32(t_o + c * 32, v);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(sb));
+            }
+            if (!ok) break;
+            if (!busy) continue;
+            if (!warp_wait(pv_done((n - 1) & 1), (uint32_t)((n - 1) >> 1) & 1u, err, abort_flag)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const bool fix = poison[seg % kPoisonX] == seg + 1;
+            const int64_t piece = sg.job + cta;
+            const int64_t row = sg.own ? piece * gm.GT + r : piece * kRowsP + r;
+            float* orow = (sg.own ? out.o_own : out.o_prefix) + row * DH;
+            const bool mine = r < sg.rows;
+            if (mine) (sg.own ? out.ml_own : out.ml_prefix)[row] = make_float2(m, l);
+#pragma unroll 1
+            for (int c = 0; c < DH / 32; ++c) {
+                float v[32];
+                tmem_ld32(t_o + c * 32, v);
+                if (mine) {
+                    if (fix) {
+                        const __nv_bfloat16* vb = vc + ((int64_t)sg.b * gm.Hkv + sg.g) * gm.max_seq * DH + c * 32;
+                        for (int t = sg.t0; t < sg.t1; ++t) {
+                            if (!check_tile(sg, t, gm.T)) continue;
+                            for (int key = t * kKeys; key < min((t + 1) * kKeys, lim); ++key)
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) {
+                                    const float w = __bfloat162float(vb[(int64_t)key * DH + e]);
+                                    if (!(fabsf(w) < INFINITY)) v[e] += w;
+                                }
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4*>(orow + c * 32 + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 5) tmem_dealloc(tmem_base, 256);
+}
+
+// One warp per row: lane i takes piece i's maximum and sum, then all lanes add
+// the weighted pieces, dh / 32 columns each.
+template <int DH>
+__global__ void __launch_bounds__(256) k_prefix_join(PrefixParts in, PrefixGeom gm, int H,
+                                                     __nv_bfloat16* __restrict__ o) {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
     const int w = (int)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (w >= B * H * T) return;
-    const int b = w / (H * T), h = (w / T) % H, t = w % T, g = h / (H / Hkv);
-    int len = lens[b];
-    if (len < 0 || len > max_seq) {
-        len = 0;
-        raise_error(err, TFM_EINVAL);
+    const int per_b = gm.Hkv * gm.GT;                  // rows of a sequence: (g, hh, t)
+    if (w >= gm.B * per_b) return;
+    const int b = w / per_b, x = w - b * per_b, g = x / gm.GT, i = x - g * gm.GT;
+    const int up = gm.Hkv * gm.nrt * gm.np, units = up + gm.Hkv * in.cum[gm.B];
+    // pieces of the prefix job, then of the own job, each a run of CTAs
+    int n_pre = 0, n_own = 0, first_pre = 0, first_own = 0;
+    const int rt = b / gm.nb, pj = g * gm.nrt + rt;
+    if (gm.np) {
+        first_pre = cta_of(pj * gm.np, units, gm.ctas);
+        n_pre = cta_of((pj + 1) * gm.np - 1, units, gm.ctas) - first_pre + 1;
     }
-    const int own = max(0, len - (T - 1 - t));
-    const __nv_bfloat16* qr = q + (int64_t)w * dh;
-    float qv[4], acc[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        qv[c] = lane + 32 * c < dh ? __bfloat162float(qr[lane + 32 * c]) : 0.f;
-        acc[c] = 0.f;
+    const int c0 = in.cum[b], nt = in.cum[b + 1] - c0;
+    if (nt) {
+        const int a = up + c0 * gm.Hkv + g * nt;
+        first_own = cta_of(a, units, gm.ctas);
+        n_own = cta_of(a + nt - 1, units, gm.ctas) - first_own + 1;
     }
-    float mx = -INFINITY, sum = 0.f;
-    for (int j = 0; j < P + own; ++j) {
-        const bool pre = j < P;
-        const int64_t row = pre ? (int64_t)g * max_prefix + j : ((int64_t)b * Hkv + g) * max_seq + (j - P);
-        const __nv_bfloat16* kr = (pre ? kp : kc) + row * dh;
-        const __nv_bfloat16* vr = (pre ? vp : vc) + row * dh;
-        float part = 0.f;
+    const int64_t pre_row = (int64_t)(pj + first_pre) * kRowsP + (b - rt * gm.nb) * gm.GT + i;
+    const int64_t own_row = (int64_t)(b * gm.Hkv + g + first_own) * gm.GT + i;
+    constexpr int C = DH / 32;
+    float M = -INFINITY, Lsum = 0.f, acc[C];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (lane + 32 * c < dh) part = fmaf(qv[c], __bfloat162float(kr[lane + 32 * c]), part);
+    for (int c = 0; c < C; ++c) acc[c] = 0.f;
+    const int n = n_pre + n_own;
+    for (int k0 = 0; k0 < n; k0 += 32) {
+        const int k = k0 + lane;
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (k < n) ml = k < n_pre ? in.ml_prefix[pre_row + (int64_t)k * kRowsP]
+                                  : in.ml_own[own_row + (int64_t)(k - n_pre) * gm.GT];
+        float top = ml.x;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
-        const float s = part * scale;
-        const float mnew = fmaxf(mx, s);
-        const float corr = expf(mx - mnew), p = expf(s - mnew);
-        sum = sum * corr + p;
+        for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+        const float Mn = fmaxf(M, top);
+        if (Mn == -INFINITY) {                         // nothing visible so far, or NaN scores alone
+            Lsum += ml.y;
+            continue;
+        }
+        const float keep = exp2f(M - Mn), wgt = exp2f(ml.x - Mn);
+        Lsum = Lsum * keep + wgt * ml.y;               // a lane's own share
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (lane + 32 * c < dh) acc[c] = acc[c] * corr + p * __bfloat162float(vr[lane + 32 * c]);
-        mx = mnew;
+        for (int c = 0; c < C; ++c) acc[c] *= keep;
+        const int cnt = min(32, n - k0);
+#pragma unroll 4
+        for (int j = 0; j < cnt; ++j) {
+            const int kk = k0 + j;
+            const float* src = kk < n_pre ? in.o_prefix + (pre_row + (int64_t)kk * kRowsP) * DH
+                                          : in.o_own + (own_row + (int64_t)(kk - n_pre) * gm.GT) * DH;
+            const float wj = __shfl_sync(0xffffffffu, wgt, j);
+            // a piece in which this row sees nothing holds no value
+            const bool any = __shfl_sync(0xffffffffu, ml.x > -INFINITY, j);
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (any) acc[c] = fmaf(wj, src[lane * C + c], acc[c]);
+        }
+        M = Mn;
     }
-    const float inv = sum > 0.f ? 1.0f / sum : 0.f;    // no key at all: zeros
-    __nv_bfloat16* orow = o + ((int64_t)(b * T + t) * H + h) * dh;
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-        if (lane + 32 * c < dh) orow[lane + 32 * c] = __float2bfloat16_rn(acc[c] * inv);
+    for (int s = 16; s > 0; s >>= 1) Lsum += __shfl_xor_sync(0xffffffffu, Lsum, s);
+    const float inv = Lsum == 0.f ? 0.f : 1.0f / Lsum;         // no key at all: zeros
+    const int hh = i / gm.T, t = i - hh * gm.T, h = g * (gm.GT / gm.T) + hh;
+    __nv_bfloat16* dst = o + ((int64_t)(b * gm.T + t) * H + h) * DH + lane * C;
+#pragma unroll
+    for (int c = 0; c < C; ++c) dst[c] = __float2bfloat16_rn(acc[c] * inv);
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+PrefixGeom geom_of(int B, int H, int Hkv, int T, int P, int max_seq, int dh) {
+    PrefixGeom g{};
+    g.B = B;
+    g.Hkv = Hkv;
+    g.T = T;
+    g.GT = H / Hkv * T;
+    g.P = P;
+    g.max_seq = max_seq;
+    g.nb = kRowsP / g.GT;
+    if (g.nb > B) g.nb = B > 0 ? B : 1;
+    g.nrt = (B + g.nb - 1) / g.nb;
+    g.np = (P + kKeys - 1) / kKeys;
+    // swizzle atoms are 8 rows of 128 bytes, or 16 of 64
+    const int atom = dh == 32 ? 16 : 8;
+    g.q_pad = (g.GT + atom - 1) / atom * atom;
+    g.q_slots = kRowsP / g.q_pad < 8 ? kRowsP / g.q_pad : 8;
+    return g;
+}
+
+struct PrefixLayout {
+    size_t o_prefix, ml_prefix, o_own, ml_own, cum, total;
+};
+PrefixLayout layout(const PrefixGeom& g, int dh) {
+    PrefixLayout l{};
+    const size_t np = (size_t)g.Hkv * g.nrt + kMaxCtas, no = (size_t)g.B * g.Hkv + kMaxCtas;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += up256(bytes);
+        return at;
+    };
+    l.o_prefix = take(np * kRowsP * dh * 4);
+    l.ml_prefix = take(np * kRowsP * 8);
+    l.o_own = take(no * g.GT * dh * 4);
+    l.ml_own = take(no * g.GT * 8);
+    l.cum = take(((size_t)g.B + 1) * 4);
+    l.total = off;
+    return l;
+}
+
+template <int DH>
+cudaError_t launch_dh(const PrefixArgs& a, PrefixGeom g, const CUtensorMap* maps, cudaStream_t st) {
+    using L = Px<DH>;
+    const int smem = L::kBase + 4 * (a.B + 1);
+    cudaError_t e = cudaFuncSetAttribute(k_prefix_part<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const PrefixLayout l = layout(g, DH);
+    uint8_t* w = static_cast<uint8_t*>(a.ws);
+    PrefixParts parts;
+    parts.o_prefix = reinterpret_cast<float*>(w + l.o_prefix);
+    parts.ml_prefix = reinterpret_cast<float2*>(w + l.ml_prefix);
+    parts.o_own = reinterpret_cast<float*>(w + l.o_own);
+    parts.ml_own = reinterpret_cast<float2*>(w + l.ml_own);
+    parts.cum = reinterpret_cast<int*>(w + l.cum);
+    // two CTAs per SM; no more than there can be tiles
+    const int64_t most = (int64_t)g.Hkv * g.nrt * g.np +
+                         (int64_t)g.B * g.Hkv * ((a.max_seq + kKeys - 1) / kKeys);
+    g.ctas = 2 * sm_count() < kMaxCtas ? 2 * sm_count() : kMaxCtas;
+    if (most < g.ctas) g.ctas = (int)most;
+    e = launch_pdl(k_prefix_part<DH>, dim3((unsigned)g.ctas), dim3(kThreadsX), smem, st, maps[0], maps[1], maps[2],
+                   maps[3], maps[4], maps[5], static_cast<const __nv_bfloat16*>(a.vc), a.lens, g, parts,
+                   a.scale * 1.4426950408889634f, device_error_word());
+    if (e != cudaSuccess) return e;
+    return launch_pdl(k_prefix_join<DH>, dim3((unsigned)((a.B * a.H * a.T + 7) / 8)), dim3(256), 0, st, parts, g, a.H,
+                      static_cast<__nv_bfloat16*>(a.o));
 }
 
 }  // namespace
 
-size_t prefix_workspace_bytes(int B, int H, int Hkv, int T, int dh) { return 256; }
+size_t prefix_workspace_bytes(int B, int H, int Hkv, int T, int dh) {
+    return layout(geom_of(B, H, Hkv, T, 0, 1, dh), dh).total;
+}
 
 tfm_status launch_prefix_attention(const PrefixArgs& a, cudaStream_t st, cudaError_t* e) {
-    using bf = __nv_bfloat16;
-    *e = launch_pdl(k_prefix_rows, dim3((unsigned)((a.B * a.H * a.T + 7) / 8)), dim3(256), 0, st,
-                    static_cast<const bf*>(a.q), static_cast<const bf*>(a.kp),
-                    static_cast<const bf*>(a.vp), static_cast<const bf*>(a.kc),
-                    static_cast<const bf*>(a.vc), static_cast<bf*>(a.o), a.lens, a.B, a.H, a.Hkv,
-                    a.T, a.P, a.max_prefix, a.max_seq, a.dh, a.scale, device_error_word());
+    const PrefixGeom g = geom_of(a.B, a.H, a.Hkv, a.T, a.P, a.max_seq, a.dh);
+    if ((int64_t)g.Hkv * g.nrt * g.np + (int64_t)g.B * g.Hkv * ((a.max_seq + kKeys - 1) / kKeys) > INT32_MAX)
+        return TFM_EINVAL;
+    CUtensorMap maps[6];
+    if (!query_groups_map(&maps[0], a.q, a.B, a.Hkv, g.GT, a.dh, g.nb) ||
+        !query_groups_map(&maps[1], a.q, a.B, a.Hkv, g.GT, a.dh, 1) ||
+        !rows_heads_map(&maps[4], a.kc, a.max_seq, (int64_t)a.B * a.Hkv, a.dh, a.dh, (int64_t)a.max_seq * a.dh, kKeys) ||
+        !rows_heads_map(&maps[5], a.vc, a.max_seq, (int64_t)a.B * a.Hkv, a.dh, a.dh, (int64_t)a.max_seq * a.dh, kKeys))
+        return TFM_ECUDA;
+    maps[2] = maps[4];                                 // without a prefix its maps are never used
+    maps[3] = maps[5];
+    if (a.P > 0 &&
+        (!rows_heads_map(&maps[2], a.kp, a.P, a.Hkv, a.dh, a.dh, (int64_t)a.max_prefix * a.dh, kKeys) ||
+         !rows_heads_map(&maps[3], a.vp, a.P, a.Hkv, a.dh, a.dh, (int64_t)a.max_prefix * a.dh, kKeys)))
+        return TFM_ECUDA;
+    *e = a.dh == 32   ? launch_dh<32>(a, g, maps, st)
+         : a.dh == 64 ? launch_dh<64>(a, g, maps, st)
+                      : launch_dh<128>(a, g, maps, st);
     return TFM_OK;
 }
 
