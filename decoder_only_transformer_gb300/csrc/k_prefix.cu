@@ -49,7 +49,7 @@ struct Px {
     static constexpr int kNumBars = 2 * kMaxQ + 5 * kRing + 7;
     static constexpr int kMiscOff = kBarOff + 8 * kNumBars;
     static constexpr int kCumOff = kMiscOff + 16 + 4 * kPoisonX;
-    static constexpr int kBase = kCumOff + 1024;             // + 4 (B + 1)
+    static constexpr int kBase = kCumOff + 1024;             // + 4 (2 B + 1)
     static constexpr int kOCol = 2 * kKeys;                  // S 2 x 64 (P in its place), O
     static constexpr uint32_t kSwz = DH == 32 ? 4u : 2u;
     static constexpr uint32_t kGroup = 8 * kRowBytes;
@@ -91,40 +91,78 @@ struct Seg {
     int job;           // index among the jobs of its kind
 };
 
+// A run's next tile: tile t of the job of kv head g and row tile x, or (own) of
+// sequence x.  Jobs follow one another as prefix (g, x), then own (x, g), so the
+// next piece needs no search.
 struct Walk {
-    int u, end, up;    // next unit, end of the run, units of the prefix
+    int left, own, g, x, t;
 };
 
-__device__ __forceinline__ bool next_seg(Walk& w, Seg& s, const PrefixGeom& gm, const int* cum,
-                                         const int32_t* __restrict__ lens) {
-    if (w.u >= w.end) return false;
-    if (w.u < w.up) {
-        s.own = 0;
-        s.job = w.u / gm.np;
-        s.t0 = w.u - s.job * gm.np;
-        s.t1 = min(gm.np, s.t0 + w.end - w.u);
-        s.g = s.job / gm.nrt;
-        s.b = (s.job - s.g * gm.nrt) * gm.nb;
-        s.keys = gm.P;
-        s.rows = min(gm.nb, gm.B - s.b) * gm.GT;
+__device__ __forceinline__ void skip_empty(Walk& w, const PrefixGeom& gm, const int* cum) {
+    while (w.x < gm.B && cum[w.x + 1] == cum[w.x]) ++w.x;
+}
+
+__device__ __forceinline__ Walk start_walk(int u, int end, int up, const PrefixGeom& gm, const int* cum) {
+    Walk w{end - u, 0, 0, 0, 0};
+    if (end <= u) return w;
+    if (u < up) {
+        const int job = u / gm.np;
+        w.t = u - job * gm.np;
+        w.g = job / gm.nrt;
+        w.x = job - w.g * gm.nrt;
     } else {
-        const int v = w.u - w.up;
+        const int v = u - up;
         int lo = 0, hi = gm.B;                        // the last b with cum[b] Hkv <= v and keys
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (cum[mid] * gm.Hkv <= v) lo = mid + 1; else hi = mid;
         }
-        s.own = 1;
-        s.b = lo - 1;
-        const int nt = cum[lo] - cum[lo - 1], x = v - cum[lo - 1] * gm.Hkv;
-        s.g = x / nt;
-        s.t0 = x - s.g * nt;
-        s.t1 = min(nt, s.t0 + w.end - w.u);
-        s.keys = own_len(lens, s.b, gm.max_seq);
-        s.rows = gm.GT;
-        s.job = s.b * gm.Hkv + s.g;
+        w.own = 1;
+        w.x = lo - 1;
+        const int nt = cum[lo] - cum[lo - 1], y = v - cum[lo - 1] * gm.Hkv;
+        w.g = y / nt;
+        w.t = y - w.g * nt;
     }
-    w.u += s.t1 - s.t0;
+    return w;
+}
+
+__device__ __forceinline__ bool next_seg(Walk& w, Seg& s, const PrefixGeom& gm, const int* cum,
+                                         const int* slen) {
+    if (w.left <= 0) return false;
+    s.own = w.own;
+    s.g = w.g;
+    s.t0 = w.t;
+    int nt;
+    if (w.own) {
+        nt = cum[w.x + 1] - cum[w.x];
+        s.b = w.x;
+        s.keys = slen[w.x];
+        s.rows = gm.GT;
+        s.job = w.x * gm.Hkv + w.g;
+    } else {
+        nt = gm.np;
+        s.b = w.x * gm.nb;
+        s.keys = gm.P;
+        s.rows = min(gm.nb, gm.B - s.b) * gm.GT;
+        s.job = w.g * gm.nrt + w.x;
+    }
+    s.t1 = min(nt, w.t + w.left);
+    w.left -= s.t1 - s.t0;
+    w.t = 0;                                           // a run ends, or goes on with a new job
+    if (w.own) {
+        if (++w.g == gm.Hkv) {
+            w.g = 0;
+            ++w.x;
+            skip_empty(w, gm, cum);
+        }
+    } else if (++w.x == gm.nrt) {
+        w.x = 0;
+        if (++w.g == gm.Hkv) {
+            w.g = 0;
+            w.own = 1;
+            skip_empty(w, gm, cum);
+        }
+    }
     return true;
 }
 
@@ -134,15 +172,17 @@ __device__ __forceinline__ bool check_tile(const Seg& s, int t, int T) {
     return s.own && (t + 1) * kKeys > s.keys - (T - 1);
 }
 
-// cum[b]: key tiles of the own caches of sequences before b, by the whole block.
-__device__ __forceinline__ void scan_lengths(int* cum, int* warp_sum, const int32_t* __restrict__ lens,
+// cum[b]: key tiles of the own caches of sequences before b; slen[b]: their
+// lengths.  By the whole block.
+__device__ __forceinline__ void scan_lengths(int* cum, int* slen, int* warp_sum, const int32_t* __restrict__ lens,
                                              const PrefixGeom& gm) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
     int base = 0;
     for (int b0 = 0; b0 < gm.B; b0 += blockDim.x) {
         const int b = b0 + tid;
-        int n = b < gm.B ? (own_len(lens, b, gm.max_seq) + kKeys - 1) / kKeys : 0;
-        int sum = n;
+        const int len = b < gm.B ? own_len(lens, b, gm.max_seq) : 0;
+        if (b < gm.B) slen[b] = len;
+        int sum = (len + kKeys - 1) / kKeys;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, sum, o);
@@ -164,9 +204,10 @@ __device__ __forceinline__ void scan_lengths(int* cum, int* warp_sum, const int3
 }
 
 struct PrefixParts {
-    float* o_prefix;       // [jobs + ctas][128][dh]
+    // O column-block first, so that the rows of a warp lie side by side
+    float* o_prefix;       // [jobs + ctas][dh / 4][128][4]
     float2* ml_prefix;     // [jobs + ctas][128]: max (log2), sum
-    float* o_own;          // [B Hkv + ctas][GT][dh]
+    float* o_own;          // [B Hkv + ctas][dh / 4][GT][4]
     float2* ml_own;        // [B Hkv + ctas][GT]
     int* cum;              // [B + 1]
 };
@@ -202,6 +243,7 @@ __global__ void __launch_bounds__(kThreadsX, 2)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMiscOff + 4);
     volatile int* poison = reinterpret_cast<volatile int*>(gbase + L::kMiscOff + 16);
     int* cum = reinterpret_cast<int*>(gbase + L::kCumOff);
+    int* slen = cum + gm.B + 1;
     __shared__ int warp_sum[kThreadsX / 32];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -240,7 +282,7 @@ __global__ void __launch_bounds__(kThreadsX, 2)
     const uint32_t tmem_base = *tmem_holder;
     pdl_wait();
     pdl_trigger();
-    scan_lengths(cum, warp_sum, lens, gm);
+    scan_lengths(cum, slen, warp_sum, lens, gm);
     const int cta = (int)blockIdx.x;
     if (cta == 0)
         for (int b = threadIdx.x; b <= gm.B; b += kThreadsX) {
@@ -248,8 +290,8 @@ __global__ void __launch_bounds__(kThreadsX, 2)
             if (b < gm.B && (lens[b] < 0 || lens[b] > gm.max_seq)) raise_error(err, TFM_EINVAL);
         }
     const int up = gm.Hkv * gm.nrt * gm.np, units = up + gm.Hkv * cum[gm.B];
-    Walk walk{run_start(cta, units, gm.ctas), run_start(cta + 1, units, gm.ctas), up};
-    const int tiles = walk.end - walk.u;               // of this CTA, in all its pieces
+    const Walk walk = start_walk(run_start(cta, units, gm.ctas), run_start(cta + 1, units, gm.ctas), up, gm, cum);
+    const int tiles = walk.left;                       // of this CTA, in all its pieces
 
     // Q slots: a piece of the prefix takes the whole region (slot 0's barriers),
     // own pieces take q_slots slots in turn, the first after a prefix piece slot 0
@@ -265,7 +307,7 @@ __global__ void __launch_bounds__(kThreadsX, 2)
             Walk wk = walk, wv = walk;
             Seg sk, sv;
             int tk = 0, tv = 0;
-            bool hk = next_seg(wk, sk, gm, cum, lens), hv = next_seg(wv, sv, gm, cum, lens);
+            bool hk = next_seg(wk, sk, gm, cum, slen), hv = next_seg(wv, sv, gm, cum, slen);
             tk = hk ? sk.t0 : 0;
             tv = hv ? sv.t0 : 0;
             bool fresh = true;
@@ -309,7 +351,7 @@ __global__ void __launch_bounds__(kThreadsX, 2)
                     ++kn;
                     fresh = ++tk == sk.t1;
                     if (fresh) {
-                        hk = next_seg(wk, sk, gm, cum, lens);
+                        hk = next_seg(wk, sk, gm, cum, slen);
                         tk = hk ? sk.t0 : 0;
                     }
                 }
@@ -319,7 +361,7 @@ __global__ void __launch_bounds__(kThreadsX, 2)
                     load(sv, tv, false, sV + s * L::kTile, v_full(s));
                     ++vn;
                     if (++tv == sv.t1) {
-                        hv = next_seg(wv, sv, gm, cum, lens);
+                        hv = next_seg(wv, sv, gm, cum, slen);
                         tv = hv ? sv.t0 : 0;
                     }
                 }
@@ -348,7 +390,7 @@ __global__ void __launch_bounds__(kThreadsX, 2)
             bool fresh = true;
             auto do_s = [&]() {
                 if (fresh) {
-                    if (!next_seg(ws, ss, gm, cum, lens)) return;
+                    if (!next_seg(ws, ss, gm, cum, slen)) return;
                     ts = ss.t0;
                     cur_slot = ss.own ? slot : 0;
                     slot = ss.own ? (cur_slot + 1 == gm.q_slots ? 0 : cur_slot + 1) : 0;
@@ -373,7 +415,7 @@ __global__ void __launch_bounds__(kThreadsX, 2)
             };
             if (tiles > 0) do_s();
             if (ok && tiles > 1) do_s();
-            bool hp = next_seg(wp, sp, gm, cum, lens);
+            bool hp = next_seg(wp, sp, gm, cum, slen);
             tp = hp ? sp.t0 : 0;
             for (int n = 0; n < tiles && ok; ++n) {
                 const int s = n % R;
@@ -393,7 +435,7 @@ __global__ void __launch_bounds__(kThreadsX, 2)
                 umma_commit(v_empty(s));
                 umma_commit(pv_done(n & 1));
                 if (++tp == sp.t1) {
-                    hp = next_seg(wp, sp, gm, cum, lens);
+                    hp = next_seg(wp, sp, gm, cum, slen);
                     tp = hp ? sp.t0 : 0;
                 }
                 if (n + 2 < tiles) do_s();
@@ -410,7 +452,7 @@ __global__ void __launch_bounds__(kThreadsX, 2)
         Seg sv;
         bool ok = true;
         int n = 0;
-        for (int seg = 0; ok && next_seg(wv, sv, gm, cum, lens); ++seg)
+        for (int seg = 0; ok && next_seg(wv, sv, gm, cum, slen); ++seg)
             for (int t = sv.t0; t < sv.t1; ++t, ++n) {
                 const int s = n % R;
                 if (!(ok = warp_wait(v_full(s), (uint32_t)(n / R) & 1u, err, abort_flag))) break;
@@ -451,7 +493,7 @@ __global__ void __launch_bounds__(kThreadsX, 2)
         Seg sg;
         bool ok = true;
         int n = 0;
-        for (int seg = 0; ok && next_seg(ww, sg, gm, cum, lens); ++seg) {
+        for (int seg = 0; ok && next_seg(ww, sg, gm, cum, slen); ++seg) {
             const bool busy = warp * 32 < sg.rows;     // warps without rows only keep step
             // keys this row sees: all of the prefix, or the own ones up to its token
             const int lim = sg.own ? sg.keys - (gm.T - 1 - r % gm.T) : sg.keys;
@@ -490,7 +532,7 @@ __global__ void __launch_bounds__(kThreadsX, 2)
                         corr = fast_exp2(m - mx);
                         m = mx;
                     }
-                    const bool need_rescale = __any_sync(0xffffffffu, corr != 1.f && t > sg.t0);
+                    const bool need_rescale = __any_sync(0xffffffffu, corr != 1.f && t > sg.t0 && r < sg.rows);
                     const uint64_t scale2 = f2_pack(scale_log2, scale_log2);
                     const float negm = m == -INFINITY ? 0.f : -m;     // no visible key yet: every p is 0
                     const uint64_t negm2 = f2_pack(negm, negm);
@@ -540,8 +582,9 @@ __global__ void __launch_bounds__(kThreadsX, 2)
             tc_fence_after();
             const bool fix = poison[seg % kPoisonX] == seg + 1;
             const int64_t piece = sg.job + cta;
-            const int64_t row = sg.own ? piece * gm.GT + r : piece * kRowsP + r;
-            float* orow = (sg.own ? out.o_own : out.o_prefix) + row * DH;
+            const int stride = sg.own ? gm.GT : kRowsP;
+            const int64_t row = piece * stride + r;
+            float4* orow = reinterpret_cast<float4*>((sg.own ? out.o_own : out.o_prefix) + piece * stride * DH) + r;
             const bool mine = r < sg.rows;
             if (mine) (sg.own ? out.ml_own : out.ml_prefix)[row] = make_float2(m, l);
 #pragma unroll 1
@@ -563,7 +606,7 @@ __global__ void __launch_bounds__(kThreadsX, 2)
                     }
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4*>(orow + c * 32 + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                        orow[(c * 8 + e / 4) * stride] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                 }
                 __syncwarp();
             }
@@ -577,78 +620,75 @@ __global__ void __launch_bounds__(kThreadsX, 2)
     if (warp == 5) tmem_dealloc(tmem_base, 256);
 }
 
-// One warp per row: lane i takes piece i's maximum and sum, then all lanes add
-// the weighted pieces, dh / 32 columns each.
+// A thread joins 16 columns of a row, its pieces of the prefix job and of the own
+// job; a CTA takes the 128 rows of a row tile, whose prefix pieces lie side by side.
 template <int DH>
-__global__ void __launch_bounds__(256) k_prefix_join(PrefixParts in, PrefixGeom gm, int H,
-                                                     __nv_bfloat16* __restrict__ o) {
+__global__ void __launch_bounds__(kRowsP) k_prefix_join(PrefixParts in, PrefixGeom gm, int H,
+                                                        __nv_bfloat16* __restrict__ o) {
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const int w = (int)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int per_b = gm.Hkv * gm.GT;                  // rows of a sequence: (g, hh, t)
-    if (w >= gm.B * per_b) return;
-    const int b = w / per_b, x = w - b * per_b, g = x / gm.GT, i = x - g * gm.GT;
-    const int up = gm.Hkv * gm.nrt * gm.np, units = up + gm.Hkv * in.cum[gm.B];
-    // pieces of the prefix job, then of the own job, each a run of CTAs
+    constexpr int S = DH / 16;
+    const int slice = (int)blockIdx.x % S, pj = (int)blockIdx.x / S;
+    const int g = pj / gm.nrt, rt = pj - g * gm.nrt, r = threadIdx.x;
+    const int b = rt * gm.nb + r / gm.GT, i = r % gm.GT;
+    if (r >= gm.nb * gm.GT || b >= gm.B) return;
+    const int units = gm.Hkv * (gm.nrt * gm.np + __ldg(in.cum + gm.B)), up = gm.Hkv * gm.nrt * gm.np;
+    // the pieces of a job: one per CTA of a run of CTAs
     int n_pre = 0, n_own = 0, first_pre = 0, first_own = 0;
-    const int rt = b / gm.nb, pj = g * gm.nrt + rt;
     if (gm.np) {
         first_pre = cta_of(pj * gm.np, units, gm.ctas);
         n_pre = cta_of((pj + 1) * gm.np - 1, units, gm.ctas) - first_pre + 1;
     }
-    const int c0 = in.cum[b], nt = in.cum[b + 1] - c0;
+    const int c0 = __ldg(in.cum + b), nt = __ldg(in.cum + b + 1) - c0;
     if (nt) {
         const int a = up + c0 * gm.Hkv + g * nt;
         first_own = cta_of(a, units, gm.ctas);
         n_own = cta_of(a + nt - 1, units, gm.ctas) - first_own + 1;
     }
-    const int64_t pre_row = (int64_t)(pj + first_pre) * kRowsP + (b - rt * gm.nb) * gm.GT + i;
-    const int64_t own_row = (int64_t)(b * gm.Hkv + g + first_own) * gm.GT + i;
-    constexpr int C = DH / 32;
-    float M = -INFINITY, Lsum = 0.f, acc[C];
+    const int64_t pre = pj + first_pre, own = (int64_t)b * gm.Hkv + g + first_own;
+    const float2* ml_pre = in.ml_prefix + pre * kRowsP + r;
+    const float2* ml_own = in.ml_own + own * gm.GT + i;
+    float M = -INFINITY;
+#pragma unroll 8
+    for (int k = 0; k < n_pre; ++k) M = fmaxf(M, ml_pre[(int64_t)k * kRowsP].x);
+#pragma unroll 8
+    for (int k = 0; k < n_own; ++k) M = fmaxf(M, ml_own[(int64_t)k * gm.GT].x);
+    float L = 0.f, acc[16];
 #pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] = 0.f;
-    const int n = n_pre + n_own;
-    for (int k0 = 0; k0 < n; k0 += 32) {
-        const int k = k0 + lane;
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (k < n) ml = k < n_pre ? in.ml_prefix[pre_row + (int64_t)k * kRowsP]
-                                  : in.ml_own[own_row + (int64_t)(k - n_pre) * gm.GT];
-        float top = ml.x;
+    for (int c = 0; c < 16; ++c) acc[c] = 0.f;
+    auto add = [&](const float2 ml, const float4* __restrict__ src, int stride) {
+        // A piece in which the row sees nothing holds (-inf, 0) and no value; one of
+        // NaN scores alone (-inf, NaN).
+        const bool none = ml.x == -INFINITY;
+        const float w = none ? 0.f : exp2f(ml.x - M);
+        L += none ? ml.y : w * ml.y;
+        float4 v[4];
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-        const float Mn = fmaxf(M, top);
-        if (Mn == -INFINITY) {                         // nothing visible so far, or NaN scores alone
-            Lsum += ml.y;
-            continue;
+        for (int c = 0; c < 4; ++c) v[c] = src[c * stride];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (none) continue;
+            acc[4 * c] = fmaf(w, v[c].x, acc[4 * c]);
+            acc[4 * c + 1] = fmaf(w, v[c].y, acc[4 * c + 1]);
+            acc[4 * c + 2] = fmaf(w, v[c].z, acc[4 * c + 2]);
+            acc[4 * c + 3] = fmaf(w, v[c].w, acc[4 * c + 3]);
         }
-        const float keep = exp2f(M - Mn), wgt = exp2f(ml.x - Mn);
-        Lsum = Lsum * keep + wgt * ml.y;               // a lane's own share
-#pragma unroll
-        for (int c = 0; c < C; ++c) acc[c] *= keep;
-        const int cnt = min(32, n - k0);
+    };
+    const float4* o_pre = reinterpret_cast<const float4*>(in.o_prefix) + (pre * (DH / 4) + slice * 4) * kRowsP + r;
+    const float4* o_own = reinterpret_cast<const float4*>(in.o_own) + (own * (DH / 4) + slice * 4) * gm.GT + i;
 #pragma unroll 4
-        for (int j = 0; j < cnt; ++j) {
-            const int kk = k0 + j;
-            const float* src = kk < n_pre ? in.o_prefix + (pre_row + (int64_t)kk * kRowsP) * DH
-                                          : in.o_own + (own_row + (int64_t)(kk - n_pre) * gm.GT) * DH;
-            const float wj = __shfl_sync(0xffffffffu, wgt, j);
-            // a piece in which this row sees nothing holds no value
-            const bool any = __shfl_sync(0xffffffffu, ml.x > -INFINITY, j);
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-                if (any) acc[c] = fmaf(wj, src[lane * C + c], acc[c]);
-        }
-        M = Mn;
-    }
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) Lsum += __shfl_xor_sync(0xffffffffu, Lsum, s);
-    const float inv = Lsum == 0.f ? 0.f : 1.0f / Lsum;         // no key at all: zeros
+    for (int k = 0; k < n_pre; ++k)
+        add(ml_pre[(int64_t)k * kRowsP], o_pre + (int64_t)k * (DH / 4) * kRowsP, kRowsP);
+#pragma unroll 4
+    for (int k = 0; k < n_own; ++k)
+        add(ml_own[(int64_t)k * gm.GT], o_own + (int64_t)k * (DH / 4) * gm.GT, gm.GT);
+    const float inv = L == 0.f ? 0.f : 1.0f / L;       // no key at all: zeros
     const int hh = i / gm.T, t = i - hh * gm.T, h = g * (gm.GT / gm.T) + hh;
-    __nv_bfloat16* dst = o + ((int64_t)(b * gm.T + t) * H + h) * DH + lane * C;
+    uint4* dst = reinterpret_cast<uint4*>(o + ((int64_t)(b * gm.T + t) * H + h) * DH + slice * 16);
 #pragma unroll
-    for (int c = 0; c < C; ++c) dst[c] = __float2bfloat16_rn(acc[c] * inv);
+    for (int c = 0; c < 16; c += 8)
+        dst[c / 8] = make_uint4(pack_bf16x2(acc[c] * inv, acc[c + 1] * inv), pack_bf16x2(acc[c + 2] * inv, acc[c + 3] * inv),
+                                pack_bf16x2(acc[c + 4] * inv, acc[c + 5] * inv), pack_bf16x2(acc[c + 6] * inv, acc[c + 7] * inv));
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -696,7 +736,7 @@ PrefixLayout layout(const PrefixGeom& g, int dh) {
 template <int DH>
 cudaError_t launch_dh(const PrefixArgs& a, PrefixGeom g, const CUtensorMap* maps, cudaStream_t st) {
     using L = Px<DH>;
-    const int smem = L::kBase + 4 * (a.B + 1);
+    const int smem = L::kBase + 4 * (2 * a.B + 1);
     cudaError_t e = cudaFuncSetAttribute(k_prefix_part<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const PrefixLayout l = layout(g, DH);
@@ -716,7 +756,7 @@ cudaError_t launch_dh(const PrefixArgs& a, PrefixGeom g, const CUtensorMap* maps
                    maps[3], maps[4], maps[5], static_cast<const __nv_bfloat16*>(a.vc), a.lens, g, parts,
                    a.scale * 1.4426950408889634f, device_error_word());
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_prefix_join<DH>, dim3((unsigned)((a.B * a.H * a.T + 7) / 8)), dim3(256), 0, st, parts, g, a.H,
+    return launch_pdl(k_prefix_join<DH>, dim3((unsigned)(g.Hkv * g.nrt * (DH / 16))), dim3(kRowsP), 0, st, parts, g, a.H,
                       static_cast<__nv_bfloat16*>(a.o));
 }
 
