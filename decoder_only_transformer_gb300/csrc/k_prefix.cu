@@ -46,7 +46,7 @@ struct Px {
     static constexpr int kKOff = kQ;
     static constexpr int kVOff = kKOff + kRing * kTile;
     static constexpr int kBarOff = kVOff + kRing * kTile;
-    static constexpr int kNumBars = 2 * kMaxQ + 5 * kRing + 7;
+    static constexpr int kNumBars = 2 * kMaxQ + 5 * kRing + 5;
     static constexpr int kMiscOff = kBarOff + 8 * kNumBars;
     static constexpr int kCumOff = kMiscOff + 16 + 4 * kPoisonX;
     static constexpr int kBase = kCumOff + 1024;             // + 4 (2 B + 1)
@@ -230,15 +230,15 @@ __global__ void __launch_bounds__(kThreadsX, 2)
     auto q_empty = [&](int s) { return bars + 8u * (L::kMaxQ + s); };
     constexpr int B0 = 2 * L::kMaxQ;
     auto k_full = [&](int s) { return bars + 8u * (B0 + s); };
-    auto k_empty = [&](int s) { return bars + 8u * (B0 + R + s); };
-    auto v_full = [&](int s) { return bars + 8u * (B0 + 2 * R + s); };
-    auto v_empty = [&](int s) { return bars + 8u * (B0 + 3 * R + s); };
-    auto v_clean = [&](int s) { return bars + 8u * (B0 + 4 * R + s); };
+    auto v_full = [&](int s) { return bars + 8u * (B0 + R + s); };
+    auto v_clean = [&](int s) { return bars + 8u * (B0 + 2 * R + s); };
+    // S of a K slot is complete (the slot is free, S can be read); P.V of a V slot
+    auto s_done = [&](int s) { return bars + 8u * (B0 + 3 * R + s); };
+    auto pv_done = [&](int s) { return bars + 8u * (B0 + 4 * R + s); };
     constexpr int B1 = B0 + 5 * R;
-    auto s_full = [&](int i) { return bars + 8u * (B1 + i); };
-    auto p_full = [&](int i) { return bars + 8u * (B1 + 2 + i); };
-    auto pv_done = [&](int i) { return bars + 8u * (B1 + 4 + i); };
-    const uint32_t done_bar = bars + 8u * (B1 + 6);
+    auto p_pre = [&](int i) { return bars + 8u * (B1 + i); };      // P of a prefix tile, of an own one
+    auto p_own = [&](int i) { return bars + 8u * (B1 + 2 + i); };
+    const uint32_t done_bar = bars + 8u * (B1 + 4);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(gbase + L::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMiscOff + 4);
     volatile int* poison = reinterpret_cast<volatile int*>(gbase + L::kMiscOff + 16);
@@ -254,15 +254,14 @@ __global__ void __launch_bounds__(kThreadsX, 2)
         }
         for (int s = 0; s < R; ++s) {
             mbar_init(k_full(s), 1);
-            mbar_init(k_empty(s), 1);
             mbar_init(v_full(s), 1);
-            mbar_init(v_empty(s), 1);
             mbar_init(v_clean(s), 1);
+            mbar_init(s_done(s), 1);
+            mbar_init(pv_done(s), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(s_full(i), 1);
-            mbar_init(p_full(i), 4);
-            mbar_init(pv_done(i), 1);
+            mbar_init(p_pre(i), (min(gm.nb, gm.B) * gm.GT + 31) / 32);   // softmax warps with rows
+            mbar_init(p_own(i), (gm.GT + 31) / 32);
         }
         mbar_init(done_bar, 1);
         *abort_flag = 0;
@@ -291,7 +290,14 @@ __global__ void __launch_bounds__(kThreadsX, 2)
         }
     const int up = gm.Hkv * gm.nrt * gm.np, units = up + gm.Hkv * cum[gm.B];
     const Walk walk = start_walk(run_start(cta, units, gm.ctas), run_start(cta + 1, units, gm.ctas), up, gm, cum);
-    const int tiles = walk.left;                       // of this CTA, in all its pieces
+    const int tiles = (int)uniform(walk.left);         // of this CTA, in all its pieces
+    // its first own tile: P of the own tiles has barriers of its own, as fewer
+    // softmax warps write it
+    const int own0 = max(0, min(tiles, up - run_start(cta, units, gm.ctas)));
+    auto p_full = [&](bool own, int n) { return own ? p_own(n & 1) : p_pre(n & 1); };
+    auto p_phase = [&](bool own, int n) {
+        return (uint32_t)((n >> 1) - (own ? (own0 + ((n ^ own0) & 1)) >> 1 : 0)) & 1u;
+    };
 
     // Q slots: a piece of the prefix takes the whole region (slot 0's barriers),
     // own pieces take q_slots slots in turn, the first after a prefix piece slot 0
@@ -299,155 +305,151 @@ __global__ void __launch_bounds__(kThreadsX, 2)
     if (warp == 4) {
         // ---------------------------------------------------------- TMA producer
         // Q of a piece before its first K; K_{n+1} before V_n, the order in which
-        // the MMA thread takes them.
-        if (lane == 0) {
-            bool ok = true;
-            int kn = 0, vn = 0, slot = 0;
-            uint32_t q_used = 0, q_par = 0;             // slots used before, their parity
-            Walk wk = walk, wv = walk;
-            Seg sk, sv;
-            int tk = 0, tv = 0;
-            bool hk = next_seg(wk, sk, gm, cum, slen), hv = next_seg(wv, sv, gm, cum, slen);
-            tk = hk ? sk.t0 : 0;
-            tv = hv ? sv.t0 : 0;
-            bool fresh = true;
-            auto load_q = [&]() {
-                const int s = sk.own ? slot : 0;
-                if (q_used >> s & 1u) {
-                    ok = mbar_wait(q_empty(s), (q_par >> s) & 1u, err, abort_flag);
-                    q_par ^= 1u << s;
-                    if (!ok) return;
-                }
-                q_used |= 1u << s;
-                const int rows = sk.own ? gm.GT : gm.nb * gm.GT;
-                mbar_arrive_expect_tx(q_full(s), (uint32_t)rows * DH * 2);
-                const uint32_t dst = sQ + (sk.own ? s * gm.q_pad * DH * 2 : 0);
-                const uint32_t sub = (sk.own ? gm.q_pad : kRowsP) * L::kRowBytes;
-#pragma unroll
-                for (int c = 0; c < L::kSub; ++c)
-                    asm volatile(
-                        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-                        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst + c * sub),
-                        "l"(reinterpret_cast<uint64_t>(sk.own ? &qomap : &qpmap)), "r"(64 * c), "r"(0),
-                        "r"(sk.g), "r"(sk.b), "r"(q_full(s))
-                        : "memory");
-                slot = sk.own ? (s + 1 == gm.q_slots ? 0 : s + 1) : 0;
-            };
-            auto load = [&](const Seg& s, int t, bool is_k, uint32_t dst, uint32_t bar) {
-                mbar_arrive_expect_tx(bar, L::kTile);
-                const CUtensorMap* map = s.own ? (is_k ? &kcmap : &vcmap) : (is_k ? &kpmap : &vpmap);
-                const int z = s.own ? s.b * gm.Hkv + s.g : s.g;
-#pragma unroll
-                for (int c = 0; c < L::kSub; ++c)
-                    tma_load_3d(dst + c * L::kSubTile, map, 64 * c, t * kKeys, z, bar);
-            };
-            for (int n = 0; n <= tiles && ok; ++n) {
-                if (n < tiles) {
-                    if (fresh) load_q();
-                    if (!ok) break;
-                    const int s = kn % R;
-                    if (!(ok = mbar_wait(k_empty(s), ((uint32_t)(kn / R) & 1u) ^ 1u, err, abort_flag))) break;
-                    load(sk, tk, true, sK + s * L::kTile, k_full(s));
-                    ++kn;
-                    fresh = ++tk == sk.t1;
-                    if (fresh) {
-                        hk = next_seg(wk, sk, gm, cum, slen);
-                        tk = hk ? sk.t0 : 0;
-                    }
-                }
-                if (n > 0) {
-                    const int s = vn % R;
-                    if (!(ok = mbar_wait(v_empty(s), ((uint32_t)(vn / R) & 1u) ^ 1u, err, abort_flag))) break;
-                    load(sv, tv, false, sV + s * L::kTile, v_full(s));
-                    ++vn;
-                    if (++tv == sv.t1) {
-                        hv = next_seg(wv, sv, gm, cum, slen);
-                        tv = hv ? sv.t0 : 0;
-                    }
-                }
+        // the MMA warp takes them.
+        bool ok = true;
+        int slot = 0;
+        uint32_t q_used = 0, q_par = 0;                 // slots used before, their parity
+        Walk wk = walk, wv = walk;
+        Seg sk, sv;
+        int lk = 0, lv = 0;                             // tiles left in the pieces of K and V
+        auto load_q = [&]() {
+            const bool own = uniform(sk.own);
+            const int s = own ? slot : 0;
+            if (q_used >> s & 1u) {
+                ok = warp_wait(q_empty(s), (q_par >> s) & 1u, err, abort_flag);
+                q_par ^= 1u << s;
+                if (!ok) return;
             }
-            // nothing may be in flight when the CTA ends
-            for (int k = kn < R ? 0 : kn - R; k < kn; ++k)
-                mbar_wait(k_full(k % R), (uint32_t)(k / R) & 1u, err, abort_flag);
-            for (int k = vn < R ? 0 : vn - R; k < vn; ++k)
-                mbar_wait(v_full(k % R), (uint32_t)(k / R) & 1u, err, abort_flag);
+            q_used |= 1u << s;
+            const int rows = own ? gm.GT : gm.nb * gm.GT;
+            const uint32_t dst = sQ + (own ? s * gm.q_pad * DH * 2 : 0);
+            const uint32_t sub = (own ? gm.q_pad : kRowsP) * L::kRowBytes;
+            const CUtensorMap* map = own ? &qomap : &qpmap;
+            const int g = (int)uniform(sk.g), b = (int)uniform(sk.b);
+            mbar_arrive_expect_tx_e(q_full(s), (uint32_t)rows * DH * 2);
+#pragma unroll
+            for (int c = 0; c < L::kSub; ++c) tma_load_4d_e(dst + c * sub, map, 64 * c, 0, g, b, q_full(s));
+            slot = own ? (s + 1 == gm.q_slots ? 0 : s + 1) : 0;
+        };
+        int kn = 0, vn = 0;                             // K and V tiles loaded
+        int ky = 0, kz = 0, vy = 0, vz = 0;             // coordinates of the next K and V tile
+        const CUtensorMap *km = &kpmap, *vm = &vpmap;
+        for (int n = 0; n <= tiles && ok; ++n) {
+            const int s = n % R;
+            if (n < tiles) {
+                if (lk == 0) {
+                    next_seg(wk, sk, gm, cum, slen);
+                    lk = (int)uniform(sk.t1 - sk.t0);
+                    ky = (int)uniform(sk.t0) * kKeys;
+                    kz = (int)uniform(sk.own ? sk.b * gm.Hkv + sk.g : sk.g);
+                    km = uniform(sk.own) ? &kcmap : &kpmap;
+                    load_q();
+                    if (!ok) break;
+                }
+                if (n >= R && !(ok = warp_wait(s_done(s), ((uint32_t)(n / R) & 1u) ^ 1u, err, abort_flag))) break;
+                mbar_arrive_expect_tx_e(k_full(s), L::kTile);
+#pragma unroll
+                for (int c = 0; c < L::kSub; ++c)
+                    tma_load_3d_e(sK + s * L::kTile + c * L::kSubTile, km, 64 * c, ky, kz, k_full(s));
+                ky += kKeys;
+                --lk;
+                ++kn;
+            }
+            if (n > 0) {
+                const int m = n - 1, sv_ = m % R;
+                if (lv == 0) {
+                    next_seg(wv, sv, gm, cum, slen);
+                    lv = (int)uniform(sv.t1 - sv.t0);
+                    vy = (int)uniform(sv.t0) * kKeys;
+                    vz = (int)uniform(sv.own ? sv.b * gm.Hkv + sv.g : sv.g);
+                    vm = uniform(sv.own) ? &vcmap : &vpmap;
+                }
+                if (m >= R && !(ok = warp_wait(pv_done(sv_), ((uint32_t)(m / R) & 1u) ^ 1u, err, abort_flag))) break;
+                mbar_arrive_expect_tx_e(v_full(sv_), L::kTile);
+#pragma unroll
+                for (int c = 0; c < L::kSub; ++c)
+                    tma_load_3d_e(sV + sv_ * L::kTile + c * L::kSubTile, vm, 64 * c, vy, vz, v_full(sv_));
+                vy += kKeys;
+                --lv;
+                ++vn;
+            }
+        }
+        // The MMA and check warps wait for every load; after a wait that gave up,
+        // the last ones still have to land before the CTA ends.
+        if (!ok && lane == 0) {
+            volatile int never = 0;
+            for (int m = max(0, kn - R); m < kn; ++m) mbar_wait(k_full(m % R), (uint32_t)(m / R) & 1u, nullptr, &never);
+            for (int m = max(0, vn - R); m < vn; ++m) mbar_wait(v_full(m % R), (uint32_t)(m / R) & 1u, nullptr, &never);
         }
     } else if (warp == 5) {
         // ---------------------------------------------------------- MMAs
         // S_0, S_1, then P_n.V_n and S_{n+2}, which takes the place of P_n: the
         // MMAs of one thread complete in the order they are issued.
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = umma_idesc_bf16(kRowsP, kKeys);
-            constexpr uint32_t idesc_o = umma_idesc_bf16(kRowsP, DH, true);
-            const uint64_t dq = sdesc(sQ, L::kSwz, 16, L::kGroup), dk = sdesc(sK, L::kSwz, 16, L::kGroup);
-            const uint64_t dv = sdesc(sV, L::kSwz, DH > 64 ? L::kSubTile : 0, L::kGroup);
-            bool ok = true;
-            int kn = 0, slot = 0, cur_slot = 0;
-            uint32_t q_par = 0, clean = 0;
-            Walk ws = walk, wp = walk;
-            Seg ss, sp;
-            int ts = 0, tp = 0;
-            bool fresh = true;
-            auto do_s = [&]() {
-                if (fresh) {
-                    if (!next_seg(ws, ss, gm, cum, slen)) return;
-                    ts = ss.t0;
-                    cur_slot = ss.own ? slot : 0;
-                    slot = ss.own ? (cur_slot + 1 == gm.q_slots ? 0 : cur_slot + 1) : 0;
-                    if (!(ok = mbar_wait(q_full(cur_slot), (q_par >> cur_slot) & 1u, err, abort_flag))) return;
-                    q_par ^= 1u << cur_slot;
-                }
-                const int s = kn % R;
-                if (!(ok = mbar_wait(k_full(s), (uint32_t)(kn / R) & 1u, err, abort_flag))) return;
-                tc_fence_after();
-                const uint64_t a0 = dq + (uint64_t)((ss.own ? cur_slot * gm.q_pad * DH * 2 : 0) >> 4);
-                const uint32_t asub = ((ss.own ? gm.q_pad : kRowsP) * L::kRowBytes) >> 4;
-                const uint64_t b0 = dk + (uint64_t)((s * L::kTile) >> 4);
-#pragma unroll
-                for (int kk = 0; kk < DH / 16; ++kk)
-                    umma_bf16(tmem_base + (kn & 1) * kKeys, a0 + (kk >> 2) * asub + (kk & 3) * 2,
-                              b0 + (kk >> 2) * (L::kSubTile >> 4) + (kk & 3) * 2, idesc_s, kk > 0 ? 1u : 0u);
-                umma_commit(k_empty(s));
-                umma_commit(s_full(kn & 1));
-                ++kn;
-                fresh = ++ts == ss.t1;
-                if (fresh) umma_commit(q_empty(cur_slot));
-            };
-            if (tiles > 0) do_s();
-            if (ok && tiles > 1) do_s();
-            bool hp = next_seg(wp, sp, gm, cum, slen);
-            tp = hp ? sp.t0 : 0;
-            for (int n = 0; n < tiles && ok; ++n) {
-                const int s = n % R;
-                if (!(ok = mbar_wait(v_full(s), (uint32_t)(n / R) & 1u, err, abort_flag))) break;
-                if (check_tile(sp, tp, gm.T)) {
-                    if (!(ok = mbar_wait(v_clean(s), (clean >> s) & 1u, err, abort_flag))) break;
-                    clean ^= 1u << s;
-                }
-                if (!(ok = mbar_wait(p_full(n & 1), (uint32_t)(n >> 1) & 1u, err, abort_flag))) break;
-                tc_fence_after();
-                const uint64_t b0 = dv + (uint64_t)((s * L::kTile) >> 4);
-#pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)
-                    umma_bf16_ts(tmem_base + L::kOCol, tmem_base + (n & 1) * kKeys + kk * 8,
-                                 b0 + kk * ((16 * L::kRowBytes) >> 4), idesc_o,
-                                 (tp > sp.t0 || kk > 0) ? 1u : 0u);
-                umma_commit(v_empty(s));
-                umma_commit(pv_done(n & 1));
-                if (++tp == sp.t1) {
-                    hp = next_seg(wp, sp, gm, cum, slen);
-                    tp = hp ? sp.t0 : 0;
-                }
-                if (n + 2 < tiles) do_s();
+        constexpr uint32_t idesc_s = umma_idesc_bf16(kRowsP, kKeys);
+        constexpr uint32_t idesc_o = umma_idesc_bf16(kRowsP, DH, true);
+        const uint32_t tm = uniform(tmem_base);
+        const uint64_t dq = sdesc(sQ, L::kSwz, 16, L::kGroup), dk = sdesc(sK, L::kSwz, 16, L::kGroup);
+        const uint64_t dv = sdesc(sV, L::kSwz, DH > 64 ? L::kSubTile : 0, L::kGroup);
+        bool ok = true;
+        int slot = 0, cur = 0, ls = 0, lp = 0;          // Q slots; tiles left in the pieces of S and P.V
+        uint32_t q_par = 0, asub = 0;
+        uint64_t a0 = 0;
+        Walk ws = walk, wp = walk;
+        Seg ss, sp;
+        auto do_s = [&](int n) {
+            if (ls == 0) {
+                next_seg(ws, ss, gm, cum, slen);
+                ls = (int)uniform(ss.t1 - ss.t0);
+                const bool own = uniform(ss.own);
+                cur = own ? slot : 0;
+                slot = own ? (cur + 1 == gm.q_slots ? 0 : cur + 1) : 0;
+                a0 = dq + (uint64_t)((own ? cur * gm.q_pad * DH * 2 : 0) >> 4);
+                asub = ((own ? gm.q_pad : kRowsP) * L::kRowBytes) >> 4;
+                if (!(ok = warp_wait(q_full(cur), (q_par >> cur) & 1u, err, abort_flag))) return;
+                q_par ^= 1u << cur;
             }
-            umma_commit(done_bar);
-            mbar_wait(done_bar, 0, err, abort_flag);
+            const int s = n % R;
+            if (!(ok = warp_wait(k_full(s), (uint32_t)(n / R) & 1u, err, abort_flag))) return;
+            tc_fence_after();
+            const uint64_t b0 = dk + (uint64_t)((s * L::kTile) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < DH / 16; ++kk)
+                umma_bf16_e(tm + (n & 1) * kKeys, a0 + (kk >> 2) * asub + (kk & 3) * 2,
+                            b0 + (kk >> 2) * (L::kSubTile >> 4) + (kk & 3) * 2, idesc_s, kk > 0 ? 1u : 0u);
+            umma_commit_e(s_done(s));
+            if (--ls == 0) umma_commit_e(q_empty(cur));
+        };
+        if (tiles > 0) do_s(0);
+        if (ok && tiles > 1) do_s(1);
+        bool own = false, first = false;
+        for (int n = 0; n < tiles && ok; ++n) {
+            first = lp == 0;
+            if (first) {
+                next_seg(wp, sp, gm, cum, slen);
+                lp = (int)uniform(sp.t1 - sp.t0);
+                own = uniform(sp.own);
+            }
+            const int s = n % R;
+            if (!(ok = warp_wait(v_clean(s), (uint32_t)(n / R) & 1u, err, abort_flag))) break;
+            if (!(ok = warp_wait(p_full(own, n), p_phase(own, n), err, abort_flag))) break;
+            tc_fence_after();
+            const uint64_t b0 = dv + (uint64_t)((s * L::kTile) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+                umma_bf16_ts_e(tm + L::kOCol, tm + (n & 1) * kKeys + kk * 8,
+                               b0 + kk * ((16 * L::kRowBytes) >> 4), idesc_o, (!first || kk > 0) ? 1u : 0u);
+            umma_commit_e(pv_done(s));
+            --lp;
+            if (n + 2 < tiles) do_s(n + 2);
         }
+        umma_commit_e(done_bar);
+        warp_wait(done_bar, 0, err, abort_flag);
     } else if (warp == 6) {
         // ---------------------------------------------------------- V check
         // Values that are not finite are taken out of the tiles whose keys some
         // row does not see (zero times infinity is not zero) and added back in
-        // the epilogue for the rows that do.
+        // the epilogue for the rows that do.  Every tile passes through here, so
+        // that a V slot is never refilled past a phase this warp has not seen.
         Walk wv = walk;
         Seg sv;
         bool ok = true;
@@ -456,7 +458,10 @@ __global__ void __launch_bounds__(kThreadsX, 2)
             for (int t = sv.t0; t < sv.t1; ++t, ++n) {
                 const int s = n % R;
                 if (!(ok = warp_wait(v_full(s), (uint32_t)(n / R) & 1u, err, abort_flag))) break;
-                if (!check_tile(sv, t, gm.T)) continue;
+                if (!check_tile(sv, t, gm.T)) {
+                    if (lane == 0) mbar_arrive(v_clean(s));
+                    continue;
+                }
                 const uint32_t at = sV + s * L::kTile + lane * 16;
                 bool found = false;
 #pragma unroll 1
@@ -494,15 +499,23 @@ __global__ void __launch_bounds__(kThreadsX, 2)
         bool ok = true;
         int n = 0;
         for (int seg = 0; ok && next_seg(ww, sg, gm, cum, slen); ++seg) {
-            const bool busy = warp * 32 < sg.rows;     // warps without rows only keep step
+            if (warp * 32 >= sg.rows) {                // this warp has no row of the piece
+                if (sg.own || warp * 32 >= gm.nb * gm.GT) break;       // nor of any later one
+                // the prefix's last row tile: keep step
+                for (int t = sg.t0; t < sg.t1 && ok; ++t, ++n) {
+                    ok = warp_wait(s_done(n % R), (uint32_t)(n / R) & 1u, err, abort_flag);
+                    if (lane == 0) mbar_arrive(p_pre(n & 1));
+                }
+                continue;
+            }
             // keys this row sees: all of the prefix, or the own ones up to its token
             const int lim = sg.own ? sg.keys - (gm.T - 1 - r % gm.T) : sg.keys;
             float m = -INFINITY, l = 0.f;
             for (int t = sg.t0; t < sg.t1; ++t, ++n) {
                 const int sb = n & 1;
-                if (!warp_wait(s_full(sb), (uint32_t)(n >> 1) & 1u, err, abort_flag)) { ok = false; break; }
+                if (!warp_wait(s_done(n % R), (uint32_t)(n / R) & 1u, err, abort_flag)) { ok = false; break; }
                 tc_fence_after();
-                if (busy) {
+                {
                     const uint32_t t_s = tmem_base + sb * kKeys + lane_off;
                     uint32_t sr[2][32];
                     tmem_ld32_issue(t_s, sr[0]);
@@ -554,7 +567,7 @@ __global__ void __launch_bounds__(kThreadsX, 2)
                     l = l * corr + (((sa[0] + sb4[0]) + (sa[1] + sb4[1])) + ((sa[2] + sb4[2]) + (sa[3] + sb4[3])));
                     if (need_rescale) {
                         // O must hold P_{n-1} V_{n-1}
-                        if (!warp_wait(pv_done((n - 1) & 1), (uint32_t)((n - 1) >> 1) & 1u, err, abort_flag)) {
+                        if (!warp_wait(pv_done((n - 1) % R), (uint32_t)((n - 1) / R) & 1u, err, abort_flag)) {
                             ok = false;
                             break;
                         }
@@ -571,11 +584,10 @@ __global__ void __launch_bounds__(kThreadsX, 2)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(sb));
+                if (lane == 0) mbar_arrive(p_full(sg.own, n));
             }
             if (!ok) break;
-            if (!busy) continue;
-            if (!warp_wait(pv_done((n - 1) & 1), (uint32_t)((n - 1) >> 1) & 1u, err, abort_flag)) {
+            if (!warp_wait(pv_done((n - 1) % R), (uint32_t)((n - 1) / R) & 1u, err, abort_flag)) {
                 ok = false;
                 break;
             }
