@@ -632,26 +632,28 @@ __global__ void __launch_bounds__(kThreadsX, 2)
     if (warp == 5) tmem_dealloc(tmem_base, 256);
 }
 
-// A thread joins 16 columns of a row, its pieces of the prefix job and of the own
-// job; a CTA takes the 128 rows of a row tile, whose prefix pieces lie side by side.
+// A thread joins four columns of a row, its pieces of the prefix job and of the
+// own job, eight at a time: maxima, sums and values of all eight are in flight
+// together, so that a row costs one trip to L2 per eight pieces.  A CTA takes the
+// 128 rows of a row tile, whose prefix pieces lie side by side.
 template <int DH>
 __global__ void __launch_bounds__(kRowsP) k_prefix_join(PrefixParts in, PrefixGeom gm, int H,
                                                         __nv_bfloat16* __restrict__ o) {
-    pdl_wait();
-    pdl_trigger();
-    constexpr int S = DH / 16;
-    const int slice = (int)blockIdx.x % S, pj = (int)blockIdx.x / S;
+    constexpr int S = DH / 4;
+    const int c4 = (int)blockIdx.x % S, pj = (int)blockIdx.x / S;
     const int g = pj / gm.nrt, rt = pj - g * gm.nrt, r = threadIdx.x;
     const int b = rt * gm.nb + r / gm.GT, i = r % gm.GT;
+    pdl_wait();
+    pdl_trigger();
     if (r >= gm.nb * gm.GT || b >= gm.B) return;
-    const int units = gm.Hkv * (gm.nrt * gm.np + __ldg(in.cum + gm.B)), up = gm.Hkv * gm.nrt * gm.np;
+    const int all = __ldg(in.cum + gm.B), c0 = __ldg(in.cum + b), nt = __ldg(in.cum + b + 1) - c0;
+    const int up = gm.Hkv * gm.nrt * gm.np, units = up + gm.Hkv * all;
     // the pieces of a job: one per CTA of a run of CTAs
     int n_pre = 0, n_own = 0, first_pre = 0, first_own = 0;
     if (gm.np) {
         first_pre = cta_of(pj * gm.np, units, gm.ctas);
         n_pre = cta_of((pj + 1) * gm.np - 1, units, gm.ctas) - first_pre + 1;
     }
-    const int c0 = __ldg(in.cum + b), nt = __ldg(in.cum + b + 1) - c0;
     if (nt) {
         const int a = up + c0 * gm.Hkv + g * nt;
         first_own = cta_of(a, units, gm.ctas);
@@ -660,47 +662,53 @@ __global__ void __launch_bounds__(kRowsP) k_prefix_join(PrefixParts in, PrefixGe
     const int64_t pre = pj + first_pre, own = (int64_t)b * gm.Hkv + g + first_own;
     const float2* ml_pre = in.ml_prefix + pre * kRowsP + r;
     const float2* ml_own = in.ml_own + own * gm.GT + i;
-    float M = -INFINITY;
-#pragma unroll 8
-    for (int k = 0; k < n_pre; ++k) M = fmaxf(M, ml_pre[(int64_t)k * kRowsP].x);
-#pragma unroll 8
-    for (int k = 0; k < n_own; ++k) M = fmaxf(M, ml_own[(int64_t)k * gm.GT].x);
-    float L = 0.f, acc[16];
+    const float4* o_pre = reinterpret_cast<const float4*>(in.o_prefix) + (pre * S + c4) * kRowsP + r;
+    const float4* o_own = reinterpret_cast<const float4*>(in.o_own) + (own * S + c4) * gm.GT + i;
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int n = n_pre + n_own;
+    for (int k0 = 0; k0 < n; k0 += 8) {
+        float2 ml[8];
+        float4 v[8];
 #pragma unroll
-    for (int c = 0; c < 16; ++c) acc[c] = 0.f;
-    auto add = [&](const float2 ml, const float4* __restrict__ src, int stride) {
-        // A piece in which the row sees nothing holds (-inf, 0) and no value; one of
-        // NaN scores alone (-inf, NaN).
-        const bool none = ml.x == -INFINITY;
-        const float w = none ? 0.f : exp2f(ml.x - M);
-        L += none ? ml.y : w * ml.y;
-        float4 v[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] = src[c * stride];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            if (none) continue;
-            acc[4 * c] = fmaf(w, v[c].x, acc[4 * c]);
-            acc[4 * c + 1] = fmaf(w, v[c].y, acc[4 * c + 1]);
-            acc[4 * c + 2] = fmaf(w, v[c].z, acc[4 * c + 2]);
-            acc[4 * c + 3] = fmaf(w, v[c].w, acc[4 * c + 3]);
+        for (int j = 0; j < 8; ++j) {
+            const int k = k0 + j;
+            ml[j] = make_float2(-INFINITY, 0.f);
+            v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k < n_pre) {
+                ml[j] = ml_pre[(int64_t)k * kRowsP];
+                v[j] = o_pre[(int64_t)k * S * kRowsP];
+            } else if (k < n) {
+                ml[j] = ml_own[(int64_t)(k - n_pre) * gm.GT];
+                v[j] = o_own[(int64_t)(k - n_pre) * S * gm.GT];
+            }
         }
-    };
-    const float4* o_pre = reinterpret_cast<const float4*>(in.o_prefix) + (pre * (DH / 4) + slice * 4) * kRowsP + r;
-    const float4* o_own = reinterpret_cast<const float4*>(in.o_own) + (own * (DH / 4) + slice * 4) * gm.GT + i;
-#pragma unroll 4
-    for (int k = 0; k < n_pre; ++k)
-        add(ml_pre[(int64_t)k * kRowsP], o_pre + (int64_t)k * (DH / 4) * kRowsP, kRowsP);
-#pragma unroll 4
-    for (int k = 0; k < n_own; ++k)
-        add(ml_own[(int64_t)k * gm.GT], o_own + (int64_t)k * (DH / 4) * gm.GT, gm.GT);
+        float Mn = M;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) Mn = fmaxf(Mn, ml[j].x);
+        const float keep = M == -INFINITY ? 0.f : exp2f(M - Mn);
+        // (the sum of pieces without a maximum is 0, or NaN if the scores are: it goes on)
+        L = M == -INFINITY ? L : L * keep;
+        acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            // A piece in which the row sees nothing holds (-inf, 0) and no value; one of
+            // NaN scores alone (-inf, NaN).
+            const bool none = ml[j].x == -INFINITY;
+            const float w = none ? 0.f : exp2f(ml[j].x - Mn);
+            L += none ? ml[j].y : w * ml[j].y;
+            if (none) continue;
+            acc.x = fmaf(w, v[j].x, acc.x);
+            acc.y = fmaf(w, v[j].y, acc.y);
+            acc.z = fmaf(w, v[j].z, acc.z);
+            acc.w = fmaf(w, v[j].w, acc.w);
+        }
+        M = Mn;
+    }
     const float inv = L == 0.f ? 0.f : 1.0f / L;       // no key at all: zeros
     const int hh = i / gm.T, t = i - hh * gm.T, h = g * (gm.GT / gm.T) + hh;
-    uint4* dst = reinterpret_cast<uint4*>(o + ((int64_t)(b * gm.T + t) * H + h) * DH + slice * 16);
-#pragma unroll
-    for (int c = 0; c < 16; c += 8)
-        dst[c / 8] = make_uint4(pack_bf16x2(acc[c] * inv, acc[c + 1] * inv), pack_bf16x2(acc[c + 2] * inv, acc[c + 3] * inv),
-                                pack_bf16x2(acc[c + 4] * inv, acc[c + 5] * inv), pack_bf16x2(acc[c + 6] * inv, acc[c + 7] * inv));
+    *reinterpret_cast<uint2*>(o + ((int64_t)(b * gm.T + t) * H + h) * DH + c4 * 4) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -768,7 +776,7 @@ cudaError_t launch_dh(const PrefixArgs& a, PrefixGeom g, const CUtensorMap* maps
                    maps[3], maps[4], maps[5], static_cast<const __nv_bfloat16*>(a.vc), a.lens, g, parts,
                    a.scale * 1.4426950408889634f, device_error_word());
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_prefix_join<DH>, dim3((unsigned)(g.Hkv * g.nrt * (DH / 16))), dim3(kRowsP), 0, st, parts, g, a.H,
+    return launch_pdl(k_prefix_join<DH>, dim3((unsigned)(g.Hkv * g.nrt * (DH / 4))), dim3(kRowsP), 0, st, parts, g, a.H,
                       static_cast<__nv_bfloat16*>(a.o));
 }
 
