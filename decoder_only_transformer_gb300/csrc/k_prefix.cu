@@ -43,10 +43,12 @@ struct Px {
     static constexpr int kSubTile = kKeys * kRowBytes;
     static constexpr int kRing = DH == 128 ? 2 : DH == 64 ? 4 : 6;
     static constexpr int kMaxQ = 8;                          // Q slots of own jobs
-    static constexpr int kKOff = kQ;
-    static constexpr int kVOff = kKOff + kRing * kTile;
+    // Q lies between the rings: the MMA reads 128 rows from an own piece's slot on,
+    // whose last one ends with the region
+    static constexpr int kQOff = kRing * kTile;
+    static constexpr int kVOff = kQOff + kQ;
     static constexpr int kBarOff = kVOff + kRing * kTile;
-    static constexpr int kNumBars = 2 * kMaxQ + 5 * kRing + 5;
+    static constexpr int kNumBars = 2 * kMaxQ + 4 * kRing + 5;
     static constexpr int kMiscOff = kBarOff + 8 * kNumBars;
     static constexpr int kCumOff = kMiscOff + 16 + 4 * kPoisonX;
     static constexpr int kBase = kCumOff + 1024;             // + 4 (2 B + 1)
@@ -54,6 +56,7 @@ struct Px {
     static constexpr uint32_t kSwz = DH == 32 ? 4u : 2u;
     static constexpr uint32_t kGroup = 8 * kRowBytes;
     static_assert(kOCol + DH <= 256, "tensor memory: two CTAs per SM");
+    static_assert(kRing * kTile >= kRowsP * kRowBytes, "room around the Q slots");
 };
 
 // How the work is laid out; the same on the host and in both kernels.
@@ -84,12 +87,18 @@ __device__ __forceinline__ int own_len(const int32_t* __restrict__ lens, int b, 
 // A piece of a job: key tiles [t0, t1) of it.
 struct Seg {
     int own;           // 0: prefix
-    int g, b;          // kv head; first sequence of the row tile, or the sequence
+    int g, x;          // kv head; row tile, or sequence
     int t0, t1;
-    int keys;          // P, or the sequence's length
-    int rows;          // valid rows
-    int job;           // index among the jobs of its kind
 };
+__device__ __forceinline__ int keys_of(const Seg& s, const PrefixGeom& gm, const int* slen) {
+    return s.own ? slen[s.x] : gm.P;
+}
+__device__ __forceinline__ int rows_of(const Seg& s, const PrefixGeom& gm) {
+    return s.own ? gm.GT : min(gm.nb, gm.B - s.x * gm.nb) * gm.GT;
+}
+__device__ __forceinline__ int job_of(const Seg& s, const PrefixGeom& gm) {    // among the jobs of its kind
+    return s.own ? s.x * gm.Hkv + s.g : s.g * gm.nrt + s.x;
+}
 
 // A run's next tile: tile t of the job of kv head g and row tile x, or (own) of
 // sequence x.  Jobs follow one another as prefix (g, x), then own (x, g), so the
@@ -126,29 +135,12 @@ __device__ __forceinline__ Walk start_walk(int u, int end, int up, const PrefixG
     return w;
 }
 
-__device__ __forceinline__ bool next_seg(Walk& w, Seg& s, const PrefixGeom& gm, const int* cum,
-                                         const int* slen) {
+__device__ __forceinline__ bool next_seg(Walk& w, Seg& s, const PrefixGeom& gm, const int* cum) {
     if (w.left <= 0) return false;
-    s.own = w.own;
-    s.g = w.g;
-    s.t0 = w.t;
-    int nt;
-    if (w.own) {
-        nt = cum[w.x + 1] - cum[w.x];
-        s.b = w.x;
-        s.keys = slen[w.x];
-        s.rows = gm.GT;
-        s.job = w.x * gm.Hkv + w.g;
-    } else {
-        nt = gm.np;
-        s.b = w.x * gm.nb;
-        s.keys = gm.P;
-        s.rows = min(gm.nb, gm.B - s.b) * gm.GT;
-        s.job = w.g * gm.nrt + w.x;
-    }
-    s.t1 = min(nt, w.t + w.left);
+    s = Seg{w.own, w.g, w.x, w.t, min(w.own ? cum[w.x + 1] - cum[w.x] : gm.np, w.t + w.left)};
     w.left -= s.t1 - s.t0;
-    w.t = 0;                                           // a run ends, or goes on with a new job
+    if (w.left == 0) return true;
+    w.t = 0;                                           // the run goes on with the next job
     if (w.own) {
         if (++w.g == gm.Hkv) {
             w.g = 0;
@@ -168,8 +160,8 @@ __device__ __forceinline__ bool next_seg(Walk& w, Seg& s, const PrefixGeom& gm, 
 
 // An own tile that holds keys some row does not see: behind the length, or the
 // newest tokens' own.
-__device__ __forceinline__ bool check_tile(const Seg& s, int t, int T) {
-    return s.own && (t + 1) * kKeys > s.keys - (T - 1);
+__device__ __forceinline__ bool check_tile(const Seg& s, int t, int keys, int T) {
+    return s.own && (t + 1) * kKeys > keys - (T - 1);
 }
 
 // cum[b]: key tiles of the own caches of sequences before b; slen[b]: their
@@ -212,6 +204,17 @@ struct PrefixParts {
     int* cum;              // [B + 1]
 };
 
+// Adds the values of keys [k0, k1) that are not finite to a row's partial O in
+// memory (column c at (c / 4) * stride + c % 4).
+__device__ __noinline__ void put_back(float* orow, int stride, const __nv_bfloat16* __restrict__ v, int dh,
+                                      int k0, int k1) {
+    for (int key = k0; key < k1; ++key)
+        for (int c = 0; c < dh; ++c) {
+            const float w = __bfloat162float(v[(int64_t)key * dh + c]);
+            if (!(fabsf(w) < INFINITY)) orow[(int64_t)(c >> 2) * stride + (c & 3)] += w;
+        }
+}
+
 template <int DH>
 __global__ void __launch_bounds__(kThreadsX, 2)
     k_prefix_part(const __grid_constant__ CUtensorMap qpmap, const __grid_constant__ CUtensorMap qomap,
@@ -225,18 +228,21 @@ __global__ void __launch_bounds__(kThreadsX, 2)
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - raw);
-    const uint32_t sQ = base, sK = base + L::kKOff, sV = base + L::kVOff, bars = base + L::kBarOff;
+    const uint32_t sK = base, sQ = base + L::kQOff, sV = base + L::kVOff, bars = base + L::kBarOff;
     auto q_full = [&](int s) { return bars + 8u * s; };
     auto q_empty = [&](int s) { return bars + 8u * (L::kMaxQ + s); };
     constexpr int B0 = 2 * L::kMaxQ;
     auto k_full = [&](int s) { return bars + 8u * (B0 + s); };
     auto v_full = [&](int s) { return bars + 8u * (B0 + R + s); };
-    auto v_clean = [&](int s) { return bars + 8u * (B0 + 2 * R + s); };
     // S of a K slot is complete (the slot is free, S can be read); P.V of a V slot
-    auto s_done = [&](int s) { return bars + 8u * (B0 + 3 * R + s); };
-    auto pv_done = [&](int s) { return bars + 8u * (B0 + 4 * R + s); };
-    constexpr int B1 = B0 + 5 * R;
-    auto p_pre = [&](int i) { return bars + 8u * (B1 + i); };      // P of a prefix tile, of an own one
+    auto s_done = [&](int s) { return bars + 8u * (B0 + 2 * R + s); };
+    auto pv_done = [&](int s) { return bars + 8u * (B0 + 3 * R + s); };
+    constexpr int B1 = B0 + 4 * R;
+    // Tile n can be multiplied: P is written (by the softmax warps with rows), V_n
+    // is there and checked and K_{n+2} is there (the check warp), so that the MMA
+    // warp, whose every wait costs ~100 cycles, waits once per tile.  The own
+    // tiles have barriers of their own, as fewer softmax warps write their P.
+    auto p_pre = [&](int i) { return bars + 8u * (B1 + i); };
     auto p_own = [&](int i) { return bars + 8u * (B1 + 2 + i); };
     const uint32_t done_bar = bars + 8u * (B1 + 4);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(gbase + L::kMiscOff);
@@ -255,16 +261,15 @@ __global__ void __launch_bounds__(kThreadsX, 2)
         for (int s = 0; s < R; ++s) {
             mbar_init(k_full(s), 1);
             mbar_init(v_full(s), 1);
-            mbar_init(v_clean(s), 1);
             mbar_init(s_done(s), 1);
             mbar_init(pv_done(s), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(p_pre(i), (min(gm.nb, gm.B) * gm.GT + 31) / 32);   // softmax warps with rows
-            mbar_init(p_own(i), (gm.GT + 31) / 32);
+            mbar_init(p_pre(i), (gm.nb * gm.GT + 31) / 32 + 1);    // softmax warps with rows, check warp
+            mbar_init(p_own(i), (gm.GT + 31) / 32 + 1);
         }
         mbar_init(done_bar, 1);
-        *abort_flag = 0;
+        abort_flag[0] = abort_flag[1] = 0;
         for (int i = 0; i < kPoisonX; ++i) poison[i] = 0;
         fence_mbar_init();
         tma_prefetch_desc(&qpmap);
@@ -291,9 +296,7 @@ __global__ void __launch_bounds__(kThreadsX, 2)
     const int up = gm.Hkv * gm.nrt * gm.np, units = up + gm.Hkv * cum[gm.B];
     const Walk walk = start_walk(run_start(cta, units, gm.ctas), run_start(cta + 1, units, gm.ctas), up, gm, cum);
     const int tiles = (int)uniform(walk.left);         // of this CTA, in all its pieces
-    // its first own tile: P of the own tiles has barriers of its own, as fewer
-    // softmax warps write it
-    const int own0 = max(0, min(tiles, up - run_start(cta, units, gm.ctas)));
+    const int own0 = max(0, min(tiles, up - run_start(cta, units, gm.ctas)));   // its first own tile
     auto p_full = [&](bool own, int n) { return own ? p_own(n & 1) : p_pre(n & 1); };
     auto p_phase = [&](bool own, int n) {
         return (uint32_t)((n >> 1) - (own ? (own0 + ((n ^ own0) & 1)) >> 1 : 0)) & 1u;
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(kThreadsX, 2)
         int slot = 0;
         uint32_t q_used = 0, q_par = 0;                 // slots used before, their parity
         Walk wk = walk, wv = walk;
-        Seg sk, sv;
+        Seg sk{}, sv{};
         int lk = 0, lv = 0;                             // tiles left in the pieces of K and V
         auto load_q = [&]() {
             const bool own = uniform(sk.own);
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(kThreadsX, 2)
             const uint32_t dst = sQ + (own ? s * gm.q_pad * DH * 2 : 0);
             const uint32_t sub = (own ? gm.q_pad : kRowsP) * L::kRowBytes;
             const CUtensorMap* map = own ? &qomap : &qpmap;
-            const int g = (int)uniform(sk.g), b = (int)uniform(sk.b);
+            const int g = (int)uniform(sk.g), b = (int)uniform(own ? sk.x : sk.x * gm.nb);
             mbar_arrive_expect_tx_e(q_full(s), (uint32_t)rows * DH * 2);
 #pragma unroll
             for (int c = 0; c < L::kSub; ++c) tma_load_4d_e(dst + c * sub, map, 64 * c, 0, g, b, q_full(s));
@@ -338,10 +341,10 @@ __global__ void __launch_bounds__(kThreadsX, 2)
             const int s = n % R;
             if (n < tiles) {
                 if (lk == 0) {
-                    next_seg(wk, sk, gm, cum, slen);
+                    next_seg(wk, sk, gm, cum);
                     lk = (int)uniform(sk.t1 - sk.t0);
                     ky = (int)uniform(sk.t0) * kKeys;
-                    kz = (int)uniform(sk.own ? sk.b * gm.Hkv + sk.g : sk.g);
+                    kz = (int)uniform(sk.own ? sk.x * gm.Hkv + sk.g : sk.g);
                     km = uniform(sk.own) ? &kcmap : &kpmap;
                     load_q();
                     if (!ok) break;
@@ -358,10 +361,10 @@ __global__ void __launch_bounds__(kThreadsX, 2)
             if (n > 0) {
                 const int m = n - 1, sv_ = m % R;
                 if (lv == 0) {
-                    next_seg(wv, sv, gm, cum, slen);
+                    next_seg(wv, sv, gm, cum);
                     lv = (int)uniform(sv.t1 - sv.t0);
                     vy = (int)uniform(sv.t0) * kKeys;
-                    vz = (int)uniform(sv.own ? sv.b * gm.Hkv + sv.g : sv.g);
+                    vz = (int)uniform(sv.own ? sv.x * gm.Hkv + sv.g : sv.g);
                     vm = uniform(sv.own) ? &vcmap : &vpmap;
                 }
                 if (m >= R && !(ok = warp_wait(pv_done(sv_), ((uint32_t)(m / R) & 1u) ^ 1u, err, abort_flag))) break;
@@ -374,12 +377,12 @@ __global__ void __launch_bounds__(kThreadsX, 2)
                 ++vn;
             }
         }
-        // The MMA and check warps wait for every load; after a wait that gave up,
+        // The other warps wait for every load; after a wait that gave up,
         // the last ones still have to land before the CTA ends.
         if (!ok && lane == 0) {
-            volatile int never = 0;
-            for (int m = max(0, kn - R); m < kn; ++m) mbar_wait(k_full(m % R), (uint32_t)(m / R) & 1u, nullptr, &never);
-            for (int m = max(0, vn - R); m < vn; ++m) mbar_wait(v_full(m % R), (uint32_t)(m / R) & 1u, nullptr, &never);
+            volatile int* never = abort_flag + 1;       // stays 0: these waits run to their own limit
+            for (int m = max(0, kn - R); m < kn; ++m) mbar_wait(k_full(m % R), (uint32_t)(m / R) & 1u, nullptr, never);
+            for (int m = max(0, vn - R); m < vn; ++m) mbar_wait(v_full(m % R), (uint32_t)(m / R) & 1u, nullptr, never);
         }
     } else if (warp == 5) {
         // ---------------------------------------------------------- MMAs
@@ -398,7 +401,7 @@ __global__ void __launch_bounds__(kThreadsX, 2)
         Seg ss, sp;
         auto do_s = [&](int n) {
             if (ls == 0) {
-                next_seg(ws, ss, gm, cum, slen);
+                next_seg(ws, ss, gm, cum);
                 ls = (int)uniform(ss.t1 - ss.t0);
                 const bool own = uniform(ss.own);
                 cur = own ? slot : 0;
@@ -409,7 +412,8 @@ __global__ void __launch_bounds__(kThreadsX, 2)
                 q_par ^= 1u << cur;
             }
             const int s = n % R;
-            if (!(ok = warp_wait(k_full(s), (uint32_t)(n / R) & 1u, err, abort_flag))) return;
+            if (n < 2) ok = warp_wait(k_full(s), (uint32_t)(n / R) & 1u, err, abort_flag);
+            if (!ok) return;
             tc_fence_after();
             const uint64_t b0 = dk + (uint64_t)((s * L::kTile) >> 4);
 #pragma unroll
@@ -425,12 +429,11 @@ __global__ void __launch_bounds__(kThreadsX, 2)
         for (int n = 0; n < tiles && ok; ++n) {
             first = lp == 0;
             if (first) {
-                next_seg(wp, sp, gm, cum, slen);
+                next_seg(wp, sp, gm, cum);
                 lp = (int)uniform(sp.t1 - sp.t0);
                 own = uniform(sp.own);
             }
             const int s = n % R;
-            if (!(ok = warp_wait(v_clean(s), (uint32_t)(n / R) & 1u, err, abort_flag))) break;
             if (!(ok = warp_wait(p_full(own, n), p_phase(own, n), err, abort_flag))) break;
             tc_fence_after();
             const uint64_t b0 = dv + (uint64_t)((s * L::kTile) >> 4);
@@ -448,18 +451,22 @@ __global__ void __launch_bounds__(kThreadsX, 2)
         // ---------------------------------------------------------- V check
         // Values that are not finite are taken out of the tiles whose keys some
         // row does not see (zero times infinity is not zero) and added back in
-        // the epilogue for the rows that do.  Every tile passes through here, so
-        // that a V slot is never refilled past a phase this warp has not seen.
+        // the epilogue for the rows that do.  This warp goes in step with the MMAs
+        // (its arrival for tile n comes behind S_n, which comes behind P.V of tile
+        // n - 2), so no barrier runs past a phase that it has not seen.
         Walk wv = walk;
         Seg sv;
         bool ok = true;
         int n = 0;
-        for (int seg = 0; ok && next_seg(wv, sv, gm, cum, slen); ++seg)
+        for (int seg = 0; ok && next_seg(wv, sv, gm, cum); ++seg)
             for (int t = sv.t0; t < sv.t1; ++t, ++n) {
                 const int s = n % R;
-                if (!(ok = warp_wait(v_full(s), (uint32_t)(n / R) & 1u, err, abort_flag))) break;
-                if (!check_tile(sv, t, gm.T)) {
-                    if (lane == 0) mbar_arrive(v_clean(s));
+                ok = warp_wait(s_done(s), (uint32_t)(n / R) & 1u, err, abort_flag) &&
+                     warp_wait(v_full(s), (uint32_t)(n / R) & 1u, err, abort_flag) &&
+                     (n + 2 >= tiles || warp_wait(k_full((n + 2) % R), (uint32_t)((n + 2) / R) & 1u, err, abort_flag));
+                if (!ok) break;
+                if (!check_tile(sv, t, keys_of(sv, gm, slen), gm.T)) {
+                    if (lane == 0) mbar_arrive(p_full(sv.own, n));
                     continue;
                 }
                 const uint32_t at = sV + s * L::kTile + lane * 16;
@@ -487,20 +494,23 @@ __global__ void __launch_bounds__(kThreadsX, 2)
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(v_clean(s));
+                if (lane == 0) mbar_arrive(p_full(sv.own, n));
             }
     } else {
         // ---------------------------------------------------------- softmax (warps 0..3)
-        const int r = warp * 32 + lane;
         const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-        const uint32_t t_o = tmem_base + L::kOCol + lane_off;
         Walk ww = walk;
         Seg sg;
         bool ok = true;
         int n = 0;
-        for (int seg = 0; ok && next_seg(ww, sg, gm, cum, slen); ++seg) {
-            if (warp * 32 >= sg.rows) {                // this warp has no row of the piece
-                if (sg.own || warp * 32 >= gm.nb * gm.GT) break;       // nor of any later one
+        for (int seg = 0; ok && next_seg(ww, sg, gm, cum); ++seg) {
+            const int r0 = warp * 32, r = r0 + lane;   // this warp's first row, this lane's row
+            if (r0 >= rows_of(sg, gm)) {               // this warp has no row of the piece
+                if (sg.own) break;                     // nor of any later one
+                if (r0 >= gm.nb * gm.GT) {             // nor of any prefix piece
+                    n += sg.t1 - sg.t0;
+                    continue;
+                }
                 // the prefix's last row tile: keep step
                 for (int t = sg.t0; t < sg.t1 && ok; ++t, ++n) {
                     ok = warp_wait(s_done(n % R), (uint32_t)(n / R) & 1u, err, abort_flag);
@@ -508,8 +518,12 @@ __global__ void __launch_bounds__(kThreadsX, 2)
                 }
                 continue;
             }
+            const uint32_t t_o = tmem_base + L::kOCol + lane_off;
             // keys this row sees: all of the prefix, or the own ones up to its token
-            const int lim = sg.own ? sg.keys - (gm.T - 1 - r % gm.T) : sg.keys;
+            const int keys = keys_of(sg, gm, slen);
+            const int lim = sg.own ? keys - (gm.T - 1 - r % gm.T) : keys;
+            const int full = sg.own ? keys - (gm.T - 1) : keys;        // keys that all rows see
+            const bool mine = r < rows_of(sg, gm);
             float m = -INFINITY, l = 0.f;
             for (int t = sg.t0; t < sg.t1; ++t, ++n) {
                 const int sb = n & 1;
@@ -527,7 +541,7 @@ __global__ void __launch_bounds__(kThreadsX, 2)
 #pragma unroll
                     for (int e = 0; e < kKeys; ++e) s[e] = __uint_as_float(sr[e >> 5][e & 31]);
                     const int k0 = t * kKeys;
-                    if (k0 + kKeys > sg.keys - (sg.own ? gm.T - 1 : 0)) {
+                    if (k0 + kKeys > full) {
                         const int d = lim - k0;
 #pragma unroll
                         for (int e = 0; e < kKeys; ++e) s[e] = e >= d ? -INFINITY : s[e];
@@ -545,21 +559,24 @@ __global__ void __launch_bounds__(kThreadsX, 2)
                         corr = fast_exp2(m - mx);
                         m = mx;
                     }
-                    const bool need_rescale = __any_sync(0xffffffffu, corr != 1.f && t > sg.t0 && r < sg.rows);
+                    const bool need_rescale = __any_sync(0xffffffffu, corr != 1.f && t > sg.t0 && mine);
                     const uint64_t scale2 = f2_pack(scale_log2, scale_log2);
                     const float negm = m == -INFINITY ? 0.f : -m;     // no visible key yet: every p is 0
                     const uint64_t negm2 = f2_pack(negm, negm);
                     uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
-                    uint32_t pw[32];
 #pragma unroll
-                    for (int e = 0; e < kKeys; e += 2) {
-                        float t0, t1;
-                        f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), scale2, negm2), t0, t1);
-                        const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
-                        sum2[(e >> 1) & 3] = f2_add(sum2[(e >> 1) & 3], f2_pack(p0, p1));
-                        pw[e >> 1] = pack_bf16x2(p0, p1);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pw[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float t0, t1;
+                            f2_unpack(f2_fma(f2_pack(s[32 * h + e], s[32 * h + e + 1]), scale2, negm2), t0, t1);
+                            const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
+                            sum2[(e >> 1) & 3] = f2_add(sum2[(e >> 1) & 3], f2_pack(p0, p1));
+                            pw[e >> 1] = pack_bf16x2(p0, p1);
+                        }
+                        tmem_st16_async(t_s + 16 * h, pw);
                     }
-                    tmem_st32_async(t_s, pw);
                     tmem_st_wait();
                     float sa[4], sb4[4];
 #pragma unroll
@@ -592,36 +609,33 @@ __global__ void __launch_bounds__(kThreadsX, 2)
                 break;
             }
             tc_fence_after();
-            const bool fix = poison[seg % kPoisonX] == seg + 1;
-            const int64_t piece = sg.job + cta;
+            const int64_t piece = job_of(sg, gm) + cta;
             const int stride = sg.own ? gm.GT : kRowsP;
             const int64_t row = piece * stride + r;
             float4* orow = reinterpret_cast<float4*>((sg.own ? out.o_own : out.o_prefix) + piece * stride * DH) + r;
-            const bool mine = r < sg.rows;
             if (mine) (sg.own ? out.ml_own : out.ml_prefix)[row] = make_float2(m, l);
 #pragma unroll 1
             for (int c = 0; c < DH / 32; ++c) {
                 float v[32];
                 tmem_ld32(t_o + c * 32, v);
                 if (mine) {
-                    if (fix) {
-                        const __nv_bfloat16* vb = vc + ((int64_t)sg.b * gm.Hkv + sg.g) * gm.max_seq * DH + c * 32;
-                        for (int t = sg.t0; t < sg.t1; ++t) {
-                            if (!check_tile(sg, t, gm.T)) continue;
-                            for (int key = t * kKeys; key < min((t + 1) * kKeys, lim); ++key)
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) {
-                                    const float w = __bfloat162float(vb[(int64_t)key * DH + e]);
-                                    if (!(fabsf(w) < INFINITY)) v[e] += w;
-                                }
-                        }
-                    }
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
                         orow[(c * 8 + e / 4) * stride] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                 }
                 __syncwarp();
             }
+            if (poison[seg % kPoisonX] == seg + 1 && mine) {
+                // what the V check took out, for the keys this row sees
+                const __nv_bfloat16* vb = vc + (int64_t)job_of(sg, gm) * gm.max_seq * DH;
+#pragma unroll 1
+                for (int t = sg.t0; t < sg.t1; ++t)
+                    if (check_tile(sg, t, keys, gm.T))
+                        put_back(reinterpret_cast<float*>(orow), stride * 4, vb, DH, t * kKeys,
+                                 min((t + 1) * kKeys, lim));
+            }
+            __syncwarp();
+            // O is read out before this warp publishes the next piece's first P
             tc_fence_before();
         }
     }
