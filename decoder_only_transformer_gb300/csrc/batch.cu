@@ -121,8 +121,8 @@ tfm_status tfm_prefix_attention(const void* q, const void* k_prefix, const void*
         return fail(TFM_EINVAL, "bad sizes: 0 <= B <= 4096, H %% Hkv == 0, T >= 1, B*H*T <= 2^24");
     if (prefix_len < 0 || max_prefix < prefix_len)
         return fail(TFM_EINVAL, "prefix_len=%d outside [0, max_prefix=%d]", prefix_len, max_prefix);
-    if (max_seq < 1 || (int64_t)B * Hkv * max_seq > INT32_MAX || (int64_t)Hkv * max_prefix > INT32_MAX)
-        return fail(TFM_EINVAL, "max_seq must be positive, B*Hkv*max_seq and Hkv*max_prefix below 2^31");
+    if (max_seq < 1 || (int64_t)B * Hkv * max_seq >= (1 << 30) || (int64_t)Hkv * max_prefix > INT32_MAX)
+        return fail(TFM_EINVAL, "max_seq must be positive, B*Hkv*max_seq below 2^30, Hkv*max_prefix below 2^31");
     if (!std::isfinite(scale)) return fail(TFM_EINVAL, "scale must be finite");
     if (dh != 32 && dh != 64 && dh != 128) return fail(TFM_EUNSUPPORTED, "prefix attention: dh in {32, 64, 128}");
     if ((int64_t)(H / Hkv) * T > 128) return fail(TFM_EUNSUPPORTED, "prefix attention: (H / Hkv) * T <= 128");

@@ -15,9 +15,12 @@
 // HBM bandwidth, and its two products ~500.  (On CUDA cores G T = 4 rows would
 // already need ~40 % of all FMAs to keep up with memory.)
 //
-// All tiles of all jobs are laid end to end and cut into equal runs, one per
-// CTA, whatever the lengths are (two CTAs per SM, so that one's loads run during
-// the other's softmax).  A run crosses jobs; each piece of a job leaves (max,
+// All tiles of all jobs are laid end to end and cut into runs of equal cost, one
+// per CTA, whatever the lengths are (two CTAs per SM, so that one's loads run
+// during the other's softmax).  The cost of a tile and of a job's beginning and end
+// are measured cycles (Px below): short caches cost more per key than long ones, and
+// equal numbers of tiles left the last CTAs at twice the time of the first.  A run
+// crosses jobs; each piece of a job leaves (max,
 // sum, unnormalised O) per row, and a second kernel joins a row's pieces of the
 // prefix and its own cache exactly: with M = max m, o = sum 2^(m - M) O / sum 2^(m - M) l.
 #include "common.cuh"
@@ -51,10 +54,15 @@ struct Px {
     static constexpr int kNumBars = 2 * kMaxQ + 4 * kRing + 5;
     static constexpr int kMiscOff = kBarOff + 8 * kNumBars;
     static constexpr int kCumOff = kMiscOff + 16 + 4 * kPoisonX;
-    static constexpr int kBase = kCumOff + 1024;             // + 4 (2 B + 1)
+    static constexpr int kBase = kCumOff + 1024;             // + 4 (3 B + 2)
     static constexpr int kOCol = 2 * kKeys;                  // S 2 x 64 (P in its place), O
     static constexpr uint32_t kSwz = DH == 32 ? 4u : 2u;
     static constexpr uint32_t kGroup = 8 * kRowBytes;
+    // Costs in ~100 cycles of a CTA: a tile of the prefix (from L2, four softmax
+    // warps busy) and of an own cache (one warp; d_head 128: its share of HBM
+    // bandwidth), and what a piece costs besides (Q, the last P.V, writing O out).
+    static constexpr int kPreTile = DH == 128 ? 15 : 13, kPrePiece = DH == 128 ? 50 : 35;
+    static constexpr int kOwnTile = DH == 128 ? 24 : 13, kOwnPiece = DH == 128 ? 24 : 32;
     static_assert(kOCol + DH <= 256, "tensor memory: two CTAs per SM");
     static_assert(kRing * kTile >= kRowsP * kRowBytes, "room around the Q slots");
 };
@@ -69,7 +77,7 @@ struct PrefixGeom {
     int q_slots, q_pad;   // Q slots of own jobs, rows of each (GT padded)
 };
 
-// Run of CTA i of n over u units: [start, end).
+// Run of CTA i of n over a cost of u: [start, end).
 __device__ __forceinline__ int run_start(int i, int u, int n) {
     const int q = u / n, r = u - q * n;
     return i * q + min(i, r);
@@ -164,35 +172,81 @@ __device__ __forceinline__ bool check_tile(const Seg& s, int t, int keys, int T)
     return s.own && (t + 1) * kKeys > keys - (T - 1);
 }
 
-// cum[b]: key tiles of the own caches of sequences before b; slen[b]: their
-// lengths.  By the whole block.
-__device__ __forceinline__ void scan_lengths(int* cum, int* slen, int* warp_sum, const int32_t* __restrict__ lens,
-                                             const PrefixGeom& gm) {
+// cum[b]: key tiles of the own caches of sequences before b; cost[b]: their cost;
+// slen[b]: their lengths.  By the whole block.
+template <int DH>
+__device__ __forceinline__ void scan_lengths(int* cum, int* cost, int* slen, int2* warp_sum,
+                                             const int32_t* __restrict__ lens, const PrefixGeom& gm) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-    int base = 0;
+    int base = 0, base_c = 0;
     for (int b0 = 0; b0 < gm.B; b0 += blockDim.x) {
         const int b = b0 + tid;
         const int len = b < gm.B ? own_len(lens, b, gm.max_seq) : 0;
         if (b < gm.B) slen[b] = len;
         int sum = (len + kKeys - 1) / kKeys;
+        int sum_c = sum ? Px<DH>::kOwnPiece + sum * Px<DH>::kOwnTile : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += v;
+            const int v = __shfl_up_sync(0xffffffffu, sum, o), c = __shfl_up_sync(0xffffffffu, sum_c, o);
+            if (lane >= o) {
+                sum += v;
+                sum_c += c;
+            }
         }
-        if (lane == 31) warp_sum[warp] = sum;
+        if (lane == 31) warp_sum[warp] = make_int2(sum, sum_c);
         __syncthreads();
-        int before = base, all = base;
+        int before = base, before_c = base_c;
         for (int w = 0; w < nw; ++w) {
-            if (w < warp) before += warp_sum[w];
-            all += warp_sum[w];
+            if (w < warp) {
+                before += warp_sum[w].x;
+                before_c += warp_sum[w].y;
+            }
+            base += warp_sum[w].x;
+            base_c += warp_sum[w].y;
         }
-        if (b < gm.B) cum[b + 1] = before + sum;
-        base = all;
+        if (b < gm.B) {
+            cum[b + 1] = before + sum;
+            cost[b + 1] = before_c + sum_c;
+        }
         __syncthreads();
     }
-    if (tid == 0) cum[0] = 0;
+    if (tid == 0) cum[0] = cost[0] = 0;
     __syncthreads();
+}
+
+// Cost of everything, and of a job of the prefix.
+template <int DH>
+__device__ __forceinline__ int prefix_job_cost(const PrefixGeom& gm) {
+    return gm.np ? Px<DH>::kPrePiece + gm.np * Px<DH>::kPreTile : 0;
+}
+
+// CTAs that get a run: with runs of at least a tile's cost every run that lies
+// between a job's first and last piece has a tile of it.
+template <int DH>
+__device__ __forceinline__ int runs_of(int all, int ctas) {
+    constexpr int most = Px<DH>::kPreTile > Px<DH>::kOwnTile ? Px<DH>::kPreTile : Px<DH>::kOwnTile;
+    return max(1, min(ctas, all / most));
+}
+
+// The number of tiles that lie before cost c: a job's tiles end at its piece cost
+// plus one tile cost each.
+template <int DH>
+__device__ __forceinline__ int tiles_before(int c, const PrefixGeom& gm, const int* cum, const int* cost) {
+    const int jc = prefix_job_cost<DH>(gm), jobs = gm.Hkv * gm.nrt;
+    if (c < jc * jobs) {
+        const int job = c / jc;
+        return job * gm.np + max(0, (c - job * jc - Px<DH>::kPrePiece) / Px<DH>::kPreTile);
+    }
+    const int v = c - jc * jobs, up = jobs * gm.np;
+    if (v >= cost[gm.B] * gm.Hkv) return up + gm.Hkv * cum[gm.B];
+    int lo = 0, hi = gm.B;                            // the last b with cost[b] Hkv <= v
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (cost[mid] * gm.Hkv <= v) lo = mid + 1; else hi = mid;
+    }
+    const int b = lo - 1, each = cost[lo] - cost[b], nt = cum[lo] - cum[b];
+    const int x = v - cost[b] * gm.Hkv, g = x / each;
+    return up + gm.Hkv * cum[b] + g * nt + max(0, (x - g * each - Px<DH>::kOwnPiece) / Px<DH>::kOwnTile);
 }
 
 struct PrefixParts {
@@ -201,7 +255,7 @@ struct PrefixParts {
     float2* ml_prefix;     // [jobs + ctas][128]: max (log2), sum
     float* o_own;          // [B Hkv + ctas][dh / 4][GT][4]
     float2* ml_own;        // [B Hkv + ctas][GT]
-    int* cum;              // [B + 1]
+    int* cost;             // [B + 1]
 };
 
 // Adds the values of keys [k0, k1) that are not finite to a row's partial O in
@@ -249,8 +303,9 @@ __global__ void __launch_bounds__(kThreadsX, 2)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMiscOff + 4);
     volatile int* poison = reinterpret_cast<volatile int*>(gbase + L::kMiscOff + 16);
     int* cum = reinterpret_cast<int*>(gbase + L::kCumOff);
-    int* slen = cum + gm.B + 1;
-    __shared__ int warp_sum[kThreadsX / 32];
+    int* cost = cum + gm.B + 1;
+    int* slen = cost + gm.B + 1;
+    __shared__ int2 warp_sum[kThreadsX / 32];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 4 && lane == 0) {
@@ -286,17 +341,21 @@ __global__ void __launch_bounds__(kThreadsX, 2)
     const uint32_t tmem_base = *tmem_holder;
     pdl_wait();
     pdl_trigger();
-    scan_lengths(cum, slen, warp_sum, lens, gm);
+    scan_lengths<DH>(cum, cost, slen, warp_sum, lens, gm);
     const int cta = (int)blockIdx.x;
     if (cta == 0)
         for (int b = threadIdx.x; b <= gm.B; b += kThreadsX) {
-            out.cum[b] = cum[b];
+            out.cost[b] = cost[b];
             if (b < gm.B && (lens[b] < 0 || lens[b] > gm.max_seq)) raise_error(err, TFM_EINVAL);
         }
-    const int up = gm.Hkv * gm.nrt * gm.np, units = up + gm.Hkv * cum[gm.B];
-    const Walk walk = start_walk(run_start(cta, units, gm.ctas), run_start(cta + 1, units, gm.ctas), up, gm, cum);
+    const int up = gm.Hkv * gm.nrt * gm.np;
+    const int all = prefix_job_cost<DH>(gm) * gm.Hkv * gm.nrt + cost[gm.B] * gm.Hkv;
+    const int runs = runs_of<DH>(all, gm.ctas);
+    const int u0 = cta < runs ? tiles_before<DH>(run_start(cta, all, runs), gm, cum, cost) : 0;
+    const int u1 = cta < runs ? tiles_before<DH>(run_start(cta + 1, all, runs), gm, cum, cost) : 0;
+    const Walk walk = start_walk(u0, u1, up, gm, cum);
     const int tiles = (int)uniform(walk.left);         // of this CTA, in all its pieces
-    const int own0 = max(0, min(tiles, up - run_start(cta, units, gm.ctas)));   // its first own tile
+    const int own0 = max(0, min(tiles, up - u0));   // its first own tile
     auto p_full = [&](bool own, int n) { return own ? p_own(n & 1) : p_pre(n & 1); };
     auto p_phase = [&](bool own, int n) {
         return (uint32_t)((n >> 1) - (own ? (own0 + ((n ^ own0) & 1)) >> 1 : 0)) & 1u;
@@ -660,18 +719,20 @@ __global__ void __launch_bounds__(kRowsP) k_prefix_join(PrefixParts in, PrefixGe
     pdl_wait();
     pdl_trigger();
     if (r >= gm.nb * gm.GT || b >= gm.B) return;
-    const int all = __ldg(in.cum + gm.B), c0 = __ldg(in.cum + b), nt = __ldg(in.cum + b + 1) - c0;
-    const int up = gm.Hkv * gm.nrt * gm.np, units = up + gm.Hkv * all;
-    // the pieces of a job: one per CTA of a run of CTAs
+    const int c0 = __ldg(in.cost + b), each = __ldg(in.cost + b + 1) - c0;
+    const int jc = prefix_job_cost<DH>(gm), own_from = jc * gm.Hkv * gm.nrt;
+    const int all = own_from + __ldg(in.cost + gm.B) * gm.Hkv, runs = runs_of<DH>(all, gm.ctas);
+    // The pieces of a job: one per CTA from that of the first tile's end to that of
+    // the last one's.
     int n_pre = 0, n_own = 0, first_pre = 0, first_own = 0;
-    if (gm.np) {
-        first_pre = cta_of(pj * gm.np, units, gm.ctas);
-        n_pre = cta_of((pj + 1) * gm.np - 1, units, gm.ctas) - first_pre + 1;
+    if (jc) {
+        first_pre = cta_of(pj * jc + Px<DH>::kPrePiece + Px<DH>::kPreTile - 1, all, runs);
+        n_pre = cta_of((pj + 1) * jc - 1, all, runs) - first_pre + 1;
     }
-    if (nt) {
-        const int a = up + c0 * gm.Hkv + g * nt;
-        first_own = cta_of(a, units, gm.ctas);
-        n_own = cta_of(a + nt - 1, units, gm.ctas) - first_own + 1;
+    if (each) {
+        const int a = own_from + c0 * gm.Hkv + g * each;
+        first_own = cta_of(a + Px<DH>::kOwnPiece + Px<DH>::kOwnTile - 1, all, runs);
+        n_own = cta_of(a + each - 1, all, runs) - first_own + 1;
     }
     const int64_t pre = pj + first_pre, own = (int64_t)b * gm.Hkv + g + first_own;
     const float2* ml_pre = in.ml_prefix + pre * kRowsP + r;
@@ -747,7 +808,7 @@ PrefixGeom geom_of(int B, int H, int Hkv, int T, int P, int max_seq, int dh) {
 }
 
 struct PrefixLayout {
-    size_t o_prefix, ml_prefix, o_own, ml_own, cum, total;
+    size_t o_prefix, ml_prefix, o_own, ml_own, cost, total;
 };
 PrefixLayout layout(const PrefixGeom& g, int dh) {
     PrefixLayout l{};
@@ -762,7 +823,7 @@ PrefixLayout layout(const PrefixGeom& g, int dh) {
     l.ml_prefix = take(np * kRowsP * 8);
     l.o_own = take(no * g.GT * dh * 4);
     l.ml_own = take(no * g.GT * 8);
-    l.cum = take(((size_t)g.B + 1) * 4);
+    l.cost = take(((size_t)g.B + 1) * 4);
     l.total = off;
     return l;
 }
@@ -770,7 +831,7 @@ PrefixLayout layout(const PrefixGeom& g, int dh) {
 template <int DH>
 cudaError_t launch_dh(const PrefixArgs& a, PrefixGeom g, const CUtensorMap* maps, cudaStream_t st) {
     using L = Px<DH>;
-    const int smem = L::kBase + 4 * (2 * a.B + 1);
+    const int smem = L::kBase + 4 * (3 * a.B + 2);
     cudaError_t e = cudaFuncSetAttribute(k_prefix_part<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const PrefixLayout l = layout(g, DH);
@@ -780,7 +841,7 @@ cudaError_t launch_dh(const PrefixArgs& a, PrefixGeom g, const CUtensorMap* maps
     parts.ml_prefix = reinterpret_cast<float2*>(w + l.ml_prefix);
     parts.o_own = reinterpret_cast<float*>(w + l.o_own);
     parts.ml_own = reinterpret_cast<float2*>(w + l.ml_own);
-    parts.cum = reinterpret_cast<int*>(w + l.cum);
+    parts.cost = reinterpret_cast<int*>(w + l.cost);
     // two CTAs per SM; no more than there can be tiles
     const int64_t most = (int64_t)g.Hkv * g.nrt * g.np +
                          (int64_t)g.B * g.Hkv * ((a.max_seq + kKeys - 1) / kKeys);
@@ -802,8 +863,8 @@ size_t prefix_workspace_bytes(int B, int H, int Hkv, int T, int dh) {
 
 tfm_status launch_prefix_attention(const PrefixArgs& a, cudaStream_t st, cudaError_t* e) {
     const PrefixGeom g = geom_of(a.B, a.H, a.Hkv, a.T, a.P, a.max_seq, a.dh);
-    if ((int64_t)g.Hkv * g.nrt * g.np + (int64_t)g.B * g.Hkv * ((a.max_seq + kKeys - 1) / kKeys) > INT32_MAX)
-        return TFM_EINVAL;
+    if ((int64_t)g.Hkv * g.nrt * g.np + (int64_t)g.B * g.Hkv * ((a.max_seq + kKeys - 1) / kKeys) > (1 << 25))
+        return TFM_EINVAL;                             // costs stay below 2^31
     CUtensorMap maps[6];
     if (!query_groups_map(&maps[0], a.q, a.B, a.Hkv, g.GT, a.dh, g.nb) ||
         !query_groups_map(&maps[1], a.q, a.B, a.Hkv, g.GT, a.dh, 1) ||

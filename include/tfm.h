@@ -476,8 +476,8 @@ tfm_status tfm_packed_attention(const void* q, const void* k, const void* v, voi
  * [B, T, H*dh]; query head h reads kv head h / (H / Hkv).  What lies in the
  * caches behind lens[b] and in the prefix behind prefix_len is not looked at.
  * bf16 only, everything dense; dh in {32, 64, 128}, (H / Hkv) * T <= 128,
- * B <= 4096, B * H * T <= 2^24, Hkv * max_prefix and B * Hkv * max_seq below
- * 2^31, B * H * T * prefix_len below 2^42.
+ * B <= 4096, B * H * T <= 2^24, Hkv * max_prefix below 2^31, B * Hkv * max_seq
+ * below 2^30, B * H * T * prefix_len below 2^37.
  * prefix_len may be 0 (its pointers may then be NULL), and lens[b] may be 0.
  * scale <= 0 means 1/sqrt(dh); it must be finite.  Pointers 16-byte aligned,
  * lens 4-byte.  workspace: device, 16-byte aligned,
