@@ -8,16 +8,19 @@
 // race, argmax_v weight(v) / noise(v), which needs no normalised sum of the
 // weights and no running sum over the vocabulary.
 //
-// Two launches.  The first takes every row that can matter once through the SMs
-// and leaves, per chunk of 4096 logits, the maximum m and the sum of
-// e^((z - m) / temperature) (greedy: the largest logit and its index).  The
-// second merges them per sequence, decides which tokens are accepted, and runs
-// the race over the one row of p (and q) that it then needs, a CTA per chunk;
+// Three launches.  The first takes every row that can matter once through the SMs
+// and leaves, per chunk of 8192 logits, the maximum m and the sum of
+// e^((z - m) / temperature) (greedy: the largest logit and its index).  The second
+// merges them, a CTA per sequence, and decides which tokens are accepted.  The third
+// runs the race over the one row of p (and q) that is then needed, a CTA per chunk;
 // the last CTA of a sequence to finish merges the chunks' winners and writes the
-// answer.  Bound by reading the logits.
+// answer.  (Deciding again in every CTA of the race saved a launch but made 13 chains of
+// dependent loads of one, and 22 us of the race at 64 sequences of 50257 logits.)
+// Bound by reading the logits.
 //
 // Both decisions compare computed numbers, so a rounding may turn them.  The
-// acceptance test is done in fp64 from the merged statistics.  The race is run
+// acceptance test is done in fp32 where its two sides are further apart than
+// their errors, else in fp64 from the merged statistics.  The race is run
 // in fp32 with bounds: a weight p - q is known to kEps (p + q), every chunk
 // keeps what may still be its winner, and where more than one token may be, those
 // few are evaluated in fp64.  Ties go to the lowest token.
@@ -29,8 +32,11 @@ namespace tfm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kVec = 4;                                   // float4 loads per thread
-constexpr int kChunk = kThreads * kVec * 4;               // logits per CTA
+// float4 loads per thread and logits per CTA: of the statistics (8 loads: at 4 the
+// instructions a warp needs besides were half of all, 28 us instead of 23 for 64 x 11 rows of
+// 50257), and of the race, which holds three rows' values
+constexpr int kVec = 8, kRaceVec = 4;
+constexpr int kChunk = kThreads * kVec * 4, kRaceChunk = kThreads * kRaceVec * 4;
 constexpr int kMaxK = 64;
 // Relative error of an fp32 weight e^((z - m) / temperature): the exponent
 // x = (z - m) log2(e) / temperature carries three roundings, 3 * 2^-24 |x|, so
@@ -44,12 +50,21 @@ struct __align__(16) Cand {
     int pad;
 };
 
+// What the race of a sequence is run over: the place of the new token, whether a
+// drafted one was refused there, and both rows' statistics.
+struct __align__(16) Decision {
+    int n, refused;
+    float mt, st, md, sd;
+    int pad[2];
+};
+
 struct VerifyParams {
     VerifyArgs a;
-    int C;             // chunks per row
+    int C, RC;         // chunks per row: of the statistics, of the race
     float c2;          // log2(e) / temperature
     float2* part;      // [B*(K+1) + B*K][C]
-    Cand* cand;        // [B][C]
+    Cand* cand;        // [B][RC]
+    Decision* dec;     // [B]
     int* done;         // [B] CTAs of a sequence that have finished
     int* err;
 };
@@ -57,10 +72,11 @@ struct VerifyParams {
 __device__ __forceinline__ float no_nan(float z) { return fmaxf(z, -INFINITY); }   // NaN -> -inf
 
 // e^((z - m) / temperature) as an fp32 power of two; z = m gives 1 (also for an
-// infinite m), a NaN exponent 0.
+// infinite m), a NaN exponent 0.  (2^-200 is 0: ex2.approx.ftz has no subnormal
+// results, and a weight below 1e-38 of the largest one never decides.)
 __device__ __forceinline__ float weight(float z, float m, float c2) {
     const float x = z == m ? 0.f : (z - m) * c2;
-    return exp2f(fmaxf(x, -INFINITY));
+    return fast_exp2(fmaxf(x, -200.f));
 }
 __device__ __forceinline__ double weight64(float z, float m, double temperature) {
     if (z == m) return 1.0;
@@ -76,28 +92,42 @@ __device__ __forceinline__ int drafted(const VerifyArgs& a, int b, int* err) {
     return n;
 }
 
-// 16 logits of this thread: chunk c, [j][e] at c*kChunk + (j*kThreads + tid)*4 + e;
-// `fill` behind the row's end.  ld is a multiple of 4 and at least V, so a vector
-// that starts inside the row lies inside its storage.
-__device__ __forceinline__ void load16(const float* __restrict__ row, int c, int V, float fill,
-                                       float (&z)[16]) {
-    float4 w[kVec];
+// The 4 N logits of this thread: chunk c of kThreads * 4 N, [j][e] at
+// (j*kThreads + tid)*4 + e of it; `fill` behind the row's end.  ld is a multiple of 4
+// and at least V, so a vector that starts inside the row lies inside its storage.
+template <int N>
+__device__ __forceinline__ void load_chunk(const float* __restrict__ row, int c, int V, float fill,
+                                           float (&z)[4 * N]) {
+    const int i0 = c * (kThreads * 4 * N) + (int)threadIdx.x * 4;
+    const float4* src = reinterpret_cast<const float4*>(row + i0);
+    float4 w[N];
+    const bool whole = (c + 1) * (kThreads * 4 * N) <= V;
+    if (whole) {
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-        const int64_t i = (int64_t)c * kChunk + (j * kThreads + (int)threadIdx.x) * 4;
-        w[j] = i < V ? __ldg(reinterpret_cast<const float4*>(row + i)) : make_float4(fill, fill, fill, fill);
+        for (int j = 0; j < N; ++j) w[j] = __ldg(src + j * kThreads);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            w[j] = i0 + j * kThreads * 4 < V ? __ldg(src + j * kThreads) : make_float4(fill, fill, fill, fill);
     }
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-        const int64_t i = (int64_t)c * kChunk + (j * kThreads + (int)threadIdx.x) * 4;
+    for (int j = 0; j < N; ++j) {
         z[4 * j] = w[j].x;
-        z[4 * j + 1] = i + 1 < V ? w[j].y : fill;
-        z[4 * j + 2] = i + 2 < V ? w[j].z : fill;
-        z[4 * j + 3] = i + 3 < V ? w[j].w : fill;
+        z[4 * j + 1] = w[j].y;
+        z[4 * j + 2] = w[j].z;
+        z[4 * j + 3] = w[j].w;
+    }
+    if (!whole) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int e = 1; e < 4; ++e)
+                if (i0 + j * kThreads * 4 + e >= V) z[4 * j + e] = fill;
     }
 }
-__device__ __forceinline__ int index16(int c, int k) {
-    return c * kChunk + ((k >> 2) * kThreads + (int)threadIdx.x) * 4 + (k & 3);
+template <int N>
+__device__ __forceinline__ int index_of(int c, int k) {
+    return c * (kThreads * 4 * N) + ((k >> 2) * kThreads + (int)threadIdx.x) * 4 + (k & 3);
 }
 
 __device__ __forceinline__ float block_max(float v, float* red) {
@@ -143,25 +173,25 @@ __global__ void __launch_bounds__(kThreads) k_verify_stats(const VerifyParams p)
     const int r = is_draft ? row - nt : row;
     const int per = is_draft ? a.K : a.K + 1;
     const int b = r / per, i = r - b * per;
-    if (!is_draft && i == 0 && c == 0 && threadIdx.x == 0) p.done[b] = 0;
     const int nd = drafted(a, b, p.err);
     if (is_draft ? i >= nd : i > nd) return;          // a row nobody asks for
-    float z[16];
-    load16(is_draft ? a.dlogits + (int64_t)r * a.ld_draft : a.target + (int64_t)r * a.ld_target, c, a.V,
+    float z[4 * kVec];
+    load_chunk<kVec>(is_draft ? a.dlogits + (int64_t)r * a.ld_draft : a.target + (int64_t)r * a.ld_target, c, a.V,
            -INFINITY, z);
-    float m = -INFINITY;
+    // (a maximum with a NaN is the other operand)
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-        z[k] = no_nan(z[k]);
-        m = fmaxf(m, z[k]);
-    }
+    for (int k = 0; k < 4 * kVec; k += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmax3(mx[e], z[k + 2 * e], z[k + 2 * e + 1]);
+    float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float2* out = p.part + (int64_t)row * p.C + c;
     if (kGreedy) {
         int best = -1;
 #pragma unroll
-        for (int k = 15; k >= 0; --k)
-            if (z[k] == m && m > -INFINITY) best = index16(c, k);
+        for (int k = 4 * kVec - 1; k >= 0; --k)
+            if (z[k] == m && m > -INFINITY) best = index_of<kVec>(c, k);
         warp_best(m, best);
         if (lane == 0) {
             red[warp] = m;
@@ -177,9 +207,22 @@ __global__ void __launch_bounds__(kThreads) k_verify_stats(const VerifyParams p)
     }
     m = block_max(m, red);
     float s = 0.f;
-    if (m > -INFINITY) {
+    if (m > -INFINITY && m < INFINITY) {
+        // packed pairs: (z - m) c2, then the power; NaN and -inf end at the bound
+        const uint64_t negm = f2_pack(-m, -m), c2 = f2_pack(p.c2, p.c2);
+        uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-        for (int k = 0; k < 16; ++k) s += weight(z[k], m, p.c2);
+        for (int k = 0; k < 4 * kVec; k += 2) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_add(f2_pack(z[k], z[k + 1]), negm), c2, 0ull), x0, x1);
+            sum[(k >> 1) & 1] = f2_add(sum[(k >> 1) & 1], f2_pack(fast_exp2(fmaxf(x0, -200.f)), fast_exp2(fmaxf(x1, -200.f))));
+        }
+        float s0, s1;
+        f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
+        s = s0 + s1;
+    } else if (m == INFINITY) {                        // all the weight on the infinite ones
+#pragma unroll
+        for (int k = 0; k < 4 * kVec; ++k) s += z[k] == INFINITY ? 1.f : 0.f;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -195,30 +238,106 @@ __global__ void __launch_bounds__(kThreads) k_verify_stats(const VerifyParams p)
 
 // The maximum and the sum of a whole row from its chunks, by one warp.
 __device__ __forceinline__ void row_stats(const float2* __restrict__ part, int C, float c2, float& m,
-                                          double& s) {
+                                          float& s) {
     const int lane = threadIdx.x & 31;
     m = -INFINITY;
-    for (int c = lane; c < C; c += 32) m = fmaxf(m, part[c].x);
+    s = 0.f;
+    for (int c = lane; c < C; c += 32) {
+        const float2 v = part[c];
+        const float mn = fmaxf(m, v.x);
+        if (mn > -INFINITY) s = s * weight(m, mn, c2) + v.y * weight(v.x, mn, c2);
+        m = mn;
+    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    s = 0.0;
+    for (int o = 16; o > 0; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+        const float mn = fmaxf(m, m2);
+        if (mn > -INFINITY) s = s * weight(m, mn, c2) + s2 * weight(m2, mn, c2);
+        m = mn;
+    }
+}
+// Its sum in fp64, by one thread (the fp64 units take 32 cycles an instruction: only
+// where a decision needs it).
+__device__ __noinline__ double row_sum64(const float2* __restrict__ part, int C, float m, double temperature) {
+    double s = 0.0;
     if (m > -INFINITY)
-        for (int c = lane; c < C; c += 32) s += (double)part[c].y * (double)weight(part[c].x, m, c2);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        for (int c = 0; c < C; ++c) s += (double)part[c].y * weight64(part[c].x, m, temperature);
+    return s;
+}
+// p(z) or q(z) in fp64; 0 in a row without any weight.
+__device__ __noinline__ double prob64(float z, float m, double sum, double temperature) {
+    return sum > 0.0 ? weight64(z, m, temperature) / sum : 0.0;
 }
 
-// tokens[b] and n_accepted[b]; called by one thread.
+// tokens[b] and n_accepted[b]; called by one warp.
 __device__ __forceinline__ void write_answer(const VerifyArgs& a, int b, int n, int token) {
-    for (int i = 0; i <= a.K; ++i)
+    const int lane = threadIdx.x & 31;
+    for (int i = lane; i <= a.K; i += 32)
         a.tokens[(int64_t)b * (a.K + 1) + i] = i < n ? a.draft[(int64_t)b * a.K + i] : i == n ? token : -1;
-    a.n_accepted[b] = n;
+    if (lane == 0) a.n_accepted[b] = n;
 }
 
-__global__ void __launch_bounds__(kThreads) k_verify_race(const VerifyParams p) {
-    __shared__ float m_t[kMaxK + 1], m_d[kMaxK];
-    __shared__ double s_t[kMaxK + 1], s_d[kMaxK];
+// Which drafted tokens of a sequence are accepted: a CTA per sequence, a warp per
+// place; what does not depend on one another is asked for together.
+__global__ void __launch_bounds__(kThreads) k_verify_decide(const VerifyParams p) {
+    __shared__ float2 row_t[kMaxK + 1], row_d[kMaxK];     // maximum, sum
     __shared__ int take[kMaxK];
+    pdl_wait();
+    pdl_trigger();
+    const VerifyArgs& a = p.a;
+    const int b = (int)blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nd = drafted(a, b, nullptr);
+    const double temp = (double)a.temperature;
+    for (int i = warp; i <= nd; i += kThreads / 32) {
+        const bool drafted_here = i < nd;
+        const int x = drafted_here ? a.draft[(int64_t)b * a.K + i] : 0;
+        const float u = drafted_here ? a.u[(int64_t)b * a.K + i] : 0.f;
+        const float2* part_t = p.part + ((int64_t)b * (a.K + 1) + i) * p.C;
+        const float2* part_d = p.part + ((int64_t)a.B * (a.K + 1) + (int64_t)b * a.K + i) * p.C;
+        bool ok = drafted_here && x >= 0 && x < a.V;
+        if (drafted_here && !ok && lane == 0) raise_error(p.err, TFM_EBADTOKEN);
+        float zt = 0.f, zd = 0.f;
+        if (ok) {
+            zt = no_nan(a.target[((int64_t)b * (a.K + 1) + i) * a.ld_target + x]);
+            zd = no_nan(a.dlogits[((int64_t)b * a.K + i) * a.ld_draft + x]);
+        }
+        float mt, md = 0.f, st, sd = 0.f;
+        row_stats(part_t, p.C, p.c2, mt, st);
+        if (drafted_here) row_stats(part_d, p.C, p.c2, md, sd);
+        if (lane == 0) {
+            row_t[i] = make_float2(mt, st);
+            if (drafted_here) {
+                row_d[i] = make_float2(md, sd);
+                if (ok) {
+                    const float px = st > 0.f ? weight(zt, mt, p.c2) / st : 0.f;
+                    const float uq = u * (sd > 0.f ? weight(zd, md, p.c2) / sd : 0.f);
+                    // fp32 decides where the two sides are further apart than their errors
+                    // (and not lost below its normal numbers)
+                    if (px > 1e-30f && uq * (1.f + 2.f * kEps) < px * (1.f - 2.f * kEps)) {
+                        ok = true;
+                    } else if (uq > 1e-30f && uq * (1.f - 2.f * kEps) > px * (1.f + 2.f * kEps)) {
+                        ok = false;
+                    } else {
+                        const double p64 = prob64(zt, mt, row_sum64(part_t, p.C, mt, temp), temp);
+                        const double q64 = prob64(zd, md, row_sum64(part_d, p.C, md, temp), temp);
+                        ok = (double)u * q64 < p64;
+                    }
+                }
+                take[i] = ok;
+            }
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int n = 0;
+        while (n < nd && take[n]) ++n;
+        const bool refused = n < nd;
+        p.dec[b] = Decision{n, refused, row_t[n].x, row_t[n].y, refused ? row_d[n].x : 0.f, refused ? row_d[n].y : 0.f, {0, 0}};
+        p.done[b] = 0;
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 4) k_verify_race(const VerifyParams p) {
     __shared__ float red[kThreads / 32];
     __shared__ double redv[kThreads / 32];
     __shared__ int redi[kThreads / 32];
@@ -226,103 +345,69 @@ __global__ void __launch_bounds__(kThreads) k_verify_race(const VerifyParams p) 
     pdl_wait();
     pdl_trigger();
     const VerifyArgs& a = p.a;
-    const int c = (int)(blockIdx.x % (unsigned)p.C), b = (int)(blockIdx.x / (unsigned)p.C);
+    const int c = (int)(blockIdx.x % (unsigned)p.RC), b = (int)(blockIdx.x / (unsigned)p.RC);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nd = drafted(a, b, nullptr);
     const double temp = (double)a.temperature;
-    // Statistics and acceptance of every place, a warp each.
-    for (int i = warp; i <= nd; i += kThreads / 32) {
-        float mt, md = 0.f;
-        double st, sd = 0.0;
-        row_stats(p.part + ((int64_t)b * (a.K + 1) + i) * p.C, p.C, p.c2, mt, st);
-        if (i < nd) row_stats(p.part + ((int64_t)a.B * (a.K + 1) + (int64_t)b * a.K + i) * p.C, p.C, p.c2, md, sd);
-        if (lane == 0) {
-            m_t[i] = mt;
-            s_t[i] = st;
-            if (i < nd) {
-                m_d[i] = md;
-                s_d[i] = sd;
-                const int x = a.draft[(int64_t)b * a.K + i];
-                bool ok = x >= 0 && x < a.V;
-                if (!ok && c == 0) raise_error(p.err, TFM_EBADTOKEN);
-                if (ok) {
-                    const float zt = no_nan(a.target[((int64_t)b * (a.K + 1) + i) * a.ld_target + x]);
-                    const float zd = no_nan(a.dlogits[((int64_t)b * a.K + i) * a.ld_draft + x]);
-                    const double px = st > 0.0 ? weight64(zt, mt, temp) / st : 0.0;
-                    const double qx = sd > 0.0 ? weight64(zd, md, temp) / sd : 0.0;
-                    ok = (double)a.u[(int64_t)b * a.K + i] * qx < px;
-                }
-                take[i] = ok;
-            }
-        }
-    }
-    __syncthreads();
-    int n = 0;
-    while (n < nd && take[n]) ++n;
-    const bool refused = n < nd;
-    const float mt = m_t[n], md = refused ? m_d[n] : 0.f;
-    const double st = s_t[n], sd = refused ? s_d[n] : 0.0;
-    const float inv_t = st > 0.0 ? (float)(1.0 / st) : 0.f, inv_d = sd > 0.0 ? (float)(1.0 / sd) : 0.f;
+    const float* erow = a.noise + (int64_t)b * a.ld_noise;
+    float e[4 * kRaceVec];
+    load_chunk<kRaceVec>(erow, c, a.V, 0.f, e);        // needed whatever the row is
+    const Decision d = p.dec[b];
+    const int n = d.n;
+    const bool refused = d.refused;
+    const float mt = d.mt, st = d.st, md = d.md, sd = d.sd;
+    const float inv_t = st > 0.f ? 1.f / st : 0.f, inv_d = sd > 0.f ? 1.f / sd : 0.f;
     const float* zrow = a.target + ((int64_t)b * (a.K + 1) + n) * a.ld_target;
     const float* yrow = refused ? a.dlogits + ((int64_t)b * a.K + n) * a.ld_draft : nullptr;
-    const float* erow = a.noise + (int64_t)b * a.ld_noise;
     // weight / noise of token v in fp64; with_q false: of p alone
-    auto score64 = [&](int v, bool with_q) -> double {
-        const float e = erow[v];
-        if (!(e > 0.f) || !(st > 0.0)) return 0.0;
-        double w = weight64(no_nan(zrow[v]), mt, temp) / st;
-        if (with_q && yrow && sd > 0.0) w -= weight64(no_nan(yrow[v]), md, temp) / sd;
-        return w / (double)e;
+    auto score64 = [&](int v, bool with_q, double st64, double sd64) -> double {
+        const float ev = erow[v];
+        if (!(ev > 0.f)) return 0.0;
+        double w = prob64(no_nan(zrow[v]), mt, st64, temp);
+        if (with_q && yrow) w -= prob64(no_nan(yrow[v]), md, sd64, temp);
+        return w / (double)ev;
     };
-    float hi[16];
+    auto sum_t64 = [&]() { return row_sum64(p.part + ((int64_t)b * (a.K + 1) + n) * p.C, p.C, mt, temp); };
+    auto sum_d64 = [&]() {
+        return refused ? row_sum64(p.part + ((int64_t)a.B * (a.K + 1) + (int64_t)b * a.K + n) * p.C, p.C, md, temp) : 0.0;
+    };
+    float hi[4 * kRaceVec];
     float lo = -INFINITY;
     {
-        float z[16], y[16], e[16];
-        load16(zrow, c, a.V, -INFINITY, z);
-        load16(erow, c, a.V, 0.f, e);
-        if (refused) load16(yrow, c, a.V, -INFINITY, y);
+        float z[4 * kRaceVec], y[4 * kRaceVec];
+        load_chunk<kRaceVec>(zrow, c, a.V, -INFINITY, z);
+        if (refused) load_chunk<kRaceVec>(yrow, c, a.V, -INFINITY, y);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const float pw = st > 0.0 ? weight(no_nan(z[k]), mt, p.c2) * inv_t : 0.f;
-            const float qw = refused && sd > 0.0 ? weight(no_nan(y[k]), md, p.c2) * inv_d : 0.f;
+        for (int k = 0; k < 4 * kRaceVec; ++k) {
+            const float pw = st > 0.f ? weight(no_nan(z[k]), mt, p.c2) * inv_t : 0.f;
+            const float qw = refused && sd > 0.f ? weight(no_nan(y[k]), md, p.c2) * inv_d : 0.f;
             const bool in = pw > 0.f && e[k] > 0.f;
-            const float r = pw - qw, er = kEps * (pw + qw);
-            hi[k] = in ? (r + er) / e[k] : -INFINITY;
-            lo = fmaxf(lo, in ? (r - er) / e[k] : -INFINITY);
+            const float r = pw - qw, er = kEps * (pw + qw), inv_e = __fdividef(1.f, e[k]);
+            hi[k] = in ? (r + er) * inv_e : -INFINITY;
+            lo = fmaxf(lo, in ? (r - er) * inv_e : -INFINITY);
         }
     }
     lo = block_max(lo, red);
-    int mine = 0;
+    uint32_t mine = 0;                                 // this thread's possible winners, as bits
+    float top = 0.f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) mine += hi[k] > 0.f && hi[k] >= lo;
-    // how many may be the chunk's winner: 0, 1, or more
-    const int any = __syncthreads_count(mine > 0), several = __syncthreads_or(mine > 1);
-    Cand* out = p.cand + (int64_t)b * p.C + c;
-    if (any == 1 && !several && lo > 0.f) {
-        if (mine) {
-            int best = -1;
-            float h = 0.f;
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-                if (hi[k] > 0.f && hi[k] >= lo) {
-                    best = index16(c, k);
-                    h = hi[k];
-                }
-            *out = Cand{lo, h, best, 0};
+    for (int k = 0; k < 4 * kRaceVec; ++k)
+        if (hi[k] > 0.f && hi[k] >= lo) {
+            mine |= 1u << k;
+            top = fmaxf(top, hi[k]);
         }
+    // how many may be the chunk's winner: 0, 1, or more
+    const int any = __syncthreads_count(mine != 0), several = __syncthreads_or(mine & (mine - 1));
+    Cand* out = p.cand + (int64_t)b * p.RC + c;
+    if (any == 1 && !several && lo > 0.f) {
+        if (mine) *out = Cand{lo, top, index_of<kRaceVec>(c, __ffs(mine) - 1), 0};
     } else {
         double v = 0.0;
         int best = -1;
         if (mine) {
-#pragma unroll 1
-            for (int k = 0; k < 16; ++k) {
-                float h = hi[0];
-#pragma unroll
-                for (int kk = 1; kk < 16; ++kk)
-                    if (kk == k) h = hi[kk];
-                if (!(h > 0.f && h >= lo)) continue;
-                const int idx = index16(c, k);
-                const double s = score64(idx, true);
+            const double st64 = sum_t64(), sd64 = sum_d64();
+            for (; mine; mine &= mine - 1) {
+                const int idx = index_of<kRaceVec>(c, __ffs(mine) - 1);
+                const double s = score64(idx, true, st64, sd64);
                 if (s > 0.0) take_better(v, best, s, idx);
             }
         }
@@ -342,27 +427,27 @@ __global__ void __launch_bounds__(kThreads) k_verify_race(const VerifyParams p) 
     // The last CTA of the sequence merges the chunks.
     __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) last = atomicAdd(p.done + b, 1) == p.C - 1;
+    if (threadIdx.x == 0) last = atomicAdd(p.done + b, 1) == p.RC - 1;
     __syncthreads();
     if (!last) return;
     __threadfence();
     double v = 0.0;
     int token = -1;
     if (warp == 0) {
-        const int4* cd = reinterpret_cast<const int4*>(p.cand + (int64_t)b * p.C);
+        const int4* cd = reinterpret_cast<const int4*>(p.cand + (int64_t)b * p.RC);
         auto cand = [&](int k) {                       // from L2: other CTAs wrote them
             const int4 w = __ldcg(cd + k);
             return Cand{__int_as_float(w.x), __int_as_float(w.y), w.z, 0};
         };
         float lb = -INFINITY;
-        for (int k = lane; k < p.C; k += 32) {
+        for (int k = lane; k < p.RC; k += 32) {
             const Cand x = cand(k);
             if (x.idx >= 0) lb = fmaxf(lb, x.lo);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) lb = fmaxf(lb, __shfl_xor_sync(0xffffffffu, lb, o));
         int cnt = 0, only = -1;
-        for (int k = lane; k < p.C; k += 32) {
+        for (int k = lane; k < p.RC; k += 32) {
             const Cand x = cand(k);
             if (x.idx >= 0 && x.hi >= lb) {
                 ++cnt;
@@ -373,9 +458,10 @@ __global__ void __launch_bounds__(kThreads) k_verify_race(const VerifyParams p) 
         if (total == 1) {
             token = __reduce_max_sync(0xffffffffu, only);
         } else if (total > 1) {
-            for (int k = lane; k < p.C; k += 32) {
+            const double st64 = sum_t64(), sd64 = sum_d64();
+            for (int k = lane; k < p.RC; k += 32) {
                 const Cand x = cand(k);
-                if (x.idx >= 0 && x.hi >= lb) take_better(v, token, score64(x.idx, true), x.idx);
+                if (x.idx >= 0 && x.hi >= lb) take_better(v, token, score64(x.idx, true, st64, sd64), x.idx);
             }
             warp_best(v, token);
         }
@@ -387,8 +473,9 @@ __global__ void __launch_bounds__(kThreads) k_verify_race(const VerifyParams p) 
     if (token < 0 && refused) {
         // max(p - q, 0) is zero everywhere: the race over p, in fp64
         v = 0.0;
+        const double st64 = sum_t64();
         for (int x = threadIdx.x; x < a.V; x += kThreads) {
-            const double s = score64(x, false);
+            const double s = score64(x, false, st64, 0.0);
             if (s > 0.0) take_better(v, token, s, x);
         }
         warp_best(v, token);
@@ -397,10 +484,10 @@ __global__ void __launch_bounds__(kThreads) k_verify_race(const VerifyParams p) 
             redi[warp] = token;
         }
         __syncthreads();
-        if (threadIdx.x == 0)
-            for (int w = 1; w < kThreads / 32; ++w) take_better(v, token, redv[w], redi[w]);
+        if (warp == 0)
+            for (int w = 0; w < kThreads / 32; ++w) take_better(v, token, redv[w], redi[w]);
     }
-    if (threadIdx.x == 0) write_answer(a, b, n, token);
+    if (warp == 0) write_answer(a, b, n, token);
 }
 
 // Greedy: one warp per sequence.
@@ -424,7 +511,7 @@ __global__ void __launch_bounds__(kThreads) k_verify_greedy(const VerifyParams p
         if (x != best || best < 0) break;
         ++n;
     }
-    if (lane == 0) write_answer(a, b, n, best);
+    write_answer(a, b, n, best);
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -432,30 +519,34 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 }  // namespace
 
 size_t verify_workspace_bytes(int B, int K, int V) {
-    const size_t C = ((size_t)V + kChunk - 1) / kChunk;
-    return align256((size_t)B * (2 * K + 1) * C * sizeof(float2)) + align256((size_t)B * C * sizeof(Cand)) +
-           align256((size_t)B * 4);
+    const size_t C = ((size_t)V + kChunk - 1) / kChunk, RC = ((size_t)V + kRaceChunk - 1) / kRaceChunk;
+    return align256((size_t)B * (2 * K + 1) * C * sizeof(float2)) + align256((size_t)B * RC * sizeof(Cand)) +
+           align256((size_t)B * sizeof(Decision)) + align256((size_t)B * 4);
 }
 
 cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t st) {
     VerifyParams p{};
     p.a = a;
     p.C = (a.V + kChunk - 1) / kChunk;
+    p.RC = (a.V + kRaceChunk - 1) / kRaceChunk;
     const bool greedy = a.temperature == 0.f;
     p.c2 = greedy ? 0.f : 1.4426950408889634f / a.temperature;
     uint8_t* w = static_cast<uint8_t*>(a.ws);
     p.part = reinterpret_cast<float2*>(w);
     w += align256((size_t)a.B * (2 * a.K + 1) * p.C * sizeof(float2));
     p.cand = reinterpret_cast<Cand*>(w);
-    w += align256((size_t)a.B * p.C * sizeof(Cand));
+    w += align256((size_t)a.B * p.RC * sizeof(Cand));
+    p.dec = reinterpret_cast<Decision*>(w);
+    w += align256((size_t)a.B * sizeof(Decision));
     p.done = reinterpret_cast<int*>(w);
     p.err = device_error_word();
     const unsigned rows = (unsigned)(a.B * (greedy ? a.K + 1 : 2 * a.K + 1));
     cudaError_t e = greedy ? launch_pdl(k_verify_stats<true>, dim3(rows * p.C), dim3(kThreads), 0, st, p)
                            : launch_pdl(k_verify_stats<false>, dim3(rows * p.C), dim3(kThreads), 0, st, p);
     if (e != cudaSuccess) return e;
-    return greedy ? launch_pdl(k_verify_greedy, dim3((a.B + 7) / 8), dim3(kThreads), 0, st, p)
-                  : launch_pdl(k_verify_race, dim3((unsigned)(a.B * p.C)), dim3(kThreads), 0, st, p);
+    if (greedy) return launch_pdl(k_verify_greedy, dim3((a.B + 7) / 8), dim3(kThreads), 0, st, p);
+    e = launch_pdl(k_verify_decide, dim3((unsigned)a.B), dim3(kThreads), 0, st, p);
+    return e != cudaSuccess ? e : launch_pdl(k_verify_race, dim3((unsigned)(a.B * p.RC)), dim3(kThreads), 0, st, p);
 }
 
 }  // namespace tfm
