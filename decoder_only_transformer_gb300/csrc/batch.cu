@@ -43,7 +43,7 @@ tfm_status tfm_packed_attention(const void* q, const void* k, const void* v, voi
     if (T < 0 || T > (1 << 30) || n_seq < 0 || n_seq > (1 << 20))
         return fail(TFM_EINVAL, "T=%d outside [0, 2^30] or n_seq=%d outside [0, 2^20]", T, n_seq);
     if (H < 1 || Hkv < 1 || H % Hkv) return fail(TFM_EINVAL, "bad head counts");
-    if (((int64_t)T / 128 + n_seq) * H >= (int64_t)1 << 31) return fail(TFM_EINVAL, "(T / 128 + n_seq) * H too large");
+    if (((int64_t)T / 32 + n_seq) * H >= (int64_t)1 << 31) return fail(TFM_EINVAL, "(T / 32 + n_seq) * H too large");
     if (mode != TFM_FP32 && mode != TFM_BF16) return fail(TFM_EINVAL, "bad mode");
     if (window < 0) return fail(TFM_EINVAL, "window must be >= 0");
     if (!std::isfinite(scale)) return fail(TFM_EINVAL, "scale must be finite");

@@ -27,76 +27,254 @@ struct PackedStrides {
     int64_t qt, qh, kt, kh, vt, vh, ot, oh;
 };
 
-// One warp per (row, head): lane l holds coordinates l, l + 32, ...; the visible
-// keys in order with a running maximum and sum.
-__global__ void __launch_bounds__(256) k_packed_rows(const float* __restrict__ q, const float* __restrict__ k,
-                                                     const float* __restrict__ v, float* __restrict__ o,
-                                                     const int32_t* __restrict__ cu, int n_seq, int T,
-                                                     int H, int Hkv, int dh, PackedStrides sd,
-                                                     float scale, int window, int* err) {
+// Block t of sequence b has the slot cu[b] / rows + b + t, so that blocks are found
+// without a scan: slots of different sequences never meet (a sequence of L rows from
+// row c on has at most (c + L) / rows - c / rows + 1 blocks), and the sequence of a
+// slot is the last b with cu[b] / rows + b <= slot, which grows with b.  By a warp,
+// 32 probes at a time; -1: none.
+template <int kRows>
+__device__ __forceinline__ int sequence_of(const int32_t* __restrict__ cu, int n_seq, int slot) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = n_seq;                             // the answer + 1 lies in [lo, lo + n]
+    while (n > 0) {
+        const int step = (n + 31) / 32, b = lo + lane * step;
+        const bool in = lane * step < n && __ldg(cu + b) / kRows + b <= slot;
+        const int k = __popc(__ballot_sync(0xffffffffu, in));
+        if (k == 0) break;
+        const int from = (k - 1) * step;               // probe k - 1 holds, probe k does not
+        lo += from + 1;
+        n = min(n - from, step) - 1;
+    }
+    return lo - 1;
+}
+
+// ------------------------------------------------------------------ fp32
+// CUDA cores: tf32 keeps 10 mantissa bits and fp32 mode is there for fp32 results.
+// A CTA takes 32 query rows of a head against key tiles of 64, 128 threads with 4 x 4
+// scores and 4 rows x 4 or more columns of the output each (below d_head 64 the
+// threads that this leaves share the keys out and add up at the end: with one or two
+// columns each the loads of P and V bound it), K and V tiles copied asynchronously one ahead.
+// Per 16-byte step of the products a warp reads 12 shared-memory wavefronts for
+// 2048 FMAs (16 cycles), so the FMA pipe is what bounds a long sequence; short ones
+// are bound by the chain load, scores, softmax, output of a tile or two.  (One warp
+// per row took 291 us for 64 lines of up to 300 tokens at 4 x 16, this 24; blocks of 64
+// rows 30, as more of them lies above the diagonal and the last ones end later.)
+constexpr int kF32Rows = 32, kF32Keys = 64, kF32Threads = 128;
+
+__device__ __forceinline__ void cp_async16(float* dst, const float* src, bool in) {
+    const int bytes = in ? 16 : 0;                     // 0: zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes)
+                 : "memory");
+}
+
+template <int DP>
+struct F32Smem {
+    static constexpr int kPitch = DP + 4;              // floats; rows four banks apart
+    static constexpr int kQ = 0, kK = kF32Rows * kPitch, kV = kK + 2 * kF32Keys * kPitch;
+    static constexpr int kP = kV + 2 * kF32Keys * kPitch;             // [key][row]
+    static constexpr int kBytes = (kP + kF32Keys * (kF32Rows + 4)) * 4;
+};
+
+template <int DP>
+__global__ void __launch_bounds__(kF32Threads, DP <= 32 ? 5 : DP == 64 ? 4 : 1) k_packed_f32(const float* __restrict__ q, const float* __restrict__ k,
+                                                    const float* __restrict__ v, float* __restrict__ o,
+                                                    const int32_t* __restrict__ cu, int n_seq, int T, int slots,
+                                                    int H, int group, int dh, PackedStrides sd,
+                                                    float scale_log2, int window, int* err) {
+    using Sm = F32Smem<DP>;
+    constexpr int NC = DP < 64 ? 4 : DP / 16;          // output columns per thread
+    constexpr int KG = DP < 64 ? 64 / DP : 1;          // threads that share a column group's keys
+    extern __shared__ __align__(16) float sm[];
     pdl_wait();
     pdl_trigger();
     if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < n_seq; b += blockDim.x) {
+        for (int b = threadIdx.x; b < n_seq; b += kF32Threads) {
             const int s = cu[b], e = cu[b + 1];
             if (s < 0 || s > e || e > T) raise_error(err, TFM_EINVAL);
         }
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    if (w >= (int64_t)T * H) return;
-    const int i = (int)(w / H), h = (int)(w - (int64_t)i * H), g = h / (H / Hkv);
-    // the last sequence that starts at or before row i
-    int lo = 0, hi = n_seq;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (cu[mid] <= i) lo = mid + 1; else hi = mid;
+    // the last blocks of a sequence, which see the most keys, first
+    const int slot = slots - 1 - (int)(blockIdx.x / (unsigned)H), h = (int)(blockIdx.x % (unsigned)H), g = h / group;
+    const int b = sequence_of<kF32Rows>(cu, n_seq, slot);
+    if (b < 0) return;
+    const SeqRange sr = seq_range(cu, b, T);
+    const int row0 = (slot - (sr.start / kF32Rows + b)) * kF32Rows;
+    if (row0 < 0 || row0 >= sr.len) return;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int cg = tx % (16 / KG), kg = tx / (16 / KG);
+    const int d4 = dh / 4;
+    const float* kb = k + sr.start * sd.kt + g * sd.kh;
+    const float* vb = v + sr.start * sd.vt + g * sd.vh;
+    const int j0 = (window > 0 && row0 - window + 1 > 0) ? (row0 - window + 1) / kF32Keys : 0;
+    const int j1 = (row0 + kF32Rows - 1) / kF32Keys;                 // key tiles j0..j1
+    auto load_kv = [&](int j) {
+        float* ks = sm + Sm::kK + (j & 1) * kF32Keys * Sm::kPitch;
+        float* vs = sm + Sm::kV + (j & 1) * kF32Keys * Sm::kPitch;
+        for (int i = tid; i < kF32Keys * d4; i += kF32Threads) {
+            const int r = i / d4, c = (i - r * d4) * 4, key = j * kF32Keys + r;
+            const bool in = key < sr.len;
+            const int64_t at = in ? key : 0;
+            cp_async16(ks + r * Sm::kPitch + c, kb + at * sd.kt + c, in);
+            cp_async16(vs + r * Sm::kPitch + c, vb + at * sd.vt + c, in);
+        }
+    };
+    const float* qb = q + (int64_t)(sr.start + row0) * sd.qt + h * sd.qh;
+    for (int i = tid; i < kF32Rows * d4; i += kF32Threads) {
+        const int r = i / d4, c = (i - r * d4) * 4;
+        const bool in = row0 + r < sr.len;
+        cp_async16(sm + Sm::kQ + r * Sm::kPitch + c, qb + (in ? r : 0) * sd.qt + c, in);
     }
-    if (lo == 0) return;
-    const SeqRange r = seq_range(cu, lo - 1, T);
-    if (i < r.start || i >= r.start + r.len) return;
-    const float* qr = q + i * sd.qt + h * sd.qh;
-    float qv[4], acc[4];
+    load_kv(j0);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    float m[4], l[4];
+    uint64_t acc[4][NC / 2];                           // column pairs
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const int d = lane + 32 * t;
-        qv[t] = d < dh ? (qr[d]) : 0.f;
-        acc[t] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC / 2; ++c) acc[i][c] = 0ull;
     }
-    float mx = -INFINITY, sum = 0.f;
-    const int j0 = (window > 0 && i - window + 1 > r.start) ? i - window + 1 : r.start;
-    for (int j = j0; j <= i; ++j) {
-        const float* kr = k + j * sd.kt + g * sd.kh;
-        const float* vr = v + j * sd.vt + g * sd.vh;
-        float part = 0.f;
+    float* ps = sm + Sm::kP;                           // [key][row]
+    for (int j = j0; j <= j1; ++j) {
+        if (j < j1) load_kv(j + 1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();
+        const float* qs = sm + Sm::kQ + ty * 4 * Sm::kPitch;
+        const float* ks = sm + Sm::kK + (j & 1) * kF32Keys * Sm::kPitch + tx * Sm::kPitch;
+        const float* vs = sm + Sm::kV + (j & 1) * kF32Keys * Sm::kPitch + cg * 4;
+        // Packed pairs: even and odd coordinates of a score side by side, added at the end.
+        uint64_t s2[4][4];                             // rows 4 ty + i, keys tx + 16 e
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-            if (lane + 32 * t < dh) part = fmaf(qv[t], (kr[lane + 32 * t]), part);
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
-        const float s = part * scale;
-        const float mnew = fmaxf(mx, s);
-        const float corr = expf(mx - mnew), p = expf(s - mnew);
-        sum = sum * corr + p;
+            for (int e = 0; e < 4; ++e) s2[i][e] = 0ull;
+#pragma unroll 2
+        for (int c = 0; c < d4; ++c) {
+            ulonglong2 qa[4], ka[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-            if (lane + 32 * t < dh) acc[t] = acc[t] * corr + p * (vr[lane + 32 * t]);
-        mx = mnew;
+            for (int i = 0; i < 4; ++i) qa[i] = *reinterpret_cast<const ulonglong2*>(qs + i * Sm::kPitch + 4 * c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ka[e] = *reinterpret_cast<const ulonglong2*>(ks + 16 * e * Sm::kPitch + 4 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s2[i][e] = f2_fma(qa[i].y, ka[e].y, f2_fma(qa[i].x, ka[e].x, s2[i][e]));
+        }
+        float s[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float even, odd;
+                f2_unpack(s2[i][e], even, odd);
+                s[i][e] = even + odd;
+            }
+        // keys of this tile that row i sees: [lo, hi]
+        const int k0 = j * kF32Keys;
+        const bool masked = k0 + kF32Keys - 1 > row0 || (window > 0 && k0 < row0 + kF32Rows - window);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int qi = row0 + ty * 4 + i, hi = qi - k0, lo = window > 0 ? hi - window + 1 : 0;
+            float mx = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = tx + 16 * e;
+                s[i][e] = masked && (key > hi || key < lo) ? -INFINITY : s[i][e] * scale_log2;
+                mx = fmaxf(mx, s[i][e]);
+            }
+#pragma unroll
+            for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+            const float mn = fmaxf(m[i], mx), ref = mn == -INFINITY ? 0.f : mn;
+            const float corr = exp2f(m[i] - ref);      // m = -inf: 0
+            m[i] = mn;
+            l[i] *= corr;
+            const uint64_t corr2 = f2_pack(corr, corr);
+#pragma unroll
+            for (int c = 0; c < NC / 2; ++c) acc[i][c] = f2_fma(acc[i][c], corr2, 0ull);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[i][e] = exp2f(s[i][e] - ref);
+                l[i] += s[i][e];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<float4*>(ps + (tx + 16 * e) * (kF32Rows + 4) + ty * 4) =
+                make_float4(s[0][e], s[1][e], s[2][e], s[3][e]);
+        __syncthreads();
+        auto add = [&](int key, bool check) {
+            const float4 p4 = *reinterpret_cast<const float4*>(ps + key * (kF32Rows + 4) + ty * 4);
+            const float p[4] = {p4.x, p4.y, p4.z, p4.w};
+            uint64_t x[NC / 2];
+#pragma unroll
+            for (int c = 0; c < NC; c += 4) {
+                const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(vs + key * Sm::kPitch + 16 * c);
+                x[c / 2] = w.x;
+                x[c / 2 + 1] = w.y;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // a weight of zero does not make a product zero if the value is not finite
+                const int hi = row0 + ty * 4 + i - k0;
+                if (check && (key > hi || (window > 0 && key < hi - window + 1))) continue;
+                const uint64_t p2 = f2_pack(p[i], p[i]);
+#pragma unroll
+                for (int c = 0; c < NC / 2; ++c) acc[i][c] = f2_fma(p2, x[c], acc[i][c]);
+            }
+        };
+        if (masked) {
+#pragma unroll 2
+            for (int key = kg; key < kF32Keys; key += KG) add(key, true);
+        } else {
+#pragma unroll 4
+            for (int key = kg; key < kF32Keys; key += KG) add(key, false);
+        }
+        __syncthreads();                               // this tile's buffers are free
     }
-    const float inv = 1.0f / sum;
-    float* orow = o + i * sd.ot + h * sd.oh;
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-        if (lane + 32 * t < dh) orow[lane + 32 * t] = acc[t] * inv;
+    for (int i = 0; i < 4; ++i) {
+        float sum = l[i];
+#pragma unroll
+        for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+        float out[NC];
+#pragma unroll
+        for (int c = 0; c < NC / 2; ++c) f2_unpack(acc[i][c], out[2 * c], out[2 * c + 1]);
+#pragma unroll
+        for (int w = 8; w > 16 / KG / 2; w >>= 1)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) out[c] += __shfl_xor_sync(0xffffffffu, out[c], w);
+        const int qi = row0 + ty * 4 + i;
+        if (qi >= sr.len || kg) continue;
+        const float inv = 1.0f / sum;
+        float* orow = o + (int64_t)(sr.start + qi) * sd.ot + h * sd.oh + cg * 4;
+#pragma unroll
+        for (int c = 0; c < NC; c += 4)
+            if (cg * 4 + 16 * c < dh)
+                *reinterpret_cast<float4*>(orow + 16 * c) =
+                    make_float4(out[c] * inv, out[c + 1] * inv, out[c + 2] * inv, out[c + 3] * inv);
+    }
 }
 
-cudaError_t launch_rows(const PackedArgs& a, cudaStream_t st) {
-    const int64_t blocks = ((int64_t)a.T * a.H + 7) / 8;
+template <int DP>
+cudaError_t launch_f32_dp(const PackedArgs& a, int slots, const PackedStrides& sd, cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(k_packed_f32<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               F32Smem<DP>::kBytes);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(k_packed_f32<DP>, dim3((unsigned)slots * a.H), dim3(kF32Threads), F32Smem<DP>::kBytes, st,
+                      static_cast<const float*>(a.q), static_cast<const float*>(a.k),
+                      static_cast<const float*>(a.v), static_cast<float*>(a.o), a.cu, a.n_seq, a.T, slots, a.H,
+                      a.H / a.Hkv, a.dh, sd, a.scale * 1.4426950408889634f, a.window, device_error_word());
+}
+
+cudaError_t launch_f32(const PackedArgs& a, cudaStream_t st) {
+    const int slots = a.T / kF32Rows + a.n_seq;
     const PackedStrides sd{a.strides[0], a.strides[1], a.strides[2], a.strides[3],
                            a.strides[4], a.strides[5], a.strides[6], a.strides[7]};
-    return launch_pdl(k_packed_rows, dim3((unsigned)blocks), dim3(256), 0, st,
-                      static_cast<const float*>(a.q), static_cast<const float*>(a.k),
-                      static_cast<const float*>(a.v), static_cast<float*>(a.o), a.cu, a.n_seq, a.T, a.H,
-                      a.Hkv, a.dh, sd, a.scale, a.window, device_error_word());
+    return a.dh <= 16   ? launch_f32_dp<16>(a, slots, sd, st)
+           : a.dh <= 32 ? launch_f32_dp<32>(a, slots, sd, st)
+           : a.dh <= 64 ? launch_f32_dp<64>(a, slots, sd, st)
+                        : launch_f32_dp<128>(a, slots, sd, st);
 }
 
 // ------------------------------------------------------------------ work list
@@ -792,7 +970,7 @@ size_t packed_workspace_bytes(int T, int n_seq) { return 256 + sizeof(Block) * (
 
 tfm_status launch_packed_attention(const PackedArgs& a, cudaStream_t st, cudaError_t* e) {
     if (!a.bf16) {
-        *e = launch_rows(a, st);
+        *e = launch_f32(a, st);
         return TFM_OK;
     }
     CUtensorMap maps[3];

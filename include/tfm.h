@@ -450,7 +450,7 @@ tfm_status tfm_decode_attention(const void* q, const void* k_cache, const void* 
  * Strides are at least dh (a dimension of one row or head excepted), multiples
  * of 16 bytes and below 2^39 bytes; o's rows must not overlap.  bf16 mode: dh in {32, 64, 128};
  * fp32 mode: dh % 4 == 0, dh <= 128.  T <= 2^30, n_seq <= 2^20,
- * (T / 128 + n_seq) * H < 2^31.  scale <= 0 means 1/sqrt(dh); it must be finite.
+ * (T / 32 + n_seq) * H < 2^31.  scale <= 0 means 1/sqrt(dh); it must be finite.
  * Pointers 16-byte aligned, cu_seqlens 4-byte.  workspace: device, 16-byte
  * aligned, tfm_packed_attention_workspace_bytes(T, n_seq) bytes (0 for bad
  * sizes), not used by another call in flight; its contents need not survive.
