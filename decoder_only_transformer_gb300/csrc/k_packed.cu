@@ -420,6 +420,25 @@ __device__ __forceinline__ void make_item(Item& it, const int4 blk, int sub, con
     it.nmax = it.n[1] > it.n[0] ? it.n[1] : it.n[0];
 }
 
+// The same values, known to the compiler to be equal in all lanes.
+__device__ __forceinline__ Item uniform_item(const Item& it) {
+    Item u;
+    u.start = (int)uniform(it.start);
+    u.len = 0;
+    u.row[0] = (int)uniform(it.row[0]);
+    u.row[1] = (int)uniform(it.row[1]);
+    u.h[0] = (int)uniform(it.h[0]);
+    u.h[1] = (int)uniform(it.h[1]);
+    u.g = (int)uniform(it.g);
+    u.j0 = (int)uniform(it.j0);
+    u.lo[0] = 0;
+    u.lo[1] = (int)uniform(it.lo[1]);
+    u.n[0] = (int)uniform(it.n[0]);
+    u.n[1] = (int)uniform(it.n[1]);
+    u.nmax = u.n[1] > u.n[0] ? u.n[1] : u.n[0];
+    return u;
+}
+
 // Whether key tile j of the item holds a key that some row of it does not see:
 // the diagonals, and with a window the tiles that start before some row's window.
 template <bool kWin>
@@ -427,6 +446,16 @@ __device__ __forceinline__ bool masked_tile(const Item& it, int j, int window) {
     const int k0 = (it.j0 + j) * kKV;
     return k0 == it.row[0] || (it.n[1] && k0 == it.row[1]) ||
            (kWin && k0 < it.row[it.n[1] ? 1 : 0] + kQ - window);
+}
+
+// Adds the values of n keys that are not finite to an output row.
+__device__ __noinline__ void put_back(__nv_bfloat16* orow, const __nv_bfloat16* __restrict__ v, int64_t vt, int dh,
+                                      int n) {
+    for (int k = 0; k < n; ++k)
+        for (int c = 0; c < dh; ++c) {
+            const float w = __bfloat162float(v[k * vt + c]);
+            if (!(fabsf(w) < INFINITY)) orow[c] = __float2bfloat16_rn(__bfloat162float(orow[c]) + w);
+        }
 }
 
 template <int DH, bool kWin>
@@ -482,7 +511,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             mbar_init(o_done(x), 1);
         }
         mbar_init(done_bar, L::kAlias ? 1 : 2);
-        *abort_flag = 0;
+        abort_flag[0] = abort_flag[1] = 0;
         for (int i = 0; i < kPoison; ++i) poison[i] = 0;
         fence_mbar_init();
         tma_prefetch_desc(&qmap);
@@ -525,20 +554,21 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     // Q, K: K-major tiles in 64-column sub-tiles of 16 KB; V: MN-major
     const uint64_t dq = sdesc(sQ, L::kSwz, 16, L::kGroup), dk = sdesc(sK, L::kSwz, 16, L::kGroup);
     const uint64_t dv = sdesc(sV, L::kSwz, DH > 64 ? 16384 : 0, L::kGroup);
+    const uint32_t tm = uniform(tmem_base);
     auto issue_s = [&](int x, int qs, int ks) {
         const uint64_t a0 = dq + (uint64_t)(qs * (L::kTile >> 4)), b0 = dk + (uint64_t)(ks * (L::kTile >> 4));
 #pragma unroll
         for (int kk = 0; kk < DH / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-            umma_bf16(tmem_base + x * kKV, a0 + off, b0 + off, idesc_s, kk > 0 ? 1u : 0u);
+            umma_bf16_e(tm + x * kKV, a0 + off, b0 + off, idesc_s, kk > 0 ? 1u : 0u);
         }
-        umma_commit(s_full(x));
+        umma_commit_e(s_full(x));
     };
     auto issue_pv = [&](int x, int vs, bool first) {
         const uint64_t b0 = dv + (uint64_t)(vs * (L::kTile >> 4));
 #pragma unroll
         for (int kk = 0; kk < kKV / 16; ++kk)
-            umma_bf16_ts(tmem_base + L::kOCol + x * DH, tmem_base + L::p_col(x) + kk * 8,
+            umma_bf16_ts_e(tm + L::kOCol + x * DH, tm + L::p_col(x) + kk * 8,
                          b0 + kk * ((16 * L::kRowBytes) >> 4), idesc_o, (!first || kk > 0) ? 1u : 0u);
     };
 
@@ -547,66 +577,74 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     if (warp == 0) {
         // ---------------------------------------------------------- TMA producer
         // Per item Q_A, Q_B and K_0, then V_j, K_{j+1}, the order in which the
-        // MMA threads take them.  It leaves once its last copies have landed.
-        if (lane == 0) {
-            int qn = 0, kn = 0, vn = 0;
-            bool ok = true;
-            Item it;
-            auto load = [&](uint32_t dst, const CUtensorMap* map, int row, int head, uint32_t bar) {
+        // MMA warps take them.
+        int qn = 0, kn = 0, vn = 0;
+        bool ok = true;
+        Item raw_it;
+        while (ok && next_item(raw_it)) {
+            const Item it = uniform_item(raw_it);
 #pragma unroll
-                for (int s = 0; s < L::kSub; ++s)
-                    tma_load_3d(dst + s * 16384, map, 64 * s, row, head, bar);
-            };
-            while (ok && next_item(it)) {
-                for (int x = 0; x < 2 && ok; ++x) {
-                    if (it.n[x] == 0) continue;
-                    const int s = qn % NQ;
-                    ok = mbar_wait(q_empty(s), ((uint32_t)(qn / NQ) & 1u) ^ 1u, err, abort_flag);
+            for (int x = 0; x < 2; ++x) {
+                if (!ok || it.n[x] == 0) continue;
+                const int s = qn % NQ;
+                if (qn >= NQ) ok = warp_wait(q_empty(s), ((uint32_t)(qn / NQ) & 1u) ^ 1u, err, abort_flag);
+                if (!ok) continue;
+                mbar_arrive_expect_tx_e(q_full(s), L::kTile);
+#pragma unroll
+                for (int c2 = 0; c2 < L::kSub; ++c2)
+                    tma_load_3d_e(sQ + s * L::kTile + c2 * 16384, &qmap, 64 * c2, it.start + it.row[x], it.h[x], q_full(s));
+                ++qn;
+            }
+            int y = it.start + it.j0 * kKV;            // the next K tile's first row
+            for (int j = 0; j <= it.nmax && ok; ++j, y += kKV) {
+                if (j > 0) {
+                    const int s = vn % SV;
+                    if (vn >= SV) ok = warp_wait(v_empty(s), ((uint32_t)(vn / SV) & 1u) ^ 1u, err, abort_flag);
                     if (!ok) break;
-                    mbar_arrive_expect_tx(q_full(s), L::kTile);
-                    load(sQ + s * L::kTile, &qmap, it.start + it.row[x], it.h[x], q_full(s));
-                    ++qn;
+                    mbar_arrive_expect_tx_e(v_full(s), L::kTile);
+#pragma unroll
+                    for (int c2 = 0; c2 < L::kSub; ++c2)
+                        tma_load_3d_e(sV + s * L::kTile + c2 * 16384, &vmap, 64 * c2, y - kKV, it.g, v_full(s));
+                    ++vn;
                 }
-                for (int j = 0; j <= it.nmax && ok; ++j) {
-                    if (j > 0) {
-                        const int s = vn % SV;
-                        ok = mbar_wait(v_empty(s), ((uint32_t)(vn / SV) & 1u) ^ 1u, err, abort_flag);
-                        if (!ok) break;
-                        mbar_arrive_expect_tx(v_full(s), L::kTile);
-                        load(sV + s * L::kTile, &vmap, it.start + (it.j0 + j - 1) * kKV, it.g, v_full(s));
-                        ++vn;
-                    }
-                    if (j < it.nmax) {
-                        const int s = kn % SK;
-                        ok = mbar_wait(k_empty(s), ((uint32_t)(kn / SK) & 1u) ^ 1u, err, abort_flag);
-                        if (!ok) break;
-                        mbar_arrive_expect_tx(k_full(s), L::kTile);
-                        load(sK + s * L::kTile, &kmap, it.start + (it.j0 + j) * kKV, it.g, k_full(s));
-                        ++kn;
-                    }
+                if (j < it.nmax) {
+                    const int s = kn % SK;
+                    if (kn >= SK) ok = warp_wait(k_empty(s), ((uint32_t)(kn / SK) & 1u) ^ 1u, err, abort_flag);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx_e(k_full(s), L::kTile);
+#pragma unroll
+                    for (int c2 = 0; c2 < L::kSub; ++c2)
+                        tma_load_3d_e(sK + s * L::kTile + c2 * 16384, &kmap, 64 * c2, y, it.g, k_full(s));
+                    ++kn;
                 }
             }
-            for (int k = qn < NQ ? 0 : qn - NQ; k < qn; ++k)
-                mbar_wait(q_full(k % NQ), (uint32_t)(k / NQ) & 1u, err, abort_flag);
-            for (int k = kn < SK ? 0 : kn - SK; k < kn; ++k)
-                mbar_wait(k_full(k % SK), (uint32_t)(k / SK) & 1u, err, abort_flag);
-            for (int k = vn < SV ? 0 : vn - SV; k < vn; ++k)
-                mbar_wait(v_full(k % SV), (uint32_t)(k / SV) & 1u, err, abort_flag);
+        }
+        // The other warps wait for every load; after a wait that gave up, the last
+        // ones still have to land before the CTA ends.
+        if (!ok && lane == 0) {
+            volatile int* never = abort_flag + 1;       // stays 0: these waits run to their own limit
+            for (int k = qn < NQ ? 0 : qn - NQ; k < qn; ++k) mbar_wait(q_full(k % NQ), (uint32_t)(k / NQ) & 1u, nullptr, never);
+            for (int k = kn < SK ? 0 : kn - SK; k < kn; ++k) mbar_wait(k_full(k % SK), (uint32_t)(k / SK) & 1u, nullptr, never);
+            for (int k = vn < SV ? 0 : vn - SV; k < vn; ++k) mbar_wait(v_full(k % SV), (uint32_t)(k / SV) & 1u, nullptr, never);
         }
     } else if (warp == 3) {
         // ---------------------------------------------------------- V check
         // In a tile that some row does not see whole, P is zero where the row
         // does not look, but zero times infinity is not: such values are taken
         // out here (and added back for the rows that see them, in the epilogue).
+        // Every tile passes through here before its P.V, so that no barrier runs
+        // past a phase that this warp has not seen.
         int vn = 0, items = 0;
         bool ok = true;
         Item it;
         for (; ok && next_item(it); ++items)
             for (int j = 0; j < it.nmax; ++j, ++vn) {
-                // every tile is waited for: a barrier's parity tells only its last phase
                 const int s = vn % SV;
                 if (!(ok = warp_wait(v_full(s), (uint32_t)(vn / SV) & 1u, err, abort_flag))) break;
-                if (!masked_tile<kWin>(it, j, gm.window)) continue;
+                if (!masked_tile<kWin>(it, j, gm.window)) {
+                    if (lane == 0) mbar_arrive(v_clean(s));
+                    continue;
+                }
                 const uint32_t at = sV + s * L::kTile + lane * 16;
                 bool found = false;
 #pragma unroll 1
@@ -635,137 +673,135 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 if (lane == 0) mbar_arrive(v_clean(s));
             }
     } else if (L::kAlias && warp == 1) {
-        // ---------------------------------------------------------- MMAs, one thread
+        // ---------------------------------------------------------- MMAs, one warp
         // A round is one key tile.  Behind P_x.V of a round comes S_x of the next
         // (of the same or the next item), which overwrites P_x: MMAs of one
         // thread complete in the order they are issued.  While the softmax works
         // on one tile, the other one's P.V and S run.
-        if (lane == 0) {
-            bool ok = true;
-            int kn = 0, vn = 0, qn = 0, pc[2] = {0, 0};
-            uint32_t clean = 0;                        // a V slot's checks so far, modulo 2
-            Item cur, nxt;
-            bool has = next_item(cur);
-            int qs[2] = {0, 0};
-            auto open_item = [&](const Item& it) {     // Q slots of an item
-                for (int x = 0; x < 2; ++x)
-                    if (it.n[x]) qs[x] = qn++;
-            };
-            auto do_s = [&](const Item& it, int j, int x) {
-                if (j < it.lo[x] || j >= it.n[x]) return;
-                const int s = qs[x] % NQ;
-                if (j == it.lo[x]) ok = ok && mbar_wait(q_full(s), (uint32_t)(qs[x] / NQ) & 1u, err, abort_flag);
-                ok = ok && mbar_wait(k_full(kn % SK), (uint32_t)(kn / SK) & 1u, err, abort_flag);
-                if (!ok) return;
-                tc_fence_after();
-                issue_s(x, s, kn % SK);
-                if (j == it.n[x] - 1) umma_commit(q_empty(s));
-            };
-            if (has) {
-                open_item(cur);
-                do_s(cur, 0, 0);
-                do_s(cur, 0, 1);
-                if (ok) umma_commit(k_empty(kn % SK));
-                ++kn;
-            }
-            while (has && ok) {
-                bool has_next = false;
-                for (int j = 0; j < cur.nmax && ok; ++j, ++vn) {
-                    const bool last = j == cur.nmax - 1;
-                    if (last) {
-                        has_next = next_item(nxt);
-                        if (has_next) open_item(nxt);
+        bool ok = true;
+        int kn = 0, vn = 0, qn = 0, pc[2] = {0, 0};
+        Item raw_it, cur, nxt;
+        bool has = next_item(raw_it);
+        if (has) cur = nxt = uniform_item(raw_it);
+        int qs[2] = {0, 0};
+        auto open_item = [&](const Item& it) {         // Q slots of an item
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                if (it.n[x]) qs[x] = qn++;
+        };
+        auto do_s = [&](const Item& it, int j, int x) {
+            if (!ok || j < it.lo[x] || j >= it.n[x]) return;
+            const int s = qs[x] % NQ;
+            if (j == it.lo[x]) ok = warp_wait(q_full(s), (uint32_t)(qs[x] / NQ) & 1u, err, abort_flag);
+            ok = ok && warp_wait(k_full(kn % SK), (uint32_t)(kn / SK) & 1u, err, abort_flag);
+            if (!ok) return;
+            tc_fence_after();
+            issue_s(x, s, kn % SK);
+            if (j == it.n[x] - 1) umma_commit_e(q_empty(s));
+        };
+        if (has) {
+            open_item(cur);
+            do_s(cur, 0, 0);
+            do_s(cur, 0, 1);
+            if (ok) umma_commit_e(k_empty(kn % SK));
+            ++kn;
+        }
+        while (has && ok) {
+            bool has_next = false;
+            for (int j = 0; j < cur.nmax && ok; ++j, ++vn) {
+                const bool last = j == cur.nmax - 1;
+                if (last) {
+                    has_next = next_item(raw_it);
+                    if (has_next) {
+                        nxt = uniform_item(raw_it);
+                        open_item(nxt);
                     }
-                    const bool ahead_s = !last || has_next;
-                    const Item& si = last ? nxt : cur;
-                    const int sj = last ? 0 : j + 1;
-                    ok = mbar_wait(v_full(vn % SV), (uint32_t)(vn / SV) & 1u, err, abort_flag);
-                    if (ok && masked_tile<kWin>(cur, j, gm.window)) {
-                        ok = mbar_wait(v_clean(vn % SV), (clean >> (vn % SV)) & 1u, err, abort_flag);
-                        clean ^= 1u << (vn % SV);
-                    }
-                    for (int x = 0; x < 2 && ok; ++x) {
-                        if (j >= cur.lo[x] && j < cur.n[x]) {
-                            ok = mbar_wait(p_full(x), (uint32_t)pc[x] & 1u, err, abort_flag);
-                            if (!ok) break;
+                }
+                const bool ahead_s = !last || has_next;
+                ok = warp_wait(v_clean(vn % SV), (uint32_t)(vn / SV) & 1u, err, abort_flag);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (ok && j >= cur.lo[x] && j < cur.n[x]) {
+                        ok = warp_wait(p_full(x), (uint32_t)pc[x] & 1u, err, abort_flag);
+                        if (ok) {
                             ++pc[x];
                             tc_fence_after();
                             issue_pv(x, vn % SV, j == cur.lo[x]);
-                            if (j == cur.n[x] - 1) umma_commit(o_done(x));
+                            if (j == cur.n[x] - 1) umma_commit_e(o_done(x));
                         }
-                        if (x == 1) umma_commit(v_empty(vn % SV));
-                        if (ahead_s) do_s(si, sj, x);
                     }
+                    if (ok && x == 1) umma_commit_e(v_empty(vn % SV));
                     if (ok && ahead_s) {
-                        umma_commit(k_empty(kn % SK));
-                        ++kn;
+                        if (last) do_s(nxt, 0, x);
+                        else do_s(cur, j + 1, x);
                     }
                 }
-                has = has_next;
-                cur = nxt;
+                if (ok && ahead_s) {
+                    umma_commit_e(k_empty(kn % SK));
+                    ++kn;
+                }
             }
-            umma_commit(done_bar);
-            mbar_wait(done_bar, 0, err, abort_flag);
+            has = has_next;
+            cur = nxt;
         }
+        umma_commit_e(done_bar);
+        warp_wait(done_bar, 0, err, abort_flag);
     } else if (!L::kAlias && warp == 1) {
         // ---------------------------------------------------------- S MMAs
         // S_x of the next tile as soon as the softmax has read the last one into
         // registers (P has columns of its own).
-        if (lane == 0) {
-            bool ok = true;
-            int kn = 0, qn = 0, cnt[2] = {0, 0};
-            Item it;
-            while (ok && next_item(it)) {
-                int qs[2] = {0, 0};
-                for (int x = 0; x < 2; ++x)
-                    if (it.n[x]) qs[x] = qn++;
-                for (int j = 0; j < it.nmax && ok; ++j, ++kn) {
-                    ok = mbar_wait(k_full(kn % SK), (uint32_t)(kn / SK) & 1u, err, abort_flag);
-                    for (int x = 0; x < 2 && ok; ++x) {
-                        if (j < it.lo[x] || j >= it.n[x]) continue;
-                        const int s = qs[x] % NQ;
-                        if (j == it.lo[x]) ok = mbar_wait(q_full(s), (uint32_t)(qs[x] / NQ) & 1u, err, abort_flag);
-                        if (ok && cnt[x] > 0) ok = mbar_wait(s_free(x), (uint32_t)(cnt[x] - 1) & 1u, err, abort_flag);
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_s(x, s, kn % SK);
-                        if (j == it.n[x] - 1) umma_commit(q_empty(s));
-                        ++cnt[x];
-                    }
-                    if (ok) umma_commit(k_empty(kn % SK));
+        bool ok = true;
+        int kn = 0, qn = 0, cnt[2] = {0, 0};
+        Item raw_it;
+        while (ok && next_item(raw_it)) {
+            const Item it = uniform_item(raw_it);
+            int qs[2] = {0, 0};
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                if (it.n[x]) qs[x] = qn++;
+            for (int j = 0; j < it.nmax && ok; ++j, ++kn) {
+                ok = warp_wait(k_full(kn % SK), (uint32_t)(kn / SK) & 1u, err, abort_flag);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (!ok || j < it.lo[x] || j >= it.n[x]) continue;
+                    const int s = qs[x] % NQ;
+                    if (j == it.lo[x]) ok = warp_wait(q_full(s), (uint32_t)(qs[x] / NQ) & 1u, err, abort_flag);
+                    if (ok && cnt[x] > 0) ok = warp_wait(s_free(x), (uint32_t)(cnt[x] - 1) & 1u, err, abort_flag);
+                    if (!ok) continue;
+                    tc_fence_after();
+                    issue_s(x, s, kn % SK);
+                    if (j == it.n[x] - 1) umma_commit_e(q_empty(s));
+                    ++cnt[x];
                 }
+                if (ok) umma_commit_e(k_empty(kn % SK));
             }
-            umma_commit(done_bar);
-            mbar_wait(done_bar, 0, err, abort_flag);
         }
+        umma_commit_e(done_bar);
+        warp_wait(done_bar, 0, err, abort_flag);
     } else if (!L::kAlias && warp == 2) {
         // ---------------------------------------------------------- P.V MMAs
-        if (lane == 0) {
-            bool ok = true;
-            int vn = 0, cnt[2] = {0, 0};
-            uint32_t clean = 0;                        // a V slot's checks so far, modulo 2
-            Item it;
-            while (ok && next_item(it))
-                for (int j = 0; j < it.nmax && ok; ++j, ++vn) {
-                    ok = mbar_wait(v_full(vn % SV), (uint32_t)(vn / SV) & 1u, err, abort_flag);
-                    if (ok && masked_tile<kWin>(it, j, gm.window)) {
-                        ok = mbar_wait(v_clean(vn % SV), (clean >> (vn % SV)) & 1u, err, abort_flag);
-                        clean ^= 1u << (vn % SV);
-                    }
-                    for (int x = 0; x < 2 && ok; ++x) {
-                        if (j < it.lo[x] || j >= it.n[x]) continue;
-                        ok = mbar_wait(p_full(x), (uint32_t)cnt[x] & 1u, err, abort_flag);
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_pv(x, vn % SV, j == it.lo[x]);
-                        umma_commit(o_done(x));
-                        ++cnt[x];
-                    }
-                    if (ok) umma_commit(v_empty(vn % SV));
+        bool ok = true;
+        int vn = 0, cnt[2] = {0, 0};
+        Item raw_it;
+        while (ok && next_item(raw_it)) {
+            const Item it = uniform_item(raw_it);
+            for (int j = 0; j < it.nmax && ok; ++j, ++vn) {
+                ok = warp_wait(v_clean(vn % SV), (uint32_t)(vn / SV) & 1u, err, abort_flag);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (!ok || j < it.lo[x] || j >= it.n[x]) continue;
+                    ok = warp_wait(p_full(x), (uint32_t)cnt[x] & 1u, err, abort_flag);
+                    if (!ok) continue;
+                    tc_fence_after();
+                    issue_pv(x, vn % SV, j == it.lo[x]);
+                    umma_commit_e(o_done(x));
+                    ++cnt[x];
                 }
-            umma_commit(done_bar);
-            mbar_wait(done_bar, 0, err, abort_flag);
+                if (ok) umma_commit_e(v_empty(vn % SV));
+            }
         }
+        umma_commit_e(done_bar);
+        warp_wait(done_bar, 0, err, abort_flag);
     }
     } else {
         // ---------------------------------------------------------- softmax (warps 4..11)
@@ -885,7 +921,6 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             if (!ok) break;
             tc_fence_after();
             const float inv = 1.0f / l;
-            const bool fix = poison[items % kPoison] == items + 1;
             __nv_bfloat16* orow = o + (int64_t)(it.start + qi) * ot + (int64_t)it.h[x] * oh;
 #pragma unroll 1
             for (int cc = 0; cc < DH / 32; ++cc) {
@@ -893,21 +928,6 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 tmem_ld32(t_o + cc * 32, ov);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) ov[e] *= inv;
-                if (fix && qi < it.len) {
-                    // what the V check took out, for the keys this row sees
-                    for (int j = it.lo[x]; j < n; ++j) {
-                        if (!masked_tile<kWin>(it, j, gm.window)) continue;
-                        const int k0 = (it.j0 + j) * kKV;
-                        for (int key = max(k0, kWin ? kmin : 0); key <= min(k0 + kKV - 1, qi); ++key) {
-                            const __nv_bfloat16* vr = v + (int64_t)(it.start + key) * vt + (int64_t)it.g * vh + cc * 32;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const float w = __bfloat162float(vr[e]);
-                                if (!(fabsf(w) < INFINITY)) ov[e] += w;
-                            }
-                        }
-                    }
-                }
                 if (qi < it.len) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
@@ -921,6 +941,17 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 }
                 __syncwarp();
             }
+            if (poison[items % kPoison] == items + 1 && qi < it.len) {
+                // what the V check took out, for the keys this row sees
+#pragma unroll 1
+                for (int j = it.lo[x]; j < n; ++j)
+                    if (masked_tile<kWin>(it, j, gm.window)) {
+                        const int k0 = (it.j0 + j) * kKV, from = max(k0, kWin ? kmin : 0);
+                        put_back(orow, v + (int64_t)(it.start + from) * vt + (int64_t)it.g * vh, vt, DH,
+                                 min(k0 + kKV - 1, qi) - from + 1);
+                    }
+            }
+            __syncwarp();
             // O is read out before this warp publishes the next item's first P
             tc_fence_before();
         }
