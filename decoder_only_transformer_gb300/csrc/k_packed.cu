@@ -370,12 +370,16 @@ struct Pk {
     static constexpr int kRowBytes = DH >= 64 ? 128 : 64;   // of a shared-memory tile
     static constexpr int kSub = DH / 64 > 1 ? DH / 64 : 1;  // 64-column sub-tiles
     static constexpr int kTile = kQ * DH * 2;               // bytes of a Q, K or V tile
-    static constexpr int kNQ = DH == 128 ? 3 : 4;
+    static constexpr int kNQ = DH == 128 ? 2 : 4;
     static constexpr int kSK = DH == 128 ? 2 : (DH == 64 ? 4 : 6);
     static constexpr int kSV = kSK;
     static constexpr int kKOff = kNQ * kTile;
     static constexpr int kVOff = kKOff + kSK * kTile;
-    static constexpr int kBarOff = kVOff + kSV * kTile;
+    // output rows of a softmax warp, 64 columns at a time
+    static constexpr int kStageRow = DH >= 64 ? 128 : 64;
+    static constexpr int kStage = 32 * kStageRow;
+    static constexpr int kStageOff = kVOff + kSV * kTile;
+    static constexpr int kBarOff = kStageOff + 8 * kStage;
     static constexpr int kNumBars = 2 * (kNQ + kSK + kSV) + kSV + 9;
     static constexpr int kMiscOff = kBarOff + 8 * kNumBars;
     static constexpr int kBytes = kMiscOff + 16 + 4 * kPoison + 1024;
@@ -445,7 +449,7 @@ template <bool kWin>
 __device__ __forceinline__ bool masked_tile(const Item& it, int j, int window) {
     const int k0 = (it.j0 + j) * kKV;
     return k0 == it.row[0] || (it.n[1] && k0 == it.row[1]) ||
-           (kWin && k0 < it.row[it.n[1] ? 1 : 0] + kQ - window);
+           (kWin && k0 < (it.n[1] ? it.row[1] : it.row[0]) + kQ - window);
 }
 
 // Adds the values of n keys that are not finite to an output row.
@@ -497,11 +501,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         }
         for (int s = 0; s < SK; ++s) {
             mbar_init(k_full(s), 1);
-            mbar_init(k_empty(s), 1);
+            mbar_init(k_empty(s), 2);                  // both MMA warps are done with the slot
         }
         for (int s = 0; s < SV; ++s) {
             mbar_init(v_full(s), 1);
-            mbar_init(v_empty(s), 1);
+            mbar_init(v_empty(s), 2);
             mbar_init(v_clean(s), 1);
         }
         for (int x = 0; x < 2; ++x) {
@@ -510,7 +514,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             mbar_init(p_full(x), 4);
             mbar_init(o_done(x), 1);
         }
-        mbar_init(done_bar, L::kAlias ? 1 : 2);
+        mbar_init(done_bar, 2);
         abort_flag[0] = abort_flag[1] = 0;
         for (int i = 0; i < kPoison; ++i) poison[i] = 0;
         fence_mbar_init();
@@ -573,7 +577,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     };
 
     if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     if (warp == 0) {
         // ---------------------------------------------------------- TMA producer
         // Per item Q_A, Q_B and K_0, then V_j, K_{j+1}, the order in which the
@@ -672,41 +676,58 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(v_clean(s));
             }
-    } else if (L::kAlias && warp == 1) {
-        // ---------------------------------------------------------- MMAs, one warp
-        // A round is one key tile.  Behind P_x.V of a round comes S_x of the next
-        // (of the same or the next item), which overwrites P_x: MMAs of one
-        // thread complete in the order they are issued.  While the softmax works
-        // on one tile, the other one's P.V and S run.
+    } else {
+        // ---------------------------------------------------------- MMAs (warp 1: tile A, warp 2: tile B)
+        // A warp per tile: each runs at the pace of its own softmax, and the two
+        // pipelines drift into the phase in which one's exponentials run beside the
+        // other's products (issued by one warp in the order A, B, A, ..., each
+        // waited for the other: d_head 64, 8192 tokens, 2400 cycles per pair of tiles
+        // instead of TODO).  A round is a key tile of the item; a tile that this
+        // warp's queries do not see is passed on unread.
+        // P in columns of its own: S of the next round as soon as the softmax has
+        // read this one's.  P in the place of S (d_head 128): behind this round's P.V,
+        // as MMAs of one thread complete in the order they are issued.
+        const int x = (int)uniform((uint32_t)(warp - 1));
         bool ok = true;
-        int kn = 0, vn = 0, qn = 0, pc[2] = {0, 0};
+        int kn = 0, vn = 0, qn = 0, cnt = 0, qs = 0;    // tiles, Q slots so far; own tiles; own Q slot
         Item raw_it, cur, nxt;
         bool has = next_item(raw_it);
         if (has) cur = nxt = uniform_item(raw_it);
-        int qs[2] = {0, 0};
-        auto open_item = [&](const Item& it) {         // Q slots of an item
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-                if (it.n[x]) qs[x] = qn++;
+        int lo = 0, n = 0;                              // own rounds of the item S is at
+        auto open_item = [&](const Item& it) {
+            lo = x ? it.lo[1] : 0;
+            n = x ? it.n[1] : it.n[0];
+            qs = qn + x;
+            qn += it.n[1] ? 2 : 1;
         };
-        auto do_s = [&](const Item& it, int j, int x) {
-            if (!ok || j < it.lo[x] || j >= it.n[x]) return;
-            const int s = qs[x] % NQ;
-            if (j == it.lo[x]) ok = warp_wait(q_full(s), (uint32_t)(qs[x] / NQ) & 1u, err, abort_flag);
-            ok = ok && warp_wait(k_full(kn % SK), (uint32_t)(kn / SK) & 1u, err, abort_flag);
-            if (!ok) return;
+        // Round j of the item that was opened last; false: not this warp's.
+        auto do_s = [&](int j) -> bool {
+            const int s = kn % SK;
+            ok = warp_wait(k_full(s), (uint32_t)(kn / SK) & 1u, err, abort_flag);
+            if (j < lo || j >= n) {
+                if (lane == 0) mbar_arrive(k_empty(s));
+                ++kn;
+                return false;
+            }
+            if (j == lo) ok = ok && warp_wait(q_full(qs % NQ), (uint32_t)(qs / NQ) & 1u, err, abort_flag);
+            if (!L::kAlias && cnt > 0) ok = ok && warp_wait(s_free(x), (uint32_t)(cnt - 1) & 1u, err, abort_flag);
+            if (!ok) return false;
             tc_fence_after();
-            issue_s(x, s, kn % SK);
-            if (j == it.n[x] - 1) umma_commit_e(q_empty(s));
+            issue_s(x, qs % NQ, s);
+            umma_commit_e(k_empty(s));
+            if (j == n - 1) umma_commit_e(q_empty(qs % NQ));
+            ++kn;
+            ++cnt;
+            return true;
         };
+        int pv = 0;                                     // own P.V so far
+        bool own = false;                               // the round P.V is at is this warp's
         if (has) {
             open_item(cur);
-            do_s(cur, 0, 0);
-            do_s(cur, 0, 1);
-            if (ok) umma_commit_e(k_empty(kn % SK));
-            ++kn;
+            own = do_s(0);
         }
         while (has && ok) {
+            const int cur_lo = x ? cur.lo[1] : 0, cur_n = x ? cur.n[1] : cur.n[0];
             bool has_next = false;
             for (int j = 0; j < cur.nmax && ok; ++j, ++vn) {
                 const bool last = j == cur.nmax - 1;
@@ -717,95 +738,35 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                         open_item(nxt);
                     }
                 }
-                const bool ahead_s = !last || has_next;
-                ok = warp_wait(v_clean(vn % SV), (uint32_t)(vn / SV) & 1u, err, abort_flag);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (ok && j >= cur.lo[x] && j < cur.n[x]) {
-                        ok = warp_wait(p_full(x), (uint32_t)pc[x] & 1u, err, abort_flag);
-                        if (ok) {
-                            ++pc[x];
-                            tc_fence_after();
-                            issue_pv(x, vn % SV, j == cur.lo[x]);
-                            if (j == cur.n[x] - 1) umma_commit_e(o_done(x));
-                        }
-                    }
-                    if (ok && x == 1) umma_commit_e(v_empty(vn % SV));
-                    if (ok && ahead_s) {
-                        if (last) do_s(nxt, 0, x);
-                        else do_s(cur, j + 1, x);
-                    }
+                const bool more = !last || has_next;
+                const int sj = last ? 0 : j + 1;
+                const bool next_own = more && sj >= lo && sj < n;
+                if (!L::kAlias && next_own) do_s(sj);
+                const int s = vn % SV;
+                ok = ok && warp_wait(v_clean(s), (uint32_t)(vn / SV) & 1u, err, abort_flag);
+                if (ok && own) {
+                    ok = warp_wait(p_full(x), (uint32_t)pv & 1u, err, abort_flag);
+                    if (!ok) break;
+                    ++pv;
+                    tc_fence_after();
+                    issue_pv(x, s, j == cur_lo);
+                    if (!L::kAlias || j == cur_n - 1) umma_commit_e(o_done(x));
+                    umma_commit_e(v_empty(s));
+                } else if (ok && lane == 0) {
+                    mbar_arrive(v_empty(s));
                 }
-                if (ok && ahead_s) {
-                    umma_commit_e(k_empty(kn % SK));
-                    ++kn;
-                }
+                if (ok && more && (L::kAlias || !next_own)) do_s(sj);
+                own = next_own;
             }
             has = has_next;
             cur = nxt;
         }
         umma_commit_e(done_bar);
         warp_wait(done_bar, 0, err, abort_flag);
-    } else if (!L::kAlias && warp == 1) {
-        // ---------------------------------------------------------- S MMAs
-        // S_x of the next tile as soon as the softmax has read the last one into
-        // registers (P has columns of its own).
-        bool ok = true;
-        int kn = 0, qn = 0, cnt[2] = {0, 0};
-        Item raw_it;
-        while (ok && next_item(raw_it)) {
-            const Item it = uniform_item(raw_it);
-            int qs[2] = {0, 0};
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-                if (it.n[x]) qs[x] = qn++;
-            for (int j = 0; j < it.nmax && ok; ++j, ++kn) {
-                ok = warp_wait(k_full(kn % SK), (uint32_t)(kn / SK) & 1u, err, abort_flag);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (!ok || j < it.lo[x] || j >= it.n[x]) continue;
-                    const int s = qs[x] % NQ;
-                    if (j == it.lo[x]) ok = warp_wait(q_full(s), (uint32_t)(qs[x] / NQ) & 1u, err, abort_flag);
-                    if (ok && cnt[x] > 0) ok = warp_wait(s_free(x), (uint32_t)(cnt[x] - 1) & 1u, err, abort_flag);
-                    if (!ok) continue;
-                    tc_fence_after();
-                    issue_s(x, s, kn % SK);
-                    if (j == it.n[x] - 1) umma_commit_e(q_empty(s));
-                    ++cnt[x];
-                }
-                if (ok) umma_commit_e(k_empty(kn % SK));
-            }
-        }
-        umma_commit_e(done_bar);
-        warp_wait(done_bar, 0, err, abort_flag);
-    } else if (!L::kAlias && warp == 2) {
-        // ---------------------------------------------------------- P.V MMAs
-        bool ok = true;
-        int vn = 0, cnt[2] = {0, 0};
-        Item raw_it;
-        while (ok && next_item(raw_it)) {
-            const Item it = uniform_item(raw_it);
-            for (int j = 0; j < it.nmax && ok; ++j, ++vn) {
-                ok = warp_wait(v_clean(vn % SV), (uint32_t)(vn / SV) & 1u, err, abort_flag);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (!ok || j < it.lo[x] || j >= it.n[x]) continue;
-                    ok = warp_wait(p_full(x), (uint32_t)cnt[x] & 1u, err, abort_flag);
-                    if (!ok) continue;
-                    tc_fence_after();
-                    issue_pv(x, vn % SV, j == it.lo[x]);
-                    umma_commit_e(o_done(x));
-                    ++cnt[x];
-                }
-                if (ok) umma_commit_e(v_empty(vn % SV));
-            }
-        }
-        umma_commit_e(done_bar);
-        warp_wait(done_bar, 0, err, abort_flag);
     }
     } else {
         // ---------------------------------------------------------- softmax (warps 4..11)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int x = (warp >> 2) - 1;                 // 0: tile A, 1: tile B
         const int q4 = warp & 3;
         const int r = q4 * 32 + lane;
@@ -817,13 +778,13 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         bool ok = true;
         Item it;
         for (; ok && next_item(it); ++items) {
-            const int n = it.n[x];
+            const int n = x ? it.n[1] : it.n[0], lo = x ? it.lo[1] : 0;
             if (n == 0) continue;
-            const int row0 = it.row[x], qi = row0 + r;
+            const int row0 = x ? it.row[1] : it.row[0], qi = row0 + r;
             const int kmin = kWin ? qi - gm.window + 1 : 0;
             const int win_lo = kWin ? row0 + kQ - gm.window : INT_MIN;
             float m = -INFINITY, l = 0.f;
-            for (int j = it.lo[x]; j < n && ok; ++j, ++cnt) {
+            for (int j = lo; j < n && ok; ++j, ++cnt) {
                 if (!warp_wait(s_full(x), (uint32_t)cnt & 1u, err, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 uint32_t sr[kKV / 32][32];
@@ -850,9 +811,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                     for (int cc = 0; cc < kKV; ++cc) s[cc] = cc > r ? -INFINITY : s[cc];
                 }
                 if (kWin && k0 < win_lo) {
-                    const int lo = kmin - k0;
+                    const int from = kmin - k0;
 #pragma unroll
-                    for (int cc = 0; cc < kKV; ++cc) s[cc] = cc < lo ? -INFINITY : s[cc];
+                    for (int cc = 0; cc < kKV; ++cc) s[cc] = cc < from ? -INFINITY : s[cc];
                 }
                 float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -865,7 +826,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                     corr = fast_exp2(m - mx);
                     m = mx;
                 }
-                const bool need_rescale = __any_sync(0xffffffffu, corr != 1.f && j > it.lo[x]);
+                const bool need_rescale = __any_sync(0xffffffffu, corr != 1.f && j > lo && qi < it.len);
                 const uint64_t scale2 = f2_pack(scale_log2, scale_log2);
                 const float negm = (kWin && m == -INFINITY) ? 0.f : -m;
                 const uint64_t negm2 = f2_pack(negm, negm);
@@ -921,33 +882,44 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             if (!ok) break;
             tc_fence_after();
             const float inv = 1.0f / l;
-            __nv_bfloat16* orow = o + (int64_t)(it.start + qi) * ot + (int64_t)it.h[x] * oh;
+            // Rows go out through shared memory, 64 columns (32 at d_head 32) at a time,
+            // so that a store writes whole lines: 16 bytes of 32 rows per store kept the
+            // warp for 5000 to 10000 cycles at d_head 128.
+            __nv_bfloat16* obase = o + (int64_t)(it.start + row0 + q4 * 32) * ot + (int64_t)(x ? it.h[1] : it.h[0]) * oh;
+            const int rows = it.len - row0 - q4 * 32;  // of this warp's 32, those of the sequence
+            const uint32_t stage = base + L::kStageOff + (warp - 4) * L::kStage;
+            constexpr int kChunks = L::kStageRow / 16, kRowsPer = 32 / kChunks;
 #pragma unroll 1
-            for (int cc = 0; cc < DH / 32; ++cc) {
-                float ov[32];
-                tmem_ld32(t_o + cc * 32, ov);
+            for (int c0 = 0; c0 < DH; c0 += L::kStageRow / 2) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) ov[e] *= inv;
-                if (qi < it.len) {
+                for (int cc = 0; cc < L::kStageRow / 64; ++cc) {
+                    float ov[32];
+                    tmem_ld32(t_o + c0 + cc * 32, ov);
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
-                        uint4 w;
-                        w.x = pack_bf16x2(ov[e], ov[e + 1]);
-                        w.y = pack_bf16x2(ov[e + 2], ov[e + 3]);
-                        w.z = pack_bf16x2(ov[e + 4], ov[e + 5]);
-                        w.w = pack_bf16x2(ov[e + 6], ov[e + 7]);
-                        *reinterpret_cast<uint4*>(orow + cc * 32 + e) = w;
+                        const int ch = cc * 4 + e / 8;
+                        st_shared_v4(stage + lane * L::kStageRow + ((ch ^ (lane & (kChunks - 1))) * 16),
+                                     pack_bf16x2(ov[e] * inv, ov[e + 1] * inv), pack_bf16x2(ov[e + 2] * inv, ov[e + 3] * inv),
+                                     pack_bf16x2(ov[e + 4] * inv, ov[e + 5] * inv), pack_bf16x2(ov[e + 6] * inv, ov[e + 7] * inv));
                     }
+                }
+                __syncwarp();
+                const int ch = lane % kChunks;
+#pragma unroll
+                for (int i = 0; i < 32; i += kRowsPer) {
+                    const int rr = i + lane / kChunks;
+                    const uint4 w = ld_shared_v4(stage + rr * L::kStageRow + ((ch ^ (rr & (kChunks - 1))) * 16));
+                    if (rr < rows) *reinterpret_cast<uint4*>(obase + rr * ot + c0 + ch * 8) = w;
                 }
                 __syncwarp();
             }
             if (poison[items % kPoison] == items + 1 && qi < it.len) {
                 // what the V check took out, for the keys this row sees
 #pragma unroll 1
-                for (int j = it.lo[x]; j < n; ++j)
+                for (int j = lo; j < n; ++j)
                     if (masked_tile<kWin>(it, j, gm.window)) {
                         const int k0 = (it.j0 + j) * kKV, from = max(k0, kWin ? kmin : 0);
-                        put_back(orow, v + (int64_t)(it.start + from) * vt + (int64_t)it.g * vh, vt, DH,
+                        put_back(obase + lane * ot, v + (int64_t)(it.start + from) * vt + (int64_t)it.g * vh, vt, DH,
                                  min(k0 + kKV - 1, qi) - from + 1);
                     }
             }
