@@ -297,12 +297,14 @@ constexpr int kBins = 1024;
 struct __align__(16) Block {
     int start, len;    // rows of the sequence
     int row;           // the block's first row in it
+    int j0;            // first key tile
+    int n0, n1, lo1;   // key tiles of the two query tiles (struct Item)
     int pad;
 };
 
 template <int kRows>
 __global__ void __launch_bounds__(kPlanThreads) k_packed_plan(const int32_t* __restrict__ cu, int n_seq,
-                                                              int T, int slots, int shift, int window_blocks,
+                                                              int T, int slots, int shift, int window,
                                                               int* __restrict__ count,
                                                               Block* __restrict__ list, int* err) {
     __shared__ int bins[kBins];
@@ -328,8 +330,12 @@ __global__ void __launch_bounds__(kPlanThreads) k_packed_plan(const int32_t* __r
         const SeqRange r = seq_range(cu, b, T);
         const int t = s - (r.start / kRows + b);
         if (t < 0 || (int64_t)t * kRows >= r.len) return false;
-        blk = Block{r.start, r.len, t * kRows, 0};
-        bin = kBins - 1 - ((t < window_blocks ? t : window_blocks) >> shift);
+        const int rowA = t * kRows, rowB = kRows == 128 ? rowA : rowA + 128;
+        const int jA = window > 0 && rowA >= window ? (rowA - window + 1) / 128 : 0;
+        const int jB = window > 0 && rowB >= window ? (rowB - window + 1) / 128 : 0;
+        const bool two = rowB < r.len;
+        blk = Block{r.start, r.len, rowA, jA, rowA / 128 + 1 - jA, two ? rowB / 128 + 1 - jA : 0, two ? jB - jA : 0, 0};
+        bin = kBins - 1 - ((max(blk.n0, blk.n1) - 1) >> shift);
         return true;
     };
     Block blk;
@@ -402,45 +408,30 @@ struct PackedGeom {
     int group, subs;       // subs: items per block (H / 2 pairs of heads, or H heads)
     int by_heads;          // 1: two heads of one tile, 0: two tiles of one head
     int window;
+    uint32_t subs_inv, group_inv;
 };
 
-template <bool kWin>
-__device__ __forceinline__ void make_item(Item& it, const int4 blk, int sub, const PackedGeom& gm) {
-    it.start = blk.x;
-    it.len = blk.y;
-    it.row[0] = blk.z;
-    it.h[0] = gm.by_heads ? 2 * sub : sub;
-    it.h[1] = gm.by_heads ? it.h[0] + 1 : sub;
-    it.g = it.h[0] / gm.group;
-    it.row[1] = gm.by_heads ? blk.z : blk.z + kQ;
-    const bool two = it.row[1] < it.len;
-    const int wsA = it.row[0] - gm.window + 1, wsB = it.row[1] - gm.window + 1;
-    const int jA = (kWin && wsA > 0) ? wsA / kKV : 0, jB = (kWin && wsB > 0) ? wsB / kKV : 0;
-    it.j0 = jA;
-    it.lo[0] = 0;
-    it.n[0] = it.row[0] / kQ + 1 - jA;
-    it.lo[1] = two ? jB - jA : 0;
-    it.n[1] = two ? it.row[1] / kQ + 1 - jA : 0;
-    it.nmax = it.n[1] > it.n[0] ? it.n[1] : it.n[0];
+// x / d with inv = floor(2^32 / d) (2^32 - 1 for d = 1): the estimate is at most one
+// too small.
+__device__ __forceinline__ int div_by(int x, int d, uint32_t inv) {
+    const int q = (int)__umulhi((uint32_t)x, inv);
+    return x - q * d >= d ? q + 1 : q;
 }
 
-// The same values, known to the compiler to be equal in all lanes.
-__device__ __forceinline__ Item uniform_item(const Item& it) {
-    Item u;
-    u.start = (int)uniform(it.start);
-    u.len = 0;
-    u.row[0] = (int)uniform(it.row[0]);
-    u.row[1] = (int)uniform(it.row[1]);
-    u.h[0] = (int)uniform(it.h[0]);
-    u.h[1] = (int)uniform(it.h[1]);
-    u.g = (int)uniform(it.g);
-    u.j0 = (int)uniform(it.j0);
-    u.lo[0] = 0;
-    u.lo[1] = (int)uniform(it.lo[1]);
-    u.n[0] = (int)uniform(it.n[0]);
-    u.n[1] = (int)uniform(it.n[1]);
-    u.nmax = u.n[1] > u.n[0] ? u.n[1] : u.n[0];
-    return u;
+__device__ __forceinline__ void make_item(Item& it, const int4 a, const int4 b, int sub, const PackedGeom& gm) {
+    it.start = a.x;
+    it.len = a.y;
+    it.row[0] = a.z;
+    it.row[1] = gm.by_heads ? a.z : a.z + kQ;
+    it.h[0] = gm.by_heads ? 2 * sub : sub;
+    it.h[1] = gm.by_heads ? it.h[0] + 1 : sub;
+    it.g = div_by(it.h[0], gm.group, gm.group_inv);
+    it.j0 = a.w;
+    it.lo[0] = 0;
+    it.lo[1] = b.z;
+    it.n[0] = b.x;
+    it.n[1] = b.y;
+    it.nmax = b.y > b.x ? b.y : b.x;
 }
 
 // Whether key tile j of the item holds a key that some row of it does not see:
@@ -537,19 +528,25 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     const int G = (int)gridDim.x, c = (int)blockIdx.x;
     const int rounds = (total + G - 1) / G;
     auto index_of = [&](int rnd) { return rnd * G + ((rnd & 1) ? G - 1 - c : c); };
-    auto entry = [&](int rnd) -> int4 {
-        const int idx = index_of(rnd);
-        if (rnd >= rounds || idx >= total) return make_int4(0, 0, 0, -1);
-        return __ldg(reinterpret_cast<const int4*>(list) + idx / gm.subs);
+    int4 ea, eb;                                       // entry of the next item, its sub-item
+    int sub = 0, at_round = 0;
+    auto look_ahead = [&]() {
+        const int idx = index_of(at_round);
+        eb.x = 0;
+        if (at_round >= rounds || idx >= total) return;
+        const int k = div_by(idx, gm.subs, gm.subs_inv);
+        const int4* e = reinterpret_cast<const int4*>(list + k);
+        ea = __ldg(e);
+        eb = __ldg(e + 1);
+        sub = idx - k * gm.subs;
     };
-    int4 ahead = entry(0);
-    int at_round = 0;
+    look_ahead();
     // The next item; false when there is none.
     auto next_item = [&](Item& it) -> bool {
-        const int4 e = ahead;
-        if (e.w < 0) return false;                    // only the last round can be short
-        make_item<kWin>(it, e, index_of(at_round) % gm.subs, gm);
-        ahead = entry(++at_round);
+        if (eb.x == 0) return false;                   // only the last round can be short
+        make_item(it, ea, eb, sub, gm);
+        ++at_round;
+        look_ahead();
         return true;
     };
 
@@ -584,12 +581,12 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         // MMA warps take them.
         int qn = 0, kn = 0, vn = 0;
         bool ok = true;
-        Item raw_it;
-        while (ok && next_item(raw_it)) {
-            const Item it = uniform_item(raw_it);
+        Item it;
+        while (ok && next_item(it)) {
+            const int nmax = (int)uniform(it.nmax), two = (int)uniform(it.n[1]);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                if (!ok || it.n[x] == 0) continue;
+                if (!ok || (x && !two)) continue;
                 const int s = qn % NQ;
                 if (qn >= NQ) ok = warp_wait(q_empty(s), ((uint32_t)(qn / NQ) & 1u) ^ 1u, err, abort_flag);
                 if (!ok) continue;
@@ -600,7 +597,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 ++qn;
             }
             int y = it.start + it.j0 * kKV;            // the next K tile's first row
-            for (int j = 0; j <= it.nmax && ok; ++j, y += kKV) {
+            for (int j = 0; j <= nmax && ok; ++j, y += kKV) {
                 if (j > 0) {
                     const int s = vn % SV;
                     if (vn >= SV) ok = warp_wait(v_empty(s), ((uint32_t)(vn / SV) & 1u) ^ 1u, err, abort_flag);
@@ -611,7 +608,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                         tma_load_3d_e(sV + s * L::kTile + c2 * 16384, &vmap, 64 * c2, y - kKV, it.g, v_full(s));
                     ++vn;
                 }
-                if (j < it.nmax) {
+                if (j < nmax) {
                     const int s = kn % SK;
                     if (kn >= SK) ok = warp_wait(k_empty(s), ((uint32_t)(kn / SK) & 1u) ^ 1u, err, abort_flag);
                     if (!ok) break;
@@ -649,24 +646,28 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                     if (lane == 0) mbar_arrive(v_clean(s));
                     continue;
                 }
+                // An exponent of all ones carries into the bit above it when one is
+                // added; eight vectors are looked at together.
                 const uint32_t at = sV + s * L::kTile + lane * 16;
                 bool found = false;
 #pragma unroll 1
-                for (int i = 0; i < L::kTile; i += 4 * 512) {
-                    uint4 w[4];
+                for (int i = 0; i < L::kTile; i += 8 * 512) {
+                    uint4 w[8];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) w[u] = ld_shared_v4(at + i + u * 512);
+                    for (int u = 0; u < 8; ++u) w[u] = ld_shared_v4(at + i + u * 512);
+                    auto carry = [](uint32_t v) { return (v & 0x7F807F80u) + 0x00800080u; };
+                    uint32_t any = 0;
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const uint32_t bx = __vcmpeq2(w[u].x & 0x7F807F80u, 0x7F807F80u);
-                        const uint32_t by = __vcmpeq2(w[u].y & 0x7F807F80u, 0x7F807F80u);
-                        const uint32_t bz = __vcmpeq2(w[u].z & 0x7F807F80u, 0x7F807F80u);
-                        const uint32_t bw = __vcmpeq2(w[u].w & 0x7F807F80u, 0x7F807F80u);
-                        if (bx | by | bz | bw) {
-                            found = true;
-                            st_shared_v4(at + i + u * 512, w[u].x & ~bx, w[u].y & ~by, w[u].z & ~bz,
-                                         w[u].w & ~bw);
-                        }
+                    for (int u = 0; u < 8; ++u) any |= carry(w[u].x) | carry(w[u].y) | carry(w[u].z) | carry(w[u].w);
+                    if (any & 0x80008000u) {
+                        found = true;
+                        auto keep = [&](uint32_t v) {  // 0 in place of each that is not finite
+                            const uint32_t bad = (carry(v) & 0x80008000u) >> 15;
+                            return v & ~(bad * 0xFFFFu);
+                        };
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            st_shared_v4(at + i + u * 512, keep(w[u].x), keep(w[u].y), keep(w[u].z), keep(w[u].w));
                     }
                 }
                 if (__any_sync(0xffffffffu, found)) {
@@ -690,15 +691,17 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         const int x = (int)uniform((uint32_t)(warp - 1));
         bool ok = true;
         int kn = 0, vn = 0, qn = 0, cnt = 0, qs = 0;    // tiles, Q slots so far; own tiles; own Q slot
-        Item raw_it, cur, nxt;
-        bool has = next_item(raw_it);
-        if (has) cur = nxt = uniform_item(raw_it);
-        int lo = 0, n = 0;                              // own rounds of the item S is at
-        auto open_item = [&](const Item& it) {
-            lo = x ? it.lo[1] : 0;
-            n = x ? it.n[1] : it.n[0];
+        // own rounds [lo, n) and all rounds of the item S is at, and of the one P.V is at
+        int lo = 0, n = 0, nmax = 0, pv_lo = 0, pv_n = 0, pv_max = 0;
+        auto open_item = [&]() -> bool {
+            Item it;
+            if (!uniform(next_item(it))) return false;
+            nmax = (int)uniform(it.nmax);
+            lo = (int)uniform(x ? it.lo[1] : 0);
+            n = (int)uniform(x ? it.n[1] : it.n[0]);
             qs = qn + x;
-            qn += it.n[1] ? 2 : 1;
+            qn += uniform(it.n[1]) ? 2 : 1;
+            return true;
         };
         // Round j of the item that was opened last; false: not this warp's.
         auto do_s = [&](int j) -> bool {
@@ -722,22 +725,16 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         };
         int pv = 0;                                     // own P.V so far
         bool own = false;                               // the round P.V is at is this warp's
-        if (has) {
-            open_item(cur);
-            own = do_s(0);
-        }
+        bool has = open_item();
+        if (has) own = do_s(0);
         while (has && ok) {
-            const int cur_lo = x ? cur.lo[1] : 0, cur_n = x ? cur.n[1] : cur.n[0];
             bool has_next = false;
-            for (int j = 0; j < cur.nmax && ok; ++j, ++vn) {
-                const bool last = j == cur.nmax - 1;
-                if (last) {
-                    has_next = next_item(raw_it);
-                    if (has_next) {
-                        nxt = uniform_item(raw_it);
-                        open_item(nxt);
-                    }
-                }
+            pv_lo = lo;
+            pv_n = n;
+            pv_max = nmax;
+            for (int j = 0; j < pv_max && ok; ++j, ++vn) {
+                const bool last = j == pv_max - 1;
+                if (last) has_next = open_item();
                 const bool more = !last || has_next;
                 const int sj = last ? 0 : j + 1;
                 const bool next_own = more && sj >= lo && sj < n;
@@ -749,8 +746,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                     if (!ok) break;
                     ++pv;
                     tc_fence_after();
-                    issue_pv(x, s, j == cur_lo);
-                    if (!L::kAlias || j == cur_n - 1) umma_commit_e(o_done(x));
+                    issue_pv(x, s, j == pv_lo);
+                    if (!L::kAlias || j == pv_n - 1) umma_commit_e(o_done(x));
                     umma_commit_e(v_empty(s));
                 } else if (ok && lane == 0) {
                     mbar_arrive(v_empty(s));
@@ -759,7 +756,6 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 own = next_own;
             }
             has = has_next;
-            cur = nxt;
         }
         umma_commit_e(done_bar);
         warp_wait(done_bar, 0, err, abort_flag);
@@ -788,8 +784,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 if (!warp_wait(s_full(x), (uint32_t)cnt & 1u, err, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 uint32_t sr[kKV / 32][32];
+                float mq[kKV / 32];                    // maxima of the 32-column blocks
 #pragma unroll
-                for (int cc = 0; cc < kKV / 32; ++cc) tmem_ld32_issue(t_s + cc * 32, sr[cc]);
+                for (int cc = 0; cc < kKV / 32; ++cc) tmem_ld32_max_issue(t_s + cc * 32, sr[cc], mq[cc]);
                 tmem_ld_wait();
                 if (!L::kAlias) {
                     tc_fence_before();
@@ -800,6 +797,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 #pragma unroll
                 for (int cc = 0; cc < kKV / 32; ++cc) {
                     reg_fence32(sr[cc]);
+                    reg_fence(mq[cc]);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) s[cc * 32 + e] = __uint_as_float(sr[cc][e]);
                 }
@@ -815,12 +813,17 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 #pragma unroll
                     for (int cc = 0; cc < kKV; ++cc) s[cc] = cc < from ? -INFINITY : s[cc];
                 }
-                float mx4[4] = {s[0], s[1], s[2], s[3]};
+                float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+                if (k0 == row0 || (kWin && k0 < win_lo)) {
+                    // a masked tile: of the scores that are left
+                    float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int cc = 4; cc < kKV; cc += 8)
+                    for (int cc = 4; cc < kKV; cc += 8)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mx4[e] = fmax3(mx4[e], s[cc + 2 * e], s[cc + 2 * e + 1]);
-                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * scale_log2;
+                        for (int e = 0; e < 4; ++e) mx4[e] = fmax3(mx4[e], s[cc + 2 * e], s[cc + 2 * e + 1]);
+                    mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+                }
+                mx *= scale_log2;
                 float corr = 1.f;
                 if (mx > m + kRescale) {
                     corr = fast_exp2(m - mx);
@@ -889,19 +892,23 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             const int rows = it.len - row0 - q4 * 32;  // of this warp's 32, those of the sequence
             const uint32_t stage = base + L::kStageOff + (warp - 4) * L::kStage;
             constexpr int kChunks = L::kStageRow / 16, kRowsPer = 32 / kChunks;
-#pragma unroll 1
-            for (int c0 = 0; c0 < DH; c0 += L::kStageRow / 2) {
+            uint32_t ov[DH / 32][32];
+#pragma unroll
+            for (int cc = 0; cc < DH / 32; ++cc) tmem_ld32_issue(t_o + cc * 32, ov[cc]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int cc = 0; cc < DH / 32; ++cc) reg_fence32(ov[cc]);
+#pragma unroll
+            for (int c0 = 0; c0 < DH / 32; c0 += L::kStageRow / 64) {
 #pragma unroll
                 for (int cc = 0; cc < L::kStageRow / 64; ++cc) {
-                    float ov[32];
-                    tmem_ld32(t_o + c0 + cc * 32, ov);
+                    auto two = [&](int e) {
+                        return pack_bf16x2(__uint_as_float(ov[c0 + cc][e]) * inv, __uint_as_float(ov[c0 + cc][e + 1]) * inv);
+                    };
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        const int ch = cc * 4 + e / 8;
-                        st_shared_v4(stage + lane * L::kStageRow + ((ch ^ (lane & (kChunks - 1))) * 16),
-                                     pack_bf16x2(ov[e] * inv, ov[e + 1] * inv), pack_bf16x2(ov[e + 2] * inv, ov[e + 3] * inv),
-                                     pack_bf16x2(ov[e + 4] * inv, ov[e + 5] * inv), pack_bf16x2(ov[e + 6] * inv, ov[e + 7] * inv));
-                    }
+                    for (int e = 0; e < 32; e += 8)
+                        st_shared_v4(stage + lane * L::kStageRow + (((cc * 4 + e / 8) ^ (lane & (kChunks - 1))) * 16),
+                                     two(e), two(e + 2), two(e + 4), two(e + 6));
                 }
                 __syncwarp();
                 const int ch = lane % kChunks;
@@ -909,7 +916,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 for (int i = 0; i < 32; i += kRowsPer) {
                     const int rr = i + lane / kChunks;
                     const uint4 w = ld_shared_v4(stage + rr * L::kStageRow + ((ch ^ (rr & (kChunks - 1))) * 16));
-                    if (rr < rows) *reinterpret_cast<uint4*>(obase + rr * ot + c0 + ch * 8) = w;
+                    if (rr < rows) *reinterpret_cast<uint4*>(obase + rr * ot + c0 * 32 + ch * 8) = w;
                 }
                 __syncwarp();
             }
@@ -957,11 +964,11 @@ cudaError_t launch_tc_w(const PackedArgs& a, const CUtensorMap* maps, const Pack
 
 template <int kRows>
 cudaError_t launch_plan(const PackedArgs& a, int slots, cudaStream_t st) {
+    // most key tiles of a block: all of T, or a window's
+    const int most = a.window > 0 ? (a.window + kRows - 2) / 128 + 2 : a.T / 128 + 2;
     int shift = 0;
-    while (((a.T / kRows + 1) >> shift) >= kBins) ++shift;
-    // behind a window's length all blocks read the same number of key tiles
-    const int wb = a.window > 0 ? (a.window + kRows - 1) / kRows : INT_MAX;
-    return launch_pdl(k_packed_plan<kRows>, dim3(1), dim3(kPlanThreads), 0, st, a.cu, a.n_seq, a.T, slots, shift, wb,
+    while ((most >> shift) >= kBins) ++shift;
+    return launch_pdl(k_packed_plan<kRows>, dim3(1), dim3(kPlanThreads), 0, st, a.cu, a.n_seq, a.T, slots, shift, a.window,
                       static_cast<int*>(a.ws), reinterpret_cast<Block*>(static_cast<uint8_t*>(a.ws) + 256),
                       device_error_word());
 }
@@ -986,6 +993,9 @@ tfm_status launch_packed_attention(const PackedArgs& a, cudaStream_t st, cudaErr
     gm.by_heads = gm.group % 2 == 0;
     gm.subs = gm.by_heads ? a.H / 2 : a.H;
     gm.window = a.window;
+    auto inverse = [](int d) { return d == 1 ? 0xFFFFFFFFu : (uint32_t)(((uint64_t)1 << 32) / d); };
+    gm.subs_inv = inverse(gm.subs);
+    gm.group_inv = inverse(gm.group);
     const int slots = a.T / (gm.by_heads ? 128 : 256) + a.n_seq;
     *e = gm.by_heads ? launch_plan<128>(a, slots, st) : launch_plan<256>(a, slots, st);
     if (*e != cudaSuccess) return TFM_OK;
