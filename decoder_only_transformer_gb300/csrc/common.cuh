@@ -553,6 +553,64 @@ __device__ __forceinline__ void umma_bf16_ts_e(uint32_t d_tmem, uint32_t a_tmem,
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// A run of MMAs over K in one statement: one election, the low words of both
+// descriptors advanced by constants (the high words do not change), the first MMA
+// overwriting D unless `accumulate`, a commit to `bar` behind the last one.  As
+// separate statements an MMA cost the issuing warp ~100 cycles where two busy warps
+// share its scheduler.
+#define TFM_MMA_HEAD                                    \
+    "{\n\t.reg .pred e, p, t;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t" \
+    "elect.sync _|e, 0xffffffff;\n\t"                   \
+    "setp.ne.b32 p, %5, 0;\n\t"                         \
+    "setp.eq.b32 t, 0, 0;\n\t"
+#define TFM_MMA_SS(da, db, pred)                        \
+    "add.u32 x, %1, " #da ";\n\tadd.u32 y, %2, " #db ";\n\t" \
+    "mov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"     \
+    "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, " #pred ";\n\t"
+#define TFM_MMA_TS(da, db, pred)                        \
+    "add.u32 x, %1, " #da ";\n\tadd.u32 y, %2, " #db ";\n\t" \
+    "mov.b64 b, {y, %3};\n\t"                           \
+    "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, " #pred ";\n\t"
+#define TFM_MMA_TAIL                                    \
+    "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n\t}"
+#define TFM_MMA_ARGS(d, alo, blo, hi, idesc, acc, bar) \
+    ::"r"(d), "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "r"(acc), "r"(bar) : "memory"
+
+// S = Q K^T of d_head DH: rows of 64 columns 32 bytes (2 descriptor units) a step, the
+// second 64 columns 16 KB (1024 units) further.
+template <int DH>
+__device__ __forceinline__ void umma_scores(uint32_t d, uint32_t alo, uint32_t blo, uint32_t hi, uint32_t idesc,
+                                            uint32_t bar) {
+    if constexpr (DH == 32)
+        asm volatile(TFM_MMA_HEAD TFM_MMA_SS(0, 0, p) TFM_MMA_SS(2, 2, t) TFM_MMA_TAIL
+                         TFM_MMA_ARGS(d, alo, blo, hi, idesc, 0u, bar));
+    else if constexpr (DH == 64)
+        asm volatile(TFM_MMA_HEAD TFM_MMA_SS(0, 0, p) TFM_MMA_SS(2, 2, t) TFM_MMA_SS(4, 4, t) TFM_MMA_SS(6, 6, t)
+                         TFM_MMA_TAIL TFM_MMA_ARGS(d, alo, blo, hi, idesc, 0u, bar));
+    else
+        asm volatile(TFM_MMA_HEAD TFM_MMA_SS(0, 0, p) TFM_MMA_SS(2, 2, t) TFM_MMA_SS(4, 4, t) TFM_MMA_SS(6, 6, t)
+                         TFM_MMA_SS(1024, 1024, t) TFM_MMA_SS(1026, 1026, t) TFM_MMA_SS(1028, 1028, t)
+                             TFM_MMA_SS(1030, 1030, t) TFM_MMA_TAIL TFM_MMA_ARGS(d, alo, blo, hi, idesc, 0u, bar));
+}
+// O (+)= P V over 128 keys: P 16 keys (8 columns) a step in tensor memory, V 16 rows of
+// 128 bytes (128 descriptor units) or of 64 (64).
+template <int DH>
+__device__ __forceinline__ void umma_values(uint32_t d, uint32_t p_tmem, uint32_t blo, uint32_t hi, uint32_t idesc,
+                                            uint32_t accumulate, uint32_t bar) {
+    if constexpr (DH == 32)
+        asm volatile(TFM_MMA_HEAD TFM_MMA_TS(0, 0, p) TFM_MMA_TS(8, 64, t) TFM_MMA_TS(16, 128, t) TFM_MMA_TS(24, 192, t)
+                         TFM_MMA_TS(32, 256, t) TFM_MMA_TS(40, 320, t) TFM_MMA_TS(48, 384, t) TFM_MMA_TS(56, 448, t)
+                             TFM_MMA_TAIL TFM_MMA_ARGS(d, p_tmem, blo, hi, idesc, accumulate, bar));
+    else
+        asm volatile(TFM_MMA_HEAD TFM_MMA_TS(0, 0, p) TFM_MMA_TS(8, 128, t) TFM_MMA_TS(16, 256, t) TFM_MMA_TS(24, 384, t)
+                         TFM_MMA_TS(32, 512, t) TFM_MMA_TS(40, 640, t) TFM_MMA_TS(48, 768, t) TFM_MMA_TS(56, 896, t)
+                             TFM_MMA_TAIL TFM_MMA_ARGS(d, p_tmem, blo, hi, idesc, accumulate, bar));
+}
+#undef TFM_MMA_HEAD
+#undef TFM_MMA_SS
+#undef TFM_MMA_TS
+#undef TFM_MMA_TAIL
+#undef TFM_MMA_ARGS
 __device__ __forceinline__ void umma_commit_e(uint32_t bar) {
     asm volatile(
         "{\n\t.reg .pred e;\n\t"

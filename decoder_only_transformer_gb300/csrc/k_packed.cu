@@ -556,22 +556,6 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     const uint64_t dq = sdesc(sQ, L::kSwz, 16, L::kGroup), dk = sdesc(sK, L::kSwz, 16, L::kGroup);
     const uint64_t dv = sdesc(sV, L::kSwz, DH > 64 ? 16384 : 0, L::kGroup);
     const uint32_t tm = uniform(tmem_base);
-    auto issue_s = [&](int x, int qs, int ks) {
-        const uint64_t a0 = dq + (uint64_t)(qs * (L::kTile >> 4)), b0 = dk + (uint64_t)(ks * (L::kTile >> 4));
-#pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-            umma_bf16_e(tm + x * kKV, a0 + off, b0 + off, idesc_s, kk > 0 ? 1u : 0u);
-        }
-        umma_commit_e(s_full(x));
-    };
-    auto issue_pv = [&](int x, int vs, bool first) {
-        const uint64_t b0 = dv + (uint64_t)(vs * (L::kTile >> 4));
-#pragma unroll
-        for (int kk = 0; kk < kKV / 16; ++kk)
-            umma_bf16_ts_e(tm + L::kOCol + x * DH, tm + L::p_col(x) + kk * 8,
-                         b0 + kk * ((16 * L::kRowBytes) >> 4), idesc_o, (!first || kk > 0) ? 1u : 0u);
-    };
 
     if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
@@ -716,7 +700,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             if (!L::kAlias && cnt > 0) ok = ok && warp_wait(s_free(x), (uint32_t)(cnt - 1) & 1u, err, abort_flag);
             if (!ok) return false;
             tc_fence_after();
-            issue_s(x, qs % NQ, s);
+            umma_scores<DH>(tm + x * kKV, (uint32_t)dq + (qs % NQ) * (L::kTile >> 4), (uint32_t)dk + s * (L::kTile >> 4),
+                            (uint32_t)(dq >> 32), idesc_s, s_full(x));
             umma_commit_e(k_empty(s));
             if (j == n - 1) umma_commit_e(q_empty(qs % NQ));
             ++kn;
@@ -746,9 +731,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                     if (!ok) break;
                     ++pv;
                     tc_fence_after();
-                    issue_pv(x, s, j == pv_lo);
+                    umma_values<DH>(tm + L::kOCol + x * DH, tm + L::p_col(x), (uint32_t)dv + s * (L::kTile >> 4),
+                                    (uint32_t)(dv >> 32), idesc_o, j > pv_lo ? 1u : 0u, v_empty(s));
                     if (!L::kAlias || j == pv_n - 1) umma_commit_e(o_done(x));
-                    umma_commit_e(v_empty(s));
                 } else if (ok && lane == 0) {
                     mbar_arrive(v_empty(s));
                 }
