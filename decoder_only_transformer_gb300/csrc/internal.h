@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "tfm.h"
 
 namespace tfm {
@@ -56,6 +58,21 @@ struct EpiParams {
     float* lse_tgt;
     int lse_slots;
 };
+
+// Raises a kernel's limit of dynamic shared memory, once per device and kernel:
+// `done` is a static of the caller, a bit per device (devices from 64 on set it on
+// every launch).
+template <typename... KArgs>
+inline cudaError_t allow_smem(std::atomic<uint64_t>& done, void (*kernel)(KArgs...), int bytes) {
+    int d = 0;
+    cudaError_t e = cudaGetDevice(&d);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = d < 64 ? (uint64_t)1 << d : 0;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // Launch with programmatic stream serialization allowed (see pdl_wait in
 // common.cuh): only for kernels that call pdl_wait() before global accesses.

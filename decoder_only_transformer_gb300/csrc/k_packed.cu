@@ -258,8 +258,8 @@ __global__ void __launch_bounds__(kF32Threads, DP <= 32 ? 5 : DP == 64 ? 4 : 1) 
 
 template <int DP>
 cudaError_t launch_f32_dp(const PackedArgs& a, int slots, const PackedStrides& sd, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(k_packed_f32<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               F32Smem<DP>::kBytes);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(done, k_packed_f32<DP>, F32Smem<DP>::kBytes);
     if (e != cudaSuccess) return e;
     return launch_pdl(k_packed_f32<DP>, dim3((unsigned)slots * a.H), dim3(kF32Threads), F32Smem<DP>::kBytes, st,
                       static_cast<const float*>(a.q), static_cast<const float*>(a.k),
@@ -930,7 +930,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 template <int DH, bool kWin>
 cudaError_t launch_tc(const PackedArgs& a, const CUtensorMap* maps, const PackedGeom& gm, int slots, cudaStream_t st) {
     using L = Pk<DH>;
-    cudaError_t e = cudaFuncSetAttribute(k_packed_tc<DH, kWin>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(done, k_packed_tc<DH, kWin>, L::kBytes);
     if (e != cudaSuccess) return e;
     const int64_t items = (int64_t)slots * gm.subs;
     const int grid = items < sm_count() ? (int)items : sm_count();

@@ -832,7 +832,9 @@ template <int DH>
 cudaError_t launch_dh(const PrefixArgs& a, PrefixGeom g, const CUtensorMap* maps, cudaStream_t st) {
     using L = Px<DH>;
     const int smem = L::kBase + 4 * (3 * a.B + 2);
-    cudaError_t e = cudaFuncSetAttribute(k_prefix_part<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // room for the largest batch (two CTAs of the common sizes fit an SM all the same)
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(done, k_prefix_part<DH>, L::kBase + 4 * (3 * 4096 + 2));
     if (e != cudaSuccess) return e;
     const PrefixLayout l = layout(g, DH);
     uint8_t* w = static_cast<uint8_t*>(a.ws);

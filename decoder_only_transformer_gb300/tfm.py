@@ -516,7 +516,24 @@ def decode_attention(q, k_cache, v_cache, o, pos, workspace, window=0, scale=0.0
 
 
 # ---- batched serving: packed prompts, a shared prefix, drafted tokens
+# These calls are short, so their tensors are checked by one expression; only if it
+# does not hold are they looked at one by one, for the refusal to name the culprit.
 _Strides = ctypes.c_int64 * 8
+_torch_module = None
+
+
+def _now():
+    """The torch module and the current device's index (-2, which no tensor's is,
+    before CUDA is in use)."""
+    global _torch_module
+    if _torch_module is None:
+        _torch_module = _torch()
+    cuda = _torch_module.cuda
+    return _torch_module, cuda.current_device() if cuda.is_initialized() else -2
+
+
+def _raw_stream(stream, device):
+    return _torch_module._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def _one_device(*named):
@@ -527,12 +544,27 @@ def _one_device(*named):
             raise ValueError(f"{name}: on {t.device}, the current device is cuda:{here}")
 
 
-def _space(workspace):
-    return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
-
-
 def packed_attention_workspace_bytes(T, n_seq):
     return load().tfm_packed_attention_workspace_bytes(T, n_seq)
+
+
+def _refuse_packed(q, k, v, o, cu_seqlens, workspace):
+    for t, name in ((q, "q"), (k, "k"), (v, "v"), (o, "o")):
+        if not t.is_cuda:
+            raise ValueError(f"{name}: a CUDA tensor is required, got one on {t.device}")
+        if t.dim() != 3 or (t.numel() and t.stride(2) != 1):
+            raise ValueError(f"{name}: [T, heads, dh] with dense rows of dh is required")
+        if t.dtype != q.dtype:
+            raise TypeError(f"{name}: dtype {t.dtype}, {q.dtype} is required")
+    T, H, dh = q.shape
+    _shape(k, (T, k.shape[1], dh), "k")
+    _shape(v, k.shape, "v")
+    _shape(o, (T, H, dh), "o")
+    _dev(cu_seqlens, "cu_seqlens", _t("int32"))
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens: one dimension of n_seq + 1 offsets is required")
+    _dev(workspace, "workspace")
+    _one_device((q, "q"), (k, "k"), (v, "v"), (o, "o"), (cu_seqlens, "cu_seqlens"), (workspace, "workspace"))
 
 
 def packed_attention(q, k, v, o, cu_seqlens, workspace, window=0, scale=0.0, stream=None):
@@ -540,32 +572,52 @@ def packed_attention(q, k, v, o, cu_seqlens, workspace, window=0, scale=0.0, str
     [T, Hkv, dh] (bf16 or fp32) with dense rows of dh and any token and head
     strides; sequence b is the rows [cu_seqlens[b], cu_seqlens[b + 1]) (int32,
     device).  Query i sees keys i-window < j <= i of its sequence (0: all)."""
-    for t, name in ((q, "q"), (k, "k"), (v, "v"), (o, "o")):
-        if not t.is_cuda:
-            raise ValueError(f"{name}: a CUDA tensor is required, got one on {t.device}")
-        if t.dim() != 3 or (t.numel() and t.stride(2) != 1 and t.shape[2] != 1):
-            raise ValueError(f"{name}: [T, heads, dh] with dense rows of dh is required")
-        if t.dtype != q.dtype:
-            raise TypeError(f"{name}: dtype {t.dtype}, {q.dtype} is required")
+    lib = _lib or load()
+    torch, here = _now()
+    if not (here == q.get_device() == k.get_device() == v.get_device() == o.get_device()
+            == cu_seqlens.get_device() == workspace.get_device()
+            and q.dtype is k.dtype is v.dtype is o.dtype and cu_seqlens.dtype is torch.int32
+            and q.dim() == 3 == k.dim() and q.shape == o.shape and k.shape == v.shape
+            and q.shape[0] == k.shape[0] and q.shape[2] == k.shape[2]
+            and 1 == q.stride(2) == k.stride(2) == v.stride(2) == o.stride(2)
+            and cu_seqlens.dim() == 1 and cu_seqlens.shape[0] and cu_seqlens.is_contiguous()
+            and workspace.is_contiguous()):
+        _refuse_packed(q, k, v, o, cu_seqlens, workspace)
     T, H, dh = q.shape
-    Hkv = k.shape[1]
-    _shape(k, (T, Hkv, dh), "k")
-    _shape(v, (T, Hkv, dh), "v")
-    _shape(o, (T, H, dh), "o")
-    cp = _dev(cu_seqlens, "cu_seqlens", _t("int32"))
-    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
-        raise ValueError("cu_seqlens: one dimension of n_seq + 1 offsets is required")
-    wp, nbytes = _space(workspace)
-    _one_device((q, "q"), (k, "k"), (v, "v"), (o, "o"), (cu_seqlens, "cu_seqlens"), (workspace, "workspace"))
-    strides = _Strides(q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
-                       o.stride(0), o.stride(1))
-    _check(load().tfm_packed_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), cp,
-                                       cu_seqlens.shape[0] - 1, T, H, Hkv, dh, strides, scale,
-                                       int(window), _mode_of(q), wp, nbytes, _stream(stream)))
+    strides = _Strides(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *o.stride()[:2])
+    status = lib.tfm_packed_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                      cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1, T, H, k.shape[1], dh,
+                                      strides, scale, window, _mode_of(q), workspace.data_ptr(),
+                                      workspace.nbytes, _raw_stream(stream, here))
+    if status:
+        _check(status)
 
 
 def prefix_attention_workspace_bytes(B, H, Hkv, T, dh):
     return load().tfm_prefix_attention_workspace_bytes(B, H, Hkv, T, dh)
+
+
+def _refuse_prefix(q, k_prefix, v_prefix, k_cache, v_cache, o, lens, workspace):
+    bf = _t("bfloat16")
+    _dev(q, "q", bf)
+    if q.dim() != 4:
+        raise ValueError("q: [B, H, T, dh] is required")
+    B, H, T, dh = q.shape
+    for t, name in ((k_prefix, "k_prefix"), (v_prefix, "v_prefix"), (k_cache, "k_cache"), (v_cache, "v_cache")):
+        _dev(t, name, bf)
+    if k_cache.dim() != 4 or k_cache.shape[0] < B or k_cache.shape[3] != dh:
+        raise ValueError(f"k_cache: shape {tuple(k_cache.shape)} does not hold {B} sequences of d_head {dh}")
+    _shape(v_cache, k_cache.shape, "v_cache")
+    if k_prefix.dim() != 3 or k_prefix.shape[0] != k_cache.shape[1] or k_prefix.shape[2] != dh:
+        raise ValueError(f"k_prefix: shape {tuple(k_prefix.shape)}, ({k_cache.shape[1]}, max_prefix, {dh}) is required")
+    _shape(v_prefix, k_prefix.shape, "v_prefix")
+    _numel(lens, B, "lens")
+    _dev(lens, "lens", _t("int32"))
+    _numel(o, B * T * H * dh, "o")
+    _dev(o, "o", bf)
+    _dev(workspace, "workspace")
+    _one_device((q, "q"), (k_prefix, "k_prefix"), (v_prefix, "v_prefix"), (k_cache, "k_cache"),
+                (v_cache, "v_cache"), (o, "o"), (lens, "lens"), (workspace, "workspace"))
 
 
 def prefix_attention(q, k_prefix, v_prefix, k_cache, v_cache, o, lens, workspace, prefix_len=None,
@@ -574,35 +626,67 @@ def prefix_attention(q, k_prefix, v_prefix, k_cache, v_cache, o, lens, workspace
     prefix [Hkv, max_prefix, dh] (its first prefix_len positions; default all)
     and each sequence's own cache [B, Hkv, max_seq, dh] of lens[b] positions
     (int32, device), the T new ones the last; o [B, T, H*dh]; all bf16."""
-    bf = _t("bfloat16")
-    qp = _dev(q, "q", bf)
-    if q.dim() != 4:
-        raise ValueError("q: [B, H, T, dh] is required")
+    lib = _lib or load()
+    torch, here = _now()
+    bf = torch.bfloat16
+    if not (here == q.get_device() == k_prefix.get_device() == v_prefix.get_device() == k_cache.get_device()
+            == v_cache.get_device() == o.get_device() == lens.get_device() == workspace.get_device()
+            and bf is q.dtype is k_prefix.dtype is v_prefix.dtype is k_cache.dtype is v_cache.dtype is o.dtype
+            and lens.dtype is torch.int32 and q.dim() == 4 == k_cache.dim() and k_prefix.dim() == 3
+            and k_cache.shape == v_cache.shape and k_prefix.shape == v_prefix.shape
+            and k_cache.shape[0] >= q.shape[0] and k_cache.shape[3] == q.shape[3] == k_prefix.shape[2]
+            and k_prefix.shape[0] == k_cache.shape[1] and lens.numel() == q.shape[0] and o.numel() == q.numel()
+            and q.is_contiguous() and k_prefix.is_contiguous() and v_prefix.is_contiguous()
+            and k_cache.is_contiguous() and v_cache.is_contiguous() and o.is_contiguous()
+            and lens.is_contiguous() and workspace.is_contiguous()):
+        _refuse_prefix(q, k_prefix, v_prefix, k_cache, v_cache, o, lens, workspace)
     B, H, T, dh = q.shape
-    ptrs = [_dev(t, name, bf) for t, name in ((k_prefix, "k_prefix"), (v_prefix, "v_prefix"),
-                                              (k_cache, "k_cache"), (v_cache, "v_cache"))]
-    if k_cache.dim() != 4 or k_cache.shape[0] < B or k_cache.shape[3] != dh:
-        raise ValueError(f"k_cache: shape {tuple(k_cache.shape)} does not hold {B} sequences of d_head {dh}")
-    Hkv, max_seq = k_cache.shape[1], k_cache.shape[2]
-    _shape(v_cache, k_cache.shape, "v_cache")
-    if k_prefix.dim() != 3 or k_prefix.shape[0] != Hkv or k_prefix.shape[2] != dh:
-        raise ValueError(f"k_prefix: shape {tuple(k_prefix.shape)}, ({Hkv}, max_prefix, {dh}) is required")
-    _shape(v_prefix, k_prefix.shape, "v_prefix")
-    _numel(lens, B, "lens")
-    lp = _dev(lens, "lens", _t("int32"))
-    _numel(o, B * T * H * dh, "o")
-    op = _dev(o, "o", bf)
-    wp, nbytes = _space(workspace)
-    _one_device((q, "q"), (k_prefix, "k_prefix"), (v_prefix, "v_prefix"), (k_cache, "k_cache"),
-                (v_cache, "v_cache"), (o, "o"), (lens, "lens"), (workspace, "workspace"))
+    _, Hkv, max_seq, _ = k_cache.shape
     max_prefix = k_prefix.shape[1]
-    _check(load().tfm_prefix_attention(qp, *ptrs, op, lp, B, H, Hkv, T,
-                                       max_prefix if prefix_len is None else int(prefix_len),
-                                       max_prefix, max_seq, dh, scale, wp, nbytes, _stream(stream)))
+    status = lib.tfm_prefix_attention(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(),
+                                      v_cache.data_ptr(), o.data_ptr(), lens.data_ptr(), B, H, Hkv, T,
+                                      max_prefix if prefix_len is None else prefix_len, max_prefix, max_seq, dh,
+                                      scale, workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, here))
+    if status:
+        _check(status)
 
 
 def verify_draft_workspace_bytes(B, K, V):
     return load().tfm_verify_draft_workspace_bytes(B, K, V)
+
+
+def _refuse_verify(target, draft_logits, draft, n_draft, u, noise, vocab, tokens, n_accepted, workspace, greedy):
+    f32, i32 = _t("float32"), _t("int32")
+    if draft.dim() != 2:
+        raise ValueError("draft: [B, K] is required")
+    B, K = draft.shape
+    _dev(draft, "draft", i32)
+    for t, name, rows, must in ((target, "target", B * (K + 1), True),
+                                (draft_logits, "draft_logits", B * K, not greedy and K > 0),
+                                (noise, "noise", B, not greedy)):
+        if t is None:
+            if must:
+                raise ValueError(f"{name}: required unless temperature is 0")
+            continue
+        _dev(t, name, f32, rows=True)
+        if t.shape[0] < rows or t.shape[1] < vocab:
+            raise ValueError(f"{name}: {rows} rows of at least {vocab} columns are required, got {tuple(t.shape)}")
+    if u is not None:
+        _numel(u, B * K, "u")
+        _dev(u, "u", f32)
+    elif not greedy and K:
+        raise ValueError("u: required unless temperature is 0")
+    if n_draft is not None:
+        _numel(n_draft, B, "n_draft")
+        _dev(n_draft, "n_draft", i32)
+    _numel(tokens, B * (K + 1), "tokens")
+    _numel(n_accepted, B, "n_accepted")
+    _dev(tokens, "tokens", i32)
+    _dev(n_accepted, "n_accepted", i32)
+    _dev(workspace, "workspace")
+    _one_device((target, "target"), (draft_logits, "draft_logits"), (draft, "draft"), (n_draft, "n_draft"),
+                (u, "u"), (noise, "noise"), (tokens, "tokens"), (n_accepted, "n_accepted"),
+                (workspace, "workspace"))
 
 
 def verify_draft(target, draft_logits, draft, n_draft, u, noise, vocab, tokens, n_accepted,
@@ -613,43 +697,40 @@ def verify_draft(target, draft_logits, draft, n_draft, u, noise, vocab, tokens, 
     numbers noise [B, >= vocab] (fp32); writes tokens [B, K+1] (the accepted
     ones, the new one, -1) and n_accepted [B].  temperature 0 is greedy, and
     draft_logits, u and noise may be None."""
-    f32, i32 = _t("float32"), _t("int32")
-    if draft.dim() != 2:
-        raise ValueError("draft: [B, K] is required")
-    B, K = draft.shape
-    dp = _dev(draft, "draft", i32)
+    lib = _lib or load()
+    torch, here = _now()
+    f32, i32 = torch.float32, torch.int32
     greedy = temperature == 0
-    checked = []
-    for t, name, rows, must in ((target, "target", B * (K + 1), True),
-                                (draft_logits, "draft_logits", B * K, not greedy and K > 0),
-                                (noise, "noise", B, not greedy)):
-        if t is None:
-            if must:
-                raise ValueError(f"{name}: required unless temperature is 0")
-            checked.append((None, 0))
-            continue
-        ptr = _dev(t, name, f32, rows=True)
-        if t.shape[0] < rows or t.shape[1] < vocab:
-            raise ValueError(f"{name}: {rows} rows of at least {vocab} columns are required, got {tuple(t.shape)}")
-        checked.append((ptr, t.stride(0)))
-    (tp, ldt), (lp, ldd), (zp, ldn) = checked
-    if u is None:
-        if not greedy and K:
-            raise ValueError("u: required unless temperature is 0")
-    else:
-        _numel(u, B * K, "u")
-    if n_draft is not None:
-        _numel(n_draft, B, "n_draft")
-    _numel(tokens, B * (K + 1), "tokens")
-    _numel(n_accepted, B, "n_accepted")
-    up, np_ = _dev(u, "u", f32), _dev(n_draft, "n_draft", i32)
-    op, ap = _dev(tokens, "tokens", i32), _dev(n_accepted, "n_accepted", i32)
-    wp, nbytes = _space(workspace)
-    _one_device((target, "target"), (draft_logits, "draft_logits"), (draft, "draft"), (n_draft, "n_draft"),
-                (u, "u"), (noise, "noise"), (tokens, "tokens"), (n_accepted, "n_accepted"),
-                (workspace, "workspace"))
-    _check(load().tfm_verify_draft(tp, ldt, lp, ldd, dp, np_, up, zp, ldn, B, K, int(vocab),
-                                   float(temperature), op, ap, wp, nbytes, _stream(stream)))
+    if greedy or not (
+            draft_logits is not None and u is not None and noise is not None
+            and here == target.get_device() == draft_logits.get_device() == draft.get_device() == u.get_device()
+            == noise.get_device() == tokens.get_device() == n_accepted.get_device() == workspace.get_device()
+            and f32 is target.dtype is draft_logits.dtype is u.dtype is noise.dtype
+            and i32 is draft.dtype is tokens.dtype is n_accepted.dtype
+            and 2 == draft.dim() == target.dim() == draft_logits.dim() == noise.dim()
+            and 1 == target.stride(1) == draft_logits.stride(1) == noise.stride(1)
+            and target.shape[0] >= draft.shape[0] * (draft.shape[1] + 1) and draft_logits.shape[0] >= draft.numel()
+            and noise.shape[0] >= draft.shape[0]
+            and min(target.shape[1], draft_logits.shape[1], noise.shape[1]) >= vocab
+            and u.numel() == draft.numel() and tokens.numel() == draft.shape[0] * (draft.shape[1] + 1)
+            and n_accepted.numel() == draft.shape[0]
+            and draft.is_contiguous() and u.is_contiguous() and tokens.is_contiguous()
+            and n_accepted.is_contiguous() and workspace.is_contiguous()
+            and (n_draft is None or (n_draft.get_device() == here and n_draft.dtype is i32
+                                     and n_draft.numel() == draft.shape[0] and n_draft.is_contiguous()))):
+        _refuse_verify(target, draft_logits, draft, n_draft, u, noise, vocab, tokens, n_accepted, workspace, greedy)
+    B, K = draft.shape
+
+    def at(t):
+        return None if t is None else t.data_ptr()
+
+    status = lib.tfm_verify_draft(target.data_ptr(), target.stride(0), at(draft_logits),
+                                  0 if draft_logits is None else draft_logits.stride(0), draft.data_ptr(),
+                                  at(n_draft), at(u), at(noise), 0 if noise is None else noise.stride(0), B, K,
+                                  vocab, temperature, tokens.data_ptr(), n_accepted.data_ptr(),
+                                  workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, here))
+    if status:
+        _check(status)
 
 
 def linear(x, W, y, accumulate=False, stream=None):
