@@ -43,7 +43,7 @@ tfm_status tfm_packed_attention(const void* q, const void* k, const void* v, voi
     if (T < 0 || T > (1 << 30) || n_seq < 0 || n_seq > (1 << 20))
         return fail(TFM_EINVAL, "T=%d outside [0, 2^30] or n_seq=%d outside [0, 2^20]", T, n_seq);
     if (H < 1 || Hkv < 1 || H % Hkv) return fail(TFM_EINVAL, "bad head counts");
-    if (((int64_t)T / 32 + n_seq) * H >= (int64_t)1 << 31) return fail(TFM_EINVAL, "(T / 32 + n_seq) * H too large");
+    if (((int64_t)T / 32 + n_seq) * H > (int64_t)1 << 30) return fail(TFM_EINVAL, "(T / 32 + n_seq) * H too large");
     if (mode != TFM_FP32 && mode != TFM_BF16) return fail(TFM_EINVAL, "bad mode");
     if (window < 0) return fail(TFM_EINVAL, "window must be >= 0");
     if (!std::isfinite(scale)) return fail(TFM_EINVAL, "scale must be finite");
@@ -161,7 +161,7 @@ tfm_status tfm_prefix_attention(const void* q, const void* k_prefix, const void*
 }
 
 static bool verify_sizes_ok(int32_t B, int32_t K, int32_t V) {
-    return B >= 0 && K >= 0 && K <= 64 && V >= 1 && V <= (1 << 30) && (int64_t)B * (K + 1) <= (1 << 20) &&
+    return B >= 0 && K >= 0 && K <= 64 && V >= 1 && V <= (1 << 24) && (int64_t)B * (K + 1) <= (1 << 20) &&
            tfm::verify_workspace_bytes(B, K, V) < (size_t)1 << 33;   // and so its grids below 2^31 CTAs
 }
 
@@ -176,9 +176,10 @@ tfm_status tfm_verify_draft(const float* target, int64_t ld_target, const float*
                             int32_t* n_accepted, void* workspace, size_t workspace_bytes,
                             void* stream) {
     if (!verify_sizes_ok(B, K, V))
-        return fail(TFM_EINVAL, "bad sizes: B >= 0, 0 <= K <= 64, V >= 1, B*(K+1) <= 2^20, B*(2K+1)*V/4096 < 2^30");
-    if (!(temperature >= 0.f) || !std::isfinite(temperature))
-        return fail(TFM_EINVAL, "temperature must be finite and not negative");
+        return fail(TFM_EINVAL, "bad sizes: B >= 0, 0 <= K <= 64, 1 <= V <= 2^24, B*(K+1) <= 2^20, B*(2K+1)*V/4096 < 2^30");
+    // outside, log2(e) / temperature or a difference of logits leaves fp32's range
+    if (temperature != 0.f && !(temperature >= 1e-30f && temperature <= 1e30f))
+        return fail(TFM_EINVAL, "temperature must be 0 or in [1e-30, 1e30]");
     const bool greedy = temperature == 0.f;
     if (ld_target < V || ld_target % 4) return fail(TFM_EINVAL, "ld_target must be >= V and a multiple of 4");
     if (!greedy && ((K && (ld_draft < V || ld_draft % 4)) || ld_noise < V || ld_noise % 4))

@@ -41,8 +41,9 @@ constexpr int kMaxK = 64;
 // Relative error of an fp32 weight e^((z - m) / temperature): the exponent
 // x = (z - m) log2(e) / temperature carries three roundings, 3 * 2^-24 |x|, so
 // the weight 0.7 * 3 * 2^-24 |x| <= 1.6e-5 down to the smallest normal number
-// (|x| = 126); the sums and the exponential itself stay below 1e-6.
-constexpr float kEps = 2e-5f;
+// (|x| = 126).  A row's sum has 20 roundings within a chunk and up to 64 over the chunks of
+// 2^24 logits, 5e-6; the exponential, the divisions and the product with 1 / noise stay below 1e-6.
+constexpr float kEps = 2.5e-5f;
 
 struct __align__(16) Cand {
     float lo, hi;      // bounds of weight / noise

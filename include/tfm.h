@@ -448,9 +448,9 @@ tfm_status tfm_decode_attention(const void* q, const void* k_cache, const void* 
  * the head-major q, k, v of tfm_rope and tfm_causal_attention ([H, T, dh]) and
  * the columns of one fused [T, (H + 2 Hkv) dh] projection are read in place.
  * Strides are at least dh (a dimension of one row or head excepted), multiples
- * of 16 bytes and below 2^39 bytes; o's rows must not overlap.  bf16 mode: dh in {32, 64, 128};
+ * of 16 bytes and below 2^39 bytes; o's rows must not overlap each other or an input.  bf16 mode: dh in {32, 64, 128};
  * fp32 mode: dh % 4 == 0, dh <= 128.  T <= 2^30, n_seq <= 2^20,
- * (T / 32 + n_seq) * H < 2^31.  scale <= 0 means 1/sqrt(dh); it must be finite.
+ * (T / 32 + n_seq) * H <= 2^30.  scale <= 0 means 1/sqrt(dh); it must be finite.
  * Pointers 16-byte aligned, cu_seqlens 4-byte.  workspace: device, 16-byte
  * aligned, tfm_packed_attention_workspace_bytes(T, n_seq) bytes (0 for bad
  * sizes), not used by another call in flight; its contents need not survive.
@@ -516,8 +516,8 @@ tfm_status tfm_prefix_attention(const void* q, const void* k_prefix, const void*
  * sets TFM_EINVAL in the device error word and is clamped; a drafted id outside
  * [0, V) sets TFM_EBADTOKEN and is refused.  V >= 1, 0 <= K <= 64, leading
  * dimensions >= V and multiples of 4, logits and noise 16-byte aligned, the rest
- * 4-byte, V <= 2^30, B * (K + 1) <= 2^20, B * (2K + 1) * V / 4096 < 2^30,
- * 0 <= temperature < infinity.
+ * 4-byte, V <= 2^24, B * (K + 1) <= 2^20, B * (2K + 1) * V / 4096 < 2^30,
+ * temperature 0 or in [1e-30, 1e30].
  * workspace: device, 16-byte aligned, tfm_verify_draft_workspace_bytes(B, K, V)
  * bytes (0 for bad sizes), not used by another call in flight.  Results do not
  * depend on timing; capturable in a CUDA graph. */

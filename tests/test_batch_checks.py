@@ -165,3 +165,14 @@ def test_binding_refuses_host_tensors_and_wrong_layouts():
     for call in calls:
         with pytest.raises(ValueError, match="CUDA tensor"):
             call()
+
+
+@pytest.mark.parametrize("call,kw,status", [
+    (_verify, dict(temp=1e-31), E), (_verify, dict(temp=1e31), E),
+    (_verify, dict(V=(1 << 24) + 1, ldt=1 << 25, ldd=1 << 25, ldn=1 << 25), E),
+    (_packed, dict(T=1, n_seq=1, H=(1 << 30) + 2, strides=None), E),      # items beyond int32 less a grid
+    (_packed, dict(T=0, n_seq=1 << 20, H=1024, Hkv=1024, strides=None), OK),
+    (_packed, dict(T=0, n_seq=1 << 20, H=1026, Hkv=2, strides=None), E),
+])
+def test_limits_of_the_arithmetic(lib, call, kw, status):
+    assert call(lib, **kw) == status, lib.tfm_last_error()
