@@ -665,10 +665,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         // ---------------------------------------------------------- MMAs (warp 1: tile A, warp 2: tile B)
         // A warp per tile: each runs at the pace of its own softmax, and the two
         // pipelines drift into the phase in which one's exponentials run beside the
-        // other's products (issued by one warp in the order A, B, A, ..., each
-        // waited for the other: d_head 64, 8192 tokens, 2400 cycles per pair of tiles
-        // instead of TODO).  A round is a key tile of the item; a tile that this
-        // warp's queries do not see is passed on unread.
+        // other's products (issued by one warp in the order A, B, A, ..., each waited for
+        // the other: 46 us instead of 40 for 24 prompts of up to 1024 tokens at 12 x 64).
+        // A round is a key tile of the item; a tile that this warp's queries do not see is
+        // passed on unread.
         // P in columns of its own: S of the next round as soon as the softmax has
         // read this one's.  P in the place of S (d_head 128): behind this round's P.V,
         // as MMAs of one thread complete in the order they are issued.
