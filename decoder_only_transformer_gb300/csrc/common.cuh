@@ -112,6 +112,31 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* er
     return __all_sync(0xffffffffu, ok);
 }
 
+// The same for a warp whose loop is short beside that of the warps it shares a scheduler
+// with (and is fetched anew every time): a few instructions, the bounded wait out of line.
+static __device__ __noinline__ bool warp_wait_long(uint32_t bar, uint32_t parity, int* err, volatile int* abort) {
+    return warp_wait(bar, parity, err, abort);
+}
+__device__ __forceinline__ bool warp_wait_short(uint32_t bar, uint32_t parity, int* err, volatile int* abort) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, 64;\n\t"
+        "WAIT:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2;\n\t"
+        "vote.sync.all.pred p, q, 0xffffffff;\n\t"
+        "@p bra DONE;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 q, n, 0;\n\t"
+        "@q bra WAIT;\n\t"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok ? true : warp_wait_long(bar, parity, err, abort);
+}
+
 // ------------------------------------------------------------------ TMA
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int32_t x,
                                             int32_t y, uint32_t bar) {
@@ -576,8 +601,9 @@ __device__ __forceinline__ void umma_bf16_ts_e(uint32_t d_tmem, uint32_t a_tmem,
 #define TFM_MMA_ARGS(d, alo, blo, hi, idesc, acc, bar) \
     ::"r"(d), "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "r"(acc), "r"(bar) : "memory"
 
-// S = Q K^T of d_head DH: rows of 64 columns 32 bytes (2 descriptor units) a step, the
-// second 64 columns 16 KB (1024 units) further.
+// S = Q K^T of d_head DH, 128 rows against 64 keys: rows of 64 columns 32 bytes (2
+// descriptor units) a step, the second 64 columns 16 KB (1024 units) further in Q and
+// 8 KB in K.
 template <int DH>
 __device__ __forceinline__ void umma_scores(uint32_t d, uint32_t alo, uint32_t blo, uint32_t hi, uint32_t idesc,
                                             uint32_t bar) {
@@ -589,22 +615,20 @@ __device__ __forceinline__ void umma_scores(uint32_t d, uint32_t alo, uint32_t b
                          TFM_MMA_TAIL TFM_MMA_ARGS(d, alo, blo, hi, idesc, 0u, bar));
     else
         asm volatile(TFM_MMA_HEAD TFM_MMA_SS(0, 0, p) TFM_MMA_SS(2, 2, t) TFM_MMA_SS(4, 4, t) TFM_MMA_SS(6, 6, t)
-                         TFM_MMA_SS(1024, 1024, t) TFM_MMA_SS(1026, 1026, t) TFM_MMA_SS(1028, 1028, t)
-                             TFM_MMA_SS(1030, 1030, t) TFM_MMA_TAIL TFM_MMA_ARGS(d, alo, blo, hi, idesc, 0u, bar));
+                         TFM_MMA_SS(1024, 512, t) TFM_MMA_SS(1026, 514, t) TFM_MMA_SS(1028, 516, t)
+                             TFM_MMA_SS(1030, 518, t) TFM_MMA_TAIL TFM_MMA_ARGS(d, alo, blo, hi, idesc, 0u, bar));
 }
-// O (+)= P V over 128 keys: P 16 keys (8 columns) a step in tensor memory, V 16 rows of
+// O (+)= P V over 64 keys: P 16 keys (8 columns) a step in tensor memory, V 16 rows of
 // 128 bytes (128 descriptor units) or of 64 (64).
 template <int DH>
 __device__ __forceinline__ void umma_values(uint32_t d, uint32_t p_tmem, uint32_t blo, uint32_t hi, uint32_t idesc,
                                             uint32_t accumulate, uint32_t bar) {
     if constexpr (DH == 32)
         asm volatile(TFM_MMA_HEAD TFM_MMA_TS(0, 0, p) TFM_MMA_TS(8, 64, t) TFM_MMA_TS(16, 128, t) TFM_MMA_TS(24, 192, t)
-                         TFM_MMA_TS(32, 256, t) TFM_MMA_TS(40, 320, t) TFM_MMA_TS(48, 384, t) TFM_MMA_TS(56, 448, t)
-                             TFM_MMA_TAIL TFM_MMA_ARGS(d, p_tmem, blo, hi, idesc, accumulate, bar));
+                         TFM_MMA_TAIL TFM_MMA_ARGS(d, p_tmem, blo, hi, idesc, accumulate, bar));
     else
         asm volatile(TFM_MMA_HEAD TFM_MMA_TS(0, 0, p) TFM_MMA_TS(8, 128, t) TFM_MMA_TS(16, 256, t) TFM_MMA_TS(24, 384, t)
-                         TFM_MMA_TS(32, 512, t) TFM_MMA_TS(40, 640, t) TFM_MMA_TS(48, 768, t) TFM_MMA_TS(56, 896, t)
-                             TFM_MMA_TAIL TFM_MMA_ARGS(d, p_tmem, blo, hi, idesc, accumulate, bar));
+                         TFM_MMA_TAIL TFM_MMA_ARGS(d, p_tmem, blo, hi, idesc, accumulate, bar));
 }
 #undef TFM_MMA_HEAD
 #undef TFM_MMA_SS

@@ -17,8 +17,7 @@ namespace {
 struct SeqRange {
     int start, len;
 };
-__device__ __forceinline__ SeqRange seq_range(const int32_t* __restrict__ cu, int b, int T) {
-    const int s = __ldg(cu + b), e = __ldg(cu + b + 1);
+__device__ __forceinline__ SeqRange seq_range(int s, int e, int T) {
     const bool ok = s >= 0 && s <= e && e <= T;
     return SeqRange{ok ? s : 0, ok ? e - s : 0};
 }
@@ -96,7 +95,7 @@ __global__ void __launch_bounds__(kF32Threads, DP <= 32 ? 5 : DP == 64 ? 4 : 1) 
     const int slot = slots - 1 - (int)(blockIdx.x / (unsigned)H), h = (int)(blockIdx.x % (unsigned)H), g = h / group;
     const int b = sequence_of<kF32Rows>(cu, n_seq, slot);
     if (b < 0) return;
-    const SeqRange sr = seq_range(cu, b, T);
+    const SeqRange sr = seq_range(__ldg(cu + b), __ldg(cu + b + 1), T);
     const int row0 = (slot - (sr.start / kF32Rows + b)) * kF32Rows;
     if (row0 < 0 || row0 >= sr.len) return;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
@@ -293,6 +292,7 @@ cudaError_t launch_f32(const PackedArgs& a, cudaStream_t st) {
 // grows with b.  A counting sort over at most 1024 length classes then orders them.
 constexpr int kPlanThreads = 1024;
 constexpr int kBins = 1024;
+constexpr int kPlanCache = 4096;        // offsets kept in shared memory
 
 struct __align__(16) Block {
     int start, len;    // rows of the sequence
@@ -309,25 +309,32 @@ __global__ void __launch_bounds__(kPlanThreads) k_packed_plan(const int32_t* __r
                                                               Block* __restrict__ list, int* err) {
     __shared__ int bins[kBins];
     __shared__ int warp_sum[kPlanThreads / 32];
+    __shared__ int cached[kPlanCache];
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     bins[tid] = 0;
+    // the searches read shared memory, if the offsets fit: a trip to L2 per probe made
+    // most of this kernel
+    const bool in_smem = n_seq < kPlanCache;
+    if (in_smem)
+        for (int b = tid; b <= n_seq; b += kPlanThreads) cached[b] = __ldg(cu + b);
+    __syncthreads();
+    auto offset = [&](int b) { return in_smem ? cached[b] : __ldg(cu + b); };
     for (int b = tid; b < n_seq; b += kPlanThreads) {
-        const int s = __ldg(cu + b), e = __ldg(cu + b + 1);
+        const int s = offset(b), e = offset(b + 1);
         if (s < 0 || s > e || e > T) raise_error(err, TFM_EINVAL);
     }
-    __syncthreads();
     // block of slot s, and its length class; false: the slot is empty
     auto find = [&](int s, Block& blk, int& bin) -> bool {
         int lo = 0, hi = n_seq;                       // the last b with cu[b] / kRows + b <= s
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
-            if (__ldg(cu + mid) / kRows + mid <= s) lo = mid + 1; else hi = mid;
+            if (offset(mid) / kRows + mid <= s) lo = mid + 1; else hi = mid;
         }
         if (lo == 0) return false;
         const int b = lo - 1;
-        const SeqRange r = seq_range(cu, b, T);
+        const SeqRange r = seq_range(offset(b), offset(b + 1), T);
         const int t = s - (r.start / kRows + b);
         if (t < 0 || (int64_t)t * kRows >= r.len) return false;
         const int rowA = t * kRows, rowB = kRows == 128 ? rowA : rowA + 128;
@@ -338,10 +345,15 @@ __global__ void __launch_bounds__(kPlanThreads) k_packed_plan(const int32_t* __r
         bin = kBins - 1 - ((max(blk.n0, blk.n1) - 1) >> shift);
         return true;
     };
+    // Counted, then placed; what a thread finds last it keeps, which is all there is to
+    // find up to 1024 slots.
     Block blk;
     int bin;
-    for (int s = tid; s < slots; s += kPlanThreads)
-        if (find(s, blk, bin)) atomicAdd(&bins[bin], 1);
+    bool found = false;
+    for (int s = tid; s < slots; s += kPlanThreads) {
+        found = find(s, blk, bin);
+        if (found) atomicAdd(&bins[bin], 1);
+    }
     __syncthreads();
     // exclusive sums of the classes' counts
     const int n = bins[tid];
@@ -358,44 +370,54 @@ __global__ void __launch_bounds__(kPlanThreads) k_packed_plan(const int32_t* __r
     bins[tid] = before + sum - n;
     if (tid == kPlanThreads - 1) *count = before + sum;
     __syncthreads();
-    for (int s = tid; s < slots; s += kPlanThreads)
+    if (found) list[atomicAdd(&bins[bin], 1)] = blk;
+    for (int s = tid; s + kPlanThreads < slots; s += kPlanThreads)
         if (find(s, blk, bin)) list[atomicAdd(&bins[bin], 1)] = blk;
 }
 
 // ------------------------------------------------------------------ tensor cores
+// A persistent CTA per SM: a TMA warp, an MMA warp per query tile, a warp that checks V, and
+// four softmax warps per query tile, a row a thread.  S = Q K^T and O += P V on tcgen05, S, P
+// and O in tensor memory.  Key tiles of 64 with two places for S per query tile, P in the place
+// of S: the softmax of one tile runs beside the products of the next, and a diagonal tile
+// is half as wide.  (Tiles of 128 with one place: 12 prompts of up to 2048 at 16/4 x 128 90 us
+// instead of 77, 24 of up to 1024 at 12 x 64 35.5 instead of 32.5; 3 of up to 8192 at
+// 12 x 64 the same 168.)  What bounds it is latency, of softmax and MMA warps alike: at
+// d_head 64 a pair of tiles takes 1210 cycles, of them ~510 the exponentials of both on
+// the MUFU, ~550 the tensor pipe; without exponentials it takes 960, without any
+// arithmetic of the softmax 860, and with a quarter of the MMAs besides 690.  (Two CTAs per
+// SM, one place for S each and 96 registers a softmax thread: 173 us instead of 168.)
 constexpr int kQ = 128;
-constexpr int kKV = 128;
 constexpr int kThreadsP = 384;          // control, softmax of tile A, softmax of tile B
+constexpr int kKV = 64;                 // keys per tile
 constexpr float kRescale = 8.0f;        // log2 units: P entries stay below 2^8
 constexpr int kPoison = 8;
 
 template <int DH>
 struct Pk {
-    // d_head 128: S and O of two tiles fill tensor memory, P takes the place of S
-    static constexpr bool kAlias = DH == 128;
     static constexpr int kRowBytes = DH >= 64 ? 128 : 64;   // of a shared-memory tile
     static constexpr int kSub = DH / 64 > 1 ? DH / 64 : 1;  // 64-column sub-tiles
-    static constexpr int kTile = kQ * DH * 2;               // bytes of a Q, K or V tile
+    static constexpr int kQTile = kQ * DH * 2;              // bytes of a Q tile
+    static constexpr int kTile = kKV * DH * 2;              // of a K or V tile
+    static constexpr int kSubQ = kQ * 128, kSubKV = kKV * 128;      // of their sub-tiles
     static constexpr int kNQ = DH == 128 ? 2 : 4;
-    static constexpr int kSK = DH == 128 ? 2 : (DH == 64 ? 4 : 6);
-    static constexpr int kSV = kSK;
-    static constexpr int kKOff = kNQ * kTile;
-    static constexpr int kVOff = kKOff + kSK * kTile;
+    static constexpr int kRing = DH == 128 ? 4 : 8;         // slots of a K and a V tile
+    static constexpr int kKOff = kNQ * kQTile;
+    static constexpr int kVOff = kKOff + kRing * kTile;
     // output rows of a softmax warp, 64 columns at a time
     static constexpr int kStageRow = DH >= 64 ? 128 : 64;
     static constexpr int kStage = 32 * kStageRow;
-    static constexpr int kStageOff = kVOff + kSV * kTile;
+    static constexpr int kStageOff = kVOff + kRing * kTile;
     static constexpr int kBarOff = kStageOff + 8 * kStage;
-    static constexpr int kNumBars = 2 * (kNQ + kSK + kSV) + kSV + 9;
+    static constexpr int kNumBars = 2 * kNQ + 3 * kRing + 13;
     static constexpr int kMiscOff = kBarOff + 8 * kNumBars;
     static constexpr int kBytes = kMiscOff + 16 + 4 * kPoison + 1024;
-    // tensor-memory columns: S (2 x 128), O (2 x DH), P (2 x 64, or in S's place)
-    static constexpr int kOCol = 2 * kKV;
-    __host__ __device__ static constexpr int p_col(int x) { return kAlias ? x * kKV : kOCol + 2 * DH + x * (kKV / 2); }
+    // tensor-memory columns: S (2 x 2 x 64, P in its place), O (2 x DH)
+    static constexpr int kOCol = 4 * kKV;
     static constexpr uint32_t kSwz = DH == 32 ? 4u : 2u;
     static constexpr uint32_t kGroup = 8 * kRowBytes;
     static_assert(kBytes <= 232448, "shared memory budget");
-    static_assert(kAlias ? kOCol + 2 * DH <= 512 : p_col(1) + kKV / 2 <= 512, "tensor memory budget");
+    static_assert(kOCol + 2 * DH <= 512, "tensor memory budget");
 };
 
 // Both tiles of an item read key tiles j0 + j, j in [0, nmax); tile x those with
@@ -419,6 +441,7 @@ __device__ __forceinline__ int div_by(int x, int d, uint32_t inv) {
 }
 
 __device__ __forceinline__ void make_item(Item& it, const int4 a, const int4 b, int sub, const PackedGeom& gm) {
+    constexpr int kPer = 128 / kKV;                    // a block's entry counts in 128 keys
     it.start = a.x;
     it.len = a.y;
     it.row[0] = a.z;
@@ -426,12 +449,12 @@ __device__ __forceinline__ void make_item(Item& it, const int4 a, const int4 b, 
     it.h[0] = gm.by_heads ? 2 * sub : sub;
     it.h[1] = gm.by_heads ? it.h[0] + 1 : sub;
     it.g = div_by(it.h[0], gm.group, gm.group_inv);
-    it.j0 = a.w;
+    it.j0 = a.w * kPer;
     it.lo[0] = 0;
-    it.lo[1] = b.z;
-    it.n[0] = b.x;
-    it.n[1] = b.y;
-    it.nmax = b.y > b.x ? b.y : b.x;
+    it.lo[1] = b.z * kPer;
+    it.n[0] = b.x * kPer;
+    it.n[1] = b.y * kPer;
+    it.nmax = it.n[1] > it.n[0] ? it.n[1] : it.n[0];
 }
 
 // Whether key tile j of the item holds a key that some row of it does not see:
@@ -439,7 +462,8 @@ __device__ __forceinline__ void make_item(Item& it, const int4 a, const int4 b, 
 template <bool kWin>
 __device__ __forceinline__ bool masked_tile(const Item& it, int j, int window) {
     const int k0 = (it.j0 + j) * kKV;
-    return k0 == it.row[0] || (it.n[1] && k0 == it.row[1]) ||
+    auto diagonal = [&](int row) { return k0 >= row && k0 < row + kQ; };
+    return diagonal(it.row[0]) || (it.n[1] && diagonal(it.row[1])) ||
            (kWin && k0 < (it.n[1] ? it.row[1] : it.row[0]) + kQ - window);
 }
 
@@ -461,7 +485,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 const Block* __restrict__ list, PackedGeom gm, int64_t vt, int64_t vh, int64_t ot,
                 int64_t oh, float scale_log2, int* err) {
     using L = Pk<DH>;
-    constexpr int NQ = L::kNQ, SK = L::kSK, SV = L::kSV;
+    constexpr int NQ = L::kNQ, R = L::kRing;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -469,17 +493,19 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     const uint32_t sQ = base, sK = base + L::kKOff, sV = base + L::kVOff, bars = base + L::kBarOff;
     auto q_full = [&](int s) { return bars + 8u * s; };
     auto q_empty = [&](int s) { return bars + 8u * (NQ + s); };
-    auto k_full = [&](int s) { return bars + 8u * (2 * NQ + s); };
-    auto k_empty = [&](int s) { return bars + 8u * (2 * NQ + SK + s); };
-    auto v_full = [&](int s) { return bars + 8u * (2 * NQ + 2 * SK + s); };
-    auto v_empty = [&](int s) { return bars + 8u * (2 * NQ + 2 * SK + SV + s); };
-    constexpr int B0 = 2 * (NQ + SK + SV);
-    auto s_full = [&](int x) { return bars + 8u * (B0 + x); };
-    auto s_free = [&](int x) { return bars + 8u * (B0 + 2 + x); };
-    auto p_full = [&](int x) { return bars + 8u * (B0 + 4 + x); };
-    auto o_done = [&](int x) { return bars + 8u * (B0 + 6 + x); };
-    const uint32_t done_bar = bars + 8u * (B0 + 8);
-    auto v_clean = [&](int s) { return bars + 8u * (B0 + 9 + s); };
+    // A slot of the ring takes, in step u, K of round u and V of round u - 1, which are
+    // multiplied in the same step: loaded, V checked, both multiplied.
+    constexpr int B0 = 2 * NQ;
+    auto full = [&](int s) { return bars + 8u * (B0 + s); };
+    auto clean = [&](int s) { return bars + 8u * (B0 + R + s); };
+    auto empty = [&](int s) { return bars + 8u * (B0 + 2 * R + s); };
+    // of tile x's n-th S, in buffer n & 1: S is complete, P is written, P.V is complete
+    constexpr int B1 = B0 + 3 * R;
+    auto s_full = [&](int x, int n) { return bars + 8u * (B1 + 2 * x + (n & 1)); };
+    auto p_full = [&](int x, int n) { return bars + 8u * (B1 + 4 + 2 * x + (n & 1)); };
+    auto o_done = [&](int x, int n) { return bars + 8u * (B1 + 8 + 2 * x + (n & 1)); };
+    auto phase = [&](int n) { return (uint32_t)(n >> 1) & 1u; };
+    const uint32_t done_bar = bars + 8u * (B1 + 12);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(gbase + L::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMiscOff + 4);
     volatile int* poison = reinterpret_cast<volatile int*>(gbase + L::kMiscOff + 16);
@@ -490,21 +516,17 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             mbar_init(q_full(s), 1);
             mbar_init(q_empty(s), 1);
         }
-        for (int s = 0; s < SK; ++s) {
-            mbar_init(k_full(s), 1);
-            mbar_init(k_empty(s), 2);                  // both MMA warps are done with the slot
+        for (int s = 0; s < R; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(clean(s), 1);
+            mbar_init(empty(s), 2);                    // both MMA warps are done with the slot
         }
-        for (int s = 0; s < SV; ++s) {
-            mbar_init(v_full(s), 1);
-            mbar_init(v_empty(s), 2);
-            mbar_init(v_clean(s), 1);
-        }
-        for (int x = 0; x < 2; ++x) {
-            mbar_init(s_full(x), 1);
-            mbar_init(s_free(x), 4);
-            mbar_init(p_full(x), 4);
-            mbar_init(o_done(x), 1);
-        }
+        for (int x = 0; x < 2; ++x)
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(s_full(x, i), 1);
+                mbar_init(p_full(x, i), 4);
+                mbar_init(o_done(x, i), 1);
+            }
         mbar_init(done_bar, 2);
         abort_flag[0] = abort_flag[1] = 0;
         for (int i = 0; i < kPoison; ++i) poison[i] = 0;
@@ -554,54 +576,50 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     constexpr uint32_t idesc_o = umma_idesc_bf16(kQ, DH, true);
     // Q, K: K-major tiles in 64-column sub-tiles of 16 KB; V: MN-major
     const uint64_t dq = sdesc(sQ, L::kSwz, 16, L::kGroup), dk = sdesc(sK, L::kSwz, 16, L::kGroup);
-    const uint64_t dv = sdesc(sV, L::kSwz, DH > 64 ? 16384 : 0, L::kGroup);
+    const uint64_t dv = sdesc(sV, L::kSwz, DH > 64 ? L::kSubKV : 0, L::kGroup);
     const uint32_t tm = uniform(tmem_base);
 
     if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     if (warp == 0) {
         // ---------------------------------------------------------- TMA producer
-        // Per item Q_A, Q_B and K_0, then V_j, K_{j+1}, the order in which the
-        // MMA warps take them.
-        int qn = 0, kn = 0, vn = 0;
-        bool ok = true;
+        // Per step K of a round and V of the round before; Q_A and Q_B before the first
+        // K of an item.
+        int qn = 0, u = 0, vy = 0, vg = 0;             // Q tiles, steps; place of the V to be loaded
+        bool ok = true, has = true;
         Item it;
-        while (ok && next_item(it)) {
-            const int nmax = (int)uniform(it.nmax), two = (int)uniform(it.n[1]);
+        while (has && ok) {
+            has = next_item(it);
+            if (!has && u == 0) break;                 // nothing at all
+            const int nmax = has ? (int)uniform(it.nmax) : 1, two = has ? (int)uniform(it.n[1]) : 0;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                if (!ok || (x && !two)) continue;
+                if (!ok || !has || (x && !two)) continue;
                 const int s = qn % NQ;
                 if (qn >= NQ) ok = warp_wait(q_empty(s), ((uint32_t)(qn / NQ) & 1u) ^ 1u, err, abort_flag);
                 if (!ok) continue;
-                mbar_arrive_expect_tx_e(q_full(s), L::kTile);
+                mbar_arrive_expect_tx_e(q_full(s), L::kQTile);
 #pragma unroll
                 for (int c2 = 0; c2 < L::kSub; ++c2)
-                    tma_load_3d_e(sQ + s * L::kTile + c2 * 16384, &qmap, 64 * c2, it.start + it.row[x], it.h[x], q_full(s));
+                    tma_load_3d_e(sQ + s * L::kQTile + c2 * L::kSubQ, &qmap, 64 * c2, it.start + it.row[x], it.h[x], q_full(s));
                 ++qn;
             }
             int y = it.start + it.j0 * kKV;            // the next K tile's first row
-            for (int j = 0; j <= nmax && ok; ++j, y += kKV) {
-                if (j > 0) {
-                    const int s = vn % SV;
-                    if (vn >= SV) ok = warp_wait(v_empty(s), ((uint32_t)(vn / SV) & 1u) ^ 1u, err, abort_flag);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx_e(v_full(s), L::kTile);
+            for (int j = 0; j < nmax && ok; ++j, ++u, y += kKV) {
+                const int s = u % R;
+                if (u >= R) ok = warp_wait(empty(s), ((uint32_t)(u / R) & 1u) ^ 1u, err, abort_flag);
+                if (!ok) break;
+                mbar_arrive_expect_tx_e(full(s), (has ? L::kTile : 0) + (u > 0 ? L::kTile : 0));
+                if (has)
 #pragma unroll
                     for (int c2 = 0; c2 < L::kSub; ++c2)
-                        tma_load_3d_e(sV + s * L::kTile + c2 * 16384, &vmap, 64 * c2, y - kKV, it.g, v_full(s));
-                    ++vn;
-                }
-                if (j < nmax) {
-                    const int s = kn % SK;
-                    if (kn >= SK) ok = warp_wait(k_empty(s), ((uint32_t)(kn / SK) & 1u) ^ 1u, err, abort_flag);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx_e(k_full(s), L::kTile);
+                        tma_load_3d_e(sK + s * L::kTile + c2 * L::kSubKV, &kmap, 64 * c2, y, it.g, full(s));
+                if (u > 0)
 #pragma unroll
                     for (int c2 = 0; c2 < L::kSub; ++c2)
-                        tma_load_3d_e(sK + s * L::kTile + c2 * 16384, &kmap, 64 * c2, y, it.g, k_full(s));
-                    ++kn;
-                }
+                        tma_load_3d_e(sV + s * L::kTile + c2 * L::kSubKV, &vmap, 64 * c2, vy, vg, full(s));
+                vy = y;
+                vg = it.g;
             }
         }
         // The other warps wait for every load; after a wait that gave up, the last
@@ -609,25 +627,31 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         if (!ok && lane == 0) {
             volatile int* never = abort_flag + 1;       // stays 0: these waits run to their own limit
             for (int k = qn < NQ ? 0 : qn - NQ; k < qn; ++k) mbar_wait(q_full(k % NQ), (uint32_t)(k / NQ) & 1u, nullptr, never);
-            for (int k = kn < SK ? 0 : kn - SK; k < kn; ++k) mbar_wait(k_full(k % SK), (uint32_t)(k / SK) & 1u, nullptr, never);
-            for (int k = vn < SV ? 0 : vn - SV; k < vn; ++k) mbar_wait(v_full(k % SV), (uint32_t)(k / SV) & 1u, nullptr, never);
+            for (int k = u < R ? 0 : u - R; k < u; ++k) mbar_wait(full(k % R), (uint32_t)(k / R) & 1u, nullptr, never);
         }
     } else if (warp == 3) {
         // ---------------------------------------------------------- V check
         // In a tile that some row does not see whole, P is zero where the row
         // does not look, but zero times infinity is not: such values are taken
         // out here (and added back for the rows that see them, in the epilogue).
-        // Every tile passes through here before its P.V, so that no barrier runs
-        // past a phase that this warp has not seen.
-        int vn = 0, items = 0;
-        bool ok = true;
+        // Every step passes through here, so that no barrier runs past a phase that this
+        // warp has not seen.
+        int u = 0, items = 0, v_item = 0;              // steps, items; item of V
+        bool ok = true, has = true, masked = false;    // some row does not see all of V
         Item it;
-        for (; ok && next_item(it); ++items)
-            for (int j = 0; j < it.nmax; ++j, ++vn) {
-                const int s = vn % SV;
-                if (!(ok = warp_wait(v_full(s), (uint32_t)(vn / SV) & 1u, err, abort_flag))) break;
-                if (!masked_tile<kWin>(it, j, gm.window)) {
-                    if (lane == 0) mbar_arrive(v_clean(s));
+        while (has && ok) {
+            has = next_item(it);
+            if (!has && u == 0) break;
+            const int nmax = has ? it.nmax : 1;
+            for (int j = 0; j < nmax; ++j, ++u) {
+                const int s = u % R;
+                if (!(ok = warp_wait(full(s), (uint32_t)(u / R) & 1u, err, abort_flag))) break;
+                const bool check = masked;
+                const int at_item = v_item;
+                masked = has && masked_tile<kWin>(it, j, gm.window);
+                v_item = items;
+                if (!check) {
+                    if (lane == 0) mbar_arrive(clean(s));
                     continue;
                 }
                 // An exponent of all ones carries into the bit above it when one is
@@ -655,93 +679,97 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                     }
                 }
                 if (__any_sync(0xffffffffu, found)) {
-                    if (lane == 0) poison[items % kPoison] = items + 1;
+                    if (lane == 0) poison[at_item % kPoison] = at_item + 1;
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(v_clean(s));
+                if (lane == 0) mbar_arrive(clean(s));
             }
+            ++items;
+        }
     } else {
         // ---------------------------------------------------------- MMAs (warp 1: tile A, warp 2: tile B)
         // A warp per tile: each runs at the pace of its own softmax, and the two
         // pipelines drift into the phase in which one's exponentials run beside the
         // other's products (issued by one warp in the order A, B, A, ..., each waited for
         // the other: 46 us instead of 40 for 24 prompts of up to 1024 tokens at 12 x 64).
-        // A round is a key tile of the item; a tile that this warp's queries do not see is
-        // passed on unread.
-        // P in columns of its own: S of the next round as soon as the softmax has
-        // read this one's.  P in the place of S (d_head 128): behind this round's P.V,
-        // as MMAs of one thread complete in the order they are issued.
+        // Step u: S of round u, then P.V of round u - 1, each if its key tile is one that
+        // this tile's queries see.  The two places of S let the softmax of round u - 1
+        // run beside S of round u, and S of an item's first round beside the last softmax
+        // of the item before.  MMAs of one thread complete in the order they are issued:
+        // S of round u, in the place of P of round u - 2, lies behind its P.V.
         const int x = (int)uniform((uint32_t)(warp - 1));
-        bool ok = true;
-        int kn = 0, vn = 0, qn = 0, cnt = 0, qs = 0;    // tiles, Q slots so far; own tiles; own Q slot
-        // own rounds [lo, n) and all rounds of the item S is at, and of the one P.V is at
-        int lo = 0, n = 0, nmax = 0, pv_lo = 0, pv_n = 0, pv_max = 0;
-        auto open_item = [&]() -> bool {
-            Item it;
-            if (!uniform(next_item(it))) return false;
-            nmax = (int)uniform(it.nmax);
-            lo = (int)uniform(x ? it.lo[1] : 0);
-            n = (int)uniform(x ? it.n[1] : it.n[0]);
-            qs = qn + x;
-            qn += uniform(it.n[1]) ? 2 : 1;
-            return true;
-        };
-        // Round j of the item that was opened last; false: not this warp's.
-        auto do_s = [&](int j) -> bool {
-            const int s = kn % SK;
-            ok = warp_wait(k_full(s), (uint32_t)(kn / SK) & 1u, err, abort_flag);
-            if (j < lo || j >= n) {
-                if (lane == 0) mbar_arrive(k_empty(s));
-                ++kn;
-                return false;
-            }
-            if (j == lo) ok = ok && warp_wait(q_full(qs % NQ), (uint32_t)(qs / NQ) & 1u, err, abort_flag);
-            if (!L::kAlias && cnt > 0) ok = ok && warp_wait(s_free(x), (uint32_t)(cnt - 1) & 1u, err, abort_flag);
-            if (!ok) return false;
+        // This loop is what a short tile waits for: the warp waits out the latency of each of
+        // its instructions (~10 cycles, two busy warps beside it), so its own rounds, an even
+        // number in every item, go in pairs with the places of S and P fixed.
+        const uint32_t t_s = tm + 2 * x * kKV, t_o = tm + L::kOCol + x * DH;
+        const uint32_t hi_k = (uint32_t)(dq >> 32), hi_v = (uint32_t)(dv >> 32);
+        const uint32_t s_bar = uniform(s_full(x, 0)), p_bar = uniform(p_full(x, 0)), o_bar = uniform(o_done(x, 0));
+        bool ok = true, pv = false;                     // P.V of an odd round is to come
+        uint32_t slot = 0, par = 0, pair = 0;           // ring slot and its phase's parity; parity of own pairs
+        int qn = 0;                                     // Q tiles so far
+        auto ready = [&]() -> bool { return ok = warp_wait_short(clean(slot), par, err, abort_flag); };
+        auto scores = [&](uint32_t q_lo, int b) {
             tc_fence_after();
-            umma_scores<DH>(tm + x * kKV, (uint32_t)dq + (qs % NQ) * (L::kTile >> 4), (uint32_t)dk + s * (L::kTile >> 4),
-                            (uint32_t)(dq >> 32), idesc_s, s_full(x));
-            umma_commit_e(k_empty(s));
-            if (j == n - 1) umma_commit_e(q_empty(qs % NQ));
-            ++kn;
-            ++cnt;
+            umma_scores<DH>(t_s + b * kKV, q_lo, (uint32_t)dk + slot * (L::kTile >> 4), hi_k, idesc_s, s_bar + 8 * b);
+        };
+        auto values = [&](int b, uint32_t parity, uint32_t acc) -> bool {
+            if (!(ok = warp_wait_short(p_bar + 8 * b, parity, err, abort_flag))) return false;
+            tc_fence_after();
+            umma_values<DH>(t_o, t_s + b * kKV, (uint32_t)dv + slot * (L::kTile >> 4), hi_v, idesc_o, acc, o_bar + 8 * b);
             return true;
         };
-        int pv = 0;                                     // own P.V so far
-        bool own = false;                               // the round P.V is at is this warp's
-        bool has = open_item();
-        if (has) own = do_s(0);
-        while (has && ok) {
-            bool has_next = false;
-            pv_lo = lo;
-            pv_n = n;
-            pv_max = nmax;
-            for (int j = 0; j < pv_max && ok; ++j, ++vn) {
-                const bool last = j == pv_max - 1;
-                if (last) has_next = open_item();
-                const bool more = !last || has_next;
-                const int sj = last ? 0 : j + 1;
-                const bool next_own = more && sj >= lo && sj < n;
-                if (!L::kAlias && next_own) do_s(sj);
-                const int s = vn % SV;
-                ok = ok && warp_wait(v_clean(s), (uint32_t)(vn / SV) & 1u, err, abort_flag);
-                if (ok && own) {
-                    ok = warp_wait(p_full(x), (uint32_t)pv & 1u, err, abort_flag);
-                    if (!ok) break;
-                    ++pv;
-                    tc_fence_after();
-                    umma_values<DH>(tm + L::kOCol + x * DH, tm + L::p_col(x), (uint32_t)dv + s * (L::kTile >> 4),
-                                    (uint32_t)(dv >> 32), idesc_o, j > pv_lo ? 1u : 0u, v_empty(s));
-                    if (!L::kAlias || j == pv_n - 1) umma_commit_e(o_done(x));
-                } else if (ok && lane == 0) {
-                    mbar_arrive(v_empty(s));
-                }
-                if (ok && more && (L::kAlias || !next_own)) do_s(sj);
-                own = next_own;
+        auto release = [&]() {
+            umma_commit_e(empty(slot));
+            if (++slot == R) {
+                slot = 0;
+                par ^= 1u;
             }
-            has = has_next;
+        };
+        // a round that this tile does not see, or the step behind the last round
+        auto pass = [&]() {
+            if (!ready() || (pv && !values(1, pair ^ 1u, 1u))) return;
+            pv = false;
+            release();
+        };
+        // all rounds of the next item (0: none), those of this tile, its Q tile
+        int t_max, t_lo, t_n, t_q;
+        auto fetch = [&]() {
+            Item it;
+            it.nmax = it.n[1] = 0;
+            const bool has = next_item(it);
+            t_max = has ? (int)uniform(it.nmax) : 0;
+            t_lo = (int)uniform(x ? it.lo[1] : 0);
+            t_n = (int)uniform(x ? it.n[1] : it.n[0]);
+            t_q = qn + x;
+            qn += uniform(it.n[1]) ? 2 : 1;
+        };
+        fetch();
+        const bool any = t_max > 0;
+        while (ok && t_max > 0) {
+            const int nmax = t_max, lo = t_lo, n = t_n, qs = t_q;
+            int j = 0;
+            if (n == 0) fetch();
+            for (; j < lo && ok; ++j) pass();
+            const uint32_t q_lo = (uint32_t)dq + (qs % NQ) * (L::kQTile >> 4);
+            for (; j < n && ok; j += 2) {
+                if (!ready()) break;
+                if (j == lo && !(ok = warp_wait_short(q_full(qs % NQ), (uint32_t)(qs / NQ) & 1u, err, abort_flag))) break;
+                scores(q_lo, 0);
+                if (pv && !values(1, pair ^ 1u, 1u)) break;
+                release();
+                if (!ready()) break;
+                scores(q_lo, 1);
+                if (j == n - 2) umma_commit_e(q_empty(qs % NQ));
+                if (!values(0, pair, j > lo ? 1u : 0u)) break;
+                release();
+                pv = true;
+                pair ^= 1u;
+                if (j == lo) fetch();                  // not when its first S is due
+            }
+            for (; j < nmax && ok; ++j) pass();
         }
+        if (any && ok) pass();
         umma_commit_e(done_bar);
         warp_wait(done_bar, 0, err, abort_flag);
     }
@@ -752,10 +780,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         const int q4 = warp & 3;
         const int r = q4 * 32 + lane;
         const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-        const uint32_t t_s = tmem_base + x * kKV + lane_off;
+        const uint32_t t_s = tmem_base + 2 * x * kKV + lane_off;
         const uint32_t t_o = tmem_base + L::kOCol + x * DH + lane_off;
-        const uint32_t t_p = tmem_base + L::p_col(x) + lane_off;
-        int cnt = 0, items = 0, outs = 0;              // tiles of this x, items, items with this x
+        int cnt = 0, items = 0;                        // own tiles, items
         bool ok = true;
         Item it;
         for (; ok && next_item(it); ++items) {
@@ -765,19 +792,15 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             const int kmin = kWin ? qi - gm.window + 1 : 0;
             const int win_lo = kWin ? row0 + kQ - gm.window : INT_MIN;
             float m = -INFINITY, l = 0.f;
-            for (int j = lo; j < n && ok; ++j, ++cnt) {
-                if (!warp_wait(s_full(x), (uint32_t)cnt & 1u, err, abort_flag)) { ok = false; break; }
+            for (int j = lo; j < n; ++j, ++cnt) {
+                if (!(ok = warp_wait(s_full(x, cnt), phase(cnt), err, abort_flag))) break;
                 tc_fence_after();
                 uint32_t sr[kKV / 32][32];
                 float mq[kKV / 32];                    // maxima of the 32-column blocks
 #pragma unroll
-                for (int cc = 0; cc < kKV / 32; ++cc) tmem_ld32_max_issue(t_s + cc * 32, sr[cc], mq[cc]);
+                for (int cc = 0; cc < kKV / 32; ++cc)
+                    tmem_ld32_max_issue(t_s + (cnt & 1) * kKV + cc * 32, sr[cc], mq[cc]);
                 tmem_ld_wait();
-                if (!L::kAlias) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(s_free(x));
-                }
                 float s[kKV];
 #pragma unroll
                 for (int cc = 0; cc < kKV / 32; ++cc) {
@@ -787,25 +810,28 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                     for (int e = 0; e < 32; ++e) s[cc * 32 + e] = __uint_as_float(sr[cc][e]);
                 }
                 const int k0 = (it.j0 + j) * kKV;
+                float mx = fmaxf(mq[0], mq[1]);
                 // A row of the sequence sees keys up to itself, which lie in the
                 // sequence: the diagonal masks the next sequence's keys too.
-                if (k0 == row0) {
+                if (k0 >= row0) {
+                    const int to = r - (k0 - row0);
 #pragma unroll
-                    for (int cc = 0; cc < kKV; ++cc) s[cc] = cc > r ? -INFINITY : s[cc];
+                    for (int cc = 0; cc < kKV; ++cc) s[cc] = cc > to ? -INFINITY : s[cc];
                 }
                 if (kWin && k0 < win_lo) {
                     const int from = kmin - k0;
 #pragma unroll
                     for (int cc = 0; cc < kKV; ++cc) s[cc] = cc < from ? -INFINITY : s[cc];
                 }
-                float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-                if (k0 == row0 || (kWin && k0 < win_lo)) {
+                if (k0 >= row0 || (kWin && k0 < win_lo)) {
                     // a masked tile: of the scores that are left
                     float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                    for (int cc = 4; cc < kKV; cc += 8)
+                    for (int cc = 4; cc + 8 <= kKV; cc += 8)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) mx4[e] = fmax3(mx4[e], s[cc + 2 * e], s[cc + 2 * e + 1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(mx4[e], s[kKV - 4 + e]);
                     mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
                 }
                 mx *= scale_log2;
@@ -814,42 +840,30 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                     corr = fast_exp2(m - mx);
                     m = mx;
                 }
-                const bool need_rescale = __any_sync(0xffffffffu, corr != 1.f && j > lo && qi < it.len);
+                const bool rescale = __any_sync(0xffffffffu, corr != 1.f && j > lo && qi < it.len);
                 const uint64_t scale2 = f2_pack(scale_log2, scale_log2);
-                const float negm = (kWin && m == -INFINITY) ? 0.f : -m;
+                const float negm = m == -INFINITY ? 0.f : -m;      // a row that has seen no key yet
                 const uint64_t negm2 = f2_pack(negm, negm);
                 uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
-                uint32_t pw[kKV / 64][32];
+                uint32_t pw[32];
 #pragma unroll
-                for (int h64 = 0; h64 < kKV / 64; ++h64) {
-#pragma unroll
-                    for (int e = 0; e < 64; e += 2) {
-                        float t0, t1;
-                        const int cc = h64 * 64 + e;
-                        f2_unpack(f2_fma(f2_pack(s[cc], s[cc + 1]), scale2, negm2), t0, t1);
-                        const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
-                        sum2[(e >> 1) & 3] = f2_add(sum2[(e >> 1) & 3], f2_pack(p0, p1));
-                        pw[h64][e >> 1] = pack_bf16x2(p0, p1);
-                    }
+                for (int e = 0; e < kKV; e += 2) {
+                    float t0, t1;
+                    f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), scale2, negm2), t0, t1);
+                    const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
+                    sum2[(e >> 1) & 3] = f2_add(sum2[(e >> 1) & 3], f2_pack(p0, p1));
+                    pw[e >> 1] = pack_bf16x2(p0, p1);
                 }
-                // P.V of the previous tile must be complete before P and O are
-                // written; in S's place it is, as S comes behind it.
-                if (!L::kAlias) {
-                    if (cnt > 0 && !warp_wait(o_done(x), (uint32_t)(cnt - 1) & 1u, err, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                }
-#pragma unroll
-                for (int h64 = 0; h64 < kKV / 64; ++h64) tmem_st32_async(t_p + h64 * 32, pw[h64]);
+                tmem_st32_async(t_s + (cnt & 1) * kKV, pw);
                 tmem_st_wait();
                 float sa[4], sb[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) f2_unpack(sum2[e], sa[e], sb[e]);
                 const float sum = ((sa[0] + sb[0]) + (sa[1] + sb[1])) + ((sa[2] + sb[2]) + (sa[3] + sb[3]));
                 l = l * corr + sum;
-                if (need_rescale) {
+                if (rescale) {
+                    // O must hold what the tile before adds to it
+                    if (!(ok = warp_wait(o_done(x, cnt - 1), phase(cnt - 1), err, abort_flag))) break;
                     tc_fence_after();
 #pragma unroll 1
                     for (int cc = 0; cc < DH / 32; ++cc) {
@@ -862,11 +876,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(x));
+                if (lane == 0) mbar_arrive(p_full(x, cnt));
             }
             if (!ok) break;
-            ok = warp_wait(o_done(x), (uint32_t)(L::kAlias ? outs : cnt - 1) & 1u, err, abort_flag);
-            ++outs;
+            ok = warp_wait(o_done(x, cnt - 1), phase(cnt - 1), err, abort_flag);
             if (!ok) break;
             tc_fence_after();
             const float inv = 1.0f / l;
@@ -972,7 +985,8 @@ tfm_status launch_packed_attention(const PackedArgs& a, cudaStream_t st, cudaErr
     CUtensorMap maps[3];
     const void* ptr[3] = {a.q, a.k, a.v};
     for (int i = 0; i < 3; ++i)
-        if (!rows_heads_map(&maps[i], ptr[i], a.T, i ? a.Hkv : a.H, a.dh, a.strides[2 * i], a.strides[2 * i + 1]))
+        if (!rows_heads_map(&maps[i], ptr[i], a.T, i ? a.Hkv : a.H, a.dh, a.strides[2 * i], a.strides[2 * i + 1],
+                            i ? kKV : kQ))
             return TFM_ECUDA;
     PackedGeom gm;
     gm.group = a.H / a.Hkv;
