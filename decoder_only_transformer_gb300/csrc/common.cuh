@@ -596,17 +596,21 @@ __device__ __forceinline__ void umma_bf16_ts_e(uint32_t d_tmem, uint32_t a_tmem,
     "add.u32 x, %1, " #da ";\n\tadd.u32 y, %2, " #db ";\n\t" \
     "mov.b64 b, {y, %3};\n\t"                           \
     "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, " #pred ";\n\t"
+#define TFM_MMA_SS2(da, db, pred)                       \
+    "add.u32 x, %7, " #da ";\n\tadd.u32 y, %2, " #db ";\n\t" \
+    "mov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"     \
+    "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, " #pred ";\n\t"
 #define TFM_MMA_TAIL                                    \
     "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n\t}"
 #define TFM_MMA_ARGS(d, alo, blo, hi, idesc, acc, bar) \
     ::"r"(d), "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "r"(acc), "r"(bar) : "memory"
 
 // S = Q K^T of d_head DH, 128 rows against 64 keys: rows of 64 columns 32 bytes (2
-// descriptor units) a step, the second 64 columns 16 KB (1024 units) further in Q and
-// 8 KB in K.
+// descriptor units) a step, the second 64 columns 8 KB (512 units) further in K and at
+// alo2 in Q.
 template <int DH>
-__device__ __forceinline__ void umma_scores(uint32_t d, uint32_t alo, uint32_t blo, uint32_t hi, uint32_t idesc,
-                                            uint32_t bar) {
+__device__ __forceinline__ void umma_scores(uint32_t d, uint32_t alo, uint32_t alo2, uint32_t blo, uint32_t hi,
+                                            uint32_t idesc, uint32_t bar) {
     if constexpr (DH == 32)
         asm volatile(TFM_MMA_HEAD TFM_MMA_SS(0, 0, p) TFM_MMA_SS(2, 2, t) TFM_MMA_TAIL
                          TFM_MMA_ARGS(d, alo, blo, hi, idesc, 0u, bar));
@@ -615,8 +619,9 @@ __device__ __forceinline__ void umma_scores(uint32_t d, uint32_t alo, uint32_t b
                          TFM_MMA_TAIL TFM_MMA_ARGS(d, alo, blo, hi, idesc, 0u, bar));
     else
         asm volatile(TFM_MMA_HEAD TFM_MMA_SS(0, 0, p) TFM_MMA_SS(2, 2, t) TFM_MMA_SS(4, 4, t) TFM_MMA_SS(6, 6, t)
-                         TFM_MMA_SS(1024, 512, t) TFM_MMA_SS(1026, 514, t) TFM_MMA_SS(1028, 516, t)
-                             TFM_MMA_SS(1030, 518, t) TFM_MMA_TAIL TFM_MMA_ARGS(d, alo, blo, hi, idesc, 0u, bar));
+                         TFM_MMA_SS2(0, 512, t) TFM_MMA_SS2(2, 514, t) TFM_MMA_SS2(4, 516, t) TFM_MMA_SS2(6, 518, t)
+                             TFM_MMA_TAIL ::"r"(d), "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "r"(0u), "r"(bar), "r"(alo2)
+                     : "memory");
 }
 // O (+)= P V over 64 keys: P 16 keys (8 columns) a step in tensor memory, V 16 rows of
 // 128 bytes (128 descriptor units) or of 64 (64).
@@ -632,6 +637,7 @@ __device__ __forceinline__ void umma_values(uint32_t d, uint32_t p_tmem, uint32_
 }
 #undef TFM_MMA_HEAD
 #undef TFM_MMA_SS
+#undef TFM_MMA_SS2
 #undef TFM_MMA_TS
 #undef TFM_MMA_TAIL
 #undef TFM_MMA_ARGS

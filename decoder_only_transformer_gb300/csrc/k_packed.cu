@@ -711,7 +711,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         auto ready = [&]() -> bool { return ok = warp_wait_short(clean(slot), par, err, abort_flag); };
         auto scores = [&](uint32_t q_lo, int b) {
             tc_fence_after();
-            umma_scores<DH>(t_s + b * kKV, q_lo, (uint32_t)dk + slot * (L::kTile >> 4), hi_k, idesc_s, s_bar + 8 * b);
+            umma_scores<DH>(t_s + b * kKV, q_lo, q_lo + (L::kSubQ >> 4), (uint32_t)dk + slot * (L::kTile >> 4), hi_k, idesc_s, s_bar + 8 * b);
         };
         auto values = [&](int b, uint32_t parity, uint32_t acc) -> bool {
             if (!(ok = warp_wait_short(p_bar + 8 * b, parity, err, abort_flag))) return false;

@@ -371,9 +371,9 @@ __global__ void __launch_bounds__(kThreadsX, 2)
         bool ok = true;
         int slot = 0;
         uint32_t q_used = 0, q_par = 0;                 // slots used before, their parity
-        Walk wk = walk, wv = walk;
-        Seg sk{}, sv{};
-        int lk = 0, lv = 0;                             // tiles left in the pieces of K and V
+        Walk wk = walk;
+        Seg sk{};
+        int lk = 0;                                     // tiles left in the piece
         auto load_q = [&]() {
             const bool own = uniform(sk.own);
             const int s = own ? slot : 0;
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreadsX, 2)
             slot = own ? (s + 1 == gm.q_slots ? 0 : s + 1) : 0;
         };
         int kn = 0, vn = 0;                             // K and V tiles loaded
-        int ky = 0, kz = 0, vy = 0, vz = 0;             // coordinates of the next K and V tile
+        int ky = 0, kz = 0, vy = 0, vz = 0;             // coordinates of the next K tile, of the last one's V
         const CUtensorMap *km = &kpmap, *vm = &vpmap;
         for (int n = 0; n <= tiles && ok; ++n) {
             const int s = n % R;
@@ -419,22 +419,16 @@ __global__ void __launch_bounds__(kThreadsX, 2)
             }
             if (n > 0) {
                 const int m = n - 1, sv_ = m % R;
-                if (lv == 0) {
-                    next_seg(wv, sv, gm, cum);
-                    lv = (int)uniform(sv.t1 - sv.t0);
-                    vy = (int)uniform(sv.t0) * kKeys;
-                    vz = (int)uniform(sv.own ? sv.x * gm.Hkv + sv.g : sv.g);
-                    vm = uniform(sv.own) ? &vcmap : &vpmap;
-                }
                 if (m >= R && !(ok = warp_wait(pv_done(sv_), ((uint32_t)(m / R) & 1u) ^ 1u, err, abort_flag))) break;
                 mbar_arrive_expect_tx_e(v_full(sv_), L::kTile);
 #pragma unroll
                 for (int c = 0; c < L::kSub; ++c)
                     tma_load_3d_e(sV + sv_ * L::kTile + c * L::kSubTile, vm, 64 * c, vy, vz, v_full(sv_));
-                vy += kKeys;
-                --lv;
                 ++vn;
             }
+            vy = ky - kKeys;
+            vz = kz;
+            vm = km == &kpmap ? &vpmap : &vcmap;
         }
         // The other warps wait for every load; after a wait that gave up,
         // the last ones still have to land before the CTA ends.
@@ -453,56 +447,47 @@ __global__ void __launch_bounds__(kThreadsX, 2)
         const uint64_t dq = sdesc(sQ, L::kSwz, 16, L::kGroup), dk = sdesc(sK, L::kSwz, 16, L::kGroup);
         const uint64_t dv = sdesc(sV, L::kSwz, DH > 64 ? L::kSubTile : 0, L::kGroup);
         bool ok = true;
-        int slot = 0, cur = 0, ls = 0, lp = 0;          // Q slots; tiles left in the pieces of S and P.V
-        uint32_t q_par = 0, asub = 0;
-        uint64_t a0 = 0;
-        Walk ws = walk, wp = walk;
-        Seg ss, sp;
+        int slot = 0, cur = 0, left = 0;                // Q slots; tiles left in the piece of S
+        uint32_t q_par = 0, a0 = 0, asub = 0;
+        Walk ws = walk;
+        Seg ss;
+        // of the tile whose S was issued last: an own tile, the first of its piece
+        bool own = false, first = false;
         auto do_s = [&](int n) {
-            if (ls == 0) {
+            first = left == 0;
+            if (first) {
                 next_seg(ws, ss, gm, cum);
-                ls = (int)uniform(ss.t1 - ss.t0);
-                const bool own = uniform(ss.own);
+                left = (int)uniform(ss.t1 - ss.t0);
+                own = uniform(ss.own);
                 cur = own ? slot : 0;
                 slot = own ? (cur + 1 == gm.q_slots ? 0 : cur + 1) : 0;
-                a0 = dq + (uint64_t)((own ? cur * gm.q_pad * DH * 2 : 0) >> 4);
+                a0 = (uint32_t)dq + ((own ? cur * gm.q_pad * DH * 2 : 0) >> 4);
                 asub = ((own ? gm.q_pad : kRowsP) * L::kRowBytes) >> 4;
-                if (!(ok = warp_wait(q_full(cur), (q_par >> cur) & 1u, err, abort_flag))) return;
+                if (!(ok = warp_wait_short(q_full(cur), (q_par >> cur) & 1u, err, abort_flag))) return;
                 q_par ^= 1u << cur;
             }
             const int s = n % R;
-            if (n < 2) ok = warp_wait(k_full(s), (uint32_t)(n / R) & 1u, err, abort_flag);
-            if (!ok) return;
+            if (n < 2 && !(ok = warp_wait_short(k_full(s), (uint32_t)(n / R) & 1u, err, abort_flag))) return;
             tc_fence_after();
-            const uint64_t b0 = dk + (uint64_t)((s * L::kTile) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < DH / 16; ++kk)
-                umma_bf16_e(tm + (n & 1) * kKeys, a0 + (kk >> 2) * asub + (kk & 3) * 2,
-                            b0 + (kk >> 2) * (L::kSubTile >> 4) + (kk & 3) * 2, idesc_s, kk > 0 ? 1u : 0u);
-            umma_commit_e(s_done(s));
-            if (--ls == 0) umma_commit_e(q_empty(cur));
+            umma_scores<DH>(tm + (n & 1) * kKeys, a0, a0 + asub, (uint32_t)dk + s * (L::kTile >> 4), (uint32_t)(dq >> 32),
+                            idesc_s, s_done(s));
+            if (--left == 0) umma_commit_e(q_empty(cur));
         };
         if (tiles > 0) do_s(0);
+        bool pv_own = own, pv_first = first;            // of tile n, and of the one behind it
         if (ok && tiles > 1) do_s(1);
-        bool own = false, first = false;
+        bool next_own = own, next_first = first;
         for (int n = 0; n < tiles && ok; ++n) {
-            first = lp == 0;
-            if (first) {
-                next_seg(wp, sp, gm, cum);
-                lp = (int)uniform(sp.t1 - sp.t0);
-                own = uniform(sp.own);
-            }
             const int s = n % R;
-            if (!(ok = warp_wait(p_full(own, n), p_phase(own, n), err, abort_flag))) break;
+            if (!(ok = warp_wait_short(p_full(pv_own, n), p_phase(pv_own, n), err, abort_flag))) break;
             tc_fence_after();
-            const uint64_t b0 = dv + (uint64_t)((s * L::kTile) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-                umma_bf16_ts_e(tm + L::kOCol, tm + (n & 1) * kKeys + kk * 8,
-                               b0 + kk * ((16 * L::kRowBytes) >> 4), idesc_o, (!first || kk > 0) ? 1u : 0u);
-            umma_commit_e(pv_done(s));
-            --lp;
+            umma_values<DH>(tm + L::kOCol, tm + (n & 1) * kKeys, (uint32_t)dv + s * (L::kTile >> 4), (uint32_t)(dv >> 32),
+                            idesc_o, pv_first ? 0u : 1u, pv_done(s));
+            pv_own = next_own;
+            pv_first = next_first;
             if (n + 2 < tiles) do_s(n + 2);
+            next_own = own;
+            next_first = first;
         }
         umma_commit_e(done_bar);
         warp_wait(done_bar, 0, err, abort_flag);
