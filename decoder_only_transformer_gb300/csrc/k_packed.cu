@@ -280,9 +280,8 @@ cudaError_t launch_f32(const PackedArgs& a, cudaStream_t st) {
 // even group two neighbouring query heads on the same rows (equal lengths, no
 // half-empty pair in short sequences), otherwise two neighbouring tiles of one
 // head.  The list holds one entry per block of kRows rows (128 or 256) of a
-// sequence, the longest key ranges first, so that the persistent kernel's snake
-// order deals every CTA about the same number of key tiles whatever the lengths
-// are.
+// sequence, the longest key ranges first, from which the persistent kernel's CTAs take
+// their items.
 //
 // Blocks are found without a scan: block t of sequence b has the slot
 // cu[b] / kRows + b + t, slots of different sequences never meet (a sequence of
@@ -373,7 +372,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_packed_plan(const int32_t* __r
     int before = 0;
     for (int w = 0; w < warp; ++w) before += warp_sum[w];
     bins[tid] = before + sum - n;
-    if (tid == kPlanThreads - 1) *count = before + sum;
+    if (tid == kPlanThreads - 1) {
+        count[0] = before + sum;
+        count[1] = 0;                                  // items taken beyond the CTAs' first
+    }
     __syncthreads();
     if (found) list[atomicAdd(&bins[bin], 1)] = blk;
     for (int s = tid; s + kPlanThreads < slots; s += kPlanThreads)
@@ -387,7 +389,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_packed_plan(const int32_t* __r
 // of S: the softmax of one tile runs beside the products of the next, and a diagonal tile
 // is half as wide.  (Tiles of 128 with one place: 12 prompts of up to 2048 at 16/4 x 128 90 us
 // instead of 77, 24 of up to 1024 at 12 x 64 35.5 instead of 32.5; 3 of up to 8192 at
-// 12 x 64 the same 168.)  What bounds it is latency, of softmax and MMA warps alike: at
+// 16 x 64 the same 168.)  What bounds it is latency, of softmax and MMA warps alike: at
 // d_head 64 a pair of tiles takes 1210 cycles, of them ~510 the exponentials of both on
 // the MUFU, ~550 the tensor pipe; without exponentials it takes 960, without any
 // arithmetic of the softmax 860, and with a quarter of the MMAs besides 690.  (Two CTAs per
@@ -397,6 +399,7 @@ constexpr int kThreadsP = 384;          // control, softmax of tile A, softmax o
 constexpr int kKV = 64;                 // keys per tile
 constexpr float kRescale = 8.0f;        // log2 units: P entries stay below 2^8
 constexpr int kPoison = 8;
+constexpr int kItems = 8;               // entries of work items in shared memory
 
 template <int DH>
 struct Pk {
@@ -414,9 +417,10 @@ struct Pk {
     static constexpr int kStage = 32 * kStageRow;
     static constexpr int kStageOff = kVOff + kRing * kTile;
     static constexpr int kBarOff = kStageOff + 8 * kStage;
-    static constexpr int kNumBars = 2 * kNQ + 3 * kRing + 13;
+    static constexpr int kNumBars = 2 * kNQ + 3 * kRing + 2 * kItems + 13;
     static constexpr int kMiscOff = kBarOff + 8 * kNumBars;
-    static constexpr int kBytes = kMiscOff + 16 + 4 * kPoison + 1024;
+    static constexpr int kItemOff = kMiscOff + 16 + 4 * kPoison;
+    static constexpr int kBytes = kItemOff + 32 * kItems + 16 + 1024;
     // tensor-memory columns: S (2 x 2 x 64, P in its place), O (2 x DH)
     static constexpr int kOCol = 4 * kKV;
     static constexpr uint32_t kSwz = DH == 32 ? 4u : 2u;
@@ -448,7 +452,8 @@ __device__ __forceinline__ int div_by(int x, int d, uint32_t inv) {
     return x - q * d >= d ? q + 1 : q;
 }
 
-__device__ __forceinline__ void make_item(Item& it, const int4 a, const int4 b, int sub, const PackedGeom& gm) {
+__device__ __forceinline__ void make_item(Item& it, const int4 a, const int4 b, const PackedGeom& gm) {
+    const int sub = b.w;
     constexpr int kPer = 128 / kKV;                    // a block's entry counts in 128 keys
     it.start = a.x;
     it.len = a.y;
@@ -489,7 +494,7 @@ template <int DH, bool kWin>
 __global__ void __launch_bounds__(kThreadsP, 1)
     k_packed_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap, const __nv_bfloat16* __restrict__ v,
-                __nv_bfloat16* __restrict__ o, const int* __restrict__ count,
+                __nv_bfloat16* __restrict__ o, int* __restrict__ count,
                 const Block* __restrict__ list, PackedGeom gm, int64_t vt, int64_t vh, int64_t ot,
                 int64_t oh, float scale_log2, int* err) {
     using L = Pk<DH>;
@@ -514,6 +519,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     auto o_done = [&](int x, int n) { return bars + 8u * (B1 + 8 + 2 * x + (n & 1)); };
     auto phase = [&](int n) { return (uint32_t)(n >> 1) & 1u; };
     const uint32_t done_bar = bars + 8u * (B1 + 12);
+    auto item_full = [&](int i) { return bars + 8u * (B1 + 13 + i); };
+    auto item_empty = [&](int i) { return bars + 8u * (B1 + 13 + kItems + i); };
+    const uint32_t item_at = base + (L::kItemOff + 15 & ~15);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(gbase + L::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMiscOff + 4);
     volatile int* poison = reinterpret_cast<volatile int*>(gbase + L::kMiscOff + 16);
@@ -535,6 +543,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 mbar_init(p_full(x, i), 4);
                 mbar_init(o_done(x, i), 1);
             }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(item_full(i), 1);
+            mbar_init(item_empty(i), kThreadsP / 32 - 1);
+        }
         mbar_init(done_bar, 2);
         abort_flag[0] = abort_flag[1] = 0;
         for (int i = 0; i < kPoison; ++i) poison[i] = 0;
@@ -551,51 +563,67 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     pdl_wait();
     pdl_trigger();
 
-    // Items are dealt round by round in snake order (even rounds c, odd rounds
-    // G-1-c); every role walks the same sequence, loading the entry of its next
-    // item while it works on the current one.
-    const int total = gm.cu ? 0 : __ldg(count) * gm.subs;
-    const int G = (int)gridDim.x, c = (int)blockIdx.x;
-    const int rounds = (total + G - 1) / G;
-    auto index_of = [&](int rnd) { return rnd * G + ((rnd & 1) ? G - 1 - c : c); };
-    int4 ea, eb;                                       // entry of the next item, its sub-item
-    int sub = 0, at_round = 0;
-    auto look_ahead = [&]() {
-        const int idx = index_of(at_round);
-        eb.x = 0;
-        if (at_round >= rounds || idx >= total) return;
-        const int k = div_by(idx, gm.subs, gm.subs_inv);
-        const int4* e = reinterpret_cast<const int4*>(list + k);
-        ea = __ldg(e);
-        eb = __ldg(e + 1);
-        sub = idx - k * gm.subs;
-    };
-    if (gm.cu) {
-        // One item a CTA, found by each warp itself.
-        eb.x = 0;
-        const int slot = c / gm.subs, rows = gm.by_heads ? 128 : 256, b = sequence_of(gm.cu, gm.n_seq, rows, slot);
-        Block blk;
-        if (b >= 0 && make_block(blk, seq_range(__ldg(gm.cu + b), __ldg(gm.cu + b + 1), gm.T), b, slot, rows, gm.window)) {
-            ea = make_int4(blk.start, blk.len, blk.row, blk.j0);
-            eb = make_int4(blk.n0, blk.n1, blk.lo1, 0);
-            sub = c - slot * gm.subs;
-        }
-        if (c == 0)
-            for (int k = threadIdx.x; k < gm.n_seq; k += kThreadsP) {
-                const int from = __ldg(gm.cu + k), to = __ldg(gm.cu + k + 1);
-                if (from < 0 || from > to || to > gm.T) raise_error(err, TFM_EINVAL);
+    // A CTA's first item is its own number, each further one the next in the list that no CTA
+    // has taken yet: the longest come first, so that all end together (dealt in a fixed order,
+    // to and fro: 77 us instead of 73 for 12 prompts at 16/4 x 128, 167 instead of 163 for 3
+    // of up to 8192 at 16 x 64).  The TMA warp takes it and leaves its entry for the others.
+    int n_item = 0;
+    auto take_item = [&](Item& it) -> bool {
+        const int slot = n_item % kItems, c = (int)blockIdx.x;
+        if (n_item >= kItems && !warp_wait(item_empty(slot), ((uint32_t)(n_item / kItems) & 1u) ^ 1u, err, abort_flag))
+            return false;
+        int4 ea = make_int4(0, 0, 0, 0), eb = ea;      // none: no key tiles
+        if (gm.cu) {
+            if (n_item == 0) {
+                const int k = c / gm.subs, rows = gm.by_heads ? 128 : 256, b = sequence_of(gm.cu, gm.n_seq, rows, k);
+                Block blk;
+                if (b >= 0 && make_block(blk, seq_range(__ldg(gm.cu + b), __ldg(gm.cu + b + 1), gm.T), b, k, rows, gm.window)) {
+                    ea = make_int4(blk.start, blk.len, blk.row, blk.j0);
+                    eb = make_int4(blk.n0, blk.n1, blk.lo1, c - k * gm.subs);
+                }
             }
-    } else {
-        look_ahead();
-    }
-    // The next item; false when there is none.
-    auto next_item = [&](Item& it) -> bool {
-        if (eb.x == 0) return false;                   // only the last round can be short
-        make_item(it, ea, eb, sub, gm);
-        ++at_round;
-        look_ahead();
+        } else {
+            int idx = c;
+            if (n_item > 0) {
+                if (lane == 0) idx = (int)gridDim.x + atomicAdd(count + 1, 1);
+                idx = __shfl_sync(0xffffffffu, idx, 0);
+            }
+            if (idx < __ldg(count) * gm.subs) {
+                const int k = div_by(idx, gm.subs, gm.subs_inv);
+                const int4* e = reinterpret_cast<const int4*>(list + k);
+                ea = __ldg(e);
+                eb = __ldg(e + 1);
+                eb.w = idx - k * gm.subs;
+            }
+        }
+        if (lane == 0) {
+            st_shared_v4(item_at + slot * 32, ea.x, ea.y, ea.z, ea.w);
+            st_shared_v4(item_at + slot * 32 + 16, eb.x, eb.y, eb.z, eb.w);
+            mbar_arrive(item_full(slot));
+        }
+        __syncwarp();
+        ++n_item;
+        if (eb.x == 0) return false;
+        make_item(it, ea, eb, gm);
         return true;
     };
+    // The next item, for the other warps; false when there is none.
+    auto next_item = [&](Item& it) -> bool {
+        const int slot = n_item % kItems;
+        if (!warp_wait(item_full(slot), (uint32_t)(n_item / kItems) & 1u, err, abort_flag)) return false;
+        const uint4 a = ld_shared_v4(item_at + slot * 32), b = ld_shared_v4(item_at + slot * 32 + 16);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(item_empty(slot));
+        ++n_item;
+        if (b.x == 0) return false;
+        make_item(it, make_int4(a.x, a.y, a.z, a.w), make_int4(b.x, b.y, b.z, b.w), gm);
+        return true;
+    };
+    if (gm.cu && blockIdx.x == 0)
+        for (int k = threadIdx.x; k < gm.n_seq; k += kThreadsP) {
+            const int from = __ldg(gm.cu + k), to = __ldg(gm.cu + k + 1);
+            if (from < 0 || from > to || to > gm.T) raise_error(err, TFM_EINVAL);
+        }
 
     constexpr uint32_t idesc_s = umma_idesc_bf16(kQ, kKV);
     constexpr uint32_t idesc_o = umma_idesc_bf16(kQ, DH, true);
@@ -614,7 +642,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         bool ok = true, has = true;
         Item it;
         while (has && ok) {
-            has = next_item(it);
+            has = take_item(it);
             if (!has && u == 0) break;                 // nothing at all
             const int nmax = has ? (int)uniform(it.nmax) : 1, two = has ? (int)uniform(it.n[1]) : 0;
 #pragma unroll
@@ -774,7 +802,6 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         while (ok && t_max > 0) {
             const int nmax = t_max, lo = t_lo, n = t_n, qs = t_q;
             int j = 0;
-            if (n == 0) fetch();
             for (; j < lo && ok; ++j) pass();
             const uint32_t q_lo = (uint32_t)dq + (qs % NQ) * (L::kQTile >> 4);
             for (; j < n && ok; j += 2) {
@@ -790,9 +817,12 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 release();
                 pv = true;
                 pair ^= 1u;
-                if (j == lo) fetch();                  // not when its first S is due
+                // (before the next item's first S is due; its entry waits for none of this
+                // warp's rounds: all their tiles are on their way)
+                if (j == n - 2) fetch();
             }
             for (; j < nmax && ok; ++j) pass();
+            if (n == 0 && ok) fetch();
         }
         if (any && ok) pass();
         umma_commit_e(done_bar);
@@ -975,7 +1005,7 @@ cudaError_t launch_tc(const PackedArgs& a, const CUtensorMap* maps, const Packed
     const int grid = items < sm_count() ? (int)items : sm_count();
     return launch_pdl(k_packed_tc<DH, kWin>, dim3(grid), dim3(kThreadsP), L::kBytes, st, maps[0], maps[1], maps[2],
                       static_cast<const __nv_bfloat16*>(a.v), static_cast<__nv_bfloat16*>(a.o),
-                      static_cast<const int*>(a.ws),
+                      static_cast<int*>(a.ws),
                       reinterpret_cast<const Block*>(static_cast<const uint8_t*>(a.ws) + 256), gm,
                       a.strides[4], a.strides[5], a.strides[6], a.strides[7],
                       a.scale * 1.4426950408889634f, device_error_word());
