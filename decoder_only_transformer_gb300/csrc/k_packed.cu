@@ -636,44 +636,56 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     if (warp == 0) {
         // ---------------------------------------------------------- TMA producer
-        // Per step K of a round and V of the round before; Q_A and Q_B before the first
-        // K of an item.
+        // Per step K of a round and V of the round before; Q_A and Q_B behind the first K of
+        // an item, as their slots may still be read and the last V of the item before is
+        // waited for.  The next item is taken before the last round is loaded: two trips to L2
+        // that are over when its first K is due.
         int qn = 0, u = 0, vy = 0, vg = 0;             // Q tiles, steps; place of the V to be loaded
-        bool ok = true, has = true;
-        Item it;
+        bool ok = true;
+        auto load_v = [&](int s) {
+#pragma unroll
+            for (int c2 = 0; c2 < L::kSub; ++c2)
+                tma_load_3d_e(sV + s * L::kTile + c2 * L::kSubKV, &vmap, 64 * c2, vy, vg, full(s));
+        };
+        auto slot_free = [&]() -> bool {
+            return u < R || (ok = warp_wait(empty(u % R), ((uint32_t)(u / R) & 1u) ^ 1u, err, abort_flag));
+        };
+        Item it, next;
+        bool has = take_item(it);
         while (has && ok) {
-            has = take_item(it);
-            if (!has && u == 0) break;                 // nothing at all
-            const int nmax = has ? (int)uniform(it.nmax) : 1, two = has ? (int)uniform(it.n[1]) : 0;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (!ok || !has || (x && !two)) continue;
-                const int s = qn % NQ;
-                if (qn >= NQ) ok = warp_wait(q_empty(s), ((uint32_t)(qn / NQ) & 1u) ^ 1u, err, abort_flag);
-                if (!ok) continue;
-                mbar_arrive_expect_tx_e(q_full(s), L::kQTile);
-#pragma unroll
-                for (int c2 = 0; c2 < L::kSub; ++c2)
-                    tma_load_3d_e(sQ + s * L::kQTile + c2 * L::kSubQ, &qmap, 64 * c2, it.start + it.row[x], it.h[x], q_full(s));
-                ++qn;
-            }
+            const int nmax = (int)uniform(it.nmax), two = (int)uniform(it.n[1]);
             int y = it.start + it.j0 * kKV;            // the next K tile's first row
             for (int j = 0; j < nmax && ok; ++j, ++u, y += kKV) {
                 const int s = u % R;
-                if (u >= R) ok = warp_wait(empty(s), ((uint32_t)(u / R) & 1u) ^ 1u, err, abort_flag);
-                if (!ok) break;
-                mbar_arrive_expect_tx_e(full(s), (has ? L::kTile : 0) + (u > 0 ? L::kTile : 0));
-                if (has)
+                if (j == nmax - 1) has = take_item(next);
+                if (!slot_free()) break;
+                mbar_arrive_expect_tx_e(full(s), u > 0 ? 2 * L::kTile : L::kTile);
 #pragma unroll
-                    for (int c2 = 0; c2 < L::kSub; ++c2)
-                        tma_load_3d_e(sK + s * L::kTile + c2 * L::kSubKV, &kmap, 64 * c2, y, it.g, full(s));
-                if (u > 0)
-#pragma unroll
-                    for (int c2 = 0; c2 < L::kSub; ++c2)
-                        tma_load_3d_e(sV + s * L::kTile + c2 * L::kSubKV, &vmap, 64 * c2, vy, vg, full(s));
+                for (int c2 = 0; c2 < L::kSub; ++c2)
+                    tma_load_3d_e(sK + s * L::kTile + c2 * L::kSubKV, &kmap, 64 * c2, y, it.g, full(s));
+                if (u > 0) load_v(s);
                 vy = y;
                 vg = it.g;
+                if (j > 0) continue;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (!ok || (x && !two)) continue;
+                    const int q = qn % NQ;
+                    if (qn >= NQ) ok = warp_wait(q_empty(q), ((uint32_t)(qn / NQ) & 1u) ^ 1u, err, abort_flag);
+                    if (!ok) continue;
+                    mbar_arrive_expect_tx_e(q_full(q), L::kQTile);
+#pragma unroll
+                    for (int c2 = 0; c2 < L::kSub; ++c2)
+                        tma_load_3d_e(sQ + q * L::kQTile + c2 * L::kSubQ, &qmap, 64 * c2, it.start + it.row[x], it.h[x], q_full(q));
+                    ++qn;
+                }
             }
+            it = next;
+        }
+        if (ok && u > 0 && slot_free()) {              // the last V
+            mbar_arrive_expect_tx_e(full(u % R), L::kTile);
+            load_v(u % R);
+            ++u;
         }
         // The other warps wait for every load; after a wait that gave up, the last
         // ones still have to land before the CTA ends.
@@ -806,9 +818,15 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             const uint32_t q_lo = (uint32_t)dq + (qs % NQ) * (L::kQTile >> 4);
             for (; j < n && ok; j += 2) {
                 if (!ready()) break;
-                if (j == lo && !(ok = warp_wait_short(q_full(qs % NQ), (uint32_t)(qs / NQ) & 1u, err, abort_flag))) break;
-                scores(q_lo, 0);
-                if (pv && !values(1, pair ^ 1u, 1u)) break;
+                if (j == lo) {
+                    // the last P.V of the item before is waited for, Q may still be on its way
+                    if (pv && !values(1, pair ^ 1u, 1u)) break;
+                    if (!(ok = warp_wait_short(q_full(qs % NQ), (uint32_t)(qs / NQ) & 1u, err, abort_flag))) break;
+                    scores(q_lo, 0);
+                } else {
+                    scores(q_lo, 0);
+                    if (!values(1, pair ^ 1u, 1u)) break;
+                }
                 release();
                 if (!ready()) break;
                 scores(q_lo, 1);
