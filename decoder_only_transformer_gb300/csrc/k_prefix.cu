@@ -82,10 +82,6 @@ __device__ __forceinline__ int run_start(int i, int u, int n) {
     const int q = u / n, r = u - q * n;
     return i * q + min(i, r);
 }
-__device__ __forceinline__ int cta_of(int x, int u, int n) {
-    const int q = u / n, r = u - q * n, split = r * (q + 1);
-    return x < split ? x / (q + 1) : r + (x - split) / q;
-}
 
 __device__ __forceinline__ int own_len(const int32_t* __restrict__ lens, int b, int max_seq) {
     const int n = __ldg(lens + b);
@@ -183,6 +179,7 @@ __device__ __forceinline__ void scan_lengths(int* cum, int* cost, int* slen, int
         const int b = b0 + tid;
         const int len = b < gm.B ? own_len(lens, b, gm.max_seq) : 0;
         if (b < gm.B) slen[b] = len;
+        if (b == 0) cum[0] = cost[0] = 0;
         int sum = (len + kKeys - 1) / kKeys;
         int sum_c = sum ? Px<DH>::kOwnPiece + sum * Px<DH>::kOwnTile : 0;
 #pragma unroll
@@ -210,8 +207,6 @@ __device__ __forceinline__ void scan_lengths(int* cum, int* cost, int* slen, int
         }
         __syncthreads();
     }
-    if (tid == 0) cum[0] = cost[0] = 0;
-    __syncthreads();
 }
 
 // Cost of everything, and of a job of the prefix.
@@ -255,7 +250,9 @@ struct PrefixParts {
     float2* ml_prefix;     // [jobs + ctas][128]: max (log2), sum
     float* o_own;          // [B Hkv + ctas][dh / 4][GT][4]
     float2* ml_own;        // [B Hkv + ctas][GT]
-    int* cost;             // [B + 1]
+    // per job of the prefix, and of the own caches: the CTAs of its first and last piece
+    int2* range_prefix;    // [jobs]
+    int2* range_own;       // [B Hkv], of caches that hold keys
 };
 
 // Adds the values of keys [k0, k1) that are not finite to a row's partial O in
@@ -344,15 +341,14 @@ __global__ void __launch_bounds__(kThreadsX, 2)
     scan_lengths<DH>(cum, cost, slen, warp_sum, lens, gm);
     const int cta = (int)blockIdx.x;
     if (cta == 0)
-        for (int b = threadIdx.x; b <= gm.B; b += kThreadsX) {
-            out.cost[b] = cost[b];
-            if (b < gm.B && (lens[b] < 0 || lens[b] > gm.max_seq)) raise_error(err, TFM_EINVAL);
-        }
+        for (int b = threadIdx.x; b < gm.B; b += kThreadsX)
+            if (lens[b] < 0 || lens[b] > gm.max_seq) raise_error(err, TFM_EINVAL);
     const int up = gm.Hkv * gm.nrt * gm.np;
     const int all = prefix_job_cost<DH>(gm) * gm.Hkv * gm.nrt + cost[gm.B] * gm.Hkv;
     const int runs = runs_of<DH>(all, gm.ctas);
-    const int u0 = cta < runs ? tiles_before<DH>(run_start(cta, all, runs), gm, cum, cost) : 0;
-    const int u1 = cta < runs ? tiles_before<DH>(run_start(cta + 1, all, runs), gm, cum, cost) : 0;
+    // the run's ends, one in the even and one in the odd lanes
+    const int edge = cta < runs ? tiles_before<DH>(run_start(cta + (lane & 1), all, runs), gm, cum, cost) : 0;
+    const int u0 = __shfl_sync(0xffffffffu, edge, 0), u1 = __shfl_sync(0xffffffffu, edge, 1);
     const Walk walk = start_walk(u0, u1, up, gm, cum);
     const int tiles = (int)uniform(walk.left);         // of this CTA, in all its pieces
     const int own0 = max(0, min(tiles, up - u0));   // its first own tile
@@ -658,6 +654,11 @@ __global__ void __launch_bounds__(kThreadsX, 2)
             const int64_t row = piece * stride + r;
             float4* orow = reinterpret_cast<float4*>((sg.own ? out.o_own : out.o_prefix) + piece * stride * DH) + r;
             if (mine) (sg.own ? out.ml_own : out.ml_prefix)[row] = make_float2(m, l);
+            if (threadIdx.x == 0) {
+                int2* range = (sg.own ? out.range_own : out.range_prefix) + job_of(sg, gm);
+                if (sg.t0 == 0) range->x = cta;
+                if (sg.t1 == (sg.own ? cum[sg.x + 1] - cum[sg.x] : gm.np)) range->y = cta;
+            }
 #pragma unroll 1
             for (int c = 0; c < DH / 32; ++c) {
                 float v[32];
@@ -696,6 +697,7 @@ __global__ void __launch_bounds__(kThreadsX, 2)
 // 128 rows of a row tile, whose prefix pieces lie side by side.
 template <int DH>
 __global__ void __launch_bounds__(kRowsP) k_prefix_join(PrefixParts in, PrefixGeom gm, int H,
+                                                        const int32_t* __restrict__ lens,
                                                         __nv_bfloat16* __restrict__ o) {
     constexpr int S = DH / 4;
     const int c4 = (int)blockIdx.x % S, pj = (int)blockIdx.x / S;
@@ -704,21 +706,17 @@ __global__ void __launch_bounds__(kRowsP) k_prefix_join(PrefixParts in, PrefixGe
     pdl_wait();
     pdl_trigger();
     if (r >= gm.nb * gm.GT || b >= gm.B) return;
-    const int c0 = __ldg(in.cost + b), each = __ldg(in.cost + b + 1) - c0;
-    const int jc = prefix_job_cost<DH>(gm), own_from = jc * gm.Hkv * gm.nrt;
-    const int all = own_from + __ldg(in.cost + gm.B) * gm.Hkv, runs = runs_of<DH>(all, gm.ctas);
-    // The pieces of a job: one per CTA from that of the first tile's end to that of
-    // the last one's.
+    // The pieces of a job: one per CTA from that of its first tile to that of its last.
+    // (In bounds even where a kernel that gave up left them unwritten.)
     int n_pre = 0, n_own = 0, first_pre = 0, first_own = 0;
-    if (jc) {
-        first_pre = cta_of(pj * jc + Px<DH>::kPrePiece + Px<DH>::kPreTile - 1, all, runs);
-        n_pre = cta_of((pj + 1) * jc - 1, all, runs) - first_pre + 1;
-    }
-    if (each) {
-        const int a = own_from + c0 * gm.Hkv + g * each;
-        first_own = cta_of(a + Px<DH>::kOwnPiece + Px<DH>::kOwnTile - 1, all, runs);
-        n_own = cta_of(a + each - 1, all, runs) - first_own + 1;
-    }
+    auto pieces = [&](const int2 range, int& first, int& n) {
+        first = min(max(range.x, 0), gm.ctas - 1);
+        n = min(max(range.y, first), gm.ctas - 1) - first + 1;
+    };
+    const int keys = own_len(lens, b, gm.max_seq);
+    const int2 range_own = __ldcg(in.range_own + b * gm.Hkv + g);
+    if (gm.np) pieces(__ldcg(in.range_prefix + pj), first_pre, n_pre);
+    if (keys) pieces(range_own, first_own, n_own);
     const int64_t pre = pj + first_pre, own = (int64_t)b * gm.Hkv + g + first_own;
     const float2* ml_pre = in.ml_prefix + pre * kRowsP + r;
     const float2* ml_own = in.ml_own + own * gm.GT + i;
@@ -793,7 +791,7 @@ PrefixGeom geom_of(int B, int H, int Hkv, int T, int P, int max_seq, int dh) {
 }
 
 struct PrefixLayout {
-    size_t o_prefix, ml_prefix, o_own, ml_own, cost, total;
+    size_t o_prefix, ml_prefix, o_own, ml_own, range_prefix, range_own, total;
 };
 PrefixLayout layout(const PrefixGeom& g, int dh) {
     PrefixLayout l{};
@@ -808,7 +806,8 @@ PrefixLayout layout(const PrefixGeom& g, int dh) {
     l.ml_prefix = take(np * kRowsP * 8);
     l.o_own = take(no * g.GT * dh * 4);
     l.ml_own = take(no * g.GT * 8);
-    l.cost = take(((size_t)g.B + 1) * 4);
+    l.range_prefix = take((size_t)g.Hkv * g.nrt * 8);
+    l.range_own = take((size_t)g.B * g.Hkv * 8);
     l.total = off;
     return l;
 }
@@ -828,7 +827,8 @@ cudaError_t launch_dh(const PrefixArgs& a, PrefixGeom g, const CUtensorMap* maps
     parts.ml_prefix = reinterpret_cast<float2*>(w + l.ml_prefix);
     parts.o_own = reinterpret_cast<float*>(w + l.o_own);
     parts.ml_own = reinterpret_cast<float2*>(w + l.ml_own);
-    parts.cost = reinterpret_cast<int*>(w + l.cost);
+    parts.range_prefix = reinterpret_cast<int2*>(w + l.range_prefix);
+    parts.range_own = reinterpret_cast<int2*>(w + l.range_own);
     // two CTAs per SM; no more than there can be tiles
     const int64_t most = (int64_t)g.Hkv * g.nrt * g.np +
                          (int64_t)g.B * g.Hkv * ((a.max_seq + kKeys - 1) / kKeys);
@@ -838,7 +838,7 @@ cudaError_t launch_dh(const PrefixArgs& a, PrefixGeom g, const CUtensorMap* maps
                    maps[3], maps[4], maps[5], static_cast<const __nv_bfloat16*>(a.vc), a.lens, g, parts,
                    a.scale * 1.4426950408889634f, device_error_word());
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_prefix_join<DH>, dim3((unsigned)(g.Hkv * g.nrt * (DH / 4))), dim3(kRowsP), 0, st, parts, g, a.H,
+    return launch_pdl(k_prefix_join<DH>, dim3((unsigned)(g.Hkv * g.nrt * (DH / 4))), dim3(kRowsP), 0, st, parts, g, a.H, a.lens,
                       static_cast<__nv_bfloat16*>(a.o));
 }
 
