@@ -115,30 +115,6 @@ __device__ __forceinline__ void skip_empty(Walk& w, const PrefixGeom& gm, const 
     while (w.x < gm.B && cum[w.x + 1] == cum[w.x]) ++w.x;
 }
 
-__device__ __forceinline__ Walk start_walk(int u, int end, int up, const PrefixGeom& gm, const int* cum) {
-    Walk w{end - u, 0, 0, 0, 0};
-    if (end <= u) return w;
-    if (u < up) {
-        const int job = u / gm.np;
-        w.t = u - job * gm.np;
-        w.g = job / gm.nrt;
-        w.x = job - w.g * gm.nrt;
-    } else {
-        const int v = u - up;
-        int lo = 0, hi = gm.B;                        // the last b with cum[b] Hkv <= v and keys
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (cum[mid] * gm.Hkv <= v) lo = mid + 1; else hi = mid;
-        }
-        w.own = 1;
-        w.x = lo - 1;
-        const int nt = cum[lo] - cum[lo - 1], y = v - cum[lo - 1] * gm.Hkv;
-        w.g = y / nt;
-        w.t = y - w.g * nt;
-    }
-    return w;
-}
-
 __device__ __forceinline__ bool next_seg(Walk& w, Seg& s, const PrefixGeom& gm, const int* cum) {
     if (w.left <= 0) return false;
     s = Seg{w.own, w.g, w.x, w.t, min(w.own ? cum[w.x + 1] - cum[w.x] : gm.np, w.t + w.left)};
@@ -223,25 +199,36 @@ __device__ __forceinline__ int runs_of(int all, int ctas) {
     return max(1, min(ctas, all / most));
 }
 
-// The number of tiles that lie before cost c: a job's tiles end at its piece cost
-// plus one tile cost each.
+// The tile at cost c (a job's tiles end at its piece cost plus one tile cost each), and
+// how many lie before it.
 template <int DH>
-__device__ __forceinline__ int tiles_before(int c, const PrefixGeom& gm, const int* cum, const int* cost) {
+__device__ __forceinline__ Walk tile_at(int c, int& before, const PrefixGeom& gm, const int* cum, const int* cost) {
     const int jc = prefix_job_cost<DH>(gm), jobs = gm.Hkv * gm.nrt;
+    Walk w{0, 0, 0, 0, 0};
     if (c < jc * jobs) {
         const int job = c / jc;
-        return job * gm.np + max(0, (c - job * jc - Px<DH>::kPrePiece) / Px<DH>::kPreTile);
+        w.t = max(0, (c - job * jc - Px<DH>::kPrePiece) / Px<DH>::kPreTile);
+        w.g = job / gm.nrt;
+        w.x = job - w.g * gm.nrt;
+        before = job * gm.np + w.t;
+        return w;
     }
     const int v = c - jc * jobs, up = jobs * gm.np;
-    if (v >= cost[gm.B] * gm.Hkv) return up + gm.Hkv * cum[gm.B];
+    before = up + gm.Hkv * cum[gm.B];
+    if (v >= cost[gm.B] * gm.Hkv) return w;            // the end
     int lo = 0, hi = gm.B;                            // the last b with cost[b] Hkv <= v
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (cost[mid] * gm.Hkv <= v) lo = mid + 1; else hi = mid;
     }
     const int b = lo - 1, each = cost[lo] - cost[b], nt = cum[lo] - cum[b];
-    const int x = v - cost[b] * gm.Hkv, g = x / each;
-    return up + gm.Hkv * cum[b] + g * nt + max(0, (x - g * each - Px<DH>::kOwnPiece) / Px<DH>::kOwnTile);
+    const int x = v - cost[b] * gm.Hkv;
+    w.own = 1;
+    w.g = x / each;
+    w.x = b;
+    w.t = max(0, (x - w.g * each - Px<DH>::kOwnPiece) / Px<DH>::kOwnTile);
+    before = up + gm.Hkv * cum[b] + w.g * nt + w.t;
+    return w;
 }
 
 struct PrefixParts {
@@ -347,9 +334,15 @@ __global__ void __launch_bounds__(kThreadsX, 2)
     const int all = prefix_job_cost<DH>(gm) * gm.Hkv * gm.nrt + cost[gm.B] * gm.Hkv;
     const int runs = runs_of<DH>(all, gm.ctas);
     // the run's ends, one in the even and one in the odd lanes
-    const int edge = cta < runs ? tiles_before<DH>(run_start(cta + (lane & 1), all, runs), gm, cum, cost) : 0;
-    const int u0 = __shfl_sync(0xffffffffu, edge, 0), u1 = __shfl_sync(0xffffffffu, edge, 1);
-    const Walk walk = start_walk(u0, u1, up, gm, cum);
+    int before = 0;
+    Walk walk{0, 0, 0, 0, 0};
+    if (cta < runs) walk = tile_at<DH>(run_start(cta + (lane & 1), all, runs), before, gm, cum, cost);
+    const int u0 = __shfl_sync(0xffffffffu, before, 0), u1 = __shfl_sync(0xffffffffu, before, 1);
+    walk.left = u1 - u0;
+    walk.own = __shfl_sync(0xffffffffu, walk.own, 0);
+    walk.g = __shfl_sync(0xffffffffu, walk.g, 0);
+    walk.x = __shfl_sync(0xffffffffu, walk.x, 0);
+    walk.t = __shfl_sync(0xffffffffu, walk.t, 0);
     const int tiles = (int)uniform(walk.left);         // of this CTA, in all its pieces
     const int own0 = max(0, min(tiles, up - u0));   // its first own tile
     auto p_full = [&](bool own, int n) { return own ? p_own(n & 1) : p_pre(n & 1); };
