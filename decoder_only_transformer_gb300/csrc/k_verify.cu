@@ -14,8 +14,8 @@
 // merges them, a CTA per sequence, and decides which tokens are accepted.  The third
 // runs the race over the one row of p (and q) that is then needed, a CTA per chunk;
 // the last CTA of a sequence to finish merges the chunks' winners and writes the
-// answer.  (Deciding again in every CTA of the race saved a launch but made 13 chains of
-// dependent loads of one, and 22 us of the race at 64 sequences of 50257 logits.)
+// answer.  A race of few CTAs decides itself, without the second launch; of many, each
+// would repeat 13 chains of dependent loads.
 // Bound by reading the logits.
 //
 // Both decisions compare computed numbers, so a rounding may turn them.  The
@@ -38,6 +38,7 @@ constexpr int kThreads = 256;
 constexpr int kVec = 8, kRaceVec = 4;
 constexpr int kChunk = kThreads * kVec * 4, kRaceChunk = kThreads * kRaceVec * 4;
 constexpr int kMaxK = 64;
+constexpr int kFewCtas = 128;           // of the race: it decides itself then
 // Relative error of an fp32 weight e^((z - m) / temperature): the exponent
 // x = (z - m) log2(e) / temperature carries three roundings, 3 * 2^-24 |x|, so
 // the weight 0.7 * 3 * 2^-24 |x| <= 1.6e-5 down to the smallest normal number
@@ -175,6 +176,7 @@ __global__ void __launch_bounds__(kThreads) k_verify_stats(const VerifyParams p)
     const int per = is_draft ? a.K : a.K + 1;
     const int b = r / per, i = r - b * per;
     const int nd = drafted(a, b, p.err);
+    if (!kGreedy && !is_draft && i == 0 && c == 0 && threadIdx.x == 0) p.done[b] = 0;
     if (is_draft ? i >= nd : i > nd) return;          // a row nobody asks for
     float z[4 * kVec];
     load_chunk<kVec>(is_draft ? a.dlogits + (int64_t)r * a.ld_draft : a.target + (int64_t)r * a.ld_target, c, a.V,
@@ -278,15 +280,13 @@ __device__ __forceinline__ void write_answer(const VerifyArgs& a, int b, int n, 
     if (lane == 0) a.n_accepted[b] = n;
 }
 
-// Which drafted tokens of a sequence are accepted: a CTA per sequence, a warp per
-// place; what does not depend on one another is asked for together.
-__global__ void __launch_bounds__(kThreads) k_verify_decide(const VerifyParams p) {
+// Which drafted tokens of sequence b are accepted: by a CTA, a warp per place; what
+// does not depend on one another is asked for together.  The answer is thread 0's.
+__device__ __forceinline__ Decision decide(const VerifyParams& p, int b) {
     __shared__ float2 row_t[kMaxK + 1], row_d[kMaxK];     // maximum, sum
     __shared__ int take[kMaxK];
-    pdl_wait();
-    pdl_trigger();
     const VerifyArgs& a = p.a;
-    const int b = (int)blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nd = drafted(a, b, nullptr);
     const double temp = (double)a.temperature;
     for (int i = warp; i <= nd; i += kThreads / 32) {
@@ -329,15 +329,24 @@ __global__ void __launch_bounds__(kThreads) k_verify_decide(const VerifyParams p
         }
     }
     __syncthreads();
+    Decision d{};
     if (threadIdx.x == 0) {
         int n = 0;
         while (n < nd && take[n]) ++n;
         const bool refused = n < nd;
-        p.dec[b] = Decision{n, refused, row_t[n].x, row_t[n].y, refused ? row_d[n].x : 0.f, refused ? row_d[n].y : 0.f, {0, 0}};
-        p.done[b] = 0;
+        d = Decision{n, refused, row_t[n].x, row_t[n].y, refused ? row_d[n].x : 0.f, refused ? row_d[n].y : 0.f, {0, 0}};
     }
+    return d;
+}
+__global__ void __launch_bounds__(kThreads) k_verify_decide(const VerifyParams p) {
+    pdl_wait();
+    pdl_trigger();
+    const Decision d = decide(p, (int)blockIdx.x);
+    if (threadIdx.x == 0) p.dec[blockIdx.x] = d;
 }
 
+// kDecide: each CTA decides for itself (see launch_verify_draft).
+template <bool kDecide>
 __global__ void __launch_bounds__(kThreads, 4) k_verify_race(const VerifyParams p) {
     __shared__ float red[kThreads / 32];
     __shared__ double redv[kThreads / 32];
@@ -352,7 +361,13 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify_race(const VerifyParams 
     const float* erow = a.noise + (int64_t)b * a.ld_noise;
     float e[4 * kRaceVec];
     load_chunk<kRaceVec>(erow, c, a.V, 0.f, e);        // needed whatever the row is
-    const Decision d = p.dec[b];
+    __shared__ Decision own;
+    if (kDecide) {
+        const Decision mine = decide(p, b);
+        if (threadIdx.x == 0) own = mine;
+        __syncthreads();
+    }
+    const Decision d = kDecide ? own : p.dec[b];
     const int n = d.n;
     const bool refused = d.refused;
     const float mt = d.mt, st = d.st, md = d.md, sd = d.sd;
@@ -546,8 +561,13 @@ cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t st) {
                            : launch_pdl(k_verify_stats<false>, dim3(rows * p.C), dim3(kThreads), 0, st, p);
     if (e != cudaSuccess) return e;
     if (greedy) return launch_pdl(k_verify_greedy, dim3((a.B + 7) / 8), dim3(kThreads), 0, st, p);
+    // Few CTAs: they decide themselves, all at once, which saves a launch (one sequence of
+    // 4 drafted tokens and 32000 logits: 9.4 us instead of 10.2).  Many: a CTA per sequence
+    // decides first (16 of 4 and 50257: 15.9 us instead of 17.4, 64 of 5: 46 instead of 51).
+    const dim3 race((unsigned)(a.B * p.RC));
+    if ((int64_t)a.B * p.RC <= kFewCtas) return launch_pdl(k_verify_race<true>, race, dim3(kThreads), 0, st, p);
     e = launch_pdl(k_verify_decide, dim3((unsigned)a.B), dim3(kThreads), 0, st, p);
-    return e != cudaSuccess ? e : launch_pdl(k_verify_race, dim3((unsigned)(a.B * p.RC)), dim3(kThreads), 0, st, p);
+    return e != cudaSuccess ? e : launch_pdl(k_verify_race<false>, race, dim3(kThreads), 0, st, p);
 }
 
 }  // namespace tfm
