@@ -520,16 +520,19 @@ def decode_attention(q, k_cache, v_cache, o, pos, workspace, window=0, scale=0.0
 # does not hold are they looked at one by one, for the refusal to name the culprit.
 _Strides = ctypes.c_int64 * 8
 _torch_module = None
+_cuda_ready = False
 
 
 def _now():
     """The torch module and the current device's index (-2, which no tensor's is,
     before CUDA is in use)."""
-    global _torch_module
-    if _torch_module is None:
+    global _torch_module, _cuda_ready
+    if not _cuda_ready:
         _torch_module = _torch()
-    cuda = _torch_module.cuda
-    return _torch_module, cuda.current_device() if cuda.is_initialized() else -2
+        _cuda_ready = _torch_module.cuda.is_initialized()
+        if not _cuda_ready:
+            return _torch_module, -2
+    return _torch_module, _torch_module._C._cuda_getDevice()
 
 
 def _raw_stream(stream, device):
@@ -574,21 +577,22 @@ def packed_attention(q, k, v, o, cu_seqlens, workspace, window=0, scale=0.0, str
     device).  Query i sees keys i-window < j <= i of its sequence (0: all)."""
     lib = _lib or load()
     torch, here = _now()
-    if not (here == q.get_device() == k.get_device() == v.get_device() == o.get_device()
-            == cu_seqlens.get_device() == workspace.get_device()
+    shape, kv = q.shape, k.shape
+    sq, sk, sv, so = q.stride(), k.stride(), v.stride(), o.stride()
+    if not (len(shape) == 3 == len(kv) and here == q.get_device() == k.get_device() == v.get_device()
+            == o.get_device() == cu_seqlens.get_device() == workspace.get_device()
             and q.dtype is k.dtype is v.dtype is o.dtype and cu_seqlens.dtype is torch.int32
-            and q.dim() == 3 == k.dim() and q.shape == o.shape and k.shape == v.shape
-            and q.shape[0] == k.shape[0] and q.shape[2] == k.shape[2]
-            and 1 == q.stride(2) == k.stride(2) == v.stride(2) == o.stride(2)
+            and shape == o.shape and kv == v.shape and shape[0] == kv[0] and shape[2] == kv[2]
+            and 1 == sq[2] == sk[2] == sv[2] == so[2]
             and cu_seqlens.dim() == 1 and cu_seqlens.shape[0] and cu_seqlens.is_contiguous()
             and workspace.is_contiguous()):
         _refuse_packed(q, k, v, o, cu_seqlens, workspace)
-    T, H, dh = q.shape
-    strides = _Strides(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *o.stride()[:2])
+    T, H, dh = shape
     status = lib.tfm_packed_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                      cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1, T, H, k.shape[1], dh,
-                                      strides, scale, window, _mode_of(q), workspace.data_ptr(),
-                                      workspace.nbytes, _raw_stream(stream, here))
+                                      cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1, T, H, kv[1], dh,
+                                      _Strides(sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1]), scale,
+                                      window, _mode_of(q), workspace.data_ptr(), workspace.nbytes,
+                                      _raw_stream(stream, here))
     if status:
         _check(status)
 
@@ -629,20 +633,21 @@ def prefix_attention(q, k_prefix, v_prefix, k_cache, v_cache, o, lens, workspace
     lib = _lib or load()
     torch, here = _now()
     bf = torch.bfloat16
-    if not (here == q.get_device() == k_prefix.get_device() == v_prefix.get_device() == k_cache.get_device()
+    shape, cache, prefix = q.shape, k_cache.shape, k_prefix.shape
+    if not (len(shape) == 4 == len(cache) and len(prefix) == 3
+            and here == q.get_device() == k_prefix.get_device() == v_prefix.get_device() == k_cache.get_device()
             == v_cache.get_device() == o.get_device() == lens.get_device() == workspace.get_device()
             and bf is q.dtype is k_prefix.dtype is v_prefix.dtype is k_cache.dtype is v_cache.dtype is o.dtype
-            and lens.dtype is torch.int32 and q.dim() == 4 == k_cache.dim() and k_prefix.dim() == 3
-            and k_cache.shape == v_cache.shape and k_prefix.shape == v_prefix.shape
-            and k_cache.shape[0] >= q.shape[0] and k_cache.shape[3] == q.shape[3] == k_prefix.shape[2]
-            and k_prefix.shape[0] == k_cache.shape[1] and lens.numel() == q.shape[0] and o.numel() == q.numel()
+            and lens.dtype is torch.int32 and cache == v_cache.shape and prefix == v_prefix.shape
+            and cache[0] >= shape[0] and cache[3] == shape[3] == prefix[2] and prefix[0] == cache[1]
+            and lens.numel() == shape[0] and o.numel() == q.numel()
             and q.is_contiguous() and k_prefix.is_contiguous() and v_prefix.is_contiguous()
             and k_cache.is_contiguous() and v_cache.is_contiguous() and o.is_contiguous()
             and lens.is_contiguous() and workspace.is_contiguous()):
         _refuse_prefix(q, k_prefix, v_prefix, k_cache, v_cache, o, lens, workspace)
-    B, H, T, dh = q.shape
-    _, Hkv, max_seq, _ = k_cache.shape
-    max_prefix = k_prefix.shape[1]
+    B, H, T, dh = shape
+    _, Hkv, max_seq, _ = cache
+    max_prefix = prefix[1]
     status = lib.tfm_prefix_attention(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(),
                                       v_cache.data_ptr(), o.data_ptr(), lens.data_ptr(), B, H, Hkv, T,
                                       max_prefix if prefix_len is None else prefix_len, max_prefix, max_seq, dh,
@@ -701,24 +706,25 @@ def verify_draft(target, draft_logits, draft, n_draft, u, noise, vocab, tokens, 
     torch, here = _now()
     f32, i32 = torch.float32, torch.int32
     greedy = temperature == 0
-    if greedy or not (
-            draft_logits is not None and u is not None and noise is not None
-            and here == target.get_device() == draft_logits.get_device() == draft.get_device() == u.get_device()
-            == noise.get_device() == tokens.get_device() == n_accepted.get_device() == workspace.get_device()
-            and f32 is target.dtype is draft_logits.dtype is u.dtype is noise.dtype
-            and i32 is draft.dtype is tokens.dtype is n_accepted.dtype
-            and 2 == draft.dim() == target.dim() == draft_logits.dim() == noise.dim()
-            and 1 == target.stride(1) == draft_logits.stride(1) == noise.stride(1)
-            and target.shape[0] >= draft.shape[0] * (draft.shape[1] + 1) and draft_logits.shape[0] >= draft.numel()
-            and noise.shape[0] >= draft.shape[0]
-            and min(target.shape[1], draft_logits.shape[1], noise.shape[1]) >= vocab
-            and u.numel() == draft.numel() and tokens.numel() == draft.shape[0] * (draft.shape[1] + 1)
-            and n_accepted.numel() == draft.shape[0]
-            and draft.is_contiguous() and u.is_contiguous() and tokens.is_contiguous()
-            and n_accepted.is_contiguous() and workspace.is_contiguous()
-            and (n_draft is None or (n_draft.get_device() == here and n_draft.dtype is i32
-                                     and n_draft.numel() == draft.shape[0] and n_draft.is_contiguous()))):
+    if greedy or draft_logits is None or u is None or noise is None or draft.dim() != 2:
         _refuse_verify(target, draft_logits, draft, n_draft, u, noise, vocab, tokens, n_accepted, workspace, greedy)
+    else:
+        B, K = draft.shape
+        ts, ds, ns = target.shape, draft_logits.shape, noise.shape
+        if not (2 == len(ts) == len(ds) == len(ns)
+                and here == target.get_device() == draft_logits.get_device() == draft.get_device() == u.get_device()
+                == noise.get_device() == tokens.get_device() == n_accepted.get_device() == workspace.get_device()
+                and f32 is target.dtype is draft_logits.dtype is u.dtype is noise.dtype
+                and i32 is draft.dtype is tokens.dtype is n_accepted.dtype
+                and 1 == target.stride(1) == draft_logits.stride(1) == noise.stride(1)
+                and ts[0] >= B * (K + 1) and ds[0] >= B * K and ns[0] >= B
+                and ts[1] >= vocab and ds[1] >= vocab and ns[1] >= vocab
+                and u.numel() == B * K and tokens.numel() == B * (K + 1) and n_accepted.numel() == B
+                and draft.is_contiguous() and u.is_contiguous() and tokens.is_contiguous()
+                and n_accepted.is_contiguous() and workspace.is_contiguous()
+                and (n_draft is None or (n_draft.get_device() == here and n_draft.dtype is i32
+                                         and n_draft.numel() == B and n_draft.is_contiguous()))):
+            _refuse_verify(target, draft_logits, draft, n_draft, u, noise, vocab, tokens, n_accepted, workspace, greedy)
     B, K = draft.shape
 
     def at(t):
