@@ -259,12 +259,15 @@ __device__ __forceinline__ void row_stats(const float2* __restrict__ part, int C
         m = mn;
     }
 }
-// Its sum in fp64, by one thread (the fp64 units take 32 cycles an instruction: only
-// where a decision needs it).
+// Its sum in fp64, by one warp, a chunk a lane (the fp64 units take 32 cycles an
+// instruction: only where a decision needs it; by one thread it took 10 us and more, which
+// two of ten batches of 64 x 5 drafts waited for: 52 and 58 us instead of 39, now 40 and 46).
 __device__ __noinline__ double row_sum64(const float2* __restrict__ part, int C, float m, double temperature) {
     double s = 0.0;
     if (m > -INFINITY)
-        for (int c = 0; c < C; ++c) s += (double)part[c].y * weight64(part[c].x, m, temperature);
+        for (int c = threadIdx.x & 31; c < C; c += 32) s += (double)part[c].y * weight64(part[c].x, m, temperature);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s;
 }
 // p(z) or q(z) in fp64; 0 in a row without any weight.
@@ -305,28 +308,29 @@ __device__ __forceinline__ Decision decide(const VerifyParams& p, int b) {
         float mt, md = 0.f, st, sd = 0.f;
         row_stats(part_t, p.C, p.c2, mt, st);
         if (drafted_here) row_stats(part_d, p.C, p.c2, md, sd);
+        // (the lanes' sums may differ in the last bit; one decides for all)
+        st = __shfl_sync(0xffffffffu, st, 0);
+        sd = __shfl_sync(0xffffffffu, sd, 0);
         if (lane == 0) {
             row_t[i] = make_float2(mt, st);
-            if (drafted_here) {
-                row_d[i] = make_float2(md, sd);
-                if (ok) {
-                    const float px = st > 0.f ? weight(zt, mt, p.c2) / st : 0.f;
-                    const float uq = u * (sd > 0.f ? weight(zd, md, p.c2) / sd : 0.f);
-                    // fp32 decides where the two sides are further apart than their errors
-                    // (and not lost below its normal numbers)
-                    if (px > 1e-30f && uq * (1.f + 2.f * kEps) < px * (1.f - 2.f * kEps)) {
-                        ok = true;
-                    } else if (uq > 1e-30f && uq * (1.f - 2.f * kEps) > px * (1.f + 2.f * kEps)) {
-                        ok = false;
-                    } else {
-                        const double p64 = prob64(zt, mt, row_sum64(part_t, p.C, mt, temp), temp);
-                        const double q64 = prob64(zd, md, row_sum64(part_d, p.C, md, temp), temp);
-                        ok = (double)u * q64 < p64;
-                    }
-                }
-                take[i] = ok;
+            if (drafted_here) row_d[i] = make_float2(md, sd);
+        }
+        if (ok) {
+            const float px = st > 0.f ? weight(zt, mt, p.c2) / st : 0.f;
+            const float uq = u * (sd > 0.f ? weight(zd, md, p.c2) / sd : 0.f);
+            // fp32 decides where the two sides are further apart than their errors (and not
+            // lost below its normal numbers); the same in all lanes
+            if (px > 1e-30f && uq * (1.f + 2.f * kEps) < px * (1.f - 2.f * kEps)) {
+                ok = true;
+            } else if (uq > 1e-30f && uq * (1.f - 2.f * kEps) > px * (1.f + 2.f * kEps)) {
+                ok = false;
+            } else {
+                const double p64 = prob64(zt, mt, row_sum64(part_t, p.C, mt, temp), temp);
+                const double q64 = prob64(zd, md, row_sum64(part_d, p.C, md, temp), temp);
+                ok = (double)u * q64 < p64;
             }
         }
+        if (drafted_here && lane == 0) take[i] = ok;
     }
     __syncthreads();
     Decision d{};
@@ -352,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify_race(const VerifyParams 
     __shared__ double redv[kThreads / 32];
     __shared__ int redi[kThreads / 32];
     __shared__ int last;
+    __shared__ double sums[2];                         // of the rows of p and q, in fp64
     pdl_wait();
     pdl_trigger();
     const VerifyArgs& a = p.a;
@@ -419,8 +424,18 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify_race(const VerifyParams 
     } else {
         double v = 0.0;
         int best = -1;
+        if (any) {                                     // (the same in all threads)
+            if (warp == 0) {
+                const double t = sum_t64();
+                if (lane == 0) sums[0] = t;
+            } else if (warp == 1) {
+                const double q = sum_d64();
+                if (lane == 0) sums[1] = q;
+            }
+            __syncthreads();
+        }
         if (mine) {
-            const double st64 = sum_t64(), sd64 = sum_d64();
+            const double st64 = sums[0], sd64 = sums[1];
             for (; mine; mine &= mine - 1) {
                 const int idx = index_of<kRaceVec>(c, __ffs(mine) - 1);
                 const double s = score64(idx, true, st64, sd64);
