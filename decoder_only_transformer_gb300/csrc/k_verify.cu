@@ -16,7 +16,10 @@
 // the last CTA of a sequence to finish merges the chunks' winners and writes the
 // answer.  A race of few CTAs decides itself, without the second launch; of many, each
 // would repeat 13 chains of dependent loads.
-// Bound by reading the logits.
+// 64 sequences of 5 drafted tokens and 50257 logits take 36 us: the first launch 23, bound by
+// reading the logits (127 MB); decisions and race, bound by their chains of dependent
+// loads and by the race's ~50 instructions per logit, the rest.  One sequence of 4 and 32000
+// takes 9 us, the latency of two launches.
 //
 // Both decisions compare computed numbers, so a rounding may turn them.  The
 // acceptance test is done in fp32 where its two sides are further apart than
@@ -261,7 +264,7 @@ __device__ __forceinline__ void row_stats(const float2* __restrict__ part, int C
 }
 // Its sum in fp64, by one warp, a chunk a lane (the fp64 units take 32 cycles an
 // instruction: only where a decision needs it; by one thread it took 10 us and more, which
-// two of ten batches of 64 x 5 drafts waited for: 52 and 58 us instead of 39, now 40 and 46).
+// two of ten batches of 64 x 5 drafts waited for: 52 and 58 us instead of 39, 40 and 46 now).
 __device__ __noinline__ double row_sum64(const float2* __restrict__ part, int C, float m, double temperature) {
     double s = 0.0;
     if (m > -INFINITY)
@@ -397,14 +400,42 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify_race(const VerifyParams 
         float z[4 * kRaceVec], y[4 * kRaceVec];
         load_chunk<kRaceVec>(zrow, c, a.V, -INFINITY, z);
         if (refused) load_chunk<kRaceVec>(yrow, c, a.V, -INFINITY, y);
+        if (fabsf(mt) < INFINITY && (!refused || fabsf(md) < INFINITY)) {
+            // finite maxima: packed pairs, the exponents as in k_verify_stats (one at a time
+            // and for any maximum 64 x 50257 took 38.7 us in all, this way 36.4)
+            const uint64_t c2 = f2_pack(p.c2, p.c2), nmt = f2_pack(-mt, -mt), nmd = f2_pack(-md, -md);
+            const uint64_t it = f2_pack(inv_t, inv_t), nid = f2_pack(-inv_d, -inv_d), minus = f2_pack(-1.f, -1.f);
+            const uint64_t eps = f2_pack(kEps, kEps), neps = f2_pack(-kEps, -kEps);
+            auto weights = [&](float a, float b, uint64_t neg_m, uint64_t scale) {
+                float x0, x1;
+                f2_unpack(f2_fma(f2_add(f2_pack(a, b), neg_m), c2, 0ull), x0, x1);
+                return f2_fma(f2_pack(fast_exp2(fmaxf(x0, -200.f)), fast_exp2(fmaxf(x1, -200.f))), scale, 0ull);
+            };
 #pragma unroll
-        for (int k = 0; k < 4 * kRaceVec; ++k) {
-            const float pw = st > 0.f ? weight(no_nan(z[k]), mt, p.c2) * inv_t : 0.f;
-            const float qw = refused && sd > 0.f ? weight(no_nan(y[k]), md, p.c2) * inv_d : 0.f;
-            const bool in = pw > 0.f && e[k] > 0.f;
-            const float r = pw - qw, er = kEps * (pw + qw), inv_e = __fdividef(1.f, e[k]);
-            hi[k] = in ? (r + er) * inv_e : -INFINITY;
-            lo = fmaxf(lo, in ? (r - er) * inv_e : -INFINITY);
+            for (int k = 0; k < 4 * kRaceVec; k += 2) {
+                const uint64_t pw = weights(z[k], z[k + 1], nmt, it);
+                const uint64_t nq = refused ? weights(y[k], y[k + 1], nmd, nid) : 0ull;       // -q
+                const uint64_t r = f2_add(pw, nq), sum = f2_fma(nq, minus, pw);
+                const uint64_t inv_e = f2_pack(__fdividef(1.f, e[k]), __fdividef(1.f, e[k + 1]));
+                float p0, p1, h0, h1, l0, l1;
+                f2_unpack(pw, p0, p1);
+                f2_unpack(f2_fma(f2_fma(sum, eps, r), inv_e, 0ull), h0, h1);
+                f2_unpack(f2_fma(f2_fma(sum, neps, r), inv_e, 0ull), l0, l1);
+                const bool in0 = p0 > 0.f && e[k] > 0.f, in1 = p1 > 0.f && e[k + 1] > 0.f;
+                hi[k] = in0 ? h0 : -INFINITY;
+                hi[k + 1] = in1 ? h1 : -INFINITY;
+                lo = fmax3(lo, in0 ? l0 : -INFINITY, in1 ? l1 : -INFINITY);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4 * kRaceVec; ++k) {
+                const float pw = st > 0.f ? weight(no_nan(z[k]), mt, p.c2) * inv_t : 0.f;
+                const float qw = refused && sd > 0.f ? weight(no_nan(y[k]), md, p.c2) * inv_d : 0.f;
+                const bool in = pw > 0.f && e[k] > 0.f;
+                const float r = pw - qw, er = kEps * (pw + qw), inv_e = __fdividef(1.f, e[k]);
+                hi[k] = in ? (r + er) * inv_e : -INFINITY;
+                lo = fmaxf(lo, in ? (r - er) * inv_e : -INFINITY);
+            }
         }
     }
     lo = block_max(lo, red);
@@ -577,7 +608,7 @@ cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (greedy) return launch_pdl(k_verify_greedy, dim3((a.B + 7) / 8), dim3(kThreads), 0, st, p);
     // Few CTAs: they decide themselves, all at once, which saves a launch (one sequence of
-    // 4 drafted tokens and 32000 logits: 9.4 us instead of 10.2).  Many: a CTA per sequence
+    // 4 drafted tokens and 32000 logits: 0.8 us of 10).  Many: a CTA per sequence
     // decides first (16 of 4 and 50257: 15.9 us instead of 17.4, 64 of 5: 46 instead of 51).
     const dim3 race((unsigned)(a.B * p.RC));
     if ((int64_t)a.B * p.RC <= kFewCtas) return launch_pdl(k_verify_race<true>, race, dim3(kThreads), 0, st, p);
