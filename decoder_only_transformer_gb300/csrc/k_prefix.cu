@@ -23,6 +23,13 @@
 // crosses jobs; each piece of a job leaves (max,
 // sum, unnormalised O) per row, and a second kernel joins a row's pieces of the
 // prefix and its own cache exactly: with M = max m, o = sum 2^(m - M) O / sum 2^(m - M) l.
+//
+// Measured: own caches of 1280 positions, 192 sequences of 16 x 64, without a prefix: 149 us,
+// 6.7 TB/s, as fast as a copy.  Short caches are bound by what a piece costs besides its
+// tiles (2000 cycles and more of the chain S, softmax, P.V, O out; 192 over a prefix of
+// 16384, up to 300 own positions: 60 us, of them ~17 pieces' ends, 20 own tiles, 18 the
+// prefix), small calls by the latency of the two launches (4 chats: 8.7 us; 64 at 16/4 x 128
+// under 2048: 19 us, of them ~5 until the first scores, ~3 the join).
 #include "common.cuh"
 #include "internal.h"
 
@@ -565,28 +572,34 @@ __global__ void __launch_bounds__(kThreadsX, 2)
                 {
                     const uint32_t t_s = tmem_base + sb * kKeys + lane_off;
                     uint32_t sr[2][32];
-                    tmem_ld32_issue(t_s, sr[0]);
-                    tmem_ld32_issue(t_s + 32, sr[1]);
+                    float mq[2];                       // maxima of the 32-column blocks
+                    tmem_ld32_max_issue(t_s, sr[0], mq[0]);
+                    tmem_ld32_max_issue(t_s + 32, sr[1], mq[1]);
                     tmem_ld_wait();
                     reg_fence32(sr[0]);
                     reg_fence32(sr[1]);
+                    reg_fence(mq[0]);
+                    reg_fence(mq[1]);
                     float s[kKeys];
 #pragma unroll
                     for (int e = 0; e < kKeys; ++e) s[e] = __uint_as_float(sr[e >> 5][e & 31]);
                     const int k0 = t * kKeys;
+                    float mx = fmaxf(mq[0], mq[1]);
                     if (k0 + kKeys > full) {
+                        // a masked tile: of the scores that are left
                         const int d = lim - k0;
 #pragma unroll
                         for (int e = 0; e < kKeys; ++e) s[e] = e >= d ? -INFINITY : s[e];
+                        float mx4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                        for (int e = 4; e + 8 <= kKeys; e += 8)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) mx4[i] = fmax3(mx4[i], s[e + 2 * i], s[e + 2 * i + 1]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mx4[i] = fmaxf(mx4[i], s[kKeys - 4 + i]);
+                        mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
                     }
-                    float mx4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                    for (int e = 4; e + 8 <= kKeys; e += 8)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) mx4[i] = fmax3(mx4[i], s[e + 2 * i], s[e + 2 * i + 1]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) mx4[i] = fmaxf(mx4[i], s[kKeys - 4 + i]);
-                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * scale_log2;
+                    mx *= scale_log2;
                     float corr = 1.f;
                     if (mx > m + kRescaleX) {
                         corr = fast_exp2(m - mx);
