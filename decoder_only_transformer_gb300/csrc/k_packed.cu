@@ -53,10 +53,12 @@ __device__ __forceinline__ int sequence_of(const int32_t* __restrict__ cu, int n
 // threads that this leaves share the keys out and add up at the end: with one or two
 // columns each the loads of P and V bound it), K and V tiles copied asynchronously one ahead.
 // Per 16-byte step of the products a warp reads 12 shared-memory wavefronts for
-// 2048 FMAs (16 cycles), so the FMA pipe is what bounds a long sequence; short ones
-// are bound by the chain load, scores, softmax, output of a tile or two.  (One warp
-// per row took 291 us for 64 lines of up to 300 tokens at 4 x 16, this 24; blocks of 64
-// rows 30, as more of them lies above the diagonal and the last ones end later.)
+// 2048 FMAs (16 cycles), so the FMA pipe is what bounds a long sequence at a large d_head.
+// At d_head 16 the instructions beside the products do, ~600 of ~800 a warp and tile, at
+// half of the issue slots: 19 us for 64 lines of up to 300 tokens at 4 x 16.  (A division
+// per copy, the accurate exponential and the scale as a product of its own: 24 us; one
+// warp per row 291; blocks of 64 rows 30, as more of them lies above the diagonal and the
+// last ones end later.)
 constexpr int kF32Rows = 32, kF32Keys = 64, kF32Threads = 128;
 
 __device__ __forceinline__ void cp_async16(float* dst, const float* src, bool in) {
@@ -74,7 +76,7 @@ struct F32Smem {
 };
 
 template <int DP>
-__global__ void __launch_bounds__(kF32Threads, DP <= 32 ? 5 : DP == 64 ? 4 : 1) k_packed_f32(const float* __restrict__ q, const float* __restrict__ k,
+__global__ void __launch_bounds__(kF32Threads, DP <= 64 ? 4 : 1) k_packed_f32(const float* __restrict__ q, const float* __restrict__ k,
                                                     const float* __restrict__ v, float* __restrict__ o,
                                                     const int32_t* __restrict__ cu, int n_seq, int T, int slots,
                                                     int H, int group, int dh, PackedStrides sd,
@@ -104,15 +106,24 @@ __global__ void __launch_bounds__(kF32Threads, DP <= 32 ? 5 : DP == 64 ? 4 : 1) 
     const float* vb = v + sr.start * sd.vt + g * sd.vh;
     const int j0 = (window > 0 && row0 - window + 1 > 0) ? (row0 - window + 1) / kF32Keys : 0;
     const int j1 = (row0 + kF32Rows - 1) / kF32Keys;                 // key tiles j0..j1
+    const int first_r = tid / d4, first_c = tid - first_r * d4;
+    const int step_r = kF32Threads / d4, step_c = kF32Threads - step_r * d4;
     auto load_kv = [&](int j) {
         float* ks = sm + Sm::kK + (j & 1) * kF32Keys * Sm::kPitch;
         float* vs = sm + Sm::kV + (j & 1) * kF32Keys * Sm::kPitch;
-        for (int i = tid; i < kF32Keys * d4; i += kF32Threads) {
-            const int r = i / d4, c = (i - r * d4) * 4, key = j * kF32Keys + r;
+        int r = first_r, c = first_c;
+        while (r < kF32Keys) {
+            const int key = j * kF32Keys + r;
             const bool in = key < sr.len;
             const int64_t at = in ? key : 0;
-            cp_async16(ks + r * Sm::kPitch + c, kb + at * sd.kt + c, in);
-            cp_async16(vs + r * Sm::kPitch + c, vb + at * sd.vt + c, in);
+            cp_async16(ks + r * Sm::kPitch + 4 * c, kb + at * sd.kt + 4 * c, in);
+            cp_async16(vs + r * Sm::kPitch + 4 * c, vb + at * sd.vt + 4 * c, in);
+            r += step_r;
+            c += step_c;
+            if (c >= d4) {
+                c -= d4;
+                ++r;
+            }
         }
     };
     const float* qb = q + (int64_t)(sr.start + row0) * sd.qt + h * sd.qh;
@@ -171,20 +182,20 @@ __global__ void __launch_bounds__(kF32Threads, DP <= 32 ? 5 : DP == 64 ? 4 : 1) 
         // keys of this tile that row i sees: [lo, hi]
         const int k0 = j * kF32Keys;
         const bool masked = k0 + kF32Keys - 1 > row0 || (window > 0 && k0 < row0 + kF32Rows - window);
+        if (masked)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int qi = row0 + ty * 4 + i, hi = qi - k0, lo = window > 0 ? hi - window + 1 : 0;
-            float mx = -INFINITY;
+            for (int i = 0; i < 4; ++i) {
+                const int hi = row0 + ty * 4 + i - k0 - tx, lo = window > 0 ? hi - window + 1 : INT_MIN;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int key = tx + 16 * e;
-                s[i][e] = masked && (key > hi || key < lo) ? -INFINITY : s[i][e] * scale_log2;
-                mx = fmaxf(mx, s[i][e]);
+                for (int e = 0; e < 4; ++e) s[i][e] = 16 * e > hi || 16 * e < lo ? -INFINITY : s[i][e];
             }
 #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float mx = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
+#pragma unroll
             for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-            const float mn = fmaxf(m[i], mx), ref = mn == -INFINITY ? 0.f : mn;
-            const float corr = exp2f(m[i] - ref);      // m = -inf: 0
+            const float mn = fmaxf(m[i], mx * scale_log2), ref = mn == -INFINITY ? 0.f : -mn;
+            const float corr = fast_exp2(m[i] + ref);  // m = -inf: 0
             m[i] = mn;
             l[i] *= corr;
             const uint64_t corr2 = f2_pack(corr, corr);
@@ -192,7 +203,7 @@ __global__ void __launch_bounds__(kF32Threads, DP <= 32 ? 5 : DP == 64 ? 4 : 1) 
             for (int c = 0; c < NC / 2; ++c) acc[i][c] = f2_fma(acc[i][c], corr2, 0ull);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                s[i][e] = exp2f(s[i][e] - ref);
+                s[i][e] = fast_exp2(fmaf(s[i][e], scale_log2, ref));
                 l[i] += s[i][e];
             }
         }
