@@ -227,3 +227,59 @@ def test_many_sequences_and_a_long_one():
     _check(torch.cat([o[:2100], torch.full_like(o[:1], 7.0)]), q[:2100], k[:2100], v[:2100], few)
     _check(o[a:a + n], q[a:a + n], k[a:a + n], v[a:a + n], [n])
     _check(o[a + n:], q[a + n:], k[a + n:], v[a + n:], [17] * 300)
+
+
+MANY = [0, 5, 0, 128, 1, 0, 255, 257, 700, 64, 1300, 2, 127, 0]
+
+
+@pytest.mark.parametrize("dh,H,Hkv", [(32, 32, 16), (64, 24, 24), (64, 48, 8), (128, 24, 12), (128, 21, 21)])
+@pytest.mark.parametrize("window", [0, 1, 100, 320])
+def test_more_items_than_ctas(window, dh, H, Hkv):
+    """Several items per CTA, taken from the list, of one and of two query tiles."""
+    T = sum(MANY) + 3
+    q, k, v = _inputs(dh + H + window, T, H, Hkv, dh)
+    o = _call(q, k, v, _cu(MANY), window)
+    _check(o, q, k, v, MANY, window)
+    assert torch.equal(_call(q, k, v, _cu(MANY), window), o)
+
+
+@pytest.mark.parametrize("dh,H,Hkv", [(64, 24, 24), (128, 24, 12)])
+def test_list_and_no_list_agree(dh, H, Hkv):
+    """The first sequences alone, without a list, and among many: the same bits, as an item's own work is the same."""
+    T = sum(MANY)
+    q, k, v = _inputs(dh, T, H, Hkv, dh)
+    n = sum(MANY[:4])
+    few = [t[:n].contiguous() for t in (q, k, v)]
+    assert torch.equal(_call(*few, _cu(MANY[:4])), _call(q, k, v, _cu(MANY))[:n])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("window", [0, 70])
+def test_values_that_are_not_finite_among_many_items(window, bad):
+    q, k, v = _inputs(3, sum(MANY), 24, 12, 128)
+    clean = _call(q, k, v, _cu(MANY), window)
+    start = np.cumsum([0] + MANY)
+    v2, seen = v.clone(), torch.zeros_like(clean, dtype=torch.bool)
+    for b, L in enumerate(MANY):                        # in every sequence, another kv head and column
+        if L > 1:
+            at, g, c = int(start[b]) + L // 2, b % 12, 7 * b % 128
+            v2[at, g, c] = bad
+            end = int(start[b + 1]) if window == 0 else min(int(start[b + 1]), at + window)
+            seen[at:end, 2 * g:2 * g + 2, c] = True
+    o = _call(q, k, v2, _cu(MANY), window)
+    assert torch.equal(o[~seen], clean[~seen])
+    assert not torch.isfinite(o[seen]).any()
+
+
+def test_offsets_out_of_range_among_many():
+    q, k, v = _inputs(15, 2000, 48, 24, 64)
+    lens = [300, 500, 64, 700]
+    ok = _call(q, k, v, _cu(lens))
+    for cu in ([0, 300, 800, 400, 1564], [0, 300, 800, 864, 2 ** 31 - 1], [-7, 300, 800, 864, 1564]):
+        o = _call(q, k, v, torch.tensor(cu, dtype=torch.int32).cuda())
+        with pytest.raises(tfm.TfmError) as e:
+            tfm.device_status()
+        assert e.value.status == tfm.TFM_EINVAL
+        if cu[1:3] == [300, 800] and cu[3] == 864:
+            assert torch.equal(o[300:864], ok[300:864])
+        assert (o[1600:] == 7.0).all()

@@ -205,3 +205,47 @@ def test_graph_replay_and_repeats_agree():
             g.replay()
             torch.cuda.synchronize()
             _same((tokens.cpu().numpy(), acc.cpu().numpy()), verify(*new[:3], [K] * B, *new[3:], V, 1.0))
+
+
+@pytest.mark.parametrize("B", [4, 100])                 # the race's CTAs decide, or a launch before it
+@pytest.mark.parametrize("V", [600, 9001])
+def test_acceptance_on_the_verge(B, V):
+    """u q(x) within 2e-5 of p(x): closer than fp32 can tell, further than the fp32 sums are off (5e-6)."""
+    K = 3
+    target, dl, draft, u, noise = _inputs(B + V, B, K, V, off=0.2)
+    p = (target[:, :V].double().softmax(1)).view(B, K + 1, V)[:, :K].gather(2, draft[..., None].long())[..., 0]
+    q = (dl[:, :V].double().softmax(1)).view(B, K, V).gather(2, draft[..., None].long())[..., 0]
+    g = torch.Generator().manual_seed(V)
+    side = (torch.randint(0, 2, (B, K), generator=g) * 2 - 1).cuda().double()
+    u = (p / q * (1 + 2e-5 * side)).float()
+    u = torch.where(u < 1, u, torch.full_like(u, 0.25))
+    want = verify(target, dl, draft, [K] * B, u, noise, V, 1.0)
+    _same(_call(target, dl, draft, u, noise, V), want)
+    assert 0 < want[1].sum() < B * K
+
+
+@pytest.mark.parametrize("B", [4, 90])
+@pytest.mark.parametrize("refused", [False, True])
+def test_close_races_of_few_and_many(B, refused):
+    """Six tokens 3e-5 apart, with and without a refused row: closer than fp32 can tell (its bound is 2.5e-5 of
+    p + q on each side), further than the fp32 sums of both rows, 1.4e-6 each, move p - q against one another
+    (p / (p - q) stays below 4 among the largest weights: 1.1e-5)."""
+    V, K = 8300, 1 if refused else 0
+    g = torch.Generator().manual_seed(B)
+    target = (torch.randn(B * (K + 1), V, generator=g) * 0.1).cuda()
+    dl = (torch.randn(B * K, V, generator=g) * 0.1 - 1).cuda()
+    draft = torch.zeros(B, K, dtype=torch.int32, device="cuda")
+    u = torch.ones(B, K, device="cuda")
+    if refused:                                         # p(0) = 0: always refused
+        target[0::2, 0] = -INF
+    noise = torch.full((B, V), 30.0, device="cuda")
+    rows = target.view(B, K + 1, V)[:, 0, :].double()
+    w = rows.softmax(1)
+    if refused:
+        w = (w - dl[:, :V].double().softmax(1)).clamp(min=0)
+    for b in range(B):
+        top = torch.argsort(w[b], descending=True)[torch.randperm(200, generator=g)[:6]]
+        noise[b, top] = (w[b, top] * 4000 * (1 + 3e-5 * torch.randperm(6, generator=g).cuda().double())).float()
+    want = verify(target, dl if K else None, draft, [K] * B, u if K else None, noise, V, 1.0)
+    got = _call(target, dl if K else torch.empty(0, V, device="cuda"), draft, u, noise, V)
+    _same(got, want)
