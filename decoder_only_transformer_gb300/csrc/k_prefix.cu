@@ -701,11 +701,14 @@ __global__ void __launch_bounds__(kThreadsX, 2)
 }
 
 // A thread joins four columns of a row, its pieces of the prefix job and of the
-// own job, eight at a time: maxima, sums and values of all eight are in flight
-// together, so that a row costs one trip to L2 per eight pieces.  A CTA takes the
-// 128 rows of a row tile, whose prefix pieces lie side by side.
-template <int DH>
-__global__ void __launch_bounds__(kRowsP) k_prefix_join(PrefixParts in, PrefixGeom gm, int H,
+// own job, kAtOnce at a time: their maxima, sums and values are in flight together, so
+// that a row costs one trip to L2 per kAtOnce pieces.  A CTA takes the 128 rows of a row
+// tile, whose prefix pieces lie side by side.  Eight at once up to a wave of CTAs (16 answers
+// of 5 tokens over 8192, 16 pieces a row: 20.4 us in all, four at once 22); with more rows
+// there are few pieces each and four at once fit more CTAs on an SM (101 sequences of 8
+// tokens, 16/4 x 128: 19.6 us, eight at once 21.1).
+template <int DH, int kAtOnce>
+__global__ void __launch_bounds__(kRowsP, kAtOnce == 8 ? 6 : 10) k_prefix_join(PrefixParts in, PrefixGeom gm, int H,
                                                         const int32_t* __restrict__ lens,
                                                         __nv_bfloat16* __restrict__ o) {
     constexpr int S = DH / 4;
@@ -734,11 +737,11 @@ __global__ void __launch_bounds__(kRowsP) k_prefix_join(PrefixParts in, PrefixGe
     float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     const int n = n_pre + n_own;
-    for (int k0 = 0; k0 < n; k0 += 8) {
-        float2 ml[8];
-        float4 v[8];
+    for (int k0 = 0; k0 < n; k0 += kAtOnce) {
+        float2 ml[kAtOnce];
+        float4 v[kAtOnce];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kAtOnce; ++j) {
             const int k = k0 + j;
             ml[j] = make_float2(-INFINITY, 0.f);
             v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -752,13 +755,13 @@ __global__ void __launch_bounds__(kRowsP) k_prefix_join(PrefixParts in, PrefixGe
         }
         float Mn = M;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) Mn = fmaxf(Mn, ml[j].x);
+        for (int j = 0; j < kAtOnce; ++j) Mn = fmaxf(Mn, ml[j].x);
         const float keep = M == -INFINITY ? 0.f : exp2f(M - Mn);
         // (the sum of pieces without a maximum is 0, or NaN if the scores are: it goes on)
         L = M == -INFINITY ? L : L * keep;
         acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kAtOnce; ++j) {
             // A piece in which the row sees nothing holds (-inf, 0) and no value; one of
             // NaN scores alone (-inf, NaN).
             const bool none = ml[j].x == -INFINITY;
@@ -847,8 +850,10 @@ cudaError_t launch_dh(const PrefixArgs& a, PrefixGeom g, const CUtensorMap* maps
                    maps[3], maps[4], maps[5], static_cast<const __nv_bfloat16*>(a.vc), a.lens, g, parts,
                    a.scale * 1.4426950408889634f, device_error_word());
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_prefix_join<DH>, dim3((unsigned)(g.Hkv * g.nrt * (DH / 4))), dim3(kRowsP), 0, st, parts, g, a.H, a.lens,
-                      static_cast<__nv_bfloat16*>(a.o));
+    const unsigned join = (unsigned)(g.Hkv * g.nrt * (DH / 4));
+    auto* const o = static_cast<__nv_bfloat16*>(a.o);
+    return join > (unsigned)(6 * sm_count()) ? launch_pdl(k_prefix_join<DH, 4>, dim3(join), dim3(kRowsP), 0, st, parts, g, a.H, a.lens, o)
+                        : launch_pdl(k_prefix_join<DH, 8>, dim3(join), dim3(kRowsP), 0, st, parts, g, a.H, a.lens, o);
 }
 
 }  // namespace
