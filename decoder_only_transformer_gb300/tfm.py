@@ -591,7 +591,8 @@ def packed_attention(q, k, v, o, cu_seqlens, workspace, window=0, scale=0.0, str
     status = lib.tfm_packed_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                                       cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1, T, H, kv[1], dh,
                                       _Strides(sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1]), scale,
-                                      window, _mode_of(q), workspace.data_ptr(), workspace.nbytes,
+                                      window, TFM_BF16 if q.dtype is torch.bfloat16 else _mode_of(q),
+                                      workspace.data_ptr(), workspace.nbytes,
                                       _raw_stream(stream, here))
     if status:
         _check(status)
