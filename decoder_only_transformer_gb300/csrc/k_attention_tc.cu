@@ -522,17 +522,16 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeTiledFn att_encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static bool tried = false;
-    if (!tried) {
+    // (looked up once, by the first thread that asks)
+    static const EncodeTiledFn fn = []() -> EncodeTiledFn {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult q;
         if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
                                              cudaEnableDefault, &q) == cudaSuccess &&
             q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-        tried = true;
-    }
+            return reinterpret_cast<EncodeTiledFn>(p);
+        return nullptr;
+    }();
     return fn;
 }
 
@@ -581,8 +580,17 @@ cudaError_t launch_tc(const AttnPlan& p, cudaStream_t st) {
 
 }  // namespace
 
+// The driver encodes only with a current context, which a host thread has from its first
+// call of the runtime that needs one; cudaSetDevice is such a call, also on a capturing stream.
+template <typename Encode>
+static bool encode_with_context(const Encode& encode) {
+    if (encode() == CUDA_SUCCESS) return true;
+    int d = 0;
+    return cudaGetDevice(&d) == cudaSuccess && cudaSetDevice(d) == cudaSuccess && encode() == CUDA_SUCCESS;
+}
+
 // [T, heads, dh] bf16 at any token and head stride (elements), box min(dh, 64) x
-// 128 rows x 1 head, zero fill past T.
+// box_rows rows x 1 head, zero fill past T.
 bool rows_heads_map(CUtensorMap* map, const void* ptr, int64_t T, int64_t heads, int dh, int64_t token_stride,
                     int64_t head_stride, int box_rows) {
     EncodeTiledFn fn = att_encode_fn();
@@ -592,10 +600,12 @@ bool rows_heads_map(CUtensorMap* map, const void* ptr, int64_t T, int64_t heads,
     cuuint64_t strides[2] = {(cuuint64_t)(token_stride * 2), (cuuint64_t)(head_stride * 2)};
     cuuint32_t box[3] = {inner, (cuuint32_t)box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE,
-              inner * 2 == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_with_context([&] {
+        return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  inner * 2 == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
 }
 
 // [B, Hkv, GT, dh] bf16, dense, as boxes of nb sequences' GT rows of one kv head.
@@ -608,10 +618,12 @@ bool query_groups_map(CUtensorMap* map, const void* ptr, int B, int Hkv, int GT,
     cuuint64_t strides[3] = {row, group, group * Hkv};
     cuuint32_t box[4] = {inner, (cuuint32_t)GT, 1, (cuuint32_t)nb};
     cuuint32_t estr[4] = {1, 1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE,
-              inner * 2 == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_with_context([&] {
+        return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  inner * 2 == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
 }
 
 bool attention_tc_supported(int dh) { return dh == 32 || dh == 64 || dh == 128; }

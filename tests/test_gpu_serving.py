@@ -2,6 +2,11 @@
 then steps that score drafted tokens over the shared prefix and the own caches and keep what the verification
 accepts.  And the calls around that: other streams, two at once, graphs that share a workspace, the smallest and
 the largest sizes."""
+import os
+import subprocess
+import sys
+import threading
+
 import numpy as np
 import pytest
 
@@ -406,3 +411,74 @@ def test_offsets_beyond_32_bits():
                      _bytes(tfm.verify_draft_workspace_bytes(1, K, V)))
     want = verify(a[0], a[1], a[2], [K], a[3] * 0.01, a[4], V, 1.0)
     assert want[1][0] == K and np.array_equal(tokens.cpu().numpy(), want[0])
+
+
+FIRST = """
+import torch
+from decoder_only_transformer_gb300 import tfm
+r = lambda *s: torch.randn(*s, device="cuda")
+ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+b = lambda n: torch.empty(n, dtype=torch.uint8, device="cuda")
+q, cu = r(300, {H}, 64).to(torch.{dtype}), ints([0, 120, 300])
+o1, w1 = torch.zeros_like(q), b(tfm.packed_attention_workspace_bytes(300, 2))
+x, kp, kc = (r(*s).bfloat16() for s in ((3, 8, 2, 64), (2, 100, 64), (3, 2, 50, 64)))
+o2, lens, w2 = torch.zeros(3, 2, 512, dtype=torch.bfloat16, device="cuda"), ints([50, 2, 9]), b(tfm.prefix_attention_workspace_bytes(3, 8, 2, 2, 64))
+t, d, draft, u, e = r({B} * 3, 5000), r({B} * 2, 5000), ints([[1, 2]] * {B}), torch.rand({B}, 2, device="cuda"), r({B}, 5000).abs() + 0.01
+tok, n, w3 = ints([[0] * 3] * {B}), ints([0] * {B}), b(tfm.verify_draft_workspace_bytes({B}, 2, 5000))
+def run():
+    tfm.packed_attention(q, q, q, o1, cu, w1)
+    tfm.prefix_attention(x, kp, kp, kc, kc, o2, lens, w2)
+    tfm.verify_draft(t, d, draft, None, u, e, 5000, tok, n, w3, temperature={temperature})
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    run()
+g.replay()
+torch.cuda.synchronize()
+first = [z.clone() for z in (o1, o2, tok, n)]
+run()
+torch.cuda.synchronize()
+assert all(torch.equal(a, c) for a, c in zip(first, (o1, o2, tok, n))) and o1.abs().sum() > 0 and o2.abs().sum() > 0
+tfm.device_status()
+print("same")
+"""
+
+
+@pytest.mark.parametrize("H,dtype,B,temperature", [(4, "bfloat16", 3, 1.0), (64, "bfloat16", 100, 1.0), (4, "float32", 3, 0.0)])
+def test_first_calls_of_a_process_are_captured(H, dtype, B, temperature):
+    """Nothing has to run before a capture: a fresh process records its first call of each operator."""
+    code = FIRST.format(H=H, dtype=dtype, B=B, temperature=temperature)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.strip().endswith("same"), r.stderr[-2000:]
+
+
+def test_threads_on_streams_of_their_own():
+    """Calls from two host threads at once, each with its stream and workspaces."""
+    sets = [_calls(5), _calls(70)]
+    want = []
+    for runs, outs, _ in sets:
+        for run in runs:
+            run()
+        want.append(_outputs(outs))
+        _clear(outs)
+    errors = []
+
+    def work(runs):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(30):
+                for run in runs:
+                    run(stream)
+        except Exception as e:                          # shown by the assertion below
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(runs,)) for runs, _, _ in sets]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for (_, outs, _), w in zip(sets, want):
+        for got, ref in zip(_outputs(outs), w):
+            assert torch.equal(got, ref)
