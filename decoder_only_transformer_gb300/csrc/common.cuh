@@ -417,25 +417,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// The split form below with the maximum of the thread's 32 columns (sm_103a): the
-// load takes it on the way, a NaN losing to any number.  Like the registers, `mx`
-// belongs to the load until the wait, even where it is not used: reg_fence() it.
-__device__ __forceinline__ void tmem_ld32_max_issue(uint32_t taddr, uint32_t (&r)[32], float& mx) {
-    asm volatile(
-        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32"
-        " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31]), "=f"(mx)
-        : "r"(taddr)
-        : "memory");
-}
-__device__ __forceinline__ void reg_fence(float& x) { asm volatile("" : "+f"(x)); }
-
 // Split form of the load above: issue now, wait later.  After tmem_ld_wait()
 // the registers must pass through reg_fence32() before use, so that the
 // compiler cannot schedule a read of them above the wait.

@@ -25,13 +25,13 @@
 // exponentials with a polynomial on the FMA pipe was measured slower here: it
 // costs more issue slots than it frees.  Taking an unmasked tile's row maximum
 // from the tensor-memory load with tcgen05.ld.red measured faster, 144.7 ->
-// 134.1 us at long context.  It is not used, because with it one
-// prefill-against-forward bit-equality check failed: a 37-position sequence
-// whose only key tile is masked, so that path never uses the hardware maximum.
-// The likely cause: on that path the load's maximum outputs were dead while the
-// asynchronous load could still write them, so their registers may have been
-// reused meanwhile.  Every destination of an asynchronous load has to stay live
-// until its wait.)  S_x(j+1) is issued as soon as the
+// 134.1 us at long context.  It is not used: in builds with it the maximum of a
+// masked row, which is taken from the masked scores, came out raised to the
+// load's own maximum of columns 32..63, masked ones among them - the same rows
+// every time, whether or not the load's outputs were kept live past the wait,
+// and with loads and wait in one statement too.
+// Results were right up to roundings, but the first rows of a 37-position
+// sequence were not those of a 40-position one bit for bit.)  S_x(j+1) is issued as soon as the
 // softmax of tile x has read S_x(j) into registers, P_x.V_j as soon as it has
 // written P_x(j); the exponentials of tile j+1 run before the wait for P_x.V_j
 // (which frees the P_x columns), so that wait overlaps them.  (Two threads per

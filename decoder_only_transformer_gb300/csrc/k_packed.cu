@@ -881,21 +881,17 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 if (!(ok = warp_wait(s_full(x, cnt), phase(cnt), err, abort_flag))) break;
                 tc_fence_after();
                 uint32_t sr[kKV / 32][32];
-                float mq[kKV / 32];                    // maxima of the 32-column blocks
 #pragma unroll
-                for (int cc = 0; cc < kKV / 32; ++cc)
-                    tmem_ld32_max_issue(t_s + (cnt & 1) * kKV + cc * 32, sr[cc], mq[cc]);
+                for (int cc = 0; cc < kKV / 32; ++cc) tmem_ld32_issue(t_s + (cnt & 1) * kKV + cc * 32, sr[cc]);
                 tmem_ld_wait();
                 float s[kKV];
 #pragma unroll
                 for (int cc = 0; cc < kKV / 32; ++cc) {
                     reg_fence32(sr[cc]);
-                    reg_fence(mq[cc]);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) s[cc * 32 + e] = __uint_as_float(sr[cc][e]);
                 }
                 const int k0 = (it.j0 + j) * kKV;
-                float mx = fmaxf(mq[0], mq[1]);
                 // A row of the sequence sees keys up to itself, which lie in the
                 // sequence: the diagonal masks the next sequence's keys too.
                 if (k0 >= row0) {
@@ -908,18 +904,15 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 #pragma unroll
                     for (int cc = 0; cc < kKV; ++cc) s[cc] = cc < from ? -INFINITY : s[cc];
                 }
-                if (k0 >= row0 || (kWin && k0 < win_lo)) {
-                    // a masked tile: of the scores that are left
-                    float mx4[4] = {s[0], s[1], s[2], s[3]};
+                // row maximum: four independent chains of three-input maxima
+                float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                    for (int cc = 4; cc + 8 <= kKV; cc += 8)
+                for (int cc = 4; cc + 8 <= kKV; cc += 8)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) mx4[e] = fmax3(mx4[e], s[cc + 2 * e], s[cc + 2 * e + 1]);
+                    for (int e = 0; e < 4; ++e) mx4[e] = fmax3(mx4[e], s[cc + 2 * e], s[cc + 2 * e + 1]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(mx4[e], s[kKV - 4 + e]);
-                    mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-                }
-                mx *= scale_log2;
+                for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(mx4[e], s[kKV - 4 + e]);
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * scale_log2;
                 float corr = 1.f;
                 if (mx > m + kRescale) {
                     corr = fast_exp2(m - mx);

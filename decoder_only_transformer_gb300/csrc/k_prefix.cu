@@ -575,34 +575,29 @@ __global__ void __launch_bounds__(kThreadsX, 2)
                 {
                     const uint32_t t_s = tmem_base + sb * kKeys + lane_off;
                     uint32_t sr[2][32];
-                    float mq[2];                       // maxima of the 32-column blocks
-                    tmem_ld32_max_issue(t_s, sr[0], mq[0]);
-                    tmem_ld32_max_issue(t_s + 32, sr[1], mq[1]);
+                    tmem_ld32_issue(t_s, sr[0]);
+                    tmem_ld32_issue(t_s + 32, sr[1]);
                     tmem_ld_wait();
                     reg_fence32(sr[0]);
                     reg_fence32(sr[1]);
-                    reg_fence(mq[0]);
-                    reg_fence(mq[1]);
                     float s[kKeys];
 #pragma unroll
                     for (int e = 0; e < kKeys; ++e) s[e] = __uint_as_float(sr[e >> 5][e & 31]);
                     const int k0 = t * kKeys;
-                    float mx = fmaxf(mq[0], mq[1]);
                     if (k0 + kKeys > full) {
-                        // a masked tile: of the scores that are left
                         const int d = lim - k0;
 #pragma unroll
                         for (int e = 0; e < kKeys; ++e) s[e] = e >= d ? -INFINITY : s[e];
-                        float mx4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                        for (int e = 4; e + 8 <= kKeys; e += 8)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) mx4[i] = fmax3(mx4[i], s[e + 2 * i], s[e + 2 * i + 1]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) mx4[i] = fmaxf(mx4[i], s[kKeys - 4 + i]);
-                        mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
                     }
-                    mx *= scale_log2;
+                    // row maximum: four independent chains of three-input maxima
+                    float mx4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                    for (int e = 4; e + 8 <= kKeys; e += 8)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mx4[i] = fmax3(mx4[i], s[e + 2 * i], s[e + 2 * i + 1]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mx4[i] = fmaxf(mx4[i], s[kKeys - 4 + i]);
+                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * scale_log2;
                     float corr = 1.f;
                     if (mx > m + kRescaleX) {
                         corr = fast_exp2(m - mx);
