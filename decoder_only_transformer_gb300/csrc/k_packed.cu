@@ -410,8 +410,12 @@ constexpr int kQ = 128;
 constexpr int kThreadsP = 384;          // control, softmax of tile A, softmax of tile B
 constexpr int kKV = 64;                 // keys per tile
 constexpr float kRescale = 8.0f;        // log2 units: P entries stay below 2^8
-constexpr int kPoison = 8;
 constexpr int kItems = 8;               // entries of work items in shared memory
+// Items whose V held values that are not finite.  A softmax warp in the epilogue of item i
+// has released the entries up to i's, so item i + kItems can be on its way while the other
+// tile's warps run ahead: its mark must not take the place of item i's.
+constexpr int kPoison = 16;
+static_assert(kPoison > kItems, "a mark lives until the item's last epilogue");
 
 template <int DH>
 struct Pk {

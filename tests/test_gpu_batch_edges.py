@@ -1,0 +1,50 @@
+"""Calls of the batched-serving operators that lie at the edge of what their documentation allows."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from decoder_only_transformer_gb300 import tfm  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    tfm.load()
+    yield
+    tfm.device_status()
+
+
+def _ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _bytes(n):
+    return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+
+def _packed(q, k, v, cu, **kw):
+    o = torch.full_like(q, 7.0)
+    tfm.packed_attention(q, k, v, o, cu, _bytes(tfm.packed_attention_workspace_bytes(len(q), len(cu) - 1)), **kw)
+    torch.cuda.synchronize()
+    return o
+
+
+@pytest.mark.parametrize("H,Hkv,dh", [(1, 1, 32), (3, 1, 64), (2, 1, 32)])
+def test_a_value_that_is_not_finite_in_every_prompt(H, Hkv, dh):
+    """Thousands of items, twenty and more per CTA, with and without a second query tile, each with an infinity at its
+    last key: only the row of that key sees it."""
+    rng = np.random.default_rng(H * dh)
+    lens = np.where(rng.random(3600 // H) < 0.2, rng.integers(129, 300, 3600 // H), rng.integers(1, 129, 3600 // H))
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    g = torch.Generator().manual_seed(dh)
+    q, k, v = (torch.randn(int(cu[-1]), h, dh, generator=g).to(torch.bfloat16).cuda() for h in (H, Hkv, Hkv))
+    want = _packed(q, k, v, _ints(cu))
+    last = torch.from_numpy(cu[1:] - 1).cuda()
+    bad = v.clone()
+    bad[last, :, 5] = float("inf")
+    want[last, :, 5] = float("inf")
+    for _ in range(5):
+        assert torch.equal(_packed(q, k, bad, _ints(cu)), want)
