@@ -42,12 +42,14 @@ constexpr int kVec = 8, kRaceVec = 4;
 constexpr int kChunk = kThreads * kVec * 4, kRaceChunk = kThreads * kRaceVec * 4;
 constexpr int kMaxK = 64;
 constexpr int kFewCtas = 128;           // of the race: it decides itself then
-// Relative error of an fp32 weight e^((z - m) / temperature): the exponent
-// x = (z - m) log2(e) / temperature carries three roundings, 3 * 2^-24 |x|, so
-// the weight 0.7 * 3 * 2^-24 |x| <= 1.6e-5 down to the smallest normal number
-// (|x| = 126).  A row's sum has 20 roundings within a chunk and up to 64 over the chunks of
-// 2^24 logits, 5e-6; the exponential, the divisions and the product with 1 / noise stay below 1e-6.
-constexpr float kEps = 2.5e-5f;
+// Relative error of an fp32 probability.  The exponent x = (z - m) log2(e) / temperature
+// carries three roundings (the factor, taken in fp64 on the host, the difference, the
+// product), 3 * 2^-24 |x|, and so its weight 0.7 times that: 1.57e-5 down to the smallest
+// normal number (|x| = 126).  A row's sum has the same error in its weights' exponents, |x|
+// being at most log2(V) <= 24 on their average: 3.0e-6; 20 roundings within a chunk and up to 70
+// over the chunks of 2^24 logits, 5.4e-6; the exponentials (2^-22 each, two in the sum), the
+// division and the product with 1 / noise 1.2e-6.  2.6e-5 in all.
+constexpr float kEps = 3e-5f;
 
 struct __align__(16) Cand {
     float lo, hi;      // bounds of weight / noise
@@ -242,25 +244,25 @@ __global__ void __launch_bounds__(kThreads) k_verify_stats(const VerifyParams p)
     }
 }
 
-// The maximum and the sum of a whole row from its chunks, by one warp.
+// The maximum and the sum of a whole row from its chunks, by one warp.  The maximum first:
+// a sum that is scaled anew whenever the maximum grows takes an exponential's error each time.
 __device__ __forceinline__ void row_stats(const float2* __restrict__ part, int C, float c2, float& m,
                                           float& s) {
     const int lane = threadIdx.x & 31;
-    m = -INFINITY;
+    const float2 first = lane < C ? part[lane] : make_float2(-INFINITY, 0.f);
+    m = first.x;
     s = 0.f;
-    for (int c = lane; c < C; c += 32) {
+    for (int c = lane + 32; c < C; c += 32) m = fmaxf(m, part[c].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (m == -INFINITY) return;
+    s = first.y * weight(first.x, m, c2);
+    for (int c = lane + 32; c < C; c += 32) {
         const float2 v = part[c];
-        const float mn = fmaxf(m, v.x);
-        if (mn > -INFINITY) s = s * weight(m, mn, c2) + v.y * weight(v.x, mn, c2);
-        m = mn;
+        s += v.y * weight(v.x, m, c2);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-        const float mn = fmaxf(m, m2);
-        if (mn > -INFINITY) s = s * weight(m, mn, c2) + s2 * weight(m2, mn, c2);
-        m = mn;
-    }
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
 }
 // Its sum in fp64, by one warp, a chunk a lane (the fp64 units take 32 cycles an
 // instruction: only where a decision needs it; by one thread it took 10 us and more, which
@@ -592,7 +594,7 @@ cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t st) {
     p.C = (a.V + kChunk - 1) / kChunk;
     p.RC = (a.V + kRaceChunk - 1) / kRaceChunk;
     const bool greedy = a.temperature == 0.f;
-    p.c2 = greedy ? 0.f : 1.4426950408889634f / a.temperature;
+    p.c2 = greedy ? 0.f : (float)(1.4426950408889634 / (double)a.temperature);
     uint8_t* w = static_cast<uint8_t*>(a.ws);
     p.part = reinterpret_cast<float2*>(w);
     w += align256((size_t)a.B * (2 * a.K + 1) * p.C * sizeof(float2));
