@@ -21,12 +21,17 @@
 // loads and by the race's ~50 instructions per logit, the rest.  One sequence of 4 and 32000
 // takes 9 us, the latency of two launches.
 //
-// Both decisions compare computed numbers, so a rounding may turn them.  The
-// acceptance test is done in fp32 where its two sides are further apart than
-// their errors, else in fp64 from the merged statistics.  The race is run
-// in fp32 with bounds: a weight p - q is known to kEps (p + q), every chunk
-// keeps what may still be its winner, and where more than one token may be, those
-// few are evaluated in fp64.  Ties go to the lowest token.
+// Both decisions compare computed numbers, so a rounding may turn them.  Each is made
+// in fp32 where the sides are further apart than their errors (kEps), else in fp64 with
+// the rows' sums as the first launch left them, in fp32 per chunk (kEpsSum).  Where that
+// leaves it open too, by the bounds' widths in one of some 200 batches of 64 x 5 drafts, the CTA
+// takes the rows' sums anew from the logits, as pairs of fp32 numbers (kEpsPair), and if
+// those do not tell, in fp64.  In the race a weight p - q is known to eps (p + q); every chunk keeps
+// what may still be its winner, or itself as a whole if the chunks' sums do not tell.
+// (Without a refused token the sum scales all weights alike and decides nothing.)  Ties go
+// to the lowest token.
+#include <climits>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -50,12 +55,18 @@ constexpr int kFewCtas = 128;           // of the race: it decides itself then
 // over the chunks of 2^24 logits, 5.4e-6; the exponentials (2^-22 each, two in the sum), the
 // division and the product with 1 / noise 1.2e-6.  2.6e-5 in all.
 constexpr float kEps = 3e-5f;
+// of a row's sum that adds the chunks' in fp64: 3.0e-6, 20 roundings within a chunk
+// and one exponential, 4.4e-6
+constexpr double kEpsSum = 5e-6;
+constexpr double kEpsPair = 1e-11;      // of a sum of pairs (pair_share)
 
 struct __align__(16) Cand {
     float lo, hi;      // bounds of weight / noise
-    int idx;           // -1: none
+    int idx;           // the token; kNone, or kOpen: more than one of the chunk may be it
     int pad;
 };
+constexpr int kNone = -1, kOpen = -2;
+constexpr int kMostOpen = 64;           // threads with candidates that fp64 looks at within a chunk
 
 // What the race of a sequence is run over: the place of the new token, whether a
 // drafted one was refused there, and both rows' statistics.
@@ -69,6 +80,7 @@ struct VerifyParams {
     VerifyArgs a;
     int C, RC;         // chunks per row: of the statistics, of the race
     float c2;          // log2(e) / temperature
+    double inv_temp;   // 1 / temperature (a division in fp64 costs the race's CTAs 8 us of 64 x 5 drafts)
     float2* part;      // [B*(K+1) + B*K][C]
     Cand* cand;        // [B][RC]
     Decision* dec;     // [B]
@@ -85,9 +97,9 @@ __device__ __forceinline__ float weight(float z, float m, float c2) {
     const float x = z == m ? 0.f : (z - m) * c2;
     return fast_exp2(fmaxf(x, -200.f));
 }
-__device__ __forceinline__ double weight64(float z, float m, double temperature) {
+__device__ __forceinline__ double weight64(float z, float m, double inv_temp) {
     if (z == m) return 1.0;
-    return exp(fmax(((double)z - (double)m) / temperature, -1e300));
+    return exp(fmax(((double)z - (double)m) * inv_temp, -1e300));
 }
 
 __device__ __forceinline__ int drafted(const VerifyArgs& a, int b, int* err) {
@@ -148,7 +160,7 @@ __device__ __forceinline__ float block_max(float v, float* red) {
     return v;
 }
 
-// A larger value wins, the lower index among equal ones; index -1 never wins.
+// A larger value wins, the lower index among equal ones; a negative index never wins.
 template <typename F>
 __device__ __forceinline__ void take_better(F& v, int& i, F v2, int i2) {
     if (i2 >= 0 && (i < 0 || v2 > v || (v2 == v && i2 < i))) {
@@ -164,6 +176,21 @@ __device__ __forceinline__ void warp_best(F& v, int& i) {
         const int i2 = __shfl_xor_sync(0xffffffffu, i, o);
         take_better(v, i, v2, i2);
     }
+}
+
+// The block's best, in all threads.
+__device__ __forceinline__ void block_best(double& v, int& i, double* redv, int* redi) {
+    warp_best(v, i);
+    if ((threadIdx.x & 31) == 0) {
+        redv[threadIdx.x >> 5] = v;
+        redi[threadIdx.x >> 5] = i;
+    }
+    __syncthreads();
+    v = redv[0];
+    i = redi[0];
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w) take_better(v, i, redv[w], redi[w]);
+    __syncthreads();
 }
 
 template <bool kGreedy>
@@ -264,20 +291,113 @@ __device__ __forceinline__ void row_stats(const float2* __restrict__ part, int C
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
 }
-// Its sum in fp64, by one warp, a chunk a lane (the fp64 units take 32 cycles an
-// instruction: only where a decision needs it; by one thread it took 10 us and more, which
-// two of ten batches of 64 x 5 drafts waited for: 52 and 58 us instead of 39, 40 and 46 now).
-__device__ __noinline__ double row_sum64(const float2* __restrict__ part, int C, float m, double temperature) {
+// Its sum in fp64 from the chunks' in fp32 (kEpsSum), by one warp, a chunk a lane (the fp64
+// units take 32 cycles an instruction: only where a decision needs it; by one thread it took
+// 10 us and more, which two of ten batches of 64 x 5 drafts waited for: 52 and 58 us instead of 39,
+// 40 and 46 now).
+__device__ __noinline__ double row_sum64(const float2* __restrict__ part, int C, float m, double inv_temp) {
     double s = 0.0;
     if (m > -INFINITY)
-        for (int c = threadIdx.x & 31; c < C; c += 32) s += (double)part[c].y * weight64(part[c].x, m, temperature);
+        for (int c = threadIdx.x & 31; c < C; c += 32) s += (double)part[c].y * weight64(part[c].x, m, inv_temp);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s;
 }
+// This thread's share of a row's sum from its logits (m finite), as pairs of fp32 numbers; `tab`
+// holds 2^(k / 256) so.  The difference and its product with log2(e) / temperature are
+// taken with their rounding errors: y = yh + yl, to 5e-13 for |y| <= 24.  With yh = k / 256 + g the weight is
+// 2^(k / 256) (1 + h + h^2 / 2 + ...), h = (g + yl) ln 2, |h| < 1.4e-3, each product that counts taken with
+// its error: ~1e-12 in all.  Two rows of 50257 logits take a CTA 85 us so, in fp64 ~800.
+__device__ __noinline__ double pair_share(const float* __restrict__ row, int V, float m, double inv_temp,
+                                          const float2* tab) {
+    constexpr double kLn2 = 0.69314718055994530942;
+    constexpr float kLn2Hi = (float)kLn2, kLn2Lo = (float)(kLn2 - (double)kLn2Hi);
+    const double c = 1.4426950408889634 * inv_temp;
+    const float ch = (float)c, cl = (float)(c - (double)ch);
+    double total = 0.0;
+    for (int v0 = threadIdx.x; v0 < V; v0 += 64 * kThreads) {
+        float sum = 0.f, low = 0.f;                    // 64 weights: `low` stays small beside `sum`
+        auto add = [&](float x) {
+            const float t = __fadd_rn(sum, x), w = __fsub_rn(t, sum);
+            low = __fadd_rn(low, __fadd_rn(__fsub_rn(sum, __fsub_rn(t, w)), __fsub_rn(x, w)));
+            sum = t;
+        };
+        auto weigh = [&](float z) {
+            const float d = __fsub_rn(z, m);
+            if (!(d * ch > -80.f)) return;             // all of these together: below 2^-56 of the sum
+            const float w = __fsub_rn(d, z);           // d + de = z - m
+            const float de = __fsub_rn(__fsub_rn(z, __fsub_rn(d, w)), __fadd_rn(m, w));
+            const float yh = __fmul_rn(d, ch);
+            const float yl = __fadd_rn(__fmaf_rn(d, ch, -yh), __fmaf_rn(d, cl, __fmul_rn(de, ch)));
+            const float n = rintf(yh * 256.f), g = __fmaf_rn(n, -1.f / 256.f, yh);
+            const int k = (int)n;
+            const float2 t = tab[k & 255];
+            const float scale = __int_as_float(((k >> 8) + 127) << 23);
+            const float hh = __fmul_rn(g, kLn2Hi);
+            const float hl = __fadd_rn(__fmaf_rn(g, kLn2Hi, -hh), __fmaf_rn(g, kLn2Lo, __fmul_rn(yl, kLn2Hi)));
+            const float r = hh * (hl + hh * (0.5f + hh * (1.f / 6.f + hh * (1.f / 24.f))));
+            const float x = __fmul_rn(t.x, hh), xl = __fmaf_rn(t.x, hh, -x);
+            add(t.x * scale);
+            add(x * scale);
+            low = __fmaf_rn(__fadd_rn(t.y, __fmaf_rn(t.x, __fadd_rn(hl, r), xl)), scale, low);
+        };
+        for (int v = v0; v < V && v < v0 + 64 * kThreads; v += 8 * kThreads) {
+            float z[8];                                // asked for together
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = v + i * kThreads < V ? no_nan(__ldg(row + v + i * kThreads)) : -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) weigh(z[i]);
+        }
+        total += (double)sum + (double)low;
+    }
+    return total;
+}
+// The same in fp64; for any m.
+__device__ __noinline__ double share64(const float* __restrict__ row, int V, float m, double inv_temp) {
+    double s = 0.0;
+    if (m > -INFINITY) {
+#pragma unroll 4
+        for (int v = threadIdx.x; v < V; v += kThreads) s += weight64(no_nan(row[v]), m, inv_temp);
+    }
+    return s;
+}
+// A row's sum from its logits, in all threads of the block.
+struct SumSpace {
+    float2 tab[256];
+    double warp[kThreads / 32];
+};
+__device__ __noinline__ double logit_sum(const float* row, int V, float m, double inv_temp, bool exact, SumSpace& sp) {
+    if (!exact) {
+        const double t = exp2((double)threadIdx.x / 256.0);
+        sp.tab[threadIdx.x] = make_float2((float)t, (float)(t - (double)(float)t));
+        __syncthreads();
+    }
+    double s = exact || !(fabsf(m) < INFINITY) ? share64(row, V, m, inv_temp) : pair_share(row, V, m, inv_temp, sp.tab);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((threadIdx.x & 31) == 0) sp.warp[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = 0.0;
+    for (int w = 0; w < kThreads / 32; ++w) s += sp.warp[w];
+    __syncthreads();
+    return s;
+}
+static_assert(kThreads == 256, "a thread per entry of the table");
 // p(z) or q(z) in fp64; 0 in a row without any weight.
-__device__ __noinline__ double prob64(float z, float m, double sum, double temperature) {
-    return sum > 0.0 ? weight64(z, m, temperature) / sum : 0.0;
+__device__ __noinline__ double prob64(float z, float m, double sum, double inv_temp) {
+    return sum > 0.0 ? weight64(z, m, inv_temp) / sum : 0.0;
+}
+
+// Whether token x is accepted, u q(x) < p(x), from the logits of both rows; by the block.  (Here and
+// in settle_race out of line: within the kernels they cost 4.6 us of 35 where nothing is open.)
+__device__ __noinline__ bool settle_draft(const float* __restrict__ trow, const float* __restrict__ drow, int V, int x,
+                                          float u, float mt, float md, double inv_temp, SumSpace& sp) {
+    for (int exact = 0;; ++exact) {
+        const double st = logit_sum(trow, V, mt, inv_temp, exact, sp), sd = logit_sum(drow, V, md, inv_temp, exact, sp);
+        const double p = prob64(no_nan(trow[x]), mt, st, inv_temp);
+        const double uq = (double)u * prob64(no_nan(drow[x]), md, sd, inv_temp);
+        if (exact || !(fabs(uq - p) < 2.0 * kEpsPair * p)) return uq < p;
+    }
 }
 
 // tokens[b] and n_accepted[b]; called by one warp.
@@ -290,20 +410,22 @@ __device__ __forceinline__ void write_answer(const VerifyArgs& a, int b, int n, 
 
 // Which drafted tokens of sequence b are accepted: by a CTA, a warp per place; what
 // does not depend on one another is asked for together.  The answer is thread 0's.
+// What the chunks' sums leave open the whole CTA settles, in order, as far as it is reached.
 __device__ __forceinline__ Decision decide(const VerifyParams& p, int b) {
     __shared__ float2 row_t[kMaxK + 1], row_d[kMaxK];     // maximum, sum
-    __shared__ int take[kMaxK];
+    __shared__ int take[kMaxK];                           // 0: refused, 1: accepted, 2: open
+    __shared__ SumSpace space;
     const VerifyArgs& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nd = drafted(a, b, nullptr);
-    const double temp = (double)a.temperature;
+    const double inv_temp = p.inv_temp;
     for (int i = warp; i <= nd; i += kThreads / 32) {
         const bool drafted_here = i < nd;
         const int x = drafted_here ? a.draft[(int64_t)b * a.K + i] : 0;
         const float u = drafted_here ? a.u[(int64_t)b * a.K + i] : 0.f;
         const float2* part_t = p.part + ((int64_t)b * (a.K + 1) + i) * p.C;
         const float2* part_d = p.part + ((int64_t)a.B * (a.K + 1) + (int64_t)b * a.K + i) * p.C;
-        bool ok = drafted_here && x >= 0 && x < a.V;
+        bool ok = drafted_here && x >= 0 && x < a.V, open = false;
         if (drafted_here && !ok && lane == 0) raise_error(p.err, TFM_EBADTOKEN);
         float zt = 0.f, zd = 0.f;
         if (ok) {
@@ -330,18 +452,27 @@ __device__ __forceinline__ Decision decide(const VerifyParams& p, int b) {
             } else if (uq > 1e-30f && uq * (1.f - 2.f * kEps) > px * (1.f + 2.f * kEps)) {
                 ok = false;
             } else {
-                const double p64 = prob64(zt, mt, row_sum64(part_t, p.C, mt, temp), temp);
-                const double q64 = prob64(zd, md, row_sum64(part_d, p.C, md, temp), temp);
-                ok = (double)u * q64 < p64;
+                const double p64 = prob64(zt, mt, row_sum64(part_t, p.C, mt, inv_temp), inv_temp);
+                const double uq64 = (double)u * prob64(zd, md, row_sum64(part_d, p.C, md, inv_temp), inv_temp);
+                ok = uq64 < p64;
+                open = fabs(uq64 - p64) < 2.0 * kEpsSum * p64;
             }
         }
-        if (drafted_here && lane == 0) take[i] = ok;
+        if (drafted_here && lane == 0) take[i] = open ? 2 : ok;
     }
     __syncthreads();
+    int n = 0;
+    for (; n < nd; ++n) {
+        int ok = take[n];
+        if (ok == 2) {
+            ok = settle_draft(a.target + ((int64_t)b * (a.K + 1) + n) * a.ld_target,
+                              a.dlogits + ((int64_t)b * a.K + n) * a.ld_draft, a.V, a.draft[(int64_t)b * a.K + n],
+                              a.u[(int64_t)b * a.K + n], row_t[n].x, row_d[n].x, p.inv_temp, space);
+        }
+        if (!ok) break;
+    }
     Decision d{};
     if (threadIdx.x == 0) {
-        int n = 0;
-        while (n < nd && take[n]) ++n;
         const bool refused = n < nd;
         d = Decision{n, refused, row_t[n].x, row_t[n].y, refused ? row_d[n].x : 0.f, refused ? row_d[n].y : 0.f, {0, 0}};
     }
@@ -354,6 +485,63 @@ __global__ void __launch_bounds__(kThreads) k_verify_decide(const VerifyParams p
     if (threadIdx.x == 0) p.dec[blockIdx.x] = d;
 }
 
+// weight / noise of token v in fp64, and what a relative error of the sums is multiplied
+// with there: (p + q) / noise; yrow null: of p alone.
+__device__ __forceinline__ double race_score(const float* __restrict__ zrow, const float* __restrict__ yrow,
+                                             const float* __restrict__ erow, int v, float mt, float md, double st,
+                                             double sd, double inv_temp, double& mag) {
+    mag = 0.0;
+    const float ev = erow[v];
+    if (!(ev > 0.f)) return 0.0;
+    double w = prob64(no_nan(zrow[v]), mt, st, inv_temp);
+    if (yrow) {
+        const double q = prob64(no_nan(yrow[v]), md, sd, inv_temp);
+        mag = (w + q) / (double)ev;
+        w -= q;
+    }
+    return w / (double)ev;
+}
+__device__ __forceinline__ Cand load_cand(const int4* cd, int k) {     // from L2: other CTAs wrote them
+    const int4 w = __ldcg(cd + k);
+    return Cand{__int_as_float(w.x), __int_as_float(w.y), w.z, 0};
+}
+// The winner of a race over max(p - q, 0), kNone if that is zero everywhere: with the sums from the
+// logits, among the tokens and chunks whose upper bound reaches `from`; by the block.
+__device__ __noinline__ int settle_race(const float* __restrict__ zrow, const float* __restrict__ yrow,
+                                        const float* __restrict__ erow, const int4* cd, int RC, int V, float mt, float md,
+                                        float from, double inv_temp, SumSpace& sp, double* redv, int* redi) {
+    for (int exact = 0;; ++exact) {
+        const double st = logit_sum(zrow, V, mt, inv_temp, exact, sp), sd = logit_sum(yrow, V, md, inv_temp, exact, sp);
+        double low = 0.0, high = 0.0, next = 0.0;      // bounds: the best lower one; the two best upper ones
+        int best = kNone;
+        for (int k = 0; k < RC; ++k) {
+            const Cand x = load_cand(cd, k);
+            if (x.idx == kNone || !(x.hi >= from && x.hi > 0.f)) continue;
+            const int end = x.idx == kOpen ? min((k + 1) * kRaceChunk, V) : x.idx + 1;
+            for (int i = (x.idx == kOpen ? k * kRaceChunk : x.idx) + (int)threadIdx.x; i < end; i += kThreads) {
+                double mag;
+                const double s = race_score(zrow, yrow, erow, i, mt, md, st, sd, inv_temp, mag);
+                const double err = exact ? 0.0 : kEpsPair * mag, h = s + err;
+                if (!(h > 0.0)) continue;
+                low = fmax(low, s - err);
+                next = fmax(next, fmin(high, h));
+                take_better(high, best, h, i);
+            }
+        }
+        double top = high;
+        int token = best;
+        if (!exact) {
+            int who = low > 0.0 ? (int)threadIdx.x : kNone;
+            block_best(low, who, redv, redi);          // the best lower bound
+            const int left = __syncthreads_count(best >= 0 && high >= low);
+            const int more = __syncthreads_or(next > 0.0 && next >= low);
+            if (left > 1 || more || (left == 1 && who < 0)) continue;
+        }
+        block_best(top, token, redv, redi);
+        return token;
+    }
+}
+
 // kDecide: each CTA decides for itself (see launch_verify_draft).
 template <bool kDecide>
 __global__ void __launch_bounds__(kThreads, 4) k_verify_race(const VerifyParams p) {
@@ -361,13 +549,15 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify_race(const VerifyParams 
     __shared__ double redv[kThreads / 32];
     __shared__ int redi[kThreads / 32];
     __shared__ int last;
+    __shared__ SumSpace space;
     __shared__ double sums[2];                         // of the rows of p and q, in fp64
+    __shared__ float open_from;                        // the bound of what the chunks' sums leave open
     pdl_wait();
     pdl_trigger();
     const VerifyArgs& a = p.a;
     const int c = (int)(blockIdx.x % (unsigned)p.RC), b = (int)(blockIdx.x / (unsigned)p.RC);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const double temp = (double)a.temperature;
+    const double inv_temp = p.inv_temp;
     const float* erow = a.noise + (int64_t)b * a.ld_noise;
     float e[4 * kRaceVec];
     load_chunk<kRaceVec>(erow, c, a.V, 0.f, e);        // needed whatever the row is
@@ -384,17 +574,15 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify_race(const VerifyParams 
     const float inv_t = st > 0.f ? 1.f / st : 0.f, inv_d = sd > 0.f ? 1.f / sd : 0.f;
     const float* zrow = a.target + ((int64_t)b * (a.K + 1) + n) * a.ld_target;
     const float* yrow = refused ? a.dlogits + ((int64_t)b * a.K + n) * a.ld_draft : nullptr;
-    // weight / noise of token v in fp64; with_q false: of p alone
-    auto score64 = [&](int v, bool with_q, double st64, double sd64) -> double {
-        const float ev = erow[v];
-        if (!(ev > 0.f)) return 0.0;
-        double w = prob64(no_nan(zrow[v]), mt, st64, temp);
-        if (with_q && yrow) w -= prob64(no_nan(yrow[v]), md, sd64, temp);
-        return w / (double)ev;
+    auto score64 = [&](int v, bool with_q, double st64, double sd64, double& mag) -> double {
+        return race_score(zrow, with_q ? yrow : nullptr, erow, v, mt, md, st64, sd64, inv_temp, mag);
     };
-    auto sum_t64 = [&]() { return row_sum64(p.part + ((int64_t)b * (a.K + 1) + n) * p.C, p.C, mt, temp); };
+    // bounds in fp32 of a score in fp64
+    auto below = [](double x) { return (float)x - kEps * fabsf((float)x); };
+    auto above = [](double x) { return (float)x + kEps * fabsf((float)x); };
+    auto sum_t64 = [&]() { return row_sum64(p.part + ((int64_t)b * (a.K + 1) + n) * p.C, p.C, mt, inv_temp); };
     auto sum_d64 = [&]() {
-        return refused ? row_sum64(p.part + ((int64_t)a.B * (a.K + 1) + (int64_t)b * a.K + n) * p.C, p.C, md, temp) : 0.0;
+        return refused ? row_sum64(p.part + ((int64_t)a.B * (a.K + 1) + (int64_t)b * a.K + n) * p.C, p.C, md, inv_temp) : 0.0;
     };
     float hi[4 * kRaceVec];
     float lo = -INFINITY;
@@ -454,38 +642,56 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify_race(const VerifyParams 
     Cand* out = p.cand + (int64_t)b * p.RC + c;
     if (any == 1 && !several && lo > 0.f) {
         if (mine) *out = Cand{lo, top, index_of<kRaceVec>(c, __ffs(mine) - 1), 0};
-    } else {
+    } else if (!refused) {
         double v = 0.0;
-        int best = -1;
+        int best = kNone;
         if (any) {                                     // (the same in all threads)
             if (warp == 0) {
                 const double t = sum_t64();
                 if (lane == 0) sums[0] = t;
-            } else if (warp == 1) {
-                const double q = sum_d64();
-                if (lane == 0) sums[1] = q;
             }
             __syncthreads();
         }
-        if (mine) {
-            const double st64 = sums[0], sd64 = sums[1];
-            for (; mine; mine &= mine - 1) {
-                const int idx = index_of<kRaceVec>(c, __ffs(mine) - 1);
-                const double s = score64(idx, true, st64, sd64);
-                if (s > 0.0) take_better(v, best, s, idx);
-            }
+        for (; mine; mine &= mine - 1) {
+            const int idx = index_of<kRaceVec>(c, __ffs(mine) - 1);
+            double mag;
+            const double s = score64(idx, false, sums[0], 0.0, mag);
+            if (s > 0.0) take_better(v, best, s, idx);
         }
-        warp_best(v, best);
-        if (lane == 0) {
-            redv[warp] = v;
-            redi[warp] = best;
+        block_best(v, best, redv, redi);
+        if (threadIdx.x == 0) *out = Cand{below(v), above(v), best, 0};
+    } else if (any == 0 || any > kMostOpen) {
+        top = block_max(top, red);
+        if (threadIdx.x == 0) *out = Cand{lo, top, any ? kOpen : kNone, 0};
+    } else {
+        if (warp == 0) {
+            const double t = sum_t64();
+            if (lane == 0) sums[0] = t;
+        } else if (warp == 1) {
+            const double q = sum_d64();
+            if (lane == 0) sums[1] = q;
         }
         __syncthreads();
-        if (threadIdx.x == 0) {
-#pragma unroll
-            for (int w = 1; w < kThreads / 32; ++w) take_better(v, best, redv[w], redi[w]);
-            // the winner's bounds: fp64 to fp32 and back
-            *out = Cand{(float)v * (1.f - kEps), (float)v * (1.f + kEps), best, 0};
+        float low = -INFINITY, high = -INFINITY, next = -INFINITY;    // next: the second highest upper bound
+        int best = kNone;
+        for (; mine; mine &= mine - 1) {
+            const int idx = index_of<kRaceVec>(c, __ffs(mine) - 1);
+            double mag;
+            const double s = score64(idx, true, sums[0], sums[1], mag), err = kEpsSum * mag;
+            low = fmaxf(low, below(s - err));
+            const float h = above(s + err);
+            if (h > high) best = idx;
+            next = fmaxf(next, fminf(high, h));
+            high = fmaxf(high, h);
+        }
+        low = block_max(low, red);
+        const bool may = high > 0.f && high >= low;
+        const int left = __syncthreads_count(may), more = __syncthreads_or(next > 0.f && next >= low);
+        if (left == 1 && !more) {
+            if (may) *out = Cand{low, high, best, 0};
+        } else {
+            high = block_max(high, red);
+            if (threadIdx.x == 0) *out = Cand{low, high, left ? kOpen : kNone, 0};
         }
     }
     // The last CTA of the sequence merges the chunks.
@@ -495,61 +701,77 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify_race(const VerifyParams 
     __syncthreads();
     if (!last) return;
     __threadfence();
-    double v = 0.0;
-    int token = -1;
+    int4* const cd = reinterpret_cast<int4*>(p.cand + (int64_t)b * p.RC);
+    auto cand = [&](int k) { return load_cand(cd, k); };
     if (warp == 0) {
-        const int4* cd = reinterpret_cast<const int4*>(p.cand + (int64_t)b * p.RC);
-        auto cand = [&](int k) {                       // from L2: other CTAs wrote them
-            const int4 w = __ldcg(cd + k);
-            return Cand{__int_as_float(w.x), __int_as_float(w.y), w.z, 0};
-        };
         float lb = -INFINITY;
+        int only, total;
+        auto contenders = [&]() {                      // how many, and the one if it is one
+            int cnt = 0;
+            only = INT_MIN;
+            for (int k = lane; k < p.RC; k += 32) {
+                const Cand x = cand(k);
+                if (x.idx != kNone && x.hi >= lb) {
+                    ++cnt;
+                    only = x.idx;
+                }
+            }
+            total = __reduce_add_sync(0xffffffffu, cnt);
+            only = __reduce_max_sync(0xffffffffu, only);
+        };
         for (int k = lane; k < p.RC; k += 32) {
             const Cand x = cand(k);
-            if (x.idx >= 0) lb = fmaxf(lb, x.lo);
+            if (x.idx != kNone) lb = fmaxf(lb, x.lo);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) lb = fmaxf(lb, __shfl_xor_sync(0xffffffffu, lb, o));
-        int cnt = 0, only = -1;
-        for (int k = lane; k < p.RC; k += 32) {
-            const Cand x = cand(k);
-            if (x.idx >= 0 && x.hi >= lb) {
-                ++cnt;
-                only = x.idx;
-            }
-        }
-        const int total = __reduce_add_sync(0xffffffffu, cnt);
-        if (total == 1) {
-            token = __reduce_max_sync(0xffffffffu, only);
-        } else if (total > 1) {
+        contenders();
+        int token = kNone;
+        bool open = false;
+        if (total == 1 && only >= 0 && (!refused || lb > 0.f)) {
+            token = only;
+        } else if (total > 0) {
             const double st64 = sum_t64(), sd64 = sum_d64();
+            double v = 0.0;
+            float low = lb;
             for (int k = lane; k < p.RC; k += 32) {
                 const Cand x = cand(k);
-                if (x.idx >= 0 && x.hi >= lb) take_better(v, token, score64(x.idx, true, st64, sd64), x.idx);
+                if (x.idx < 0 || !(x.hi >= lb)) continue;
+                double mag;
+                const double s = score64(x.idx, true, st64, sd64, mag), err = kEpsSum * mag;
+                take_better(v, token, s, x.idx);
+                low = fmaxf(low, below(s - err));
+                __stcg(cd + k, make_int4(__float_as_int(below(s - err)), __float_as_int(above(s + err)), x.idx, 0));
             }
             warp_best(v, token);
+            if (refused) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) low = fmaxf(low, __shfl_xor_sync(0xffffffffu, low, o));
+                lb = low;
+                contenders();
+                open = !(total == 1 && only >= 0 && lb > 0.f);
+                token = open ? kNone : only;
+            }
         }
-        if (lane == 0) redi[0] = token;
+        if (lane == 0) {
+            redi[0] = token;
+            open_from = open ? lb : INFINITY;
+        }
     }
     __syncthreads();
-    token = redi[0];
+    int token = redi[0];
+    const float from = open_from;
     __syncthreads();
+    if (from < INFINITY) token = settle_race(zrow, yrow, erow, cd, p.RC, a.V, mt, md, from, inv_temp, space, redv, redi);
     if (token < 0 && refused) {
         // max(p - q, 0) is zero everywhere: the race over p, in fp64
-        v = 0.0;
+        double v = 0.0, mag;
         const double st64 = sum_t64();
         for (int x = threadIdx.x; x < a.V; x += kThreads) {
-            const double s = score64(x, false, st64, 0.0);
+            const double s = score64(x, false, st64, 0.0, mag);
             if (s > 0.0) take_better(v, token, s, x);
         }
-        warp_best(v, token);
-        if (lane == 0) {
-            redv[warp] = v;
-            redi[warp] = token;
-        }
-        __syncthreads();
-        if (warp == 0)
-            for (int w = 0; w < kThreads / 32; ++w) take_better(v, token, redv[w], redi[w]);
+        block_best(v, token, redv, redi);
     }
     if (warp == 0) write_answer(a, b, n, token);
 }
@@ -594,6 +816,7 @@ cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t st) {
     p.C = (a.V + kChunk - 1) / kChunk;
     p.RC = (a.V + kRaceChunk - 1) / kRaceChunk;
     const bool greedy = a.temperature == 0.f;
+    p.inv_temp = greedy ? 0.0 : 1.0 / (double)a.temperature;
     p.c2 = greedy ? 0.f : (float)(1.4426950408889634 / (double)a.temperature);
     uint8_t* w = static_cast<uint8_t*>(a.ws);
     p.part = reinterpret_cast<float2*>(w);

@@ -503,15 +503,16 @@ tfm_status tfm_prefix_attention(const void* q, const void* k_prefix, const void*
  * drawn from max(p_i - q_i, 0) (from p_i, should that be zero everywhere),
  * after n accepted tokens from p_n.  The draw is an exponential race: the token
  * with the largest weight / noise[b, v] wins, noise [B, ld_noise] fp32
- * independent Exp(1) values (normal, positive), so every token is distributed
+ * independent Exp(1) values (normal, positive, below 2^126), so every token is distributed
  * as if drawn from the target model alone.  temperature 0 is greedy: accepted
  * iff x is target_i's largest logit, the new token the largest logit;
  * draft_logits, u and noise are then not read and may be NULL.
  * Ties go to the lowest token.  A logit of -infinity or NaN has no weight; +infinity takes
  * all of it.  Outputs: n_accepted [B], tokens [B, K + 1] (int32): the accepted
  * tokens, the new one, then -1; the new one is -1 as well if no token has any
- * weight.  Statistics are kept in fp32, decisions that fp32 leaves open are made
- * in fp64.
+ * weight.  Decisions are those of 64 bits: what fp32
+ * statistics leave open within their error bounds is decided in fp64 with the rows' sums taken
+ * anew from the logits.  (A weight below 2^-126 of its row's largest counts as none in a draw.)
  * n_draft (int32 [B], device) may be NULL: K everywhere.  A value outside [0, K]
  * sets TFM_EINVAL in the device error word and is clamped; a drafted id outside
  * [0, V) sets TFM_EBADTOKEN and is refused.  V >= 1, 0 <= K <= 64, leading
