@@ -455,8 +455,8 @@ tfm_status tfm_decode_attention(const void* q, const void* k_cache, const void* 
  * aligned, tfm_packed_attention_workspace_bytes(T, n_seq) bytes (0 for bad
  * sizes), not used by another call in flight; its contents need not survive.
  * Offsets that decrease or leave [0, T] set TFM_EINVAL in the device error word
- * (tfm_device_status); such a sequence is skipped and nothing outside the
- * buffers is touched.  Capturable in a CUDA graph. */
+ * (tfm_device_status); o's T rows, those of the other sequences too, then hold values that
+ * are not specified, and nothing outside the buffers is touched.  Capturable in a CUDA graph. */
 size_t tfm_packed_attention_workspace_bytes(int32_t T, int32_t n_seq);
 tfm_status tfm_packed_attention(const void* q, const void* k, const void* v, void* o,
                                 const int32_t* cu_seqlens, int32_t n_seq, int32_t T, int32_t H,

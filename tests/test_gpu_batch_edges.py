@@ -48,3 +48,27 @@ def test_a_value_that_is_not_finite_in_every_prompt(H, Hkv, dh):
     want[last, :, 5] = float("inf")
     for _ in range(5):
         assert torch.equal(_packed(q, k, bad, _ints(cu)), want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cu", [[0, 150, 20, 110], [0, 300, 50, 110], [0, 200, 0, 200, 0, 200], [-5, 70, 200], [10, 2 ** 31 - 1, -2 ** 31, 90],
+                                [200, 150, 100, 50, 0], [0] + [190, 10] * 300], ids=lambda x: "-".join(map(str, x[:5])))
+@pytest.mark.parametrize("H", [1, 40])                  # each block a CTA of its own, or a list
+def test_offsets_that_decrease_or_leave_the_rows(cu, H, dtype):
+    """The device error word says so, and nothing around the buffers is written."""
+    T, dh = 200, 32
+    g = torch.Generator().manual_seed(1)
+    q, k, v = (torch.randn(T, H, dh, generator=g).to(dtype).cuda() for _ in range(3))
+    around = torch.full((3 * T, H, dh), 7.0, dtype=dtype, device="cuda")
+    n = tfm.packed_attention_workspace_bytes(T, len(cu) - 1)
+    ws = torch.full((3 * 4096 + n,), 99, dtype=torch.uint8, device="cuda")
+    tfm.packed_attention(q, k, v, around[T:2 * T], _ints(cu), ws[4096:4096 + n])
+    with pytest.raises(tfm.TfmError) as e:
+        tfm.device_status()
+    assert e.value.status == tfm.TFM_EINVAL
+    assert (around[:T] == 7.0).all() and (around[2 * T:] == 7.0).all()
+    assert (ws[:4096] == 99).all() and (ws[4096 + n:] == 99).all()
+    # the next call with offsets as they should be is as ever
+    want = _packed(q, k, v, _ints([0, 150, 200]))
+    tfm.device_status()
+    assert torch.isfinite(want).all()
