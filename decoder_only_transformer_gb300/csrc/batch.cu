@@ -126,6 +126,9 @@ tfm_status tfm_prefix_attention(const void* q, const void* k_prefix, const void*
     if (!std::isfinite(scale)) return fail(TFM_EINVAL, "scale must be finite");
     if (dh != 32 && dh != 64 && dh != 128) return fail(TFM_EUNSUPPORTED, "prefix attention: dh in {32, 64, 128}");
     if ((int64_t)(H / Hkv) * T > 128) return fail(TFM_EUNSUPPORTED, "prefix attention: (H / Hkv) * T <= 128");
+    if (tfm::prefix_key_tiles(B, H, Hkv, T, prefix_len, max_seq) > tfm::kMaxPrefixTiles)
+        return fail(TFM_EINVAL, "too many key tiles: Hkv * ceil(B / floor(128 / (H / Hkv * T))) * ceil(prefix_len / 64) + "
+                                "B * Hkv * ceil(max_seq / 64) at most 2^25");
     if (B == 0) return TFM_OK;
     if (!q || !k_cache || !v_cache || !o || !lens || !workspace || (prefix_len && (!k_prefix || !v_prefix)))
         return fail(TFM_EINVAL, "NULL pointer");
@@ -155,7 +158,6 @@ tfm_status tfm_prefix_attention(const void* q, const void* k_prefix, const void*
     a.ws = workspace;
     cudaError_t e = cudaSuccess;
     const tfm_status st = tfm::launch_prefix_attention(a, static_cast<cudaStream_t>(stream), &e);
-    if (st == TFM_EINVAL) return fail(st, "B * H * T * prefix_len too large");
     if (st != TFM_OK) return fail(st, "could not encode prefix attention tensor maps");
     return e == cudaSuccess ? TFM_OK : cuda_fail(e, "prefix attention launch");
 }
@@ -176,7 +178,7 @@ tfm_status tfm_verify_draft(const float* target, int64_t ld_target, const float*
                             int32_t* n_accepted, void* workspace, size_t workspace_bytes,
                             void* stream) {
     if (!verify_sizes_ok(B, K, V))
-        return fail(TFM_EINVAL, "bad sizes: B >= 0, 0 <= K <= 64, 1 <= V <= 2^24, B*(K+1) <= 2^20, B*(2K+1)*V/4096 < 2^30");
+        return fail(TFM_EINVAL, "bad sizes: B >= 0, 0 <= K <= 64, 1 <= V <= 2^24, B*(K+1) <= 2^20, a workspace below 2^33 bytes");
     // outside, log2(e) / temperature or a difference of logits leaves fp32's range
     if (temperature != 0.f && !(temperature >= 1e-30f && temperature <= 1e30f))
         return fail(TFM_EINVAL, "temperature must be 0 or in [1e-30, 1e30]");

@@ -289,6 +289,10 @@ struct PrefixArgs {
     void* ws;
 };
 size_t prefix_workspace_bytes(int B, int H, int Hkv, int T, int dh);
+// Tiles of 64 keys of all jobs, with every cache full: at most kMaxPrefixTiles, so that
+// their costs stay below 2^31.
+constexpr int64_t kMaxPrefixTiles = 1 << 25;
+int64_t prefix_key_tiles(int B, int H, int Hkv, int T, int P, int max_seq);
 tfm_status launch_prefix_attention(const PrefixArgs& a, cudaStream_t st, cudaError_t* e);
 
 // Verification of drafted tokens (k_verify.cu).

@@ -789,7 +789,7 @@ PrefixGeom geom_of(int B, int H, int Hkv, int T, int P, int max_seq, int dh) {
     g.nb = kRowsP / g.GT;
     if (g.nb > B) g.nb = B > 0 ? B : 1;
     g.nrt = (B + g.nb - 1) / g.nb;
-    g.np = (P + kKeys - 1) / kKeys;
+    g.np = (int)(((int64_t)P + kKeys - 1) / kKeys);
     // swizzle atoms are 8 rows of 128 bytes, or 16 of 64
     const int atom = dh == 32 ? 16 : 8;
     g.q_pad = (g.GT + atom - 1) / atom * atom;
@@ -838,7 +838,7 @@ cudaError_t launch_dh(const PrefixArgs& a, PrefixGeom g, const CUtensorMap* maps
     parts.range_own = reinterpret_cast<int2*>(w + l.range_own);
     // two CTAs per SM; no more than there can be tiles
     const int64_t most = (int64_t)g.Hkv * g.nrt * g.np +
-                         (int64_t)g.B * g.Hkv * ((a.max_seq + kKeys - 1) / kKeys);
+                         (int64_t)g.B * g.Hkv * (((int64_t)a.max_seq + kKeys - 1) / kKeys);
     g.ctas = 2 * sm_count() < kMaxCtas ? 2 * sm_count() : kMaxCtas;
     if (most < g.ctas) g.ctas = (int)most;
     e = launch_pdl(k_prefix_part<DH>, dim3((unsigned)g.ctas), dim3(kThreadsX), smem, st, maps[0], maps[1], maps[2],
@@ -857,10 +857,13 @@ size_t prefix_workspace_bytes(int B, int H, int Hkv, int T, int dh) {
     return layout(geom_of(B, H, Hkv, T, 0, 1, dh), dh).total;
 }
 
+int64_t prefix_key_tiles(int B, int H, int Hkv, int T, int P, int max_seq) {
+    const PrefixGeom g = geom_of(B, H, Hkv, T, P, max_seq, 64);
+    return (int64_t)g.Hkv * g.nrt * g.np + (int64_t)g.B * g.Hkv * (((int64_t)g.max_seq + kKeys - 1) / kKeys);
+}
+
 tfm_status launch_prefix_attention(const PrefixArgs& a, cudaStream_t st, cudaError_t* e) {
     const PrefixGeom g = geom_of(a.B, a.H, a.Hkv, a.T, a.P, a.max_seq, a.dh);
-    if ((int64_t)g.Hkv * g.nrt * g.np + (int64_t)g.B * g.Hkv * ((a.max_seq + kKeys - 1) / kKeys) > (1 << 25))
-        return TFM_EINVAL;                             // costs stay below 2^31
     CUtensorMap maps[6];
     if (!query_groups_map(&maps[0], a.q, a.B, a.Hkv, g.GT, a.dh, g.nb) ||
         !query_groups_map(&maps[1], a.q, a.B, a.Hkv, g.GT, a.dh, 1) ||

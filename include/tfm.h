@@ -477,7 +477,8 @@ tfm_status tfm_packed_attention(const void* q, const void* k, const void* v, voi
  * caches behind lens[b] and in the prefix behind prefix_len is not looked at.
  * bf16 only, everything dense; dh in {32, 64, 128}, (H / Hkv) * T <= 128,
  * B <= 4096, B * H * T <= 2^24, Hkv * max_prefix below 2^31, B * Hkv * max_seq
- * below 2^30, B * H * T * prefix_len below 2^37.
+ * below 2^30, and at most 2^25 key tiles: Hkv * ceil(B / floor(128 / ((H / Hkv) * T)))
+ * * ceil(prefix_len / 64) + B * Hkv * ceil(max_seq / 64).
  * prefix_len may be 0 (its pointers may then be NULL), and lens[b] may be 0.
  * scale <= 0 means 1/sqrt(dh); it must be finite.  Pointers 16-byte aligned,
  * lens 4-byte.  workspace: device, 16-byte aligned,
@@ -517,7 +518,7 @@ tfm_status tfm_prefix_attention(const void* q, const void* k_prefix, const void*
  * sets TFM_EINVAL in the device error word and is clamped; a drafted id outside
  * [0, V) sets TFM_EBADTOKEN and is refused.  V >= 1, 0 <= K <= 64, leading
  * dimensions >= V and multiples of 4, logits and noise 16-byte aligned, the rest
- * 4-byte, V <= 2^24, B * (K + 1) <= 2^20, B * (2K + 1) * V / 4096 < 2^30,
+ * 4-byte, V <= 2^24, B * (K + 1) <= 2^20, a workspace below 2^33 bytes,
  * temperature 0 or in [1e-30, 1e30].
  * workspace: device, 16-byte aligned, tfm_verify_draft_workspace_bytes(B, K, V)
  * bytes (0 for bad sizes), not used by another call in flight.  Results do not
