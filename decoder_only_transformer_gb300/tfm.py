@@ -547,7 +547,15 @@ def _one_device(*named):
             raise ValueError(f"{name}: on {t.device}, the current device is cuda:{here}")
 
 
+def _int32(*named):
+    """Refuses numbers that the C ABI takes as int32 and ctypes would cut to their low bits."""
+    for value, name in named:
+        if not -1 << 31 <= value < 1 << 31:
+            raise ValueError(f"{name}: {value} does not fit 32 bits")
+
+
 def packed_attention_workspace_bytes(T, n_seq):
+    _int32((T, "T"), (n_seq, "n_seq"))
     return load().tfm_packed_attention_workspace_bytes(T, n_seq)
 
 
@@ -588,8 +596,11 @@ def packed_attention(q, k, v, o, cu_seqlens, workspace, window=0, scale=0.0, str
             and workspace.is_contiguous()):
         _refuse_packed(q, k, v, o, cu_seqlens, workspace)
     T, H, dh = shape
+    Hkv, n_seq = kv[1], cu_seqlens.shape[0] - 1
+    if (T | H | Hkv | n_seq | window) >> 31:
+        _int32((T, "T"), (H, "H"), (Hkv, "Hkv"), (n_seq, "n_seq"), (window, "window"))
     status = lib.tfm_packed_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                      cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1, T, H, kv[1], dh,
+                                      cu_seqlens.data_ptr(), n_seq, T, H, Hkv, dh,
                                       _Strides(sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1]), scale,
                                       window, TFM_BF16 if q.dtype is torch.bfloat16 else _mode_of(q),
                                       workspace.data_ptr(), workspace.nbytes,
@@ -599,6 +610,7 @@ def packed_attention(q, k, v, o, cu_seqlens, workspace, window=0, scale=0.0, str
 
 
 def prefix_attention_workspace_bytes(B, H, Hkv, T, dh):
+    _int32((B, "B"), (H, "H"), (Hkv, "Hkv"), (T, "T"), (dh, "dh"))
     return load().tfm_prefix_attention_workspace_bytes(B, H, Hkv, T, dh)
 
 
@@ -649,15 +661,21 @@ def prefix_attention(q, k_prefix, v_prefix, k_cache, v_cache, o, lens, workspace
     B, H, T, dh = shape
     _, Hkv, max_seq, _ = cache
     max_prefix = prefix[1]
+    if prefix_len is None:
+        prefix_len = max_prefix
+    if (B | H | T | Hkv | max_seq | max_prefix | prefix_len) >> 31:
+        _int32((B, "B"), (H, "H"), (T, "T"), (Hkv, "Hkv"), (max_seq, "max_seq"), (max_prefix, "max_prefix"),
+               (prefix_len, "prefix_len"))
     status = lib.tfm_prefix_attention(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(),
                                       v_cache.data_ptr(), o.data_ptr(), lens.data_ptr(), B, H, Hkv, T,
-                                      max_prefix if prefix_len is None else prefix_len, max_prefix, max_seq, dh,
+                                      prefix_len, max_prefix, max_seq, dh,
                                       scale, workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, here))
     if status:
         _check(status)
 
 
 def verify_draft_workspace_bytes(B, K, V):
+    _int32((B, "B"), (K, "K"), (V, "V"))
     return load().tfm_verify_draft_workspace_bytes(B, K, V)
 
 
@@ -707,6 +725,8 @@ def verify_draft(target, draft_logits, draft, n_draft, u, noise, vocab, tokens, 
     torch, here = _now()
     f32, i32 = torch.float32, torch.int32
     greedy = temperature == 0
+    if vocab >> 31:
+        _int32((vocab, "vocab"))
     if greedy or draft_logits is None or u is None or noise is None or draft.dim() != 2:
         _refuse_verify(target, draft_logits, draft, n_draft, u, noise, vocab, tokens, n_accepted, workspace, greedy)
     else:
@@ -727,6 +747,8 @@ def verify_draft(target, draft_logits, draft, n_draft, u, noise, vocab, tokens, 
                                          and n_draft.numel() == B and n_draft.is_contiguous()))):
             _refuse_verify(target, draft_logits, draft, n_draft, u, noise, vocab, tokens, n_accepted, workspace, greedy)
     B, K = draft.shape
+    if (B | K) >> 31:
+        _int32((B, "B"), (K, "K"))
 
     def at(t):
         return None if t is None else t.data_ptr()

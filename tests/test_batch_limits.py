@@ -1,8 +1,8 @@
 """Limits of the batched-serving entry points as the header states them, on both sides: what is beyond is refused by name;
 what is not gets past that check, to the one for the pointers, which are NULL here.  No GPU is touched."""
-import ctypes
-
+import numpy as np
 import pytest
+import torch
 
 from decoder_only_transformer_gb300 import tfm
 
@@ -54,3 +54,93 @@ def test_verification_workspace_limit(lib):
         n = lib.tfm_verify_draft_workspace_bytes(B, 0, V)
         assert (0 < n < 1 << 33) if ok else n == 0
         assert ("NULL pointer" if ok else "2^33 bytes") in _verify(lib, B, 0, V)
+
+
+class _Cuda:
+    """As much of a dense tensor on device 0 as the binding looks at, of any size."""
+
+    def __init__(self, shape, dtype):
+        self.shape, self.dtype, self.is_cuda, self.device = tuple(shape), dtype, True, torch.device("cuda:0")
+        self.nbytes = 1 << 62
+
+    def stride(self, i=None):
+        s = [1]
+        for n in self.shape[:0:-1]:
+            s.insert(0, s[0] * max(n, 1))
+        return tuple(s) if i is None else s[i]
+
+    def numel(self):
+        return int(np.prod([int(n) for n in self.shape], dtype=object))
+
+    def dim(self):
+        return len(self.shape)
+
+    def get_device(self):
+        return 0
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 256
+
+
+BIG = (1 << 32) + 5                                      # 5 in its low bits
+
+
+@pytest.fixture
+def no_library(monkeypatch):
+    """No call reaches the library: what it was given is returned."""
+    calls = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *args: calls.append((name, args)) or 0
+
+    monkeypatch.setattr(tfm, "_lib", Lib())
+    monkeypatch.setattr(tfm, "_now", lambda: (torch, 0))
+    monkeypatch.setattr(tfm, "_raw_stream", lambda stream, device: 0)
+    return calls
+
+
+def _packed_call(T=8, H=2, Hkv=2, n=1, **kw):
+    bf, ints = torch.bfloat16, torch.int32
+    q, kv = (T, H, 32), (T, Hkv, 32)
+    tfm.packed_attention(_Cuda(q, bf), _Cuda(kv, bf), _Cuda(kv, bf), _Cuda(q, bf), _Cuda((n + 1,), ints), _Cuda((64,), torch.uint8), **kw)
+
+
+def _prefix_call(B=2, H=2, T=1, P=8, cap=2, rows=8, **kw):
+    bf = torch.bfloat16
+    p, c = (2, P, 32), (cap, 2, rows, 32)
+    tfm.prefix_attention(_Cuda((B, H, T, 32), bf), _Cuda(p, bf), _Cuda(p, bf), _Cuda(c, bf), _Cuda(c, bf),
+                         _Cuda((B, T, H * 32), bf), _Cuda((B,), torch.int32), _Cuda((64,), torch.uint8), **kw)
+
+
+def _verify_call(B=2, K=2, V=8, vocab=8, **kw):
+    f, i = torch.float32, torch.int32
+    tfm.verify_draft(_Cuda((B * (K + 1), V), f), _Cuda((B * K, V), f), _Cuda((B, K), i), None, _Cuda((B, K), f), _Cuda((B, V), f),
+                     vocab, _Cuda((B, K + 1), i), _Cuda((B,), i), _Cuda((64,), torch.uint8), **kw)
+
+
+@pytest.mark.parametrize("call,kw", [
+    (_packed_call, dict(T=BIG)), (_packed_call, dict(H=BIG, Hkv=1)), (_packed_call, dict(H=BIG, Hkv=BIG)),
+    (_packed_call, dict(n=BIG)), (_packed_call, dict(window=BIG)), (_packed_call, dict(window=-BIG)),
+    (_prefix_call, dict(B=BIG, cap=BIG)), (_prefix_call, dict(T=BIG)), (_prefix_call, dict(P=BIG)), (_prefix_call, dict(rows=BIG)),
+    (_prefix_call, dict(prefix_len=BIG)), (_prefix_call, dict(prefix_len=-BIG)),
+    (_verify_call, dict(B=BIG)), (_verify_call, dict(V=BIG, vocab=BIG)), (_verify_call, dict(V=BIG, vocab=BIG, temperature=0.0)),
+], ids=str)
+def test_numbers_beyond_32_bits_are_refused(no_library, call, kw):
+    call()
+    assert len(no_library) == 1                          # the call is otherwise in order
+    with pytest.raises(ValueError, match="32 bits"):
+        call(**kw)
+    assert len(no_library) == 1
+
+
+@pytest.mark.parametrize("size", [lambda n: tfm.packed_attention_workspace_bytes(n, 1), lambda n: tfm.packed_attention_workspace_bytes(1, n),
+                                  lambda n: tfm.prefix_attention_workspace_bytes(n, 1, 1, 1, 64),
+                                  lambda n: tfm.verify_draft_workspace_bytes(1, 1, n)])
+def test_workspaces_of_numbers_beyond_32_bits(size):
+    assert size(5) > 0
+    with pytest.raises(ValueError, match="32 bits"):
+        size(BIG)
