@@ -24,6 +24,9 @@ tfm_status cuda_fail(cudaError_t e, const char* what) {
     return fail(TFM_ECUDA, "%s: %s", what, tfm::cuda_error_text(e));
 }
 
+// (beyond 2^126 its product with log2(e), by which the kernels scale, leaves fp32)
+bool scale_ok(float scale) { return std::isfinite(scale) && scale <= 0x1p126f; }
+
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 }  // namespace
@@ -46,7 +49,7 @@ tfm_status tfm_packed_attention(const void* q, const void* k, const void* v, voi
     if (((int64_t)T / 32 + n_seq) * H > (int64_t)1 << 30) return fail(TFM_EINVAL, "(T / 32 + n_seq) * H too large");
     if (mode != TFM_FP32 && mode != TFM_BF16) return fail(TFM_EINVAL, "bad mode");
     if (window < 0) return fail(TFM_EINVAL, "window must be >= 0");
-    if (!std::isfinite(scale)) return fail(TFM_EINVAL, "scale must be finite");
+    if (!scale_ok(scale)) return fail(TFM_EINVAL, "scale must be finite and at most 2^126");
     if (dh < 1) return fail(TFM_EINVAL, "dh must be positive");
     if (mode == TFM_BF16 && dh != 32 && dh != 64 && dh != 128)
         return fail(TFM_EUNSUPPORTED, "bf16 packed attention: dh in {32, 64, 128}");
@@ -123,7 +126,7 @@ tfm_status tfm_prefix_attention(const void* q, const void* k_prefix, const void*
         return fail(TFM_EINVAL, "prefix_len=%d outside [0, max_prefix=%d]", prefix_len, max_prefix);
     if (max_seq < 1 || (int64_t)B * Hkv * max_seq >= (1 << 30) || (int64_t)Hkv * max_prefix > INT32_MAX)
         return fail(TFM_EINVAL, "max_seq must be positive, B*Hkv*max_seq below 2^30, Hkv*max_prefix below 2^31");
-    if (!std::isfinite(scale)) return fail(TFM_EINVAL, "scale must be finite");
+    if (!scale_ok(scale)) return fail(TFM_EINVAL, "scale must be finite and at most 2^126");
     if (dh != 32 && dh != 64 && dh != 128) return fail(TFM_EUNSUPPORTED, "prefix attention: dh in {32, 64, 128}");
     if ((int64_t)(H / Hkv) * T > 128) return fail(TFM_EUNSUPPORTED, "prefix attention: (H / Hkv) * T <= 128");
     if (tfm::prefix_key_tiles(B, H, Hkv, T, prefix_len, max_seq) > tfm::kMaxPrefixTiles)

@@ -450,7 +450,7 @@ tfm_status tfm_decode_attention(const void* q, const void* k_cache, const void* 
  * Strides are at least dh (a dimension of one row or head excepted), multiples
  * of 16 bytes and below 2^39 bytes; o's rows must not overlap each other or an input.  bf16 mode: dh in {32, 64, 128};
  * fp32 mode: dh % 4 == 0, dh <= 128.  T <= 2^30, n_seq <= 2^20,
- * (T / 32 + n_seq) * H <= 2^30.  scale <= 0 means 1/sqrt(dh); it must be finite.
+ * (T / 32 + n_seq) * H <= 2^30.  scale <= 0 means 1/sqrt(dh); it must be finite and at most 2^126.
  * Pointers 16-byte aligned, cu_seqlens 4-byte.  workspace: device, 16-byte
  * aligned, tfm_packed_attention_workspace_bytes(T, n_seq) bytes (0 for bad
  * sizes), not used by another call in flight; its contents need not survive.
@@ -480,7 +480,7 @@ tfm_status tfm_packed_attention(const void* q, const void* k, const void* v, voi
  * below 2^30, and at most 2^25 key tiles: Hkv * ceil(B / floor(128 / ((H / Hkv) * T)))
  * * ceil(prefix_len / 64) + B * Hkv * ceil(max_seq / 64).
  * prefix_len may be 0 (its pointers may then be NULL), and lens[b] may be 0.
- * scale <= 0 means 1/sqrt(dh); it must be finite.  Pointers 16-byte aligned,
+ * scale <= 0 means 1/sqrt(dh); it must be finite and at most 2^126.  Pointers 16-byte aligned,
  * lens 4-byte.  workspace: device, 16-byte aligned,
  * tfm_prefix_attention_workspace_bytes(B, H, Hkv, T, dh) bytes (0 for bad
  * sizes), not used by another call in flight.  A length outside [0, max_seq]

@@ -46,6 +46,16 @@ def test_prefix_beyond_its_key_tiles(lib, B, H, Hkv, T, P):
     assert "key tiles" in _prefix(lib, B, H, Hkv, T, P, 1)
 
 
+@pytest.mark.parametrize("scale,ok", [(2.0 ** 126, True), (2.0 ** 126 * (1 + 2.0 ** -23), False), (3.4e38, False), (1e-45, True),
+                                      (-3.4e38, True), (float("inf"), False)])
+def test_scales_that_the_kernels_can_apply(lib, scale, ok):
+    want = "NULL pointer" if ok else "scale"
+    assert want in _prefix(lib, 1, 1, 1, 1, 1, 1, scale=scale)
+    for mode in (tfm.TFM_BF16, tfm.TFM_FP32):
+        assert lib.tfm_packed_attention(None, None, None, None, None, 1, 4, 1, 1, 64, None, scale, 0, mode, None, 0, None) == tfm.TFM_EINVAL
+        assert want in lib.tfm_last_error().decode()
+
+
 def test_verification_workspace_limit(lib):
     V = 1 << 24
     each = 8 * 2048 + 16 * 4096 + 32 + 4                 # statistics, candidates, decision, counter of a sequence
