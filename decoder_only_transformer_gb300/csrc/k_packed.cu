@@ -927,6 +927,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 const float negm = m == -INFINITY ? 0.f : -m;      // a row that has seen no key yet
                 const uint64_t negm2 = f2_pack(negm, negm);
                 uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
+                // P in bf16, as the MMA that sums in fp32 takes it with V in bf16: up to 2^-8 off each, at
+                // random, which the average over the keys keeps below the output's own rounding; the
+                // row sum adds the weights before it (rounded ones would be unpacked again for it).
                 uint32_t pw[32];
 #pragma unroll
                 for (int e = 0; e < kKV; e += 2) {

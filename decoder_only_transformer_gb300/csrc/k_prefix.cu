@@ -608,6 +608,8 @@ __global__ void __launch_bounds__(kThreadsX, 2)
                     const float negm = m == -INFINITY ? 0.f : -m;     // no visible key yet: every p is 0
                     const uint64_t negm2 = f2_pack(negm, negm);
                     uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
+                    // P in bf16, the operand's type beside V in bf16; the row sum adds the weights
+                    // before that rounding (up to 2^-8 each, at random)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t pw[16];

@@ -432,7 +432,11 @@ tfm_status tfm_decode_attention(const void* q, const void* k_cache, const void* 
 /* ---- Serving a batch whose sequences have different lengths: packed prompts,
  * new tokens over a prefix all sequences share, and drafted tokens checked
  * against the model's own distribution.  All three read their lengths from the
- * device, so a recorded graph serves every later batch of the same bounds. */
+ * device, so a recorded graph serves every later batch of the same bounds.
+ * In bf16 both attentions keep scores, row maxima, row sums and outputs in fp32; the
+ * unnormalised weights are rounded to bf16 for their product with the values (the tensor
+ * cores' operand; the row's sum adds them unrounded), and the output once more at the end:
+ * two roundings of 2^-8 relative at most. */
 
 /* Causal attention over packed prompts: n_seq sequences one behind the other in
  * T rows, sequence b the rows [cu_seqlens[b], cu_seqlens[b + 1]) (int32

@@ -72,3 +72,18 @@ def test_offsets_that_decrease_or_leave_the_rows(cu, H, dtype):
     want = _packed(q, k, v, _ints([0, 150, 200]))
     tfm.device_status()
     assert torch.isfinite(want).all()
+
+
+def test_large_scores_in_fp32():
+    """Scores of some hundreds: the scale folded with log2(e) and the approximate exponential stay within the roundings
+    that the bound counts (it has 2 dh for the score, of which the product takes dh, the folded scale 2)."""
+    from batch_ref import bound, f64, packed
+    for dh, lens, factor, scale in ((16, [150, 31], 4.0, 1.7), (64, [200], 3.0, 0.0), (128, [97, 64], 2.0, 0.3), (4, [300], 8.0, 0.9)):
+        g = torch.Generator().manual_seed(dh)
+        q, k, v = (torch.randn(sum(lens), 2, dh, generator=g).cuda() * f for f in (factor, factor, 1.0))
+        got = f64(_packed(q, k, v, _ints(np.cumsum([0] + lens)), scale=scale))
+        s = float(np.float32(scale)) or dh ** -0.5
+        norm = lambda t: float(np.sqrt((f64(t) ** 2).sum(-1).max()))
+        smax = norm(q) * norm(k) * s
+        assert smax > 100
+        assert np.abs(got - packed(q, k, v, lens, 0, s)).max() <= bound(f64(v), dh, max(lens), smax, torch.float32)
