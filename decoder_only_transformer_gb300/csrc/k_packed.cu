@@ -294,12 +294,9 @@ cudaError_t launch_f32(const PackedArgs& a, cudaStream_t st) {
 // sequence, the longest key ranges first, from which the persistent kernel's CTAs take
 // their items.
 //
-// Blocks are found without a scan: block t of sequence b has the slot
-// cu[b] / kRows + b + t, slots of different sequences never meet (a sequence of
-// L rows from row c on has at most (c + L) / kRows - c / kRows + 1 blocks), and
-// the sequence of a slot is found by a search over cu[b] / kRows + b, which
-// grows with b.  A counting sort over at most 256 length classes then orders them (by 256
-// threads: 1024 took 0.5 us more, and most batches have fewer blocks).
+// Blocks are found without a scan, by their slots (sequence_of; here a slot a thread).  A
+// counting sort over at most 256 length classes then orders them (by 256 threads: 1024 took
+// 0.5 us more, and most batches have fewer blocks).
 constexpr int kPlanThreads = 256;
 constexpr int kBins = 256;
 constexpr int kPlanCache = 4096;        // offsets kept in shared memory
@@ -402,9 +399,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_packed_plan(const int32_t* __r
 // is half as wide.  (Tiles of 128 with one place: 12 prompts of up to 2048 at 16/4 x 128 90 us
 // instead of 77, 24 of up to 1024 at 12 x 64 35.5 instead of 32.5; 3 of up to 8192 at
 // 16 x 64 the same 168.)  What bounds it is latency, of softmax and MMA warps alike: at
-// d_head 64 a pair of tiles takes 1210 cycles, of them ~510 the exponentials of both on
-// the MUFU, ~550 the tensor pipe; without exponentials it takes 960, without any
-// arithmetic of the softmax 860, and with a quarter of the MMAs besides 690.  (Two CTAs per
+// d_head 64 a pair of tiles takes ~1260 cycles, of them ~510 the exponentials of both on
+// the MUFU, ~550 the tensor pipe; of 1210 (before the row maxima were taken from the scores)
+// 960 were left without exponentials, 860 without any arithmetic of the softmax, and 690 with a
+// quarter of the MMAs besides.  (Two CTAs per
 // SM, one place for S each and 96 registers a softmax thread: 173 us instead of 168.)
 constexpr int kQ = 128;
 constexpr int kThreadsP = 384;          // control, softmax of tile A, softmax of tile B

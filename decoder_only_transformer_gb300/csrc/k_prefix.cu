@@ -24,10 +24,10 @@
 // sum, unnormalised O) per row, and a second kernel joins a row's pieces of the
 // prefix and its own cache exactly: with M = max m, o = sum 2^(m - M) O / sum 2^(m - M) l.
 //
-// Measured: own caches of 1280 positions, 192 sequences of 16 x 64, without a prefix: 149 us,
-// 6.7 TB/s, as fast as a copy.  Short caches are bound by what a piece costs besides its
+// Measured: own caches of 1280 positions, 192 sequences of 16 x 64, without a prefix: 152 us,
+// 6.6 TB/s, as fast as a copy.  Short caches are bound by what a piece costs besides its
 // tiles (2000 cycles and more of the chain S, softmax, P.V, O out; 192 over a prefix of
-// 16384, up to 300 own positions: 60 us, of them ~17 pieces' ends, 20 own tiles, 18 the
+// 16384, up to 300 own positions: 61 us, of them ~17 pieces' ends, 20 own tiles, 18 the
 // prefix), small calls by the latency of the two launches (4 chats: 8.7 us; 64 at 16/4 x 128
 // under 2048: 19 us, of them ~5 until the first scores, ~3 the join).
 #include "common.cuh"
@@ -701,9 +701,9 @@ __global__ void __launch_bounds__(kThreadsX, 2)
 // own job, kAtOnce at a time: their maxima, sums and values are in flight together, so
 // that a row costs one trip to L2 per kAtOnce pieces.  A CTA takes the 128 rows of a row
 // tile, whose prefix pieces lie side by side.  Eight at once up to a wave of CTAs (16 answers
-// of 5 tokens over 8192, 16 pieces a row: 20.4 us in all, four at once 22); with more rows
+// of 5 tokens over 8192, 16 pieces a row: 20 us in all, four at once 22); with more rows
 // there are few pieces each and four at once fit more CTAs on an SM (101 sequences of 8
-// tokens, 16/4 x 128: 19.6 us, eight at once 21.1).
+// tokens over 64 shared ones, 16/4 x 128: 17.0 us, eight at once 18.6).
 template <int DH, int kAtOnce>
 __global__ void __launch_bounds__(kRowsP, kAtOnce == 8 ? 6 : 10) k_prefix_join(PrefixParts in, PrefixGeom gm, int H,
                                                         const int32_t* __restrict__ lens,

@@ -16,7 +16,7 @@
 // the last CTA of a sequence to finish merges the chunks' winners and writes the
 // answer.  A race of few CTAs decides itself, without the second launch; of many, each
 // would repeat 13 chains of dependent loads.
-// 64 sequences of 5 drafted tokens and 50257 logits take 36 us: the first launch 23, bound by
+// 64 sequences of 5 drafted tokens and 50257 logits take 35 us: the first launch 23, bound by
 // reading the logits (127 MB); decisions and race, bound by their chains of dependent
 // loads and by the race's ~50 instructions per logit, the rest.  One sequence of 4 and 32000
 // takes 9 us, the latency of two launches.
