@@ -505,20 +505,26 @@ __device__ __forceinline__ Cand load_cand(const int4* cd, int k) {     // from L
     const int4 w = __ldcg(cd + k);
     return Cand{__int_as_float(w.x), __int_as_float(w.y), w.z, 0};
 }
-// The winner of a race over max(p - q, 0), kNone if that is zero everywhere: with the sums from the
-// logits, among the tokens and chunks whose upper bound reaches `from`; by the block.
+// The new token after a refused one, where the chunks' sums leave it open: the winner of the race over
+// max(p - q, 0) with the sums from the logits, among the tokens and chunks whose upper bound
+// reaches `from`; then, if the residual there is no more than fp32 holds (or `from` is inf: nothing
+// is there), among all; then, if it is zero everywhere, the winner of the race over p.  By the block.
 __device__ __noinline__ int settle_race(const float* __restrict__ zrow, const float* __restrict__ yrow,
                                         const float* __restrict__ erow, const int4* cd, int RC, int V, float mt, float md,
                                         float from, double inv_temp, SumSpace& sp, double* redv, int* redi) {
-    for (int exact = 0;; ++exact) {
+    bool all = !(from < INFINITY);
+    for (int exact = all;; ++exact) {
         const double st = logit_sum(zrow, V, mt, inv_temp, exact, sp), sd = logit_sum(yrow, V, md, inv_temp, exact, sp);
+        bool every = true;                             // were looked at
         double low = 0.0, high = 0.0, next = 0.0;      // bounds: the best lower one; the two best upper ones
         int best = kNone;
         for (int k = 0; k < RC; ++k) {
             const Cand x = load_cand(cd, k);
-            if (x.idx == kNone || !(x.hi >= from && x.hi > 0.f)) continue;
-            const int end = x.idx == kOpen ? min((k + 1) * kRaceChunk, V) : x.idx + 1;
-            for (int i = (x.idx == kOpen ? k * kRaceChunk : x.idx) + (int)threadIdx.x; i < end; i += kThreads) {
+            const bool chunk = all || x.idx == kOpen, in = all || (x.idx != kNone && x.hi >= from && x.hi > 0.f);
+            every = every && chunk && in;
+            if (!in) continue;
+            const int end = chunk ? min((k + 1) * kRaceChunk, V) : x.idx + 1;
+            for (int i = (chunk ? k * kRaceChunk : x.idx) + (int)threadIdx.x; i < end; i += kThreads) {
                 double mag;
                 const double s = race_score(zrow, yrow, erow, i, mt, md, st, sd, inv_temp, mag);
                 const double err = exact ? 0.0 : kEpsPair * mag, h = s + err;
@@ -528,8 +534,6 @@ __device__ __noinline__ int settle_race(const float* __restrict__ zrow, const fl
                 take_better(high, best, h, i);
             }
         }
-        double top = high;
-        int token = best;
         if (!exact) {
             int who = low > 0.0 ? (int)threadIdx.x : kNone;
             block_best(low, who, redv, redi);          // the best lower bound
@@ -537,9 +541,20 @@ __device__ __noinline__ int settle_race(const float* __restrict__ zrow, const fl
             const int more = __syncthreads_or(next > 0.0 && next >= low);
             if (left > 1 || more || (left == 1 && who < 0)) continue;
         }
-        block_best(top, token, redv, redi);
-        return token;
+        block_best(high, best, redv, redi);
+        if (best >= 0 && (every || high * (double)erow[best] > 0x1p-125)) return best;
+        if (every) break;
+        all = true;
+        exact = 0;
     }
+    double v = 0.0, mag;
+    int token = kNone;
+    for (int x = threadIdx.x; x < V; x += kThreads) {
+        const double s = race_score(zrow, nullptr, erow, x, mt, md, 1.0, 0.0, inv_temp, mag);
+        if (s > 0.0) take_better(v, token, s, x);
+    }
+    block_best(v, token, redv, redi);
+    return token;
 }
 
 // kDecide: each CTA decides for itself (see launch_verify_draft).
@@ -762,17 +777,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_verify_race(const VerifyParams 
     int token = redi[0];
     const float from = open_from;
     __syncthreads();
-    if (from < INFINITY) token = settle_race(zrow, yrow, erow, cd, p.RC, a.V, mt, md, from, inv_temp, space, redv, redi);
-    if (token < 0 && refused) {
-        // max(p - q, 0) is zero everywhere: the race over p, in fp64
-        double v = 0.0, mag;
-        const double st64 = sum_t64();
-        for (int x = threadIdx.x; x < a.V; x += kThreads) {
-            const double s = score64(x, false, st64, 0.0, mag);
-            if (s > 0.0) take_better(v, token, s, x);
-        }
-        block_best(v, token, redv, redi);
-    }
+    if (refused && token < 0 && st > 0.f)
+        token = settle_race(zrow, yrow, erow, cd, p.RC, a.V, mt, md, from, inv_temp, space, redv, redi);
     if (warp == 0) write_answer(a, b, n, token);
 }
 

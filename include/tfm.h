@@ -517,7 +517,8 @@ tfm_status tfm_prefix_attention(const void* q, const void* k_prefix, const void*
  * tokens, the new one, then -1; the new one is -1 as well if no token has any
  * weight.  Decisions are those of 64 bits: what fp32
  * statistics leave open within their error bounds is decided in fp64 with the rows' sums taken
- * anew from the logits.  (A weight below 2^-126 of its row's largest counts as none in a draw.)
+ * anew from the logits.  (A weight below 2^-126 of its row's largest counts as none in a draw,
+ * unless there are no others.)
  * n_draft (int32 [B], device) may be NULL: K everywhere.  A value outside [0, K]
  * sets TFM_EINVAL in the device error word and is clamped; a drafted id outside
  * [0, V) sets TFM_EBADTOKEN and is refused.  V >= 1, 0 <= K <= 64, leading

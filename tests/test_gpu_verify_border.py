@@ -156,3 +156,26 @@ def test_refused_drafts_of_nearly_equal_models(B):
     draft, u = torch.zeros(B, 1, dtype=torch.int32), torch.full((B, 1), 2.0)      # u outside [0, 1): always refused
     noise = torch.empty(B, target.shape[1]).exponential_(generator=g).clamp_(min=1e-30)
     _same(target, dl, draft, u, noise, V, 1.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [50, 9001])
+@pytest.mark.parametrize("B", [4, 90])
+def test_residuals_that_fp32_does_not_hold(B, V):
+    """All of p and of q but e^-100 lies on one token, so that the residual is among weights that fp32 has none of."""
+    g = torch.Generator().manual_seed(B + V)
+    ld = (V + 3) // 4 * 4
+    target = -100 - 20 * torch.rand(B * 2, ld, generator=g)
+    dl = -100 - 20 * torch.rand(B, ld, generator=g)
+    top = torch.randint(0, V, (B,), generator=g)
+    rows = target.view(B, 2, ld)[:, 0]
+    at = torch.arange(B)
+    rows[at, top] = 0.0
+    dl[at, top] = 0.0
+    draft = (dl[:, :V] - rows[:, :V]).argmax(1, keepdim=True).int()      # q(x) far above p(x): refused
+    u = torch.full((B, 1), 0.99)
+    noise = torch.empty(B, ld).exponential_(generator=g).clamp_(min=1e-30)
+    p, q = _probs64(rows[:, :V], 1.0), _probs64(dl[:, :V], 1.0)
+    assert (p[at, top] == 1).all() and (q[at, top] == 1).all()
+    assert not np.isin(verify(target, dl, draft, [1] * B, u, noise, V, 1.0)[0][:, 0], top.numpy()[:, None]).all()
+    _same(target, dl, draft, u, noise, V, 1.0)
