@@ -1,0 +1,137 @@
+// cache8.cuh - the 8-bit key/value cache: codes, scales, and the rows of its sequences.
+//
+// Codes [B, Hkv, max_seq, dh], one byte each: int8, or e4m3 (the fp8 format of 4 exponent
+// and 3 mantissa bits).  Scales [B, Hkv, ceil(max_seq / block)] fp32: a position's value is
+// code * scale of its block of positions.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace tfm {
+
+// Rows of sequence b among the packed new rows, n = 0 if they are not as they should be.
+struct SeqRows {
+    int row0;          // first row
+    int n;             // rows
+    int len;           // cached positions, the n new ones the last
+    bool ok;
+};
+
+__device__ __forceinline__ SeqRows seq_rows(const int32_t* __restrict__ cu, const int32_t* __restrict__ lens, int b,
+                                            int per, int T, int max_seq) {
+    SeqRows s;
+    s.len = __ldg(lens + b);
+    s.ok = s.len >= 0 && s.len <= max_seq;
+    if (cu) {
+        const int a = __ldg(cu + b), e = __ldg(cu + b + 1);
+        const bool rows_ok = a >= 0 && e >= a && e <= T;
+        s.row0 = a;
+        s.n = rows_ok ? e - a : 0;
+        s.ok = s.ok && rows_ok;
+    } else {
+        s.row0 = b * per;
+        s.n = per;
+    }
+    return s;
+}
+
+// ------------------------------------------------------------------ codes
+// The code of x / s (s > 0), the nearest, ties to even, as 64 bits decide it: the quotient
+// of two fp32 numbers is never within 2^-53 of a border between two codes unless it lies
+// on it, so its rounding to fp64 decides as the quotient itself would.  NaN gives 0,
+// infinities the largest code.  Slow: for extreme scales and rows with such values only.
+template <bool E4M3>
+static __device__ __noinline__ uint32_t code_exact(float x, float s) {
+    if (x != x) return 0;
+    const double q = (double)x / (double)s;
+    if constexpr (E4M3) {
+        float f = __double2float_rz(q);
+        if ((double)f != q) f = __uint_as_float(__float_as_uint(f) | 1u);       // to odd: no second rounding
+        return (uint32_t)__nv_cvt_float_to_fp8(f, __NV_SATFINITE, __NV_E4M3);
+    } else {
+        return (uint32_t)__double2int_rn(fmin(fmax(q, -127.0), 127.0)) & 255u;
+    }
+}
+
+template <bool E4M3>
+__device__ __forceinline__ float code_top() { return E4M3 ? 448.0f : 127.0f; }
+
+// x / s as fp32 on the right side of the one border between two codes in its cell: y = x r
+// (r = 1 / s rounded) is within 2 ulp of the quotient, and the sign of x - s m, which a
+// fused multiply-add gives exactly for scales between 2^-100 and 2^100, says on which side
+// of the border m the quotient lies, or that it lies on it.
+template <bool E4M3>
+__device__ __forceinline__ float settled(float x, float s, float r) {
+    float a = fabsf(x) * r;
+    float m;
+    if constexpr (E4M3) {
+        m = a < 0.015625f ? (floorf(a * 512.0f) + 0.5f) * 0x1p-9f                       // subnormal codes: steps of 2^-9
+                          : __uint_as_float((__float_as_uint(a) & 0xFFF00000u) | 0x80000u);
+    } else {
+        m = floorf(a) + 0.5f;
+    }
+    const float d = fmaf(-s, m, fabsf(x));
+    if (d > 0.0f) a = fmaxf(a, __uint_as_float(__float_as_uint(m) + 1u));
+    else if (d < 0.0f) a = fminf(a, __uint_as_float(__float_as_uint(m) - 1u));
+    else a = m;
+    return copysignf(a, x);
+}
+
+// Four codes of x[0..4) / s in a word, from x r; where that is too near a border to
+// decide, `open` is set and the word is not to be used.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t codes4(const float* x, float r, bool& open) {
+    if constexpr (E4M3) {
+        uint32_t w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float y0 = x[2 * h] * r, y1 = x[2 * h + 1] * r;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float y = j ? y1 : y0;
+                // normal codes drop 20 mantissa bits, half of their step is 0x80000; below
+                // 2^-6 the step is that of the subnormals: left to the exact form
+                const uint32_t u = __float_as_uint(y);
+                open = open || ((u & 0xFFFFFu) - 0x7FFF8u) <= 16u || (fabsf(y) < 0.0156251f && y != 0.0f);
+            }
+            asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n\tcvt.u32.u16 %0, t;\n\t}"
+                : "=r"(w[h]) : "f"(y0), "f"(y1));
+        }
+        return w[0] | w[1] << 16;
+    } else {
+        uint32_t u[4];
+        float far = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float y = x[j] * r;
+            const float t = y + 12582912.0f;                   // 1.5 2^23: the sum's last bits are the integer
+            far = fmaxf(far, fabsf(y - (t - 12582912.0f)));
+            u[j] = __float_as_uint(t);
+        }
+        open = open || far > 0.49995f;                         // |y| <= 128, off by 2^-22 of it at most
+        return __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+    }
+}
+
+// One code of a quotient that fp32 holds on the right side of every border.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t code_of(float y) {
+    if constexpr (E4M3) return (uint32_t)__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+    else return (uint32_t)__float2int_rn(y) & 255u;
+}
+
+template <bool E4M3>
+__device__ __forceinline__ float code_value(uint32_t c) {      // the low byte
+    if constexpr (E4M3) {
+        const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)(c & 255u), __NV_E4M3);
+        return __half2float(__half(h));
+    } else {
+        return (float)(int8_t)(c & 255u);
+    }
+}
+
+}  // namespace tfm

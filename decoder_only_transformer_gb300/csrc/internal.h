@@ -315,4 +315,59 @@ struct VerifyArgs {
 size_t verify_workspace_bytes(int B, int K, int V);
 cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t st);
 
+// ---- the 8-bit key/value cache (cache8.cu has the entry points)
+// Rotary positions of packed rows (k_rope_rows.cu): strides in elements, {q token, q head,
+// k token, k head, then the outputs' four}.
+struct RopeRowsArgs {
+    const void* q;
+    const void* k;
+    void* qo;
+    void* ko;
+    const int32_t* positions;
+    const double* inv_freq;
+    int T, H, Hkv, dh, rot, interleaved;
+    float mscale;
+    int bf16;
+    int64_t strides[8];
+};
+cudaError_t launch_rope_rows(const RopeRowsArgs& a, cudaStream_t st);
+
+// New rows into the cache, and rows out of it (k_cache8.cu): strides {k token, k head, v
+// token, v head}; reading writes k and v and nothing else.
+struct Cache8Args {
+    const void* k;
+    const void* v;
+    uint8_t* kc;
+    uint8_t* vc;
+    float* ks;
+    float* vs;
+    const int32_t* cu;
+    const int32_t* lens;
+    int B, T, Hkv, dh, max_seq, block;
+    int e4m3, bf16;
+    int64_t strides[4];
+};
+cudaError_t launch_cache8_write(const Cache8Args& a, cudaStream_t st);
+cudaError_t launch_cache8_read(const Cache8Args& a, cudaStream_t st);
+
+// Attention of new rows over the cache (k_cache8_attn.cu): strides {q token, q head, o
+// token, o head}.
+struct Cache8AttnArgs {
+    const void* q;
+    const uint8_t* kc;
+    const uint8_t* vc;
+    const float* ks;
+    const float* vs;
+    void* o;
+    const int32_t* cu;
+    const int32_t* lens;
+    int B, T, H, Hkv, max_new, dh, max_seq, block;
+    int e4m3, window;
+    float scale;
+    int64_t strides[4];
+    void* ws;
+};
+size_t cache8_attention_workspace_bytes(int B, int H, int Hkv, int max_new, int dh);
+tfm_status launch_cache8_attention(const Cache8AttnArgs& a, cudaStream_t st, cudaError_t* e);
+
 }  // namespace tfm

@@ -15,6 +15,8 @@ from . import _build
 
 TFM_OK, TFM_EINVAL, TFM_ENOMEM, TFM_ECUDA, TFM_EBADTOKEN, TFM_ETIMEOUT, TFM_EUNSUPPORTED = range(7)
 TFM_FP32, TFM_BF16 = 0, 1
+TFM_CODE_INT8, TFM_CODE_E4M3 = 0, 1
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3, "wavelength": 4}
 STATUS_NAMES = {0: "TFM_OK", 1: "TFM_EINVAL", 2: "TFM_ENOMEM", 3: "TFM_ECUDA",
                 4: "TFM_EBADTOKEN", 5: "TFM_ETIMEOUT", 6: "TFM_EUNSUPPORTED"}
 HEADER = os.path.join(_build.ROOT, "include", "tfm.h")
@@ -66,6 +68,7 @@ _lib = None
 
 _V, _I32, _I64, _F, _SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
                            ctypes.c_size_t)
+_D = ctypes.c_double
 _SIGS = {
     "tfm_abi_version": ([], _I32),
     "tfm_validate_config": ([ctypes.POINTER(Config)], _I32),
@@ -107,6 +110,16 @@ _SIGS = {
     "tfm_verify_draft_workspace_bytes": ([_I32, _I32, _I32], _SZ),
     "tfm_verify_draft": ([_V, _I64, _V, _I64, _V, _V, _V, _V, _I64, _I32, _I32, _I32, _F, _V, _V,
                           _V, _SZ, _V], _I32),
+    "tfm_rope_frequencies": ([_D, _I32, _I32, _D, _D, _D, _D, ctypes.POINTER(_D), ctypes.POINTER(_F)], _I32),
+    "tfm_rope_rows": ([_V, _V, _V, _V, _V, _V, _I32, _I32, _I32, _I32, _I32, _I32, ctypes.POINTER(ctypes.c_int64), _F,
+                       _I32, _V], _I32),
+    "tfm_cache8_write": ([_V, _V, _V, _V, _V, _V, _V, _V, _I32, _I32, _I32, _I32, _I32, _I32,
+                          ctypes.POINTER(ctypes.c_int64), _I32, _I32, _V], _I32),
+    "tfm_cache8_read": ([_V, _V, _V, _V, _V, _V, _V, _V, _I32, _I32, _I32, _I32, _I32, _I32,
+                         ctypes.POINTER(ctypes.c_int64), _I32, _I32, _V], _I32),
+    "tfm_cache8_attention_workspace_bytes": ([_I32, _I32, _I32, _I32, _I32], _SZ),
+    "tfm_cache8_attention": ([_V, _V, _V, _V, _V, _V, _V, _V, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
+                              ctypes.POINTER(ctypes.c_int64), _I32, _I32, _F, _V, _SZ, _V], _I32),
     "tfm_linear": ([_V, _V, _V, _I64, _I32, _I32, _I64, _I32, _I32, _I32, _V], _I32),
     "tfm_swiglu": ([_V, _V, _V, _V, _V, _I64, _I32, _I32, _I32, _V, _SZ, _I32, _V], _I32),
     "tfm_swiglu_workspace_bytes": ([_I64, _I32, _I32], _SZ),
@@ -758,6 +771,211 @@ def verify_draft(target, draft_logits, draft, n_draft, u, noise, vocab, tokens, 
                                   at(n_draft), at(u), at(noise), 0 if noise is None else noise.stride(0), B, K,
                                   vocab, temperature, tokens.data_ptr(), n_accepted.data_ptr(),
                                   workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, here))
+    if status:
+        _check(status)
+
+
+# ---- the 8-bit key/value cache: rotary positions of packed rows, write, read, attention
+_Strides4 = ctypes.c_int64 * 4
+
+
+def rope_frequencies(theta, rot, scaling="plain", factor=1.0, original=0.0, low=1.0, high=32.0):
+    """The rot/2 rotary frequencies (radians a position; a float64 tensor on the host) and
+    the factor for the rotated values; scaling is one of ROPE_SCALINGS."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling: {scaling!r}, one of {', '.join(ROPE_SCALINGS)} is required")
+    _int32((rot, "rot"))
+    out = _torch().empty(max(rot // 2, 1), dtype=_torch().float64)
+    mscale = ctypes.c_float()
+    _check(load().tfm_rope_frequencies(theta, rot, ROPE_SCALINGS[scaling], factor, original, low, high,
+                                       ctypes.cast(out.data_ptr(), ctypes.POINTER(_D)), ctypes.byref(mscale)))
+    return out, mscale.value
+
+
+def _refuse_rows(named, T, dh, dtype):
+    """Rows [T, heads, dh] with dense dh at any token and head strides."""
+    for t, name in named:
+        if not t.is_cuda:
+            raise ValueError(f"{name}: a CUDA tensor is required, got one on {t.device}")
+        if t.dim() != 3 or t.shape[0] != T or t.shape[2] != dh or (t.numel() and t.stride(2) != 1):
+            raise ValueError(f"{name}: [{T}, heads, {dh}] with dense rows of dh is required, got {tuple(t.shape)}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name}: dtype {t.dtype}, {dtype} is required")
+
+
+def _refuse_rope_rows(q, k, q_out, k_out, positions, inv_freq):
+    if q.dim() != 3:
+        raise ValueError("q: [T, heads, dh] is required")
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out: both or neither")
+    pairs = ((q, "q", q_out, "q_out"),) + (((k, "k", k_out, "k_out"),) if k is not None else ())
+    for a, name, b, out in pairs:
+        _refuse_rows(((a, name), (b, out)), q.shape[0], q.shape[2], q.dtype)
+        _shape(b, a.shape, out)
+    _numel(positions, q.shape[0], "positions")
+    _dev(positions, "positions", _t("int32"))
+    _dev(inv_freq, "inv_freq", _t("float64"))
+    _one_device(*((t, n) for p in pairs for t, n in ((p[0], p[1]), (p[2], p[3]))), (positions, "positions"),
+                (inv_freq, "inv_freq"))
+
+
+def rope_rows(q, k, q_out, k_out, positions, inv_freq, interleaved=True, mscale=1.0, stream=None):
+    """Rotary positions of packed rows q [T, H, dh] and k [T, Hkv, dh] (bf16 or fp32, dense
+    rows of dh at any token and head strides; k may be None) into q_out and k_out, which may
+    be q and k: the first 2 len(inv_freq) coordinates of every head turn by
+    positions[t] * inv_freq[i] (int32 and float64, device) and are multiplied by mscale."""
+    lib = _lib or load()
+    torch, here = _now()
+    shape = q.shape
+    kk, ko = (q, q_out) if k is None or k_out is None else (k, k_out)
+    if not (len(shape) == 3 and here == q.get_device() == q_out.get_device() == kk.get_device() == ko.get_device()
+            == positions.get_device() == inv_freq.get_device() and (k is None) == (k_out is None)
+            and q.dtype is q_out.dtype is kk.dtype is ko.dtype and shape == q_out.shape and kk.shape == ko.shape
+            and len(kk.shape) == 3 and kk.shape[0] == shape[0] and kk.shape[2] == shape[2]
+            and 1 == q.stride(2) == q_out.stride(2) == kk.stride(2) == ko.stride(2)
+            and positions.dtype is torch.int32 and positions.numel() == shape[0] and positions.is_contiguous()
+            and inv_freq.dtype is torch.float64 and inv_freq.is_contiguous()):
+        _refuse_rope_rows(q, k, q_out, k_out, positions, inv_freq)
+    T, H, dh = shape
+    Hkv, rot = 0 if k is None else kk.shape[1], 2 * inv_freq.numel()
+    if (T | H | Hkv | rot) >> 31:
+        _int32((T, "T"), (H, "H"), (Hkv, "Hkv"), (rot, "rot"))
+    sq, sk, so, sp = q.stride(), kk.stride(), q_out.stride(), ko.stride()
+    status = lib.tfm_rope_rows(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+                               None if k is None else k_out.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), T, H,
+                               Hkv, dh, rot, 1 if interleaved else 0,
+                               _Strides(sq[0], sq[1], sk[0], sk[1], so[0], so[1], sp[0], sp[1]), mscale,
+                               TFM_BF16 if q.dtype is torch.bfloat16 else _mode_of(q), _raw_stream(stream, here))
+    if status:
+        _check(status)
+
+
+def _refuse_cache8(k_codes, v_codes, k_scales, v_scales, lens, block, cu_seqlens, Hkv, dh):
+    """The cache and the lengths; Hkv None: any."""
+    for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+        _dev(t, name, _t("int8", "float8_e4m3fn"))
+        if t.dim() != 4 or t.shape[3] != dh or (Hkv is not None and t.shape[1] != Hkv):
+            raise ValueError(f"{name}: [B, {'Hkv' if Hkv is None else Hkv}, max_seq, {dh}] is required, got {tuple(t.shape)}")
+    _shape(v_codes, k_codes.shape, "v_codes")
+    if v_codes.dtype != k_codes.dtype:
+        raise TypeError(f"v_codes: dtype {v_codes.dtype}, {k_codes.dtype} is required")
+    _dev(lens, "lens", _t("int32"))
+    if lens.dim() != 1 or lens.shape[0] > k_codes.shape[0]:
+        raise ValueError(f"lens: one dimension of at most {k_codes.shape[0]} sequences is required, got {tuple(lens.shape)}")
+    if block < 1:
+        raise ValueError(f"block: {block} positions")
+    shape = (*k_codes.shape[:2], -(-k_codes.shape[2] // block))
+    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        _dev(t, name, _t("float32"))
+        _shape(t, shape, name)
+    if cu_seqlens is not None:
+        _dev(cu_seqlens, "cu_seqlens", _t("int32"))
+        _shape(cu_seqlens, (lens.shape[0] + 1,), "cu_seqlens")
+    _one_device((k_codes, "k_codes"), (v_codes, "v_codes"), (k_scales, "k_scales"), (v_scales, "v_scales"),
+                (lens, "lens"), (cu_seqlens, "cu_seqlens"))
+
+
+def _cache8_ok(torch, here, kc, vc, ks, vs, lens, block, cu):
+    shape, scales = kc.shape, ks.shape
+    return (len(shape) == 4 and here == kc.get_device() == vc.get_device() == ks.get_device() == vs.get_device()
+            == lens.get_device() and kc.dtype is vc.dtype and (kc.dtype is torch.int8 or kc.dtype is torch.float8_e4m3fn)
+            and torch.float32 is ks.dtype is vs.dtype and lens.dtype is torch.int32 and shape == vc.shape
+            and scales == vs.shape and block > 0 and tuple(scales) == (shape[0], shape[1], -(-shape[2] // block))
+            and len(lens.shape) == 1 and lens.shape[0] <= shape[0] and kc.is_contiguous() and vc.is_contiguous()
+            and ks.is_contiguous() and vs.is_contiguous() and lens.is_contiguous()
+            and (cu is None or (cu.get_device() == here and cu.dtype is torch.int32 and cu.dim() == 1
+                                and cu.shape[0] == lens.shape[0] + 1 and cu.is_contiguous())))
+
+
+def _cache8_rows(read, k, v, kc, vc, ks, vs, lens, block, cu, stream):
+    lib = _lib or load()
+    torch, here = _now()
+    shape, cache = k.shape, kc.shape
+    if not (len(shape) == 3 and here == k.get_device() == v.get_device() and k.dtype is v.dtype and shape == v.shape
+            and 1 == k.stride(2) == v.stride(2) and _cache8_ok(torch, here, kc, vc, ks, vs, lens, block, cu)
+            and shape[1] == cache[1] and shape[2] == cache[3]):
+        if k.dim() != 3:
+            raise ValueError("k: [T, Hkv, dh] is required")
+        _refuse_rows(((k, "k"), (v, "v")), shape[0], shape[2], k.dtype)
+        _shape(v, shape, "v")
+        _one_device((k, "k"), (v, "v"))
+        _refuse_cache8(kc, vc, ks, vs, lens, block, cu, shape[1], shape[2])
+    T, Hkv, dh = shape
+    B, max_seq = lens.shape[0], cache[2]
+    if (T | Hkv | max_seq | block) >> 31:
+        _int32((T, "T"), (Hkv, "Hkv"), (max_seq, "max_seq"), (block, "block"))
+    sk, sv = k.stride(), v.stride()
+    rows, cached = (k.data_ptr(), v.data_ptr()), (kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr())
+    status = (lib.tfm_cache8_read if read else lib.tfm_cache8_write)(
+        *(cached + rows if read else rows + cached), None if cu is None else cu.data_ptr(), lens.data_ptr(), B, T, Hkv, dh,
+        max_seq, block, _Strides4(sk[0], sk[1], sv[0], sv[1]), TFM_CODE_INT8 if kc.dtype is torch.int8 else TFM_CODE_E4M3,
+        TFM_BF16 if k.dtype is torch.bfloat16 else _mode_of(k), _raw_stream(stream, here))
+    if status:
+        _check(status)
+
+
+def cache8_write(k, v, k_codes, v_codes, k_scales, v_scales, lens, block, cu_seqlens=None, stream=None):
+    """Quantises new keys and values k, v [T, Hkv, dh] (bf16 or fp32, dense rows of dh at any
+    token and head strides) into the 8-bit cache: codes [B, Hkv, max_seq, dh] (int8 or
+    float8_e4m3fn), scales [B, Hkv, ceil(max_seq / block)] (fp32).  Sequence b's n rows
+    [cu_seqlens[b], cu_seqlens[b + 1]) (int32, device; None: T / B each) become its
+    positions [lens[b] - n, lens[b]) (int32, device)."""
+    _cache8_rows(False, k, v, k_codes, v_codes, k_scales, v_scales, lens, block, cu_seqlens, stream)
+
+
+def cache8_read(k_codes, v_codes, k_scales, v_scales, k, v, lens, block, cu_seqlens=None, stream=None):
+    """The values of the last n positions of every sequence, [lens[b] - n, lens[b]), into
+    rows k, v [T, Hkv, dh]; arguments as for cache8_write."""
+    _cache8_rows(True, k, v, k_codes, v_codes, k_scales, v_scales, lens, block, cu_seqlens, stream)
+
+
+def cache8_attention_workspace_bytes(B, H, Hkv, max_new, dh):
+    _int32((B, "B"), (H, "H"), (Hkv, "Hkv"), (max_new, "max_new"), (dh, "dh"))
+    return load().tfm_cache8_attention_workspace_bytes(B, H, Hkv, max_new, dh)
+
+
+def _refuse_cache8_attention(q, kc, vc, ks, vs, o, lens, workspace, block, cu):
+    if q.dim() != 3:
+        raise ValueError("q: [T, H, dh] is required")
+    _refuse_rows(((q, "q"), (o, "o")), q.shape[0], q.shape[2], _torch().bfloat16)
+    _shape(o, q.shape, "o")
+    _refuse_cache8(kc, vc, ks, vs, lens, block, cu, None, q.shape[2])
+    _dev(workspace, "workspace")
+    _one_device((q, "q"), (o, "o"), (workspace, "workspace"))
+
+
+def cache8_attention(q, k_codes, v_codes, k_scales, v_scales, o, lens, workspace, block, cu_seqlens=None,
+                     max_new=None, window=0, scale=0.0, stream=None):
+    """Attention of new rows q [T, H, dh] (bf16, dense rows of dh at any token and head
+    strides) over the 8-bit cache that already holds them, into o [T, H, dh]: sequence b's n
+    rows are its positions [lens[b] - n, lens[b]), each sees the positions up to its own
+    (the last `window` of them; 0: all).  No sequence has more than max_new rows (None:
+    T / B, without offsets).  Cache, lens and cu_seqlens as for cache8_write."""
+    lib = _lib or load()
+    torch, here = _now()
+    shape, cache = q.shape, k_codes.shape
+    if not (len(shape) == 3 and here == q.get_device() == o.get_device() == workspace.get_device()
+            and torch.bfloat16 is q.dtype is o.dtype and shape == o.shape and 1 == q.stride(2) == o.stride(2)
+            and _cache8_ok(torch, here, k_codes, v_codes, k_scales, v_scales, lens, block, cu_seqlens)
+            and shape[2] == cache[3] and workspace.is_contiguous()):
+        _refuse_cache8_attention(q, k_codes, v_codes, k_scales, v_scales, o, lens, workspace, block, cu_seqlens)
+    T, H, dh = shape
+    _, Hkv, max_seq, _ = cache
+    B = lens.shape[0]
+    if max_new is None:
+        if cu_seqlens is not None:
+            raise ValueError("max_new: required with cu_seqlens")
+        max_new = max(T // max(B, 1), 1)
+    if (T | H | Hkv | max_seq | max_new | block | window) >> 31:
+        _int32((T, "T"), (H, "H"), (Hkv, "Hkv"), (max_seq, "max_seq"), (max_new, "max_new"), (block, "block"),
+               (window, "window"))
+    sq, so = q.stride(), o.stride()
+    status = lib.tfm_cache8_attention(q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
+                                      v_scales.data_ptr(), o.data_ptr(),
+                                      None if cu_seqlens is None else cu_seqlens.data_ptr(), lens.data_ptr(), B, T, H, Hkv,
+                                      max_new, dh, max_seq, block, _Strides4(sq[0], sq[1], so[0], so[1]),
+                                      TFM_CODE_INT8 if k_codes.dtype is torch.int8 else TFM_CODE_E4M3, window, scale,
+                                      workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, here))
     if status:
         _check(status)
 

@@ -361,7 +361,7 @@ const char* tfm_profile_kind_name(int32_t kind);
  * against the oracle and for callers that assemble their own model.
  * Empty calls (M = 0; B, H or S = 0 for RoPE; B or S = 0 for attention; T or
  * n_seq = 0 for packed attention; B = 0 for decode and prefix attention and for
- * verification) check their other arguments, then return TFM_OK
+ * verification; T = 0 for packed rows' RoPE, B or T = 0 for the 8-bit cache) check their other arguments, then return TFM_OK
  * without launching anything or reading any pointer, which may then be NULL. */
 
 /* Embedding lookup (CS336 walkthrough, section 5.2): h[m, :] = E[tokens[m], :]
@@ -535,6 +535,118 @@ tfm_status tfm_verify_draft(const float* target, int64_t ld_target, const float*
                             int32_t K, int32_t V, float temperature, int32_t* tokens,
                             int32_t* n_accepted, void* workspace, size_t workspace_bytes,
                             void* stream);
+
+/* ---- An 8-bit key/value cache for a batch whose sequences have different lengths
+ * ("LLM 2", section KV cache, where its size is what limits batch and context): rotary
+ * positions of packed rows, the rows quantised as they are written, read back, and
+ * attended to.  Codes [B, Hkv, max_seq, dh], a byte each; scales fp32
+ * [B, Hkv, ceil(max_seq / block)], one for each head and block of positions: a position's
+ * value is code * scale.  int8 codes are -127 .. 127; e4m3 codes (fp8 of 4 exponent and 3
+ * mantissa bits) up to 448 in magnitude, never NaN as they are written.  dh in {32, 64, 128},
+ * block in {16, 32, 64, 128}, B <= 4096, Hkv <= 4096, B * Hkv * max_seq below 2^31.
+ * New rows are packed as for tfm_packed_attention: sequence b has the rows
+ * [cu_seqlens[b], cu_seqlens[b + 1]) of T (int32 [B + 1], device; none is allowed), or,
+ * cu_seqlens NULL, T / B rows each (T a multiple of B).  lens[b] (int32 [B], device) counts
+ * the positions of the cache after its new rows have joined it, of which they are the last.
+ * So one tensor of lengths serves the write, the read and the attention of a step, and all
+ * read it when they run: a recorded graph serves every later batch of the same bounds. */
+typedef enum { TFM_CODE_INT8 = 0, TFM_CODE_E4M3 = 1 } tfm_code;
+
+/* Host only: the rotary frequencies inv_freq[0 .. rot/2) (radians per position, fp64) of
+ * theta^(-2i/rot) ("LLM 2", section RoPE), scaled for contexts longer than the model was
+ * trained on, and the factor *mscale for the rotated values:
+ *   TFM_ROPE_PLAIN       as they are;
+ *   TFM_ROPE_LINEAR      divided by factor (positions interpolated);
+ *   TFM_ROPE_NTK         of the base theta * factor^(rot / (rot - 2)): the slowest pair is
+ *                        divided by factor, the fastest stays;
+ *   TFM_ROPE_YARN        pairs below the one that turns `high` times over `original`
+ *                        positions stay, those beyond the one that turns `low` times are
+ *                        divided by factor, linear in the pair's number between
+ *                        (both bounds rounded outwards); mscale = 0.1 ln(factor) + 1;
+ *   TFM_ROPE_WAVELENGTH  the same, linear in the turns themselves between low and high;
+ *                        mscale 1.
+ * factor in [1, 1e6] (not read for PLAIN); original in [1, 1e9] and 0 < low < high <= 1e9
+ * (read for the last two). */
+typedef enum {
+    TFM_ROPE_PLAIN = 0, TFM_ROPE_LINEAR = 1, TFM_ROPE_NTK = 2, TFM_ROPE_YARN = 3, TFM_ROPE_WAVELENGTH = 4
+} tfm_rope_scaling;
+tfm_status tfm_rope_frequencies(double theta, int32_t rot, int32_t scaling, double factor, double original,
+                                double low, double high, double* inv_freq, float* mscale);
+
+/* Rotary positions of packed rows: q [T, H, dh], k [T, Hkv, dh] at any token and head
+ * strides (host, may be NULL: all dense; {q token, q head, k token, k head, then the same
+ * of q_out and k_out}, in elements, at least dh, below 2^39 bytes).  In row t, pair i of
+ * the first `rot` coordinates of every head, (x[2i], x[2i+1]) (interleaved != 0, the pairs
+ * of tfm_rope) or (x[i], x[i + rot/2]), turns by positions[t] * inv_freq[i] and is
+ * multiplied by mscale; the coordinates behind rot are copied.  positions int32 [T],
+ * inv_freq fp64 [rot/2] (device; finite).  The angle is reduced exactly for every int32
+ * position, up to the 53 bits of inv_freq; the rest is fp32, rounded once.  bf16 or fp32 rows by
+ * mode.  q_out and k_out may be q and k themselves (same strides) and must not overlap them
+ * otherwise, nor their own rows each other.  Hkv may be 0 (k and k_out are then not used).
+ * T <= 2^30, H and Hkv <= 4096, 2 <= dh <= 256, rot even in [2, dh].  Rows aligned to their
+ * element size; 16-byte aligned rows and rot a multiple of 32 bytes run at full speed.
+ * T = 0 returns at once.  Capturable in a CUDA graph. */
+tfm_status tfm_rope_rows(const void* q, const void* k, void* q_out, void* k_out, const int32_t* positions,
+                         const double* inv_freq, int32_t T, int32_t H, int32_t Hkv, int32_t dh, int32_t rot,
+                         int32_t interleaved, const int64_t* strides, float mscale, int32_t mode, void* stream);
+
+/* Writes new keys and values into the cache: k, v [T, Hkv, dh] (bf16 or fp32 by mode) at
+ * strides {k token, k head, v token, v head} (host, may be NULL: dense; elements, at least
+ * dh, multiples of 16 bytes, below 2^39 bytes), sequence b's rows to positions
+ * [lens[b] - n, lens[b]).  For each head and block that gets rows, with m their largest
+ * magnitude and need = m / 127 (int8) or m / 448 (e4m3), at least 2^-126 (fp32; 0 if all
+ * are 0): the block's scale becomes need if no earlier position of the sequence lies in it
+ * (or its scale is 0); else it stays if it is at least need, or is multiplied by the
+ * smallest power of two that makes it so, and the codes of the earlier positions are
+ * divided by that power and rounded.  A new code is x / scale, rounded to the nearest, ties
+ * to even, as decided without rounding the quotient.  So a sequence may be cut back (drafted tokens refused): the
+ * next rows overwrite what was there.  What lies behind lens[b] in its last block keeps its
+ * codes and is not looked at.  NaN is stored as 0 and an infinity as the largest code (their block's
+ * scale is that of its finite values), and either sets TFM_EINVAL in the device error word.
+ * So do offsets that decrease or leave [0, T], lens[b] outside [0, max_seq] and more rows than
+ * lens[b]: nothing is then written for that sequence (offsets of others that are not in
+ * order included), and nothing outside the buffers is touched.
+ * Rows 16-byte aligned, codes 16-byte, scales and lengths 4-byte.  B = 0 or T = 0 returns at once.
+ * Calls that write the same cache must be ordered.  Capturable in a CUDA graph. */
+tfm_status tfm_cache8_write(const void* k, const void* v, void* k_codes, void* v_codes, float* k_scales,
+                            float* v_scales, const int32_t* cu_seqlens, const int32_t* lens, int32_t B,
+                            int32_t T, int32_t Hkv, int32_t dh, int32_t max_seq, int32_t block,
+                            const int64_t* strides, int32_t codes, int32_t mode, void* stream);
+
+/* Reads the cache back: row r of sequence b's n rows gets the values code * scale (fp32,
+ * rounded to the mode's type) of position lens[b] - n + r; with n = lens[b] that is all of
+ * it.  Layouts, limits and errors as for tfm_cache8_write; the cache is not changed, and
+ * rows of no sequence are not written. */
+tfm_status tfm_cache8_read(const void* k_codes, const void* v_codes, const float* k_scales, const float* v_scales,
+                           void* k, void* v, const int32_t* cu_seqlens, const int32_t* lens, int32_t B, int32_t T,
+                           int32_t Hkv, int32_t dh, int32_t max_seq, int32_t block, const int64_t* strides,
+                           int32_t codes, int32_t mode, void* stream);
+
+/* Attention of new rows over the cache they have joined: q, o [T, H, dh] bf16 at strides
+ * {q token, q head, o token, o head} (as above; o's rows must not overlap each other or q),
+ * query head h reading kv head h / (H / Hkv).  Row t of sequence b's n is at position
+ * p = lens[b] - n + t and sees the positions j <= p, with window > 0 those with j > p - window;
+ * o = softmax(scale * q . k_j) v_j over them, scale <= 0 meaning 1/sqrt(dh).  A row that
+ * sees no position (lens[b] < n) gets zeros; rows of no sequence are not written.  What
+ * lies in the cache behind lens[b] or before the window is not looked at; codes
+ * and scales that are seen must be finite (those tfm_cache8_write stores are).  Scores, maxima and sums are fp32;
+ * a row of q is held in fp16 after division by a power of two (exact but for elements below
+ * 2^-14 of the row's largest, which are rounded to 2^-24 of it), the weights are rounded to
+ * fp16 for their product with the codes (2^-11 relative), the output once to bf16.
+ * No sequence has more than max_new rows, (H / Hkv) * max_new <= 128, B * H * max_new <= 2^24.
+ * scale must be finite and at most 2^126.
+ * workspace: device, 16-byte aligned, tfm_cache8_attention_workspace_bytes(B, H, Hkv,
+ * max_new, dh) bytes (0 for bad sizes), not used by another call in flight; its contents
+ * need not survive.  Offsets that decrease or leave [0, T] or give a sequence more than max_new rows
+ * set TFM_EINVAL in the device error word and leave that sequence's rows unwritten; a length outside
+ * [0, max_seq] sets it and counts as 0.  Results do not depend on timing.  Capturable in a CUDA graph. */
+size_t tfm_cache8_attention_workspace_bytes(int32_t B, int32_t H, int32_t Hkv, int32_t max_new, int32_t dh);
+tfm_status tfm_cache8_attention(const void* q, const void* k_codes, const void* v_codes, const float* k_scales,
+                                const float* v_scales, void* o, const int32_t* cu_seqlens, const int32_t* lens,
+                                int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t max_new, int32_t dh,
+                                int32_t max_seq, int32_t block, const int64_t* strides, int32_t codes,
+                                int32_t window, float scale, void* workspace, size_t workspace_bytes,
+                                void* stream);
 
 /* Bias-free Linear (CS336 walkthrough, section 5.3): y = x W^T.
  * x [M, K], W [N, K] (bf16 or fp32 by mode); y [M, ldy] fp32 when
