@@ -246,6 +246,8 @@ bool rows_heads_map(CUtensorMap* map, const void* ptr, int64_t T, int64_t heads,
 // Tensor map of dense queries [B, Hkv, GT, dh]: boxes of nb sequences' GT rows of
 // one kv head.
 bool query_groups_map(CUtensorMap* map, const void* ptr, int B, int Hkv, int GT, int dh, int nb);
+// Tensor map of dense rows of dh single bytes, boxes of box_rows rows.
+bool byte_rows_map(CUtensorMap* map, const void* ptr, int64_t rows, int dh, int box_rows);
 tfm_status plan_attention_tc(AttnPlan* p, const void* q, const void* k, const void* v, void* o,
                              int B, int H, int Hkv, int S, int dh, float scale);
 cudaError_t launch_attention_tc(const AttnPlan& p, cudaStream_t st);

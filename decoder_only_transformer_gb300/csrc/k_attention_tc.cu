@@ -626,6 +626,23 @@ bool query_groups_map(CUtensorMap* map, const void* ptr, int B, int Hkv, int GT,
     });
 }
 
+// [rows, dh] single bytes, dense, as boxes of box_rows rows, zero fill past the last one;
+// swizzled over the row's length (rows of 32 bytes as they are).
+bool byte_rows_map(CUtensorMap* map, const void* ptr, int64_t rows, int dh, int box_rows) {
+    EncodeTiledFn fn = att_encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)dh, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)dh};
+    cuuint32_t box[2] = {(cuuint32_t)dh, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return encode_with_context([&] {
+        return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  dh == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : dh == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
+}
+
 bool attention_tc_supported(int dh) { return dh == 32 || dh == 64 || dh == 128; }
 
 tfm_status plan_attention_tc(AttnPlan* p, const void* q, const void* k, const void* v, void* o,
