@@ -12,13 +12,15 @@
 //     registers, where the codes have just been converted; tcgen05 reads them from shared
 //     memory, so every converted code (two bytes) would be written there and read again, for
 //     tiles of 128 rows of which a decode step fills 1 to 16.  int8 codes and e4m3 codes are
-//     fp16 numbers, so the products are exact; so is a row of q after division by a power of two (but
-//     for elements below 2^-14 of its largest).
+//     fp16 numbers, so the products are exact; so is a row of q times a power of two (but
+//     for elements below 2^-24 of its largest).
 //   - the scales are not multiplied into the codes: s_k is one factor of the 16 scores of a
 //     warp's step, which lies in one block; s_v multiplies the step's 16-key sum of P V as it
 //     is added to the fp32 output.
-//   - a code costs 1.25 to 1.5 instructions: for int8, bytes to the low halves of fp16 numbers
-//     1024 + (c + 128) by masks, less 1152; for e4m3 the conversion of two at a time.
+//   - a code costs 0.75 to 1 instruction: an int8 byte with its sign bit turned over is the fp16
+//     subnormal (c + 128) 2^-24, and 128 times the sum of q, or of the weights, is taken off the
+//     fp32 sums (it is of their size or below: at most 2^-16 of a step of the code is lost); e4m3 codes
+//     are converted two at a time.
 //   - the order of the coordinates inside a product of 16, and of the keys inside a step, is
 //     free.  They are taken as 16-byte loads from shared memory bring them (see kappa below):
 //     no transposition, no bank conflicts.
@@ -40,18 +42,20 @@ namespace {
 constexpr int kTileKeys = 64;
 constexpr int kMaxRuns = 152 * 3 * 2;             // CTAs at most, and places for them in the workspace
 
-template <int DH, bool HALF, int RG>
+template <int DH, int NT, int RG>
 struct Ax {
     static constexpr int kTile = kTileKeys * DH;                       // bytes of K or V
-    static constexpr int kStages = (HALF ? 3 : 4) * (128 / DH);
-    static constexpr int kCtas = HALF ? 3 : RG == 1 ? 2 : 1;           // per SM
-    static constexpr int kRows = HALF ? 8 : 16;                        // of a warp
+    static constexpr int kStages = (NT == 1 ? 3 : 4) * (128 / DH);
+    static constexpr int kCtas = NT == 1 ? 3 : RG == 1 ? 2 : 1;           // per SM
+    static constexpr int kRows = 8 * NT;                               // of a warp
     static constexpr int kThreads = 128 * RG + 32;
     static constexpr int kBuf = 4 * RG * kRows * DH * 4;               // the warps' o, to be added up
     static constexpr int kBufOff = kStages * 2 * kTile;
     static constexpr int kMlOff = kBufOff + kBuf;                      // float2 [RG][4][rows]
-    static constexpr int kBarOff = kMlOff + RG * 4 * kRows * 8;
-    static constexpr int kCumOff = kBarOff + 16 * kStages + 16;
+    static constexpr int kQ = RG * kRows * DH * 2;                     // the job's rows of q, as they are
+    static constexpr int kQOff = kMlOff + RG * 4 * kRows * 8;          // two places
+    static constexpr int kBarOff = kQOff + 2 * kQ;                     // full, empty of the ring; of the places for q; of the buffers
+    static constexpr int kCumOff = kBarOff + 16 * kStages + 32 + 16 * RG;
     static constexpr int kBase = kCumOff + 1024;                       // + 4 (B + 1); the ring on a multiple of 1024
     static constexpr uint32_t kSwzMask = DH == 128 ? 7 : DH == 64 ? 3 : 0;
     static constexpr int kSwzShift = DH == 128 ? 0 : 1;
@@ -98,6 +102,10 @@ __device__ __forceinline__ int run_start(int i, int total, int runs) {
     const int q = total / runs, r = total - q * runs;
     return i * q + min(i, r);
 }
+__device__ __forceinline__ int run_of(int u, int total, int runs) {      // the run that tile u is in
+    const int q = total / runs, r = total - q * runs;
+    return u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q;
+}
 // Runs of at least kLeast tiles.
 constexpr int kLeast = 2;
 __device__ __forceinline__ int run_count(int total, int ctas) { return max(1, min(ctas, total / kLeast)); }
@@ -106,35 +114,16 @@ __device__ __forceinline__ int run_count(int total, int ctas) { return max(1, mi
 // j % blocks), tile t of the job.
 struct Walk {
     int b, j, t, left;
-    Seq s;
 };
-// Tiles [t0, t1) of job j of sequence b.
+// A segment: tiles of one job, as the warps that load tell those that compute.
 struct Seg {
-    int b, j, t0, t1;
-    Seq s;
+    int tiles;                // none: the run is over
+    int key;                  // first key
+    int len, n, row0;
+    int bh, kvh, rb;          // sequence and kv head, kv head, row block
+    int nrows;
+    int piece;                // -1: the whole job; else where its part goes
 };
-__device__ __forceinline__ bool next_seg(Walk& w, Seg& g, const Geom& gm, const int* cum,
-                                         const int32_t* __restrict__ cu, const int32_t* __restrict__ lens) {
-    if (w.left <= 0) return false;
-    bool bad;
-    if (w.t >= w.s.tiles) {                                // the next job
-        w.t = 0;
-        if (++w.j >= w.s.blocks * gm.Hkv) {
-            w.j = 0;
-            do ++w.b;
-            while (cum[w.b + 1] == cum[w.b]);              // a run ends before the jobs do
-            w.s = get_seq(cu, lens, gm, w.b, bad);
-        }
-    }
-    g.b = w.b;
-    g.j = w.j;
-    g.s = w.s;
-    g.t0 = w.t;
-    g.t1 = min(w.s.tiles, w.t + w.left);
-    w.left -= g.t1 - g.t0;
-    w.t = g.t1;
-    return true;
-}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -142,21 +131,36 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1, float c0, float c1, float c2, float c3) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1,
+                                         float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+// An 8 x 8 block of fp16: lane (g, t) gives row g, columns 2 t and 2 t + 1, and gets rows 2 t
+// and 2 t + 1 of column g.
+__device__ __forceinline__ uint32_t transposed(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
 }
 
-__device__ __forceinline__ uint32_t half2_sub(uint32_t a) {          // less 1152 in both halves, exact
-    const __half2 v = __hsub2(*reinterpret_cast<__half2*>(&a), __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
-    return *reinterpret_cast<const uint32_t*>(&v);
+__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t mask, uint32_t x) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(a), "r"(mask), "r"(x));
+    return r;
 }
+// int8 codes in bytes 0 and 2 of a word as a pair of fp16 numbers (c + 128) 2^-24, which are
+// subnormals: the byte itself, the sign bit turned over.
+__device__ __forceinline__ uint32_t biased(uint32_t w) { return and_xor(w, 0x00FF00FFu, 0x00800080u); }
 __device__ __forceinline__ uint32_t e4m3x2(uint32_t w) {             // the low two bytes as fp16
     uint32_t r;
-    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(w));
+    asm("{\n\t.reg .b16 t, u;\n\tmov.b32 {t, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_hi(uint32_t w) {          // the high two
+    uint32_t r;
+    asm("{\n\t.reg .b16 t, u;\n\tmov.b32 {t, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, u;\n\t}" : "=r"(r) : "r"(w));
     return r;
 }
 
@@ -166,10 +170,10 @@ template <bool E4M3>
 __device__ __forceinline__ void key_halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
     if constexpr (E4M3) {
         lo = e4m3x2(w);
-        hi = e4m3x2(w >> 16);
+        hi = e4m3x2_hi(w);
     } else {
-        lo = half2_sub((w & 0x00FF00FFu) ^ 0x64806480u);
-        hi = half2_sub(((w >> 8) & 0x00FF00FFu) ^ 0x64806480u);
+        lo = biased(w);
+        hi = biased(w >> 8);
     }
 }
 // Four codes of two keys, a and b: pair i is (a's code i, b's code i).
@@ -178,15 +182,15 @@ __device__ __forceinline__ void value_halves(uint32_t a, uint32_t b, uint32_t (&
     if constexpr (E4M3) {
         const uint32_t x = __byte_perm(a, b, 0x5140), y = __byte_perm(a, b, 0x7362);
         v[0] = e4m3x2(x);
-        v[1] = e4m3x2(x >> 16);
+        v[1] = e4m3x2_hi(x);
         v[2] = e4m3x2(y);
-        v[3] = e4m3x2(y >> 16);
+        v[3] = e4m3x2_hi(y);
     } else {
         const uint32_t x = __byte_perm(a, b, 0x5410), y = __byte_perm(a, b, 0x7632);
-        v[0] = half2_sub((x & 0x00FF00FFu) ^ 0x64806480u);
-        v[1] = half2_sub(((x >> 8) & 0x00FF00FFu) ^ 0x64806480u);
-        v[2] = half2_sub((y & 0x00FF00FFu) ^ 0x64806480u);
-        v[3] = half2_sub(((y >> 8) & 0x00FF00FFu) ^ 0x64806480u);
+        v[0] = biased(x);
+        v[1] = biased(x >> 8);
+        v[2] = biased(y);
+        v[3] = biased(y >> 8);
     }
 }
 
@@ -200,71 +204,83 @@ __device__ __forceinline__ int kappa(int c) {
     else return (0x67453210u >> (4 * c)) & 7;                          // 0 1 2 3 5 4 7 6
 }
 
-__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[4]) {
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
-}
-__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[2]) {
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
-}
-__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[1]) {
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
-}
-
-template <int DH, bool HALF, int RG>
-__device__ __forceinline__ int buf_at(int row, int f) {      // place of float4 f of a row, spread over the banks
-    constexpr int VPT = DH / 16;                             // float4s of a lane
-    const int t = f / VPT;
-    if constexpr (DH == 128) return row * 32 + (f ^ (2 * t + (row & 1)));
-    else if constexpr (DH == 64) return row * 16 + (f ^ ((t >> 1) | (row & 1) << 1));
-    else return row * 8 + (f ^ (row & 1));
+// W words of a tile.
+template <int W>
+__device__ __forceinline__ void words(const uint8_t* at, uint32_t (&w)[W]) {
+    if constexpr (W == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(at);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (W == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(at);
+        w[0] = v.x, w[1] = v.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(at);
+    }
 }
 
-template <bool E4M3, int DH, bool HALF, int RG>
-__global__ void __launch_bounds__(Ax<DH, HALF, RG>::kThreads, Ax<DH, HALF, RG>::kCtas)
+// Place of float4 f of a row in the buffer where warps add up, spread over the banks.
+template <int DH>
+__device__ __forceinline__ int buf_at(int row, int f) {
+    const int t = (row >> 1) & 3;
+    return row * (DH / 4) + (f ^ (DH == 128 ? t : DH == 64 ? (t & 1) | (t >> 1) << 2 : t << 1));
+}
+
+template <bool E4M3, int DH, int NT, int RG>
+__global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCtas)
     k_cache8_part(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const __nv_bfloat16* __restrict__ q, const float* __restrict__ ks, const float* __restrict__ vs,
                   __nv_bfloat16* __restrict__ o, const int32_t* __restrict__ cu, const int32_t* __restrict__ lens,
                   PieceHead* __restrict__ heads, float2* __restrict__ part_ml, float4* __restrict__ part_o, const Geom gm,
                   int* err) {
-    using X = Ax<DH, HALF, RG>;
+    using X = Ax<DH, NT, RG>;
     constexpr int KW = DH >= 64 ? 4 : 2;                     // words of a load of K
     constexpr int KL = DH == 128 ? 2 : 1;                    // loads of K per key
-    constexpr int VW = DH / 32;                              // words of a load of V
-    constexpr int VPT = DH / 16;                             // float4s of o that a lane holds per row
+    constexpr int VW = DH / 32;                              // words of a load of V, float4s of o of a lane and row
     constexpr int R = X::kRows;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int abort_flag, place;
+    __shared__ int abort_flag;
+    __shared__ Seg segs[2];
     const uint32_t raw_base = smem_u32(smem_raw);
     const uint32_t sbase = (raw_base + 1023u) & ~1023u;
     uint8_t* sm = smem_raw + (sbase - raw_base);
     const uint32_t full = sbase + X::kBarOff, empty = full + 8 * X::kStages;
-    int* cum = reinterpret_cast<int*>(sm + X::kCumOff);
+    const uint32_t qfull = empty + 8 * X::kStages, qempty = qfull + 16, bfull = qempty + 16, bempty = bfull + 8 * RG;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) {
+    if (tid == 128 * RG) {
         abort_flag = 0;
         for (int i = 0; i < X::kStages; ++i) {
             mbar_init(full + 8 * i, 1);
             mbar_init(empty + 8 * i, 4 * RG);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(qfull + 8 * i, 1);
+            mbar_init(qempty + 8 * i, 4 * RG);
+        }
+        for (int i = 0; i < 2 * RG; ++i) mbar_init(bfull + 8 * i, 4);
         fence_mbar_init();
         tma_prefetch_desc(&kmap);
         tma_prefetch_desc(&vmap);
     }
+    __syncthreads();
+    int st = 0;                                              // stage of the ring, and its phase
+    uint32_t phase = 0;
+    int sn = 0;                                              // segments so far
     pdl_wait();
     pdl_trigger();
-    // tiles of the sequences, added up
-    for (int b = tid; b < gm.B; b += X::kThreads) {
-        bool bad;
-        const Seq s = get_seq(cu, lens, gm, b, bad);
-        if (bad && blockIdx.x == 0) raise_error(err, TFM_EINVAL);
-        cum[b + 1] = s.tiles * s.blocks * gm.Hkv;
-    }
-    if (tid == 0) cum[0] = 0;
-    __syncthreads();
-    if (warp == 0) {
+    if (warp == 4 * RG) {
+        // ---------------------------------------------------------------- loads
+        // Tiles of the sequences, added up (by this warp alone; the others wait for its first segment).
+        int* cum = reinterpret_cast<int*>(sm + X::kCumOff);
         int carry = 0;
+        if (lane == 0) cum[0] = 0;
         for (int b0 = 0; b0 < gm.B; b0 += 32) {
-            int x = b0 + lane < gm.B ? cum[b0 + lane + 1] : 0;
+            int x = 0;
+            if (b0 + lane < gm.B) {
+                bool bad;
+                const Seq s = get_seq(cu, lens, gm, b0 + lane, bad);
+                if (bad && blockIdx.x == 0) raise_error(err, TFM_EINVAL);
+                x = s.tiles * s.blocks * gm.Hkv;
+            }
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, x, d);
@@ -274,97 +290,117 @@ __global__ void __launch_bounds__(Ax<DH, HALF, RG>::kThreads, Ax<DH, HALF, RG>::
             if (b0 + lane < gm.B) cum[b0 + lane + 1] = x;
             carry = __shfl_sync(0xffffffffu, x, 31);
         }
-    }
-    __syncthreads();
-    const int total = cum[gm.B];
-    const int runs = run_count(total, gridDim.x);
-    if ((int)blockIdx.x >= runs || total == 0) {
-        if (tid == 0) heads[blockIdx.x] = PieceHead{0, 0, -1, total};
-        return;
-    }
-    const int u0 = run_start(blockIdx.x, total, runs), u1 = run_start(blockIdx.x + 1, total, runs);
-    for (int b = tid; b < gm.B; b += X::kThreads)
-        if (cum[b] <= u0 && u0 < cum[b + 1]) place = b;
-    __syncthreads();
-    Walk w;
-    {
-        bool bad;
-        w.b = place;
-        w.s = get_seq(cu, lens, gm, w.b, bad);
-        w.j = (u0 - cum[w.b]) / w.s.tiles;
-        w.t = (u0 - cum[w.b]) % w.s.tiles;
-        w.left = u1 - u0;
-        if (tid == 0) {
-            const int start = u0 - w.t;
-            heads[blockIdx.x] = PieceHead{start, start + w.s.tiles,
-                                          (w.b * gm.Hkv + w.j / w.s.blocks) * gm.row_blocks + w.j % w.s.blocks, total};
-        }
-    }
-    Seg seg;
-    int st = 0;                                              // stage of the ring, and its phase
-    uint32_t phase = 0;
-    if (warp == 4 * RG) {
-        // ---------------------------------------------------------------- loads
-        if (lane != 0) return;
-        bool filled = false;                                 // every stage once
-        while (next_seg(w, seg, gm, cum, cu, lens)) {
-            const int row = (seg.b * gm.Hkv + seg.j / seg.s.blocks) * gm.max_seq + seg.s.tile0 * kTileKeys;
-            for (int t = seg.t0; t < seg.t1; ++t) {
-                if (filled && !mbar_wait(empty + 8 * st, phase ^ 1, err, &abort_flag)) return;
-                mbar_arrive_expect_tx(full + 8 * st, 2 * X::kTile);
-                tma_load_2d(sbase + st * 2 * X::kTile, &kmap, 0, row + t * kTileKeys, full + 8 * st);
-                tma_load_2d(sbase + st * 2 * X::kTile + X::kTile, &vmap, 0, row + t * kTileKeys, full + 8 * st);
-                if (++st == X::kStages) st = 0, phase ^= 1, filled = true;
+        __syncwarp();
+        const int total = carry;
+        const int runs = run_count(total, gridDim.x);
+        Walk w{0, 0, 0, 0};
+        if ((int)blockIdx.x < runs && total > 0) {
+            const int u0 = run_start(blockIdx.x, total, runs);
+            w.left = run_start(blockIdx.x + 1, total, runs) - u0;
+            int lo = 0, hi = gm.B;                           // cum[lo] <= u0 < cum[hi]
+            while (hi - lo > 1) {
+                const int step = (hi - lo + 31) / 32;
+                const int b = lo + lane * step;
+                const int last = 31 - __clz(__ballot_sync(0xffffffffu, b < hi && cum[b] <= u0) | 1u);
+                lo += last * step;
+                hi = min(hi, lo + step);
             }
+            w.b = lo;
+            bool bad;
+            const Seq s = get_seq(cu, lens, gm, lo, bad);
+            w.j = (u0 - cum[lo]) / s.tiles;
+            w.t = (u0 - cum[lo]) % s.tiles;
+            if (lane == 0)
+                heads[blockIdx.x] = PieceHead{u0 - w.t, u0 - w.t + s.tiles,
+                                              (lo * gm.Hkv + w.j / s.blocks) * gm.row_blocks + w.j % s.blocks, total};
+        } else if (lane == 0) {
+            heads[blockIdx.x] = PieceHead{0, 0, -1, total};
         }
-        return;
+        bool filled = false;                                 // every stage of the ring once
+        for (;; ++sn) {
+            const int place = sn & 1;
+            if (sn >= 2 && !warp_wait(qempty + 8 * place, (sn >> 1) + 1 & 1, err, &abort_flag)) return;
+            if (w.left <= 0) {
+                if (lane == 0) {
+                    segs[place].tiles = 0;
+                    mbar_arrive(qfull + 8 * place);
+                }
+                return;
+            }
+            while (cum[w.b + 1] == cum[w.b]) ++w.b;          // a run ends before the jobs do
+            bool bad;
+            const Seq s = get_seq(cu, lens, gm, w.b, bad);
+            const int kvh = w.j / s.blocks, rb = w.j % s.blocks;
+            const int tiles = min(s.tiles - w.t, w.left);
+            const int nrows = min(s.n * gm.G - rb * gm.block_rows, gm.block_rows);
+            int row = (w.b * gm.Hkv + kvh) * gm.max_seq + (s.tile0 + w.t) * kTileKeys;
+            if (lane == 0) {
+                segs[place] = Seg{tiles, (s.tile0 + w.t) * kTileKeys, s.len, s.n, s.row0, w.b * gm.Hkv + kvh, kvh, rb, nrows,
+                                  tiles == s.tiles ? -1 : (int)blockIdx.x * 2 + (sn > 0)};
+                mbar_arrive_expect_tx(qfull + 8 * place, nrows * DH * 2);
+            }
+            __syncwarp();
+            if (lane < nrows) {
+                const int rr = rb * gm.block_rows + lane;
+                bulk_load(sbase + X::kQOff + place * X::kQ + lane * DH * 2,
+                          q + ((int64_t)s.row0 + rr / gm.G) * gm.sq_t + (int64_t)(kvh * gm.G + rr % gm.G) * gm.sq_h, DH * 2,
+                          qfull + 8 * place);
+            }
+            bool ok = true;
+            if (lane == 0)
+                for (int i = 0; i < tiles; ++i, row += kTileKeys) {
+                    if (filled && !mbar_wait(empty + 8 * st, phase ^ 1, err, &abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(full + 8 * st, 2 * X::kTile);
+                    tma_load_2d(sbase + st * 2 * X::kTile, &kmap, 0, row, full + 8 * st);
+                    tma_load_2d(sbase + st * 2 * X::kTile + X::kTile, &vmap, 0, row, full + 8 * st);
+                    if (++st == X::kStages) st = 0, phase ^= 1, filled = true;
+                }
+            if (!__shfl_sync(0xffffffffu, (int)ok, 0)) return;
+            w.left -= tiles;
+            w.t = 0;                                         // whatever comes next is another job
+            if (++w.j == s.blocks * gm.Hkv) w.j = 0, ++w.b;
+        }
     }
     // -------------------------------------------------------------------- rows
     const int kw = warp & 3, rg = warp >> 2, g = lane >> 2, t = lane & 3;
-    // where this lane reads, inside a tile
-    uint32_t koff[2][KL], voff[4];
+    // where this lane reads, inside a tile: keys of the step's second half are 8 rows further, the
+    // second half of a K row of 128 bytes is 64 bytes away (both keep the swizzle)
+    const int kr = kw * 16 + kappa<DH>(g);
+    const uint32_t koff = kr * DH + (DH >= 64 ? (t ^ ((kr >> X::kSwzShift) & X::kSwzMask)) * 16 : t * 8);
+    uint32_t voff[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int r = kw * 16 + i * 8 + kappa<DH>(g);
-#pragma unroll
-        for (int p = 0; p < KL; ++p)
-            koff[i][p] = r * DH + (DH >= 64 ? ((t + 4 * p) ^ ((r >> X::kSwzShift) & X::kSwzMask)) * 16 : t * 8);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = kw * 16 + (i >> 1) * 8 + kappa<DH>(2 * t + (i & 1));
-        voff[i] = r * DH + (DH == 128 ? (g ^ (r & 7)) * 16 : DH == 64 ? ((g >> 1) ^ ((r >> 1) & 3)) * 16 + (g & 1) * 8 : g * 4);
+        const int r = kw * 16 + kappa<DH>(2 * t + i);
+        voff[i] = X::kTile + r * DH + (DH == 128 ? (g ^ (r & 7)) * 16 : DH == 64 ? ((g >> 1) ^ ((r >> 1) & 3)) * 16 + (g & 1) * 8 : g * 4);
     }
     float4* buf = reinterpret_cast<float4*>(sm + X::kBufOff) + rg * 4 * R * (DH / 4);
     float2* ml = reinterpret_cast<float2*>(sm + X::kMlOff) + rg * 4 * R;
-    bool dead = false;
-    bool first_seg = true;
-    while (next_seg(w, seg, gm, cum, cu, lens)) {
-        const Seq& s = seg.s;
-        const int kvh = seg.j / s.blocks, rb = seg.j % s.blocks;
-        const int64_t bh = (int64_t)seg.b * gm.Hkv + kvh;
-        const int nrows = min(s.n * gm.G - rb * gm.block_rows, gm.block_rows) - rg * R;     // of this row group
-        // q: row r of the group is token r / G, head r % G
-        uint32_t qa[HALF ? 1 : 2][KL * KW][2];
-        float qinv[2];
-        int seen_hi[2], seen_lo[2];                          // a row sees the positions [lo, hi]
+    for (;; ++sn) {
+        if (!warp_wait(qfull + 8 * (sn & 1), sn >> 1 & 1, err, &abort_flag)) return;
+        const Seg& s = segs[sn & 1];
+        const int tiles = s.tiles, len = s.len, news = s.n, rb = s.rb;
+        if (tiles == 0) return;
+        const int nrows = s.nrows - rg * R;                  // of this row group
+        // q: row r of the job is token r / G, head r % G.  Lane (g, t) holds row 8 n + g, for the products, of
+        // what belongs to the rows 8 n + 2 t and + 1, whose scores it gets, in the arrays [n][2].
+        uint32_t qb[NT][KL * KW][2];
+        float qinv[NT][2], qbias[NT][2];
+        int seen_hi[NT][2], seen_lo[NT][2];                  // a row sees the positions [lo, hi]
 #pragma unroll
-        for (int i = 0; i < (HALF ? 1 : 2); ++i) {
-            const int r = g + 8 * i;
-            const int rr = rb * gm.block_rows + rg * R + r;
-            const int tok = rr / gm.G;
-            seen_hi[i] = r < nrows ? s.len - s.n + tok : s.len - 1;
-            seen_lo[i] = gm.window > 0 ? seen_hi[i] - gm.window + 1 : 0;
+        for (int n = 0; n < NT; ++n) {
+            const int r = 8 * n + g;
             uint2 raw[KL * KW];
-            float top = 0.0f;
             if (r < nrows) {
-                const __nv_bfloat16* at = q + ((int64_t)s.row0 + tok) * gm.sq_t + (int64_t)(kvh * gm.G + rr % gm.G) * gm.sq_h;
+                const uint8_t* at = sm + X::kQOff + (sn & 1) * X::kQ + (rg * R + r) * DH * 2;
 #pragma unroll
                 for (int p = 0; p < KL; ++p) {
-                    const uint4* a4 = reinterpret_cast<const uint4*>(at + p * 64 + t * (DH >= 64 ? 16 : 8));
+                    const uint4* a4 = reinterpret_cast<const uint4*>(at + p * 128 + t * (DH >= 64 ? 32 : 16));
 #pragma unroll
                     for (int x = 0; x < KW / 2; ++x) {
-                        const uint4 y = __ldg(a4 + x);
+                        const uint4 y = a4[x];
                         raw[p * KW + 2 * x] = make_uint2(y.x, y.y);
                         raw[p * KW + 2 * x + 1] = make_uint2(y.z, y.w);
                     }
@@ -373,133 +409,183 @@ __global__ void __launch_bounds__(Ax<DH, HALF, RG>::kThreads, Ax<DH, HALF, RG>::
 #pragma unroll
                 for (int x = 0; x < KL * KW; ++x) raw[x] = make_uint2(0, 0);
             }
+            float top = 0.0f;
 #pragma unroll
             for (int x = 0; x < KL * KW; ++x)
                 top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(raw[x].x)), fabsf(bf16_hi(raw[x].x))),
                                        fmaxf(fabsf(bf16_lo(raw[x].y)), fabsf(bf16_hi(raw[x].y)))));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // the row divided by the power of two of its largest element
+            // the row times the power of two that brings its largest element to [2^10, 2^11)
             int e = (int)(__float_as_uint(top) >> 23);
-            e = e == 0 || e == 255 ? 127 : min(e, 253);
-            const float mul = __uint_as_float((uint32_t)(254 - e) << 23);
-            qinv[i] = __uint_as_float((uint32_t)e << 23);
+            e = e == 255 ? 127 : max(e, 10);
+            const float mul = __uint_as_float((uint32_t)(264 - e) << 23);
+            float sum = 0.0f;
 #pragma unroll
             for (int x = 0; x < KL * KW; ++x) {
                 const float y0 = bf16_lo(raw[x].x) * mul, y1 = bf16_hi(raw[x].x) * mul;
                 const float y2 = bf16_lo(raw[x].y) * mul, y3 = bf16_hi(raw[x].y) * mul;
                 const __half2 a = E4M3 ? __floats2half2_rn(y0, y1) : __floats2half2_rn(y0, y2);
                 const __half2 b = E4M3 ? __floats2half2_rn(y2, y3) : __floats2half2_rn(y1, y3);
-                qa[i][x][0] = *reinterpret_cast<const uint32_t*>(&a);
-                qa[i][x][1] = *reinterpret_cast<const uint32_t*>(&b);
+                qb[n][x][0] = *reinterpret_cast<const uint32_t*>(&a);
+                qb[n][x][1] = *reinterpret_cast<const uint32_t*>(&b);
+                const float2 fa = __half22float2(a), fb = __half22float2(b);
+                sum += (fa.x + fa.y) + (fb.x + fb.y);
+            }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int from = (2 * t + j) * 4;            // a lane of that row
+                qinv[n][j] = __uint_as_float((uint32_t)__shfl_sync(0xffffffffu, e, from) << 23);
+                qbias[n][j] = __shfl_sync(0xffffffffu, sum, from) * -0x1p-17f;       // 128 of the codes' 2^-24
+                const int ro = 8 * n + 2 * t + j;
+                seen_hi[n][j] = ro < nrows ? len - news + (rb * gm.block_rows + rg * R + ro) / gm.G : len - 1;
+                seen_lo[n][j] = gm.window > 0 ? seen_hi[n][j] - gm.window + 1 : 0;
             }
         }
-        float acc[VW * 4][HALF ? 2 : 4];
+        // acc[n][2 x + h]: rows 8 n + 2 t (elements 0, 2) and + 1 (1, 3), coordinates g DH / 8 + 4 x + 2 h (0, 1) and + 1
+        float acc[NT][2 * VW][4];
+        float m[NT][2], l[NT][2], lv[NT][2];                 // lv: the weights' sum with the values' scales (int8)
 #pragma unroll
-        for (int i = 0; i < VW * 4; ++i)
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-            for (int j = 0; j < (HALF ? 2 : 4); ++j) acc[i][j] = 0.0f;
-        float m[2] = {-3.402823466e38f, -3.402823466e38f}, l[2] = {0.0f, 0.0f};
+            for (int i = 0; i < 2 * VW; ++i) acc[n][i][0] = acc[n][i][1] = acc[n][i][2] = acc[n][i][3] = 0.0f;
+            m[n][0] = m[n][1] = -3.402823466e38f;
+            l[n][0] = l[n][1] = lv[n][0] = lv[n][1] = 0.0f;
+        }
         // positions that some row sees, that every row sees
-        const int any_lo = gm.window > 0 ? max(0, s.len - s.n - gm.window + 1) : 0;
-        const int all_lo = gm.window > 0 ? s.len - gm.window : 0, all_hi = s.len - s.n;
-        const float* ksp = ks + bh * gm.nblk;
-        const float* vsp = vs + bh * gm.nblk;
-        int key = (s.tile0 + seg.t0) * kTileKeys + kw * 16;
-        const int last_blk = s.len > 0 ? (s.len - 1) >> gm.shift : 0;
-        float ksc = __ldg(ksp + min(key >> gm.shift, last_blk)), vsc = __ldg(vsp + min(key >> gm.shift, last_blk));
-        for (int tile = seg.t0; tile < seg.t1; ++tile, key += kTileKeys) {
-            const int nb = min((key + kTileKeys) >> gm.shift, last_blk);       // the next step's block
-            const float ksn = __ldg(ksp + nb), vsn = __ldg(vsp + nb);
-            if (!dead) dead = !warp_wait(full + 8 * st, phase, err, &abort_flag);
-            if (key < s.len && key + 16 > any_lo) {
-                const uint32_t kt = sbase + st * 2 * X::kTile, vt = kt + X::kTile;
-                float c[2][4];
+        const int any_lo = gm.window > 0 ? max(0, len - news - gm.window + 1) : 0;
+        const int all_lo = gm.window > 0 ? len - gm.window : 0, all_hi = len - news;
+        const float* ksp = ks + (int64_t)s.bh * gm.nblk;
+        const float* vsp = vs + (int64_t)s.bh * gm.nblk;
+        int key = s.key + kw * 16;
+        const int last_blk = len > 0 ? (len - 1) >> gm.shift : 0;
+        int blk = min(key >> gm.shift, last_blk);
+        float ksc = __ldg(ksp + blk), vsc = __ldg(vsp + blk);
+        for (int tile = 0; tile < tiles; ++tile, key += kTileKeys) {
+            blk = min((key + kTileKeys) >> gm.shift, last_blk);                 // the next step's
+            const float ksn = __ldg(ksp + blk), vsn = __ldg(vsp + blk);
+            if (!warp_wait(full + 8 * st, phase, err, &abort_flag)) return;
+            if (key < len && key + 16 > any_lo) {
+                const uint8_t* kt = sm + st * 2 * X::kTile;
+                float c[NT][4];
+                {
+                    uint32_t kd[2][KL][KW];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t kwd[KL][KW];
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int p = 0; p < KL; ++p) lds(kt + koff[i][p], kwd[p]);
-                    c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.0f;
+                        for (int p = 0; p < KL; ++p) words<KW>(kt + (koff ^ (p * 64)) + i * 8 * DH, kd[i][p]);
+                    float c2[NT][4];                          // a second chain of sums: half the latency
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        c[n][0] = c[n][2] = E4M3 ? 0.0f : qbias[n][0];
+                        c[n][1] = c[n][3] = E4M3 ? 0.0f : qbias[n][1];
+                        c2[n][0] = c2[n][1] = c2[n][2] = c2[n][3] = 0.0f;
+                    }
 #pragma unroll
                     for (int p = 0; p < KL; ++p)
 #pragma unroll
                         for (int x = 0; x < KW; ++x) {
-                            uint32_t b0, b1;
-                            key_halves<E4M3>(kwd[p][x], b0, b1);
+                            uint32_t a[4];                    // keys g, g + 8
+                            key_halves<E4M3>(kd[0][p][x], a[0], a[2]);
+                            key_halves<E4M3>(kd[1][p][x], a[1], a[3]);
                             const int y = p * KW + x;
-                            mma16816(c[i], qa[0][y][0], HALF ? 0u : qa[HALF ? 0 : 1][y][0], qa[0][y][1],
-                                     HALF ? 0u : qa[HALF ? 0 : 1][y][1], b0, b1, c[i][0], c[i][1], c[i][2], c[i][3]);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                float(&d)[4] = y & 1 ? c2[n] : c[n];
+                                mma16816(d, a, qb[n][y][0], qb[n][y][1], d[0], d[1], d[2], d[3]);
+                            }
                         }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) c[n][i] += c2[n][i];
                 }
                 const bool inside = key >= all_lo && key + 15 <= all_hi;
-                float top[2] = {-INFINITY, -INFINITY};
+                const int p0 = key + kappa<DH>(g);
+                bool up = false;
+                float top[NT][2];
 #pragma unroll
-                for (int r = 0; r < (HALF ? 1 : 2); ++r) {
-                    const float f = qinv[r] * ksc * gm.scale_log2;
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float& y = c[i >> 1][2 * r + (i & 1)];
-                        y *= f;
-                        if (!inside) {
-                            const int p = key + (i >> 1) * 8 + kappa<DH>(2 * t + (i & 1));
-                            if (p > seen_hi[r] || p < seen_lo[r]) y = -INFINITY;
+                    for (int j = 0; j < 2; ++j) {
+                        const float f = ksc * gm.scale_log2 * (E4M3 ? 0x1p-10f : 0x1p14f) * qinv[n][j];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float& y = c[n][2 * i + j];
+                            y *= f;
+                            if (!inside && (p0 + 8 * i > seen_hi[n][j] || p0 + 8 * i < seen_lo[n][j])) y = -INFINITY;
                         }
-                        top[r] = fmaxf(top[r], y);
+                        top[n][j] = fmaxf(c[n][j], c[n][2 + j]);
+                        up = up || top[n][j] > m[n][j] + 8.0f;
                     }
-                }
-                const bool up = top[0] > m[0] + 8.0f || (!HALF && top[1] > m[1] + 8.0f);
                 if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-                    for (int r = 0; r < (HALF ? 1 : 2); ++r) {
-                        float y = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
-                        y = fmaxf(y, m[r]);
-                        const float keep = ex2(m[r] - y);
-                        m[r] = y;
-                        l[r] *= keep;
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int i = 0; i < VW * 4; ++i) {
-                            acc[i][2 * r] *= keep;
-                            acc[i][2 * r + 1] *= keep;
+                        for (int j = 0; j < 2; ++j) {
+                            float y = top[n][j];
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+                            y = fmaxf(y, m[n][j]);
+                            const float keep = ex2(m[n][j] - y);
+                            m[n][j] = y;
+                            l[n][j] *= keep;
+                            lv[n][j] *= keep;
+#pragma unroll
+                            for (int i = 0; i < 2 * VW; ++i) {
+                                acc[n][i][j] *= keep;
+                                acc[n][i][2 + j] *= keep;
+                            }
                         }
-                    }
                 }
-                uint32_t pa[2][2];                            // [8 keys][row]
+                uint32_t pb[NT][2];                           // weights of keys 2 t, 2 t + 1 (+ 8) for row g
 #pragma unroll
-                for (int r = 0; r < (HALF ? 1 : 2); ++r) {
-                    const float base = m[r] - 7.0f;
+                for (int n = 0; n < NT; ++n) {
+                    const float b0 = m[n][0] - 7.0f, b1 = m[n][1] - 7.0f;
+                    float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float p0 = ex2(c[i][2 * r] - base), p1 = ex2(c[i][2 * r + 1] - base);
-                        l[r] += p0 + p1;
-                        const __half2 h = __floats2half2_rn(p0, p1);
-                        pa[i][r] = *reinterpret_cast<const uint32_t*>(&h);
+                        const __half2 h = __floats2half2_rn(ex2(c[n][2 * i] - b0), ex2(c[n][2 * i + 1] - b1));
+                        const float2 p = __half22float2(h);   // summed as they are multiplied
+                        s0 += p.x;
+                        s1 += p.y;
+                        pb[n][i] = transposed(*reinterpret_cast<const uint32_t*>(&h));
+                    }
+                    l[n][0] += s0;
+                    l[n][1] += s1;
+                    if (!E4M3) {
+                        lv[n][0] = fmaf(vsc, s0, lv[n][0]);
+                        lv[n][1] = fmaf(vsc, s1, lv[n][1]);
                     }
                 }
                 uint32_t vw[4][VW];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    lds(vt + voff[i], vw[i]);
+                    words<VW>(kt + voff[i & 1] + (i >> 1) * 8 * DH, vw[i]);
                     if (E4M3 && !inside) {                    // a code that nothing sees may be a NaN
                         const int p = key + (i >> 1) * 8 + kappa<DH>(2 * t + (i & 1));
-                        if (p >= s.len || p < any_lo)
+                        if (p >= len || p < any_lo)
 #pragma unroll
                             for (int x = 0; x < VW; ++x) vw[i][x] = 0;
                     }
                 }
 #pragma unroll
                 for (int x = 0; x < VW; ++x) {
-                    uint32_t b0[4], b1[4];
-                    value_halves<E4M3>(vw[0][x], vw[1][x], b0);
-                    value_halves<E4M3>(vw[2][x], vw[3][x], b1);
+                    uint32_t v0[4], v1[4];                    // keys 2 t, 2 t + 1; 8 further
+                    value_halves<E4M3>(vw[0][x], vw[1][x], v0);
+                    value_halves<E4M3>(vw[2][x], vw[3][x], v1);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float d[4];
-                        mma16816(d, pa[0][0], HALF ? 0u : pa[0][1], pa[1][0], HALF ? 0u : pa[1][1], b0[i], b1[i], 0.0f, 0.0f,
-                                 0.0f, 0.0f);
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t a[4] = {v0[2 * h], v0[2 * h + 1], v1[2 * h], v1[2 * h + 1]};
 #pragma unroll
-                        for (int j = 0; j < (HALF ? 2 : 4); ++j) acc[4 * x + i][j] = fmaf(vsc, d[j], acc[4 * x + i][j]);
+                        for (int n = 0; n < NT; ++n) {
+                            float d[4];
+                            mma16816(d, a, pb[n][0], pb[n][1], 0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) acc[n][2 * x + h][j] = fmaf(vsc, d[j], acc[n][2 * x + h][j]);
+                        }
                     }
                 }
             }
@@ -509,29 +595,32 @@ __global__ void __launch_bounds__(Ax<DH, HALF, RG>::kThreads, Ax<DH, HALF, RG>::
             ksc = ksn;
             vsc = vsn;
         }
-        // The four warps' parts, added up.  Lane (g, t) holds coordinates [t DH / 4, (t + 1) DH / 4) of its rows:
-        // column n = 2 t + j of product (x, i) is coordinate n DH / 8 + 4 x + i.
+        // The four warps' parts, added up.
+        if (sn > 0 && !warp_wait(bempty + 8 * rg, sn + 1 & 1, err, &abort_flag)) return;      // the last segment's have been read
 #pragma unroll
-        for (int r = 0; r < (HALF ? 1 : 2); ++r) {
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        }
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + rg) : "memory");           // the last segment's have been read
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int r = 0; r < (HALF ? 1 : 2); ++r) {
+            for (int j = 0; j < 2; ++j) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+                for (int d = 4; d < 32; d <<= 1) {
+                    l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], d);
+                    if (!E4M3) lv[n][j] += __shfl_xor_sync(0xffffffffu, lv[n][j], d);
+                }
+                const int r = 8 * n + 2 * t + j;
 #pragma unroll
-                for (int x = 0; x < VW; ++x)
-                    buf[kw * R * (DH / 4) + buf_at<DH, HALF, RG>(g + 8 * r, t * VPT + j * VW + x)] =
-                        make_float4(acc[4 * x][2 * r + j], acc[4 * x + 1][2 * r + j], acc[4 * x + 2][2 * r + j],
-                                    acc[4 * x + 3][2 * r + j]);
-            if (t == 0) ml[kw * R + g + 8 * r] = make_float2(m[r], l[r]);
-        }
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + rg) : "memory");
-        const bool whole = seg.t0 == 0 && seg.t1 == s.tiles;
-        const int slot = (int)blockIdx.x * 2 + (first_seg ? 0 : 1);
-        first_seg = false;
+                for (int x = 0; x < VW; ++x) {
+                    float4 v = make_float4(acc[n][2 * x][j], acc[n][2 * x][2 + j], acc[n][2 * x + 1][j], acc[n][2 * x + 1][2 + j]);
+                    if (!E4M3) {
+                        const float b = lv[n][j] * -128.0f;
+                        v = make_float4(fmaf(v.x, 0x1p24f, b), fmaf(v.y, 0x1p24f, b), fmaf(v.z, 0x1p24f, b), fmaf(v.w, 0x1p24f, b));
+                    }
+                    buf[kw * R * (DH / 4) + buf_at<DH>(r, g * VW + x)] = v;
+                }
+                if (g == 0) ml[kw * R + r] = make_float2(m[n][j], l[n][j]);
+            }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bfull + 8 * rg);
+        if (!warp_wait(bfull + 8 * rg, sn & 1, err, &abort_flag)) return;
         const int lt = tid & 127;
         for (int e = lt; e < R * (DH / 4); e += 128) {
             const int r = e / (DH / 4), f = e % (DH / 4);
@@ -548,7 +637,7 @@ __global__ void __launch_bounds__(Ax<DH, HALF, RG>::kThreads, Ax<DH, HALF, RG>::
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float k = ex2(x[i].x - top);
-                const float4 y = buf[i * R * (DH / 4) + buf_at<DH, HALF, RG>(r, f)];
+                const float4 y = buf[i * R * (DH / 4) + buf_at<DH>(r, f)];
                 sum = fmaf(k, x[i].y, sum);
                 v.x = fmaf(k, y.x, v.x);
                 v.y = fmaf(k, y.y, v.y);
@@ -556,93 +645,112 @@ __global__ void __launch_bounds__(Ax<DH, HALF, RG>::kThreads, Ax<DH, HALF, RG>::
                 v.w = fmaf(k, y.w, v.w);
             }
             const int rr = rb * gm.block_rows + rg * R + r;
-            if (whole) {
+            if (s.piece < 0) {
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                __nv_bfloat16* at = o + ((int64_t)s.row0 + rr / gm.G) * gm.so_t + (int64_t)(kvh * gm.G + rr % gm.G) * gm.so_h + f * 4;
+                __nv_bfloat16* at = o + ((int64_t)s.row0 + rr / gm.G) * gm.so_t + (int64_t)(s.kvh * gm.G + rr % gm.G) * gm.so_h + f * 4;
                 *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
             } else {
-                const int64_t pr = (int64_t)slot * gm.block_rows + rg * R + r;
+                const int64_t pr = (int64_t)s.piece * gm.block_rows + rg * R + r;
                 part_o[pr * (DH / 4) + f] = v;
                 if (f == 0) part_ml[pr] = make_float2(top, sum);
             }
         }
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(bempty + 8 * rg);
+            mbar_arrive(qempty + 8 * (sn & 1));
+        }
     }
 }
 
-// Joins the pieces of the jobs that runs cut: CTA i looks at the boundary before run i + 1, and
-// takes the job if that is the first boundary inside it.  Row by row; a row's float4s by
-// DH / 4 threads, the pieces by the groups of threads in turn.
+// Joins the pieces of the jobs that runs cut.  A job of P pieces has P - 1 boundaries of runs inside
+// it; CTA i looks at the boundary before run i + 1 and takes its share of that job's rows, in
+// float4s, kJoin of them at least.  The pieces are taken by the groups of threads in turn and
+// added in an order that depends on their number alone.
+constexpr int kJoin = 8, kJoinThreads = 256;
 template <int DH>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kJoinThreads)
     k_cache8_join(const PieceHead* __restrict__ heads, const float2* __restrict__ part_ml, const float4* __restrict__ part_o,
                   __nv_bfloat16* __restrict__ o, const int32_t* __restrict__ cu, const int32_t* __restrict__ lens,
                   const Geom gm, int ctas) {
-    constexpr int F = DH / 4, GR = 256 / F;
-    __shared__ float4 sum_o[GR][F];
-    __shared__ float2 sum_ml[GR];
+    constexpr int F = DH / 4;
+    __shared__ float4 sum_o[kJoinThreads];
+    __shared__ float2 sum_ml[kJoinThreads];
     pdl_wait();
     pdl_trigger();
-    const int i = (int)blockIdx.x + 1;
+    const int i = (int)blockIdx.x + 1, tid = threadIdx.x;
     const PieceHead h = heads[i];
     if (h.job_row < 0) return;
     const int runs = run_count(h.total, ctas);
-    const int u = run_start(i, h.total, runs), before = run_start(i - 1, h.total, runs);
-    if (u == h.start || before > h.start) return;
-    // pieces: run i - 1's last segment, then the first of the runs from i on, as far as the job goes
-    const int first_slot = before == h.start ? 2 * (i - 1) : 2 * (i - 1) + 1;
-    int pieces = 1;
-    {
-        // runs from i on that begin before the job's end
-        int lo = i, hi = runs;                               // run_start(lo) < end; first that does not, at most runs
-        while (lo + 1 < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (run_start(mid, h.total, runs) < h.end) lo = mid;
-            else hi = mid;
-        }
-        pieces += lo - i + 1;
-    }
+    if (run_start(i, h.total, runs) == h.start) return;      // the boundary of runs is one of jobs
+    const int ra = run_of(h.start, h.total, runs), pieces = run_of(h.end - 1, h.total, runs) - ra + 1;
+    const int first_piece = 2 * ra + (run_start(ra, h.total, runs) != h.start);
     const int rb = h.job_row % gm.row_blocks, bh = h.job_row / gm.row_blocks, b = bh / gm.Hkv, kvh = bh % gm.Hkv;
     bool bad;
     const Seq s = get_seq(cu, lens, gm, b, bad);
-    const int rows = min(s.n * gm.G - rb * gm.block_rows, gm.block_rows);
-    const int f = threadIdx.x % F, gr = threadIdx.x / F;
-    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    const int all = min(s.n * gm.G - rb * gm.block_rows, gm.block_rows) * F;
+    const int share = max(kJoin, (all + pieces - 2) / (pieces - 1));
+    const int e0 = (i - ra - 1) * share, e1 = min(all, e0 + share);
+    // entries side by side, a power of two of them; the other threads share the pieces
+    int width = kJoin;
+    while (width < share && width < kJoinThreads) width <<= 1;
+    const int groups = kJoinThreads / width, gr = tid / width;
+    for (int at = e0; at < e1; at += width) {
+        const int e = at + tid % width;
+        const int r = e / F, f = e % F;
         float top = -3.402823466e38f, sum = 0.0f;
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int p = gr; p < pieces; p += GR) {
-            const int64_t pr = (int64_t)(p == 0 ? first_slot : 2 * (i - 1 + p)) * gm.block_rows + r;
-            const float2 x = part_ml[pr];
-            const float4 y = part_o[pr * F + f];
-            const float nt = fmaxf(top, x.x), k0 = ex2(top - nt), k1 = ex2(x.x - nt);
-            sum = sum * k0 + x.y * k1;
-            v = make_float4(v.x * k0 + y.x * k1, v.y * k0 + y.y * k1, v.z * k0 + y.z * k1, v.w * k0 + y.w * k1);
+        for (int p0 = gr; p0 < pieces && e < e1; p0 += 4 * groups) {         // four at a time: their loads together
+            float2 x[4];
+            float4 y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int p = p0 + k * groups;
+                x[k] = make_float2(-3.402823466e38f, 0.0f);
+                y[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (p < pieces) {
+                    const int64_t pr = (int64_t)(p == 0 ? first_piece : 2 * (ra + p)) * gm.block_rows + r;
+                    x[k] = part_ml[pr];
+                    y[k] = part_o[pr * F + f];
+                }
+            }
+            const float nt = fmaxf(fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)), top), k0 = ex2(top - nt);
+            sum *= k0;
+            v = make_float4(v.x * k0, v.y * k0, v.z * k0, v.w * k0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float w = ex2(x[k].x - nt);
+                sum = fmaf(w, x[k].y, sum);
+                v = make_float4(fmaf(w, y[k].x, v.x), fmaf(w, y[k].y, v.y), fmaf(w, y[k].z, v.z), fmaf(w, y[k].w, v.w));
+            }
             top = nt;
         }
-        sum_o[gr][f] = v;
-        if (f == 0) sum_ml[gr] = make_float2(top, sum);
+        sum_o[tid] = v;
+        sum_ml[tid] = make_float2(top, sum);
         __syncthreads();
-        if (gr == 0) {
-            float all = -3.402823466e38f;
-            for (int k = 0; k < GR; ++k) all = fmaxf(all, sum_ml[k].x);
+        if (gr == 0 && e < e1) {
+            const int n = min(groups, pieces);
+            for (int k = 1; k < n; ++k) top = fmaxf(top, sum_ml[k * width + tid].x);
             float den = 0.0f;
-            float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int k = 0; k < GR; ++k) {
-                const float w = ex2(sum_ml[k].x - all);
-                const float4 y = sum_o[k][f];
-                den = fmaf(w, sum_ml[k].y, den);
-                z = make_float4(fmaf(w, y.x, z.x), fmaf(w, y.y, z.y), fmaf(w, y.z, z.z), fmaf(w, y.w, z.w));
+            v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int k = 0; k < n; ++k) {
+                const float2 x = sum_ml[k * width + tid];
+                const float w = ex2(x.x - top);
+                const float4 y = sum_o[k * width + tid];
+                den = fmaf(w, x.y, den);
+                v = make_float4(fmaf(w, y.x, v.x), fmaf(w, y.y, v.y), fmaf(w, y.z, v.z), fmaf(w, y.w, v.w));
             }
             const float inv = den == 0.0f ? 0.0f : 1.0f / den;
             const int rr = rb * gm.block_rows + r;
-            __nv_bfloat16* at = o + ((int64_t)s.row0 + rr / gm.G) * gm.so_t + (int64_t)(kvh * gm.G + rr % gm.G) * gm.so_h + f * 4;
-            *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16x2(z.x * inv, z.y * inv), pack_bf16x2(z.z * inv, z.w * inv));
+            __nv_bfloat16* to = o + ((int64_t)s.row0 + rr / gm.G) * gm.so_t + (int64_t)(kvh * gm.G + rr % gm.G) * gm.so_h + f * 4;
+            *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
         }
         __syncthreads();
     }
 }
 
-// Rows of a job by the rows that max_new tokens of a kv head have: 8 in one warp's tile half,
-// 16 in one, 32 in two row groups; more are blocks of 32, each of which reads the tiles.
+// Rows of a job by the rows that max_new tokens of a kv head have: 8 or 16 in every warp, 32 in
+// two row groups of warps; more are blocks of 32, each of which reads the tiles.
 int job_rows(int group, int max_new) {
     const int rows = group * max_new;
     return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
@@ -661,13 +769,13 @@ Space space(int rows, int dh) {
     return s;
 }
 
-template <bool E4M3, int DH, bool HALF, int RG>
+template <bool E4M3, int DH, int NT, int RG>
 cudaError_t launch_part(const Cache8AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, const Geom& gm, cudaStream_t st) {
-    using X = Ax<DH, HALF, RG>;
+    using X = Ax<DH, NT, RG>;
     static std::atomic<uint64_t> done{0};
     const int smem = X::kBase + 4 * (a.B + 1);
     // sequences beyond those that leave room for kCtas have fewer CTAs per SM; 4096 still fit
-    cudaError_t e = allow_smem(done, k_cache8_part<E4M3, DH, HALF, RG>, X::kBase + 4 * 4097);
+    cudaError_t e = allow_smem(done, k_cache8_part<E4M3, DH, NT, RG>, X::kBase + 4 * 4097);
     if (e != cudaSuccess) return e;
     const int ctas = sm_count() * X::kCtas < kMaxRuns ? sm_count() * X::kCtas : kMaxRuns;
     char* ws = static_cast<char*>(a.ws);
@@ -675,20 +783,20 @@ cudaError_t launch_part(const Cache8AttnArgs& a, const CUtensorMap& km, const CU
     PieceHead* heads = reinterpret_cast<PieceHead*>(ws + sp.heads);
     float2* ml = reinterpret_cast<float2*>(ws + sp.ml);
     float4* po = reinterpret_cast<float4*>(ws + sp.o);
-    e = launch_pdl(k_cache8_part<E4M3, DH, HALF, RG>, dim3(ctas), dim3(X::kThreads), smem, st, km, vm,
+    e = launch_pdl(k_cache8_part<E4M3, DH, NT, RG>, dim3(ctas), dim3(X::kThreads), smem, st, km, vm,
                    static_cast<const __nv_bfloat16*>(a.q), a.ks, a.vs, static_cast<__nv_bfloat16*>(a.o), a.cu, a.lens, heads,
                    ml, po, gm, device_error_word());
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_cache8_join<DH>, dim3(ctas - 1, gm.block_rows < 8 ? gm.block_rows : 8), dim3(256), 0, st,
+    return launch_pdl(k_cache8_join<DH>, dim3(ctas - 1), dim3(kJoinThreads), 0, st,
                       static_cast<const PieceHead*>(heads), static_cast<const float2*>(ml), static_cast<const float4*>(po),
                       static_cast<__nv_bfloat16*>(a.o), a.cu, a.lens, gm, ctas);
 }
 
 template <bool E4M3, int DH>
 cudaError_t by_rows(const Cache8AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, const Geom& gm, cudaStream_t st) {
-    if (gm.block_rows == 8) return launch_part<E4M3, DH, true, 1>(a, km, vm, gm, st);
-    if (gm.block_rows == 16) return launch_part<E4M3, DH, false, 1>(a, km, vm, gm, st);
-    return launch_part<E4M3, DH, false, 2>(a, km, vm, gm, st);
+    if (gm.block_rows == 8) return launch_part<E4M3, DH, 1, 1>(a, km, vm, gm, st);
+    if (gm.block_rows == 16) return launch_part<E4M3, DH, 2, 1>(a, km, vm, gm, st);
+    return launch_part<E4M3, DH, 2, 2>(a, km, vm, gm, st);
 }
 
 template <bool E4M3>
