@@ -40,13 +40,13 @@ namespace tfm {
 namespace {
 
 constexpr int kTileKeys = 64;
-constexpr int kMaxRuns = 152 * 3 * 2;             // CTAs at most, and places for them in the workspace
+constexpr int kMaxRuns = 152 * 3;                 // CTAs at most; the workspace has places for them
 
 template <int DH, int NT, int RG>
 struct Ax {
     static constexpr int kTile = kTileKeys * DH;                       // bytes of K or V
-    static constexpr int kStages = (NT == 1 ? 3 : 4) * (128 / DH);
-    static constexpr int kCtas = NT == 1 ? 3 : RG == 1 ? 2 : 1;           // per SM
+    static constexpr int kCtas = RG == 2 ? 1 : NT == 2 || DH == 128 ? 2 : 3;   // per SM
+    static constexpr int kStages = (RG == 2 ? 8 : NT == 2 ? 4 : DH == 128 ? 5 : 3) * (DH == 128 ? 1 : DH == 64 ? 2 : 4);
     static constexpr int kRows = 8 * NT;                               // of a warp
     static constexpr int kThreads = 128 * RG + 32;
     static constexpr int kBuf = 4 * RG * kRows * DH * 4;               // the warps' o, to be added up
@@ -57,6 +57,8 @@ struct Ax {
     static constexpr int kBarOff = kQOff + 2 * kQ;                     // full, empty of the ring; of the places for q; of the buffers
     static constexpr int kCumOff = kBarOff + 16 * kStages + 32 + 16 * RG;
     static constexpr int kBase = kCumOff + 1024;                       // + 4 (B + 1); the ring on a multiple of 1024
+    // What a segment costs beside its tiles, in tiles: q, the first scores, the sum over the warps.
+    static constexpr int kPiece = DH == 32 ? 5 : 3;
     static constexpr uint32_t kSwzMask = DH == 128 ? 7 : DH == 64 ? 3 : 0;
     static constexpr int kSwzShift = DH == 128 ? 0 : 1;
 };
@@ -71,11 +73,12 @@ struct Geom {
     int64_t sq_t, sq_h, so_t, so_h;
 };
 
-// A piece of a run that a join has to look at: the job's tiles [start, end) among all, and
-// where its rows go.
-struct PieceHead {
-    int start, end, job_row;      // job_row: (b * Hkv + g) * row_blocks + row block
-    int total;                    // tiles of all jobs
+// The job that a run begins in: its units [start, end) among all, its rows, and where they go.
+struct RunHead {
+    int start, end;               // end 0: no job
+    int total;                    // units of all jobs
+    int row0, rb, kvh, nrows;
+    int pad;
 };
 
 struct Seq {
@@ -106,12 +109,13 @@ __device__ __forceinline__ int run_of(int u, int total, int runs) {      // the 
     const int q = total / runs, r = total - q * runs;
     return u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q;
 }
-// Runs of at least kLeast tiles.
-constexpr int kLeast = 2;
+// Runs of at least kLeast units.  A job has kPiece units (what it costs beside its tiles), then one
+// for each tile; a run that ends among the first ones has none of the job's tiles.
+constexpr int kLeast = 3;
 __device__ __forceinline__ int run_count(int total, int ctas) { return max(1, min(ctas, total / kLeast)); }
 
 // The run's place among the jobs: sequence b, job j of it (kv head j / blocks, row block
-// j % blocks), tile t of the job.
+// j % blocks), unit t of the job.
 struct Walk {
     int b, j, t, left;
 };
@@ -230,7 +234,7 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
     k_cache8_part(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const __nv_bfloat16* __restrict__ q, const float* __restrict__ ks, const float* __restrict__ vs,
                   __nv_bfloat16* __restrict__ o, const int32_t* __restrict__ cu, const int32_t* __restrict__ lens,
-                  PieceHead* __restrict__ heads, float2* __restrict__ part_ml, float4* __restrict__ part_o, const Geom gm,
+                  RunHead* __restrict__ heads, float2* __restrict__ part_ml, float4* __restrict__ part_o, const Geom gm,
                   int* err) {
     using X = Ax<DH, NT, RG>;
     constexpr int KW = DH >= 64 ? 4 : 2;                     // words of a load of K
@@ -279,7 +283,7 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
                 bool bad;
                 const Seq s = get_seq(cu, lens, gm, b0 + lane, bad);
                 if (bad && blockIdx.x == 0) raise_error(err, TFM_EINVAL);
-                x = s.tiles * s.blocks * gm.Hkv;
+                x = (s.tiles + X::kPiece) * s.blocks * gm.Hkv;
             }
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -308,34 +312,47 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
             w.b = lo;
             bool bad;
             const Seq s = get_seq(cu, lens, gm, lo, bad);
-            w.j = (u0 - cum[lo]) / s.tiles;
-            w.t = (u0 - cum[lo]) % s.tiles;
+            const int units = s.tiles + X::kPiece, rb = (u0 - cum[lo]) / units % s.blocks;
+            w.j = (u0 - cum[lo]) / units;
+            w.t = (u0 - cum[lo]) % units;
             if (lane == 0)
-                heads[blockIdx.x] = PieceHead{u0 - w.t, u0 - w.t + s.tiles,
-                                              (lo * gm.Hkv + w.j / s.blocks) * gm.row_blocks + w.j % s.blocks, total};
+                heads[blockIdx.x] = RunHead{u0 - w.t, u0 - w.t + units, total, s.row0, rb, w.j / s.blocks,
+                                            min(s.n * gm.G - rb * gm.block_rows, gm.block_rows), 0};
         } else if (lane == 0) {
-            heads[blockIdx.x] = PieceHead{0, 0, -1, total};
+            heads[blockIdx.x] = RunHead{0, 0, total, 0, 0, 0, 0, 0};
         }
         bool filled = false;                                 // every stage of the ring once
         for (;; ++sn) {
             const int place = sn & 1;
+            // the next segment with tiles
+            Seq s;
+            int t0 = 0, tiles = 0;
+            Walk at = w;
+            while (tiles <= 0 && w.left > 0) {
+                while (cum[w.b + 1] == cum[w.b]) ++w.b;      // a run ends before the jobs do
+                at = w;
+                bool bad;
+                s = get_seq(cu, lens, gm, w.b, bad);
+                const int units = min(s.tiles + X::kPiece - w.t, w.left);
+                t0 = max(w.t - X::kPiece, 0);
+                tiles = w.t + units - X::kPiece - t0;
+                w.left -= units;
+                w.t = 0;                                     // whatever comes next is another job
+                if (++w.j == s.blocks * gm.Hkv) w.j = 0, ++w.b;
+            }
             if (sn >= 2 && !warp_wait(qempty + 8 * place, (sn >> 1) + 1 & 1, err, &abort_flag)) return;
-            if (w.left <= 0) {
+            if (tiles <= 0) {
                 if (lane == 0) {
                     segs[place].tiles = 0;
                     mbar_arrive(qfull + 8 * place);
                 }
                 return;
             }
-            while (cum[w.b + 1] == cum[w.b]) ++w.b;          // a run ends before the jobs do
-            bool bad;
-            const Seq s = get_seq(cu, lens, gm, w.b, bad);
-            const int kvh = w.j / s.blocks, rb = w.j % s.blocks;
-            const int tiles = min(s.tiles - w.t, w.left);
+            const int kvh = at.j / s.blocks, rb = at.j % s.blocks, bh = at.b * gm.Hkv + kvh;
             const int nrows = min(s.n * gm.G - rb * gm.block_rows, gm.block_rows);
-            int row = (w.b * gm.Hkv + kvh) * gm.max_seq + (s.tile0 + w.t) * kTileKeys;
+            int row = bh * gm.max_seq + (s.tile0 + t0) * kTileKeys;
             if (lane == 0) {
-                segs[place] = Seg{tiles, (s.tile0 + w.t) * kTileKeys, s.len, s.n, s.row0, w.b * gm.Hkv + kvh, kvh, rb, nrows,
+                segs[place] = Seg{tiles, (s.tile0 + t0) * kTileKeys, s.len, s.n, s.row0, bh, kvh, rb, nrows,
                                   tiles == s.tiles ? -1 : (int)blockIdx.x * 2 + (sn > 0)};
                 mbar_arrive_expect_tx(qfull + 8 * place, nrows * DH * 2);
             }
@@ -359,9 +376,6 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
                     if (++st == X::kStages) st = 0, phase ^= 1, filled = true;
                 }
             if (!__shfl_sync(0xffffffffu, (int)ok, 0)) return;
-            w.left -= tiles;
-            w.t = 0;                                         // whatever comes next is another job
-            if (++w.j == s.blocks * gm.Hkv) w.j = 0, ++w.b;
         }
     }
     // -------------------------------------------------------------------- rows
@@ -384,11 +398,17 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
         const int tiles = s.tiles, len = s.len, news = s.n, rb = s.rb;
         if (tiles == 0) return;
         const int nrows = s.nrows - rg * R;                  // of this row group
+        const float* ksp = ks + (int64_t)s.bh * gm.nblk;
+        const float* vsp = vs + (int64_t)s.bh * gm.nblk;
+        int key = s.key + kw * 16;
+        const int last_blk = len > 0 ? (len - 1) >> gm.shift : 0;
+        int blk = min(key >> gm.shift, last_blk);
+        float ksc = __ldg(ksp + blk), vsc = __ldg(vsp + blk);
         // q: row r of the job is token r / G, head r % G.  Lane (g, t) holds row 8 n + g, for the products, of
         // what belongs to the rows 8 n + 2 t and + 1, whose scores it gets, in the arrays [n][2].
         uint32_t qb[NT][KL * KW][2];
         float qinv[NT][2], qbias[NT][2];
-        int seen_hi[NT][2], seen_lo[NT][2];                  // a row sees the positions [lo, hi]
+        int seen_hi[NT][2];                                  // the last position that a row sees
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int r = 8 * n + g;
@@ -441,7 +461,6 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
                 qbias[n][j] = __shfl_sync(0xffffffffu, sum, from) * -0x1p-17f;       // 128 of the codes' 2^-24
                 const int ro = 8 * n + 2 * t + j;
                 seen_hi[n][j] = ro < nrows ? len - news + (rb * gm.block_rows + rg * R + ro) / gm.G : len - 1;
-                seen_lo[n][j] = gm.window > 0 ? seen_hi[n][j] - gm.window + 1 : 0;
             }
         }
         // acc[n][2 x + h]: rows 8 n + 2 t (elements 0, 2) and + 1 (1, 3), coordinates g DH / 8 + 4 x + 2 h (0, 1) and + 1
@@ -457,12 +476,6 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
         // positions that some row sees, that every row sees
         const int any_lo = gm.window > 0 ? max(0, len - news - gm.window + 1) : 0;
         const int all_lo = gm.window > 0 ? len - gm.window : 0, all_hi = len - news;
-        const float* ksp = ks + (int64_t)s.bh * gm.nblk;
-        const float* vsp = vs + (int64_t)s.bh * gm.nblk;
-        int key = s.key + kw * 16;
-        const int last_blk = len > 0 ? (len - 1) >> gm.shift : 0;
-        int blk = min(key >> gm.shift, last_blk);
-        float ksc = __ldg(ksp + blk), vsc = __ldg(vsp + blk);
         for (int tile = 0; tile < tiles; ++tile, key += kTileKeys) {
             blk = min((key + kTileKeys) >> gm.shift, last_blk);                 // the next step's
             const float ksn = __ldg(ksp + blk), vsn = __ldg(vsp + blk);
@@ -476,12 +489,11 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int p = 0; p < KL; ++p) words<KW>(kt + (koff ^ (p * 64)) + i * 8 * DH, kd[i][p]);
-                    float c2[NT][4];                          // a second chain of sums: half the latency
+                    float c2[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // a second chain of sums: half the latency
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         c[n][0] = c[n][2] = E4M3 ? 0.0f : qbias[n][0];
                         c[n][1] = c[n][3] = E4M3 ? 0.0f : qbias[n][1];
-                        c2[n][0] = c2[n][1] = c2[n][2] = c2[n][3] = 0.0f;
                     }
 #pragma unroll
                     for (int p = 0; p < KL; ++p)
@@ -493,14 +505,13 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
                             const int y = p * KW + x;
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
-                                float(&d)[4] = y & 1 ? c2[n] : c[n];
+                                float(&d)[4] = NT == 1 && (y & 1) ? c2 : c[n];
                                 mma16816(d, a, qb[n][y][0], qb[n][y][1], d[0], d[1], d[2], d[3]);
                             }
                         }
+                    if (NT == 1)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) c[n][i] += c2[n][i];
+                        for (int i = 0; i < 4; ++i) c[0][i] += c2[i];
                 }
                 const bool inside = key >= all_lo && key + 15 <= all_hi;
                 const int p0 = key + kappa<DH>(g);
@@ -515,7 +526,8 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
                         for (int i = 0; i < 2; ++i) {
                             float& y = c[n][2 * i + j];
                             y *= f;
-                            if (!inside && (p0 + 8 * i > seen_hi[n][j] || p0 + 8 * i < seen_lo[n][j])) y = -INFINITY;
+                            if (!inside && (p0 + 8 * i > seen_hi[n][j] || (gm.window > 0 && p0 + 8 * i <= seen_hi[n][j] - gm.window)))
+                                y = -INFINITY;
                         }
                         top[n][j] = fmaxf(c[n][j], c[n][2 + j]);
                         up = up || top[n][j] > m[n][j] + 8.0f;
@@ -670,27 +682,24 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
 constexpr int kJoin = 8, kJoinThreads = 256;
 template <int DH>
 __global__ void __launch_bounds__(kJoinThreads)
-    k_cache8_join(const PieceHead* __restrict__ heads, const float2* __restrict__ part_ml, const float4* __restrict__ part_o,
-                  __nv_bfloat16* __restrict__ o, const int32_t* __restrict__ cu, const int32_t* __restrict__ lens,
-                  const Geom gm, int ctas) {
+    k_cache8_join(const RunHead* __restrict__ heads, const float2* __restrict__ part_ml, const float4* __restrict__ part_o,
+                  __nv_bfloat16* __restrict__ o, const Geom gm, int ctas, int piece_units) {
     constexpr int F = DH / 4;
     __shared__ float4 sum_o[kJoinThreads];
     __shared__ float2 sum_ml[kJoinThreads];
     pdl_wait();
     pdl_trigger();
     const int i = (int)blockIdx.x + 1, tid = threadIdx.x;
-    const PieceHead h = heads[i];
-    if (h.job_row < 0) return;
-    const int runs = run_count(h.total, ctas);
-    if (run_start(i, h.total, runs) == h.start) return;      // the boundary of runs is one of jobs
-    const int ra = run_of(h.start, h.total, runs), pieces = run_of(h.end - 1, h.total, runs) - ra + 1;
-    const int first_piece = 2 * ra + (run_start(ra, h.total, runs) != h.start);
-    const int rb = h.job_row % gm.row_blocks, bh = h.job_row / gm.row_blocks, b = bh / gm.Hkv, kvh = bh % gm.Hkv;
-    bool bad;
-    const Seq s = get_seq(cu, lens, gm, b, bad);
-    const int all = min(s.n * gm.G - rb * gm.block_rows, gm.block_rows) * F;
-    const int share = max(kJoin, (all + pieces - 2) / (pieces - 1));
-    const int e0 = (i - ra - 1) * share, e1 = min(all, e0 + share);
+    const RunHead h = heads[i];
+    if (h.end == 0) return;
+    const int runs = run_count(h.total, ctas), first = h.start + piece_units;        // the unit of the first tile
+    if (run_start(i, h.total, runs) <= first) return;        // no tiles of the job before the boundary
+    const int ra = run_of(first, h.total, runs), pieces = run_of(h.end - 1, h.total, runs) - ra + 1;
+    const int first_piece = 2 * ra + (run_start(ra, h.total, runs) < h.start);
+    const int all = h.nrows * F;
+    const int shares = (pieces - 1) * (int)gridDim.y;
+    const int share = max(kJoin, (all + shares - 1) / shares);
+    const int e0 = ((i - ra - 1) * (int)gridDim.y + (int)blockIdx.y) * share, e1 = min(all, e0 + share);
     // entries side by side, a power of two of them; the other threads share the pieces
     int width = kJoin;
     while (width < share && width < kJoinThreads) width <<= 1;
@@ -725,24 +734,36 @@ __global__ void __launch_bounds__(kJoinThreads)
             }
             top = nt;
         }
+        // a warp's groups, then the warps
+        for (int d = width; d < 32; d <<= 1) {
+            const float t1 = __shfl_xor_sync(0xffffffffu, top, d), s1 = __shfl_xor_sync(0xffffffffu, sum, d);
+            const float4 y = make_float4(__shfl_xor_sync(0xffffffffu, v.x, d), __shfl_xor_sync(0xffffffffu, v.y, d),
+                                         __shfl_xor_sync(0xffffffffu, v.z, d), __shfl_xor_sync(0xffffffffu, v.w, d));
+            const float nt = fmaxf(top, t1), k0 = ex2(top - nt), k1 = ex2(t1 - nt);
+            sum = sum * k0 + s1 * k1;
+            v = make_float4(v.x * k0 + y.x * k1, v.y * k0 + y.y * k1, v.z * k0 + y.z * k1, v.w * k0 + y.w * k1);
+            top = nt;
+        }
         sum_o[tid] = v;
         sum_ml[tid] = make_float2(top, sum);
         __syncthreads();
         if (gr == 0 && e < e1) {
-            const int n = min(groups, pieces);
-            for (int k = 1; k < n; ++k) top = fmaxf(top, sum_ml[k * width + tid].x);
+            const int step = width < 32 ? 32 : width;
+#pragma unroll 4
+            for (int k = step; k < kJoinThreads; k += step) top = fmaxf(top, sum_ml[k + tid].x);
             float den = 0.0f;
             v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int k = 0; k < n; ++k) {
-                const float2 x = sum_ml[k * width + tid];
+#pragma unroll 4
+            for (int k = 0; k < kJoinThreads; k += step) {
+                const float2 x = sum_ml[k + tid];
                 const float w = ex2(x.x - top);
-                const float4 y = sum_o[k * width + tid];
+                const float4 y = sum_o[k + tid];
                 den = fmaf(w, x.y, den);
                 v = make_float4(fmaf(w, y.x, v.x), fmaf(w, y.y, v.y), fmaf(w, y.z, v.z), fmaf(w, y.w, v.w));
             }
             const float inv = den == 0.0f ? 0.0f : 1.0f / den;
-            const int rr = rb * gm.block_rows + r;
-            __nv_bfloat16* to = o + ((int64_t)s.row0 + rr / gm.G) * gm.so_t + (int64_t)(kvh * gm.G + rr % gm.G) * gm.so_h + f * 4;
+            const int rr = h.rb * gm.block_rows + r;
+            __nv_bfloat16* to = o + ((int64_t)h.row0 + rr / gm.G) * gm.so_t + (int64_t)(h.kvh * gm.G + rr % gm.G) * gm.so_h + f * 4;
             *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
         }
         __syncthreads();
@@ -763,7 +784,7 @@ Space space(int rows, int dh) {
     Space s;
     const size_t runs = kMaxRuns;
     s.heads = 0;
-    s.ml = s.heads + runs * sizeof(PieceHead);
+    s.ml = s.heads + runs * sizeof(RunHead);
     s.o = s.ml + 2 * runs * rows * sizeof(float2);
     s.bytes = s.o + 2 * runs * rows * dh * sizeof(float);
     return s;
@@ -780,16 +801,16 @@ cudaError_t launch_part(const Cache8AttnArgs& a, const CUtensorMap& km, const CU
     const int ctas = sm_count() * X::kCtas < kMaxRuns ? sm_count() * X::kCtas : kMaxRuns;
     char* ws = static_cast<char*>(a.ws);
     const Space sp = space(gm.block_rows, DH);
-    PieceHead* heads = reinterpret_cast<PieceHead*>(ws + sp.heads);
+    RunHead* heads = reinterpret_cast<RunHead*>(ws + sp.heads);
     float2* ml = reinterpret_cast<float2*>(ws + sp.ml);
     float4* po = reinterpret_cast<float4*>(ws + sp.o);
     e = launch_pdl(k_cache8_part<E4M3, DH, NT, RG>, dim3(ctas), dim3(X::kThreads), smem, st, km, vm,
                    static_cast<const __nv_bfloat16*>(a.q), a.ks, a.vs, static_cast<__nv_bfloat16*>(a.o), a.cu, a.lens, heads,
                    ml, po, gm, device_error_word());
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_cache8_join<DH>, dim3(ctas - 1), dim3(kJoinThreads), 0, st,
-                      static_cast<const PieceHead*>(heads), static_cast<const float2*>(ml), static_cast<const float4*>(po),
-                      static_cast<__nv_bfloat16*>(a.o), a.cu, a.lens, gm, ctas);
+    return launch_pdl(k_cache8_join<DH>, dim3(ctas - 1, gm.block_rows / 8), dim3(kJoinThreads), 0, st,
+                      static_cast<const RunHead*>(heads), static_cast<const float2*>(ml), static_cast<const float4*>(po),
+                      static_cast<__nv_bfloat16*>(a.o), gm, ctas, X::kPiece);
 }
 
 template <bool E4M3, int DH>
