@@ -33,6 +33,8 @@
 // (sequence, kv head, row block) jobs lie end to end and are cut into equal runs, one per
 // resident CTA, whatever the lengths are; a run's first and last job may be pieces, whose
 // (max, sum, unnormalised o) a second kernel joins exactly, in a fixed order.
+#include <type_traits>
+
 #include "cache8.cuh"
 
 namespace tfm {
@@ -45,8 +47,8 @@ constexpr int kMaxRuns = 152 * 3;                 // CTAs at most; the workspace
 template <int DH, int NT, int RG>
 struct Ax {
     static constexpr int kTile = kTileKeys * DH;                       // bytes of K or V
-    static constexpr int kCtas = RG == 2 ? 1 : NT == 2 || DH == 128 ? 2 : 3;   // per SM
-    static constexpr int kStages = (RG == 2 ? 8 : NT == 2 ? 4 : DH == 128 ? 5 : 3) * (DH == 128 ? 1 : DH == 64 ? 2 : 4);
+    static constexpr int kCtas = RG > 1 ? 1 : NT == 2 || DH == 128 ? 2 : 3;   // per SM
+    static constexpr int kStages = (RG > 1 ? 8 : NT == 2 ? 4 : DH == 128 ? 5 : 3) * (DH == 128 ? 1 : DH == 64 ? 2 : 4);
     static constexpr int kRows = 8 * NT;                               // of a warp
     static constexpr int kThreads = 128 * RG + 32;
     static constexpr int kBuf = 4 * RG * kRows * DH * 4;               // the warps' o, to be added up
@@ -67,7 +69,7 @@ struct Geom {
     int B, T, H, Hkv, G, max_new, max_seq, nblk, shift;
     int per;                  // rows per sequence without offsets
     int window;
-    int block_rows;           // rows of a job: 8, 16 or 32
+    int block_rows;           // rows of a job: 8, 16, 24 or 32
     int row_blocks;           // of max_new tokens
     float scale_log2;
     int64_t sq_t, sq_h, so_t, so_h;
@@ -476,131 +478,134 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
         // positions that some row sees, that every row sees
         const int any_lo = gm.window > 0 ? max(0, len - news - gm.window + 1) : 0;
         const int all_lo = gm.window > 0 ? len - gm.window : 0, all_hi = len - news;
-        for (int tile = 0; tile < tiles; ++tile, key += kTileKeys) {
-            blk = min((key + kTileKeys) >> gm.shift, last_blk);                 // the next step's
-            const float ksn = __ldg(ksp + blk), vsn = __ldg(vsp + blk);
-            if (!warp_wait(full + 8 * st, phase, err, &abort_flag)) return;
-            if (key < len && key + 16 > any_lo) {
-                const uint8_t* kt = sm + st * 2 * X::kTile;
-                float c[NT][4];
-                {
-                    uint32_t kd[2][KL][KW];
+        const auto step = [&](auto edge) {
+            constexpr bool EDGE = decltype(edge)::value;
+            const uint8_t* kt = sm + st * 2 * X::kTile;
+            float c[NT][4];
+            {
+                uint32_t kd[2][KL][KW];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int p = 0; p < KL; ++p) words<KW>(kt + (koff ^ (p * 64)) + i * 8 * DH, kd[i][p]);
-                    float c2[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // a second chain of sums: half the latency
+                    for (int p = 0; p < KL; ++p) words<KW>(kt + (koff ^ (p * 64)) + i * 8 * DH, kd[i][p]);
+                float c2[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // a second chain of sums: half the latency
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        c[n][0] = c[n][2] = E4M3 ? 0.0f : qbias[n][0];
-                        c[n][1] = c[n][3] = E4M3 ? 0.0f : qbias[n][1];
-                    }
-#pragma unroll
-                    for (int p = 0; p < KL; ++p)
-#pragma unroll
-                        for (int x = 0; x < KW; ++x) {
-                            uint32_t a[4];                    // keys g, g + 8
-                            key_halves<E4M3>(kd[0][p][x], a[0], a[2]);
-                            key_halves<E4M3>(kd[1][p][x], a[1], a[3]);
-                            const int y = p * KW + x;
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                float(&d)[4] = NT == 1 && (y & 1) ? c2 : c[n];
-                                mma16816(d, a, qb[n][y][0], qb[n][y][1], d[0], d[1], d[2], d[3]);
-                            }
-                        }
-                    if (NT == 1)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) c[0][i] += c2[i];
+                for (int n = 0; n < NT; ++n) {
+                    c[n][0] = c[n][2] = E4M3 ? 0.0f : qbias[n][0];
+                    c[n][1] = c[n][3] = E4M3 ? 0.0f : qbias[n][1];
                 }
-                const bool inside = key >= all_lo && key + 15 <= all_hi;
-                const int p0 = key + kappa<DH>(g);
-                bool up = false;
-                float top[NT][2];
+#pragma unroll
+                for (int p = 0; p < KL; ++p)
+#pragma unroll
+                    for (int x = 0; x < KW; ++x) {
+                        uint32_t a[4];                    // keys g, g + 8
+                        key_halves<E4M3>(kd[0][p][x], a[0], a[2]);
+                        key_halves<E4M3>(kd[1][p][x], a[1], a[3]);
+                        const int y = p * KW + x;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            float(&d)[4] = NT == 1 && (y & 1) ? c2 : c[n];
+                            mma16816(d, a, qb[n][y][0], qb[n][y][1], d[0], d[1], d[2], d[3]);
+                        }
+                    }
+                if (NT == 1)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) c[0][i] += c2[i];
+            }
+            const int p0 = key + kappa<DH>(g);
+            bool up = false;
+            float top[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float f = ksc * gm.scale_log2 * (E4M3 ? 0x1p-10f : 0x1p14f) * qinv[n][j];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float& y = c[n][2 * i + j];
+                        y *= f;
+                        if (EDGE && (p0 + 8 * i > seen_hi[n][j] || (gm.window > 0 && p0 + 8 * i <= seen_hi[n][j] - gm.window)))
+                            y = -INFINITY;
+                    }
+                    top[n][j] = fmaxf(c[n][j], c[n][2 + j]);
+                    up = up || top[n][j] > m[n][j] + 8.0f;
+                }
+            if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float f = ksc * gm.scale_log2 * (E4M3 ? 0x1p-10f : 0x1p14f) * qinv[n][j];
+                        float y = top[n][j];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            float& y = c[n][2 * i + j];
-                            y *= f;
-                            if (!inside && (p0 + 8 * i > seen_hi[n][j] || (gm.window > 0 && p0 + 8 * i <= seen_hi[n][j] - gm.window)))
-                                y = -INFINITY;
+                        for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+                        y = fmaxf(y, m[n][j]);
+                        const float keep = ex2(m[n][j] - y);
+                        m[n][j] = y;
+                        l[n][j] *= keep;
+                        lv[n][j] *= keep;
+#pragma unroll
+                        for (int i = 0; i < 2 * VW; ++i) {
+                            acc[n][i][j] *= keep;
+                            acc[n][i][2 + j] *= keep;
                         }
-                        top[n][j] = fmaxf(c[n][j], c[n][2 + j]);
-                        up = up || top[n][j] > m[n][j] + 8.0f;
                     }
-                if (__any_sync(0xffffffffu, up)) {
+            }
+            uint32_t pb[NT][2];                           // weights of keys 2 t, 2 t + 1 (+ 8) for row g
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n) {
+                const float b0 = m[n][0] - 7.0f, b1 = m[n][1] - 7.0f;
+                float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            float y = top[n][j];
-#pragma unroll
-                            for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
-                            y = fmaxf(y, m[n][j]);
-                            const float keep = ex2(m[n][j] - y);
-                            m[n][j] = y;
-                            l[n][j] *= keep;
-                            lv[n][j] *= keep;
-#pragma unroll
-                            for (int i = 0; i < 2 * VW; ++i) {
-                                acc[n][i][j] *= keep;
-                                acc[n][i][2 + j] *= keep;
-                            }
-                        }
+                for (int i = 0; i < 2; ++i) {
+                    const __half2 h = __floats2half2_rn(ex2(c[n][2 * i] - b0), ex2(c[n][2 * i + 1] - b1));
+                    const float2 p = __half22float2(h);   // summed as they are multiplied
+                    s0 += p.x;
+                    s1 += p.y;
+                    pb[n][i] = transposed(*reinterpret_cast<const uint32_t*>(&h));
                 }
-                uint32_t pb[NT][2];                           // weights of keys 2 t, 2 t + 1 (+ 8) for row g
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float b0 = m[n][0] - 7.0f, b1 = m[n][1] - 7.0f;
-                    float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const __half2 h = __floats2half2_rn(ex2(c[n][2 * i] - b0), ex2(c[n][2 * i + 1] - b1));
-                        const float2 p = __half22float2(h);   // summed as they are multiplied
-                        s0 += p.x;
-                        s1 += p.y;
-                        pb[n][i] = transposed(*reinterpret_cast<const uint32_t*>(&h));
-                    }
-                    l[n][0] += s0;
-                    l[n][1] += s1;
-                    if (!E4M3) {
-                        lv[n][0] = fmaf(vsc, s0, lv[n][0]);
-                        lv[n][1] = fmaf(vsc, s1, lv[n][1]);
-                    }
+                l[n][0] += s0;
+                l[n][1] += s1;
+                if (!E4M3) {
+                    lv[n][0] = fmaf(vsc, s0, lv[n][0]);
+                    lv[n][1] = fmaf(vsc, s1, lv[n][1]);
                 }
-                uint32_t vw[4][VW];
+            }
+            uint32_t vw[4][VW];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    words<VW>(kt + voff[i & 1] + (i >> 1) * 8 * DH, vw[i]);
-                    if (E4M3 && !inside) {                    // a code that nothing sees may be a NaN
-                        const int p = key + (i >> 1) * 8 + kappa<DH>(2 * t + (i & 1));
-                        if (p >= len || p < any_lo)
+            for (int i = 0; i < 4; ++i) {
+                words<VW>(kt + voff[i & 1] + (i >> 1) * 8 * DH, vw[i]);
+                if (E4M3 && EDGE) {                    // a code that nothing sees may be a NaN
+                    const int p = key + (i >> 1) * 8 + kappa<DH>(2 * t + (i & 1));
+                    if (p >= len || p < any_lo)
 #pragma unroll
-                            for (int x = 0; x < VW; ++x) vw[i][x] = 0;
-                    }
+                        for (int x = 0; x < VW; ++x) vw[i][x] = 0;
                 }
+            }
 #pragma unroll
-                for (int x = 0; x < VW; ++x) {
-                    uint32_t v0[4], v1[4];                    // keys 2 t, 2 t + 1; 8 further
-                    value_halves<E4M3>(vw[0][x], vw[1][x], v0);
-                    value_halves<E4M3>(vw[2][x], vw[3][x], v1);
+            for (int x = 0; x < VW; ++x) {
+                uint32_t v0[4], v1[4];                    // keys 2 t, 2 t + 1; 8 further
+                value_halves<E4M3>(vw[0][x], vw[1][x], v0);
+                value_halves<E4M3>(vw[2][x], vw[3][x], v1);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t a[4] = {v0[2 * h], v0[2 * h + 1], v1[2 * h], v1[2 * h + 1]};
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t a[4] = {v0[2 * h], v0[2 * h + 1], v1[2 * h], v1[2 * h + 1]};
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            float d[4];
-                            mma16816(d, a, pb[n][0], pb[n][1], 0.0f, 0.0f, 0.0f, 0.0f);
+                    for (int n = 0; n < NT; ++n) {
+                        float d[4];
+                        mma16816(d, a, pb[n][0], pb[n][1], 0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) acc[n][2 * x + h][j] = fmaf(vsc, d[j], acc[n][2 * x + h][j]);
-                        }
+                        for (int j = 0; j < 4; ++j) acc[n][2 * x + h][j] = fmaf(vsc, d[j], acc[n][2 * x + h][j]);
                     }
                 }
             }
+        };
+        for (int tile = 0; tile < tiles; ++tile, key += kTileKeys) {
+            blk = min((key + kTileKeys) >> gm.shift, last_blk);                 // the next step's
+            const float ksn = __ldg(ksp + blk), vsn = __ldg(vsp + blk);
+            if (!warp_wait_short(full + 8 * st, phase, err, &abort_flag)) return;
+            // a step whose keys every row sees needs no masks
+            if (key >= all_lo && key + 15 <= all_hi) step(std::false_type{});
+            else if (key < len && key + 16 > any_lo) step(std::true_type{});
             __syncwarp();
             if (lane == 0) mbar_arrive(empty + 8 * st);
             if (++st == X::kStages) st = 0, phase ^= 1;
@@ -774,7 +779,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 // two row groups of warps; more are blocks of 32, each of which reads the tiles.
 int job_rows(int group, int max_new) {
     const int rows = group * max_new;
-    return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : 32;
 }
 
 struct Space {
@@ -817,6 +822,7 @@ template <bool E4M3, int DH>
 cudaError_t by_rows(const Cache8AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, const Geom& gm, cudaStream_t st) {
     if (gm.block_rows == 8) return launch_part<E4M3, DH, 1, 1>(a, km, vm, gm, st);
     if (gm.block_rows == 16) return launch_part<E4M3, DH, 2, 1>(a, km, vm, gm, st);
+    if (gm.block_rows == 24) return launch_part<E4M3, DH, 1, 3>(a, km, vm, gm, st);
     return launch_part<E4M3, DH, 2, 2>(a, km, vm, gm, st);
 }
 
