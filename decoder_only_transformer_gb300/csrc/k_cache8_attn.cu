@@ -48,7 +48,7 @@ template <int DH, int NT, int RG>
 struct Ax {
     static constexpr int kTile = kTileKeys * DH;                       // bytes of K or V
     static constexpr int kCtas = RG > 1 ? 1 : NT == 2 || DH == 128 ? 2 : 3;   // per SM
-    static constexpr int kStages = (RG > 1 ? 8 : NT == 2 ? 4 : DH == 128 ? 5 : 3) * (DH == 128 ? 1 : DH == 64 ? 2 : 4);
+    static constexpr int kStages = (RG > 1 ? 8 : NT == 2 ? 4 : DH == 128 ? 5 : 2) * (DH == 128 ? 1 : DH == 64 ? 2 : 4);
     static constexpr int kRows = 8 * NT;                               // of a warp
     static constexpr int kThreads = 128 * RG + 32;
     static constexpr int kBuf = 4 * RG * kRows * DH * 4;               // the warps' o, to be added up
@@ -71,16 +71,17 @@ struct Geom {
     int window;
     int block_rows;           // rows of a job: 8, 16, 24 or 32
     int row_blocks;           // of max_new tokens
+    int whole;                // a CTA for each job of max_new tokens, none is cut
     float scale_log2;
     int64_t sq_t, sq_h, so_t, so_h;
 };
 
-// The job that a run begins in: its units [start, end) among all, its rows, and where they go.
-struct RunHead {
-    int start, end;               // end 0: no job
-    int total;                    // units of all jobs
+// What the join has to know of the boundary before a run: the pieces of the job that it cuts (0:
+// none), and where that job's rows go.
+struct __align__(16) Cut {
+    int pieces, share;            // which of the pieces - 1 boundaries this is
+    int run0, place0;             // the run of the first piece, and the place of its part
     int row0, rb, kvh, nrows;
-    int pad;
 };
 
 struct Seq {
@@ -99,7 +100,8 @@ __device__ __forceinline__ Seq get_seq(const int32_t* __restrict__ cu, const int
     const int first = gm.window > 0 ? max(0, s.len - s.n - gm.window + 1) : 0;
     s.tile0 = first / kTileKeys;
     s.tiles = max(1, (s.len + kTileKeys - 1) / kTileKeys - s.tile0);
-    s.blocks = (s.n * gm.G + gm.block_rows - 1) / gm.block_rows;
+    s.blocks = 0;
+    for (int r = s.n * gm.G; r > 0; r -= gm.block_rows) ++s.blocks;    // (no division: 128 / 32 at most)
     return s;
 }
 
@@ -114,6 +116,7 @@ __device__ __forceinline__ int run_of(int u, int total, int runs) {      // the 
 // Runs of at least kLeast units.  A job has kPiece units (what it costs beside its tiles), then one
 // for each tile; a run that ends among the first ones has none of the job's tiles.
 constexpr int kLeast = 3;
+constexpr int kWhole = 14;        // units of a job that is not worth cutting (see launch_part)
 __device__ __forceinline__ int run_count(int total, int ctas) { return max(1, min(ctas, total / kLeast)); }
 
 // The run's place among the jobs: sequence b, job j of it (kv head j / blocks, row block
@@ -236,7 +239,7 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
     k_cache8_part(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const __nv_bfloat16* __restrict__ q, const float* __restrict__ ks, const float* __restrict__ vs,
                   __nv_bfloat16* __restrict__ o, const int32_t* __restrict__ cu, const int32_t* __restrict__ lens,
-                  RunHead* __restrict__ heads, float2* __restrict__ part_ml, float4* __restrict__ part_o, const Geom gm,
+                  Cut* __restrict__ cuts, float2* __restrict__ part_ml, float4* __restrict__ part_o, const Geom gm,
                   int* err) {
     using X = Ax<DH, NT, RG>;
     constexpr int KW = DH >= 64 ? 4 : 2;                     // words of a load of K
@@ -272,102 +275,144 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
     uint32_t phase = 0;
     int sn = 0;                                              // segments so far
     pdl_wait();
-    pdl_trigger();
+    // (a join that is launched early sits on the SMs that are free first, many CTAs on few: 2 to 10 % slower)
+    if (gm.whole) pdl_trigger();
     if (warp == 4 * RG) {
         // ---------------------------------------------------------------- loads
-        // Tiles of the sequences, added up (by this warp alone; the others wait for its first segment).
-        int* cum = reinterpret_cast<int*>(sm + X::kCumOff);
-        int carry = 0;
-        if (lane == 0) cum[0] = 0;
-        for (int b0 = 0; b0 < gm.B; b0 += 32) {
-            int x = 0;
-            if (b0 + lane < gm.B) {
-                bool bad;
-                const Seq s = get_seq(cu, lens, gm, b0 + lane, bad);
-                if (bad && blockIdx.x == 0) raise_error(err, TFM_EINVAL);
-                x = (s.tiles + X::kPiece) * s.blocks * gm.Hkv;
-            }
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, d);
-                if (lane >= d) x += y;
-            }
-            x += carry;
-            if (b0 + lane < gm.B) cum[b0 + lane + 1] = x;
-            carry = __shfl_sync(0xffffffffu, x, 31);
-        }
-        __syncwarp();
-        const int total = carry;
-        const int runs = run_count(total, gridDim.x);
         Walk w{0, 0, 0, 0};
-        if ((int)blockIdx.x < runs && total > 0) {
-            const int u0 = run_start(blockIdx.x, total, runs);
-            w.left = run_start(blockIdx.x + 1, total, runs) - u0;
-            int lo = 0, hi = gm.B;                           // cum[lo] <= u0 < cum[hi]
-            while (hi - lo > 1) {
-                const int step = (hi - lo + 31) / 32;
-                const int b = lo + lane * step;
-                const int last = 31 - __clz(__ballot_sync(0xffffffffu, b < hi && cum[b] <= u0) | 1u);
-                lo += last * step;
-                hi = min(hi, lo + step);
+        Seq s;
+        int total = 0, runs = 0, u = 0;                      // units of all jobs; this run's next one
+        bool bad = false;
+        if (gm.whole) {
+            const int per = gm.Hkv * gm.row_blocks, kvh = (int)blockIdx.x % per / gm.row_blocks, rb = (int)blockIdx.x % gm.row_blocks;
+            w.b = (int)blockIdx.x / per;
+            s = get_seq(cu, lens, gm, w.b, bad);
+            if (bad && lane == 0) raise_error(err, TFM_EINVAL);
+            w.j = kvh * s.blocks + rb;
+            if (rb < s.blocks) w.left = s.tiles + X::kPiece;
+        } else {
+            // Units of the sequences, added up (by this warp alone; the others wait for its first segment).
+            int* cum = reinterpret_cast<int*>(sm + X::kCumOff);
+            if (lane == 0) cum[0] = 0;
+            for (int b0 = 0; b0 < gm.B; b0 += 128) {
+                int x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {                // the loads of 128 sequences together
+                    const int b = b0 + 32 * i + lane;
+                    x[i] = 0;
+                    if (b < gm.B) {
+                        const Seq y = get_seq(cu, lens, gm, b, bad);
+                        if (bad && blockIdx.x == 0) raise_error(err, TFM_EINVAL);
+                        x[i] = (y.tiles + X::kPiece) * y.blocks * gm.Hkv;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (b0 + 32 * i >= gm.B) break;
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const int y = __shfl_up_sync(0xffffffffu, x[i], d);
+                        if (lane >= d) x[i] += y;
+                    }
+                    x[i] += total;
+                    if (b0 + 32 * i + lane < gm.B) cum[b0 + 32 * i + lane + 1] = x[i];
+                    total = __shfl_sync(0xffffffffu, x[i], 31);
+                }
             }
-            w.b = lo;
-            bool bad;
-            const Seq s = get_seq(cu, lens, gm, lo, bad);
-            const int units = s.tiles + X::kPiece, rb = (u0 - cum[lo]) / units % s.blocks;
-            w.j = (u0 - cum[lo]) / units;
-            w.t = (u0 - cum[lo]) % units;
-            if (lane == 0)
-                heads[blockIdx.x] = RunHead{u0 - w.t, u0 - w.t + units, total, s.row0, rb, w.j / s.blocks,
-                                            min(s.n * gm.G - rb * gm.block_rows, gm.block_rows), 0};
-        } else if (lane == 0) {
-            heads[blockIdx.x] = RunHead{0, 0, total, 0, 0, 0, 0, 0};
+            __syncwarp();
+            runs = run_count(total, gridDim.x);
+            if ((int)blockIdx.x < runs && total > 0) {
+                const int q = total / runs, r = total - q * runs;
+                u = (int)blockIdx.x * q + min((int)blockIdx.x, r);
+                w.left = q + ((int)blockIdx.x < r);
+                int lo = 0, hi = gm.B;                       // cum[lo] <= u < cum[hi]
+                while (hi - lo > 1) {
+                    const int step = (hi - lo + 31) / 32;
+                    const int b = lo + lane * step;
+                    const int last = 31 - __clz(__ballot_sync(0xffffffffu, b < hi && cum[b] <= u) | 1u);
+                    lo += last * step;
+                    hi = min(hi, lo + step);
+                }
+                w.b = lo;
+                s = get_seq(cu, lens, gm, lo, bad);
+                w.j = (u - cum[lo]) / (s.tiles + X::kPiece);
+                w.t = u - cum[lo] - w.j * (s.tiles + X::kPiece);
+            }
         }
+        const int* cum = reinterpret_cast<const int*>(sm + X::kCumOff);
         bool filled = false;                                 // every stage of the ring once
+        const int cut_units = w.t;                           // of the job that the run begins in: units before the run
         for (;; ++sn) {
             const int place = sn & 1;
             // the next segment with tiles
-            Seq s;
-            int t0 = 0, tiles = 0;
-            Walk at = w;
+            int t0 = 0, tiles = 0, j = 0, b = 0, first = 0;
             while (tiles <= 0 && w.left > 0) {
-                while (cum[w.b + 1] == cum[w.b]) ++w.b;      // a run ends before the jobs do
-                at = w;
-                bool bad;
-                s = get_seq(cu, lens, gm, w.b, bad);
+                if (w.j == s.blocks * gm.Hkv) {
+                    do ++w.b;
+                    while (cum[w.b + 1] == cum[w.b]);        // a run ends before the jobs do
+                    s = get_seq(cu, lens, gm, w.b, bad);
+                    w.j = 0;
+                }
                 const int units = min(s.tiles + X::kPiece - w.t, w.left);
                 t0 = max(w.t - X::kPiece, 0);
                 tiles = w.t + units - X::kPiece - t0;
+                first = u - w.t + X::kPiece;                 // the unit of the job's first tile
+                j = w.j;
+                b = w.b;
                 w.left -= units;
+                u += units;
                 w.t = 0;                                     // whatever comes next is another job
-                if (++w.j == s.blocks * gm.Hkv) w.j = 0, ++w.b;
+                ++w.j;
             }
             if (sn >= 2 && !warp_wait(qempty + 8 * place, (sn >> 1) + 1 & 1, err, &abort_flag)) return;
             if (tiles <= 0) {
                 if (lane == 0) {
                     segs[place].tiles = 0;
                     mbar_arrive(qfull + 8 * place);
+                    if (sn == 0 && !gm.whole) cuts[blockIdx.x].pieces = 0;
                 }
                 return;
             }
-            const int kvh = at.j / s.blocks, rb = at.j % s.blocks, bh = at.b * gm.Hkv + kvh;
+            const int kvh = s.blocks == 1 ? j : j / s.blocks, rb = j - kvh * s.blocks, bh = b * gm.Hkv + kvh;
             const int nrows = min(s.n * gm.G - rb * gm.block_rows, gm.block_rows);
             int row = bh * gm.max_seq + (s.tile0 + t0) * kTileKeys;
+            int done = 0;
             if (lane == 0) {
+                if (sn == 0) {                               // the first tiles before anything else
+                    for (; done < min(tiles, X::kStages); ++done, row += kTileKeys) {
+                        mbar_arrive_expect_tx(full + 8 * done, 2 * X::kTile);
+                        tma_load_2d(sbase + done * 2 * X::kTile, &kmap, 0, row, full + 8 * done);
+                        tma_load_2d(sbase + done * 2 * X::kTile + X::kTile, &vmap, 0, row, full + 8 * done);
+                    }
+                    st = done;
+                    if (st == X::kStages) st = 0, phase = 1, filled = true;
+                }
                 segs[place] = Seg{tiles, (s.tile0 + t0) * kTileKeys, s.len, s.n, s.row0, bh, kvh, rb, nrows,
                                   tiles == s.tiles ? -1 : (int)blockIdx.x * 2 + (sn > 0)};
                 mbar_arrive_expect_tx(qfull + 8 * place, nrows * DH * 2);
             }
             __syncwarp();
             if (lane < nrows) {
-                const int rr = rb * gm.block_rows + lane;
+                const int rr = rb * gm.block_rows + lane, tok = rr / gm.G;
                 bulk_load(sbase + X::kQOff + place * X::kQ + lane * DH * 2,
-                          q + ((int64_t)s.row0 + rr / gm.G) * gm.sq_t + (int64_t)(kvh * gm.G + rr % gm.G) * gm.sq_h, DH * 2,
+                          q + ((int64_t)s.row0 + tok) * gm.sq_t + (int64_t)(kvh * gm.G + rr - tok * gm.G) * gm.sq_h, DH * 2,
                           qfull + 8 * place);
+            }
+            if (sn == 0 && lane == 0 && !gm.whole) {
+                // the boundary before this run cuts the job if some of its tiles lie before it
+                Cut c{0, 0, 0, 0, s.row0, rb, kvh, nrows};
+                if (cut_units > X::kPiece) {
+                    const int end = first + s.tiles;
+                    c.run0 = run_of(first, total, runs);
+                    c.pieces = run_of(end - 1, total, runs) - c.run0 + 1;
+                    c.share = (int)blockIdx.x - c.run0 - 1;
+                    c.place0 = 2 * c.run0 + (run_start(c.run0, total, runs) < first - X::kPiece);
+                }
+                cuts[blockIdx.x] = c;
             }
             bool ok = true;
             if (lane == 0)
-                for (int i = 0; i < tiles; ++i, row += kTileKeys) {
+                for (; done < tiles; ++done, row += kTileKeys) {
                     if (filled && !mbar_wait(empty + 8 * st, phase ^ 1, err, &abort_flag)) {
                         ok = false;
                         break;
@@ -681,30 +726,28 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
 }
 
 // Joins the pieces of the jobs that runs cut.  A job of P pieces has P - 1 boundaries of runs inside
-// it; CTA i looks at the boundary before run i + 1 and takes its share of that job's rows, in
+// it; CTA i takes that before run i + 1 and with it a share of the job's rows, in
 // float4s, kJoin of them at least.  The pieces are taken by the groups of threads in turn and
 // added in an order that depends on their number alone.
 constexpr int kJoin = 8, kJoinThreads = 256;
 template <int DH>
 __global__ void __launch_bounds__(kJoinThreads)
-    k_cache8_join(const RunHead* __restrict__ heads, const float2* __restrict__ part_ml, const float4* __restrict__ part_o,
-                  __nv_bfloat16* __restrict__ o, const Geom gm, int ctas, int piece_units) {
+    k_cache8_join(const Cut* __restrict__ cuts, const float2* __restrict__ part_ml, const float4* __restrict__ part_o,
+                  __nv_bfloat16* __restrict__ o, const Geom gm) {
     constexpr int F = DH / 4;
     __shared__ float4 sum_o[kJoinThreads];
     __shared__ float2 sum_ml[kJoinThreads];
     pdl_wait();
     pdl_trigger();
-    const int i = (int)blockIdx.x + 1, tid = threadIdx.x;
-    const RunHead h = heads[i];
-    if (h.end == 0) return;
-    const int runs = run_count(h.total, ctas), first = h.start + piece_units;        // the unit of the first tile
-    if (run_start(i, h.total, runs) <= first) return;        // no tiles of the job before the boundary
-    const int ra = run_of(first, h.total, runs), pieces = run_of(h.end - 1, h.total, runs) - ra + 1;
-    const int first_piece = 2 * ra + (run_start(ra, h.total, runs) < h.start);
-    const int all = h.nrows * F;
+    const int tid = threadIdx.x;
+    const int4* at4 = reinterpret_cast<const int4*>(cuts + blockIdx.x + 1);
+    const int4 c0 = __ldcg(at4), c1 = __ldcg(at4 + 1);
+    const Cut h{c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+    if (h.pieces == 0) return;
+    const int pieces = h.pieces, all = h.nrows * F;
     const int shares = (pieces - 1) * (int)gridDim.y;
-    const int share = max(kJoin, (all + shares - 1) / shares);
-    const int e0 = ((i - ra - 1) * (int)gridDim.y + (int)blockIdx.y) * share, e1 = min(all, e0 + share);
+    const int share = max(kJoin, shares == 1 ? all : (all + shares - 1) / shares);
+    const int e0 = (h.share * (int)gridDim.y + (int)blockIdx.y) * share, e1 = min(all, e0 + share);
     // entries side by side, a power of two of them; the other threads share the pieces
     int width = kJoin;
     while (width < share && width < kJoinThreads) width <<= 1;
@@ -723,7 +766,7 @@ __global__ void __launch_bounds__(kJoinThreads)
                 x[k] = make_float2(-3.402823466e38f, 0.0f);
                 y[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 if (p < pieces) {
-                    const int64_t pr = (int64_t)(p == 0 ? first_piece : 2 * (ra + p)) * gm.block_rows + r;
+                    const int64_t pr = (int64_t)(p == 0 ? h.place0 : 2 * (h.run0 + p)) * gm.block_rows + r;
                     x[k] = part_ml[pr];
                     y[k] = part_o[pr * F + f];
                 }
@@ -783,20 +826,20 @@ int job_rows(int group, int max_new) {
 }
 
 struct Space {
-    size_t heads, ml, o, bytes;
+    size_t cuts, ml, o, bytes;
 };
 Space space(int rows, int dh) {
     Space s;
     const size_t runs = kMaxRuns;
-    s.heads = 0;
-    s.ml = s.heads + runs * sizeof(RunHead);
+    s.cuts = 0;
+    s.ml = s.cuts + runs * sizeof(Cut);
     s.o = s.ml + 2 * runs * rows * sizeof(float2);
     s.bytes = s.o + 2 * runs * rows * dh * sizeof(float);
     return s;
 }
 
 template <bool E4M3, int DH, int NT, int RG>
-cudaError_t launch_part(const Cache8AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, const Geom& gm, cudaStream_t st) {
+cudaError_t launch_part(const Cache8AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, Geom gm, cudaStream_t st) {
     using X = Ax<DH, NT, RG>;
     static std::atomic<uint64_t> done{0};
     const int smem = X::kBase + 4 * (a.B + 1);
@@ -806,16 +849,21 @@ cudaError_t launch_part(const Cache8AttnArgs& a, const CUtensorMap& km, const CU
     const int ctas = sm_count() * X::kCtas < kMaxRuns ? sm_count() * X::kCtas : kMaxRuns;
     char* ws = static_cast<char*>(a.ws);
     const Space sp = space(gm.block_rows, DH);
-    RunHead* heads = reinterpret_cast<RunHead*>(ws + sp.heads);
+    Cut* cuts = reinterpret_cast<Cut*>(ws + sp.cuts);
     float2* ml = reinterpret_cast<float2*>(ws + sp.ml);
     float4* po = reinterpret_cast<float4*>(ws + sp.o);
-    e = launch_pdl(k_cache8_part<E4M3, DH, NT, RG>, dim3(ctas), dim3(X::kThreads), smem, st, km, vm,
-                   static_cast<const __nv_bfloat16*>(a.q), a.ks, a.vs, static_cast<__nv_bfloat16*>(a.o), a.cu, a.lens, heads,
+    // A few tiles more in a row are faster than a second kernel: where no job can have more than kWhole
+    // units and each can have a CTA of its own, none is cut.
+    const int64_t jobs = (int64_t)a.B * a.Hkv * gm.row_blocks;
+    const int keys = a.window > 0 && a.window + a.max_new < a.max_seq ? a.window + a.max_new : a.max_seq;
+    gm.whole = jobs <= ctas && (keys + kTileKeys - 2) / kTileKeys + 1 + X::kPiece <= kWhole;
+    e = launch_pdl(k_cache8_part<E4M3, DH, NT, RG>, dim3(gm.whole ? (unsigned)jobs : ctas), dim3(X::kThreads), smem, st, km, vm,
+                   static_cast<const __nv_bfloat16*>(a.q), a.ks, a.vs, static_cast<__nv_bfloat16*>(a.o), a.cu, a.lens, cuts,
                    ml, po, gm, device_error_word());
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || gm.whole) return e;
     return launch_pdl(k_cache8_join<DH>, dim3(ctas - 1, gm.block_rows / 8), dim3(kJoinThreads), 0, st,
-                      static_cast<const RunHead*>(heads), static_cast<const float2*>(ml), static_cast<const float4*>(po),
-                      static_cast<__nv_bfloat16*>(a.o), gm, ctas, X::kPiece);
+                      static_cast<const Cut*>(cuts), static_cast<const float2*>(ml), static_cast<const float4*>(po),
+                      static_cast<__nv_bfloat16*>(a.o), gm);
 }
 
 template <bool E4M3, int DH>
