@@ -68,6 +68,8 @@ tfm_status cache_call(bool read, const void* k, const void* v, void* k_codes, vo
     tfm_status st = check_cache(B, T, Hkv, max_seq, dh, block, codes, cu_seqlens != nullptr);
     if (st != TFM_OK) return st;
     if (mode != TFM_FP32 && mode != TFM_BF16) return fail(TFM_EINVAL, "bad mode");
+    if (((int64_t)T / block + 2 * B) * 2 * Hkv >= (int64_t)1 << 31)
+        return fail(TFM_EINVAL, "(T / block + 2 B) * 2 Hkv must be below 2^31");
     tfm::Cache8Args a{};
     static const char* const names[2] = {"k", "v"};
     const int heads[2] = {Hkv, Hkv};

@@ -43,7 +43,8 @@ __device__ __forceinline__ SeqRows seq_rows(const int32_t* __restrict__ cu, cons
 // The code of x / s (s > 0), the nearest, ties to even, as 64 bits decide it: the quotient
 // of two fp32 numbers is never within 2^-53 of a border between two codes unless it lies
 // on it, so its rounding to fp64 decides as the quotient itself would.  NaN gives 0,
-// infinities the largest code.  Slow: for extreme scales and rows with such values only.
+// infinities the largest code.  Slow: for extreme scales and
+// units with such values only.
 template <bool E4M3>
 static __device__ __noinline__ uint32_t code_exact(float x, float s) {
     if (x != x) return 0;
@@ -81,40 +82,29 @@ __device__ __forceinline__ float settled(float x, float s, float r) {
     return copysignf(a, x);
 }
 
-// Four codes of x[0..4) / s in a word, from x r; where that is too near a border to
-// decide, `open` is set and the word is not to be used.
+// Four codes of x[0..4) / s in a word, for s between 2^-100 and 2^100.  With r = 1 / s rounded, the
+// quotient lies between x r (1 - 2^-22) and x r (1 + 2^-22); where both round to the same code that
+// is the code.  Otherwise (one in some ten thousand) `open` is set and the word is not to be used.
 template <bool E4M3>
-__device__ __forceinline__ uint32_t codes4(const float* x, float r, bool& open) {
-    if constexpr (E4M3) {
-        uint32_t w[2];
+__device__ __forceinline__ uint32_t codes4(const float* x, float r_lo, float r_hi, bool& open) {
+    uint32_t w[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float y0 = x[2 * h] * r, y1 = x[2 * h + 1] * r;
+    for (int k = 0; k < 2; ++k) {
+        const float r = k ? r_hi : r_lo;
+        if constexpr (E4M3) {
+            asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
+                "mov.b32 %0, {a, b};\n\t}"
+                : "=r"(w[k]) : "f"(x[0] * r), "f"(x[1] * r), "f"(x[2] * r), "f"(x[3] * r));
+        } else {
+            // the last bits of x r + 1.5 2^23, rounded once, are the integer
+            uint32_t u[4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float y = j ? y1 : y0;
-                // normal codes drop 20 mantissa bits, half of their step is 0x80000; below
-                // 2^-6 the step is that of the subnormals: left to the exact form
-                const uint32_t u = __float_as_uint(y);
-                open = open || ((u & 0xFFFFFu) - 0x7FFF8u) <= 16u || (fabsf(y) < 0.0156251f && y != 0.0f);
-            }
-            asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n\tcvt.u32.u16 %0, t;\n\t}"
-                : "=r"(w[h]) : "f"(y0), "f"(y1));
+            for (int j = 0; j < 4; ++j) u[j] = __float_as_uint(fmaf(x[j], r, 12582912.0f));
+            w[k] = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
         }
-        return w[0] | w[1] << 16;
-    } else {
-        uint32_t u[4];
-        float far = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float y = x[j] * r;
-            const float t = y + 12582912.0f;                   // 1.5 2^23: the sum's last bits are the integer
-            far = fmaxf(far, fabsf(y - (t - 12582912.0f)));
-            u[j] = __float_as_uint(t);
-        }
-        open = open || far > 0.49995f;                         // |y| <= 128, off by 2^-22 of it at most
-        return __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
     }
+    open = open || w[0] != w[1];
+    return w[0];
 }
 
 // One code of a quotient that fp32 holds on the right side of every border.

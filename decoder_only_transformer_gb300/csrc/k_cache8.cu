@@ -10,11 +10,14 @@
 //
 // Read: value = code * scale, rounded once.
 //
-// Both are bound by memory, one pass: a CTA holds its unit's rows in registers between the
-// maximum and the codes.  16-byte loads of the rows, 8-byte stores of codes (a warp
-// covers whole 32-byte sectors).  The unit of CTA u is found without a scan: block j of
+// Both are bound by memory, one pass: the warps of a unit (one for 2048 elements) hold its rows in
+// registers between the maximum and the codes; 16-byte loads of the rows, 8-byte stores
+// of codes (a warp covers whole 32-byte sectors).  The instructions per element count too (at the
+// full bandwidth an SM has ~10 a clock-sector to spend): magnitudes of bf16 rows are compared in
+// pairs, as integers; a code is found by rounding x / s from below and from above (codes4).
+// The unit of a warp is found without a scan: block j of
 // sequence b has the number cu[b] / block + 2 b + j, which leaves room for a partly filled
-// block at either end.
+// block at either end.  Neighbouring warps take neighbouring heads, whose rows lie side by side.
 #include "cache8.cuh"
 
 namespace tfm {
@@ -28,6 +31,8 @@ struct Geom8 {
     int per;                       // rows per sequence without offsets
     int per_units;                 // units per sequence without offsets
     int shift;                     // log2(block)
+    int units;                     // of a kv head's keys
+    int warps;                     // of a unit
     int64_t s[4];                  // k token, k head, v token, v head
 };
 
@@ -65,6 +70,7 @@ __device__ __forceinline__ void check_rows(const int32_t* __restrict__ cu, const
     if (bad) raise_error(err, TFM_EINVAL);
 }
 
+// NVEC vectors of 8 elements of a unit's rows.
 template <typename T, int NVEC>
 struct Rows8;
 template <int NVEC>
@@ -75,6 +81,18 @@ struct Rows8<__nv_bfloat16, NVEC> {
     __device__ __forceinline__ void get(int i, float* x) const {
         x[0] = bf16_lo(w[i].x), x[1] = bf16_hi(w[i].x), x[2] = bf16_lo(w[i].y), x[3] = bf16_hi(w[i].y);
         x[4] = bf16_lo(w[i].z), x[5] = bf16_hi(w[i].z), x[6] = bf16_lo(w[i].w), x[7] = bf16_hi(w[i].w);
+    }
+    // the largest magnitude as the integer that its bits are (those that are not finite beyond all others)
+    __device__ __forceinline__ float top() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < NVEC; ++i) {
+            m = __vmaxu2(m, w[i].x & 0x7FFF7FFFu);
+            m = __vmaxu2(m, w[i].y & 0x7FFF7FFFu);
+            m = __vmaxu2(m, w[i].z & 0x7FFF7FFFu);
+            m = __vmaxu2(m, w[i].w & 0x7FFF7FFFu);
+        }
+        return __uint_as_float(max(m >> 16, m & 0xFFFFu) << 16);
     }
 };
 template <int NVEC>
@@ -92,65 +110,103 @@ struct Rows8<float, NVEC> {
             x[4 * j + 2] = __uint_as_float(w[2 * i + j].z), x[4 * j + 3] = __uint_as_float(w[2 * i + j].w);
         }
     }
+    __device__ __forceinline__ float top() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 2 * NVEC; ++i) {
+            m = max(max(m, w[i].x & 0x7FFFFFFFu), w[i].y & 0x7FFFFFFFu);
+            m = max(max(m, w[i].z & 0x7FFFFFFFu), w[i].w & 0x7FFFFFFFu);
+        }
+        return __uint_as_float(m);
+    }
 };
 
-// NVEC vectors of 8 elements per thread cover a unit.
+// A warp's unit: block `blk` of positions [p0, p0 + block) of kv head h of sequence b, of which
+// [lo, hi) are new; k or v.
+struct Unit {
+    int h, isv, b, blk, p0, lo, hi;
+    int64_t row0;                  // row of position 0 (positions before the new ones have none)
+    bool live;
+};
+__device__ __forceinline__ Unit find_unit(const int32_t* __restrict__ cu, const int32_t* __restrict__ lens, const Geom8& g,
+                                          int64_t flat) {
+    Unit n;
+    const int per = 2 * g.Hkv;                             // k's heads, then v's
+    const int u = (int)(flat / per), x = (int)(flat - (int64_t)u * per);
+    n.isv = x >= g.Hkv;
+    n.h = n.isv ? x - g.Hkv : x;
+    n.live = u < g.units;
+    if (!n.live) return n;
+    int j;
+    n.b = find_seq(cu, g, u, j);
+    const SeqRows s = seq_rows(cu, lens, n.b, g.per, g.T, g.max_seq);
+    const int start = s.len - s.n;
+    n.blk = (start >> g.shift) + j;
+    n.live = s.ok && s.n > 0 && s.n <= s.len && j >= 0 && n.blk <= ((s.len - 1) >> g.shift);
+    n.p0 = n.blk << g.shift;
+    n.lo = max(n.p0, start);
+    n.hi = min(n.p0 + (1 << g.shift), s.len);
+    n.row0 = (int64_t)s.row0 - start;
+    return n;
+}
+
+// W warps of a unit (g.warps of them) hold NVEC vectors of 8 elements a thread.
 template <typename T, bool E4M3, int DH, int NVEC>
 __global__ void __launch_bounds__(kMaxThreads8)
     k_cache8_write(const T* __restrict__ k, const T* __restrict__ v, uint8_t* __restrict__ kc, uint8_t* __restrict__ vc,
                    float* __restrict__ ks, float* __restrict__ vs, const int32_t* __restrict__ cu,
                    const int32_t* __restrict__ lens, const Geom8 g, int* err) {
     constexpr int kVR = DH / 8;                            // vectors of a row
-    const int h = blockIdx.y, isv = blockIdx.z, tid = threadIdx.x;
-    __shared__ float warp_max[kMaxThreads8 / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int slot = warp / g.warps, tid = threadIdx.x - slot * g.warps * 32, threads = g.warps * 32;
+    __shared__ float warp_top[kMaxThreads8 / 32];
     pdl_wait();
     pdl_trigger();
-    if (blockIdx.x == 0 && h == 0 && isv == 0) check_rows(cu, lens, g, err);
-    int j;
-    const int b = find_seq(cu, g, blockIdx.x, j);
-    const SeqRows s = seq_rows(cu, lens, b, g.per, g.T, g.max_seq);
-    if (!s.ok || s.n == 0 || s.n > s.len) return;
-    const int start = s.len - s.n;
-    const int blk = (start >> g.shift) + j;
-    if (j < 0 || blk > ((s.len - 1) >> g.shift)) return;
-    const int p0 = blk << g.shift;
-    const int lo = max(p0, start), hi = min(p0 + (1 << g.shift), s.len);
-    const T* src = (isv ? v : k) + (int64_t)h * g.s[isv ? 3 : 1];
-    const int64_t st = g.s[isv ? 2 : 0], row0 = (int64_t)s.row0 - start;
-    const int64_t bh = (int64_t)b * g.Hkv + h;
-    uint8_t* codes = (isv ? vc : kc) + (bh * g.max_seq + p0) * DH;
-    float* scale = (isv ? vs : ks) + bh * g.nblk + blk;
-    const bool held = lo > p0;                             // earlier positions of the sequence lie in the block
-    const float old = held ? *scale : 0.0f;
+    if (blockIdx.x == 0) check_rows(cu, lens, g, err);
+    const Unit n = find_unit(cu, lens, g, (int64_t)blockIdx.x * (kMaxThreads8 / threads) + slot);
+    if (!n.live) return;                                   // all warps of the unit
+    const T* src = (n.isv ? v : k) + (int64_t)n.h * g.s[n.isv ? 3 : 1];
+    const int64_t st = g.s[n.isv ? 2 : 0], bh = (int64_t)n.b * g.Hkv + n.h;
+    uint8_t* codes = (n.isv ? vc : kc) + (bh * g.max_seq + n.p0) * DH;
+    float* scale = (n.isv ? vs : ks) + bh * g.nblk + n.blk;
 
     Rows8<T, NVEC> x;
-    float top = 0.0f;
-    bool odd = false;                                      // something is not finite
 #pragma unroll
     for (int i = 0; i < NVEC; ++i) {
-        const int e = tid + i * (int)blockDim.x, p = p0 + e / kVR;
-        if (p >= lo && p < hi) x.load(i, src + (row0 + p) * st + e % kVR * 8);
+        const int e = tid + i * threads, p = n.p0 + e / kVR;
+        if (p >= n.lo && p < n.hi) x.load(i, src + (n.row0 + p) * st + e % kVR * 8);
         else x.clear(i);
     }
+    const bool held = n.lo > n.p0;                         // earlier positions of the sequence lie in the block
+    const float old = held ? *scale : 0.0f;
+    const auto unit_max = [&](float y) {
 #pragma unroll
-    for (int i = 0; i < NVEC; ++i) {
-        float f[8];
-        x.get(i, f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float a = fabsf(f[e]);
-            const bool fin = a < INFINITY;
-            odd = odd || !fin;
-            top = fmaxf(top, fin ? a : 0.0f);
+        for (int o = 16; o; o >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+        if (g.warps > 1) {
+            if (lane == 0) warp_top[warp] = y;
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(threads) : "memory");
+            for (int w = 0; w < g.warps; ++w) y = fmaxf(y, warp_top[slot * g.warps + w]);
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(threads) : "memory");
         }
+        return y;
+    };
+    // (a NaN is passed on as an infinity: fmaxf would drop it)
+    float top = x.top();
+    top = unit_max(top < INFINITY ? top : INFINITY);
+    const bool odd = !(top < INFINITY);                    // something is not finite: the largest that is
+    if (odd) {
+        if (tid == 0) raise_error(err, TFM_EINVAL);
+        top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NVEC; ++i) {
+            float f[8];
+            x.get(i, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (fabsf(f[e]) < INFINITY) top = fmaxf(top, fabsf(f[e]));
+        }
+        top = unit_max(top);
     }
-    odd = __syncthreads_or(odd);
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if ((tid & 31) == 0) warp_max[tid >> 5] = top;
-    __syncthreads();
-    for (int w = 0; w < (int)blockDim.x >> 5; ++w) top = fmaxf(top, warp_max[w]);
-    if (odd && tid == 0) raise_error(err, TFM_EINVAL);
-
     const float need = top > 0.0f ? fmaxf(__fdiv_rn(top, code_top<E4M3>()), 0x1p-126f) : 0.0f;
     float sc = old > 0.0f ? old : need;
     int up = 0;
@@ -162,81 +218,99 @@ __global__ void __launch_bounds__(kMaxThreads8)
     if (!(sc > 0.0f)) sc = 0.0f;
     if (up) {
         const float down = ldexpf(1.0f, -up);
-        for (int e = tid; e < (lo - p0) * kVR; e += blockDim.x) {
+        for (int e = tid; e < (n.lo - n.p0) * kVR; e += threads) {
             uint2* at = reinterpret_cast<uint2*>(codes) + e;
             const uint2 w = *at;
-            uint32_t n[2] = {0, 0};
+            uint32_t c[2] = {0, 0};
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float y = code_value<E4M3>((i < 4 ? w.x : w.y) >> (8 * (i & 3))) * down;
-                n[i >> 2] |= code_of<E4M3>(y) << (8 * (i & 3));
+                c[i >> 2] |= code_of<E4M3>(y) << (8 * (i & 3));
             }
-            *at = make_uint2(n[0], n[1]);
+            *at = make_uint2(c[0], c[1]);
         }
     }
     const bool plain = !odd && sc >= 0x1p-100f && sc <= 0x1p100f;
     const float r = plain ? __frcp_rn(sc) : 0.0f;
+    const float r_lo = r * (1.0f - 0x1p-22f), r_hi = r * (1.0f + 0x1p-22f);
 #pragma unroll
     for (int i = 0; i < NVEC; ++i) {
-        const int e = tid + i * (int)blockDim.x, p = p0 + e / kVR;
-        if (p < lo || p >= hi) continue;
+        const int e = tid + i * threads, p = n.p0 + e / kVR;
+        if (p < n.lo || p >= n.hi) continue;
         float f[8];
         x.get(i, f);
         bool open = !plain;
         uint2 w;
-        w.x = codes4<E4M3>(f, r, open);
-        w.y = codes4<E4M3>(f + 4, r, open);
+        w.x = codes4<E4M3>(f, r_lo, r_hi, open);
+        w.y = codes4<E4M3>(f + 4, r_lo, r_hi, open);
         if (open) {
-            uint32_t n[2] = {0, 0};
+            uint32_t c[2] = {0, 0};
             if (plain) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) n[c >> 2] |= code_of<E4M3>(settled<E4M3>(f[c], sc, r)) << (8 * (c & 3));
+                for (int j = 0; j < 8; ++j) c[j >> 2] |= code_of<E4M3>(settled<E4M3>(f[j], sc, r)) << (8 * (j & 3));
             } else if (sc > 0.0f) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) n[c >> 2] |= code_exact<E4M3>(f[c], sc) << (8 * (c & 3));
+                for (int j = 0; j < 8; ++j) c[j >> 2] |= code_exact<E4M3>(f[j], sc) << (8 * (j & 3));
             }
-            w = make_uint2(n[0], n[1]);
+            w = make_uint2(c[0], c[1]);
         }
         reinterpret_cast<uint2*>(codes)[e] = w;
     }
     if (tid == 0) *scale = sc;
 }
 
+// The values of 8 codes.
 template <bool E4M3>
 __device__ __forceinline__ void values8(uint2 w, float sc, float* f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = code_value<E4M3>((i < 4 ? w.x : w.y) >> (8 * (i & 3))) * sc;
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t c = h ? w.y : w.x;
+        if constexpr (E4M3) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const __half2_raw y = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(i ? c >> 16 : c & 0xFFFFu), __NV_E4M3);
+                const float2 z = __half22float2(__half2(y));
+                f[4 * h + 2 * i] = z.x * sc;
+                f[4 * h + 2 * i + 1] = z.y * sc;
+            }
+        } else {
+            // the byte, its sign bit turned over, as the last one of 2^23 + (c + 128)
+            const uint32_t b = c ^ 0x80808080u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[4 * h + i] = (__uint_as_float(__byte_perm(b, 0x4B000000u, 0x7440 + i)) - 8388736.0f) * sc;
+        }
+    }
 }
 
-template <typename T, bool E4M3, int DH>
+template <typename T, bool E4M3, int DH, int NVEC>
 __global__ void __launch_bounds__(kMaxThreads8)
     k_cache8_read(T* __restrict__ k, T* __restrict__ v, const uint8_t* __restrict__ kc, const uint8_t* __restrict__ vc,
                   const float* __restrict__ ks, const float* __restrict__ vs, const int32_t* __restrict__ cu,
                   const int32_t* __restrict__ lens, const Geom8 g, int* err) {
     constexpr int kVR = DH / 8;
-    const int h = blockIdx.y, isv = blockIdx.z, tid = threadIdx.x;
+    const int slot = (threadIdx.x >> 5) / g.warps, tid = threadIdx.x - slot * g.warps * 32, threads = g.warps * 32;
     pdl_wait();
     pdl_trigger();
-    if (blockIdx.x == 0 && h == 0 && isv == 0) check_rows(cu, lens, g, err);
-    int j;
-    const int b = find_seq(cu, g, blockIdx.x, j);
-    const SeqRows s = seq_rows(cu, lens, b, g.per, g.T, g.max_seq);
-    if (!s.ok || s.n == 0 || s.n > s.len) return;
-    const int start = s.len - s.n;
-    const int blk = (start >> g.shift) + j;
-    if (j < 0 || blk > ((s.len - 1) >> g.shift)) return;
-    const int p0 = blk << g.shift;
-    const int lo = max(p0, start), hi = min(p0 + (1 << g.shift), s.len);
-    T* dst = (isv ? v : k) + (int64_t)h * g.s[isv ? 3 : 1];
-    const int64_t st = g.s[isv ? 2 : 0], row0 = (int64_t)s.row0 - start;
-    const int64_t bh = (int64_t)b * g.Hkv + h;
-    const uint2* codes = reinterpret_cast<const uint2*>((isv ? vc : kc) + (bh * g.max_seq + p0) * DH);
-    const float sc = __ldg((isv ? vs : ks) + bh * g.nblk + blk);
-    for (int e = (lo - p0) * kVR + tid; e < (hi - p0) * kVR; e += blockDim.x) {
-        const uint2 w = __ldg(codes + e);
+    if (blockIdx.x == 0) check_rows(cu, lens, g, err);
+    const Unit n = find_unit(cu, lens, g, (int64_t)blockIdx.x * (kMaxThreads8 / threads) + slot);
+    if (!n.live) return;
+    T* dst = (n.isv ? v : k) + (int64_t)n.h * g.s[n.isv ? 3 : 1];
+    const int64_t st = g.s[n.isv ? 2 : 0], bh = (int64_t)n.b * g.Hkv + n.h;
+    const uint2* codes = reinterpret_cast<const uint2*>((n.isv ? vc : kc) + (bh * g.max_seq + n.p0) * DH);
+    const float sc = __ldg((n.isv ? vs : ks) + bh * g.nblk + n.blk);
+    uint2 w[NVEC];
+#pragma unroll
+    for (int i = 0; i < NVEC; ++i) {
+        const int e = tid + i * threads, p = n.p0 + e / kVR;
+        if (p >= n.lo && p < n.hi) w[i] = __ldg(codes + e);
+    }
+#pragma unroll
+    for (int i = 0; i < NVEC; ++i) {
+        const int e = tid + i * threads, p = n.p0 + e / kVR;
+        if (p < n.lo || p >= n.hi) continue;
         float f[8];
-        values8<E4M3>(w, sc, f);
-        T* at = dst + (row0 + p0 + e / kVR) * st + e % kVR * 8;
+        values8<E4M3>(w[i], sc, f);
+        T* at = dst + (n.row0 + p) * st + e % kVR * 8;
         if constexpr (sizeof(T) == 2) {
             *reinterpret_cast<uint4*>(at) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
                                                        pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
@@ -257,49 +331,36 @@ Geom8 geom8(const Cache8Args& a) {
     g.nblk = (a.max_seq + a.block - 1) >> g.shift;
     g.per = a.cu ? 0 : a.T / a.B;
     g.per_units = a.cu ? 0 : (g.per + a.block - 2) / a.block + 1;      // n positions touch at most so many blocks
+    g.units = a.cu ? (a.T >> g.shift) + 2 * a.B : a.B * g.per_units;
+    // a warp holds up to 8 vectors a thread: 1 to 8 warps a unit
+    const int vecs = a.block * a.dh / 8;
+    g.warps = vecs > 256 ? vecs / 256 : 1;
     for (int i = 0; i < 4; ++i) g.s[i] = a.strides[i];
     return g;
 }
 
-dim3 grid8(const Cache8Args& a, const Geom8& g) {
-    const int64_t units = a.cu ? (int64_t)(a.T >> g.shift) + 2 * a.B : (int64_t)a.B * g.per_units;
-    return dim3((unsigned)units, a.Hkv, 2);
-}
-
-template <typename T, bool E4M3, int DH>
-cudaError_t write_t(const Cache8Args& a, cudaStream_t st) {
+template <bool READ, typename T, bool E4M3, int DH, int NVEC>
+cudaError_t launch8(const Cache8Args& a, cudaStream_t st) {
     const Geom8 g = geom8(a);
-    const int vecs = a.block * DH / 8;                     // 64 .. 2048
-    const int threads = vecs < kMaxThreads8 ? vecs : kMaxThreads8;
-    auto go = [&](auto kernel) {
-        return launch_pdl(kernel, grid8(a, g), dim3(threads), 0, st, static_cast<const T*>(a.k), static_cast<const T*>(a.v),
-                          a.kc, a.vc, a.ks, a.vs, a.cu, a.lens, g, device_error_word());
-    };
-    switch (vecs / threads) {
-        case 1: return go(k_cache8_write<T, E4M3, DH, 1>);
-        case 2: return go(k_cache8_write<T, E4M3, DH, 2>);
-        case 4: return go(k_cache8_write<T, E4M3, DH, 4>);
-        default: return go(k_cache8_write<T, E4M3, DH, 8>);
-    }
-}
-
-template <typename T, bool E4M3, int DH>
-cudaError_t read_t(const Cache8Args& a, cudaStream_t st) {
-    const Geom8 g = geom8(a);
-    const int vecs = a.block * DH / 8;
-    const int threads = vecs < kMaxThreads8 ? vecs : kMaxThreads8;
-    return launch_pdl(k_cache8_read<T, E4M3, DH>, grid8(a, g), dim3(threads), 0, st,
-                      static_cast<T*>(const_cast<void*>(a.k)), static_cast<T*>(const_cast<void*>(a.v)), a.kc, a.vc, a.ks,
-                      a.vs, a.cu, a.lens, g, device_error_word());
+    const int per_cta = kMaxThreads8 / (32 * g.warps);
+    const unsigned ctas = (unsigned)(((int64_t)g.units * 2 * a.Hkv + per_cta - 1) / per_cta);
+    if constexpr (READ)
+        return launch_pdl(k_cache8_read<T, E4M3, DH, NVEC>, dim3(ctas), dim3(kMaxThreads8), 0, st,
+                          static_cast<T*>(const_cast<void*>(a.k)), static_cast<T*>(const_cast<void*>(a.v)), a.kc, a.vc, a.ks,
+                          a.vs, a.cu, a.lens, g, device_error_word());
+    else
+        return launch_pdl(k_cache8_write<T, E4M3, DH, NVEC>, dim3(ctas), dim3(kMaxThreads8), 0, st,
+                          static_cast<const T*>(a.k), static_cast<const T*>(a.v), a.kc, a.vc, a.ks, a.vs, a.cu, a.lens, g,
+                          device_error_word());
 }
 
 template <bool READ, typename T, bool E4M3>
 cudaError_t by_dh(const Cache8Args& a, cudaStream_t st) {
-    switch (a.dh) {
-        case 32: return READ ? read_t<T, E4M3, 32>(a, st) : write_t<T, E4M3, 32>(a, st);
-        case 64: return READ ? read_t<T, E4M3, 64>(a, st) : write_t<T, E4M3, 64>(a, st);
-        default: return READ ? read_t<T, E4M3, 128>(a, st) : write_t<T, E4M3, 128>(a, st);
-    }
+    const int vecs = a.block * a.dh / 8;
+    if (a.dh == 32) return vecs == 64 ? launch8<READ, T, E4M3, 32, 2>(a, st) : vecs == 128 ? launch8<READ, T, E4M3, 32, 4>(a, st)
+                                                                                         : launch8<READ, T, E4M3, 32, 8>(a, st);
+    if (a.dh == 64) return vecs == 128 ? launch8<READ, T, E4M3, 64, 4>(a, st) : launch8<READ, T, E4M3, 64, 8>(a, st);
+    return launch8<READ, T, E4M3, 128, 8>(a, st);
 }
 
 template <bool READ>

@@ -606,7 +606,8 @@ tfm_status tfm_rope_rows(const void* q, const void* k, void* q_out, void* k_out,
  * So do offsets that decrease or leave [0, T], lens[b] outside [0, max_seq] and more rows than
  * lens[b]: nothing is then written for that sequence (offsets of others that are not in
  * order included), and nothing outside the buffers is touched.
- * Rows 16-byte aligned, codes 16-byte, scales and lengths 4-byte.  B = 0 or T = 0 returns at once.
+ * Rows 16-byte aligned, codes 16-byte, scales and lengths 4-byte; (T / block + 2 B) * 2 Hkv below
+ * 2^31.  B = 0 or T = 0 returns at once.
  * Calls that write the same cache must be ordered.  Capturable in a CUDA graph. */
 tfm_status tfm_cache8_write(const void* k, const void* v, void* k_codes, void* v_codes, float* k_scales,
                             float* v_scales, const int32_t* cu_seqlens, const int32_t* lens, int32_t B,

@@ -103,6 +103,7 @@ CACHE = [
 @pytest.mark.parametrize("kw,status", CACHE + [
     (dict(mode=7), E), (dict(k=None), E), (dict(v=None), E), (dict(k=P(264)), E), (dict(v=P(258)), E),
     (dict(strides=_but(ROWS, 0, 63)), E), (dict(strides=_but(ROWS, 1, 68)), E), (dict(strides=_but(ROWS, 2, 1 << 39)), E),
+    (dict(B=1, Hkv=4096, max_seq=1, T=1 << 22), E), (dict(B=1, Hkv=4096, max_seq=1, T=(1 << 22) - 64, k=None), E),   # units
     (dict(strides=_but(ROWS, 3, 0)), E), (dict(strides=_but(ROWS, 1, 66), mode=F32), E),
 ])
 def test_write_and_read_refusals(lib, call, kw, status):
