@@ -82,36 +82,51 @@ __device__ __forceinline__ float settled(float x, float s, float r) {
     return copysignf(a, x);
 }
 
-// Four codes of x[0..4) / s in a word, for s between 2^-100 and 2^100.  With r = 1 / s rounded, the
-// quotient lies between x r (1 - 2^-22) and x r (1 + 2^-22); where both round to the same code that
-// is the code.  Otherwise (one in some ten thousand) `open` is set and the word is not to be used.
-template <bool E4M3>
-__device__ __forceinline__ uint32_t codes4(const float* x, float r_lo, float r_hi, bool& open) {
-    uint32_t w[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const float r = k ? r_hi : r_lo;
-        if constexpr (E4M3) {
-            asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
-                "mov.b32 %0, {a, b};\n\t}"
-                : "=r"(w[k]) : "f"(x[0] * r), "f"(x[1] * r), "f"(x[2] * r), "f"(x[3] * r));
-        } else {
-            // the last bits of x r + 1.5 2^23, rounded once, are the integer
-            uint32_t u[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) u[j] = __float_as_uint(fmaf(x[j], r, 12582912.0f));
-            w[k] = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
-        }
-    }
-    open = open || w[0] != w[1];
-    return w[0];
-}
-
 // One code of a quotient that fp32 holds on the right side of every border.
 template <bool E4M3>
 __device__ __forceinline__ uint32_t code_of(float y) {
     if constexpr (E4M3) return (uint32_t)__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
     else return (uint32_t)__float2int_rn(y) & 255u;
+}
+
+// The codes of x0 .. x3 in `w`, of which those in the bytes of `open` are still to be decided.
+template <bool E4M3>
+static __device__ __noinline__ uint32_t decide(uint32_t w, uint32_t open, float x0, float x1, float x2, float x3, float s,
+                                               float r) {
+    while (open) {
+        const int at = (__ffs(open) - 1) & 24;
+        const float x = at & 16 ? (at & 8 ? x3 : x2) : (at & 8 ? x1 : x0);
+        const uint32_t byte = 255u << at;
+        w = (w & ~byte) | code_of<E4M3>(settled<E4M3>(x, s, r)) << at;
+        open &= ~byte;
+    }
+    return w;
+}
+
+// Four codes of x[0..4) / s in a word, for s between 2^-100 and 2^100.  With r = 1 / s rounded, the
+// quotient lies between x r (1 - 2^-22) and x r (1 + 2^-22); where both round to the same code that
+// is the code.  Otherwise its side of the border is looked at: rare for fp32 rows, but a quotient of two
+// bf16 numbers lies on a border, or would if s were not rounded, as often as once in a hundred.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t codes4(const float* x, float s, float r, float r_lo, float r_hi) {
+    uint32_t w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float f = k ? r_hi : r_lo;
+        if constexpr (E4M3) {
+            asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
+                "mov.b32 %0, {a, b};\n\t}"
+                : "=r"(w[k]) : "f"(x[0] * f), "f"(x[1] * f), "f"(x[2] * f), "f"(x[3] * f));
+        } else {
+            // the last bits of x r + 1.5 2^23, rounded once, are the integer
+            uint32_t u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j] = __float_as_uint(fmaf(x[j], f, 12582912.0f));
+            w[k] = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+        }
+    }
+    if (w[0] != w[1]) w[0] = decide<E4M3>(w[0], w[0] ^ w[1], x[0], x[1], x[2], x[3], s, r);
+    return w[0];
 }
 
 template <bool E4M3>

@@ -239,20 +239,17 @@ __global__ void __launch_bounds__(kMaxThreads8)
         if (p < n.lo || p >= n.hi) continue;
         float f[8];
         x.get(i, f);
-        bool open = !plain;
-        uint2 w;
-        w.x = codes4<E4M3>(f, r_lo, r_hi, open);
-        w.y = codes4<E4M3>(f + 4, r_lo, r_hi, open);
-        if (open) {
-            uint32_t c[2] = {0, 0};
-            if (plain) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) c[j >> 2] |= code_of<E4M3>(settled<E4M3>(f[j], sc, r)) << (8 * (j & 3));
-            } else if (sc > 0.0f) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) c[j >> 2] |= code_exact<E4M3>(f[j], sc) << (8 * (j & 3));
+        uint2 w = make_uint2(0, 0);
+        if (plain) {
+            w.x = codes4<E4M3>(f, sc, r, r_lo, r_hi);
+            w.y = codes4<E4M3>(f + 4, sc, r, r_lo, r_hi);
+        } else if (sc > 0.0f) {
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t c = code_exact<E4M3>(f[j], sc) << (8 * (j & 3));
+                if (j < 4) w.x |= c;
+                else w.y |= c;
             }
-            w = make_uint2(c[0], c[1]);
         }
         reinterpret_cast<uint2*>(codes)[e] = w;
     }
