@@ -103,16 +103,13 @@ static __device__ __noinline__ uint32_t decide(uint32_t w, uint32_t open, float 
     return w;
 }
 
-// Four codes of x[0..4) / s in a word, for s between 2^-100 and 2^100.  With r = 1 / s rounded, the
-// quotient lies between x r (1 - 2^-22) and x r (1 + 2^-22); where both round to the same code that
-// is the code.  Otherwise its side of the border is looked at: rare for fp32 rows, but a quotient of two
-// bf16 numbers lies on a border, or would if s were not rounded, as often as once in a hundred.
+// Four codes of x[0..4) r in a word, for the two reciprocals r1 and r2.
 template <bool E4M3>
-__device__ __forceinline__ uint32_t codes4(const float* x, float s, float r, float r_lo, float r_hi) {
+__device__ __forceinline__ uint2 codes4(const float* x, float r1, float r2) {
     uint32_t w[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const float f = k ? r_hi : r_lo;
+        const float f = k ? r2 : r1;
         if constexpr (E4M3) {
             asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
                 "mov.b32 %0, {a, b};\n\t}"
@@ -125,8 +122,46 @@ __device__ __forceinline__ uint32_t codes4(const float* x, float s, float r, flo
             w[k] = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
         }
     }
-    if (w[0] != w[1]) w[0] = decide<E4M3>(w[0], w[0] ^ w[1], x[0], x[1], x[2], x[3], s, r);
-    return w[0];
+    return make_uint2(w[0], w[1]);
+}
+
+// How the codes of a unit's rows are decided, for scales s between 2^-100 and 2^100.  With r = 1 / s
+// rounded, x / s lies between x r (1 - 2^-22) and x r (1 + 2^-22).
+//
+// bf16 rows, s = A / top rounded to fp32 for a bf16 number A (which every scale is that bf16 rows
+// made): x top / A is a quotient of integers below 2^17 times a power of two, so that it lies on a border between
+// two codes or more than 2^-17 of itself away from it, and borders are frequent.  x / s is x top / A times
+// (1 + d), d the rounding of s (below 2^-23): quotients on a border are moved all to one side of it,
+// which d's sign gives, the others to none.  So x r (1 -+ 2^-22) rounds to the code; and if d = 0 the
+// two differ exactly where x / s lies on a border, and the even one is the code.
+// Otherwise (fp32 rows, foreign scales) `sure` is 0, and codes that differ are looked at (decide).
+struct Recip {
+    float s, r, r1, r2;
+    bool sure;
+};
+template <bool E4M3>
+__device__ __forceinline__ Recip recip(float s, bool bf16_rows) {
+    Recip c;
+    c.s = s;
+    c.r = __frcp_rn(s);
+    c.r1 = c.r * (1.0f - 0x1p-22f);
+    c.r2 = c.r * (1.0f + 0x1p-22f);
+    const float top = code_top<E4M3>();
+    const float A = __bfloat162float(__float2bfloat16_rn(s * top));
+    c.sure = bf16_rows && __fdiv_rn(A, top) == s;
+    if (c.sure) {
+        const float d = fmaf(s, top, -A);
+        if (d > 0.0f) c.r2 = c.r1;
+        if (d < 0.0f) c.r1 = c.r2;
+    }
+    return c;
+}
+template <bool E4M3, bool SURE>
+__device__ __forceinline__ uint32_t codes_of4(const float* x, const Recip& c) {
+    const uint2 w = codes4<E4M3>(x, c.r1, c.r2);
+    if (SURE) return w.x ^ ((w.x ^ w.y) & ((w.x & 0x01010101u) * 255u));  // where they differ, the even one
+    if (w.x != w.y) return decide<E4M3>(w.x, w.x ^ w.y, x[0], x[1], x[2], x[3], c.s, c.r);
+    return w.x;
 }
 
 template <bool E4M3>

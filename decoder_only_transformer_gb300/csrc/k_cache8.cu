@@ -14,7 +14,7 @@
 // registers between the maximum and the codes; 16-byte loads of the rows, 8-byte stores
 // of codes (a warp covers whole 32-byte sectors).  The instructions per element count too (at the
 // full bandwidth an SM has ~10 a clock-sector to spend): magnitudes of bf16 rows are compared in
-// pairs, as integers; a code is found by rounding x / s from below and from above (codes4).
+// pairs, as integers; a code is found by rounding x / s from below and from above (codes_of4).
 // The unit of a warp is found without a scan: block j of
 // sequence b has the number cu[b] / block + 2 b + j, which leaves room for a partly filled
 // block at either end.  Neighbouring warps take neighbouring heads, whose rows lie side by side.
@@ -165,16 +165,19 @@ __global__ void __launch_bounds__(kMaxThreads8)
     if (blockIdx.x == 0) check_rows(cu, lens, g, err);
     const Unit n = find_unit(cu, lens, g, (int64_t)blockIdx.x * (kMaxThreads8 / threads) + slot);
     if (!n.live) return;                                   // all warps of the unit
-    const T* src = (n.isv ? v : k) + (int64_t)n.h * g.s[n.isv ? 3 : 1];
+    // vector i of this thread: position first + i step, the same columns
+    const int first = n.p0 + tid / kVR, step = threads / kVR;
+    const unsigned count = n.hi - n.lo;                    // new positions
     const int64_t st = g.s[n.isv ? 2 : 0], bh = (int64_t)n.b * g.Hkv + n.h;
+    const T* src = (n.isv ? v : k) + (int64_t)n.h * g.s[n.isv ? 3 : 1] + (n.row0 + first) * st + tid % kVR * 8;
     uint8_t* codes = (n.isv ? vc : kc) + (bh * g.max_seq + n.p0) * DH;
     float* scale = (n.isv ? vs : ks) + bh * g.nblk + n.blk;
 
     Rows8<T, NVEC> x;
+    const int64_t ahead = step * st;
 #pragma unroll
-    for (int i = 0; i < NVEC; ++i) {
-        const int e = tid + i * threads, p = n.p0 + e / kVR;
-        if (p >= n.lo && p < n.hi) x.load(i, src + (n.row0 + p) * st + e % kVR * 8);
+    for (int i = 0; i < NVEC; ++i, src += ahead) {
+        if ((unsigned)(first + i * step - n.lo) < count) x.load(i, src);
         else x.clear(i);
     }
     const bool held = n.lo > n.p0;                         // earlier positions of the sequence lie in the block
@@ -231,27 +234,28 @@ __global__ void __launch_bounds__(kMaxThreads8)
         }
     }
     const bool plain = !odd && sc >= 0x1p-100f && sc <= 0x1p100f;
-    const float r = plain ? __frcp_rn(sc) : 0.0f;
-    const float r_lo = r * (1.0f - 0x1p-22f), r_hi = r * (1.0f + 0x1p-22f);
+    const Recip rc = recip<E4M3>(plain ? sc : 1.0f, sizeof(T) == 2);
+    const auto store = [&](auto code8) {
 #pragma unroll
-    for (int i = 0; i < NVEC; ++i) {
-        const int e = tid + i * threads, p = n.p0 + e / kVR;
-        if (p < n.lo || p >= n.hi) continue;
-        float f[8];
-        x.get(i, f);
-        uint2 w = make_uint2(0, 0);
-        if (plain) {
-            w.x = codes4<E4M3>(f, sc, r, r_lo, r_hi);
-            w.y = codes4<E4M3>(f + 4, sc, r, r_lo, r_hi);
-        } else if (sc > 0.0f) {
-#pragma unroll 1
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t c = code_exact<E4M3>(f[j], sc) << (8 * (j & 3));
-                if (j < 4) w.x |= c;
-                else w.y |= c;
-            }
+        for (int i = 0; i < NVEC; ++i) {
+            if ((unsigned)(first + i * step - n.lo) >= count) continue;
+            float f[8];
+            x.get(i, f);
+            reinterpret_cast<uint2*>(codes)[tid + i * threads] = code8(f);
         }
-        reinterpret_cast<uint2*>(codes)[e] = w;
+    };
+    if (sizeof(T) == 2 && plain && rc.sure) {
+        store([&](const float* f) { return make_uint2(codes_of4<E4M3, true>(f, rc), codes_of4<E4M3, true>(f + 4, rc)); });
+    } else if (plain) {
+        store([&](const float* f) { return make_uint2(codes_of4<E4M3, false>(f, rc), codes_of4<E4M3, false>(f + 4, rc)); });
+    } else {
+        store([&](const float* f) {
+            uint32_t w[2] = {0, 0};
+            if (sc > 0.0f)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j >> 2] |= code_exact<E4M3>(f[j], sc) << (8 * (j & 3));
+            return make_uint2(w[0], w[1]);
+        });
     }
     if (tid == 0) *scale = sc;
 }
@@ -291,23 +295,23 @@ __global__ void __launch_bounds__(kMaxThreads8)
     if (blockIdx.x == 0) check_rows(cu, lens, g, err);
     const Unit n = find_unit(cu, lens, g, (int64_t)blockIdx.x * (kMaxThreads8 / threads) + slot);
     if (!n.live) return;
-    T* dst = (n.isv ? v : k) + (int64_t)n.h * g.s[n.isv ? 3 : 1];
+    const int first = n.p0 + tid / kVR, step = threads / kVR;
+    const unsigned count = n.hi - n.lo;
     const int64_t st = g.s[n.isv ? 2 : 0], bh = (int64_t)n.b * g.Hkv + n.h;
+    T* at = (n.isv ? v : k) + (int64_t)n.h * g.s[n.isv ? 3 : 1] + (n.row0 + first) * st + tid % kVR * 8;
     const uint2* codes = reinterpret_cast<const uint2*>((n.isv ? vc : kc) + (bh * g.max_seq + n.p0) * DH);
     const float sc = __ldg((n.isv ? vs : ks) + bh * g.nblk + n.blk);
     uint2 w[NVEC];
 #pragma unroll
     for (int i = 0; i < NVEC; ++i) {
-        const int e = tid + i * threads, p = n.p0 + e / kVR;
-        if (p >= n.lo && p < n.hi) w[i] = __ldg(codes + e);
+        if ((unsigned)(first + i * step - n.lo) < count) w[i] = __ldg(codes + tid + i * threads);
     }
+    const int64_t ahead = step * st;
 #pragma unroll
-    for (int i = 0; i < NVEC; ++i) {
-        const int e = tid + i * threads, p = n.p0 + e / kVR;
-        if (p < n.lo || p >= n.hi) continue;
+    for (int i = 0; i < NVEC; ++i, at += ahead) {
+        if ((unsigned)(first + i * step - n.lo) >= count) continue;
         float f[8];
         values8<E4M3>(w[i], sc, f);
-        T* at = dst + (n.row0 + p) * st + e % kVR * 8;
         if constexpr (sizeof(T) == 2) {
             *reinterpret_cast<uint4*>(at) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
                                                        pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
