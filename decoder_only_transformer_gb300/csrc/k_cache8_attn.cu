@@ -44,20 +44,28 @@ namespace {
 constexpr int kTileKeys = 64;
 constexpr int kMaxRuns = 152 * 3;                 // CTAs at most; the workspace has places for them
 
-template <int DH, int NT, int RG>
+// NT: groups of 8 rows that a warp holds.  From two on, registers are what is short: the four
+// computing warps are a warpgroup that takes over most of the registers of a second one, of
+// which one warp loads (128 a thread at launch, 200 and 56 after).
+template <int DH, int NT>
 struct Ax {
     static constexpr int kTile = kTileKeys * DH;                       // bytes of K or V
-    static constexpr int kCtas = RG > 1 ? 1 : NT == 2 || DH == 128 ? 2 : 3;   // per SM
-    static constexpr int kStages = (RG > 1 ? 8 : NT == 2 ? 4 : DH == 128 ? 5 : 2) * (DH == 128 ? 1 : DH == 64 ? 2 : 4);
-    static constexpr int kRows = 8 * NT;                               // of a warp
-    static constexpr int kThreads = 128 * RG + 32;
-    static constexpr int kBuf = 4 * RG * kRows * DH * 4;               // the warps' o, to be added up
+    static constexpr bool kSplit = NT > 1;
+    static constexpr int kComputeRegs = NT == 4 ? 208 : 200, kLoadRegs = 256 - kComputeRegs;   // kSplit: of 2 x 128 at launch
+    static constexpr bool kSharedQ = NT > 2;                           // q's operands in shared memory
+    static constexpr int kCtas = NT > 1 || DH == 128 ? 2 : 3;          // per SM
+    static constexpr int kStages = (NT > 1 ? 4 : DH == 128 ? 5 : 2) * (DH == 128 ? 1 : DH == 64 ? 2 : 4);
+    static constexpr int kRows = 8 * NT;                               // of a job
+    static constexpr int kThreads = kSplit ? 256 : 160;
+    static constexpr int kBuf = 4 * 8 * DH * 4;                        // the warps' o of 8 rows, to be added up
     static constexpr int kBufOff = kStages * 2 * kTile;
-    static constexpr int kMlOff = kBufOff + kBuf;                      // float2 [RG][4][rows]
-    static constexpr int kQ = RG * kRows * DH * 2;                     // the job's rows of q, as they are
-    static constexpr int kQOff = kMlOff + RG * 4 * kRows * 8;          // two places
-    static constexpr int kBarOff = kQOff + 2 * kQ;                     // full, empty of the ring; of the places for q; of the buffers
-    static constexpr int kCumOff = kBarOff + 16 * kStages + 32 + 16 * RG;
+    static constexpr int kMlOff = kBufOff + kBuf;                      // float2 [4][8]
+    static constexpr int kQ = kRows * DH * 2;                          // the job's rows of q, as they are
+    static constexpr int kQOff = kMlOff + 4 * 8 * 8;                   // two places
+    static constexpr int kFragOff = kQOff + 2 * kQ;                    // q's operands
+    static constexpr int kRowOff = kFragOff + (kSharedQ ? kQ : 0);     // float4 [rows]: what belongs to a row
+    static constexpr int kBarOff = kRowOff + (kSharedQ ? 16 * kRows : 0);    // of the ring, the places for q, the buffer, the operands
+    static constexpr int kCumOff = kBarOff + 16 * kStages + 32 + 16 + 8;
     static constexpr int kBase = kCumOff + 1024;                       // + 4 (B + 1); the ring on a multiple of 1024
     // What a segment costs beside its tiles, in tiles: q, the first scores, the sum over the warps.
     static constexpr int kPiece = DH == 32 ? 5 : 3;
@@ -128,8 +136,8 @@ struct Walk {
 struct Seg {
     int tiles;                // none: the run is over
     int key;                  // first key
-    int len, n, row0;
-    int bh, kvh, rb;          // sequence and kv head, kv head, row block
+    int len, n;
+    int bh;                   // sequence and kv head
     int nrows;
     int piece;                // -1: the whole job; else where its part goes
 };
@@ -234,38 +242,41 @@ __device__ __forceinline__ int buf_at(int row, int f) {
     return row * (DH / 4) + (f ^ (DH == 128 ? t : DH == 64 ? (t & 1) | (t >> 1) << 2 : t << 1));
 }
 
-template <bool E4M3, int DH, int NT, int RG>
-__global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCtas)
+template <bool E4M3, int DH, int NT>
+__global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
     k_cache8_part(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const __nv_bfloat16* __restrict__ q, const float* __restrict__ ks, const float* __restrict__ vs,
                   __nv_bfloat16* __restrict__ o, const int32_t* __restrict__ cu, const int32_t* __restrict__ lens,
                   Cut* __restrict__ cuts, float2* __restrict__ part_ml, float4* __restrict__ part_o, const Geom gm,
                   int* err) {
-    using X = Ax<DH, NT, RG>;
+    using X = Ax<DH, NT>;
     constexpr int KW = DH >= 64 ? 4 : 2;                     // words of a load of K
     constexpr int KL = DH == 128 ? 2 : 1;                    // loads of K per key
     constexpr int VW = DH / 32;                              // words of a load of V, float4s of o of a lane and row
-    constexpr int R = X::kRows;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int abort_flag;
     __shared__ Seg segs[2];
+    __shared__ int64_t orow[2][8 * NT];                      // where a row of o lies,
+    __shared__ int seen[2][8 * NT];                          // and the last position that it sees
     const uint32_t raw_base = smem_u32(smem_raw);
     const uint32_t sbase = (raw_base + 1023u) & ~1023u;
     uint8_t* sm = smem_raw + (sbase - raw_base);
     const uint32_t full = sbase + X::kBarOff, empty = full + 8 * X::kStages;
-    const uint32_t qfull = empty + 8 * X::kStages, qempty = qfull + 16, bfull = qempty + 16, bempty = bfull + 8 * RG;
+    const uint32_t qfull = empty + 8 * X::kStages, qempty = qfull + 16, bfull = qempty + 16, bempty = bfull + 8, ffull = bempty + 8;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 128 * RG) {
+    if (tid == 128) {
         abort_flag = 0;
         for (int i = 0; i < X::kStages; ++i) {
             mbar_init(full + 8 * i, 1);
-            mbar_init(empty + 8 * i, 4 * RG);
+            mbar_init(empty + 8 * i, 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(qfull + 8 * i, 1);
-            mbar_init(qempty + 8 * i, 4 * RG);
+            mbar_init(qempty + 8 * i, 4);
         }
-        for (int i = 0; i < 2 * RG; ++i) mbar_init(bfull + 8 * i, 4);
+        mbar_init(bfull, 4);
+        mbar_init(bempty, 4);
+        mbar_init(ffull, 4);
         fence_mbar_init();
         tma_prefetch_desc(&kmap);
         tma_prefetch_desc(&vmap);
@@ -277,8 +288,10 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
     pdl_wait();
     // (a join that is launched early sits on the SMs that are free first, many CTAs on few: 2 to 10 % slower)
     if (gm.whole) pdl_trigger();
-    if (warp == 4 * RG) {
+    if (warp >= 4) {
         // ---------------------------------------------------------------- loads
+        if (X::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(X::kLoadRegs));
+        if (warp > 4) return;
         Walk w{0, 0, 0, 0};
         Seq s;
         int total = 0, runs = 0, u = 0;                      // units of all jobs; this run's next one
@@ -376,27 +389,32 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
             const int kvh = s.blocks == 1 ? j : j / s.blocks, rb = j - kvh * s.blocks, bh = b * gm.Hkv + kvh;
             const int nrows = min(s.n * gm.G - rb * gm.block_rows, gm.block_rows);
             int row = bh * gm.max_seq + (s.tile0 + t0) * kTileKeys;
-            int done = 0;
-            if (lane == 0) {
-                if (sn == 0) {                               // the first tiles before anything else
-                    for (; done < min(tiles, X::kStages); ++done, row += kTileKeys) {
-                        mbar_arrive_expect_tx(full + 8 * done, 2 * X::kTile);
-                        tma_load_2d(sbase + done * 2 * X::kTile, &kmap, 0, row, full + 8 * done);
-                        tma_load_2d(sbase + done * 2 * X::kTile + X::kTile, &vmap, 0, row, full + 8 * done);
-                    }
-                    st = done;
-                    if (st == X::kStages) st = 0, phase = 1, filled = true;
-                }
-                segs[place] = Seg{tiles, (s.tile0 + t0) * kTileKeys, s.len, s.n, s.row0, bh, kvh, rb, nrows,
-                                  tiles == s.tiles ? -1 : (int)blockIdx.x * 2 + (sn > 0)};
-                mbar_arrive_expect_tx(qfull + 8 * place, nrows * DH * 2);
+            int tok = 0, head = 0;
+            if (lane < X::kRows) {
+                const int rr = rb * gm.block_rows + lane;
+                tok = rr / gm.G;
+                head = kvh * gm.G + rr - tok * gm.G;
+                orow[place][lane] = ((int64_t)s.row0 + tok) * gm.so_t + (int64_t)head * gm.so_h;
+                seen[place][lane] = lane < nrows ? s.len - s.n + tok : s.len - 1;
             }
+            if (lane == 0)
+                segs[place] = Seg{tiles, (s.tile0 + t0) * kTileKeys, s.len, s.n, bh, nrows,
+                                  tiles == s.tiles ? -1 : (int)blockIdx.x * 2 + (sn > 0)};
             __syncwarp();
-            if (lane < nrows) {
-                const int rr = rb * gm.block_rows + lane, tok = rr / gm.G;
+            if (lane == 0) mbar_arrive_expect_tx(qfull + 8 * place, nrows * DH * 2);
+            __syncwarp();
+            if (lane < nrows)
                 bulk_load(sbase + X::kQOff + place * X::kQ + lane * DH * 2,
-                          q + ((int64_t)s.row0 + tok) * gm.sq_t + (int64_t)(kvh * gm.G + rr - tok * gm.G) * gm.sq_h, DH * 2,
-                          qfull + 8 * place);
+                          q + ((int64_t)s.row0 + tok) * gm.sq_t + (int64_t)head * gm.sq_h, DH * 2, qfull + 8 * place);
+            int done = 0;
+            if (sn == 0 && lane == 0) {                      // the ring is empty: no waits
+                for (; done < min(tiles, X::kStages); ++done, row += kTileKeys) {
+                    mbar_arrive_expect_tx(full + 8 * done, 2 * X::kTile);
+                    tma_load_2d(sbase + done * 2 * X::kTile, &kmap, 0, row, full + 8 * done);
+                    tma_load_2d(sbase + done * 2 * X::kTile + X::kTile, &vmap, 0, row, full + 8 * done);
+                }
+                st = done;
+                if (st == X::kStages) st = 0, phase = 1, filled = true;
             }
             if (sn == 0 && lane == 0 && !gm.whole) {
                 // the boundary before this run cuts the job if some of its tiles lie before it
@@ -426,7 +444,8 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
         }
     }
     // -------------------------------------------------------------------- rows
-    const int kw = warp & 3, rg = warp >> 2, g = lane >> 2, t = lane & 3;
+    if (X::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(X::kComputeRegs));
+    const int kw = warp, g = lane >> 2, t = lane & 3;
     // where this lane reads, inside a tile: keys of the step's second half are 8 rows further, the
     // second half of a K row of 128 bytes is 64 bytes away (both keep the swizzle)
     const int kr = kw * 16 + kappa<DH>(g);
@@ -437,14 +456,16 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
         const int r = kw * 16 + kappa<DH>(2 * t + i);
         voff[i] = X::kTile + r * DH + (DH == 128 ? (g ^ (r & 7)) * 16 : DH == 64 ? ((g >> 1) ^ ((r >> 1) & 3)) * 16 + (g & 1) * 8 : g * 4);
     }
-    float4* buf = reinterpret_cast<float4*>(sm + X::kBufOff) + rg * 4 * R * (DH / 4);
-    float2* ml = reinterpret_cast<float2*>(sm + X::kMlOff) + rg * 4 * R;
+    float4* buf = reinterpret_cast<float4*>(sm + X::kBufOff);
+    float2* ml = reinterpret_cast<float2*>(sm + X::kMlOff);
+    uint4* frag = reinterpret_cast<uint4*>(sm + X::kFragOff) + lane;          // [n][pair of words][lane]
+    float4* rowf = reinterpret_cast<float4*>(sm + X::kRowOff);
     for (;; ++sn) {
         if (!warp_wait(qfull + 8 * (sn & 1), sn >> 1 & 1, err, &abort_flag)) return;
         const Seg& s = segs[sn & 1];
-        const int tiles = s.tiles, len = s.len, news = s.n, rb = s.rb;
+        const int tiles = s.tiles, len = s.len, news = s.n;
         if (tiles == 0) return;
-        const int nrows = s.nrows - rg * R;                  // of this row group
+        const int nrows = s.nrows;
         const float* ksp = ks + (int64_t)s.bh * gm.nblk;
         const float* vsp = vs + (int64_t)s.bh * gm.nblk;
         int key = s.key + kw * 16;
@@ -453,15 +474,16 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
         float ksc = __ldg(ksp + blk), vsc = __ldg(vsp + blk);
         // q: row r of the job is token r / G, head r % G.  Lane (g, t) holds row 8 n + g, for the products, of
         // what belongs to the rows 8 n + 2 t and + 1, whose scores it gets, in the arrays [n][2].
-        uint32_t qb[NT][KL * KW][2];
-        float qinv[NT][2], qbias[NT][2];
-        int seen_hi[NT][2];                                  // the last position that a row sees
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int r = 8 * n + g;
+        // (kSharedQ: warp n prepares rows 8 n .. 8 n + 7 for all, in shared memory.)
+        constexpr int NQ = X::kSharedQ ? 1 : NT;
+        uint32_t qb[NQ][KL * KW][2];
+        float qinv[NQ][2], qbias[NQ][2];
+        int seen_hi[NQ][2];                                  // the last position that a row sees
+        const auto prepare = [&](int nn, uint32_t (&qb)[KL * KW][2], float (&qinv)[2], float (&qbias)[2], int (&seen_hi)[2]) {
+            const int r = 8 * nn + g;
             uint2 raw[KL * KW];
             if (r < nrows) {
-                const uint8_t* at = sm + X::kQOff + (sn & 1) * X::kQ + (rg * R + r) * DH * 2;
+                const uint8_t* at = sm + X::kQOff + (sn & 1) * X::kQ + r * DH * 2;
 #pragma unroll
                 for (int p = 0; p < KL; ++p) {
                     const uint4* a4 = reinterpret_cast<const uint4*>(at + p * 128 + t * (DH >= 64 ? 32 : 16));
@@ -494,8 +516,8 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
                 const float y2 = bf16_lo(raw[x].y) * mul, y3 = bf16_hi(raw[x].y) * mul;
                 const __half2 a = E4M3 ? __floats2half2_rn(y0, y1) : __floats2half2_rn(y0, y2);
                 const __half2 b = E4M3 ? __floats2half2_rn(y2, y3) : __floats2half2_rn(y1, y3);
-                qb[n][x][0] = *reinterpret_cast<const uint32_t*>(&a);
-                qb[n][x][1] = *reinterpret_cast<const uint32_t*>(&b);
+                qb[x][0] = *reinterpret_cast<const uint32_t*>(&a);
+                qb[x][1] = *reinterpret_cast<const uint32_t*>(&b);
                 const float2 fa = __half22float2(a), fb = __half22float2(b);
                 sum += (fa.x + fa.y) + (fb.x + fb.y);
             }
@@ -504,11 +526,28 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int from = (2 * t + j) * 4;            // a lane of that row
-                qinv[n][j] = __uint_as_float((uint32_t)__shfl_sync(0xffffffffu, e, from) << 23);
-                qbias[n][j] = __shfl_sync(0xffffffffu, sum, from) * -0x1p-17f;       // 128 of the codes' 2^-24
-                const int ro = 8 * n + 2 * t + j;
-                seen_hi[n][j] = ro < nrows ? len - news + (rb * gm.block_rows + rg * R + ro) / gm.G : len - 1;
+                qinv[j] = __uint_as_float((uint32_t)__shfl_sync(0xffffffffu, e, from) << 23);
+                qbias[j] = E4M3 ? 0.0f : __shfl_sync(0xffffffffu, sum, from) * -0x1p-17f;      // 128 of the codes' 2^-24
+                seen_hi[j] = seen[sn & 1][8 * nn + 2 * t + j];
             }
+        };
+        if constexpr (X::kSharedQ) {
+            if (kw < NT) {
+                prepare(kw, qb[0], qinv[0], qbias[0], seen_hi[0]);
+#pragma unroll
+                for (int y = 0; y < KL * KW; y += 2)
+                    frag[(kw * KL * KW + y) * 16] = make_uint4(qb[0][y][0], qb[0][y][1], qb[0][y + 1][0], qb[0][y + 1][1]);
+                if (g == 0)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        rowf[8 * kw + 2 * t + j] = make_float4(qinv[0][j], qbias[0][j], __int_as_float(seen_hi[0][j]), 0.0f);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ffull);
+            if (!warp_wait(ffull, sn & 1, err, &abort_flag)) return;
+        } else {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) prepare(n, qb[n], qinv[n], qbias[n], seen_hi[n]);
         }
         // acc[n][2 x + h]: rows 8 n + 2 t (elements 0, 2) and + 1 (1, 3), coordinates g DH / 8 + 4 x + 2 h (0, 1) and + 1
         float acc[NT][2 * VW][4];
@@ -536,21 +575,33 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
                 float c2[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // a second chain of sums: half the latency
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    c[n][0] = c[n][2] = E4M3 ? 0.0f : qbias[n][0];
-                    c[n][1] = c[n][3] = E4M3 ? 0.0f : qbias[n][1];
+                    float b0 = 0.0f, b1 = 0.0f;
+                    if constexpr (!E4M3) {
+                        if constexpr (X::kSharedQ) b0 = rowf[8 * n + 2 * t].y, b1 = rowf[8 * n + 2 * t + 1].y;
+                        else b0 = qbias[n][0], b1 = qbias[n][1];
+                    }
+                    c[n][0] = c[n][2] = b0;
+                    c[n][1] = c[n][3] = b1;
                 }
 #pragma unroll
                 for (int p = 0; p < KL; ++p)
 #pragma unroll
-                    for (int x = 0; x < KW; ++x) {
-                        uint32_t a[4];                    // keys g, g + 8
-                        key_halves<E4M3>(kd[0][p][x], a[0], a[2]);
-                        key_halves<E4M3>(kd[1][p][x], a[1], a[3]);
+                    for (int x = 0; x < KW; x += 2) {
+                        uint32_t a[2][4];                 // keys g, g + 8
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            key_halves<E4M3>(kd[0][p][x + z], a[z][0], a[z][2]);
+                            key_halves<E4M3>(kd[1][p][x + z], a[z][1], a[z][3]);
+                        }
                         const int y = p * KW + x;
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            float(&d)[4] = NT == 1 && (y & 1) ? c2 : c[n];
-                            mma16816(d, a, qb[n][y][0], qb[n][y][1], d[0], d[1], d[2], d[3]);
+                            uint4 b;
+                            if constexpr (X::kSharedQ) b = frag[(n * KL * KW + y) * 16];
+                            else b = make_uint4(qb[n][y][0], qb[n][y][1], qb[n][y + 1][0], qb[n][y + 1][1]);
+                            float(&d)[4] = NT == 1 ? c2 : c[n];
+                            mma16816(c[n], a[0], b.x, b.y, c[n][0], c[n][1], c[n][2], c[n][3]);
+                            mma16816(d, a[1], b.z, b.w, d[0], d[1], d[2], d[3]);
                         }
                     }
                 if (NT == 1)
@@ -564,12 +615,22 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float f = ksc * gm.scale_log2 * (E4M3 ? 0x1p-10f : 0x1p14f) * qinv[n][j];
+                    float inv;
+                    int hi = 0;
+                    if constexpr (X::kSharedQ) {
+                        const float4 w = rowf[8 * n + 2 * t + j];
+                        inv = w.x;
+                        hi = __float_as_int(w.z);
+                    } else {
+                        inv = qinv[n][j];
+                        hi = seen_hi[n][j];
+                    }
+                    const float f = ksc * gm.scale_log2 * (E4M3 ? 0x1p-10f : 0x1p14f) * inv;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         float& y = c[n][2 * i + j];
                         y *= f;
-                        if (EDGE && (p0 + 8 * i > seen_hi[n][j] || (gm.window > 0 && p0 + 8 * i <= seen_hi[n][j] - gm.window)))
+                        if (EDGE && (p0 + 8 * i > hi || (gm.window > 0 && p0 + 8 * i <= hi - gm.window)))
                             y = -INFINITY;
                     }
                     top[n][j] = fmaxf(c[n][j], c[n][2 + j]);
@@ -657,10 +718,11 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
             ksc = ksn;
             vsc = vsn;
         }
-        // The four warps' parts, added up.
-        if (sn > 0 && !warp_wait(bempty + 8 * rg, sn + 1 & 1, err, &abort_flag)) return;      // the last segment's have been read
+        // The four warps' parts, added up, 8 rows at a time.
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+            const int pass = sn * NT + n;
+            if (pass > 0 && !warp_wait(bempty, pass + 1 & 1, err, &abort_flag)) return;      // the last ones have been read
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
 #pragma unroll
@@ -668,7 +730,7 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
                     l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], d);
                     if (!E4M3) lv[n][j] += __shfl_xor_sync(0xffffffffu, lv[n][j], d);
                 }
-                const int r = 8 * n + 2 * t + j;
+                const int r = 2 * t + j;
 #pragma unroll
                 for (int x = 0; x < VW; ++x) {
                     float4 v = make_float4(acc[n][2 * x][j], acc[n][2 * x][2 + j], acc[n][2 * x + 1][j], acc[n][2 * x + 1][2 + j]);
@@ -676,52 +738,49 @@ __global__ void __launch_bounds__(Ax<DH, NT, RG>::kThreads, Ax<DH, NT, RG>::kCta
                         const float b = lv[n][j] * -128.0f;
                         v = make_float4(fmaf(v.x, 0x1p24f, b), fmaf(v.y, 0x1p24f, b), fmaf(v.z, 0x1p24f, b), fmaf(v.w, 0x1p24f, b));
                     }
-                    buf[kw * R * (DH / 4) + buf_at<DH>(r, g * VW + x)] = v;
+                    buf[kw * 8 * (DH / 4) + buf_at<DH>(r, g * VW + x)] = v;
                 }
-                if (g == 0) ml[kw * R + r] = make_float2(m[n][j], l[n][j]);
+                if (g == 0) ml[kw * 8 + r] = make_float2(m[n][j], l[n][j]);
             }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bfull + 8 * rg);
-        if (!warp_wait(bfull + 8 * rg, sn & 1, err, &abort_flag)) return;
-        const int lt = tid & 127;
-        for (int e = lt; e < R * (DH / 4); e += 128) {
-            const int r = e / (DH / 4), f = e % (DH / 4);
-            if (r >= nrows) break;
-            float2 x[4];
-            float top = -3.402823466e38f;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bfull);
+            if (!warp_wait(bfull, pass & 1, err, &abort_flag)) return;
+            for (int e = tid; e < 8 * (DH / 4); e += 128) {
+                const int r = e / (DH / 4), f = e % (DH / 4);
+                if (8 * n + r >= nrows) break;
+                float2 x[4];
+                float top = -3.402823466e38f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = ml[i * R + r];
-                top = fmaxf(top, x[i].x);
-            }
-            float sum = 0.0f;
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = ml[i * 8 + r];
+                    top = fmaxf(top, x[i].x);
+                }
+                float sum = 0.0f;
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float k = ex2(x[i].x - top);
-                const float4 y = buf[i * R * (DH / 4) + buf_at<DH>(r, f)];
-                sum = fmaf(k, x[i].y, sum);
-                v.x = fmaf(k, y.x, v.x);
-                v.y = fmaf(k, y.y, v.y);
-                v.z = fmaf(k, y.z, v.z);
-                v.w = fmaf(k, y.w, v.w);
+                for (int i = 0; i < 4; ++i) {
+                    const float k = ex2(x[i].x - top);
+                    const float4 y = buf[i * 8 * (DH / 4) + buf_at<DH>(r, f)];
+                    sum = fmaf(k, x[i].y, sum);
+                    v.x = fmaf(k, y.x, v.x);
+                    v.y = fmaf(k, y.y, v.y);
+                    v.z = fmaf(k, y.z, v.z);
+                    v.w = fmaf(k, y.w, v.w);
+                }
+                if (s.piece < 0) {
+                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    __nv_bfloat16* at = o + orow[sn & 1][8 * n + r] + f * 4;
+                    *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+                } else {
+                    const int64_t pr = (int64_t)s.piece * gm.block_rows + 8 * n + r;
+                    part_o[pr * (DH / 4) + f] = v;
+                    if (f == 0) part_ml[pr] = make_float2(top, sum);
+                }
             }
-            const int rr = rb * gm.block_rows + rg * R + r;
-            if (s.piece < 0) {
-                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                __nv_bfloat16* at = o + ((int64_t)s.row0 + rr / gm.G) * gm.so_t + (int64_t)(s.kvh * gm.G + rr % gm.G) * gm.so_h + f * 4;
-                *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
-            } else {
-                const int64_t pr = (int64_t)s.piece * gm.block_rows + rg * R + r;
-                part_o[pr * (DH / 4) + f] = v;
-                if (f == 0) part_ml[pr] = make_float2(top, sum);
-            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bempty);
         }
-        __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(bempty + 8 * rg);
-            mbar_arrive(qempty + 8 * (sn & 1));
-        }
+        if (lane == 0) mbar_arrive(qempty + 8 * (sn & 1));
     }
 }
 
@@ -818,8 +877,8 @@ __global__ void __launch_bounds__(kJoinThreads)
     }
 }
 
-// Rows of a job by the rows that max_new tokens of a kv head have: 8 or 16 in every warp, 32 in
-// two row groups of warps; more are blocks of 32, each of which reads the tiles.
+// Rows of a job by the rows that max_new tokens of a kv head have: all of up to 32; more are blocks
+// of 32, each of which reads the tiles.
 int job_rows(int group, int max_new) {
     const int rows = group * max_new;
     return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : 32;
@@ -838,14 +897,22 @@ Space space(int rows, int dh) {
     return s;
 }
 
-template <bool E4M3, int DH, int NT, int RG>
+template <bool E4M3, int DH, int NT>
 cudaError_t launch_part(const Cache8AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, Geom gm, cudaStream_t st) {
-    using X = Ax<DH, NT, RG>;
+    using X = Ax<DH, NT>;
     static std::atomic<uint64_t> done{0};
     const int smem = X::kBase + 4 * (a.B + 1);
     // sequences beyond those that leave room for kCtas have fewer CTAs per SM; 4096 still fit
-    cudaError_t e = allow_smem(done, k_cache8_part<E4M3, DH, NT, RG>, X::kBase + 4 * 4097);
+    cudaError_t e = allow_smem(done, k_cache8_part<E4M3, DH, NT>, X::kBase + 4 * 4097);
     if (e != cudaSuccess) return e;
+    if (X::kSplit) {
+        // the warps that take registers over would wait for ever if the launch had fewer than they count on
+        static const int regs = [] {
+            cudaFuncAttributes f;
+            return cudaFuncGetAttributes(&f, k_cache8_part<E4M3, DH, NT>) == cudaSuccess ? f.numRegs : 0;
+        }();
+        if (regs * 2 < X::kComputeRegs + X::kLoadRegs) return cudaErrorInvalidDeviceFunction;
+    }
     const int ctas = sm_count() * X::kCtas < kMaxRuns ? sm_count() * X::kCtas : kMaxRuns;
     char* ws = static_cast<char*>(a.ws);
     const Space sp = space(gm.block_rows, DH);
@@ -857,7 +924,7 @@ cudaError_t launch_part(const Cache8AttnArgs& a, const CUtensorMap& km, const CU
     const int64_t jobs = (int64_t)a.B * a.Hkv * gm.row_blocks;
     const int keys = a.window > 0 && a.window + a.max_new < a.max_seq ? a.window + a.max_new : a.max_seq;
     gm.whole = jobs <= ctas && (keys + kTileKeys - 2) / kTileKeys + 1 + X::kPiece <= kWhole;
-    e = launch_pdl(k_cache8_part<E4M3, DH, NT, RG>, dim3(gm.whole ? (unsigned)jobs : ctas), dim3(X::kThreads), smem, st, km, vm,
+    e = launch_pdl(k_cache8_part<E4M3, DH, NT>, dim3(gm.whole ? (unsigned)jobs : ctas), dim3(X::kThreads), smem, st, km, vm,
                    static_cast<const __nv_bfloat16*>(a.q), a.ks, a.vs, static_cast<__nv_bfloat16*>(a.o), a.cu, a.lens, cuts,
                    ml, po, gm, device_error_word());
     if (e != cudaSuccess || gm.whole) return e;
@@ -868,10 +935,12 @@ cudaError_t launch_part(const Cache8AttnArgs& a, const CUtensorMap& km, const CU
 
 template <bool E4M3, int DH>
 cudaError_t by_rows(const Cache8AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, const Geom& gm, cudaStream_t st) {
-    if (gm.block_rows == 8) return launch_part<E4M3, DH, 1, 1>(a, km, vm, gm, st);
-    if (gm.block_rows == 16) return launch_part<E4M3, DH, 2, 1>(a, km, vm, gm, st);
-    if (gm.block_rows == 24) return launch_part<E4M3, DH, 1, 3>(a, km, vm, gm, st);
-    return launch_part<E4M3, DH, 2, 2>(a, km, vm, gm, st);
+    switch (gm.block_rows) {
+        case 8: return launch_part<E4M3, DH, 1>(a, km, vm, gm, st);
+        case 16: return launch_part<E4M3, DH, 2>(a, km, vm, gm, st);
+        case 24: return launch_part<E4M3, DH, 3>(a, km, vm, gm, st);
+        default: return launch_part<E4M3, DH, 4>(a, km, vm, gm, st);
+    }
 }
 
 template <bool E4M3>
