@@ -148,6 +148,10 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {     // without an arrival
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1,
                                          float c2, float c3) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
@@ -389,19 +393,9 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
             const int kvh = s.blocks == 1 ? j : j / s.blocks, rb = j - kvh * s.blocks, bh = b * gm.Hkv + kvh;
             const int nrows = min(s.n * gm.G - rb * gm.block_rows, gm.block_rows);
             int row = bh * gm.max_seq + (s.tile0 + t0) * kTileKeys;
-            int tok = 0, head = 0;
-            if (lane < X::kRows) {
-                const int rr = rb * gm.block_rows + lane;
-                tok = rr / gm.G;
-                head = kvh * gm.G + rr - tok * gm.G;
-                orow[place][lane] = ((int64_t)s.row0 + tok) * gm.so_t + (int64_t)head * gm.so_h;
-                seen[place][lane] = lane < nrows ? s.len - s.n + tok : s.len - 1;
-            }
-            if (lane == 0)
-                segs[place] = Seg{tiles, (s.tile0 + t0) * kTileKeys, s.len, s.n, bh, nrows,
-                                  tiles == s.tiles ? -1 : (int)blockIdx.x * 2 + (sn > 0)};
-            __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(qfull + 8 * place, nrows * DH * 2);
+            // q first: it is needed first, and the first tiles are as much as memory gives in some microseconds
+            const int rr = rb * gm.block_rows + lane, tok = gm.G == 1 ? rr : rr / gm.G, head = kvh * gm.G + rr - tok * gm.G;
+            if (lane == 0) mbar_expect_tx(qfull + 8 * place, nrows * DH * 2);
             __syncwarp();
             if (lane < nrows)
                 bulk_load(sbase + X::kQOff + place * X::kQ + lane * DH * 2,
@@ -416,6 +410,15 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
                 st = done;
                 if (st == X::kStages) st = 0, phase = 1, filled = true;
             }
+            if (lane < X::kRows) {
+                orow[place][lane] = ((int64_t)s.row0 + tok) * gm.so_t + (int64_t)head * gm.so_h;
+                seen[place][lane] = lane < nrows ? s.len - s.n + tok : s.len - 1;
+            }
+            if (lane == 0)
+                segs[place] = Seg{tiles, (s.tile0 + t0) * kTileKeys, s.len, s.n, bh, nrows,
+                                  tiles == s.tiles ? -1 : (int)blockIdx.x * 2 + (sn > 0)};
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qfull + 8 * place);
             if (sn == 0 && lane == 0 && !gm.whole) {
                 // the boundary before this run cuts the job if some of its tiles lie before it
                 Cut c{0, 0, 0, 0, s.row0, rb, kvh, nrows};
