@@ -54,7 +54,7 @@ struct Ax {
     static constexpr int kComputeRegs = NT == 4 ? 208 : 200, kLoadRegs = 256 - kComputeRegs;   // kSplit: of 2 x 128 at launch
     static constexpr bool kSharedQ = NT > 2;                           // q's operands in shared memory
     static constexpr int kCtas = NT > 1 || DH == 128 ? 2 : 3;          // per SM
-    static constexpr int kStages = (NT > 1 ? 4 : DH == 128 ? 5 : 2) * (DH == 128 ? 1 : DH == 64 ? 2 : 4);
+    static constexpr int kStages = (NT > 1 ? 3 : DH == 128 ? 4 : 2) * (DH == 128 ? 1 : DH == 64 ? 2 : 4);
     static constexpr int kRows = 8 * NT;                               // of a job
     static constexpr int kThreads = kSplit ? 256 : 160;
     static constexpr int kBuf = 4 * 8 * DH * 4;                        // the warps' o of 8 rows, to be added up
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
                           q + ((int64_t)s.row0 + tok) * gm.sq_t + (int64_t)head * gm.sq_h, DH * 2, qfull + 8 * place);
             int done = 0;
             if (sn == 0 && lane == 0) {                      // the ring is empty: no waits
-                for (; done < min(tiles, X::kStages); ++done, row += kTileKeys) {
+                for (; done < min(tiles, 2); ++done, row += kTileKeys) {
                     mbar_arrive_expect_tx(full + 8 * done, 2 * X::kTile);
                     tma_load_2d(sbase + done * 2 * X::kTile, &kmap, 0, row, full + 8 * done);
                     tma_load_2d(sbase + done * 2 * X::kTile + X::kTile, &vmap, 0, row, full + 8 * done);
