@@ -79,7 +79,7 @@ struct Geom {
     int window;
     int block_rows;           // rows of a job: 8, 16, 24 or 32
     int row_blocks;           // of max_new tokens
-    int whole;                // a CTA for each job of max_new tokens, none is cut
+    int whole;                // no job is cut; 2: each of max_new tokens has a CTA of its own
     float scale_log2;
     int64_t sq_t, sq_h, so_t, so_h;
 };
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
         Seq s;
         int total = 0, runs = 0, u = 0;                      // units of all jobs; this run's next one
         bool bad = false;
-        if (gm.whole) {
+        if (gm.whole == 2) {
             const int per = gm.Hkv * gm.row_blocks, kvh = (int)blockIdx.x % per / gm.row_blocks, rb = (int)blockIdx.x % gm.row_blocks;
             w.b = (int)blockIdx.x / per;
             s = get_seq(cu, lens, gm, w.b, bad);
@@ -354,6 +354,13 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
                 s = get_seq(cu, lens, gm, lo, bad);
                 w.j = (u - cum[lo]) / (s.tiles + X::kPiece);
                 w.t = u - cum[lo] - w.j * (s.tiles + X::kPiece);
+                if (gm.whole && w.t > 0) {                   // a job belongs to the run that it begins in
+                    const int rest = s.tiles + X::kPiece - w.t;
+                    w.left -= rest;
+                    u += rest;
+                    w.t = 0;
+                    ++w.j;
+                }
             }
         }
         const int* cum = reinterpret_cast<const int*>(sm + X::kCumOff);
@@ -370,7 +377,7 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
                     s = get_seq(cu, lens, gm, w.b, bad);
                     w.j = 0;
                 }
-                const int units = min(s.tiles + X::kPiece - w.t, w.left);
+                const int units = gm.whole ? s.tiles + X::kPiece : min(s.tiles + X::kPiece - w.t, w.left);
                 t0 = max(w.t - X::kPiece, 0);
                 tiles = w.t + units - X::kPiece - t0;
                 first = u - w.t + X::kPiece;                 // the unit of the job's first tile
@@ -923,11 +930,11 @@ cudaError_t launch_part(const Cache8AttnArgs& a, const CUtensorMap& km, const CU
     float2* ml = reinterpret_cast<float2*>(ws + sp.ml);
     float4* po = reinterpret_cast<float4*>(ws + sp.o);
     // A few tiles more in a row are faster than a second kernel: where no job can have more than kWhole
-    // units and each can have a CTA of its own, none is cut.
+    // units, none is cut.
     const int64_t jobs = (int64_t)a.B * a.Hkv * gm.row_blocks;
     const int keys = a.window > 0 && a.window + a.max_new < a.max_seq ? a.window + a.max_new : a.max_seq;
-    gm.whole = jobs <= ctas && (keys + kTileKeys - 2) / kTileKeys + 1 + X::kPiece <= kWhole;
-    e = launch_pdl(k_cache8_part<E4M3, DH, NT>, dim3(gm.whole ? (unsigned)jobs : ctas), dim3(X::kThreads), smem, st, km, vm,
+    gm.whole = (keys + kTileKeys - 2) / kTileKeys + 1 + X::kPiece > kWhole ? 0 : jobs > ctas ? 1 : 2;
+    e = launch_pdl(k_cache8_part<E4M3, DH, NT>, dim3(gm.whole == 2 ? (unsigned)jobs : ctas), dim3(X::kThreads), smem, st, km, vm,
                    static_cast<const __nv_bfloat16*>(a.q), a.ks, a.vs, static_cast<__nv_bfloat16*>(a.o), a.cu, a.lens, cuts,
                    ml, po, gm, device_error_word());
     if (e != cudaSuccess || gm.whole) return e;
