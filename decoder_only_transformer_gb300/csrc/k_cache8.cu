@@ -163,8 +163,20 @@ __global__ void __launch_bounds__(kMaxThreads8)
     pdl_wait();
     pdl_trigger();
     if (blockIdx.x == 0) check_rows(cu, lens, g, err);
-    const Unit n = find_unit(cu, lens, g, (int64_t)blockIdx.x * (kMaxThreads8 / threads) + slot);
-    if (!n.live) return;                                   // all warps of the unit
+    Unit n;
+    if (g.warps == 1) {
+        n = find_unit(cu, lens, g, (int64_t)blockIdx.x * (kMaxThreads8 / threads) + slot);
+    } else {
+        // one warp looks, so that all of them come to the barriers or none
+        __shared__ Unit units[kMaxThreads8 / 64];
+        if (tid < 32) {
+            n = find_unit(cu, lens, g, (int64_t)blockIdx.x * (kMaxThreads8 / threads) + slot);
+            if (lane == 0) units[slot] = n;
+        }
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(threads) : "memory");
+        n = units[slot];
+    }
+    if (!n.live) return;
     // vector i of this thread: position first + i step, the same columns
     const int first = n.p0 + tid / kVR, step = threads / kVR;
     const unsigned count = n.hi - n.lo;                    // new positions

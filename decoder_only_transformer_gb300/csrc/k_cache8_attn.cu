@@ -28,11 +28,23 @@
 //     2^(x - m + 7), below 2^15 and so fp16 numbers; what is flushed to zero is below 2^-31
 //     of the largest weight.
 //
-// Tiles of 64 keys (K and V, by TMA, a ring of them filled by a warp of its own); the four
-// warps of a row group take 16 keys each and hold all of d_head.  All tiles of all
-// (sequence, kv head, row block) jobs lie end to end and are cut into equal runs, one per
-// resident CTA, whatever the lengths are; a run's first and last job may be pieces, whose
-// (max, sum, unnormalised o) a second kernel joins exactly, in a fixed order.
+// Tiles of 64 keys (K and V, by TMA, a ring of them filled by a warp of its own, which also hands over
+// the jobs and their rows of q); the four computing warps take 16 keys each and hold all of
+// d_head for up to 32 rows.  All tiles of all (sequence, kv head, row block) jobs lie end to end and are cut
+// into equal runs, one per resident CTA, whatever the lengths are; a run's first and last job may
+// be pieces, whose (max, sum, unnormalised o) a second kernel joins exactly, in a fixed
+// order.  Short caches are not cut, and need no second kernel.
+//
+// Measured (graph replays; GB/s of the bytes that count): 64 chats of up to 4096 positions, 16/4 x 128,
+// int8: 30.7 us, 4.4 TB/s; 131072 positions of one, e4m3: 28.5 us, 4.7 TB/s; 32 x 16 caches of 64
+// with a window of 1024: 20.5 us; up to 5 new tokens of 16 over up to 8192: 23.9 us; 4 chats under
+// 511: 6.2 us.  Of each but the last ~2 us pass until the first tile is asked for (lengths, runs, q),
+// ~2 until it is there, ~1.5 with the last sums, ~4 with the second kernel; in between memory is
+// nearly full for up to 8 rows, and a step's latency (~1500 cycles at 24 rows, two warps a
+// scheduler) counts for more.  Tried and slower: the values' scales in the weights' exponents (P V without
+// the fp32 additions: +1 to 2 us), the next step's scores ahead of this one's softmax (no
+// change), three row groups of warps with 8 rows each for 24 (24.6 for 23.9), runs and zeroed counters
+// from a kernel ahead, the last writer adding the pieces up (+3 to 6 us), deeper rings (+1).
 #include <type_traits>
 
 #include "cache8.cuh"
@@ -371,11 +383,13 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
             // the next segment with tiles
             int t0 = 0, tiles = 0, j = 0, b = 0, first = 0;
             while (tiles <= 0 && w.left > 0) {
-                if (w.j == s.blocks * gm.Hkv) {
+                if (w.j >= s.blocks * gm.Hkv) {
                     do ++w.b;
-                    while (cum[w.b + 1] == cum[w.b]);        // a run ends before the jobs do
+                    while (w.b < gm.B && cum[w.b + 1] == cum[w.b]);
+                    if (w.b >= gm.B) break;                  // (a run ends before the jobs do, while the lengths stay)
                     s = get_seq(cu, lens, gm, w.b, bad);
                     w.j = 0;
+                    if (s.blocks == 0) break;
                 }
                 const int units = gm.whole ? s.tiles + X::kPiece : min(s.tiles + X::kPiece - w.t, w.left);
                 t0 = max(w.t - X::kPiece, 0);
@@ -430,9 +444,10 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
                 // the boundary before this run cuts the job if some of its tiles lie before it
                 Cut c{0, 0, 0, 0, s.row0, rb, kvh, nrows};
                 if (cut_units > X::kPiece) {
-                    const int end = first + s.tiles;
+                    const int end = min(first + s.tiles, total);
                     c.run0 = run_of(first, total, runs);
                     c.pieces = run_of(end - 1, total, runs) - c.run0 + 1;
+                    if (c.pieces < 2) c.pieces = 0;
                     c.share = (int)blockIdx.x - c.run0 - 1;
                     c.place0 = 2 * c.run0 + (run_start(c.run0, total, runs) < first - X::kPiece);
                 }
@@ -917,11 +932,14 @@ cudaError_t launch_part(const Cache8AttnArgs& a, const CUtensorMap& km, const CU
     if (e != cudaSuccess) return e;
     if (X::kSplit) {
         // the warps that take registers over would wait for ever if the launch had fewer than they count on
-        static const int regs = [] {
+        static std::atomic<int> regs{0};
+        if (regs.load(std::memory_order_relaxed) == 0) {
             cudaFuncAttributes f;
-            return cudaFuncGetAttributes(&f, k_cache8_part<E4M3, DH, NT>) == cudaSuccess ? f.numRegs : 0;
-        }();
-        if (regs * 2 < X::kComputeRegs + X::kLoadRegs) return cudaErrorInvalidDeviceFunction;
+            e = cudaFuncGetAttributes(&f, k_cache8_part<E4M3, DH, NT>);
+            if (e != cudaSuccess) return e;
+            regs.store(f.numRegs, std::memory_order_relaxed);
+        }
+        if (regs.load(std::memory_order_relaxed) * 2 < X::kComputeRegs + X::kLoadRegs) return cudaErrorInvalidDeviceFunction;
     }
     const int ctas = sm_count() * X::kCtas < kMaxRuns ? sm_count() * X::kCtas : kMaxRuns;
     char* ws = static_cast<char*>(a.ws);

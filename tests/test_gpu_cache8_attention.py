@@ -292,6 +292,59 @@ def test_graphs_share_a_workspace_and_follow_the_lengths():
             _check(o1, q, cache, new, 32, [2] * 4)
 
 
+def test_first_calls_recorded_into_a_graph():
+    """In a fresh process the first call of each of the kernels is one that is recorded."""
+    import subprocess
+    import sys
+    code = """
+import sys, torch
+sys.path[:0] = ['tests', '.']
+import test_gpu_cache8_attention as t
+from decoder_only_transformer_gb300 import tfm
+for H, Hkv, T, dh in ((4, 4, 1, 128), (16, 1, 1, 64), (20, 1, 1, 128), (16, 2, 4, 128), (4, 4, 1, 32)):
+    cache = t._cache(1, 2, Hkv, 2000, dh, 64, t.I8)
+    lens, q = t._ints([1990, 70]), t._q(1, 2 * T, H, dh)
+    ws, o = t._bytes(tfm.cache8_attention_workspace_bytes(2, H, Hkv, T, dh)), torch.zeros_like(q)
+    k, v = t._q(2, 2 * T, Hkv, dh), t._q(3, 2 * T, Hkv, dh)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s), torch.cuda.graph(g, stream=s):
+        tfm.cache8_write(k, v, *cache, lens, 64)
+        tfm.cache8_attention(q, *cache, o, lens, ws, 64)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, t._call(q, cache, [1990, 70], 64)) and float(o.abs().max()) > 0
+tfm.device_status()
+print('recorded')
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=root)
+    assert r.returncode == 0 and "recorded" in r.stdout, r.stderr[-2000:]
+
+
+def test_scales_far_apart_and_zero():
+    """Blocks of V with scale zero, whose keys count in the sum of the weights, and scales that differ by 2^60; for K a
+    scale of zero is a score of zero."""
+    lens, block = [200, 333], 16
+    for codes in (I8, E4):
+        cache = _cache(21, 2, 2, 340, 128, block, codes)
+        for b in (0, 5, 12):
+            cache[3][:, :, b] = 0.0
+        cache[2][:, :, 7] = 0.0
+        for H, T in ((8, 1), (8, 3), (2, 1)):
+            q = _q(21, 2 * T, H, 128)
+            _check(_call(q, cache, lens, block), q, cache, lens, block, [T, T])
+        for far in (2.0 ** 30, 2.0 ** -30, 2.0 ** 60):
+            other = [t.clone() for t in cache]
+            other[3][:, :, 3:9] *= far
+            _check(_call(q, other, lens, block), q, other, lens, block, [1, 1])
+        # alone, the small ones are as precise as any
+        cache[3].mul_(2.0 ** -70)
+        _check(_call(q, cache, lens, block), q, cache, lens, block, [1, 1])
+
+
 def test_calls_on_two_streams_at_once():
     cache = _cache(18, 30, 4, 900, 64, 64, E4)
     lens = [(i * 211) % 900 for i in range(30)]
