@@ -828,19 +828,19 @@ def rope_rows(q, k, q_out, k_out, positions, inv_freq, interleaved=True, mscale=
     torch, here = _now()
     shape = q.shape
     kk, ko = (q, q_out) if k is None or k_out is None else (k, k_out)
-    if not (len(shape) == 3 and here == q.get_device() == q_out.get_device() == kk.get_device() == ko.get_device()
+    keys = kk.shape
+    sq, sk, so, sp = q.stride(), kk.stride(), q_out.stride(), ko.stride()
+    if not (len(shape) == 3 == len(keys) and here == q.get_device() == q_out.get_device() == kk.get_device() == ko.get_device()
             == positions.get_device() == inv_freq.get_device() and (k is None) == (k_out is None)
-            and q.dtype is q_out.dtype is kk.dtype is ko.dtype and shape == q_out.shape and kk.shape == ko.shape
-            and len(kk.shape) == 3 and kk.shape[0] == shape[0] and kk.shape[2] == shape[2]
-            and 1 == q.stride(2) == q_out.stride(2) == kk.stride(2) == ko.stride(2)
+            and q.dtype is q_out.dtype is kk.dtype is ko.dtype and shape == q_out.shape and keys == ko.shape
+            and keys[0] == shape[0] and keys[2] == shape[2] and 1 == sq[2] == sk[2] == so[2] == sp[2]
             and positions.dtype is torch.int32 and positions.numel() == shape[0] and positions.is_contiguous()
             and inv_freq.dtype is torch.float64 and inv_freq.is_contiguous()):
         _refuse_rope_rows(q, k, q_out, k_out, positions, inv_freq)
     T, H, dh = shape
-    Hkv, rot = 0 if k is None else kk.shape[1], 2 * inv_freq.numel()
+    Hkv, rot = 0 if k is None else keys[1], 2 * inv_freq.numel()
     if (T | H | Hkv | rot) >> 31:
         _int32((T, "T"), (H, "H"), (Hkv, "Hkv"), (rot, "rot"))
-    sq, sk, so, sp = q.stride(), kk.stride(), q_out.stride(), ko.stride()
     status = lib.tfm_rope_rows(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
                                None if k is None else k_out.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), T, H,
                                Hkv, dh, rot, 1 if interleaved else 0,
@@ -875,13 +875,13 @@ def _refuse_cache8(k_codes, v_codes, k_scales, v_scales, lens, block, cu_seqlens
                 (lens, "lens"), (cu_seqlens, "cu_seqlens"))
 
 
-def _cache8_ok(torch, here, kc, vc, ks, vs, lens, block, cu):
-    shape, scales = kc.shape, ks.shape
+def _cache8_ok(torch, here, shape, kc, vc, ks, vs, lens, block, cu):
+    scales = ks.shape
     return (len(shape) == 4 and here == kc.get_device() == vc.get_device() == ks.get_device() == vs.get_device()
             == lens.get_device() and kc.dtype is vc.dtype and (kc.dtype is torch.int8 or kc.dtype is torch.float8_e4m3fn)
             and torch.float32 is ks.dtype is vs.dtype and lens.dtype is torch.int32 and shape == vc.shape
-            and scales == vs.shape and block > 0 and tuple(scales) == (shape[0], shape[1], -(-shape[2] // block))
-            and len(lens.shape) == 1 and lens.shape[0] <= shape[0] and kc.is_contiguous() and vc.is_contiguous()
+            and block > 0 and scales == (shape[0], shape[1], -(-shape[2] // block)) and scales == vs.shape
+            and lens.dim() == 1 and lens.shape[0] <= shape[0] and kc.is_contiguous() and vc.is_contiguous()
             and ks.is_contiguous() and vs.is_contiguous() and lens.is_contiguous()
             and (cu is None or (cu.get_device() == here and cu.dtype is torch.int32 and cu.dim() == 1
                                 and cu.shape[0] == lens.shape[0] + 1 and cu.is_contiguous())))
@@ -891,8 +891,9 @@ def _cache8_rows(read, k, v, kc, vc, ks, vs, lens, block, cu, stream):
     lib = _lib or load()
     torch, here = _now()
     shape, cache = k.shape, kc.shape
+    sk, sv = k.stride(), v.stride()
     if not (len(shape) == 3 and here == k.get_device() == v.get_device() and k.dtype is v.dtype and shape == v.shape
-            and 1 == k.stride(2) == v.stride(2) and _cache8_ok(torch, here, kc, vc, ks, vs, lens, block, cu)
+            and 1 == sk[2] == sv[2] and _cache8_ok(torch, here, cache, kc, vc, ks, vs, lens, block, cu)
             and shape[1] == cache[1] and shape[2] == cache[3]):
         if k.dim() != 3:
             raise ValueError("k: [T, Hkv, dh] is required")
@@ -904,7 +905,6 @@ def _cache8_rows(read, k, v, kc, vc, ks, vs, lens, block, cu, stream):
     B, max_seq = lens.shape[0], cache[2]
     if (T | Hkv | max_seq | block) >> 31:
         _int32((T, "T"), (Hkv, "Hkv"), (max_seq, "max_seq"), (block, "block"))
-    sk, sv = k.stride(), v.stride()
     rows, cached = (k.data_ptr(), v.data_ptr()), (kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr())
     status = (lib.tfm_cache8_read if read else lib.tfm_cache8_write)(
         *(cached + rows if read else rows + cached), None if cu is None else cu.data_ptr(), lens.data_ptr(), B, T, Hkv, dh,
@@ -930,8 +930,9 @@ def cache8_read(k_codes, v_codes, k_scales, v_scales, k, v, lens, block, cu_seql
 
 
 def cache8_attention_workspace_bytes(B, H, Hkv, max_new, dh):
-    _int32((B, "B"), (H, "H"), (Hkv, "Hkv"), (max_new, "max_new"), (dh, "dh"))
-    return load().tfm_cache8_attention_workspace_bytes(B, H, Hkv, max_new, dh)
+    if (B | H | Hkv | max_new | dh) >> 31:
+        _int32((B, "B"), (H, "H"), (Hkv, "Hkv"), (max_new, "max_new"), (dh, "dh"))
+    return (_lib or load()).tfm_cache8_attention_workspace_bytes(B, H, Hkv, max_new, dh)
 
 
 def _refuse_cache8_attention(q, kc, vc, ks, vs, o, lens, workspace, block, cu):
@@ -954,9 +955,10 @@ def cache8_attention(q, k_codes, v_codes, k_scales, v_scales, o, lens, workspace
     lib = _lib or load()
     torch, here = _now()
     shape, cache = q.shape, k_codes.shape
+    sq, so = q.stride(), o.stride()
     if not (len(shape) == 3 and here == q.get_device() == o.get_device() == workspace.get_device()
-            and torch.bfloat16 is q.dtype is o.dtype and shape == o.shape and 1 == q.stride(2) == o.stride(2)
-            and _cache8_ok(torch, here, k_codes, v_codes, k_scales, v_scales, lens, block, cu_seqlens)
+            and torch.bfloat16 is q.dtype is o.dtype and shape == o.shape and 1 == sq[2] == so[2]
+            and _cache8_ok(torch, here, cache, k_codes, v_codes, k_scales, v_scales, lens, block, cu_seqlens)
             and shape[2] == cache[3] and workspace.is_contiguous()):
         _refuse_cache8_attention(q, k_codes, v_codes, k_scales, v_scales, o, lens, workspace, block, cu_seqlens)
     T, H, dh = shape
@@ -969,7 +971,6 @@ def cache8_attention(q, k_codes, v_codes, k_scales, v_scales, o, lens, workspace
     if (T | H | Hkv | max_seq | max_new | block | window) >> 31:
         _int32((T, "T"), (H, "H"), (Hkv, "Hkv"), (max_seq, "max_seq"), (max_new, "max_new"), (block, "block"),
                (window, "window"))
-    sq, so = q.stride(), o.stride()
     status = lib.tfm_cache8_attention(q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
                                       v_scales.data_ptr(), o.data_ptr(),
                                       None if cu_seqlens is None else cu_seqlens.data_ptr(), lens.data_ptr(), B, T, H, Hkv,
