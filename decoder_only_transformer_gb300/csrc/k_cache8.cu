@@ -70,14 +70,16 @@ __device__ __forceinline__ void check_rows(const int32_t* __restrict__ cu, const
     if (bad) raise_error(err, TFM_EINVAL);
 }
 
-// NVEC vectors of 8 elements of a unit's rows.
+// NVEC vectors of 8 elements of a unit's rows.  (Rows, codes and scales are read past the L1 cache: a
+// launch that overlaps the end of the one before may share an SM with its reads of lines that other SMs went on to
+// write.)
 template <typename T, int NVEC>
 struct Rows8;
 template <int NVEC>
 struct Rows8<__nv_bfloat16, NVEC> {
     uint4 w[NVEC];
     __device__ __forceinline__ void clear(int i) { w[i] = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void load(int i, const __nv_bfloat16* p) { w[i] = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void load(int i, const __nv_bfloat16* p) { w[i] = __ldcg(reinterpret_cast<const uint4*>(p)); }
     __device__ __forceinline__ void get(int i, float* x) const {
         x[0] = bf16_lo(w[i].x), x[1] = bf16_hi(w[i].x), x[2] = bf16_lo(w[i].y), x[3] = bf16_hi(w[i].y);
         x[4] = bf16_lo(w[i].z), x[5] = bf16_hi(w[i].z), x[6] = bf16_lo(w[i].w), x[7] = bf16_hi(w[i].w);
@@ -100,8 +102,8 @@ struct Rows8<float, NVEC> {
     uint4 w[2 * NVEC];
     __device__ __forceinline__ void clear(int i) { w[2 * i] = w[2 * i + 1] = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void load(int i, const float* p) {
-        w[2 * i] = __ldg(reinterpret_cast<const uint4*>(p));
-        w[2 * i + 1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+        w[2 * i] = __ldcg(reinterpret_cast<const uint4*>(p));
+        w[2 * i + 1] = __ldcg(reinterpret_cast<const uint4*>(p) + 1);
     }
     __device__ __forceinline__ void get(int i, float* x) const {
 #pragma unroll
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(kMaxThreads8)
         else x.clear(i);
     }
     const bool held = n.lo > n.p0;                         // earlier positions of the sequence lie in the block
-    const float old = held ? *scale : 0.0f;
+    const float old = held ? __ldcg(scale) : 0.0f;
     const auto unit_max = [&](float y) {
 #pragma unroll
         for (int o = 16; o; o >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(kMaxThreads8)
         const float down = ldexpf(1.0f, -up);
         for (int e = tid; e < (n.lo - n.p0) * kVR; e += threads) {
             uint2* at = reinterpret_cast<uint2*>(codes) + e;
-            const uint2 w = *at;
+            const uint2 w = __ldcg(at);
             uint32_t c[2] = {0, 0};
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -312,11 +314,11 @@ __global__ void __launch_bounds__(kMaxThreads8)
     const int64_t st = g.s[n.isv ? 2 : 0], bh = (int64_t)n.b * g.Hkv + n.h;
     T* at = (n.isv ? v : k) + (int64_t)n.h * g.s[n.isv ? 3 : 1] + (n.row0 + first) * st + tid % kVR * 8;
     const uint2* codes = reinterpret_cast<const uint2*>((n.isv ? vc : kc) + (bh * g.max_seq + n.p0) * DH);
-    const float sc = __ldg((n.isv ? vs : ks) + bh * g.nblk + n.blk);
+    const float sc = __ldcg((n.isv ? vs : ks) + bh * g.nblk + n.blk);
     uint2 w[NVEC];
 #pragma unroll
     for (int i = 0; i < NVEC; ++i) {
-        if ((unsigned)(first + i * step - n.lo) < count) w[i] = __ldg(codes + tid + i * threads);
+        if ((unsigned)(first + i * step - n.lo) < count) w[i] = __ldcg(codes + tid + i * threads);
     }
     const int64_t ahead = step * st;
 #pragma unroll

@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
         int key = s.key + kw * 16;
         const int last_blk = len > 0 ? (len - 1) >> gm.shift : 0;
         int blk = min(key >> gm.shift, last_blk);
-        float ksc = __ldg(ksp + blk), vsc = __ldg(vsp + blk);
+        float ksc = __ldcg(ksp + blk), vsc = __ldcg(vsp + blk);                // (past L1: as in k_cache8.cu)
         // q: row r of the job is token r / G, head r % G.  Lane (g, t) holds row 8 n + g, for the products, of
         // what belongs to the rows 8 n + 2 t and + 1, whose scores it gets, in the arrays [n][2].
         // (kSharedQ: warp n prepares rows 8 n .. 8 n + 7 for all, in shared memory.)
@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
         };
         for (int tile = 0; tile < tiles; ++tile, key += kTileKeys) {
             blk = min((key + kTileKeys) >> gm.shift, last_blk);                 // the next step's
-            const float ksn = __ldg(ksp + blk), vsn = __ldg(vsp + blk);
+            const float ksn = __ldcg(ksp + blk), vsn = __ldcg(vsp + blk);
             if (!warp_wait_short(full + 8 * st, phase, err, &abort_flag)) return;
             // a step whose keys every row sees needs no masks
             if (key >= all_lo && key + 15 <= all_hi) step(std::false_type{});

@@ -604,8 +604,8 @@ tfm_status tfm_rope_rows(const void* q, const void* k, void* q_out, void* k_out,
  * codes and is not looked at.  NaN is stored as 0 and an infinity as the largest code (their block's
  * scale is that of its finite values), and either sets TFM_EINVAL in the device error word.
  * So do offsets that decrease or leave [0, T], lens[b] outside [0, max_seq] and more rows than
- * lens[b]: nothing is then written for that sequence (offsets of others that are not in
- * order included), and nothing outside the buffers is touched.
+ * lens[b]: nothing is then written for that sequence (nor, perhaps, for others if offsets are
+ * not in order), and nothing outside the buffers is touched.
  * Rows 16-byte aligned, codes 16-byte, scales and lengths 4-byte; (T / block + 2 B) * 2 Hkv below
  * 2^31.  B = 0 or T = 0 returns at once.
  * Calls that write the same cache must be ordered.  Capturable in a CUDA graph. */
@@ -631,9 +631,9 @@ tfm_status tfm_cache8_read(const void* k_codes, const void* v_codes, const float
  * sees no position (lens[b] < n) gets zeros; rows of no sequence are not written.  What
  * lies in the cache behind lens[b] or before the window is not looked at; codes
  * and scales that are seen must be finite (those tfm_cache8_write stores are).  Scores, maxima and sums are fp32;
- * a row of q is held in fp16 after division by a power of two (exact but for elements below
- * 2^-14 of the row's largest, which are rounded to 2^-24 of it), the weights are rounded to
- * fp16 for their product with the codes (2^-11 relative), the output once to bf16.
+ * a row of q is held in fp16 times a power of two (exact but for elements below 2^-24 of the
+ * row's largest, which are rounded to 2^-35 of it), the weights are rounded to fp16 (2^-11
+ * relative) for their product with the codes and summed as rounded, the output once to bf16.
  * No sequence has more than max_new rows, (H / Hkv) * max_new <= 128, B * H * max_new <= 2^24.
  * scale must be finite and at most 2^126.
  * workspace: device, 16-byte aligned, tfm_cache8_attention_workspace_bytes(B, H, Hkv,

@@ -292,6 +292,72 @@ def test_graphs_share_a_workspace_and_follow_the_lengths():
             _check(o1, q, cache, new, 32, [2] * 4)
 
 
+@pytest.mark.parametrize("codes", [I8, E4])
+@pytest.mark.parametrize("H,Hkv,dh,T", [(8, 4, 32, 1), (16, 4, 128, 2), (12, 12, 64, 1)])
+def test_calls_behind_one_another_as_calls_apart(H, Hkv, dh, T, codes):
+    """Rotation in place, write, attention and reading back, launched behind one another and recorded, many layers of
+    them: the bits of the same calls with the device waited for in between."""
+    B, room, block, layers = 48, 150, 16, 6
+    g = torch.Generator().manual_seed(dh)
+    inv = tfm.rope_frequencies(10000.0, dh)[0].cuda()
+    lens = torch.randint(T, room, (B,), generator=g, dtype=torch.int32).cuda()
+    positions = (lens[:, None] - T + torch.arange(T, device="cuda", dtype=torch.int32)).flatten().contiguous()
+    rows = torch.randn(layers, B * T, H + 2 * Hkv, dh, generator=g).to(BF).cuda()
+    caches = [_cache(i, B, Hkv, room, dh, block, codes) for i in range(layers)]
+    ws = _bytes(tfm.cache8_attention_workspace_bytes(B, H, Hkv, T, dh))
+
+    def layer(x, cache, o, back, wait):
+        q, k, v = x.split((H, Hkv, Hkv), 1)
+        for call in (lambda: tfm.rope_rows(q, k, q, k, positions, inv),
+                     lambda: tfm.cache8_write(k, v, *cache, lens, block),
+                     lambda: tfm.cache8_attention(q, *cache, o, lens, ws, block),
+                     lambda: tfm.cache8_read(*cache, *back, lens, block)):
+            call()
+            if wait:
+                torch.cuda.synchronize()
+
+    def buffers():
+        return (rows.clone(), [[t.clone() for t in c] for c in caches],
+                torch.zeros(layers, B * T, H, dh, dtype=BF, device="cuda"),
+                torch.zeros(layers, 2, B * T, Hkv, dh, dtype=BF, device="cuda"))
+
+    x, cs, want, back = buffers()
+    for i in range(layers):
+        layer(x[i], cs[i], want[i], back[i], True)
+    for recorded in (False, True, True):
+        y, ds, o, b = buffers()
+        if recorded:
+            s = torch.cuda.Stream()
+            s.wait_stream(torch.cuda.current_stream())
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.stream(s), torch.cuda.graph(graph, stream=s):
+                for i in range(layers):
+                    layer(y[i], ds[i], o[i], b[i], False)
+            graph.replay()
+        else:
+            for i in range(layers):
+                layer(y[i], ds[i], o[i], b[i], False)
+        torch.cuda.synchronize()
+        assert torch.equal(y, x) and torch.equal(o, want) and torch.equal(b, back)
+        for c, d in zip(cs, ds):
+            assert all(torch.equal(p.view(torch.uint8), q.view(torch.uint8)) for p, q in zip(c, d))
+
+
+def test_tiles_that_reach_into_the_next_head():
+    """Caches whose end lies inside a tile: what follows is the next head's or sequence's, NaN codes among it."""
+    for room in (1, 63, 65, 70, 129):
+        cache = _cache(room, 3, 2, room, 64, 16, E4)
+        for t in cache[:2]:
+            t.view(torch.uint8)[1] = 0x7f
+        lens, q = [room, 0, room], _q(room, 3, 4, 64)
+        clean = [t.clone() for t in cache]
+        for t in clean[:2]:
+            t.view(torch.uint8)[1] = 0
+        o = _call(q, cache, lens, 16)
+        assert torch.equal(o, _call(q, clean, lens, 16))
+        _check(o, q, clean, lens, 16, [1, 1, 1])
+
+
 def test_first_calls_recorded_into_a_graph():
     """In a fresh process the first call of each of the kernels is one that is recorded."""
     import subprocess
