@@ -495,8 +495,11 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
         const float* vsp = vs + (int64_t)s.bh * gm.nblk;
         int key = s.key + kw * 16;
         const int last_blk = len > 0 ? (len - 1) >> gm.shift : 0;
-        int blk = min(key >> gm.shift, last_blk);
-        float ksc = __ldcg(ksp + blk), vsc = __ldcg(vsp + blk);                // (past L1: as in k_cache8.cu)
+        // The scales of 32 blocks, one in each lane, and of the next 32 (read past L1: as in k_cache8.cu).
+        int blk0 = s.key >> gm.shift;
+        const auto scales32 = [&](const float* at, int first) { return __ldcg(at + min(first + lane, last_blk)); };
+        float k32 = scales32(ksp, blk0), v32 = scales32(vsp, blk0);
+        float k64 = scales32(ksp, blk0 + 32), v64 = scales32(vsp, blk0 + 32);
         // q: row r of the job is token r / G, head r % G.  Lane (g, t) holds row 8 n + g, for the products, of
         // what belongs to the rows 8 n + 2 t and + 1, whose scores it gets, in the arrays [n][2].
         // (kSharedQ: warp n prepares rows 8 n .. 8 n + 7 for all, in shared memory.)
@@ -587,7 +590,7 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
         // positions that some row sees, that every row sees
         const int any_lo = gm.window > 0 ? max(0, len - news - gm.window + 1) : 0;
         const int all_lo = gm.window > 0 ? len - gm.window : 0, all_hi = len - news;
-        const auto step = [&](auto edge) {
+        const auto step = [&](auto edge, float ksc, float vsc) {
             constexpr bool EDGE = decltype(edge)::value;
             const uint8_t* kt = sm + st * 2 * X::kTile;
             float c[NT][4];
@@ -731,17 +734,23 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
             }
         };
         for (int tile = 0; tile < tiles; ++tile, key += kTileKeys) {
-            blk = min((key + kTileKeys) >> gm.shift, last_blk);                 // the next step's
-            const float ksn = __ldcg(ksp + blk), vsn = __ldcg(vsp + blk);
+            int blk = min(key >> gm.shift, last_blk) - blk0;
+            if (blk >= 32) {                                 // (a tile has at most 4 blocks)
+                blk -= 32;
+                blk0 += 32;
+                k32 = k64;
+                v32 = v64;
+                k64 = scales32(ksp, blk0 + 32);
+                v64 = scales32(vsp, blk0 + 32);
+            }
+            const float ksc = __shfl_sync(0xffffffffu, k32, blk), vsc = __shfl_sync(0xffffffffu, v32, blk);
             if (!warp_wait_short(full + 8 * st, phase, err, &abort_flag)) return;
             // a step whose keys every row sees needs no masks
-            if (key >= all_lo && key + 15 <= all_hi) step(std::false_type{});
-            else if (key < len && key + 16 > any_lo) step(std::true_type{});
+            if (key >= all_lo && key + 15 <= all_hi) step(std::false_type{}, ksc, vsc);
+            else if (key < len && key + 16 > any_lo) step(std::true_type{}, ksc, vsc);
             __syncwarp();
             if (lane == 0) mbar_arrive(empty + 8 * st);
             if (++st == X::kStages) st = 0, phase ^= 1;
-            ksc = ksn;
-            vsc = vsn;
         }
         // The four warps' parts, added up, 8 rows at a time.
 #pragma unroll
