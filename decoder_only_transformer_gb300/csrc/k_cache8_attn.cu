@@ -454,7 +454,9 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
                 cuts[blockIdx.x] = c;
             }
             bool ok = true;
-            if (lane == 0)
+            // (the first tile before a third is asked for: all CTAs ask at once, and memory serves the last ones too)
+            if (lane == 0 && sn == 0) ok = mbar_wait(full, 0, err, &abort_flag);
+            if (lane == 0 && ok)
                 for (; done < tiles; ++done, row += kTileKeys) {
                     if (filled && !mbar_wait(empty + 8 * st, phase ^ 1, err, &abort_flag)) {
                         ok = false;
