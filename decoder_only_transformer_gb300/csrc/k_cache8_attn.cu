@@ -170,36 +170,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
-// warp_wait and mbar_wait with a hint that the thread may sleep for a microsecond, or until the phase
-// completes: a spinning warp takes issue slots from those it waits for.
-__device__ __forceinline__ bool try_wait_asleep(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(1000u)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool wait_asleep(uint32_t bar, uint32_t parity, int* err, volatile int* abort) {
-    if (try_wait_asleep(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    for (;;) {                                               // (inline: a call would not know of the registers' split)
-        if (try_wait_asleep(bar, parity)) return true;
-        if (*abort) return false;
-        if (global_timer_ns() - t0 > kWaitLimitNs) {
-            raise_error(err, TFM_ETIMEOUT);
-            *abort = 1;
-            return false;
-        }
-    }
-}
-__device__ __forceinline__ bool warp_wait_asleep(uint32_t bar, uint32_t parity, int* err, volatile int* abort) {
-    return __all_sync(0xffffffffu, wait_asleep(bar, parity, err, abort));
-}
-
 // An 8 x 8 block of fp16: lane (g, t) gives row g, columns 2 t and 2 t + 1, and gets rows 2 t
 // and 2 t + 1 of column g.
 __device__ __forceinline__ uint32_t transposed(uint32_t a) {
@@ -432,7 +402,7 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
                 w.t = 0;                                     // whatever comes next is another job
                 ++w.j;
             }
-            if (sn >= 2 && !warp_wait_asleep(qempty + 8 * place, (sn >> 1) + 1 & 1, err, &abort_flag)) return;
+            if (sn >= 2 && !warp_wait(qempty + 8 * place, (sn >> 1) + 1 & 1, err, &abort_flag)) return;
             if (tiles <= 0) {
                 if (lane == 0) {
                     segs[place].tiles = 0;
@@ -485,10 +455,10 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
             }
             bool ok = true;
             // (the first tile before a third is asked for: all CTAs ask at once, and memory serves the last ones too)
-            if (lane == 0 && sn == 0) ok = wait_asleep(full, 0, err, &abort_flag);
+            if (lane == 0 && sn == 0) ok = mbar_wait(full, 0, err, &abort_flag);
             if (lane == 0 && ok)
                 for (; done < tiles; ++done, row += kTileKeys) {
-                    if (filled && !wait_asleep(empty + 8 * st, phase ^ 1, err, &abort_flag)) {
+                    if (filled && !mbar_wait(empty + 8 * st, phase ^ 1, err, &abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -501,6 +471,7 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
         }
     }
     // -------------------------------------------------------------------- rows
+    // (no function is called behind the split, not by a wait either: it would not know of the registers it has)
     if (X::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(X::kComputeRegs));
     const int kw = warp, g = lane >> 2, t = lane & 3;
     // where this lane reads, inside a tile: keys of the step's second half are 8 rows further, the
@@ -518,7 +489,7 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
     uint4* frag = reinterpret_cast<uint4*>(sm + X::kFragOff) + lane;          // [n][pair of words][lane]
     float4* rowf = reinterpret_cast<float4*>(sm + X::kRowOff);
     for (;; ++sn) {
-        if (!warp_wait_asleep(qfull + 8 * (sn & 1), sn >> 1 & 1, err, &abort_flag)) return;
+        if (!warp_wait(qfull + 8 * (sn & 1), sn >> 1 & 1, err, &abort_flag)) return;
         const Seg& s = segs[sn & 1];
         const int tiles = s.tiles, len = s.len, news = s.n;
         if (tiles == 0) return;
@@ -604,7 +575,7 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(ffull);
-            if (!warp_wait_asleep(ffull, sn & 1, err, &abort_flag)) return;
+            if (!warp_wait(ffull, sn & 1, err, &abort_flag)) return;
         } else {
 #pragma unroll
             for (int n = 0; n < NT; ++n) prepare(n, qb[n], qinv[n], qbias[n], seen_hi[n]);
@@ -776,7 +747,7 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
                 v64 = scales32(vsp, blk0 + 32);
             }
             const float ksc = __shfl_sync(0xffffffffu, k32, blk), vsc = __shfl_sync(0xffffffffu, v32, blk);
-            if (!warp_wait_asleep(full + 8 * st, phase, err, &abort_flag)) return;
+            if (!warp_wait(full + 8 * st, phase, err, &abort_flag)) return;
             // a step whose keys every row sees needs no masks
             if (key >= all_lo && key + 15 <= all_hi) step(std::false_type{}, ksc, vsc);
             else if (key < len && key + 16 > any_lo) step(std::true_type{}, ksc, vsc);
@@ -788,7 +759,7 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int pass = sn * NT + n;
-            if (pass > 0 && !warp_wait_asleep(bempty, pass + 1 & 1, err, &abort_flag)) return;      // the last ones have been read
+            if (pass > 0 && !warp_wait(bempty, pass + 1 & 1, err, &abort_flag)) return;      // the last ones have been read
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
 #pragma unroll
@@ -810,7 +781,7 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bfull);
-            if (!warp_wait_asleep(bfull, pass & 1, err, &abort_flag)) return;
+            if (!warp_wait(bfull, pass & 1, err, &abort_flag)) return;
             for (int e = tid; e < 8 * (DH / 4); e += 128) {
                 const int r = e / (DH / 4), f = e % (DH / 4);
                 if (8 * n + r >= nrows) break;
