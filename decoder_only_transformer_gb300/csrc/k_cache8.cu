@@ -12,8 +12,7 @@
 //
 // Both are bound by memory, one pass: the warps of a unit (one for 2048 elements) hold its rows in
 // registers between the maximum and the codes; 16-byte loads of the rows, 8-byte stores
-// of codes (a warp covers whole 32-byte sectors).  The instructions per element count too (at the
-// full bandwidth an SM has ~10 a clock-sector to spend): magnitudes of bf16 rows are compared in
+// of codes (a warp covers whole 32-byte sectors).  The instructions per element count too: magnitudes of bf16 rows are compared in
 // pairs, as integers; a code is found by rounding x / s from below and from above (codes_of4).
 // The unit of a warp is found without a scan: block j of
 // sequence b has the number cu[b] / block + 2 b + j, which leaves room for a partly filled
@@ -297,8 +296,10 @@ __device__ __forceinline__ void values8(uint2 w, float sc, float* f) {
     }
 }
 
+// (Four CTAs an SM for 2048 elements a warp: with five or six the last ones lie on some SMs only, 64 chats of up to 600 x 4 x 128
+// 15.7 and 14.3 for 13.6 us, 16 of up to 1000 6.2 and 6.9 for 5.5; with three too little is on its way.)
 template <typename T, bool E4M3, int DH, int NVEC>
-__global__ void __launch_bounds__(kMaxThreads8)
+__global__ void __launch_bounds__(kMaxThreads8, 4)
     k_cache8_read(T* __restrict__ k, T* __restrict__ v, const uint8_t* __restrict__ kc, const uint8_t* __restrict__ vc,
                   const float* __restrict__ ks, const float* __restrict__ vs, const int32_t* __restrict__ cu,
                   const int32_t* __restrict__ lens, const Geom8 g, int* err) {
