@@ -21,22 +21,20 @@ struct SeqRows {
     bool ok;
 };
 
+// Rows [first, end) and the length of a sequence.
+__device__ __forceinline__ SeqRows seq_rows(int first, int end, int len, int T, int max_seq) {
+    SeqRows s;
+    const bool rows_ok = first >= 0 && end >= first && end <= T;
+    s.row0 = first;
+    s.n = rows_ok ? end - first : 0;
+    s.len = len;
+    s.ok = rows_ok && len >= 0 && len <= max_seq;
+    return s;
+}
 __device__ __forceinline__ SeqRows seq_rows(const int32_t* __restrict__ cu, const int32_t* __restrict__ lens, int b,
                                             int per, int T, int max_seq) {
-    SeqRows s;
-    s.len = __ldg(lens + b);
-    s.ok = s.len >= 0 && s.len <= max_seq;
-    if (cu) {
-        const int a = __ldg(cu + b), e = __ldg(cu + b + 1);
-        const bool rows_ok = a >= 0 && e >= a && e <= T;
-        s.row0 = a;
-        s.n = rows_ok ? e - a : 0;
-        s.ok = s.ok && rows_ok;
-    } else {
-        s.row0 = b * per;
-        s.n = per;
-    }
-    return s;
+    const int len = __ldg(lens + b);
+    return cu ? seq_rows(__ldg(cu + b), __ldg(cu + b + 1), len, T, max_seq) : seq_rows(b * per, (b + 1) * per, len, T, max_seq);
 }
 
 // ------------------------------------------------------------------ codes

@@ -272,3 +272,47 @@ def test_offsets_beyond_32_bits():
     ks2, vs2 = torch.zeros_like(k), torch.zeros_like(v)
     tfm.cache8_read(*small, ks2, vs2, _ints([130, room - first]), block, cu_seqlens=new)
     assert torch.equal(ko, ks2) and torch.equal(vo, vs2) and float((ko - k).abs().max()) < 0.05
+
+
+@pytest.mark.parametrize("B", [31, 32, 33, 63, 64, 65, 94, 95, 96, 97])
+@pytest.mark.parametrize("block,dh", [(16, 32), (64, 64), (128, 128)])
+def test_numbers_of_sequences(B, block, dh):
+    """Up to 32, up to 95 and more of them are found in different ways; warps that share a unit, and those that do not."""
+    rng = np.random.default_rng(B)
+    new = np.where(rng.random(B) < 0.3, 0, rng.integers(1, 150, B)).tolist()
+    new[-1] = 3 if B % 2 else 0
+    lens = [n + int(e) for n, e in zip(new, rng.integers(0, 60, B))]
+    cache = _cache(B, B, 2, 210, dh, block, I8)
+    k, v = _rows(B + 1, sum(new) + 2, 2, dh, BF)
+    kc, vc, ks, vs = _written(cache, k, v, lens, new, block)
+    ko, vo = torch.full_like(k, 7.0), torch.full_like(v, 7.0)
+    tfm.cache8_read(kc, vc, ks, vs, ko, vo, _ints(lens), block, cu_seqlens=_ends(new))
+    torch.cuda.synchronize()
+    tfm.device_status()
+    for got, c, s in ((ko, kc, ks), (vo, vc, vs)):
+        want = (c.float().cpu() * s.cpu().repeat_interleave(block, 2)[:, :, :210, None]).to(BF)
+        assert torch.equal(got[:sum(new)].cpu(), torch.cat([want[b, :, L - n:L].transpose(0, 1) for b, (L, n) in enumerate(zip(lens, new))]))
+        assert (got[sum(new):] == 7.0).all()
+
+
+@pytest.mark.parametrize("bad", [2 ** 31 - 1, -2 ** 31, -1, 301])
+@pytest.mark.parametrize("B,block", [(33, 16), (64, 128), (95, 64)])
+def test_an_offset_out_of_range_among_many(B, block, bad):
+    """The two sequences that it bounds are left as they were, and what lies around the buffers."""
+    whole = _cache(7, B + 2, 2, 40, 64, block, I8)
+    kept = [t.clone() for t in whole]
+    inner = [t[1:B + 1] for t in whole]
+    new = [3] * B
+    k, v = _rows(5, 300, 2, 64, BF)
+    cu = _ends(new)
+    cu[20] = bad
+    for read in (False, True):
+        f = tfm.cache8_read if read else tfm.cache8_write
+        args = (*inner, k, v) if read else (k, v, *inner)
+        f(*args, _ints([20] * B), block, cu_seqlens=cu)
+        with pytest.raises(tfm.TfmError) as e:
+            tfm.device_status()
+        assert e.value.status == tfm.TFM_EINVAL
+    for a, b in zip(whole, kept):
+        for i in (0, 20, 21, B + 1):
+            assert torch.equal(a[i].view(torch.uint8), b[i].view(torch.uint8))
