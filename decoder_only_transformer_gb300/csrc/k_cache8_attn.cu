@@ -824,8 +824,9 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
 // Joins the pieces of the jobs that runs cut.  A job of P pieces has P - 1 boundaries of runs inside
 // it; CTA i takes that before run i + 1 and with it a share of the job's rows, in
 // float4s, kJoin of them at least.  The pieces are taken by the groups of threads in turn and
-// added in an order that depends on their number alone.
-constexpr int kJoin = 8, kJoinThreads = 256;
+// added in an order that depends on their number alone.  (256 threads: drafted tokens 23.4 for 21.9 us, windowed 20.5 for 20.0;
+// 64: 64 chats 32.0 for 30.6; eight entries at least: 131072 positions 28.6 for 28.1.)
+constexpr int kJoin = 4, kJoinThreads = 128;
 template <int DH>
 __global__ void __launch_bounds__(kJoinThreads)
     k_cache8_join(const Cut* __restrict__ cuts, const float2* __restrict__ part_ml, const float4* __restrict__ part_o,
