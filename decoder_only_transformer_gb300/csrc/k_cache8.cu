@@ -12,11 +12,16 @@
 //
 // Both are bound by memory, one pass: the warps of a unit (one for 2048 elements) hold its rows in
 // registers between the maximum and the codes; 16-byte loads of the rows, 8-byte stores
-// of codes (a warp covers whole 32-byte sectors).  The instructions per element count too: magnitudes of bf16 rows are compared in
-// pairs, as integers; a code is found by rounding x / s from below and from above (codes_of4).
-// The unit of a warp is found without a scan: block j of
+// of codes (a warp covers whole 32-byte sectors).  The instructions per element count too:
+// magnitudes of bf16 rows are compared in pairs, as integers; a code is found by rounding x / s
+// from below and from above (codes_of4).  The unit of a warp is found without a scan: block j of
 // sequence b has the number cu[b] / block + 2 b + j, which leaves room for a partly filled
-// block at either end.  Neighbouring warps take neighbouring heads, whose rows lie side by side.
+// block at either end.  Neighbouring warps take neighbouring heads, whose rows lie side by side
+// (CTAs of 4 units where 8 fit: 20 for 15 us).
+//
+// Measured (graph replays): 32768 tokens of 4 x 128, bf16 and e4m3: written in 22.4 us (4.5 TB/s; issue
+// slots 60 %), read back in 18.1 (5.6); 24 prompts of up to 1024 tokens of 12 x 64, int8, blocks of 16:
+// 15.1 and 11.0 us; one token of each of 64 sequences: 5.5 us.
 #include "cache8.cuh"
 
 namespace tfm {
@@ -48,7 +53,8 @@ __device__ __forceinline__ SeqRows find_seq(const int32_t* __restrict__ cu, cons
     const int lane = threadIdx.x & 31;
     int lo = 0;
     if (g.B > 32 && g.B <= kAtOnce) {
-        // all of them at once, lengths too: one wait instead of three (64 sequences of one new token: write 6.2 -> 5.5 us, read 13.6 -> 13.0; for up to 32 the other way has two waits and fewer instructions)
+        // all of them at once, lengths too: one wait instead of three (64 sequences: write of a token 6.2 -> 5.5 us, read
+        // 13.6 -> 13.0; up to 32 have two waits otherwise and fewer instructions, 24 prompts 23.9 for 24.7)
         constexpr int N = (kAtOnce + 1) / 32;
         int a[N], len[N];
 #pragma unroll
@@ -321,8 +327,9 @@ __device__ __forceinline__ void values8(uint2 w, float sc, float* f) {
     }
 }
 
-// (Four CTAs an SM for 2048 elements a warp: with five or six the last ones lie on some SMs only, 64 chats of up to 600 x 4 x 128
-// 15.7 and 14.3 for 13.6 us, 16 of up to 1000 6.2 and 6.9 for 5.5; with three too little is on its way.)
+// (Four CTAs an SM for 2048 elements a warp: with five or six the last ones lie on some SMs only, 64 chats of up
+// to 600 x 4 x 128 15.7 and 14.3 for 13.6 us, 16 of up to 1000 6.2 and 6.9 for 5.5; with three too little is on
+// its way, 15.0 and 7.5.)
 template <typename T, bool E4M3, int DH, int NVEC>
 __global__ void __launch_bounds__(kMaxThreads8, 4)
     k_cache8_read(T* __restrict__ k, T* __restrict__ v, const uint8_t* __restrict__ kc, const uint8_t* __restrict__ vc,

@@ -36,15 +36,17 @@
 // order.  Short caches are not cut, and need no second kernel.
 //
 // Measured (graph replays; GB/s of the bytes that count): 64 chats of up to 4096 positions, 16/4 x 128,
-// int8: 30.7 us, 4.4 TB/s; 131072 positions of one, e4m3: 28.5 us, 4.7 TB/s; 32 x 16 caches of 64
-// with a window of 1024: 20.5 us; up to 5 new tokens of 16 over up to 8192: 23.9 us; 4 chats under
-// 511: 6.2 us.  Of each but the last ~2 us pass until the first tile is asked for (lengths, runs, q),
-// ~2 until it is there, ~1.5 with the last sums, ~4 with the second kernel; in between memory is
+// int8: 30.4 us, 4.4 TB/s; 131072 positions of one, e4m3: 28.2 us, 4.7 TB/s; 32 x 16 caches of 64
+// with a window of 1024: 20.0 us; up to 5 new tokens of 16 over up to 8192: 21.9 us; 4 chats under
+// 511: 6.8 us.  Of each but the last ~2 us pass until the first tile is asked for (lengths, runs, q),
+// ~2 until it is there, ~1.5 with the last sums, ~3 with the second kernel; in between memory is
 // nearly full for up to 8 rows, and a step's latency (~1500 cycles at 24 rows, two warps a
 // scheduler) counts for more.  Tried and slower: the values' scales in the weights' exponents (P V without
 // the fp32 additions: +1 to 2 us), the next step's scores ahead of this one's softmax (no
-// change), three row groups of warps with 8 rows each for 24 (24.6 for 23.9), runs and zeroed counters
-// from a kernel ahead, the last writer adding the pieces up (+3 to 6 us), deeper rings (+1).
+// change), three row groups of warps with 8 rows each for 24 (24.6 for 23.9), two scaled additions in
+// one instruction (no change), runs and zeroed counters from a kernel ahead, the last writer adding the
+// pieces up (+3 to 6 us), deeper rings (+1), the second kernel launched early with its CTAs spread by
+// shared memory (no change).
 #include <type_traits>
 
 #include "cache8.cuh"

@@ -15,10 +15,10 @@
 //
 // Bound by memory: each row is read and written once, 16 bytes per lane and access.  A warp takes a
 // token (where they are few, some of its heads): it asks for its first rows, computes the token's
-// sines into 1 KB of shared memory of its own meanwhile, and turns row after row (32768 tokens of 16/4 x 128: 56 us,
-// 0.89 of a copy's bandwidth).  No barrier: with the
-// sines of 16 tokens shared by a CTA, sines and rows took turns (62 to 72 us), and with sines in registers, a thread for one vector of all heads, too few bytes were
-// on their way (85 us).
+// sines into 1 KB of shared memory of its own meanwhile, and turns row after row (32768 tokens of 16/4 x 128: 58 us,
+// 0.87 of a copy's bandwidth).  No barrier: with the sines of 16 tokens shared by a CTA, sines and
+// rows took turns (62 to 72 us), and with sines in registers, a thread for one vector of all
+// heads, too few bytes were on their way (85 us).
 #include "common.cuh"
 #include "internal.h"
 
