@@ -310,6 +310,8 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
         // ---------------------------------------------------------------- loads
         if (X::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(X::kLoadRegs));
         if (warp > 4) return;
+        // (the join has a record to read even if a wait gives up)
+        if (lane == 0 && !gm.whole) cuts[blockIdx.x].pieces = 0;
         Walk w{0, 0, 0, 0};
         Seq s;
         int total = 0, runs = 0, u = 0;                      // units of all jobs; this run's next one
@@ -409,7 +411,6 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
                 if (lane == 0) {
                     segs[place].tiles = 0;
                     mbar_arrive(qfull + 8 * place);
-                    if (sn == 0 && !gm.whole) cuts[blockIdx.x].pieces = 0;
                 }
                 return;
             }
