@@ -13,7 +13,9 @@
 // products as well: GB300 has two fp64 lanes a clock and SM, and one fp64 product per thread and
 // pair would take longer than the rows.
 //
-// Bound by memory: each row is read and written once, 16 bytes per lane and access.  A warp takes a
+// Bound by memory: each row is read and written once, 16 bytes per lane and access; 8 or 4 where rows,
+// strides or halves of pairs begin on no more (22041 tokens of 3/3 x 80, 40 turned in halves: 17.8 us,
+// element by element 68).  A warp takes a
 // token (where they are few, some of its heads): it asks for its first rows, computes the token's
 // sines into 1 KB of shared memory of its own meanwhile, and turns row after row (32768 tokens of 16/4 x 128: 58 us,
 // 0.87 of a copy's bandwidth).  No barrier: with the sines of 16 tokens shared by a CTA, sines and
@@ -71,7 +73,7 @@ __device__ __forceinline__ float2 cos_sin(unsigned long long turns, int position
 }
 
 template <typename T, int VE>
-struct __align__(16) Elems {
+struct __align__(VE * sizeof(T)) Elems {
     T v[VE];
 };
 
@@ -90,12 +92,12 @@ __device__ __forceinline__ void fill_sines(float2* cs, unsigned long long turns,
         for (int t = first; t < nt; t += step) cs[t * half + pair] = cos_sin(turns, positions[t0 + t], mscale);
 }
 
-// 16-byte accesses: every pointer and stride a multiple of 16 bytes, the pairs of a vector whole.
-template <typename T, bool INTER>
+// Accesses of VB bytes: every pointer and stride a multiple of them, the pairs of a vector whole.
+template <typename T, bool INTER, int VB>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     k_rope_rows(const T* q, const T* k, T* qo, T* ko,                  // outputs may be the inputs
                 const int32_t* __restrict__ positions, const double* __restrict__ inv_freq, const RopeGeom g) {
-    constexpr int VE = 16 / (int)sizeof(T);
+    constexpr int VE = VB / (int)sizeof(T);
     constexpr int NP = INTER ? VE / 2 : VE;                            // pairs of a vector
     using Vec = Elems<T, VE>;
     __shared__ unsigned long long turns[128];
@@ -136,8 +138,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
                 T* dst = (isq ? qo : ko) + (int64_t)t * g.s[isq ? 4 : 6] + (int64_t)hh * g.s[isq ? 5 : 7] + e;
                 if (pairs) {
                     const float4* r4 = reinterpret_cast<const float4*>(cs + (INTER ? x * NP : e));
+                    if constexpr (NP == 1) turn_pair(lo.v[0], lo.v[1], cs[x]);
 #pragma unroll
-                    for (int j = 0; j < NP; j += 2) {
+                    for (int j = 0; j + 1 < NP; j += 2) {
                         const float4 r = r4[j >> 1];
                         if constexpr (INTER) {
                             turn_pair(lo.v[2 * j], lo.v[2 * j + 1], make_float2(r.x, r.y));
@@ -155,7 +158,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     }
 }
 
-// Any alignment, element by element: the sines of a few tokens in shared memory for all heads.
+// Halves of an odd number of bf16 elements and the like, element by element: the sines of a few tokens in shared memory for all heads.
 template <typename T, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads)
     k_rope_plain(const T* q, const T* k, T* qo, T* ko, const int32_t* __restrict__ positions,
@@ -203,13 +206,16 @@ cudaError_t launch_t(const RopeRowsArgs& a, cudaStream_t st) {
     g.dh = a.dh;
     g.rot = a.rot;
     g.mscale = a.mscale;
-    bool vec = a.dh * sizeof(T) % 16 == 0 && a.rot * sizeof(T) % (a.interleaved ? 16 : 32) == 0;
+    // bytes of an access: what every pointer, stride and part of a head is a multiple of
+    const int es = sizeof(T);
+    int64_t whole = 16 | (int64_t)a.dh * es | (int64_t)(a.interleaved ? a.rot : a.rot / 2) * es;
     const void* ptr[4] = {a.q, a.k, a.qo, a.ko};
     for (int i = 0; i < 8; ++i) {
         g.s[i] = a.strides[i];
         if ((i / 2) % 2 && !a.Hkv) continue;
-        vec = vec && a.strides[i] * (int64_t)sizeof(T) % 16 == 0 && reinterpret_cast<uintptr_t>(ptr[i / 2]) % 16 == 0;
+        whole |= a.strides[i] * es | (int64_t)reinterpret_cast<uintptr_t>(ptr[i / 2]);
     }
+    const int vb = (int)(whole & -whole);
     g.copy_tail = a.rot < a.dh && (a.q != a.qo || (a.Hkv && a.k != a.ko));
     const int heads = a.H + a.Hkv;
     const auto go = [&](auto kernel, dim3 grid, int smem) {
@@ -217,8 +223,8 @@ cudaError_t launch_t(const RopeRowsArgs& a, cudaStream_t st) {
                           static_cast<const T*>(a.k), static_cast<T*>(a.qo), static_cast<T*>(a.ko), a.positions,
                           a.inv_freq, g);
     };
-    if (vec) {
-        const int ve = 16 / sizeof(T);
+    if (vb > es) {
+        const int ve = vb / es;
         g.pair_cols = a.interleaved ? a.rot / ve : a.rot / 2 / ve;
         g.cols = g.pair_cols + (g.copy_tail ? (a.dh - a.rot) / ve : 0);
         g.lanes = 1;
@@ -238,7 +244,10 @@ cudaError_t launch_t(const RopeRowsArgs& a, cudaStream_t st) {
         const int per = (int)((grid.x + sm_count() - 1) / sm_count());
         int smem = per < kRopeCtas ? 228 * 1024 / (per + 1) - kStatic : 0;
         if (kStatic + smem > 48 * 1024) smem = 0;
-        return a.interleaved ? go(k_rope_rows<T, true>, grid, smem) : go(k_rope_rows<T, false>, grid, smem);
+        if (vb == 16) return a.interleaved ? go(k_rope_rows<T, true, 16>, grid, smem) : go(k_rope_rows<T, false, 16>, grid, smem);
+        if (vb == 8) return a.interleaved ? go(k_rope_rows<T, true, 8>, grid, smem) : go(k_rope_rows<T, false, 8>, grid, smem);
+        if constexpr (sizeof(T) == 2)
+            return a.interleaved ? go(k_rope_rows<T, true, 4>, grid, smem) : go(k_rope_rows<T, false, 4>, grid, smem);
     }
     // As many tokens a round as leave every SM a few CTAs; a step of few tokens is split
     // over the heads, each CTA with its own sines.

@@ -157,3 +157,26 @@ def test_graph_stream_and_empty():
         assert torch.equal(qo, want) and torch.equal(ko, kw)
     e = torch.empty(0, 4, 64, dtype=BF, device="cuda")
     tfm.rope_rows(e, None, e, None, torch.empty(0, dtype=torch.int32, device="cuda"), inv[:8])
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("start", [2, 4, 8])
+@pytest.mark.parametrize("T,H,Hkv,dh,rot", [(9, 3, 2, 80, 40), (700, 2, 1, 80, 40), (6, 5, 0, 256, 256), (40, 1, 3, 36, 12), (3, 4, 4, 254, 4)])
+def test_rows_that_start_between_16_byte_marks(T, H, Hkv, dh, rot, start, dtype, interleaved):
+    """Accesses of 4, 8 and 16 bytes; what lies around the rows stays."""
+    heads = H + Hkv
+    wide = torch.randn(T, heads * dh + 24, generator=torch.Generator().manual_seed(T)).to(dtype).cuda()
+    out = torch.full_like(wide, 7.0)
+    inv, _ = tfm.rope_frequencies(10000.0, rot)
+    pos = _pos(T, T)
+    parts = lambda x: x[:, start:start + heads * dh].unflatten(1, (heads, dh)).split((H, Hkv), 1)
+    (q, k), (qo, ko) = parts(wide), parts(out)
+    if not Hkv:
+        k = ko = None
+    tfm.rope_rows(q, k, qo, ko, pos, inv.cuda(), interleaved=interleaved)
+    torch.cuda.synchronize()
+    _close(qo, q, pos, inv, interleaved, 1.0)
+    if Hkv:
+        _close(ko, k, pos, inv, interleaved, 1.0)
+    assert (out[:, :start] == 7.0).all() and (out[:, start + heads * dh:] == 7.0).all()
