@@ -123,7 +123,7 @@ __device__ __forceinline__ Seq get_seq(const int32_t* __restrict__ cu, const int
     s.tile0 = first / kTileKeys;
     s.tiles = max(1, (s.len + kTileKeys - 1) / kTileKeys - s.tile0);
     s.blocks = 0;
-    for (int r = s.n * gm.G; r > 0; r -= gm.block_rows) ++s.blocks;    // (no division: 128 / 32 at most)
+    for (int r = s.n * gm.G; r > 0; r -= gm.block_rows) ++s.blocks;    // (no division: 128 / 8 at most)
     return s;
 }
 
@@ -919,10 +919,16 @@ __global__ void __launch_bounds__(kJoinThreads)
 }
 
 // Rows of a job by the rows that max_new tokens of a kv head have: all of up to 32; more are blocks
-// of 32, each of which reads the tiles.
+// of 32, each of which reads the tiles.  (Blocks of 8 where the caches are small: launch_cache8_attention.)
 int job_rows(int group, int max_new) {
     const int rows = group * max_new;
     return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : 32;
+}
+
+// Units that a job has at most.
+int job_units(const Cache8AttnArgs& a, int piece) {
+    const int keys = a.window > 0 && a.window + a.max_new < a.max_seq ? a.window + a.max_new : a.max_seq;
+    return (keys + kTileKeys - 2) / kTileKeys + 1 + piece;
 }
 
 struct Space {
@@ -966,8 +972,7 @@ cudaError_t launch_part(const Cache8AttnArgs& a, const CUtensorMap& km, const CU
     // A few tiles more in a row are faster than a second kernel: where no job can have more than kWhole
     // units, none is cut.
     const int64_t jobs = (int64_t)a.B * a.Hkv * gm.row_blocks;
-    const int keys = a.window > 0 && a.window + a.max_new < a.max_seq ? a.window + a.max_new : a.max_seq;
-    gm.whole = (keys + kTileKeys - 2) / kTileKeys + 1 + X::kPiece > kWhole ? 0 : jobs > ctas ? 1 : 2;
+    gm.whole = job_units(a, X::kPiece) > kWhole ? 0 : jobs > ctas ? 1 : 2;
     e = launch_pdl(k_cache8_part<E4M3, DH, NT>, dim3(gm.whole == 2 ? (unsigned)jobs : ctas), dim3(X::kThreads), smem, st, km, vm,
                    static_cast<const __nv_bfloat16*>(a.q), a.ks, a.vs, static_cast<__nv_bfloat16*>(a.o), a.cu, a.lens, cuts,
                    ml, po, gm, device_error_word());
@@ -1021,6 +1026,12 @@ tfm_status launch_cache8_attention(const Cache8AttnArgs& a, cudaStream_t st, cud
     gm.per = a.cu ? 0 : a.T / a.B;
     gm.window = a.window;
     gm.block_rows = job_rows(gm.G, a.max_new);
+    // Where even full caches are no more than 16 units for each CTA, rows on more CTAs are faster than tiles read once: 5
+    // tokens of 16/4 x 128 over 300 positions 10.7 -> 6.9 us, of 4 sequences over 4000 13.9 -> 12.4 (10 units), over 8192
+    // 15.9 -> 16.3 (21).
+    const int64_t jobs8 = (int64_t)a.B * a.Hkv * ((gm.G * a.max_new + 7) / 8);
+    const int piece = a.dh == 32 ? Ax<32, 1>::kPiece : Ax<64, 1>::kPiece, ctas8 = a.dh == 128 ? Ax<128, 1>::kCtas : Ax<64, 1>::kCtas;
+    if (jobs8 * job_units(a, piece) <= (int64_t)16 * ctas8 * sm_count()) gm.block_rows = 8;
     gm.row_blocks = (gm.G * a.max_new + gm.block_rows - 1) / gm.block_rows;
     gm.scale_log2 = a.scale * 1.4426950408889634f;
     gm.sq_t = a.strides[0];

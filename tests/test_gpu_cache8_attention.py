@@ -427,6 +427,52 @@ def test_calls_on_two_streams_at_once():
         assert torch.equal(o, want)
 
 
+def _with_room(cache, block, room):
+    """The same positions in a cache of many more, which hold what is not to be looked at."""
+    B, Hkv, n, dh = cache[0].shape
+    assert n % block == 0 and room % block == 0
+    out = []
+    for c in cache[:2]:
+        wide = torch.full((B, Hkv, room, dh), 0x7f, dtype=torch.uint8, device="cuda").view(c.dtype)
+        wide[:, :, :n] = c
+        out.append(wide)
+    for x in cache[2:]:
+        wide = torch.full((B, Hkv, room // block), float("nan"), device="cuda")
+        wide[:, :, :n // block] = x
+        out.append(wide)
+    return out
+
+
+@pytest.mark.parametrize("codes", [I8, E4])
+@pytest.mark.parametrize("dh,block", [(32, 16), (64, 64), (128, 32), (128, 128)])
+@pytest.mark.parametrize("H,Hkv,T", [(8, 2, 3), (8, 2, 4), (8, 2, 5), (16, 2, 3), (8, 1, 4), (10, 2, 8), (8, 1, 16)])
+@pytest.mark.parametrize("lens", [[17, 64, 65, 0, 200, 3], [128, 129, 127, 255, 33, 256]], ids=str)
+def test_many_rows_of_large_caches(lens, H, Hkv, T, dh, block, codes):
+    """Caches that could hold more than 16 tiles for each CTA: the rows of 2 to 4 groups of 8 share a tile.  Some sequences
+    have fewer new rows."""
+    B = len(lens)
+    room = 128 * (152 * 16 * 3 // 2 // (B * Hkv * -(-H // Hkv * T // 8)) + 4)
+    new = [T, 0, 1, T, T - 1, 2]
+    cache = _cache(dh + T, B, Hkv, 256, dh, block, codes)
+    q = _q(T, sum(new) + 1, H, dh)
+    o = _call(q, _with_room(cache, block, room), lens, block, new, T)
+    _check(o[:-1], q[:-1], cache, lens, block, new)
+    assert (o[-1] == 7.0).all()
+
+
+@pytest.mark.parametrize("codes", [I8, E4])
+@pytest.mark.parametrize("H,dh,T", [(8, 64, 8), (8, 64, 12), (16, 32, 8)])
+def test_a_long_window_of_many_rows(H, dh, T, codes):
+    """Groups of 8 rows that share tiles, whose windows begin inside them."""
+    B, Hkv, room, window = 24, 4, 3200, 3000
+    lens = [3200, 3001, 3007, 2999, 130, 0] + [1] * 18
+    cache = _cache(21, B, Hkv, room, dh, 64, codes)
+    q = _q(22, B * T, H, dh)
+    o = _call(q, cache, lens, 64, [T] * B, T, window)
+    n = 6
+    _check(o[:n * T], q[:n * T], [x[:n].contiguous() for x in cache], lens[:n], 64, [T] * n, window)
+
+
 @pytest.mark.parametrize("codes", [I8, E4])
 @pytest.mark.parametrize("H,Hkv,dh,window", [(8, 2, 128, 0), (4, 4, 64, 40), (16, 1, 32, 0)])
 def test_a_serving_program(H, Hkv, dh, window, codes):
