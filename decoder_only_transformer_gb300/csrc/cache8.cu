@@ -45,13 +45,16 @@ tfm_status take_strides(int64_t* out, const int64_t* strides, int n, const char*
     return TFM_OK;
 }
 
+constexpr int32_t kMaxPositions = 0x7fffffff - 255;
+
 // What the three cache calls have in common.
 tfm_status check_cache(int32_t B, int32_t T, int32_t Hkv, int32_t max_seq, int32_t dh, int32_t block, int32_t codes,
                        bool offsets) {
     if (B < 0 || B > 4096 || T < 0 || T > (1 << 30)) return fail(TFM_EINVAL, "B=%d outside [0, 4096] or T=%d outside [0, 2^30]", B, T);
     if (Hkv < 1 || Hkv > 4096) return fail(TFM_EINVAL, "Hkv=%d outside [1, 4096]", Hkv);
-    if (max_seq < 1 || (int64_t)B * Hkv * max_seq >= (int64_t)1 << 31)
-        return fail(TFM_EINVAL, "max_seq must be positive and B*Hkv*max_seq below 2^31");
+    // (positions are ints, and so are the ends of the blocks and tiles that reach beyond the last one)
+    if (max_seq < 1 || max_seq > kMaxPositions || (int64_t)B * Hkv * max_seq >= (int64_t)1 << 31)
+        return fail(TFM_EINVAL, "max_seq must be in [1, 2^31 - 256] and B*Hkv*max_seq below 2^31");
     if (!offsets && B && T % B) return fail(TFM_EINVAL, "without offsets T=%d must be a multiple of B=%d", T, B);
     if (codes != TFM_CODE_INT8 && codes != TFM_CODE_E4M3) return fail(TFM_EINVAL, "bad code type");
     if (dh < 1 || block < 1) return fail(TFM_EINVAL, "dh and block must be positive");

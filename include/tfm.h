@@ -543,7 +543,8 @@ tfm_status tfm_verify_draft(const float* target, int64_t ld_target, const float*
  * [B, Hkv, ceil(max_seq / block)], one for each head and block of positions: a position's
  * value is code * scale.  int8 codes are -127 .. 127; e4m3 codes (fp8 of 4 exponent and 3
  * mantissa bits) up to 448 in magnitude, never NaN as they are written.  dh in {32, 64, 128},
- * block in {16, 32, 64, 128}, B <= 4096, Hkv <= 4096, B * Hkv * max_seq below 2^31.
+ * block in {16, 32, 64, 128}, B <= 4096, Hkv <= 4096, max_seq <= 2^31 - 256, B * Hkv * max_seq
+ * below 2^31.
  * New rows are packed as for tfm_packed_attention: sequence b has the rows
  * [cu_seqlens[b], cu_seqlens[b + 1]) of T (int32 [B + 1], device; none is allowed), or,
  * cu_seqlens NULL, T / B rows each (T a multiple of B).  lens[b] (int32 [B], device) counts
