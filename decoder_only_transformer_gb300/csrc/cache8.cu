@@ -26,13 +26,13 @@ tfm_status cuda_fail(cudaError_t e, const char* what) {
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // Token and head strides, in elements, of rows [T, heads, dh]: NULL is dense, and so is the
-// stride of a dimension of size one, which is never used.  `multiple` in bytes.
+// stride of a dimension of size one and are both of no heads, which are never used.  `multiple` in bytes.
 tfm_status take_strides(int64_t* out, const int64_t* strides, int n, const char* const* names, const int* heads, int64_t T,
                         int dh, int es, int multiple) {
     for (int i = 0; i < n; ++i) {
         const bool head = i & 1;
         const int64_t dense = head ? dh : (int64_t)heads[i / 2] * dh;
-        if (!strides || (head ? heads[i / 2] : T) <= 1) {
+        if (!strides || (head ? heads[i / 2] : T) <= 1 || heads[i / 2] == 0) {
             out[i] = dense;
             continue;
         }

@@ -39,3 +39,17 @@ def test_positions_that_ints_hold(call, dh, block):
         assert (n - 1) // block * block + block < 2 ** 31 and n + 64 + 48 + 16 < 2 ** 31
     for n in (last + 1, 2 ** 31 - 128, 2 ** 31 - 127, 2 ** 31 - 63, 2 ** 31 - 1, 0, -1):
         assert "max_seq" in message(n)
+
+
+def test_strides_of_no_heads_are_not_read():
+    """With Hkv = 0 neither k nor its strides are used, whatever they hold."""
+    lib = tfm.load()
+
+    def message(Hkv, kt, kh):
+        strides = (ctypes.c_int64 * 8)(256, 64, kt, kh, 256, 64, kt, kh)
+        return _message(lib.tfm_rope_rows(None, None, A, None, A, A, 10, 4, Hkv, 64, 64, 1, strides, 1.0, tfm.TFM_BF16, None))
+
+    for kt, kh in ((0, 0), (-1, 7), (1 << 40, 1 << 40), (128, 64)):
+        assert "NULL pointer" in message(0, kt, kh)
+    assert "k token stride" in message(2, 0, 64) and "k head stride" in message(2, 128, 0)
+    assert "NULL pointer" in message(1, 64, 0)               # the head stride of one head is not read either
