@@ -166,7 +166,7 @@ tfm_status tfm_rope_rows(const void* q, const void* k, void* q_out, void* k_out,
     if (st != TFM_OK) return st;
     if (T == 0) return TFM_OK;
     if (!q || !q_out || (Hkv && (!k || !k_out)) || !positions || !inv_freq) return fail(TFM_EINVAL, "NULL pointer");
-    if (!aligned(q, es) || !aligned(k, es) || !aligned(q_out, es) || !aligned(k_out, es) || !aligned(positions, 4) ||
+    if (!aligned(q, es) || !aligned(q_out, es) || (Hkv && (!aligned(k, es) || !aligned(k_out, es))) || !aligned(positions, 4) ||
         !aligned(inv_freq, 8))
         return fail(TFM_EINVAL, "rows must be aligned to their element size, positions to 4 bytes, inv_freq to 8");
     for (int i = 0; i < 2; ++i)
@@ -224,7 +224,7 @@ tfm_status tfm_cache8_attention(const void* q, const void* k_codes, const void* 
         return fail(TFM_EINVAL, "bad sizes: H %% Hkv == 0, max_new >= 1, B*H*max_new <= 2^24");
     if (!cu_seqlens && B && T / B > max_new) return fail(TFM_EINVAL, "max_new=%d below the T / B = %d rows of a sequence", max_new, T / B);
     if (window < 0) return fail(TFM_EINVAL, "window must be >= 0");
-    // (beyond 2^126 its product with log2(e), by which the kernel scales, leaves fp32)
+    // (the limit of the other attentions; the kernel itself holds scale * log2(e) as mantissa and exponent)
     if (!std::isfinite(scale) || scale > 0x1p126f) return fail(TFM_EINVAL, "scale must be finite and at most 2^126");
     if ((int64_t)(H / Hkv) * max_new > 128) return fail(TFM_EUNSUPPORTED, "8-bit cache attention: (H / Hkv) * max_new <= 128");
     tfm::Cache8AttnArgs a{};

@@ -47,6 +47,7 @@
 // one instruction (no change), runs and zeroed counters from a kernel ahead, the last writer adding the
 // pieces up (+3 to 6 us), deeper rings (+1), the second kernel launched early with its CTAs spread by
 // shared memory (no change).
+#include <cmath>
 #include <type_traits>
 
 #include "cache8.cuh"
@@ -94,7 +95,8 @@ struct Geom {
     int block_rows;           // rows of a job: 8, 16, 24 or 32
     int row_blocks;           // of max_new tokens
     int whole;                // no job is cut; 2: each of max_new tokens has a CTA of its own
-    float scale_log2;
+    float scale_m;            // scale * log2(e) = scale_m 2^scale_e, scale_m in [0.5, 1)
+    int scale_e;
     int64_t sq_t, sq_h, so_t, so_h;
 };
 
@@ -539,9 +541,15 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
                                        fmaxf(fabsf(bf16_lo(raw[x].y)), fabsf(bf16_hi(raw[x].y)))));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // the row times the power of two that brings its largest element to [2^10, 2^11)
+            // The row times the power of two that brings its largest element to [2^10, 2^12), of two such the one
+            // that leaves an even power 2^r for the scores: f = k's scale scale_m 2^r takes them from the products' units.
+            // 2^(r/2) is multiplied twice, so that on the way from the scale to f nothing is larger or smaller than both:
+            // f is right wherever fp32 holds it (it stays below 2^107, as the header limits scale, q and k's scales).
             int e = (int)(__float_as_uint(top) >> 23);
-            e = e == 255 ? 127 : max(e, 10);
+            e = e == 255 ? 127 : max(e, 11);
+            int r2 = e - 127 + gm.scale_e + (E4M3 ? -10 : 14);
+            e -= r2 & 1;
+            r2 = min(max(r2 >> 1, -126), 127);
             const float mul = __uint_as_float((uint32_t)(264 - e) << 23);
             float sum = 0.0f;
 #pragma unroll
@@ -560,7 +568,7 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int from = (2 * t + j) * 4;            // a lane of that row
-                qinv[j] = __uint_as_float((uint32_t)__shfl_sync(0xffffffffu, e, from) << 23);
+                qinv[j] = __uint_as_float((uint32_t)(__shfl_sync(0xffffffffu, r2, from) + 127) << 23);
                 qbias[j] = E4M3 ? 0.0f : __shfl_sync(0xffffffffu, sum, from) * -0x1p-17f;      // 128 of the codes' 2^-24
                 seen_hi[j] = seen[sn & 1][8 * nn + 2 * t + j];
             }
@@ -659,7 +667,7 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
                         inv = qinv[n][j];
                         hi = seen_hi[n][j];
                     }
-                    const float f = ksc * gm.scale_log2 * (E4M3 ? 0x1p-10f : 0x1p14f) * inv;
+                    const float f = ksc * inv * inv;                       // (ksc: times scale_m)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         float& y = c[n][2 * i + j];
@@ -749,7 +757,7 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
                 k64 = scales32(ksp, blk0 + 32);
                 v64 = scales32(vsp, blk0 + 32);
             }
-            const float ksc = __shfl_sync(0xffffffffu, k32, blk), vsc = __shfl_sync(0xffffffffu, v32, blk);
+            const float ksc = __shfl_sync(0xffffffffu, k32, blk) * gm.scale_m, vsc = __shfl_sync(0xffffffffu, v32, blk);
             if (!warp_wait(full + 8 * st, phase, err, &abort_flag)) return;
             // a step whose keys every row sees needs no masks
             if (key >= all_lo && key + 15 <= all_hi) step(std::false_type{}, ksc, vsc);
@@ -1033,7 +1041,7 @@ tfm_status launch_cache8_attention(const Cache8AttnArgs& a, cudaStream_t st, cud
     const int piece = a.dh == 32 ? Ax<32, 1>::kPiece : Ax<64, 1>::kPiece, ctas8 = a.dh == 128 ? Ax<128, 1>::kCtas : Ax<64, 1>::kCtas;
     if (jobs8 * job_units(a, piece) <= (int64_t)16 * ctas8 * sm_count()) gm.block_rows = 8;
     gm.row_blocks = (gm.G * a.max_new + gm.block_rows - 1) / gm.block_rows;
-    gm.scale_log2 = a.scale * 1.4426950408889634f;
+    gm.scale_m = (float)std::frexp((double)a.scale * 1.4426950408889634, &gm.scale_e);
     gm.sq_t = a.strides[0];
     gm.sq_h = a.strides[1];
     gm.so_t = a.strides[2];

@@ -631,7 +631,8 @@ tfm_status tfm_cache8_read(const void* k_codes, const void* v_codes, const float
  * o = softmax(scale * q . k_j) v_j over them, scale <= 0 meaning 1/sqrt(dh).  A row that
  * sees no position (lens[b] < n) gets zeros; rows of no sequence are not written.  What
  * lies in the cache behind lens[b] or before the window is not looked at; codes
- * and scales that are seen must be finite (those tfm_cache8_write stores are).  Scores, maxima and sums are fp32;
+ * and scales that are seen must be finite (those tfm_cache8_write stores are), and scale times a row's largest |q| times 448
+ * times the largest of k's scales below 2^100 (scores are then below 2^108).  Scores, maxima and sums are fp32;
  * a row of q is held in fp16 times a power of two (exact but for elements below 2^-24 of the
  * row's largest, which are rounded to 2^-35 of it), the weights are rounded to fp16 (2^-11
  * relative) for their product with the codes and summed as rounded, the output once to bf16.

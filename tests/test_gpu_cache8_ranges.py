@@ -1,0 +1,40 @@
+"""The 8-bit cache's operators on the GPU at the ends of their ranges, against 64 bits."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from decoder_only_transformer_gb300 import tfm  # noqa: E402
+from test_gpu_cache8_attention import _cache, _call, _check, _q, _with_room  # noqa: E402
+
+BF, I8, E4 = torch.bfloat16, torch.int8, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    tfm.load()
+    yield
+    tfm.device_status()
+
+
+@pytest.mark.parametrize("codes", [I8, E4])
+@pytest.mark.parametrize("H,Hkv,T,dh", [(8, 2, 1, 64), (8, 2, 3, 128), (10, 2, 4, 128), (8, 1, 4, 32)])
+@pytest.mark.parametrize("scale,q_size,k_size", [
+    (2.0 ** 120, -123, 0), (2.0 ** 126, -126, -3), (2.0 ** 126, -130, 1), (2.0 ** 126, 0, -126), (0.0, -124, 124), (0.0, 120, -119),
+    (2.0 ** -13, 125, -115), (2.0 ** -100, 110, -13), (2.0 ** -140, 125, 12), (2.0 ** 60, -120, 57)], ids=str)
+def test_scores_whose_factors_are_far_apart(scale, q_size, k_size, H, Hkv, T, dh, codes):
+    """scale, q and the keys' scales near the ends of fp32, their product of ordinary size; a row of zeros among the others sees
+    the mean of V.  The weights' and values' tolerances are those of ordinary factors: a power of two in each changes nothing
+    but the range.  In a small cache (8 rows a job) and in one with room (up to 32 rows)."""
+    lens, block = [200, 333], 16
+    cache = _cache(31, 2, Hkv, 336, dh, block, codes)
+    cache[2].mul_(2.0 ** k_size)
+    q = (_q(31, 2 * T, H, dh).float() * 2.0 ** q_size).to(BF)
+    q[1 % (2 * T), H - 1] = 0.0
+    q[0, 0] = 0.0
+    for c in (cache, _with_room(cache, block, 128 * (152 * 16 * 3 // 2 // (2 * Hkv) + 4))):
+        o = _call(q, c, lens, block, scale=scale)
+        _check(o, q, cache, lens, block, [T, T], 0, scale or None)
