@@ -38,3 +38,18 @@ def test_scores_whose_factors_are_far_apart(scale, q_size, k_size, H, Hkv, T, dh
     for c in (cache, _with_room(cache, block, 128 * (152 * 16 * 3 // 2 // (2 * Hkv) + 4))):
         o = _call(q, c, lens, block, scale=scale)
         _check(o, q, cache, lens, block, [T, T], 0, scale or None)
+
+
+def test_no_kv_heads():
+    """Hkv = 0: k and k_out are not used, whatever they point to."""
+    import ctypes
+    q = _q(51, 9, 4, 64)
+    inv, pos = tfm.rope_frequencies(10000.0, 64)[0].cuda(), torch.arange(9, dtype=torch.int32, device="cuda")
+    want, o = torch.zeros_like(q), torch.zeros_like(q)
+    tfm.rope_rows(q, None, want, None, pos, inv)
+    odd, strides = ctypes.c_void_p(257), (ctypes.c_int64 * 8)(256, 64, 0, -5, 256, 64, 0, 1 << 60)
+    status = tfm.load().tfm_rope_rows(q.data_ptr(), odd, o.data_ptr(), odd, pos.data_ptr(), inv.data_ptr(), 9, 4, 0, 64, 64, 1,
+                                      strides, 1.0, tfm.TFM_BF16, torch.cuda.current_stream().cuda_stream)
+    assert status == tfm.TFM_OK, tfm.load().tfm_last_error()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want)
