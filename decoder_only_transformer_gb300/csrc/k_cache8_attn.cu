@@ -18,9 +18,10 @@
 //     warp's step, which lies in one block; s_v multiplies the step's 16-key sum of P V as it
 //     is added to the fp32 output.
 //   - a code costs 0.75 to 1 instruction: an int8 byte with its sign bit turned over is the fp16
-//     subnormal (c + 128) 2^-24, and 128 times the sum of q, or of the weights, is taken off the
-//     fp32 sums (it is of their size or below: at most 2^-16 of a step of the code is lost); e4m3 codes
-//     are converted two at a time.
+//     subnormal (c + 128) 2^-24, and 128 times the sum of q, or of the step's weights (one product more), is
+//     taken off inside each product, whose fp32 sums round to 2^-16 or so of a step of the code; what is summed over the
+//     steps has no bias (with the bias left in until the end, the loss grew with the length: 2^-13 of a step after
+//     256 steps of a warp, 2^-11 after 2048); e4m3 codes are converted two at a time.
 //   - the order of the coordinates inside a product of 16, and of the keys inside a step, is
 //     free.  They are taken as 16-byte loads from shared memory bring them (see kappa below):
 //     no transposition, no bank conflicts.
@@ -593,13 +594,13 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
         }
         // acc[n][2 x + h]: rows 8 n + 2 t (elements 0, 2) and + 1 (1, 3), coordinates g DH / 8 + 4 x + 2 h (0, 1) and + 1
         float acc[NT][2 * VW][4];
-        float m[NT][2], l[NT][2], lv[NT][2];                 // lv: the weights' sum with the values' scales (int8)
+        float m[NT][2], l[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int i = 0; i < 2 * VW; ++i) acc[n][i][0] = acc[n][i][1] = acc[n][i][2] = acc[n][i][3] = 0.0f;
             m[n][0] = m[n][1] = -3.402823466e38f;
-            l[n][0] = l[n][1] = lv[n][0] = lv[n][1] = 0.0f;
+            l[n][0] = l[n][1] = 0.0f;
         }
         // positions that some row sees, that every row sees
         const int any_lo = gm.window > 0 ? max(0, len - news - gm.window + 1) : 0;
@@ -690,7 +691,6 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
                         const float keep = ex2(m[n][j] - y);
                         m[n][j] = y;
                         l[n][j] *= keep;
-                        lv[n][j] *= keep;
 #pragma unroll
                         for (int i = 0; i < 2 * VW; ++i) {
                             acc[n][i][j] *= keep;
@@ -713,10 +713,14 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
                 }
                 l[n][0] += s0;
                 l[n][1] += s1;
-                if (!E4M3) {
-                    lv[n][0] = fmaf(vsc, s0, lv[n][0]);
-                    lv[n][1] = fmaf(vsc, s1, lv[n][1]);
-                }
+            }
+            // What the codes' bias of 128 adds to the products below, taken off inside them, so that what is summed over the
+            // steps has none: -2^-17 (in fp16, as the codes) times the sum of the weights, in the lanes that need it.
+            float z[NT][4] = {};
+            if constexpr (!E4M3) {
+                const uint32_t bias[4] = {0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816(z[n], bias, pb[n][0], pb[n][1], 0.0f, 0.0f, 0.0f, 0.0f);
             }
             uint32_t vw[4][VW];
 #pragma unroll
@@ -740,7 +744,7 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         float d[4];
-                        mma16816(d, a, pb[n][0], pb[n][1], 0.0f, 0.0f, 0.0f, 0.0f);
+                        mma16816(d, a, pb[n][0], pb[n][1], z[n][0], z[n][1], z[n][2], z[n][3]);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) acc[n][2 * x + h][j] = fmaf(vsc, d[j], acc[n][2 * x + h][j]);
                     }
@@ -776,16 +780,12 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) {
                     l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], d);
-                    if (!E4M3) lv[n][j] += __shfl_xor_sync(0xffffffffu, lv[n][j], d);
                 }
                 const int r = 2 * t + j;
 #pragma unroll
                 for (int x = 0; x < VW; ++x) {
                     float4 v = make_float4(acc[n][2 * x][j], acc[n][2 * x][2 + j], acc[n][2 * x + 1][j], acc[n][2 * x + 1][2 + j]);
-                    if (!E4M3) {
-                        const float b = lv[n][j] * -128.0f;
-                        v = make_float4(fmaf(v.x, 0x1p24f, b), fmaf(v.y, 0x1p24f, b), fmaf(v.z, 0x1p24f, b), fmaf(v.w, 0x1p24f, b));
-                    }
+                    if (!E4M3) v = make_float4(v.x * 0x1p24f, v.y * 0x1p24f, v.z * 0x1p24f, v.w * 0x1p24f);
                     buf[kw * 8 * (DH / 4) + buf_at<DH>(r, g * VW + x)] = v;
                 }
                 if (g == 0) ml[kw * 8 + r] = make_float2(m[n][j], l[n][j]);

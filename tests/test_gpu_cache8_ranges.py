@@ -53,3 +53,26 @@ def test_no_kv_heads():
     assert status == tfm.TFM_OK, tfm.load().tfm_last_error()
     torch.cuda.synchronize()
     assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("codes", [I8, E4])
+@pytest.mark.parametrize("B,n,H,Hkv,dh", [(64, 4096, 8, 8, 64), (128, 8192, 8, 8, 32), (40, 4096, 64, 8, 128), (40, 4096, 128, 8, 128),
+                                          (40, 4096, 192, 8, 64), (40, 4096, 256, 8, 128)])
+def test_values_that_cancel_over_long_runs(B, n, H, Hkv, dh, codes):
+    """Scores are equal, and every other tile holds the codes of the one before with the other sign, at the same scale: what a
+    warp adds up is x, 0, x, 0 ..  Inside a step sums are of whole multiples of 2^-17 (int8: products up to 255 2^7 2^-24, and the
+    bias of 16 times 128 of them) or 2^-2 (e4m3), fewer than 2^24 of them: exact in any order.  So an output is zero but for the
+    tiles that a cut leaves without the other one: two parts, or four of a warp each, of at most 127 steps of one tile in n / 64,
+    in 8 roundings of 2^-24: below 2^-19 of a step of the code for 64 tiles, and 2^-17 is asked for."""
+    g = torch.Generator(device="cuda").manual_seed(dh)
+    c = torch.randint(-127, 128, (B, Hkv, n // 128, 1, 64, dh), generator=g, device="cuda", dtype=torch.int8).float()
+    if codes == E4:
+        c = (c / 16).round()                                  # up to 8: exact
+    cache = [torch.zeros(B, Hkv, n, dh, dtype=torch.int8, device="cuda").view(codes),
+             torch.cat([c, -c], 3).view(B, Hkv, n, dh).to(codes),
+             *((1 + torch.rand(B, Hkv, n // 128, generator=g, device="cuda")) / 50 for _ in "kv")]
+    q = torch.randn(B, H, dh, generator=g, device="cuda").to(BF)
+    o = _call(q, cache, [n] * B, 128)
+    step = cache[3].amax(-1)[:, :, None].expand(B, Hkv, H // Hkv).reshape(B, H, 1)
+    worst = float((o.float().abs() / step).max())
+    assert worst <= 2.0 ** -17, np.log2(worst)
