@@ -506,7 +506,11 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
         const int last_blk = len > 0 ? (len - 1) >> gm.shift : 0;
         // The scales of 32 blocks, one in each lane, and of the next 32 (read past L1: as in k_cache8.cu).
         int blk0 = s.key >> gm.shift;
-        const auto scales32 = [&](const float* at, int first) { return __ldcg(at + min(first + lane, last_blk)); };
+        // positions that some row sees, that every row sees
+        const int any_lo = gm.window > 0 ? max(0, len - news - gm.window + 1) : 0;
+        const int all_lo = gm.window > 0 ? len - gm.window : 0, all_hi = len - news;
+        const int first_blk = any_lo >> gm.shift;
+        const auto scales32 = [&](const float* at, int first) { return __ldcg(at + min(max(first + lane, first_blk), last_blk)); };
         float k32 = scales32(ksp, blk0), v32 = scales32(vsp, blk0);
         float k64 = scales32(ksp, blk0 + 32), v64 = scales32(vsp, blk0 + 32);
         // q: row r of the job is token r / G, head r % G.  Lane (g, t) holds row 8 n + g, for the products, of
@@ -602,9 +606,11 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
             m[n][0] = m[n][1] = -3.402823466e38f;
             l[n][0] = l[n][1] = 0.0f;
         }
-        // positions that some row sees, that every row sees
-        const int any_lo = gm.window > 0 ? max(0, len - news - gm.window + 1) : 0;
-        const int all_lo = gm.window > 0 ? len - gm.window : 0, all_hi = len - news;
+        // Weights times values are summed as they are (int8 products are in 2^-24), up to scales of kLarge: weights of up to 2^15
+        // and 2^31 keys then stay within fp32.  From the first larger scale on they are summed in units of 2^64.  (32 blocks are
+        // looked at together, outside the loop over their tiles: looked at inside, drafted tokens took 23.3 us for 22.2.)
+        constexpr float kUnit = E4M3 ? 1.0f : 0x1p24f, kLarge = 0x1p64f, kDown = 0x1p-64f;
+        bool large = false;
         const auto step = [&](auto edge, float ksc, float vsc) {
             constexpr bool EDGE = decltype(edge)::value;
             const uint8_t* kt = sm + st * 2 * X::kTile;
@@ -751,24 +757,37 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
                 }
             }
         };
-        for (int tile = 0; tile < tiles; ++tile, key += kTileKeys) {
-            int blk = min(key >> gm.shift, last_blk) - blk0;
-            if (blk >= 32) {                                 // (a tile has at most 4 blocks)
-                blk -= 32;
-                blk0 += 32;
-                k32 = k64;
-                v32 = v64;
-                k64 = scales32(ksp, blk0 + 32);
-                v64 = scales32(vsp, blk0 + 32);
+        // 32 blocks at a time, of which a tile has at most 4
+        int end = min(tiles, ((32 << gm.shift) - (s.key - (blk0 << gm.shift))) / kTileKeys);
+        for (int tile = 0;;) {
+            if (!large && __any_sync(0xffffffffu, fabsf(v32) > kLarge)) {
+                large = true;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2 * VW; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[n][i][j] *= kDown;
             }
-            const float ksc = __shfl_sync(0xffffffffu, k32, blk) * gm.scale_m, vsc = __shfl_sync(0xffffffffu, v32, blk);
-            if (!warp_wait(full + 8 * st, phase, err, &abort_flag)) return;
-            // a step whose keys every row sees needs no masks
-            if (key >= all_lo && key + 15 <= all_hi) step(std::false_type{}, ksc, vsc);
-            else if (key < len && key + 16 > any_lo) step(std::true_type{}, ksc, vsc);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(empty + 8 * st);
-            if (++st == X::kStages) st = 0, phase ^= 1;
+            v32 *= large ? kUnit * kDown : kUnit;
+            for (; tile < end; ++tile, key += kTileKeys) {
+                const int blk = min(key >> gm.shift, last_blk) - blk0;
+                const float ksc = __shfl_sync(0xffffffffu, k32, blk) * gm.scale_m, vsc = __shfl_sync(0xffffffffu, v32, blk);
+                if (!warp_wait(full + 8 * st, phase, err, &abort_flag)) return;
+                // a step whose keys every row sees needs no masks
+                if (key >= all_lo && key + 15 <= all_hi) step(std::false_type{}, ksc, vsc);
+                else if (key < len && key + 16 > any_lo) step(std::true_type{}, ksc, vsc);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + 8 * st);
+                if (++st == X::kStages) st = 0, phase ^= 1;
+            }
+            if (tile == tiles) break;
+            end = min(tiles, tile + (32 << gm.shift) / kTileKeys);
+            blk0 += 32;
+            k32 = k64;
+            v32 = v64;
+            k64 = scales32(ksp, blk0 + 32);
+            v64 = scales32(vsp, blk0 + 32);
         }
         // The four warps' parts, added up, 8 rows at a time.
 #pragma unroll
@@ -784,11 +803,11 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
                 const int r = 2 * t + j;
 #pragma unroll
                 for (int x = 0; x < VW; ++x) {
-                    float4 v = make_float4(acc[n][2 * x][j], acc[n][2 * x][2 + j], acc[n][2 * x + 1][j], acc[n][2 * x + 1][2 + j]);
-                    if (!E4M3) v = make_float4(v.x * 0x1p24f, v.y * 0x1p24f, v.z * 0x1p24f, v.w * 0x1p24f);
+                    const float4 v = make_float4(acc[n][2 * x][j], acc[n][2 * x][2 + j], acc[n][2 * x + 1][j], acc[n][2 * x + 1][2 + j]);
                     buf[kw * 8 * (DH / 4) + buf_at<DH>(r, g * VW + x)] = v;
                 }
-                if (g == 0) ml[kw * 8 + r] = make_float2(m[n][j], l[n][j]);
+                // (a part in units of 2^64 has a negative sum)
+                if (g == 0) ml[kw * 8 + r] = make_float2(m[n][j], large ? -l[n][j] : l[n][j]);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bfull);
@@ -797,32 +816,35 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
                 const int r = e / (DH / 4), f = e % (DH / 4);
                 if (8 * n + r >= nrows) break;
                 float2 x[4];
-                float top = -3.402823466e38f;
+                float top = -3.402823466e38f, least = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     x[i] = ml[i * 8 + r];
                     top = fmaxf(top, x[i].x);
+                    least = fminf(least, x[i].y);
                 }
                 float sum = 0.0f;
                 float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float k = ex2(x[i].x - top);
+                    float k = ex2(x[i].x - top);
                     const float4 y = buf[i * 8 * (DH / 4) + buf_at<DH>(r, f)];
-                    sum = fmaf(k, x[i].y, sum);
+                    sum = fmaf(k, fabsf(x[i].y), sum);
+                    if (least < 0.0f && x[i].y >= 0.0f) k *= kDown;
                     v.x = fmaf(k, y.x, v.x);
                     v.y = fmaf(k, y.y, v.y);
                     v.z = fmaf(k, y.z, v.z);
                     v.w = fmaf(k, y.w, v.w);
                 }
                 if (s.piece < 0) {
-                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    if (least < 0.0f) inv *= 1.0f / kDown;
                     __nv_bfloat16* at = o + orow[sn & 1][8 * n + r] + f * 4;
                     *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
                 } else {
                     const int64_t pr = (int64_t)s.piece * gm.block_rows + 8 * n + r;
                     part_o[pr * (DH / 4) + f] = v;
-                    if (f == 0) part_ml[pr] = make_float2(top, sum);
+                    if (f == 0) part_ml[pr] = make_float2(top, least < 0.0f ? -sum : sum);
                 }
             }
             __syncwarp();
@@ -835,7 +857,8 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
 // Joins the pieces of the jobs that runs cut.  A job of P pieces has P - 1 boundaries of runs inside
 // it; CTA i takes that before run i + 1 and with it a share of the job's rows, in
 // float4s, kJoin of them at least.  The pieces are taken by the groups of threads in turn and
-// added in an order that depends on their number alone.  (256 threads: drafted tokens 23.4 for 21.9 us, windowed 20.5 for 20.0;
+// added in an order that depends on their number alone.  Pieces in units of 2^64 (their sums are negative) bring the others to
+// these units.  (256 threads: drafted tokens 23.4 for 21.9 us, windowed 20.5 for 20.0;
 // 64: 64 chats 32.0 for 30.6; eight entries at least: 131072 positions 28.6 for 28.1.)
 constexpr int kJoin = 4, kJoinThreads = 128;
 template <int DH>
@@ -843,6 +866,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     k_cache8_join(const Cut* __restrict__ cuts, const float2* __restrict__ part_ml, const float4* __restrict__ part_o,
                   __nv_bfloat16* __restrict__ o, const Geom gm) {
     constexpr int F = DH / 4;
+    constexpr float kDown = 0x1p-64f;
     __shared__ float4 sum_o[kJoinThreads];
     __shared__ float2 sum_ml[kJoinThreads];
     pdl_wait();
@@ -865,6 +889,7 @@ __global__ void __launch_bounds__(kJoinThreads)
         const int r = e / F, f = e % F;
         float top = -3.402823466e38f, sum = 0.0f;
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        bool large = false;
         for (int p0 = gr; p0 < pieces && e < e1; p0 += 4 * groups) {         // four at a time: their loads together
             float2 x[4];
             float4 y[4];
@@ -882,15 +907,25 @@ __global__ void __launch_bounds__(kJoinThreads)
             const float nt = fmaxf(fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)), top), k0 = ex2(top - nt);
             sum *= k0;
             v = make_float4(v.x * k0, v.y * k0, v.z * k0, v.w * k0);
+            if (large || fminf(fminf(x[0].y, x[1].y), fminf(x[2].y, x[3].y)) < 0.0f) {
+                if (!large) v = make_float4(v.x * kDown, v.y * kDown, v.z * kDown, v.w * kDown);
+                large = true;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (x[k].y >= 0.0f) y[k] = make_float4(y[k].x * kDown, y[k].y * kDown, y[k].z * kDown, y[k].w * kDown);
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float w = ex2(x[k].x - nt);
-                sum = fmaf(w, x[k].y, sum);
+                sum = fmaf(w, fabsf(x[k].y), sum);
                 v = make_float4(fmaf(w, y[k].x, v.x), fmaf(w, y[k].y, v.y), fmaf(w, y[k].z, v.z), fmaf(w, y[k].w, v.w));
             }
             top = nt;
         }
-        // a warp's groups, then the warps
+        // a warp's groups, then the warps, whose units are one if any is large
+        const bool was = large;
+        large = __syncthreads_or(large);
+        if (large && !was) v = make_float4(v.x * kDown, v.y * kDown, v.z * kDown, v.w * kDown);
         for (int d = width; d < 32; d <<= 1) {
             const float t1 = __shfl_xor_sync(0xffffffffu, top, d), s1 = __shfl_xor_sync(0xffffffffu, sum, d);
             const float4 y = make_float4(__shfl_xor_sync(0xffffffffu, v.x, d), __shfl_xor_sync(0xffffffffu, v.y, d),
@@ -917,7 +952,8 @@ __global__ void __launch_bounds__(kJoinThreads)
                 den = fmaf(w, x.y, den);
                 v = make_float4(fmaf(w, y.x, v.x), fmaf(w, y.y, v.y), fmaf(w, y.z, v.z), fmaf(w, y.w, v.w));
             }
-            const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+            float inv = den == 0.0f ? 0.0f : 1.0f / den;
+            if (large) inv *= 1.0f / kDown;
             const int rr = h.rb * gm.block_rows + r;
             __nv_bfloat16* to = o + ((int64_t)h.row0 + rr / gm.G) * gm.so_t + (int64_t)(h.kvh * gm.G + rr % gm.G) * gm.so_h + f * 4;
             *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));

@@ -76,3 +76,52 @@ def test_values_that_cancel_over_long_runs(B, n, H, Hkv, dh, codes):
     step = cache[3].amax(-1)[:, :, None].expand(B, Hkv, H // Hkv).reshape(B, H, 1)
     worst = float((o.float().abs() / step).max())
     assert worst <= 2.0 ** -17, np.log2(worst)
+
+
+@pytest.mark.parametrize("codes", [I8, E4])
+@pytest.mark.parametrize("size", [120, 116, 112, 100, 64, -60, -100, -115])
+def test_values_of_any_size(size, codes):
+    """Values of up to 2^125 and down to 2^-126: the mean of values is no larger than the largest, and it comes out as precise
+    as any, whether jobs are cut or whole, in jobs of 8 and of up to 32 rows, over thousands of positions, and where the
+    running maximum lags behind (the weights are then 2^15)."""
+    for lens, H, Hkv, T, dh, block, window, room in (
+            ([1, 5], 8, 2, 1, 64, 16, 0, 0), ([200, 333], 8, 2, 3, 128, 16, 0, 0), ([20000, 70], 8, 1, 1, 64, 128, 0, 0),
+            ([3000, 1], 4, 4, 1, 32, 16, 100, 0), ([256, 130], 16, 2, 2, 128, 32, 0, 300000), ([256, 130], 10, 2, 4, 128, 32, 0, 300000),
+            ([256, 130], 8, 1, 4, 64, 32, 0, 300000)):
+        n = 256 if room else max(lens) + 3
+        cache = _cache(41, 2, Hkv, n, dh, block, codes)
+        cache[3].mul_(2.0 ** size)
+        q = _q(41, 2 * T, H, dh)
+        wide = _with_room(cache, block, room // block * block) if room else cache
+        _check(_call(q, wide, lens, block, window=window), q, cache, lens, block, [T, T], window)
+        # the first 16 scores are 0, all others 5.4 (7.8 in powers of two)
+        cache[0].zero_(), cache[2].fill_(2.0 ** -4)
+        cache[0][:, :, 16:, 0] = 64.0 if codes == E4 else 64
+        q.zero_()
+        q[:, :, 0] = 1.35
+        wide = _with_room(cache, block, room // block * block) if room else cache
+        _check(_call(q, wide, lens, block, window=window, scale=1.0), q, cache, lens, block, [T, T], window, 1.0)
+
+
+@pytest.mark.parametrize("codes", [I8, E4])
+def test_values_of_one_block_far_above_the_others(codes):
+    """Blocks of 2^110 and 2^120 among ordinary ones, early, late and between, in small and in cut jobs; rows that see none of
+    them, beside rows that do, have the precision of ordinary ones."""
+    for lens, H, Hkv, T, dh in (([200, 337], 8, 2, 3, 128), ([20000, 17], 8, 1, 1, 64), ([337, 49], 4, 2, 8, 32)):
+        for where in (slice(0, 1), slice(2, 4), slice(11, 12), slice(15, 22), slice(0, 1 << 20)):
+            for far in (2.0 ** 70, 2.0 ** 110, 2.0 ** 120):
+                cache = _cache(43, 2, Hkv, max(lens) + 3, dh, 16, codes)
+                cache[3][:, :, where] *= far
+                q = _q(43, 2 * T, H, dh)
+                _check(_call(q, cache, lens, 16), q, cache, lens, 16, [T, T])
+    # the last of T tokens begins a block of its own
+    for T, H, Hkv in ((2, 8, 2), (4, 8, 2), (8, 16, 4)):
+        lens, block = [97, 337], 16
+        cache = _cache(44, 2, Hkv, 340, 64, block, codes)
+        for b, n in enumerate(lens):
+            cache[3][b, :, n // block] = 2.0 ** 118
+        q = _q(44, 2 * T, H, 64)
+        o = _call(q, cache, lens, block)
+        _check(o, q, cache, lens, block, [T, T])
+        before, qb = (x.view(2, T, H, 64)[:, :-1].reshape(-1, H, 64) for x in (o, q))
+        _check(before, qb, cache, [n - 1 for n in lens], block, [T - 1, T - 1])
