@@ -603,7 +603,8 @@ tfm_status tfm_rope_rows(const void* q, const void* k, void* q_out, void* k_out,
  * to even, as decided without rounding the quotient.  So a sequence may be cut back (drafted tokens refused): the
  * next rows overwrite what was there.  What lies behind lens[b] in its last block keeps its
  * codes and is not looked at.  NaN is stored as 0 and an infinity as the largest code (their block's
- * scale is that of its finite values), and either sets TFM_EINVAL in the device error word.
+ * scale is that of its finite values; where these are all 0, so are the scale and the code), and either sets TFM_EINVAL in
+ * the device error word.
  * So do offsets that decrease or leave [0, T], lens[b] outside [0, max_seq] and more rows than
  * lens[b]: nothing is then written for that sequence (nor, perhaps, for others if offsets are
  * not in order), and nothing outside the buffers is touched.

@@ -125,3 +125,27 @@ def test_values_of_one_block_far_above_the_others(codes):
         _check(o, q, cache, lens, block, [T, T])
         before, qb = (x.view(2, T, H, 64)[:, :-1].reshape(-1, H, 64) for x in (o, q))
         _check(before, qb, cache, [n - 1 for n in lens], block, [T - 1, T - 1])
+
+
+@pytest.mark.parametrize("codes", [I8, E4])
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_an_infinity_among_zeros(dtype, codes):
+    """A block without a finite value but zeros has the scale 0 and the code 0 for the infinity too: when a later token gives the
+    block a scale, it stays 0, as all values that a block holds stay what they are."""
+    for bad in (float("inf"), -float("inf"), float("nan")):
+        kc, vc, ks, vs = _cache(52, 1, 2, 64, 64, 32, codes)
+        k = torch.zeros(20, 2, 64, dtype=dtype, device="cuda")
+        k[7, 1, 3] = bad
+        for rows, n in ((k, 20), (torch.ones(1, 2, 64, dtype=dtype, device="cuda"), 21)):
+            tfm.cache8_write(rows, rows, kc, vc, ks, vs, torch.tensor([n], dtype=torch.int32, device="cuda"), 32)
+            torch.cuda.synchronize()
+            if n == 20:
+                with pytest.raises(tfm.TfmError) as e:
+                    tfm.device_status()
+                assert e.value.status == tfm.TFM_EINVAL
+                assert (ks[:, :, 0] == 0).all() and (vs[:, :, 0] == 0).all()
+            for c in (kc, vc):
+                assert (c.float()[:, :, :20] == 0).all()
+        tfm.device_status()
+        top = 127 if codes == I8 else 448.0
+        assert (kc.float()[:, :, 20] == top).all() and (ks[:, :, 0] == (torch.ones(1) / top).cuda()).all()
