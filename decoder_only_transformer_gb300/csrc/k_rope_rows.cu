@@ -21,6 +21,9 @@
 // 0.87 of a copy's bandwidth).  No barrier: with the sines of 16 tokens shared by a CTA, sines and
 // rows took turns (62 to 72 us), and with sines in registers, a thread for one vector of all
 // heads, too few bytes were on their way (85 us).
+#include <cstring>
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -77,6 +80,18 @@ struct __align__(VE * sizeof(T)) Elems {
     T v[VE];
 };
 
+// Rows are read past the L1 cache, as in k_cache8.cu: a launch that overlaps the end of the one before may share an SM with
+// its reads of lines that other SMs went on to write (rows of 40 bytes, say, turned in place).
+template <typename V>
+__device__ __forceinline__ V past_l1(const V* p) {
+    using R = std::conditional_t<sizeof(V) == 16, uint4, std::conditional_t<sizeof(V) == 8, uint2,
+              std::conditional_t<sizeof(V) == 4, unsigned, unsigned short>>>;
+    const R r = __ldcg(reinterpret_cast<const R*>(p));
+    V v;
+    memcpy(&v, &r, sizeof v);
+    return v;
+}
+
 template <typename T>
 __device__ __forceinline__ void turn_pair(T& x, T& y, float2 r) {
     const float a = as_f32(x), b = as_f32(y);
@@ -125,8 +140,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
                 Vec lo, hi;
                 if (live) {
                     const T* src = (isq ? q : k) + (int64_t)t * g.s[isq ? 0 : 2] + (int64_t)hh * g.s[isq ? 1 : 3] + e;
-                    lo = *reinterpret_cast<const Vec*>(src);
-                    if (!INTER && pairs) hi = *reinterpret_cast<const Vec*>(src + half);
+                    lo = past_l1(reinterpret_cast<const Vec*>(src));
+                    if (!INTER && pairs) hi = past_l1(reinterpret_cast<const Vec*>(src + half));
                 }
                 if (!sined) {                                          // the whole warp, once a token
                     sined = true;
@@ -184,10 +199,10 @@ __global__ void __launch_bounds__(kRopeThreads)
             const T* src = (isq ? q : k) + (int64_t)(t0 + t) * g.s[isq ? 0 : 2] + (int64_t)hh * g.s[isq ? 1 : 3];
             T* dst = (isq ? qo : ko) + (int64_t)(t0 + t) * g.s[isq ? 4 : 6] + (int64_t)hh * g.s[isq ? 5 : 7];
             if (x >= half) {
-                dst[x + half] = src[x + half];
+                dst[x + half] = past_l1(src + x + half);
             } else {
                 const int a = INTER ? 2 * x : x, b = INTER ? 2 * x + 1 : x + half;
-                T va = src[a], vb = src[b];
+                T va = past_l1(src + a), vb = past_l1(src + b);
                 turn_pair(va, vb, cs[t * half + x]);
                 dst[a] = va;
                 dst[b] = vb;

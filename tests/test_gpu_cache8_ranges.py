@@ -149,3 +149,40 @@ def test_an_infinity_among_zeros(dtype, codes):
         tfm.device_status()
         top = 127 if codes == I8 else 448.0
         assert (kc.float()[:, :, 20] == top).all() and (ks[:, :, 0] == (torch.ones(1) / top).cuda()).all()
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("T,H,Hkv,dh,rot", [(1, 5, 5, 20, 20), (7, 3, 1, 20, 20), (300, 5, 5, 20, 20), (4000, 3, 3, 20, 20),
+                                            (2000, 3, 2, 36, 12), (3000, 3, 3, 10, 2), (500, 7, 1, 6, 2)])
+def test_rotations_behind_one_another_as_calls_apart(T, H, Hkv, dh, rot, interleaved):
+    """In place, where rows of neighbouring tokens and heads share a sector of memory, at accesses of 8, 4 and 2 bytes: the bits
+    of the same calls with the device waited for in between."""
+    g = torch.Generator().manual_seed(T)
+    rows = torch.randn(T, H + Hkv, dh, generator=g).to(BF).cuda()
+    inv = tfm.rope_frequencies(10000.0, rot)[0].cuda()
+    positions = [torch.randint(-1000, 1000, (T,), generator=g, dtype=torch.int32).cuda() for _ in range(12)]
+
+    def rotate(x, wait):
+        q, k = x.split((H, Hkv), 1)
+        for p in positions:
+            tfm.rope_rows(q, k, q, k, p, inv, interleaved=interleaved)
+            if wait:
+                torch.cuda.synchronize()
+
+    want = rows.clone()
+    rotate(want, True)
+    x = rows.clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s), torch.cuda.graph(graph, stream=s):
+        rotate(x, False)
+    for recorded in (False, True, True, True):
+        x.copy_(rows)
+        torch.cuda.synchronize()
+        if recorded:
+            graph.replay()
+        else:
+            rotate(x, False)
+        torch.cuda.synchronize()
+        assert torch.equal(x.view(torch.int16), want.view(torch.int16))
