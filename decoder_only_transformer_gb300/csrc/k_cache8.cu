@@ -29,6 +29,7 @@ namespace tfm {
 namespace {
 
 constexpr int kMaxThreads8 = 256;
+static_assert(kMaxThreads8 % 256 == 0, "the up to 8 warps of a unit meet at a barrier: a CTA holds whole units");
 constexpr int kAtOnce = 95;           // sequences whose offsets and lengths a warp looks at together
 
 struct Geom8 {
