@@ -19,9 +19,9 @@
 // block at either end.  Neighbouring warps take neighbouring heads, whose rows lie side by side
 // (CTAs of 4 units where 8 fit: 20 for 15 us).
 //
-// Measured (graph replays): 32768 tokens of 4 x 128, bf16 and e4m3: written in 22.4 us (4.5 TB/s; issue
-// slots 60 %), read back in 18.1 (5.6); 24 prompts of up to 1024 tokens of 12 x 64, int8, blocks of 16:
-// 15.1 and 11.0 us; one token of each of 64 sequences: 5.5 us.
+// Measured (graph replays): 32768 tokens of 4 x 128, bf16 and e4m3: written in 23.0 us (4.4 TB/s; issue
+// slots 60 %), read back in 18.4 (5.5); from and to fp32 rows 34.9 and 37.9; 24 prompts of up to 1024 tokens of 12 x 64, int8,
+// blocks of 16: 15.4 and 11.0 us (fp32: 19.2 and 19.1); one token of each of 64 sequences: 5.5 us.
 #include "cache8.cuh"
 
 namespace tfm {
@@ -54,8 +54,12 @@ __device__ __forceinline__ SeqRows find_seq(const int32_t* __restrict__ cu, cons
     const int lane = threadIdx.x & 31;
     int lo = 0;
     if (g.B > 32 && g.B <= kAtOnce) {
-        // all of them at once, lengths too: one wait instead of three (64 sequences: write of a token 6.2 -> 5.5 us, read
-        // 13.6 -> 13.0; up to 32 have two waits otherwise and fewer instructions, 24 prompts 23.9 for 24.7)
+        // All of them at once, lengths too: one wait instead of three, in more instructions.  At once against step by step (us), a
+        // token's write and read of up to 600 of 4 x 128, and prompts of 12 x 64 in blocks of 16 written and read: 24 sequences
+        // 4.1 for 4.1, 6.2 for 5.5, 15.8 for 15.3, 11.7 for 11.0; 48: 4.8 for 4.8, 10.3 for 10.9, 15.7 for 16.4, 11.6 for 11.7;
+        // 64: 5.5 for 5.5, 13.0 for 13.4, 14.6 for 15.1, 11.0 for 11.0; 95: 6.9 for 6.9, 17.9 for 18.5, 14.3 for 14.4, 10.3 for
+        // 10.3; with a fourth word of a lane, 96: 7.5 for 6.9, 18.5 for 18.7, 14.4 for 14.4, 11.0 for 10.3; 127: 8.3 for 8.3, 24.0
+        // for 24.2, 15.3 for 15.1, 11.7 for 11.0.
         constexpr int N = (kAtOnce + 1) / 32;
         int a[N], len[N];
 #pragma unroll

@@ -16,7 +16,8 @@
 //     for elements below 2^-24 of its largest).
 //   - the scales are not multiplied into the codes: s_k is one factor of the 16 scores of a
 //     warp's step, which lies in one block; s_v multiplies the step's 16-key sum of P V as it
-//     is added to the fp32 output.
+//     is added to the fp32 output, whose unit is 2^64 from the first s_v above 2^64 on (sums over 2^31 keys of values
+//     near the largest would leave fp32).
 //   - a code costs 0.75 to 1 instruction: an int8 byte with its sign bit turned over is the fp16
 //     subnormal (c + 128) 2^-24, and 128 times the sum of q, or of the step's weights (one product more), is
 //     taken off inside each product, whose fp32 sums round to 2^-16 or so of a step of the code; what is summed over the
@@ -26,7 +27,7 @@
 //     free.  They are taken as 16-byte loads from shared memory bring them (see kappa below):
 //     no transposition, no bank conflicts.
 //   - the running maximum of a row moves only when a score exceeds it by 2^8: weights are
-//     2^(x - m + 7), below 2^15 and so fp16 numbers; what is flushed to zero is below 2^-31
+//     2^(x - m + 7), below 2^15 and so fp16 numbers; what is flushed to zero is below 2^-32
 //     of the largest weight.
 //
 // Tiles of 64 keys (K and V, by TMA, a ring of them filled by a warp of its own, which also hands over
@@ -37,9 +38,10 @@
 // order.  Short caches are not cut, and need no second kernel.
 //
 // Measured (graph replays; GB/s of the bytes that count): 64 chats of up to 4096 positions, 16/4 x 128,
-// int8: 30.4 us, 4.4 TB/s; 131072 positions of one, e4m3: 28.2 us, 4.7 TB/s; 32 x 16 caches of 64
-// with a window of 1024: 20.0 us; up to 5 new tokens of 16 over up to 8192: 21.9 us; 4 chats under
-// 511: 6.8 us.  Of each but the last ~2 us pass until the first tile is asked for (lengths, runs, q),
+// int8: 30.3 us, 4.4 TB/s; 131072 positions of one, e4m3: 28.0 us, 4.8 TB/s; 32 x 16 caches of 64
+// with a window of 1024: 20.5 us; up to 5 new tokens of 16 over up to 8192: 22.4 us (int8: 23.9); 8 of them, 32 rows:
+// 31.8 (int8: 35.1, whose kernel spills); 4 chats under 511: 6.9 us (8.9 where the cache has room for 8192: what is cut
+// is decided by the capacity).  Of each but the last ~2 us pass until the first tile is asked for (lengths, runs, q),
 // ~2 until it is there, ~1.5 with the last sums, ~3 with the second kernel; in between memory is
 // nearly full for up to 8 rows, and a step's latency (~1500 cycles at 24 rows, two warps a
 // scheduler) counts for more.  Tried and slower: the values' scales in the weights' exponents (P V without
@@ -141,7 +143,11 @@ __device__ __forceinline__ int run_of(int u, int total, int runs) {      // the 
 // Runs of at least kLeast units.  A job has kPiece units (what it costs beside its tiles), then one
 // for each tile; a run that ends among the first ones has none of the job's tiles.
 constexpr int kLeast = 3;
-constexpr int kWhole = 14;        // units of a job that is not worth cutting (see launch_part)
+// Units of a job that is not worth cutting.  A CTA for each job against cut jobs and their join (us), caches of 12 to 13 units /
+// 15 / 17 / 20 / 23: 4 x 12 of 64 6.8 for 8.3 / 7.6 for 8.9 / 8.2 for 8.9 / 9.6 for 8.9 / 10.3 for 8.9; 16 x 4 of 128 7.6 for 9.6 /
+// 8.9 for 9.6 / 9.6 for 9.6 / 11.3 for 9.6; one sequence of 4 x 128 7.5 for 8.9 / 8.9 for 8.9 / 9.6 for 8.9; 188 x 12 of 64 26.6 for
+// 28.0 / 32.5 for 32.8 / 36.2 for 35.7.  Never slower up to 15, and 14 is below that: capacities are longer than their sequences.
+constexpr int kWhole = 14;
 __device__ __forceinline__ int run_count(int total, int ctas) { return max(1, min(ctas, total / kLeast)); }
 
 // The run's place among the jobs: sequence b, job j of it (kv head j / blocks, row block
@@ -1072,7 +1078,7 @@ tfm_status launch_cache8_attention(const Cache8AttnArgs& a, cudaStream_t st, cud
     gm.block_rows = job_rows(gm.G, a.max_new);
     // Where even full caches are no more than 16 units for each CTA, rows on more CTAs are faster than tiles read once: 5
     // tokens of 16/4 x 128 over 300 positions 10.7 -> 6.9 us, of 4 sequences over 4000 13.9 -> 12.4 (10 units), over 8192
-    // 15.9 -> 16.3 (21).
+    // 15.9 -> 16.3 (21).  (Full caches: in one of 8192 positions 5 tokens over 300 take 9.6 us, in one of 131072 13.7.)
     const int64_t jobs8 = (int64_t)a.B * a.Hkv * ((gm.G * a.max_new + 7) / 8);
     const int piece = a.dh == 32 ? Ax<32, 1>::kPiece : Ax<64, 1>::kPiece, ctas8 = a.dh == 128 ? Ax<128, 1>::kCtas : Ax<64, 1>::kCtas;
     if (jobs8 * job_units(a, piece) <= (int64_t)16 * ctas8 * sm_count()) gm.block_rows = 8;

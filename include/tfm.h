@@ -635,9 +635,10 @@ tfm_status tfm_cache8_read(const void* k_codes, const void* v_codes, const float
  * and scales that are seen must be finite (those tfm_cache8_write stores are), and scale times a row's largest |q| times 448
  * times the largest of k's scales below 2^100 (scores are then below 2^108).  Scores, maxima and sums are fp32;
  * a row of q is held in fp16 times a power of two (exact but for elements below 2^-24 of the
- * row's largest, which are rounded to 2^-35 of it), the weights are rounded to fp16 (2^-11
- * relative) for their product with the codes and summed as rounded, the output once to bf16.  Values may be of any size
- * that bf16 holds; where a kv head of a sequence has a scale of V above 2^64, what lies below 2^-76 is lost.
+ * row's largest, which are rounded to 2^-35 of it), the weights are rounded to fp16 for their product with the codes (2^-11
+ * relative, for weights below 2^-21 of the row's largest 2^-32 of that: below 2^-32 they are zero) and summed as rounded,
+ * the output once to bf16.  Values may be of any size that bf16 holds; where a kv head of a sequence has a scale of V
+ * above 2^64, what lies below 2^-76 is lost.
  * No sequence has more than max_new rows, (H / Hkv) * max_new <= 128, B * H * max_new <= 2^24.
  * scale must be finite and at most 2^126.
  * workspace: device, 16-byte aligned, tfm_cache8_attention_workspace_bytes(B, H, Hkv,
