@@ -557,11 +557,13 @@ __global__ void __launch_bounds__(Ax<DH, NT>::kThreads, Ax<DH, NT>::kCtas)
             // 2^(r/2) is multiplied twice, so that on the way from the scale to f nothing is larger or smaller than both:
             // f is right wherever fp32 holds it (it stays below 2^107, as the header limits scale, q and k's scales).
             int e = (int)(__float_as_uint(top) >> 23);
-            e = e == 255 ? 127 : max(e, 11);
+            const bool infinite = e == 255;
+            e = max(e, 11);
             int r2 = e - 127 + gm.scale_e + (E4M3 ? -10 : 14);
             e -= r2 & 1;
             r2 = min(max(r2 >> 1, -126), 127);
-            const float mul = __uint_as_float((uint32_t)(264 - e) << 23);
+            // (of a row with an infinity every score is NaN: scores of minus infinity alone would be a row that sees nothing)
+            const float mul = infinite ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float((uint32_t)(264 - e) << 23);
             float sum = 0.0f;
 #pragma unroll
             for (int x = 0; x < KL * KW; ++x) {

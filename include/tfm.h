@@ -630,7 +630,7 @@ tfm_status tfm_cache8_read(const void* k_codes, const void* v_codes, const float
  * query head h reading kv head h / (H / Hkv).  Row t of sequence b's n is at position
  * p = lens[b] - n + t and sees the positions j <= p, with window > 0 those with j > p - window;
  * o = softmax(scale * q . k_j) v_j over them, scale <= 0 meaning 1/sqrt(dh).  A row that
- * sees no position (lens[b] < n) gets zeros; rows of no sequence are not written.  What
+ * sees no position (lens[b] < n) gets zeros, any other with NaN or an infinity in q NaN; rows of no sequence are not written.  What
  * lies in the cache behind lens[b] or before the window is not looked at; codes
  * and scales that are seen must be finite (those tfm_cache8_write stores are), and scale times a row's largest |q| times 448
  * times the largest of k's scales below 2^100 (scores are then below 2^108).  Scores, maxima and sums are fp32;

@@ -186,3 +186,23 @@ def test_rotations_behind_one_another_as_calls_apart(T, H, Hkv, dh, rot, interle
             rotate(x, False)
         torch.cuda.synchronize()
         assert torch.equal(x.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("codes", [I8, E4])
+@pytest.mark.parametrize("H,Hkv,T,room", [(4, 4, 1, 0), (8, 2, 2, 0), (10, 2, 4, 300000)])
+def test_rows_of_q_that_are_not_finite(H, Hkv, T, room, codes):
+    """They come out NaN, whatever the keys are (with every key's score minus infinity too); a row that sees nothing is zero."""
+    lens, block = [200, 70, 0], 32
+    cache = _cache(53, 3, Hkv, 224, 64, block, codes)
+    cache[0][:, :, :, 5] = torch.tensor(-3.0).to(codes).item()
+    wide = _with_room(cache, block, room // block * block) if room else cache
+    q = _q(53, 3 * T, H, 64)
+    clean = _call(q, wide, lens, block)
+    for bad in (float("inf"), -float("inf"), float("nan")):
+        x = q.clone().view(3, T, H, 64)
+        x[:, T - 1, 1, 5] = bad
+        o = _call(x.view(3 * T, H, 64), wide, lens, block).view(3, T, H, 64)
+        assert o[:2, T - 1, 1].isnan().all() and (o[2] == 0).all()
+        same = torch.ones(3, T, H, dtype=torch.bool, device="cuda")
+        same[:2, T - 1, 1] = False
+        assert torch.equal(o[same], clean.view(3, T, H, 64)[same])
