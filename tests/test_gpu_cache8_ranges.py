@@ -206,3 +206,24 @@ def test_rows_of_q_that_are_not_finite(H, Hkv, T, room, codes):
         same = torch.ones(3, T, H, dtype=torch.bool, device="cuda")
         same[:2, T - 1, 1] = False
         assert torch.equal(o[same], clean.view(3, T, H, 64)[same])
+
+
+@pytest.mark.parametrize("codes", [I8, E4])
+@pytest.mark.parametrize("lens,H,Hkv,T,dh,block,window,room", [
+    ([200, 337], 8, 2, 1, 128, 16, 0, 0), ([20000, 70], 8, 1, 1, 64, 16, 0, 0), ([5000, 4000, 64], 4, 2, 2, 32, 128, 0, 0),
+    ([30000], 8, 1, 1, 128, 128, 0, 0), ([3000, 2999], 4, 4, 1, 64, 32, 700, 0), ([384, 130], 10, 2, 4, 128, 32, 0, 300000),
+    ([384, 200], 16, 2, 2, 64, 16, 0, 300000), ([384, 384], 8, 1, 4, 128, 16, 0, 300000)], ids=lambda x: str(x)[:20])
+def test_values_on_both_sides_of_the_larger_units(lens, H, Hkv, T, dh, block, window, room, codes):
+    """Scales of V of 2^63 and 2^64, and a few of 1.5 2^64, which some warps and pieces of a job meet and others do not (the sums
+    of those that do are in units of 2^64): a part taken for the other kind would be 2^64 off."""
+    n = -(-max(lens) // 128) * 128
+    for seed, often in ((0, 0.5), (1, 0.05), (2, 0.005), (3, 0.0)):
+        cache = _cache(45 + seed, len(lens), Hkv, n, dh, block, codes)
+        g = torch.Generator().manual_seed(seed)
+        pick = torch.rand(cache[3].shape, generator=g)
+        cache[3].copy_(torch.where(pick < often, 1.5 * 2.0 ** 64, torch.where(pick < 0.75, 2.0 ** 64, 2.0 ** 63)))
+        if often == 0.0:                                       # one block alone, the last whole one of the first sequence
+            cache[3][0, :, max(lens[0] // block - 1, 0)] = 1.5 * 2.0 ** 64
+        q = _q(45, len(lens) * T, H, dh)
+        wide = _with_room(cache, block, room // block * block) if room else cache
+        _check(_call(q, wide, lens, block, window=window), q, cache, lens, block, [T] * len(lens), window)
